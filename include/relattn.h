@@ -221,6 +221,178 @@ relattn_status relattn_decode_mxfp8(const relattn_params *params, const relattn_
                                     void *stream);
 
 /*
+ * 4-bit K / V cache.  (The pages name NVFP4 for the weights and MXFP8 for K /
+ * V; a 4-bit cache is this library's own addition, in the same manner.)
+ * Format NVFP4: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), one E4M3
+ * scale per 16 consecutive dims and one fp32 factor per kv head:
+ *     value = code * scale * factor.
+ * Two codes per byte, the lower dim in the low nibble.  A row of one head is
+ * 64 + 8 bytes for K and as many for V (bf16: 256 each).
+ *
+ * A cache holds `rows` rows: contiguous, row cu_seqlens_k[b] + p for key p of
+ * sequence b (rows >= total_k), or, where a call is given a relattn_paged_kv,
+ * pool rows as in relattn_decode_paged (rows = num_pages * page_size; here any
+ * page_size that is a multiple of 32).  rows < 2^31.
+ */
+typedef struct relattn_kv_nvfp4 {
+  void *k;                     /* uint8 [rows, num_heads_kv, 64], 16-byte aligned          */
+  void *v;                     /* uint8 [rows, num_heads_kv, 64], 16-byte aligned          */
+  void *k_scale;               /* uint8 E4M3 [rows, num_heads_kv, 8], 8-byte aligned       */
+  void *v_scale;               /* uint8 E4M3 [rows, num_heads_kv, 8], 8-byte aligned       */
+  const float *k_global;       /* fp32 [num_heads_kv] factors > 0 (device), NULL: 1        */
+  const float *v_global;       /* fp32 [num_heads_kv] factors > 0 (device), NULL: 1        */
+  int64_t rows;
+} relattn_kv_nvfp4;
+
+/*
+ * The rows of a chunk (the last Lq_b rows of every sequence, as in
+ * relattn_prologue) into the cache, or back out of it.
+ * relattn_store_nvfp4 quantises k / v and writes the cache's codes and scales:
+ * with t = x / factor (fp32), scale = t's largest magnitude of the 16 dims / 6
+ * rounded to E4M3 (nearest, ties to even, at most 448), code = t / scale
+ * rounded to E2M1 (nearest, ties to even, at most 6, the sign kept; 0 where
+ * scale is 0).  Infinities saturate; a NaN makes its block's scale NaN.
+ * relattn_load_nvfp4 writes k / v = code * scale * factor, rounded once from
+ * fp32 to bf16 (what a chunked prefill over the cached prefix reads).
+ * Cache rows outside the chunk, and chunk rows of no sequence, are left as
+ * they are.  k / v must not overlap the cache.  cu_seqlens and page numbers
+ * are checked on the device: inconsistent ones skip their rows (a load writes
+ * zeros for a page outside the pool) and record RELATTN_ERR_DEVICE_ARGS.
+ */
+typedef struct relattn_cache_rows_params {
+  void *k;                     /* bf16 [total_q, num_heads_kv, 128], 16-byte aligned       */
+  void *v;                     /* bf16 [total_q, num_heads_kv, 128]; read by the store     */
+  const int32_t *cu_seqlens_q; /* device int32 [batch+1]: the chunk's rows                 */
+  const int32_t *cu_seqlens_k; /* device int32 [batch+1]: keys per sequence, chunk included */
+  int32_t batch;
+  int32_t total_q;
+  int32_t num_heads_kv;
+  int32_t head_dim;            /* must be 128                                              */
+  const relattn_kv_nvfp4 *cache;
+  const relattn_paged_kv *pages; /* NULL: contiguous rows                                  */
+} relattn_cache_rows_params;
+
+relattn_status relattn_store_nvfp4(const relattn_cache_rows_params *params, void *stream);
+relattn_status relattn_load_nvfp4(const relattn_cache_rows_params *params, void *stream);
+
+/*
+ * Positions of cached keys that are not their row indices (a cache thinned by
+ * relattn_evict).  Key p of sequence b and kv head h sits at key_pos[h * rows
+ * + its cache row]; query row t of sequence b at q_pos[b] + t.  They decide
+ * the distances d of the relative bias, the causal and window masks and the
+ * log-scale.  Keys need no order; a negative key position is seen by no row.
+ * q_pos must be >= 0 (else the sequence is skipped and recorded).
+ */
+typedef struct relattn_positions {
+  const int32_t *key_pos;      /* device int32 [num_heads_kv, rows]                        */
+  const int32_t *q_pos;        /* device int32 [batch]                                     */
+} relattn_positions;
+
+/*
+ * Split-KV decode against the 4-bit cache: relattn_decode's arguments and
+ * results with k and v the cached values (params->k / v are ignored).  q is
+ * not quantised; products are exact, sums fp32, the softmax weights f16.  A
+ * row that sees no key gives out = 0, lse = -inf.  positions and pages may be
+ * NULL.  Any max_seqlen_q <= 16, group, r_dim <= 64 and rel_extent; speed is
+ * best with at most 8 rows per kv head (max_seqlen_q x group), 16 rows share
+ * one pass over the keys and more take a pass per 16.  num_splits: 0 chooses,
+ * n > 0 allows at most n partials per row.  Rows of no sequence keep their out
+ * and lse.  The workspace size depends on params and on whether positions are
+ * given.
+ */
+relattn_status relattn_decode_nvfp4(const relattn_params *params, const relattn_kv_nvfp4 *cache,
+                                    const relattn_positions *positions, const relattn_paged_kv *pages,
+                                    void *stream);
+relattn_status relattn_decode_nvfp4_workspace_size(const relattn_params *params,
+                                                   const relattn_positions *positions, size_t *bytes);
+
+/*
+ * The attention weight each cached key receives, summed over query rows and
+ * the query heads of its kv head, from the rows' saved lse:
+ *   weights_out[h][row] = decay * weights_in[h][row]
+ *                         + sum_{t, heads of h} exp(l(t, key, head) - lse[head][t]).
+ * The newest Lq_b keys of a sequence start from 0 (their rows were just
+ * written); weights_in = NULL or decay = 0 starts every key from 0 and reads
+ * nothing.  Rows that hold no key keep their weights_out.  A query row with
+ * lse = -inf gives nothing; a call with total_q = 0 writes nothing.  fp32 throughout.  Which rows vote is the
+ * caller's choice: a decode step's, all rows of a prompt, or (cu_seqlens_q
+ * over the last n rows of q and lse) an observation window.
+ * fwd: q, k, r, P, lengths, masks and lse (an input) as in relattn_prefill;
+ * v, out, workspace and num_splits are ignored.  cache = NULL reads the keys
+ * from fwd.k (bf16 rows, contiguous or paged).  weights_out may equal
+ * weights_in and must not overlap anything else.  workspace:
+ * relattn_key_weights_workspace_size() bytes, 16-byte aligned (with a bias: R
+ * = r . P, fp32 total_q x num_heads_q x rel_extent).
+ */
+typedef struct relattn_key_weights_params {
+  relattn_params fwd;
+  const relattn_kv_nvfp4 *cache;          /* NULL: fwd.k                                   */
+  const relattn_positions *positions;     /* NULL: row indices                             */
+  const relattn_paged_kv *pages;          /* NULL: contiguous rows                         */
+  const float *weights_in;                /* fp32 [num_heads_kv, rows] or NULL             */
+  float *weights_out;                     /* fp32 [num_heads_kv, rows]                     */
+  float decay;                            /* finite, >= 0                                  */
+  void *workspace;
+  size_t workspace_bytes;
+} relattn_key_weights_params;
+
+relattn_status relattn_key_weights(const relattn_key_weights_params *params, void *stream);
+relattn_status relattn_key_weights_workspace_size(const relattn_key_weights_params *params, size_t *bytes);
+
+/*
+ * Eviction: moves the kept keys of every (sequence, kv head) into another
+ * cache.  Sequence b keeps K_b = cu_seqlens_keep[b+1] - cu_seqlens_keep[b] <=
+ * Lk_b keys per head: the newest min(recent, K_b), then the first `sink`, then
+ * the heaviest of the rest (equal weights: the lower index; NaN below every
+ * number), in ascending order of index.  A plane is any per-key, per-head
+ * array [rows, num_heads_kv, bytes] (4-bit or MXFP8 codes, scales, bf16 rows);
+ * its kept rows are copied.  key_pos_out receives the kept keys' positions
+ * (key_pos, or their indices when it is NULL) and weights_out their weights;
+ * either may be NULL.  rows / rows_keep: rows of the source / new arrays
+ * (< 2^31); pages / pages_keep: NULL for contiguous rows cu_seqlens_k[b] + p /
+ * cu_seqlens_keep[b] + j.  Sources and destinations must not overlap.
+ * With no log-scale and every row's bias and window inside the newest
+ * `recent` keys, the other decodes read the new bf16 or MXFP8 cache as it is;
+ * otherwise pass the positions to relattn_decode_nvfp4.
+ * workspace: relattn_evict_workspace_size() bytes, 16-byte aligned.
+ * cu_seqlens are checked on the device: a sequence with K_b > Lk_b, Lk_b >
+ * max_seqlen_k or rows outside the arrays is skipped and recorded.
+ */
+#define RELATTN_MAX_PLANES 8
+typedef struct relattn_plane {
+  const void *src;             /* [rows, num_heads_kv, bytes]                              */
+  void *dst;                   /* [rows_keep, num_heads_kv, bytes]                         */
+  int32_t bytes;               /* > 0                                                      */
+} relattn_plane;
+
+typedef struct relattn_evict_params {
+  const float *weights;              /* fp32 [num_heads_kv, rows]                          */
+  const int32_t *cu_seqlens_k;       /* device int32 [batch+1]: keys per sequence          */
+  const int32_t *cu_seqlens_keep;    /* device int32 [batch+1]: keys kept per sequence     */
+  const int32_t *key_pos;            /* int32 [num_heads_kv, rows] or NULL                 */
+  int32_t batch;
+  int32_t total_k;
+  int32_t total_keep;                /* cu_seqlens_keep[batch] (host copy)                 */
+  int32_t max_seqlen_k;
+  int32_t num_heads_kv;
+  int32_t sink;
+  int32_t recent;
+  int64_t rows;
+  int64_t rows_keep;
+  const relattn_paged_kv *pages;
+  const relattn_paged_kv *pages_keep;
+  int32_t num_planes;                /* 0 .. RELATTN_MAX_PLANES                            */
+  relattn_plane planes[RELATTN_MAX_PLANES];
+  float *weights_out;                /* fp32 [num_heads_kv, rows_keep] or NULL             */
+  int32_t *key_pos_out;              /* int32 [num_heads_kv, rows_keep] or NULL            */
+  void *workspace;
+  size_t workspace_bytes;
+} relattn_evict_params;
+
+relattn_status relattn_evict(const relattn_evict_params *params, void *stream);
+relattn_status relattn_evict_workspace_size(const relattn_evict_params *params, size_t *bytes);
+
+/*
  * Log-sum-exp combine of split partials (the decode combine step, exposed so
  * partials from several KV shards can be merged):
  *   lse = ln sum_s exp(lse_s),  out = sum_s exp(lse_s - lse) * o_s.

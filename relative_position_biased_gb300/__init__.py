@@ -14,7 +14,7 @@ import contextlib
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 from . import workloads  # noqa: F401  (seeded input generators)
 
@@ -40,6 +40,9 @@ EXPORTED = (
     "relattn_prologue", "relattn_backward", "relattn_backward_workspace_size",
     "relattn_decode_paged", "relattn_decode_mxfp8", "relattn_quantize_mxfp8",
     "relattn_prologue_mxfp8",
+    "relattn_store_nvfp4", "relattn_load_nvfp4", "relattn_decode_nvfp4",
+    "relattn_decode_nvfp4_workspace_size", "relattn_key_weights",
+    "relattn_key_weights_workspace_size", "relattn_evict", "relattn_evict_workspace_size",
 )
 # exported by the test build only
 TEST_HOOKS = (
@@ -47,6 +50,7 @@ TEST_HOOKS = (
     "relattn_test_backward_skip_step",
 )
 NOALLOC_SCRATCH_BYTES = 32 << 20   # RELATTN_NOALLOC_SCRATCH_BYTES
+HEAD_DIM = workloads.HEAD_DIM
 
 
 class RelattnError(RuntimeError):
@@ -81,6 +85,63 @@ class RelattnPagedKV(ctypes.Structure):
 class RelattnKvMxfp8(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class RelattnKvNvfp4(ctypes.Structure):
+    """Mirror of ``relattn_kv_nvfp4``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_global", ctypes.c_void_p), ("v_global", ctypes.c_void_p),
+                ("rows", ctypes.c_int64)]
+
+
+class RelattnCacheRowsParams(ctypes.Structure):
+    """Mirror of ``relattn_cache_rows_params``."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
+        ("batch", ctypes.c_int32), ("total_q", ctypes.c_int32),
+        ("num_heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("cache", ctypes.POINTER(RelattnKvNvfp4)), ("pages", ctypes.POINTER(RelattnPagedKV)),
+    ]
+
+
+class RelattnPositions(ctypes.Structure):
+    """Mirror of ``relattn_positions``."""
+    _fields_ = [("key_pos", ctypes.c_void_p), ("q_pos", ctypes.c_void_p)]
+
+
+class RelattnKeyWeightsParams(ctypes.Structure):
+    """Mirror of ``relattn_key_weights_params``."""
+    _fields_ = [
+        ("fwd", RelattnParams), ("cache", ctypes.POINTER(RelattnKvNvfp4)),
+        ("positions", ctypes.POINTER(RelattnPositions)), ("pages", ctypes.POINTER(RelattnPagedKV)),
+        ("weights_in", ctypes.c_void_p), ("weights_out", ctypes.c_void_p), ("decay", ctypes.c_float),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+MAX_PLANES = 8   # RELATTN_MAX_PLANES
+
+
+class RelattnPlane(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("bytes", ctypes.c_int32)]
+
+
+class RelattnEvictParams(ctypes.Structure):
+    """Mirror of ``relattn_evict_params``."""
+    _fields_ = [
+        ("weights", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
+        ("cu_seqlens_keep", ctypes.c_void_p), ("key_pos", ctypes.c_void_p),
+        ("batch", ctypes.c_int32), ("total_k", ctypes.c_int32), ("total_keep", ctypes.c_int32),
+        ("max_seqlen_k", ctypes.c_int32), ("num_heads_kv", ctypes.c_int32),
+        ("sink", ctypes.c_int32), ("recent", ctypes.c_int32),
+        ("rows", ctypes.c_int64), ("rows_keep", ctypes.c_int64),
+        ("pages", ctypes.POINTER(RelattnPagedKV)), ("pages_keep", ctypes.POINTER(RelattnPagedKV)),
+        ("num_planes", ctypes.c_int32), ("planes", RelattnPlane * MAX_PLANES),
+        ("weights_out", ctypes.c_void_p), ("key_pos_out", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
 
 
 class RelattnBwdParams(ctypes.Structure):
@@ -203,6 +264,20 @@ def _configure(path: str):
         lib.relattn_prologue_mxfp8.argtypes = [ctypes.POINTER(RelattnPrologueParams),
                                                ctypes.POINTER(RelattnKvMxfp8), vp]
         lib.relattn_prologue_mxfp8.restype = ctypes.c_int
+        KV, PG, POS = (ctypes.POINTER(RelattnKvNvfp4), ctypes.POINTER(RelattnPagedKV),
+                       ctypes.POINTER(RelattnPositions))
+        SZ = ctypes.POINTER(ctypes.c_size_t)
+        for name, args in (
+                ("relattn_store_nvfp4", [ctypes.POINTER(RelattnCacheRowsParams), vp]),
+                ("relattn_load_nvfp4", [ctypes.POINTER(RelattnCacheRowsParams), vp]),
+                ("relattn_decode_nvfp4", [P, KV, POS, PG, vp]),
+                ("relattn_decode_nvfp4_workspace_size", [P, POS, SZ]),
+                ("relattn_key_weights", [ctypes.POINTER(RelattnKeyWeightsParams), vp]),
+                ("relattn_key_weights_workspace_size", [ctypes.POINTER(RelattnKeyWeightsParams), SZ]),
+                ("relattn_evict", [ctypes.POINTER(RelattnEvictParams), vp]),
+                ("relattn_evict_workspace_size", [ctypes.POINTER(RelattnEvictParams), SZ])):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = args, ctypes.c_int
         lib.relattn_version.argtypes = []
         lib.relattn_version.restype = ctypes.c_char_p
         _libs[path] = lib
@@ -527,3 +602,362 @@ def backward(q, k, v, r, P, out, lse, dout, cu_seqlens_q, cu_seqlens_k, *, max_s
     _check(relattn_backward(prm, _current_stream() if stream is None else stream),
            "relattn_backward")
     return dq, dk, dv, dr
+
+
+# ------------------------------------------------------------------ 4-bit cache, key weights, eviction
+
+def relattn_store_nvfp4(params: RelattnCacheRowsParams, stream: int = 0) -> int:
+    return load_library().relattn_store_nvfp4(ctypes.byref(params), ctypes.c_void_p(stream))
+
+
+def relattn_load_nvfp4(params: RelattnCacheRowsParams, stream: int = 0) -> int:
+    return load_library().relattn_load_nvfp4(ctypes.byref(params), ctypes.c_void_p(stream))
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def relattn_decode_nvfp4(params: RelattnParams, cache: RelattnKvNvfp4,
+                         positions: Optional[RelattnPositions] = None,
+                         pages: Optional[RelattnPagedKV] = None, stream: int = 0) -> int:
+    return load_library().relattn_decode_nvfp4(ctypes.byref(params), ctypes.byref(cache),
+                                               _ref(positions), _ref(pages), ctypes.c_void_p(stream))
+
+
+def relattn_decode_nvfp4_workspace_size(params: RelattnParams,
+                                        positions: Optional[RelattnPositions] = None) -> Tuple[int, int]:
+    n = ctypes.c_size_t(0)
+    st = load_library().relattn_decode_nvfp4_workspace_size(ctypes.byref(params), _ref(positions),
+                                                            ctypes.byref(n))
+    return st, int(n.value)
+
+
+def relattn_key_weights(params: RelattnKeyWeightsParams, stream: int = 0) -> int:
+    return load_library().relattn_key_weights(ctypes.byref(params), ctypes.c_void_p(stream))
+
+
+def relattn_key_weights_workspace_size(params: RelattnKeyWeightsParams) -> Tuple[int, int]:
+    n = ctypes.c_size_t(0)
+    st = load_library().relattn_key_weights_workspace_size(ctypes.byref(params), ctypes.byref(n))
+    return st, int(n.value)
+
+
+def relattn_evict(params: RelattnEvictParams, stream: int = 0) -> int:
+    return load_library().relattn_evict(ctypes.byref(params), ctypes.c_void_p(stream))
+
+
+def relattn_evict_workspace_size(params: RelattnEvictParams) -> Tuple[int, int]:
+    n = ctypes.c_size_t(0)
+    st = load_library().relattn_evict_workspace_size(ctypes.byref(params), ctypes.byref(n))
+    return st, int(n.value)
+
+
+class KvNvfp4(NamedTuple):
+    """A 4-bit (NVFP4) K / V cache: code bytes k / v uint8 [rows, Hkv, 64], E4M3
+    scale bytes k_scale / v_scale uint8 [rows, Hkv, 8], and optional fp32 [Hkv]
+    factors (None: 1)."""
+    k: "torch.Tensor"            # noqa: F821
+    v: "torch.Tensor"            # noqa: F821
+    k_scale: "torch.Tensor"      # noqa: F821
+    v_scale: "torch.Tensor"      # noqa: F821
+    k_global: Optional["torch.Tensor"] = None   # noqa: F821
+    v_global: Optional["torch.Tensor"] = None   # noqa: F821
+
+
+def empty_nvfp4(rows: int, num_heads_kv: int, device, k_global=None, v_global=None) -> KvNvfp4:
+    """A cache of ``rows`` rows, zeroed (every value reads 0 until it is stored)."""
+    import torch
+    codes = [torch.zeros(rows, num_heads_kv, 64, dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.zeros(rows, num_heads_kv, 8, dtype=torch.uint8, device=device) for _ in range(2)]
+    return KvNvfp4(*codes, *scales, k_global, v_global)
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, name: str, dtype, shape, device):
+    """A contiguous tensor of this type and shape (None: any size) on `device`."""
+    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _need(t.dim() == len(shape) and all(s is None or int(s) == n for s, n in zip(shape, t.shape)),
+          f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+    _need(t.device == device, f"{name} is on {t.device}, not {device}")
+    return t.data_ptr()
+
+
+def _cu(t, name: str, device, batch: Optional[int] = None):
+    import torch
+    return _tensor(t, name, torch.int32, [None if batch is None else batch + 1], device)
+
+
+def _cache(cache: KvNvfp4, device, num_heads_kv: Optional[int] = None) -> RelattnKvNvfp4:
+    import torch
+    _need(isinstance(cache, KvNvfp4), "cache must be a KvNvfp4")
+    rows = int(cache.k.shape[0])
+    H = int(cache.k.shape[1]) if cache.k.dim() == 3 and num_heads_kv is None else num_heads_kv
+    out = {}
+    for n in ("k", "v"):
+        out[n] = _tensor(getattr(cache, n), f"cache.{n}", torch.uint8, [rows, H, 64], device)
+        out[n + "_scale"] = _tensor(getattr(cache, n + "_scale"), f"cache.{n}_scale", torch.uint8, [rows, H, 8], device)
+        g = getattr(cache, n + "_global")
+        out[n + "_global"] = None if g is None else _tensor(g, f"cache.{n}_global", torch.float32, [H], device)
+    return RelattnKvNvfp4(rows=rows, **out)
+
+
+def _pages(block_table, page_size: int, rows: int, device, batch: int) -> Optional[RelattnPagedKV]:
+    import torch
+    if block_table is None:
+        return None
+    _need(page_size > 0 and rows % page_size == 0, "rows must be a multiple of page_size")
+    return RelattnPagedKV(block_table=_tensor(block_table, "block_table", torch.int32, [batch, None], device),
+                          max_pages_per_seq=int(block_table.shape[1]), page_size=int(page_size),
+                          num_pages=rows // int(page_size))
+
+
+def _positions(key_pos, q_pos, num_heads_kv: int, rows: int, batch: int, device) -> Optional[RelattnPositions]:
+    import torch
+    if key_pos is None and q_pos is None:
+        return None
+    _need(key_pos is not None and q_pos is not None, "key_pos and q_pos go together")
+    return RelattnPositions(key_pos=_tensor(key_pos, "key_pos", torch.int32, [num_heads_kv, rows], device),
+                            q_pos=_tensor(q_pos, "q_pos", torch.int32, [batch], device))
+
+
+class _on:
+    """Runs a block with the tensors' device current and, where a stream is
+    given, with that stream current too, so that what the block allocates
+    belongs to the stream it launches on.  Gives the stream to launch on."""
+
+    def __init__(self, device, stream: Optional[int]):
+        _need(device.type == "cuda", f"tensors must be on a CUDA device, not {device}")
+        self.device, self.stream, self.stack = device, stream, contextlib.ExitStack()
+
+    def __enter__(self) -> int:
+        import torch
+        if self.device.index != torch.cuda.current_device():
+            self.stack.enter_context(torch.cuda.device(self.device))
+        if self.stream is not None:
+            self.stack.enter_context(torch.cuda.stream(
+                torch.cuda.ExternalStream(self.stream, device=self.device) if self.stream
+                else torch.cuda.default_stream(self.device)))
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        return self.stack.__exit__(*exc)
+
+
+def _query_args(q, r, P, num_heads_kv: int, device):
+    """Checks q [Tq, Hq, 128], r [Tq, Hq, r_dim], P [r_dim, E]."""
+    import torch
+    _tensor(q, "q", torch.bfloat16, [None, None, HEAD_DIM], device)
+    _need(q.shape[1] % num_heads_kv == 0, "num_heads_q must be a multiple of num_heads_kv")
+    _need((r is None) == (P is None), "r and P go together")
+    if r is not None:
+        _tensor(r, "r", torch.bfloat16, [q.shape[0], q.shape[1], None], device)
+        _tensor(P, "P", torch.bfloat16, [r.shape[2], None], device)
+
+
+def _cache_rows(k, v, cu_q, cu_k, cache, block_table, page_size):
+    import torch
+    dev = k.device
+    kv = _cache(cache, dev)
+    H = int(cache.k.shape[1])
+    batch = int(cu_q.numel()) - 1
+    _need(batch >= 0, "cu_seqlens_q needs at least one entry")
+    pages = _pages(block_table, page_size, kv.rows, dev, batch)
+    return RelattnCacheRowsParams(
+        k=_tensor(k, "k", torch.bfloat16, [None, H, HEAD_DIM], dev),
+        v=_tensor(v, "v", torch.bfloat16, [k.shape[0], H, HEAD_DIM], dev),
+        cu_seqlens_q=_cu(cu_q, "cu_seqlens_q", dev), cu_seqlens_k=_cu(cu_k, "cu_seqlens_k", dev, batch),
+        batch=batch, total_q=int(k.shape[0]), num_heads_kv=H, head_dim=HEAD_DIM,
+        cache=ctypes.pointer(kv), pages=None if pages is None else ctypes.pointer(pages))
+
+
+def store_nvfp4(k, v, cu_seqlens_q, cu_seqlens_k, cache: KvNvfp4, *, block_table=None, page_size: int = 0,
+                stream: Optional[int] = None) -> None:
+    """Quantises the chunk's rows k / v bf16 [total_q, Hkv, 128] (the last rows
+    of every sequence) into the 4-bit cache; with ``block_table`` int32 [batch,
+    max_pages_per_seq] the cache's rows are pages of ``page_size`` keys."""
+    prm = _cache_rows(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table, page_size)
+    with _on(k.device, stream) as st:
+        _check(relattn_store_nvfp4(prm, st), "relattn_store_nvfp4")
+
+
+def load_nvfp4(cache: KvNvfp4, cu_seqlens_q, cu_seqlens_k, *, total_q: int, block_table=None, page_size: int = 0,
+               k=None, v=None, stream: Optional[int] = None):
+    """The last cu_seqlens_q rows of every sequence as bf16 (k, v) [total_q, Hkv,
+    128] (pass cu_seqlens_k twice for all of them)."""
+    import torch
+    with _on(cache.k.device, stream) as st:
+        shape = (int(total_q), int(cache.k.shape[1]), HEAD_DIM)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if v is None else v
+        _need(k.shape[0] == total_q, "k must have total_q rows")
+        prm = _cache_rows(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table, page_size)
+        _check(relattn_load_nvfp4(prm, st), "relattn_load_nvfp4")
+        return k, v
+
+
+def _forward_params(q, k, r, P, cu_q, cu_k, *, total_k, num_heads_kv, **kw) -> RelattnParams:
+    r_dim = 0 if r is None else int(r.shape[2])
+    return RelattnParams(
+        q=q.data_ptr(), k=None if k is None else k.data_ptr(),
+        r=None if r is None else r.data_ptr(), P=None if P is None else P.data_ptr(),
+        cu_seqlens_q=cu_q.data_ptr(), cu_seqlens_k=cu_k.data_ptr(), batch=int(cu_q.numel()) - 1,
+        total_q=int(q.shape[0]), total_k=int(total_k), num_heads_q=int(q.shape[1]), num_heads_kv=int(num_heads_kv),
+        head_dim=int(q.shape[2]), r_dim=r_dim, rel_extent=0 if P is None else int(P.shape[1]), **kw)
+
+
+def _total_k(total_k: Optional[int], block_table, cu_k, rows: int) -> int:
+    if total_k is not None:
+        return int(total_k)
+    return int(cu_k[-1].item()) if block_table is not None else rows
+
+
+def _workspace(nbytes: int, workspace, device):
+    """(tensor kept alive, pointer, bytes) of a workspace of at least nbytes."""
+    import torch
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device)
+    _need(workspace.device == device, "workspace is on another device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def decode_nvfp4(q, cache: KvNvfp4, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int, max_seqlen_k: int,
+                 alpha: float, window: int = 0, log_scale_base: float = 0.0, key_pos=None, q_pos=None,
+                 block_table=None, page_size: int = 0, total_k: Optional[int] = None, num_splits: int = 0,
+                 out=None, lse=None, workspace=None, stream: Optional[int] = None):
+    """Split-KV decode against the 4-bit cache (contiguous, or paged with
+    ``block_table``); ``key_pos`` int32 [Hkv, rows] and ``q_pos`` int32 [batch]
+    give positions that are not the row indices.  ``total_k`` (the sum of the
+    key counts) sizes the split plan; without it a paged call reads it back
+    from cu_seqlens_k, which waits for the stream.  Returns (out, lse)."""
+    import torch
+    dev = q.device
+    with _on(dev, stream) as st:
+        H = int(cache.k.shape[1])
+        kv = _cache(cache, dev)
+        _query_args(q, r, P, H, dev)
+        batch = int(cu_seqlens_q.numel()) - 1
+        _cu(cu_seqlens_q, "cu_seqlens_q", dev)
+        _cu(cu_seqlens_k, "cu_seqlens_k", dev, batch)
+        pages = _pages(block_table, page_size, kv.rows, dev, batch)
+        pos = _positions(key_pos, q_pos, H, kv.rows, batch, dev)
+        out, lse = _outputs(q, out, lse)
+        _tensor(out, "out", torch.bfloat16, q.shape, dev)
+        _tensor(lse, "lse", torch.float32, [q.shape[1], q.shape[0]], dev)
+        prm = _forward_params(q, None, r, P, cu_seqlens_q, cu_seqlens_k,
+                              total_k=_total_k(total_k, block_table, cu_seqlens_k, kv.rows), num_heads_kv=H,
+                              max_seqlen_q=int(max_seqlen_q), max_seqlen_k=int(max_seqlen_k), alpha=float(alpha),
+                              window=int(window), log_scale_base=float(log_scale_base), out=out.data_ptr(),
+                              lse=lse.data_ptr(), num_splits=int(num_splits))
+        status, need = relattn_decode_nvfp4_workspace_size(prm, pos)
+        _check(status, "relattn_decode_nvfp4_workspace_size")
+        keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
+        _check(relattn_decode_nvfp4(prm, kv, pos, pages, st), "relattn_decode_nvfp4")
+        return out, lse
+
+
+def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int, max_seqlen_k: int, alpha: float,
+                window: int = 0, log_scale_base: float = 0.0, weights_in=None, decay: float = 1.0, key_pos=None,
+                q_pos=None, block_table=None, page_size: int = 0, total_k: Optional[int] = None, out=None,
+                workspace=None, stream: Optional[int] = None):
+    """The attention weight each cached key receives from the rows of q, whose
+    lse [Hq, total_q] the forward or decode returned: fp32 [Hkv, rows],
+    decay * weights_in + the rows' weights (the newest rows' keys start from
+    0).  ``k`` is a bf16 tensor [rows, Hkv, 128] or a KvNvfp4 cache.  ``out`` may be
+    ``weights_in``; a new one is zeroed first, since rows that hold no key are
+    not written."""
+    import torch
+    dev = q.device
+    with _on(dev, stream) as st:
+        fp4 = isinstance(k, KvNvfp4)
+        kv = _cache(k, dev) if fp4 else None
+        if not fp4:
+            _tensor(k, "k", torch.bfloat16, [None, None, HEAD_DIM], dev)
+        rows, H = (int(x) for x in (k.k if fp4 else k).shape[:2])
+        _query_args(q, r, P, H, dev)
+        _tensor(lse, "lse", torch.float32, [q.shape[1], q.shape[0]], dev)
+        batch = int(cu_seqlens_q.numel()) - 1
+        _cu(cu_seqlens_q, "cu_seqlens_q", dev)
+        _cu(cu_seqlens_k, "cu_seqlens_k", dev, batch)
+        pages = _pages(block_table, page_size, rows, dev, batch)
+        pos = _positions(key_pos, q_pos, H, rows, batch, dev)
+        w_in = None if weights_in is None else _tensor(weights_in, "weights_in", torch.float32, [H, rows], dev)
+        if out is None:
+            out = torch.zeros(H, rows, dtype=torch.float32, device=dev)
+        _tensor(out, "out", torch.float32, [H, rows], dev)
+        total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
+        if not fp4 and block_table is None:
+            _need(total_k == rows, "a contiguous k has total_k rows")
+        fwd = _forward_params(q, None if fp4 else k, r, P, cu_seqlens_q, cu_seqlens_k, total_k=total_k, num_heads_kv=H,
+                              max_seqlen_q=int(max_seqlen_q), max_seqlen_k=int(max_seqlen_k), alpha=float(alpha),
+                              window=int(window), log_scale_base=float(log_scale_base), lse=lse.data_ptr())
+        prm = RelattnKeyWeightsParams(
+            fwd=fwd, cache=ctypes.pointer(kv) if fp4 else None, positions=None if pos is None else ctypes.pointer(pos),
+            pages=None if pages is None else ctypes.pointer(pages), weights_in=w_in, weights_out=out.data_ptr(),
+            decay=float(decay))
+        status, need = relattn_key_weights_workspace_size(prm)
+        _check(status, "relattn_key_weights_workspace_size")
+        keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
+        _check(relattn_key_weights(prm, st), "relattn_key_weights")
+        return out
+
+
+def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seqlen_k: int, recent: int, sink: int = 0,
+          total_keep: int, total_k: Optional[int] = None, key_pos=None, block_table=None, page_size: int = 0,
+          block_table_keep=None, page_size_keep: int = 0, key_pos_out=None, weights_out=None, workspace=None,
+          stream: Optional[int] = None):
+    """Keeps, per sequence and kv head, the newest ``recent`` keys, the first
+    ``sink`` and the heaviest of the rest (``weights`` fp32 [Hkv, rows]) -- in
+    all cu_seqlens_keep[b+1] - cu_seqlens_keep[b] of sequence b -- and copies
+    their rows of every plane [rows, Hkv, ...] into ``dst_planes``, in order of
+    index.  Returns (key_pos [Hkv, rows_keep] int32, weights [Hkv, rows_keep])
+    of the new cache."""
+    import torch
+    dev = weights.device
+    with _on(dev, stream) as st:
+        _need(len(planes) == len(dst_planes) <= MAX_PLANES, f"as many dst_planes as planes, at most {MAX_PLANES}")
+        _tensor(weights, "weights", torch.float32, [None, None], dev)
+        H, rows = (int(x) for x in weights.shape)
+        batch = int(cu_seqlens_k.numel()) - 1
+        _cu(cu_seqlens_k, "cu_seqlens_k", dev)
+        _cu(cu_seqlens_keep, "cu_seqlens_keep", dev, batch)
+        rows_keep = int(dst_planes[0].shape[0]) if len(dst_planes) else int(total_keep)
+        prm = RelattnEvictParams(num_planes=len(planes))
+        for i, (a, b) in enumerate(zip(planes, dst_planes)):
+            _need(a.dim() >= 2 and tuple(a.shape[:2]) == (rows, H) and tuple(b.shape) == (rows_keep, *a.shape[1:]),
+                  f"plane {i} must be [rows, Hkv, ...] and its destination [rows_keep, Hkv, ...]")
+            _tensor(a, f"plane {i}", a.dtype, a.shape, dev)
+            _tensor(b, f"destination {i}", a.dtype, b.shape, dev)
+            n = a.element_size()
+            for s in a.shape[2:]:
+                n *= int(s)
+            prm.planes[i] = RelattnPlane(src=a.data_ptr(), dst=b.data_ptr(), bytes=n)
+        pages = _pages(block_table, page_size, rows, dev, batch)
+        pages_keep = _pages(block_table_keep, page_size_keep, rows_keep, dev, batch)
+        if key_pos_out is None:
+            key_pos_out = torch.full((H, rows_keep), -1, dtype=torch.int32, device=dev)
+        if weights_out is None:
+            weights_out = torch.zeros(H, rows_keep, dtype=torch.float32, device=dev)
+        prm.weights, prm.cu_seqlens_k, prm.cu_seqlens_keep = (weights.data_ptr(), cu_seqlens_k.data_ptr(),
+                                                              cu_seqlens_keep.data_ptr())
+        prm.key_pos = None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, [H, rows], dev)
+        prm.batch, prm.total_keep, prm.num_heads_kv = batch, int(total_keep), H
+        prm.total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
+        prm.max_seqlen_k, prm.sink, prm.recent, prm.rows, prm.rows_keep = (int(max_seqlen_k), int(sink), int(recent), rows,
+                                                                           rows_keep)
+        prm.pages = None if pages is None else ctypes.pointer(pages)
+        prm.pages_keep = None if pages_keep is None else ctypes.pointer(pages_keep)
+        prm.weights_out = _tensor(weights_out, "weights_out", torch.float32, [H, rows_keep], dev)
+        prm.key_pos_out = _tensor(key_pos_out, "key_pos_out", torch.int32, [H, rows_keep], dev)
+        status, need = relattn_evict_workspace_size(prm)
+        _check(status, "relattn_evict_workspace_size")
+        keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
+        _check(relattn_evict(prm, st), "relattn_evict")
+        return key_pos_out, weights_out

@@ -323,6 +323,159 @@ relattn_status validate_prologue(const relattn_prologue_params *p, const relattn
   return RELATTN_OK;
 }
 
+// ---- the 4-bit cache, key weights and eviction
+
+constexpr long kMaxRows = 0x7fffffffL;
+
+// Checks a page table and fills the row addressing; max_k: the longest
+// sequence it has to hold (0: checked on the device).
+relattn_status cache_pages(const relattn_paged_kv *kv, int64_t rows, long max_k, CachePages *out) {
+  *out = CachePages{};
+  if (rows < 0) return RELATTN_ERR_INVALID_ARG;
+  if (rows > kMaxRows) return RELATTN_ERR_UNSUPPORTED;
+  out->rows = rows;
+  if (!kv) return RELATTN_OK;
+  if (kv->page_size <= 0 || kv->num_pages <= 0 || kv->max_pages_per_seq <= 0) return RELATTN_ERR_INVALID_ARG;
+  if (kv->page_size % kFp4PageUnit != 0) return RELATTN_ERR_UNSUPPORTED;
+  if ((long)kv->num_pages * kv->page_size > kMaxRows) return RELATTN_ERR_UNSUPPORTED;
+  if ((long)kv->num_pages * kv->page_size != rows) return RELATTN_ERR_INVALID_ARG;
+  if ((long)kv->max_pages_per_seq * kv->page_size < max_k) return RELATTN_ERR_INVALID_ARG;
+  if (!kv->block_table || !aligned(kv->block_table, 4)) return RELATTN_ERR_INVALID_ARG;
+  out->block_table = kv->block_table;
+  out->page_size = kv->page_size;
+  out->max_pages = kv->max_pages_per_seq;
+  out->num_pages = kv->num_pages;
+  return RELATTN_OK;
+}
+
+relattn_status cache_fp4(const relattn_kv_nvfp4 *c, Fp4Cache *out) {
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !aligned16(c->k) || !aligned16(c->v) ||
+      !aligned(c->k_scale, 8) || !aligned(c->v_scale, 8) || !aligned(c->k_global, 4) || !aligned(c->v_global, 4))
+    return RELATTN_ERR_INVALID_ARG;
+  out->k = static_cast<const uint8_t *>(c->k);
+  out->v = static_cast<const uint8_t *>(c->v);
+  out->k_scale = static_cast<const uint8_t *>(c->k_scale);
+  out->v_scale = static_cast<const uint8_t *>(c->v_scale);
+  out->k_global = c->k_global;
+  out->v_global = c->v_global;
+  return RELATTN_OK;
+}
+
+relattn_status cache_positions(const relattn_positions *x, WalkArgs *out) {
+  out->key_pos = out->q_pos = nullptr;
+  if (!x) return RELATTN_OK;
+  if (!x->key_pos || !x->q_pos || !aligned(x->key_pos, 4) || !aligned(x->q_pos, 4)) return RELATTN_ERR_INVALID_ARG;
+  out->key_pos = x->key_pos;
+  out->q_pos = x->q_pos;
+  return RELATTN_OK;
+}
+
+relattn_status cache_rows_args(const relattn_cache_rows_params *p, Fp4RowArgs *a) {
+  if (!p || !p->cache) return RELATTN_ERR_INVALID_ARG;
+  if (p->head_dim != kHeadDim) return RELATTN_ERR_UNSUPPORTED;
+  if (p->batch < 0 || p->total_q < 0 || p->num_heads_kv <= 0) return RELATTN_ERR_INVALID_ARG;
+  *a = Fp4RowArgs{};
+  relattn_status st = cache_pages(p->pages, p->cache->rows, 0, &a->pages);
+  if (st != RELATTN_OK || p->batch == 0 || p->total_q == 0) return st;
+  if (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v) || !p->cu_seqlens_q || !p->cu_seqlens_k)
+    return RELATTN_ERR_INVALID_ARG;
+  if ((st = cache_fp4(p->cache, &a->kv)) != RELATTN_OK) return st;
+  const size_t in = (size_t)p->total_q * p->num_heads_kv * kHeadDim * 2;
+  const size_t codes = (size_t)p->cache->rows * p->num_heads_kv * 64;
+  const void *arrays[] = {a->kv.k, a->kv.v, a->kv.k_scale, a->kv.v_scale};
+  for (int i = 0; i < 4; ++i)
+    if (overlaps(p->k, in, arrays[i], i < 2 ? codes : codes / 8) || overlaps(p->v, in, arrays[i], i < 2 ? codes : codes / 8))
+      return RELATTN_ERR_INVALID_ARG;
+  a->k = static_cast<const __nv_bfloat16 *>(p->k);
+  a->v = static_cast<const __nv_bfloat16 *>(p->v);
+  a->cu_q = p->cu_seqlens_q;
+  a->cu_k = p->cu_seqlens_k;
+  a->batch = p->batch;
+  a->total_q = p->total_q;
+  a->Hkv = p->num_heads_kv;
+  return device_state(nullptr, &a->err, nullptr);
+}
+
+// The forward parameters of a call whose keys live in a cache: `k` / `v` /
+// `out` stand in for the pointers the call does not read.
+relattn_status validate_cached(const relattn_params *p, bool decode, const void *k, const void *v, const void *out) {
+  if (!p) return RELATTN_ERR_INVALID_ARG;
+  relattn_params f = *p;
+  f.k = k;
+  f.v = v;
+  f.out = const_cast<void *>(out);
+  const relattn_status st = validate(&f, decode);
+  if (st != RELATTN_OK) return st;
+  return (long)p->batch * p->num_heads_kv > 65535 ? RELATTN_ERR_UNSUPPORTED : RELATTN_OK;
+}
+
+size_t key_weights_bytes(const relattn_params &f) {
+  if (!(f.r_dim > 0 && f.rel_extent > 0) || f.batch == 0) return 0;
+  return (size_t)f.total_q * f.num_heads_q * f.rel_extent * sizeof(float);
+}
+
+size_t evict_bytes(const relattn_evict_params &p) {
+  return (size_t)p.total_keep * ((size_t)p.num_heads_kv + 1) * sizeof(int32_t);
+}
+
+relattn_status validate_evict(const relattn_evict_params *p, EvictArgs *a) {
+  if (!p) return RELATTN_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->total_k < 0 || p->total_keep < 0 || p->max_seqlen_k < 0 || p->num_heads_kv <= 0 ||
+      p->sink < 0 || p->recent < 0 || p->num_planes < 0 || p->num_planes > RELATTN_MAX_PLANES ||
+      p->total_keep > p->total_k)
+    return RELATTN_ERR_INVALID_ARG;
+  if ((long)p->batch * p->num_heads_kv > 0x0fffffffL) return RELATTN_ERR_UNSUPPORTED;
+  *a = EvictArgs{};
+  relattn_status st = cache_pages(p->pages, p->rows, p->max_seqlen_k, &a->src);
+  if (st == RELATTN_OK) st = cache_pages(p->pages_keep, p->rows_keep, 0, &a->dst);
+  if (st != RELATTN_OK) return st;
+  if ((!p->pages && p->rows < p->total_k) || (!p->pages_keep && p->rows_keep < p->total_keep))
+    return RELATTN_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->total_keep == 0) return RELATTN_OK;
+  if (!p->weights || !aligned(p->weights, 4) || !p->cu_seqlens_k || !p->cu_seqlens_keep || !aligned(p->key_pos, 4) ||
+      !aligned(p->weights_out, 4) || !aligned(p->key_pos_out, 4))
+    return RELATTN_ERR_INVALID_ARG;
+  const size_t per = (size_t)p->num_heads_kv;
+  // sources, destinations and their sizes
+  const void *from[RELATTN_MAX_PLANES + 2];
+  size_t from_n[RELATTN_MAX_PLANES + 2];
+  const void *to[RELATTN_MAX_PLANES + 2];
+  size_t to_n[RELATTN_MAX_PLANES + 2];
+  const int n = p->num_planes;
+  for (int i = 0; i < n; ++i) {
+    const relattn_plane &x = p->planes[i];
+    if (!x.src || !x.dst || x.bytes <= 0 || x.bytes > (1 << 20)) return RELATTN_ERR_INVALID_ARG;
+    from[i] = x.src, from_n[i] = (size_t)p->rows * per * x.bytes;
+    to[i] = x.dst, to_n[i] = (size_t)p->rows_keep * per * x.bytes;
+    a->from[i] = x.src, a->to[i] = x.dst, a->bytes[i] = x.bytes;
+  }
+  from[n] = p->weights, from_n[n] = (size_t)p->rows * per * 4;
+  from[n + 1] = p->key_pos, from_n[n + 1] = p->key_pos ? (size_t)p->rows * per * 4 : 0;
+  to[n] = p->weights_out, to_n[n] = p->weights_out ? (size_t)p->rows_keep * per * 4 : 0;
+  to[n + 1] = p->key_pos_out, to_n[n + 1] = p->key_pos_out ? (size_t)p->rows_keep * per * 4 : 0;
+  for (int i = 0; i < n + 2; ++i)
+    for (int j = 0; j < n + 2; ++j)
+      if (overlaps(to[i], to_n[i], from[j], from_n[j]) || (i != j && overlaps(to[i], to_n[i], to[j], to_n[j])))
+        return RELATTN_ERR_INVALID_ARG;
+  if (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < evict_bytes(*p)) return RELATTN_ERR_WORKSPACE;
+  a->weights = p->weights;
+  a->cu_k = p->cu_seqlens_k;
+  a->cu_keep = p->cu_seqlens_keep;
+  a->key_pos = p->key_pos;
+  a->batch = p->batch;
+  a->total_keep = p->total_keep;
+  a->max_k = p->max_seqlen_k;
+  a->Hkv = p->num_heads_kv;
+  a->sink = p->sink;
+  a->recent = p->recent;
+  a->w_out = p->weights_out;
+  a->pos_out = p->key_pos_out;
+  a->src_row = static_cast<int32_t *>(p->workspace);
+  a->dst_row = a->src_row + (size_t)p->total_keep * p->num_heads_kv;
+  a->planes = n;
+  return device_state(nullptr, &a->err, nullptr);
+}
+
 }  // namespace
 
 extern "C" {
@@ -586,6 +739,117 @@ relattn_status relattn_prologue_mxfp8(const relattn_prologue_params *p, const re
   if ((st = device_state(nullptr, &err, &sms)) != RELATTN_OK) return st;
   return cuda_status(launch_prologue(p, err, sms, g_test_prologue_skip,
                                      static_cast<cudaStream_t>(stream), cache));
+}
+
+relattn_status relattn_store_nvfp4(const relattn_cache_rows_params *p, void *stream) {
+  Fp4RowArgs a;
+  const relattn_status st = cache_rows_args(p, &a);
+  if (st != RELATTN_OK || a.batch == 0) return st;
+  return cuda_status(launch_store_fp4(a, static_cast<cudaStream_t>(stream)));
+}
+
+relattn_status relattn_load_nvfp4(const relattn_cache_rows_params *p, void *stream) {
+  Fp4RowArgs a;
+  const relattn_status st = cache_rows_args(p, &a);
+  if (st != RELATTN_OK || a.batch == 0) return st;
+  return cuda_status(launch_load_fp4(a, static_cast<cudaStream_t>(stream)));
+}
+
+relattn_status relattn_decode_nvfp4_workspace_size(const relattn_params *p, const relattn_positions *positions,
+                                                   size_t *bytes) {
+  if (!p || !bytes) return RELATTN_ERR_INVALID_ARG;
+  relattn_status st = validate_cached(p, true, p->q, p->q, p->out);
+  if (st != RELATTN_OK) return st;
+  *bytes = 0;
+  if (p->batch == 0 || p->total_q == 0) return RELATTN_OK;
+  KernelArgs a;
+  if ((st = make_args(p, &a)) != RELATTN_OK) return st;
+  Fp4DecodePlan plan;
+  if (!plan_decode_fp4(a, p->total_k, positions != nullptr, p->num_splits, &plan)) return RELATTN_ERR_UNSUPPORTED;
+  *bytes = plan.ws_bytes;
+  return RELATTN_OK;
+}
+
+relattn_status relattn_decode_nvfp4(const relattn_params *p, const relattn_kv_nvfp4 *cache,
+                                    const relattn_positions *positions, const relattn_paged_kv *pages, void *stream) {
+  if (!p || !cache) return RELATTN_ERR_INVALID_ARG;
+  relattn_status st = validate_cached(p, true, cache->k, cache->v, p->out);
+  if (st != RELATTN_OK) return st;
+  Fp4DecodeArgs x{};
+  if ((st = cache_pages(pages, cache->rows, p->max_seqlen_k, &x.pages)) != RELATTN_OK) return st;
+  if (!pages && cache->rows < p->total_k) return RELATTN_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->total_q == 0) return RELATTN_OK;
+  if ((st = cache_fp4(cache, &x.kv)) != RELATTN_OK) return st;
+  if ((st = cache_positions(positions, &x)) != RELATTN_OK) return st;
+  if ((st = make_args(p, &x.a)) != RELATTN_OK) return st;
+  Fp4DecodePlan plan;
+  if (!plan_decode_fp4(x.a, p->total_k, positions != nullptr, p->num_splits, &plan)) return RELATTN_ERR_UNSUPPORTED;
+  x.row_blocks = plan.row_blocks;
+  x.splits = plan.splits;
+  x.c_min = plan.c_min;
+  if (plan.ws_bytes > 0) {
+    if (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < plan.ws_bytes) return RELATTN_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(p->workspace);
+    x.a.o_part = reinterpret_cast<float *>(ws);
+    x.a.lse_part = reinterpret_cast<float *>(ws + plan.lse_offset);
+    x.a.rdec = reinterpret_cast<const float *>(ws + plan.rel_offset);
+  }
+  return cuda_status(launch_decode_fp4(x, static_cast<cudaStream_t>(stream)));
+}
+
+relattn_status relattn_key_weights_workspace_size(const relattn_key_weights_params *p, size_t *bytes) {
+  if (!p || !bytes) return RELATTN_ERR_INVALID_ARG;
+  const relattn_status st = validate_cached(&p->fwd, false, p->fwd.q, p->fwd.q, p->fwd.q);
+  if (st != RELATTN_OK) return st;
+  *bytes = key_weights_bytes(p->fwd);
+  return RELATTN_OK;
+}
+
+relattn_status relattn_key_weights(const relattn_key_weights_params *p, void *stream) {
+  if (!p) return RELATTN_ERR_INVALID_ARG;
+  const relattn_params &f = p->fwd;
+  const void *k = p->cache ? p->cache->k : f.k;
+  relattn_status st = validate_cached(&f, false, k, k, f.q);
+  if (st != RELATTN_OK) return st;
+  if (!(isfinite(p->decay) && p->decay >= 0.f)) return RELATTN_ERR_INVALID_ARG;
+  KeyWeightArgs x{};
+  const int64_t rows = p->cache ? p->cache->rows
+                       : p->pages ? (int64_t)p->pages->num_pages * p->pages->page_size : (int64_t)f.total_k;
+  if ((st = cache_pages(p->pages, rows, f.max_seqlen_k, &x.pages)) != RELATTN_OK) return st;
+  if (!p->pages && rows < f.total_k) return RELATTN_ERR_INVALID_ARG;
+  if (f.batch == 0 || f.total_q == 0) return RELATTN_OK;
+  if (p->cache) {
+    if ((st = cache_fp4(p->cache, &x.kv)) != RELATTN_OK) return st;
+  } else {
+    x.k = static_cast<const __nv_bfloat16 *>(f.k);
+  }
+  if ((st = cache_positions(p->positions, &x)) != RELATTN_OK) return st;
+  if (!p->weights_out || !aligned(p->weights_out, 4) || !aligned(p->weights_in, 4)) return RELATTN_ERR_INVALID_ARG;
+  const size_t n = (size_t)rows * f.num_heads_kv * sizeof(float);
+  if (p->weights_in && p->weights_in != p->weights_out && overlaps(p->weights_in, n, p->weights_out, n))
+    return RELATTN_ERR_INVALID_ARG;
+  const size_t need = key_weights_bytes(f);
+  if (need > 0 && (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < need)) return RELATTN_ERR_WORKSPACE;
+  if ((st = make_args(&f, &x.a)) != RELATTN_OK) return st;
+  x.a.rdec = static_cast<const float *>(p->workspace);
+  x.lse = f.lse;
+  x.w_in = p->weights_in;
+  x.w_out = p->weights_out;
+  x.decay = p->decay;
+  return cuda_status(launch_key_weights(x, static_cast<cudaStream_t>(stream)));
+}
+
+relattn_status relattn_evict_workspace_size(const relattn_evict_params *p, size_t *bytes) {
+  if (!p || !bytes || p->total_keep < 0 || p->num_heads_kv <= 0) return RELATTN_ERR_INVALID_ARG;
+  *bytes = evict_bytes(*p);
+  return RELATTN_OK;
+}
+
+relattn_status relattn_evict(const relattn_evict_params *p, void *stream) {
+  EvictArgs a;
+  const relattn_status st = validate_evict(p, &a);
+  if (st != RELATTN_OK || a.batch == 0) return st;
+  return cuda_status(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 relattn_status relattn_get_device_error(void *stream) {

@@ -1,0 +1,166 @@
+// cache_fp4.cu -- rows into and out of the 4-bit (NVFP4) K / V cache.
+//
+// The K / V rows of a chunk (the tail of every sequence) are quantised into
+// the cache rows that the attention reads, contiguous or paged, or read back
+// as bf16.  With t = x / factor (one fp32 rounding) the scale of 16 dims is
+// E4M3(max |t| / 6), nearest, ties to even, at most 448, and each code is the
+// E2M1 value nearest to t / scale, ties to even, at most 6.  Both are the
+// roundings of the exact quotients: a border between two codes times the
+// divisor has at most 7 bits, so a dividend that is not exactly on it is at
+// least 2^-24 of it away, and the correctly rounded fp32 quotient then never
+// lands on the border by rounding.
+//
+// One thread takes 16 dims: 32 bytes of bf16 on one side, 8 bytes of codes
+// and a scale byte on the other, so a warp touches 1 KB and 256 + 32 bytes
+// without gaps.  Bound by memory.
+#include "nvfp4.cuh"
+
+namespace relattn {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// sequence of chunk row t: the last b with cu_q[b] <= t
+__device__ __forceinline__ int find_seq(const int32_t *cu_q, int batch, int t) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu_q + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Cache row of chunk row t; false when t belongs to no sequence (left alone).
+__device__ __forceinline__ bool place_row(const Fp4RowArgs &a, int t, long *row) {
+  const int b = find_seq(a.cu_q, a.batch, t);
+  const SeqRows s = seq_rows(a.cu_q, a.cu_k, b, a.total_q, a.pages);
+  if (t < s.q0 || t >= s.q0 + s.lq) {
+    if (!s.ok) atomicOr(a.err, kDevErrSeqlens);
+    return false;                 // behind the last sequence, or inconsistent
+  }
+  if (!s.ok) {
+    atomicOr(a.err, kDevErrSeqlens);
+    return false;
+  }
+  *row = a.pages.row(b, s.k0, s.lk - s.lq + (t - s.q0));
+  if (*row < 0) atomicOr(a.err, kDevErrSeqlens);
+  return true;
+}
+
+__global__ void __launch_bounds__(kRowThreads) relattn_store_fp4_kernel(const Fp4RowArgs a) {
+  const long idx = (long)blockIdx.x * kRowThreads + threadIdx.x;
+  const int per_row = a.Hkv * kFp4Blocks;
+  const long t = idx / per_row;
+  if (t >= a.total_q) return;
+  const int hb = (int)(idx - t * per_row), h = hb / kFp4Blocks;
+  long row;
+  if (!place_row(a, (int)t, &row) || row < 0) return;
+  const bool is_v = blockIdx.y != 0;
+  const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? a.v : a.k) + (t * per_row + hb) * 16);
+  const float *gp = is_v ? a.kv.v_global : a.kv.k_global;
+  const float g = gp ? __ldg(gp + h) : 1.f;
+  const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
+  const uint32_t ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  float x[16];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(ws[i] << 16);
+    x[2 * i + 1] = __uint_as_float(ws[i] & 0xffff0000u);
+    // largest magnitude as bits: a NaN is larger than every number
+    top = max(top, max((ws[i] << 16) & 0x7fff0000u, ws[i] & 0x7fff0000u));
+  }
+  float amax = __uint_as_float(top);
+  if (gp) {
+    amax = __fdiv_rn(amax, g);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], g);
+  }
+  const uint32_t sb = e4m3x2(0.f, __fdiv_rn(amax, 6.f)) & 0xffu;
+  const uint32_t sh = e4m3x2_to_f16(sb);
+  float s;
+  asm("cvt.f32.f16 %0, %1;" : "=f"(s) : "h"((uint16_t)sh));
+  uint32_t codes[2] = {0, 0};
+  if (s > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float lo = __fdiv_rn(x[i], s), hi = __fdiv_rn(x[i + 1], s);
+      uint32_t c;
+      asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\tmov.b32 %0, {c, 0, 0, 0};\n\t}"
+          : "=r"(c) : "f"(hi), "f"(lo));
+      codes[i / 8] |= c << (4 * (i & 7));
+    }
+  }
+  uint8_t *cp = const_cast<uint8_t *>(is_v ? a.kv.v : a.kv.k);
+  uint8_t *sp = const_cast<uint8_t *>(is_v ? a.kv.v_scale : a.kv.k_scale);
+  *reinterpret_cast<uint2 *>(cp + (row * per_row + hb) * 8) = make_uint2(codes[0], codes[1]);
+  sp[row * per_row + hb] = (uint8_t)sb;
+}
+
+__global__ void __launch_bounds__(kRowThreads) relattn_load_fp4_kernel(const Fp4RowArgs a) {
+  const long idx = (long)blockIdx.x * kRowThreads + threadIdx.x;
+  const int per_row = a.Hkv * kFp4Blocks;
+  const long t = idx / per_row;
+  if (t >= a.total_q) return;
+  const int hb = (int)(idx - t * per_row), h = hb / kFp4Blocks;
+  long row;
+  if (!place_row(a, (int)t, &row)) return;
+  const bool is_v = blockIdx.y != 0;
+  const uint8_t *cp = is_v ? a.kv.v : a.kv.k, *sp = is_v ? a.kv.v_scale : a.kv.k_scale;
+  const float *gp = is_v ? a.kv.v_global : a.kv.k_global;
+  const float g = gp ? __ldg(gp + h) : 1.f;
+  uint2 c = make_uint2(0, 0);
+  uint32_t sb = 0;
+  if (row >= 0) {                 // a row outside the cache reads as zero
+    c = __ldg(reinterpret_cast<const uint2 *>(cp + (row * per_row + hb) * 8));
+    sb = __ldg(sp + row * per_row + hb);
+  }
+  const uint32_t sh = e4m3x2_to_f16(sb);
+  float s;
+  asm("cvt.f32.f16 %0, %1;" : "=f"(s) : "h"((uint16_t)sh));
+  uint32_t o[8];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t f[4];
+    e2m1x8_to_f16(w ? c.y : c.x, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      asm("cvt.f32.f16 %0, %1;" : "=f"(lo) : "h"((uint16_t)(f[i] & 0xffffu)));
+      asm("cvt.f32.f16 %0, %1;" : "=f"(hi) : "h"((uint16_t)(f[i] >> 16)));
+      // code * scale is exact (6 bits); one fp32 product, then the bf16 rounding
+      o[4 * w + i] = pack_bf16x2(lo * s * g, hi * s * g);
+    }
+  }
+  uint4 *dst = reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(is_v ? a.v : a.k) + (t * per_row + hb) * 16);
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+cudaError_t row_grid(const Fp4RowArgs &a, dim3 *grid) {
+  const long n = ((long)a.total_q * a.Hkv * kFp4Blocks + kRowThreads - 1) / kRowThreads;
+  if (n > 0x7fffffffL) return cudaErrorInvalidValue;
+  *grid = dim3((unsigned)n, 2);
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_store_fp4(const Fp4RowArgs &a, cudaStream_t stream) {
+  dim3 grid;
+  const cudaError_t e = row_grid(a, &grid);
+  if (e != cudaSuccess) return e;
+  relattn_store_fp4_kernel<<<grid, kRowThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_load_fp4(const Fp4RowArgs &a, cudaStream_t stream) {
+  dim3 grid;
+  const cudaError_t e = row_grid(a, &grid);
+  if (e != cudaSuccess) return e;
+  relattn_load_fp4_kernel<<<grid, kRowThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace relattn

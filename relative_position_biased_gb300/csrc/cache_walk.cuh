@@ -1,0 +1,129 @@
+// cache_walk.cuh -- what the kernels that stream a K / V cache in warps of 32
+// keys share: the sequences' rows, the order in which tiles are walked, and
+// where a key's cache row lies.
+#pragma once
+
+#include "nvfp4.cuh"
+
+namespace relattn {
+
+struct Unit {
+  SeqRows s;
+  int b, h, rb;
+  int qbase;       // position of the sequence's first query row
+  int lo;          // first key, a multiple of 32
+  int nrows;       // query rows of the block (<= 0: none)
+};
+
+// The sequence's rows and lengths; lo / tiles of its units.  Zero tiles where
+// there is nothing to do or the lengths are inconsistent.
+__device__ __forceinline__ int unit_tiles(const WalkArgs &p, int b, SeqRows *sp, int *lo) {
+  const SeqRows s = seq_rows(p.a.cu_q, p.a.cu_k, b, p.a.total_q, p.pages);
+  *sp = s;
+  *lo = 0;
+  if (!s.ok || s.lq > p.a.max_q || s.lk > p.a.max_k || first_query_pos(s, p.q_pos, b) < 0) return -1;
+  if (s.lq == 0) return 0;
+  if (p.a.window > 0 && !p.key_pos) *lo = max(0, s.lk - s.lq - p.a.window + 1) & ~31;
+  return (s.lk - *lo + kWalkTile - 1) / kWalkTile;
+}
+
+// Row n of the unit's block: its index among all (token, head) rows, and token.
+__device__ __forceinline__ long unit_row(const WalkArgs &p, const Unit &u, int n, int *tok) {
+  const int rr = u.rb * kFp4Rows + n;
+  *tok = rr / p.a.group;
+  return (long)(u.s.q0 + *tok) * p.a.Hq + u.h * p.a.group + (rr - *tok * p.a.group);
+}
+
+// First cache row of 32 keys from key0 (they share a page), -1 outside the cache.
+__device__ __forceinline__ long group_row(const WalkArgs &p, const Unit &u, int key0) {
+  if (key0 >= u.s.lk) return -1;
+  const long r = p.pages.row(u.b, u.s.k0, key0);
+  if (r < 0) atomicOr(p.a.err, kDevErrSeqlens);
+  return r;
+}
+
+// Last i in [0, n) with v[i] <= x (0 if none): the sequence that holds x when v
+// is its running start.
+__device__ __forceinline__ int last_not_above(const int *v, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Running tile counts of the sequences into prefix[0 .. batch] (batch <=
+// kWalkBatch), by a CTA of THREADS; returns the total.  Inconsistent sequences
+// hold no tile and are recorded once.
+template <int THREADS>
+__device__ __forceinline__ int tile_prefix(const WalkArgs &p, int *prefix, int *wsum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int base = 0;
+  for (int b0 = 0; b0 < p.a.batch; b0 += THREADS) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < p.a.batch) {
+      SeqRows s;
+      int lo;
+      n = unit_tiles(p, b, &s, &lo);
+      if (n < 0) {
+        n = 0;
+        if (blockIdx.x == 0) atomicOr(p.a.err, kDevErrSeqlens);
+      }
+    }
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int before = base, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += wsum[w];
+      all += wsum[w];
+    }
+    if (b < p.a.batch) prefix[b] = before + inc - n;
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) prefix[p.a.batch] = base;
+  __syncthreads();
+  return base;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+// Power of two that brings a magnitude to 2^14 .. 2^15 (from its fp32 bits),
+// and its inverse: f16 then holds a bf16 row exactly down to 2^-38 of its
+// largest element.
+__device__ __forceinline__ float f16_row_scale(uint32_t top, float *back) {
+  const int e = min(max((int)(top >> 23) - 127, -100), 127);
+  *back = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+  return __uint_as_float((uint32_t)(14 - e + 127) << 23);
+}
+
+}  // namespace relattn

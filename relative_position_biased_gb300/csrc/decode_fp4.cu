@@ -1,0 +1,673 @@
+// decode_fp4.cu -- split-KV decode of relative attention over the 4-bit
+// (NVFP4) K / V cache.
+//
+// The computation of the other decodes (page "SGLang and Miles Add Day-0
+// Support for Inkling", section "Attention with Relative Positional
+// Embedding"; the split of the keys on the page "vLLM Day-0 support for TML
+// Inkling"), x(i,j) = s(i) (alpha q_i . k_j + [0 <= d < E] r_i . P[:, d]),
+// out = softmax(x) v, with k and v the values the cache stands for and d the
+// difference of two positions: the rows' own indices, or (a cache that
+// eviction has thinned out) positions given per row and kv head.
+//
+// What bounds it: a key of one head is 144 bytes and 256 values.  The bytes
+// alone take 21 ps at the copy rate; each value has to become an f16 operand,
+// and a conversion (two values a lane) runs at about 1.2 warp instructions a
+// clock and SM against 2 for the f16 multiply by the scale and 0.5 for the
+// matrix instruction.  So the kernel is written around few instructions a
+// key, on warp-level matrix instructions fed from registers: the tcgen05 path
+// would need the values in shared memory, 2 bytes each, which costs more than
+// the products.
+//   - Keys go along the matrix instruction's 16 rows, query rows along its 8
+//     columns: S^T = K q^T, O^T += V^T P^T.  One token of a GQA-8 group fills
+//     it; with 16 rows a unit takes two columns sets.
+//   - The dims of a product may be summed in any order, so a lane's share of a
+//     key is 16 contiguous bytes: 32 dims, two scales.  No value crosses
+//     lanes, and q is laid out to match once per unit.
+//   - For V the operand pairs two keys of one dim: the nibbles of two code
+//     words are interleaved before the conversion (four logical operations
+//     for 16 values), and a lane's 16 dims are one scale block.
+//   - A product code * scale has 6 bits and is exact in f16; the factor of the
+//     head is folded into the logit scale and the output.  q is bf16 and at
+//     most 2^38 below its row's maximum exact in f16 after a power-of-two
+//     scaling per row.  P is rounded to f16 (11 bits, half a step 2^-12 of
+//     the value), scaled by 2^7 so that what is lost below f16's range is
+//     2^-31 of the largest; everything else is fp32.
+//
+// A warp streams 32 keys at a time through its own ring of asynchronous
+// copies: no barrier among warps until the end of a piece.  The running
+// maximum is raised only when a logit passes it by more than 8 (base 2).
+//
+// Work split: the units (sequence, kv head, 16-row block) hold ceil(keys/128)
+// tiles each; they are laid end to end, head and row block outermost so that
+// the heads of one key range are read at the same time, and CTA c takes tiles
+// [c C, (c+1) C).  A piece of a unit writes its partial to slot c - (first
+// CTA of the unit); the unit's first piece marks the slots no piece fills.
+#include <algorithm>
+
+#include "cache_walk.cuh"
+
+namespace relattn {
+namespace {
+
+constexpr int FW = 4, FT = FW * 32;          // warps and threads of a CTA
+constexpr int FK = kWalkTile / FW;         // keys a warp takes at a time
+static_assert(FK == 32, "two 16-key groups");
+constexpr int F_STAGES = 3;
+// a stage of one warp: K codes, V codes, K scales, V scales
+constexpr int FS_V = FK * kFp4RowBytes, FS_KS = 2 * FS_V, FS_VS = FS_KS + FK * kFp4Blocks;
+constexpr int FS_BYTES = FS_VS + FK * kFp4Blocks;
+constexpr int F_RING = FW * F_STAGES * FS_BYTES;
+static_assert(F_RING >= FW * kFp4Rows * kHeadDim * 4 + 2 * FW * kFp4Rows * 4, "the merge reuses the ring");
+constexpr float kPShift = 7.f;               // P is held times 2^7
+constexpr float kRaise = 8.f;                // the maximum is raised past this excess
+
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }
+
+// Copies 32 keys into one stage of the warp's ring.  Within 16 keys, key k
+// (k = i + 4 j, j in {0, 1}, +8) is row 2 i + j (+8) of the matrix operand: K
+// is stored in operand order (a quarter warp then reads 128 contiguous
+// bytes), V in key order with its 16-byte chunks exchanged every other pair
+// of keys (a half warp reads keys t = 0..3 from distinct banks).
+__device__ __forceinline__ void issue_group(const Fp4DecodeArgs &p, const Unit &u, uint32_t st, int key0, long row0,
+                                            int lane) {
+  const long rb = (long)p.a.Hkv * kFp4RowBytes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = (lane >> 2) + 8 * i, c = lane & 3;
+    const bool ok = row0 >= 0 && key0 + k < u.s.lk;
+    const long off = ok ? (row0 + k) * rb + u.h * kFp4RowBytes + c * 16 : 0;
+    const int k16 = k & 15, slot = (k & 16) + (k16 & 8) + 2 * (k16 & 3) + ((k16 >> 2) & 1);
+    cp_async16(st + slot * kFp4RowBytes + c * 16, p.kv.k + off, ok);
+    cp_async16(st + FS_V + k * kFp4RowBytes + ((c ^ (((k >> 1) & 1) << 1)) << 4), p.kv.v + off, ok);
+  }
+  const bool ok = row0 >= 0 && key0 + lane < u.s.lk;
+  const long soff = ok ? ((row0 + lane) * p.a.Hkv + u.h) * kFp4Blocks : 0;
+  cp_async8(st + FS_KS + lane * kFp4Blocks, p.kv.k_scale + soff, ok);
+  cp_async8(st + FS_VS + lane * kFp4Blocks, p.kv.v_scale + soff, ok);
+}
+
+// One piece: tiles [t0, t0 + n) of unit u, partial into `slot` (or the result
+// itself when there is one slot).
+template <int NT, bool POS>
+__device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u, int t0, int n, int slot,
+                                          bool first_piece, uint8_t *smem) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_addr(smem) + warp * (F_STAGES * FS_BYTES);
+  const int k_first = u.lo + t0 * kWalkTile + warp * FK;
+  const unsigned full = 0xffffffffu;
+
+  // ---- the first copies, then the query rows while they fly
+  long next_row = -1;                       // cache row of the next group to copy
+  int pos_next = 0x7fffffff;                // its key's position (lane = key)
+  int pos_q[F_STAGES];                      // positions of the groups in flight
+  auto fetch_pos = [&](int key0, long row) {
+    int kp = 0x7fffffff;                    // masked for every row
+    if (POS && row >= 0 && key0 + lane < u.s.lk) {
+      kp = __ldg(p.key_pos + (long)u.h * p.pages.rows + row + lane);
+      if (kp < 0) kp = 0x7fffffff;
+    }
+    return kp;
+  };
+#pragma unroll
+  for (int i = 0; i < F_STAGES - 1; ++i) {
+    pos_q[i] = 0x7fffffff;
+    if (i < n) {
+      const int key0 = k_first + i * kWalkTile;
+      const long row = group_row(p, u, key0);
+      if (POS) pos_q[i] = fetch_pos(key0, row);
+      issue_group(p, u, ring + i * FS_BYTES, key0, row, lane);
+    }
+    cp_async_commit();
+  }
+  if (F_STAGES - 1 < n) {
+    next_row = group_row(p, u, k_first + (F_STAGES - 1) * kWalkTile);
+    if (POS) pos_next = fetch_pos(k_first + (F_STAGES - 1) * kWalkTile, next_row);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // R, where it was launched before this kernel
+
+  uint32_t qf[NT][16];                      // row 8 nt + g, dims 32 t .. 32 t + 31
+  float coef[NT][2], bscale[NT][2];         // of rows 8 nt + 2 t, + 1
+  int qp[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int nrow = nt * 8 + g;
+    int tok = 0;
+    float back = 1.f;
+    if (nrow < u.nrows) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + unit_row(p, u, nrow, &tok) * kHeadDim + t * 32);
+      uint4 w[4];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __ldg(src + i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qf[nt][4 * i + j] = ws[j];
+          top = max(top, max((ws[j] << 16) & 0x7fff0000u, ws[j] & 0x7fff0000u));
+        }
+      }
+      const unsigned quad = 0xfu << (lane & ~3);
+      top = max(top, __shfl_xor_sync(quad, top, 1));
+      top = max(top, __shfl_xor_sync(quad, top, 2));
+      const float up = f16_row_scale(top, &back);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        qf[nt][i] = pack_f16x2(__uint_as_float(qf[nt][i] << 16) * up, __uint_as_float(qf[nt][i] & 0xffff0000u) * up);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) qf[nt][i] = 0;
+    }
+    __syncwarp();
+    const float kg = p.kv.k_global ? __ldg(p.kv.k_global + u.h) : 1.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int m = nt * 8 + 2 * t + c;
+      const float bk = __shfl_sync(full, back, (2 * t + c) * 4);
+      int tk;
+      unit_row(p, u, m, &tk);
+      const bool live = m < u.nrows;
+      const float s = live ? log_scale(u.qbase + tk, p.a.inv_ln_base) : 0.f;
+      qp[nt][c] = live ? u.qbase + tk : -1;   // rows past the block see no key
+      coef[nt][c] = p.a.alpha_log2e * s * kg * bk;
+      bscale[nt][c] = s * kLog2e;
+    }
+  }
+  int qmin, qmax;
+  {
+    int tk;
+    unit_row(p, u, 0, &tk);
+    qmin = u.qbase + tk;
+    unit_row(p, u, u.nrows - 1, &tk);
+    qmax = u.qbase + tk;
+  }
+  const unsigned wlim = p.a.window > 0 ? (unsigned)p.a.window : 0x80000000u;
+
+  float acc[8][NT][4];                      // O^T: dims 16 g + 2 m (+1), rows 8 nt + 2 t (+1)
+  float mref[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) mref[nt][c] = -INFINITY, l[nt][c] = 0.f;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) acc[m][nt][0] = acc[m][nt][1] = acc[m][nt][2] = acc[m][nt][3] = 0.f;
+  }
+
+  int buf = 0;
+  for (int it = 0; it < n; ++it) {
+    const int key0 = k_first + it * kWalkTile;
+    cp_async_wait<F_STAGES - 2>();
+    __syncwarp();                            // the stage has landed; the one before it is read
+    {
+      const int nb = buf == 0 ? F_STAGES - 1 : buf - 1;
+      if (it + F_STAGES - 1 < n) issue_group(p, u, ring + nb * FS_BYTES, key0 + (F_STAGES - 1) * kWalkTile, next_row, lane);
+      cp_async_commit();
+    }
+    const int pos_lane = POS ? pos_q[0] : 0;
+    if (POS) {
+#pragma unroll
+      for (int i = 0; i + 2 < F_STAGES; ++i) pos_q[i] = pos_q[i + 1];
+      pos_q[F_STAGES - 2] = pos_next;
+    }
+    if (it + F_STAGES < n) {
+      next_row = group_row(p, u, key0 + F_STAGES * kWalkTile);
+      if (POS) pos_next = fetch_pos(key0 + F_STAGES * kWalkTile, next_row);
+    }
+    const uint32_t st = ring + buf * FS_BYTES;
+    buf = buf == F_STAGES - 1 ? 0 : buf + 1;
+    if (key0 >= u.s.lk) continue;            // past the sequence: nothing for this warp
+
+    // ---- S^T = K q^T
+    float x[2][NT][4];
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[gr][nt][0] = x[gr][nt][1] = x[gr][nt][2] = x[gr][nt][3] = 0.f;
+      const uint32_t kb = st + gr * 16 * kFp4RowBytes + t * 16;
+      const uint4 w0 = lds128(kb + g * kFp4RowBytes), w1 = lds128(kb + (g + 8) * kFp4RowBytes);
+      const int kg16 = (g >> 1) + 4 * (g & 1);
+      const uint32_t sb = st + FS_KS + (gr * 16 + kg16) * kFp4Blocks + 2 * t;
+      const uint32_t s0 = e4m3x2_to_f16(lds_u16(sb)), s1 = e4m3x2_to_f16(lds_u16(sb + 8 * kFp4Blocks));
+      const uint32_t ww0[4] = {w0.x, w0.y, w0.z, w0.w}, ww1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t m0 = __byte_perm(s0, 0, w < 2 ? 0x1010 : 0x3232);
+        const uint32_t m1 = __byte_perm(s1, 0, w < 2 ? 0x1010 : 0x3232);
+        uint32_t f0[4], f1[4];
+        e2m1x8_to_f16(ww0[w], f0);
+        e2m1x8_to_f16(ww1[w], f1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f0[i] = hmul2(f0[i], m0), f1[i] = hmul2(f1[i], m1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16_16816(x[gr][nt], f0[0], f1[0], f0[1], f1[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
+          mma_f16_16816(x[gr][nt], f0[2], f1[2], f0[3], f1[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+        }
+      }
+    }
+
+    // ---- logits: scale, bias, mask
+    const bool edge = POS || key0 + FK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
+    int kp[2][2];                            // positions of the lane's keys
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int k = gr * 16 + hf * 8 + (g >> 1) + 4 * (g & 1);
+        kp[gr][hf] = POS ? __shfl_sync(full, pos_lane, k) : key0 + k;
+      }
+    const bool band = p.a.E > 0 && (POS ? __any_sync(full, pos_lane != 0x7fffffff && qmin - pos_lane < p.a.E)
+                                        : qmin - (key0 + FK - 1) < p.a.E);
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[gr][nt][i] *= coef[nt][i & 1];
+    if (band) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int m = nt * 8 + 2 * t + c;
+          int tk;
+          const float *R = p.a.rdec + unit_row(p, u, min(m, u.nrows - 1), &tk) * p.a.E;
+#pragma unroll
+          for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const unsigned d = (unsigned)qp[nt][c] - (unsigned)kp[gr][hf];
+              if (d < (unsigned)p.a.E) x[gr][nt][hf * 2 + c] = fmaf(R[d], bscale[nt][c], x[gr][nt][hf * 2 + c]);
+            }
+        }
+    }
+    if (edge) {
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((unsigned)qp[nt][i & 1] - (unsigned)kp[gr][i >> 1] >= wlim) x[gr][nt][i] = -INFINITY;
+    }
+
+    // ---- the running maximum, raised only when a logit passes it by more than kRaise
+    bool need = false;
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) need |= x[gr][nt][i] > mref[nt][i & 1] + kRaise;
+    if (__any_sync(full, need)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float m = fmaxf(fmaxf(x[0][nt][c], x[0][nt][c + 2]), fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+          m = fmaxf(m, __shfl_xor_sync(full, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(full, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(full, m, 16));
+          m = fmaxf(m, mref[nt][c]);
+          const float f = m == -INFINITY ? 1.f : fast_exp2(mref[nt][c] - m);
+          mref[nt][c] = m;
+          l[nt][c] *= f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) acc[d][nt][c] *= f, acc[d][nt][c + 2] *= f;
+        }
+    }
+    uint32_t pb[2][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mo[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) mo[c] = (mref[nt][c] == -INFINITY ? 0.f : mref[nt][c]) - kPShift;
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = fast_exp2(x[gr][nt][i] - mo[i & 1]);
+        l[nt][0] += e[0] + e[2];
+        l[nt][1] += e[1] + e[3];
+        // key g x rows 2t, 2t+1  ->  row g x keys 2t, 2t+1
+        pb[gr][nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+        pb[gr][nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
+      }
+    }
+
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      // the lane's keys, in operand order 2t, 2t+1, 2t+8, 2t+9: t, 4+t, 8+t, 12+t; dims 16 g ..
+      const uint32_t vb = st + FS_V + (gr * 16 + t) * kFp4RowBytes + ((((g >> 1) ^ (((t >> 1) & 1) << 1))) << 4) + (g & 1) * 8;
+      const uint32_t sb = st + FS_VS + (gr * 16 + t) * kFp4Blocks + g;
+      uint2 w[4];
+      uint32_t sc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = lds64(vb + 4 * j * kFp4RowBytes);
+        sc[j] = lds_u8(sb + 4 * j * kFp4Blocks);
+      }
+      bool split_rows = false;               // a NaN scale that only some rows may see
+      int vk[4];
+      if (edge) {
+        // scales of keys that no row sees become zero: their values (a NaN
+        // scale, an unwritten row) do not reach the sum
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = gr * 16 + 4 * j + t;
+          vk[j] = POS ? __shfl_sync(full, pos_lane, k) : key0 + k;
+          const bool any = vk[j] <= qmax && (unsigned)max(qmin - vk[j], 0) < wlim;
+          const bool all = vk[j] <= qmin && (unsigned)(qmax - vk[j]) < wlim;
+          if (!any) sc[j] = 0;
+          bad |= any && !all && (sc[j] & 0x7f) == 0x7f;
+        }
+        split_rows = __any_sync(full, bad);
+      }
+      // the operand's two f16 scale pairs from four scale bytes
+      auto products = [&](uint32_t s0, uint32_t s1, auto &&use) {
+        s0 = e4m3x2_to_f16(s0);
+        s1 = e4m3x2_to_f16(s1);
+#pragma unroll
+        for (int hw = 0; hw < 2; ++hw) {
+          const uint32_t A = hw ? w[0].y : w[0].x, B = hw ? w[1].y : w[1].x;
+          const uint32_t C = hw ? w[2].y : w[2].x, E = hw ? w[3].y : w[3].x;
+          const uint32_t nib = 0x0f0f0f0fu;
+          uint32_t f0[4], f1[4], f2[4], f3[4];
+          e2m1x8_to_f16((A & nib) | ((B << 4) & ~nib), f0);
+          e2m1x8_to_f16(((A >> 4) & nib) | (B & ~nib), f1);
+          e2m1x8_to_f16((C & nib) | ((E << 4) & ~nib), f2);
+          e2m1x8_to_f16(((C >> 4) & nib) | (E & ~nib), f3);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            use(4 * hw + i, hmul2(f0[i], s0), hmul2(f1[i], s0), hmul2(f2[i], s1), hmul2(f3[i], s1));
+        }
+      };
+      if (!split_rows) {
+        products(sc[0] | (sc[1] << 8), sc[2] | (sc[3] << 8),
+                 [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                   for (int nt = 0; nt < NT; ++nt)
+                     mma_f16_16816(acc[m][nt], a0, a1, a2, a3, pb[gr][nt][0], pb[gr][nt][1]);
+                 });
+      } else {
+        // one row at a time, without the keys that it does not see; a NaN
+        // operand spoils every column of a product, so only the row's is kept
+#pragma unroll 1
+        for (int only = 0; only < u.nrows; ++only) {
+          int tk;
+          unit_row(p, u, only, &tk);
+          const int qr = u.qbase + tk;
+          uint32_t s0 = 0, s1 = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v = (unsigned)qr - (unsigned)vk[j] < wlim ? sc[j] : 0u;
+            if (j < 2) s0 |= v << (8 * j);
+            else s1 |= v << (8 * (j - 2));
+          }
+          products(s0, s1, [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float o[4] = {acc[m][nt][0], acc[m][nt][1], acc[m][nt][2], acc[m][nt][3]};
+              mma_f16_16816(o, a0, a1, a2, a3, pb[gr][nt][0], pb[gr][nt][1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (nt * 8 + 2 * t + (i & 1) == only) acc[m][nt][i] = o[i];
+            }
+          });
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+
+  // ---- merge the warps
+  __syncthreads();                           // every ring is idle
+  float *so = reinterpret_cast<float *>(smem);                   // [warp][row][128]
+  float *sm = so + FW * kFp4Rows * kHeadDim, *sl = sm + FW * kFp4Rows;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float z = l[nt][c];
+      z += __shfl_xor_sync(full, z, 4);
+      z += __shfl_xor_sync(full, z, 8);
+      z += __shfl_xor_sync(full, z, 16);
+      const int row = nt * 8 + 2 * t + c;
+      if (g == 0) {
+        sm[warp * kFp4Rows + row] = mref[nt][c];
+        sl[warp * kFp4Rows + row] = z;
+      }
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+        *reinterpret_cast<float2 *>(so + (warp * kFp4Rows + row) * kHeadDim + 16 * g + 2 * m) =
+            make_float2(acc[m][nt][c], acc[m][nt][c + 2]);
+    }
+  __syncthreads();
+  const float vg = p.kv.v_global ? __ldg(p.kv.v_global + u.h) : 1.f;
+  const long rows_all = (long)p.a.total_q * p.a.Hq;
+  for (int row = 0; row < u.nrows; ++row) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < FW; ++w) m = fmaxf(m, sm[w * kFp4Rows + row]);
+    float o = 0.f, z = 0.f;
+#pragma unroll
+    for (int w = 0; w < FW; ++w) {
+      const float mw = sm[w * kFp4Rows + row], zw = sl[w * kFp4Rows + row];
+      // a warp without a visible key has an empty sum; a NaN sum stays one
+      const float f = mw == -INFINITY ? (zw == 0.f ? 0.f : 1.f) : fast_exp2(mw - m);
+      z = fmaf(zw, f, z);
+      o = fmaf(so[(w * kFp4Rows + row) * kHeadDim + tid], f, o);
+    }
+    const float out = z == 0.f ? 0.f : o / z * vg;
+    const float lse = z == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) - kPShift + log2f(z)) * kLn2;
+    int tk;
+    const long grow = unit_row(p, u, row, &tk);
+    if (p.splits == 1) {
+      p.a.out[grow * kHeadDim + tid] = __float2bfloat16_rn(out);
+      if (tid == 0) p.a.lse[(grow % p.a.Hq) * p.a.total_q + grow / p.a.Hq] = lse;
+    } else {
+      p.a.o_part[((long)slot * rows_all + grow) * kHeadDim + tid] = out;
+      if (tid == 0) p.a.lse_part[(long)slot * rows_all + grow] = lse;
+    }
+  }
+  __syncthreads();                           // the merge buffers become rings again
+}
+
+template <int NT, bool POS>
+__global__ void __launch_bounds__(FT, ctas_per_sm(NT)) relattn_decode_fp4_kernel(const __grid_constant__ Fp4DecodeArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int prefix[kWalkBatch + 1];
+  __shared__ int wsum[FW];
+  const int tid = threadIdx.x;
+  Unit u;
+  if (p.splits == 1) {                       // one CTA per unit
+    const int unit = blockIdx.x;
+    const int hr = unit / p.a.batch;
+    u.b = unit - hr * p.a.batch;
+    u.h = hr / p.row_blocks;
+    u.rb = hr - u.h * p.row_blocks;
+    const int n = unit_tiles(p, u.b, &u.s, &u.lo);
+    u.nrows = min(kFp4Rows, u.s.lq * p.a.group - u.rb * kFp4Rows);
+    if (n < 0 && tid == 0) atomicOr(p.a.err, kDevErrSeqlens);
+    if (n > 0 && u.nrows > 0) {
+      u.qbase = first_query_pos(u.s, p.q_pos, u.b);
+      run_piece<NT, POS>(p, u, 0, n, 0, true, smem);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const int base = tile_prefix<FT>(p, prefix, wsum);
+  const long per = base, total = per * p.a.Hkv * p.row_blocks;
+  const long C = max((total + gridDim.x - 1) / gridDim.x, (long)p.c_min);
+  long x = blockIdx.x * C;
+  const long end = min(total, x + C);
+  while (x < end) {
+    const int hr = (int)(x / per), xb = (int)(x - hr * per);
+    u.b = last_not_above(prefix, p.a.batch, xb);   // it holds tile xb
+    u.h = hr / p.row_blocks;
+    u.rb = hr - u.h * p.row_blocks;
+    const int tiles = unit_tiles(p, u.b, &u.s, &u.lo), t0 = xb - prefix[u.b];
+    const int n = (int)min((long)(tiles - t0), end - x);
+    u.nrows = min(kFp4Rows, u.s.lq * p.a.group - u.rb * kFp4Rows);
+    if (u.nrows > 0) {
+      u.qbase = first_query_pos(u.s, p.q_pos, u.b);
+      const long ustart = hr * per + prefix[u.b], first = ustart / C;
+      if (t0 == 0) {                         // mark the slots that no piece fills
+        const int used = (int)((ustart + tiles - 1) / C - first) + 1;
+        const int empty = (p.splits - used) * u.nrows;
+        for (int i = tid; i < empty; i += FT) {
+          int tk;
+          const long grow = unit_row(p, u, i % u.nrows, &tk);
+          p.a.lse_part[(long)(used + i / u.nrows) * p.a.total_q * p.a.Hq + grow] = -INFINITY;
+        }
+      }
+      run_piece<NT, POS>(p, u, t0, n, (int)(blockIdx.x - first), t0 == 0, smem);
+    }
+    x += n;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// out / lse of one row from its partials; rows of no (valid) sequence are left
+// as they are.  A CTA per row, its warps taking the slots in turn.
+__global__ void __launch_bounds__(FT) relattn_decode_fp4_combine_kernel(const __grid_constant__ Fp4DecodeArgs p) {
+  __shared__ float red_m[FW], red_z[FW];
+  __shared__ float4 red_o[FW][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long row = blockIdx.x, rows = (long)p.a.total_q * p.a.Hq;
+  const int tq = (int)(row / p.a.Hq);
+  SeqRows s;
+  int first;
+  const int tiles = unit_tiles(p, last_not_above(p.a.cu_q, p.a.batch, tq), &s, &first);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tiles <= 0 || tq < s.q0 || tq >= s.q0 + s.lq) return;
+  float m = -INFINITY;
+  bool nan = false;
+  for (int i = threadIdx.x; i < p.splits; i += FT) {
+    const float v = p.a.lse_part[i * rows + row];
+    m = fmaxf(m, v);
+    nan |= v != v;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red_m[warp] = m;
+  nan = __syncthreads_or(nan);
+#pragma unroll
+  for (int w = 0; w < FW; ++w) m = fmaxf(m, red_m[w]);
+  if (nan) m = 0.f;                          // the weights below turn NaN by themselves
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float z = 0.f;
+  if (m != -INFINITY)
+    for (int i = warp; i < p.splits; i += FW) {
+      const float ls = p.a.lse_part[i * rows + row];
+      if (ls == -INFINITY) continue;
+      const float4 v = *reinterpret_cast<const float4 *>(p.a.o_part + (i * rows + row) * kHeadDim + lane * 4);
+      const float f = exp2f((ls - m) * kLog2e);
+      z += f;
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+  red_o[warp][lane] = acc;
+  if (lane == 0) red_z[warp] = z;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < FW; ++w) {
+    const float4 o = red_o[w][lane];
+    acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
+    z += red_z[w];
+  }
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  uint2 packed;
+  packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2 *>(p.a.out + row * kHeadDim + lane * 4) = packed;
+  if (lane == 0) p.a.lse[(row - (long)tq * p.a.Hq) * p.a.total_q + tq] = z == 0.f ? -INFINITY : m + logf(z);
+}
+
+template <int NT, bool POS>
+cudaError_t launch_main(const Fp4DecodeArgs &p, cudaStream_t stream) {
+  static std::atomic<bool> done[kMaxDevicesAttr];
+  auto *kernel = relattn_decode_fp4_kernel<NT, POS>;
+  const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), F_RING, done);
+  if (e != cudaSuccess) return e;
+  const long grid = p.splits == 1 ? (long)p.a.batch * p.a.Hkv * p.row_blocks : (long)p.a.sms * ctas_per_sm(NT);
+  if (grid > 0x7fffffffL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(FT);
+  cfg.dynamicSmemBytes = F_RING;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.a.E > 0 ? 1 : 0;          // behind the R kernel
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+bool two_columns(const KernelArgs &a) { return a.max_q * a.group > 8; }
+
+}  // namespace
+
+// Slots, workspace and the least tiles a CTA takes.  A unit holds at most U
+// tiles and meets at most ceil(U / C) + 1 ranges of C tiles, so C >= U /
+// (slots - 1) keeps its pieces within the slots.  False when the sizes do not
+// fit the kernel's index types.
+bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want_splits, Fp4DecodePlan *plan) {
+  const int rows = a.max_q * a.group;
+  plan->row_blocks = (rows + kFp4Rows - 1) / kFp4Rows;
+  long vis = a.max_k;
+  if (a.window > 0 && !positions) vis = std::min<long>(vis, (long)a.window + a.max_q - 1 + FK - 1);
+  const long U = (vis + kWalkTile - 1) / kWalkTile;
+  const long keys = std::min<long>(total_k, (long)a.batch * vis);
+  const long heads = (long)a.Hkv * plan->row_blocks;
+  const long total = (keys / kWalkTile + a.batch) * heads;
+  const long grid = (long)a.sms * ctas_per_sm(two_columns(a) ? 2 : 1);
+  constexpr long kMinTiles = 4;              // a piece's fixed cost is that of a few tiles
+  long C = std::max<long>((total + grid - 1) / grid, kMinTiles);
+  long splits = want_splits > 0 ? want_splits : U <= C ? 1 : (U + C - 1) / C + 1;
+  if (a.batch > kWalkBatch) splits = 1;
+  if (splits > 1) splits = std::min<long>(splits, U + 1);
+  plan->splits = (int)splits;
+  plan->c_min = splits > 1 ? (int)std::max<long>((U + splits - 2) / (splits - 1), want_splits > 0 ? 1 : kMinTiles) : 0;
+  const size_t rows_all = (size_t)a.total_q * a.Hq;
+  size_t end = 0;
+  plan->lse_offset = 0;
+  if (splits > 1) {
+    plan->lse_offset = ((size_t)splits * rows_all * kHeadDim * sizeof(float) + 255) / 256 * 256;
+    end = plan->lse_offset + (size_t)splits * rows_all * sizeof(float);
+  }
+  plan->rel_offset = (end + 255) / 256 * 256;
+  plan->ws_bytes = a.E > 0 ? plan->rel_offset + rows_all * a.E * sizeof(float) : end;
+  return splits <= 65535 && rows_all <= 0x7fffffffUL && (long)a.batch * heads <= 0x7fffffffL;
+}
+
+cudaError_t launch_decode_fp4(const Fp4DecodeArgs &p, cudaStream_t stream) {
+  if (p.a.E > 0) {
+    const cudaError_t e = launch_rel_bias(p.a.r, p.a.P, (long)p.a.total_q * p.a.Hq, p.a.rd, p.a.E,
+                                          const_cast<float *>(p.a.rdec), stream);
+    if (e != cudaSuccess) return e;
+  }
+  cudaError_t e;
+  if (two_columns(p.a)) e = p.key_pos ? launch_main<2, true>(p, stream) : launch_main<2, false>(p, stream);
+  else e = p.key_pos ? launch_main<1, true>(p, stream) : launch_main<1, false>(p, stream);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long)p.a.total_q * p.a.Hq));
+  cfg.blockDim = dim3(FT);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, relattn_decode_fp4_combine_kernel, p);
+}
+
+}  // namespace relattn

@@ -1,0 +1,553 @@
+// key_weights.cu -- the attention weight that every cached key receives,
+//   w_out[h][j] = decay * w_in[h][j] + sum_{i, heads of group h} exp(x_ij - lse_i),
+// from the saved logsumexp of the rows (x_ij as in the decode kernels: page
+// "SGLang and Miles Add Day-0 Support for Inkling", section "Attention with
+// Relative Positional Embedding").  It is what eviction ranks the keys by.
+// With lse known there is no running maximum and no order among keys: a key's
+// sum stays in registers from its first row to its last (fp32, one order, no
+// atomics), and only K is read.
+//
+// Keys go along the matrix instruction's 16 rows, query rows along its 8
+// columns, so a lane holds two keys' logits for two rows and a sum over rows
+// is a sum in the lane and, once at the end, over four lanes.  K is bf16 (bf16
+// products) or 4-bit (codes times scales, exact in f16, as in decode_fp4.cu).
+//
+//   few rows (at most 16 per kv head, a decode step): the walk of the decode,
+//     a warp streams 32 keys at a time through its own ring; bound by K's bytes.
+//   many rows: a CTA holds 128 keys as operands in registers and takes the
+//     rows that see them 32 at a time through shared memory; bound by the
+//     matrix instruction and the exponentials.
+#include <algorithm>
+
+#include "cache_walk.cuh"
+
+namespace relattn {
+namespace {
+
+constexpr int WW = 4, WT = WW * 32, WK = kWalkTile / WW;
+static_assert(WK == 32, "two 16-key groups");
+constexpr int W_STAGES = 3;
+constexpr int kColdKeys = 1024;              // keys out of every row's sight that a CTA takes at a time
+
+template <bool FP4>
+struct KStage {
+  static constexpr int row = FP4 ? kFp4RowBytes : kHeadDim * 2;
+  static constexpr int scales = WK * row;
+  static constexpr int bytes = scales + (FP4 ? WK * kFp4Blocks : 0);
+  static constexpr int ring = WW * W_STAGES * bytes;
+};
+
+// Key of row g of a 16-key operand (its other key is 8 further): the 4-bit
+// layout of decode_fp4.cu, or the natural one.
+template <bool FP4>
+__device__ __forceinline__ int operand_key(int g) {
+  return FP4 ? (g >> 1) + 4 * (g & 1) : g;
+}
+
+template <bool FP4>
+__device__ __forceinline__ void issue_keys(const KeyWeightArgs &p, const Unit &u, uint32_t st, int key0, long row0,
+                                           int lane) {
+  if (FP4) {
+    const long rb = (long)p.a.Hkv * kFp4RowBytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (lane >> 2) + 8 * i, c = lane & 3, k16 = k & 15;
+      const bool ok = row0 >= 0 && key0 + k < u.s.lk;
+      const long off = ok ? (row0 + k) * rb + u.h * kFp4RowBytes + c * 16 : 0;
+      const int slot = (k & 16) + (k16 & 8) + 2 * (k16 & 3) + ((k16 >> 2) & 1);
+      cp_async16(st + slot * kFp4RowBytes + c * 16, p.kv.k + off, ok);
+    }
+    const bool ok = row0 >= 0 && key0 + lane < u.s.lk;
+    cp_async8(st + KStage<true>::scales + lane * kFp4Blocks,
+              p.kv.k_scale + (ok ? ((row0 + lane) * p.a.Hkv + u.h) * kFp4Blocks : 0), ok);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = (lane >> 4) + 2 * i, c = lane & 15;
+      const bool ok = row0 >= 0 && key0 + k < u.s.lk;
+      const long off = ok ? ((row0 + k) * p.a.Hkv + u.h) * kHeadDim + c * 8 : 0;
+      cp_async16(st + k * 256 + ((c ^ (k & 7)) << 4), p.k + off, ok);
+    }
+  }
+}
+
+// The A operand of one 16-key group and 16-dim step s from a stage.
+template <bool FP4>
+__device__ __forceinline__ void key_operands(uint32_t st, int gr, int lane, uint32_t (&f)[8][4]) {
+  const int g = lane >> 2, t = lane & 3;
+  if (FP4) {
+    const uint32_t kb = st + gr * 16 * kFp4RowBytes + t * 16;
+    const uint4 w0 = lds128(kb + g * kFp4RowBytes), w1 = lds128(kb + (g + 8) * kFp4RowBytes);
+    const uint32_t sb = st + KStage<true>::scales + (gr * 16 + operand_key<true>(g)) * kFp4Blocks + 2 * t;
+    const uint32_t s0 = e4m3x2_to_f16(lds_u16(sb)), s1 = e4m3x2_to_f16(lds_u16(sb + 8 * kFp4Blocks));
+    const uint32_t ww0[4] = {w0.x, w0.y, w0.z, w0.w}, ww1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t m0 = __byte_perm(s0, 0, w < 2 ? 0x1010 : 0x3232);
+      const uint32_t m1 = __byte_perm(s1, 0, w < 2 ? 0x1010 : 0x3232);
+      uint32_t f0[4], f1[4];
+      e2m1x8_to_f16(ww0[w], f0);
+      e2m1x8_to_f16(ww1[w], f1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[2 * w + i][0] = hmul2(f0[2 * i], m0);
+        f[2 * w + i][1] = hmul2(f1[2 * i], m1);
+        f[2 * w + i][2] = hmul2(f0[2 * i + 1], m0);
+        f[2 * w + i][3] = hmul2(f1[2 * i + 1], m1);
+      }
+    }
+  } else {
+    const int row = gr * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      ldsm_x4(st + row * 256 + (((2 * s + (lane >> 4)) ^ (row & 7)) << 4), f[s][0], f[s][1], f[s][2], f[s][3]);
+  }
+}
+
+template <bool FP4>
+__device__ __forceinline__ void key_mma(float (&d)[4], const uint32_t (&f)[4], uint32_t b0, uint32_t b1) {
+  if (FP4) mma_f16_16816(d, f[0], f[1], f[2], f[3], b0, b1);
+  else mma_bf16_16816(d, f[0], f[1], f[2], f[3], b0, b1);
+}
+
+// Sum of v[0..3] over the quad's four lanes; lane t ends with v[t]'s.
+__device__ __forceinline__ float quad_reduce(const float (&v)[4], int t) {
+  const unsigned full = 0xffffffffu;
+  const float a = (t & 1) ? v[0] : v[1], b = (t & 1) ? v[2] : v[3];      // given away
+  const float x = ((t & 1) ? v[1] : v[0]) + __shfl_xor_sync(full, a, 1);
+  const float y = ((t & 1) ? v[3] : v[2]) + __shfl_xor_sync(full, b, 1);
+  return ((t & 2) ? y : x) + __shfl_xor_sync(full, (t & 2) ? x : y, 2);
+}
+
+// w_out of key `key` (cache row `row`) with the new weight `sum`.
+__device__ __forceinline__ void write_weight(const KeyWeightArgs &p, const Unit &u, int key, long row, float sum) {
+  const long at = (long)u.h * p.pages.rows + row;
+  if (p.w_in && p.decay != 0.f && key < u.s.lk - u.s.lq) sum = fmaf(p.decay, __ldg(p.w_in + at), sum);
+  p.w_out[at] = sum;
+}
+
+// ------------------------------------------------------------------ few rows
+
+template <int NT, bool POS, bool FP4>
+__device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &u, int t0, int n, uint8_t *smem) {
+  constexpr int SB = KStage<FP4>::bytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_addr(smem) + warp * (W_STAGES * SB);
+  const int k_first = u.lo + t0 * kWalkTile + warp * WK;
+  const unsigned full = 0xffffffffu;
+  long rows_q[W_STAGES];                    // cache rows of the groups in flight, then the next to copy
+#pragma unroll
+  for (int i = 0; i < W_STAGES; ++i) {
+    rows_q[i] = i < n ? group_row(p, u, k_first + i * kWalkTile) : -1;
+    if (i < W_STAGES - 1) {
+      if (i < n) issue_keys<FP4>(p, u, ring + i * SB, k_first + i * kWalkTile, rows_q[i], lane);
+      cp_async_commit();
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  uint32_t qf[NT][16];
+  float coef[NT][2], bscale[NT][2], lse2[NT][2];
+  int qp[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int nrow = nt * 8 + g;
+    int tok = 0;
+    float back = 1.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) qf[nt][i] = 0;
+    if (nrow < u.nrows) {
+      const __nv_bfloat16 *qrow = p.a.q + unit_row(p, u, nrow, &tok) * kHeadDim;
+      if (FP4) {                            // dims 32 t .., f16
+        const uint4 *src = reinterpret_cast<const uint4 *>(qrow + t * 32);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = __ldg(src + i);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            qf[nt][4 * i + j] = ws[j];
+            top = max(top, max((ws[j] << 16) & 0x7fff0000u, ws[j] & 0x7fff0000u));
+          }
+        }
+        const unsigned quad = 0xfu << (lane & ~3);
+        top = max(top, __shfl_xor_sync(quad, top, 1));
+        top = max(top, __shfl_xor_sync(quad, top, 2));
+        const float up = f16_row_scale(top, &back);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          qf[nt][i] = pack_f16x2(__uint_as_float(qf[nt][i] << 16) * up, __uint_as_float(qf[nt][i] & 0xffff0000u) * up);
+      } else {                              // dims 16 s + 2 t (+1), + 8: bf16 as they are
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(qrow) + t;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          qf[nt][2 * s] = __ldg(src + 8 * s);
+          qf[nt][2 * s + 1] = __ldg(src + 8 * s + 4);
+        }
+      }
+    }
+    __syncwarp();
+    const float kg = FP4 && p.kv.k_global ? __ldg(p.kv.k_global + u.h) : 1.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int m = nt * 8 + 2 * t + c;
+      const float bk = __shfl_sync(full, back, (2 * t + c) * 4);
+      int tk;
+      const long grow = unit_row(p, u, m, &tk);
+      const bool live = m < u.nrows;
+      const float s = live ? log_scale(u.qbase + tk, p.a.inv_ln_base) : 0.f;
+      qp[nt][c] = live ? u.qbase + tk : -1;
+      coef[nt][c] = p.a.alpha_log2e * s * kg * bk;
+      bscale[nt][c] = s * kLog2e;
+      // a row that saw nothing (lse -inf), and one past the block, give nothing
+      const float z = live ? __ldg(p.lse + (grow % p.a.Hq) * p.a.total_q + grow / p.a.Hq) : -INFINITY;
+      lse2[nt][c] = z == -INFINITY ? INFINITY : z * kLog2e;
+    }
+  }
+  int qmin, qmax, tk_;
+  unit_row(p, u, 0, &tk_);
+  qmin = u.qbase + tk_;
+  unit_row(p, u, u.nrows - 1, &tk_);
+  qmax = u.qbase + tk_;
+  const unsigned wlim = p.a.window > 0 ? (unsigned)p.a.window : 0x80000000u;
+
+  int buf = 0;
+  for (int it = 0; it < n; ++it) {
+    const int key0 = k_first + it * kWalkTile;
+    cp_async_wait<W_STAGES - 2>();
+    __syncwarp();
+    const long row0 = rows_q[0];
+    {
+      const int nb = buf == 0 ? W_STAGES - 1 : buf - 1;
+      if (it + W_STAGES - 1 < n) issue_keys<FP4>(p, u, ring + nb * SB, key0 + (W_STAGES - 1) * kWalkTile, rows_q[W_STAGES - 1], lane);
+      cp_async_commit();
+    }
+#pragma unroll
+    for (int i = 0; i + 1 < W_STAGES; ++i) rows_q[i] = rows_q[i + 1];
+    rows_q[W_STAGES - 1] = it + W_STAGES < n ? group_row(p, u, key0 + W_STAGES * kWalkTile) : -1;
+    const uint32_t st = ring + buf * SB;
+    buf = buf == W_STAGES - 1 ? 0 : buf + 1;
+    if (key0 >= u.s.lk) continue;
+    int kp_lane = 0x7fffffff;
+    if (POS && row0 >= 0 && key0 + lane < u.s.lk) {
+      kp_lane = __ldg(p.key_pos + (long)u.h * p.pages.rows + row0 + lane);
+      if (kp_lane < 0) kp_lane = 0x7fffffff;
+    }
+    float x[2][NT][4];
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      uint32_t f[8][4];
+      key_operands<FP4>(st, gr, lane, f);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        x[gr][nt][0] = x[gr][nt][1] = x[gr][nt][2] = x[gr][nt][3] = 0.f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) key_mma<FP4>(x[gr][nt], f[s], qf[nt][2 * s], qf[nt][2 * s + 1]);
+      }
+    }
+    const bool edge = POS || key0 + WK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
+    int kp[2][2];
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int k = gr * 16 + hf * 8 + operand_key<FP4>(g);
+        kp[gr][hf] = POS ? __shfl_sync(full, kp_lane, k) : key0 + k;
+      }
+    const bool band = p.a.E > 0 && (POS ? __any_sync(full, kp_lane != 0x7fffffff && qmin - kp_lane < p.a.E)
+                                        : qmin - (key0 + WK - 1) < p.a.E);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};      // keys operand_key(g) + 8 hf + 16 gr at 2 gr + hf
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float *R = nullptr;
+        if (band) {
+          int tk;
+          R = p.a.rdec + unit_row(p, u, min(nt * 8 + 2 * t + c, u.nrows - 1), &tk) * p.a.E;
+        }
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float y = x[gr][nt][2 * hf + c] * coef[nt][c];
+            const unsigned d = (unsigned)qp[nt][c] - (unsigned)kp[gr][hf];
+            if (band && d < (unsigned)p.a.E) y = fmaf(R[d], bscale[nt][c], y);
+            float e = fast_exp2(y - lse2[nt][c]);
+            if (edge && d >= wlim) e = 0.f;
+            v[2 * gr + hf] += e;
+          }
+      }
+    const float sum = quad_reduce(v, t);
+    const int key = key0 + (t >> 1) * 16 + (t & 1) * 8 + operand_key<FP4>(g);
+    if (row0 >= 0 && key < u.s.lk) write_weight(p, u, key, row0 + (key - key0), sum);
+  }
+  cp_async_wait<0>();
+  __syncwarp();
+}
+
+template <int NT, bool POS, bool FP4>
+__global__ void __launch_bounds__(WT) relattn_key_weights_rows_kernel(const __grid_constant__ KeyWeightArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int prefix[kWalkBatch + 1];
+  __shared__ int wsum[WW];
+  const int base = tile_prefix<WT>(p, prefix, wsum);
+  const long per = base, total = per * p.a.Hkv;
+  const long C = (total + gridDim.x - 1) / gridDim.x;
+  long x = blockIdx.x * C;
+  const long end = min(total, x + C);
+  Unit u;
+  u.rb = 0;
+  while (x < end) {
+    u.h = (int)(x / per);
+    const int xb = (int)(x - u.h * per);
+    u.b = last_not_above(prefix, p.a.batch, xb);
+    const int tiles = unit_tiles(p, u.b, &u.s, &u.lo), t0 = xb - prefix[u.b];
+    const int n = (int)min((long)(tiles - t0), end - x);
+    u.nrows = u.s.lq * p.a.group;
+    u.qbase = first_query_pos(u.s, p.q_pos, u.b);
+    weigh_piece<NT, POS, FP4>(p, u, t0, n, smem);
+    x += n;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ many rows
+
+constexpr int QR = 32;                       // query rows staged at a time
+
+template <bool POS, bool FP4>
+__global__ void __launch_bounds__(WT) relattn_key_weights_tiles_kernel(const __grid_constant__ KeyWeightArgs p) {
+  // K first (its stage layout, one per warp), then the staged rows
+  __shared__ __align__(128) uint8_t sk[WW * KStage<FP4>::bytes];
+  __shared__ __align__(128) uint8_t sq[QR * 256];
+  __shared__ float s_coef[QR], s_bscale[QR], s_lse[QR];
+  __shared__ int s_qp[QR];
+  __shared__ long s_row[QR];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const unsigned full = 0xffffffffu;
+  Unit u;
+  u.rb = 0;
+  u.b = blockIdx.y / p.a.Hkv;
+  u.h = blockIdx.y - u.b * p.a.Hkv;
+  const int ok = unit_tiles(p, u.b, &u.s, &u.lo);
+  if (ok < 0 && blockIdx.x == 0 && u.h == 0 && tid == 0) atomicOr(p.a.err, kDevErrSeqlens);
+  const int tile0 = blockIdx.x * kWalkTile, key0 = tile0 + warp * WK;
+  if (ok < 0 || tile0 >= u.s.lk) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  u.nrows = u.s.lq * p.a.group;
+  u.qbase = u.s.lq > 0 ? first_query_pos(u.s, p.q_pos, u.b) : 0;
+  const unsigned wlim = p.a.window > 0 ? (unsigned)p.a.window : 0x80000000u;
+  // tokens that may see a key of the tile
+  int tok0 = 0, tok1 = u.s.lq;
+  if (!POS) {
+    tok0 = max(0, tile0 - u.qbase);
+    const long last = (long)min(tile0 + kWalkTile, u.s.lk) - 1 + wlim - u.qbase;   // first token past the window
+    if (last < tok1) tok1 = (int)max(last, 0L);
+  }
+  const long row0 = group_row(p, u, key0);
+  const uint32_t st = smem_addr(sk) + warp * KStage<FP4>::bytes;
+  uint32_t f[2][8][4];
+  if (tok0 < tok1) {
+    issue_keys<FP4>(p, u, st, key0, row0, lane);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncwarp();
+    key_operands<FP4>(st, 0, lane, f[0]);
+    key_operands<FP4>(st, 1, lane, f[1]);
+  }
+  int kp[2][2], kp_lane = 0x7fffffff;
+  if (POS && row0 >= 0 && key0 + lane < u.s.lk) {
+    kp_lane = __ldg(p.key_pos + (long)u.h * p.pages.rows + row0 + lane);
+    if (kp_lane < 0) kp_lane = 0x7fffffff;
+  }
+#pragma unroll
+  for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int k = gr * 16 + hf * 8 + operand_key<FP4>(g);
+      kp[gr][hf] = POS ? __shfl_sync(full, kp_lane, k) : key0 + k;
+    }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float kg = FP4 && p.kv.k_global ? __ldg(p.kv.k_global + u.h) : 1.f;
+  const uint32_t sqa = smem_addr(sq);
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (long r0 = (long)tok0 * p.a.group; r0 < (long)tok1 * p.a.group; r0 += QR) {
+    __syncthreads();                         // the rows before these are read
+    {
+      // four threads a row, 32 dims each
+      const int n = tid >> 2, part = tid & 3;
+      const long rr = r0 + n;
+      const bool live = rr < (long)tok1 * p.a.group;
+      const int tok = (int)(rr / p.a.group), hh = (int)(rr - (long)tok * p.a.group);
+      const int head = u.h * p.a.group + hh;
+      const long grow = (long)(u.s.q0 + tok) * p.a.Hq + head;
+      uint32_t w[16];
+      float back = 1.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = 0;
+      if (live) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + grow * kHeadDim + part * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 y = __ldg(src + i);
+          w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
+        }
+      }
+      if (FP4) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+        top = max(top, __shfl_xor_sync(full, top, 1));
+        top = max(top, __shfl_xor_sync(full, top, 2));
+        const float up = f16_row_scale(top, &back);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // 16-byte chunks exchanged so that each operand read meets every bank once
+        const int c = part * 4 + i, at = FP4 ? c ^ ((part >> 1) | ((n & 1) << 1)) : c ^ (n & 7);
+        st_shared_v4(sqa + n * 256 + at * 16, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
+      if (part == 0) {
+        const float s = live ? log_scale(u.qbase + tok, p.a.inv_ln_base) : 0.f;
+        s_qp[n] = live ? u.qbase + tok : -1;
+        s_coef[n] = p.a.alpha_log2e * s * kg * back;
+        s_bscale[n] = s * kLog2e;
+        const float z = live ? __ldg(p.lse + (long)head * p.a.total_q + u.s.q0 + tok) : -INFINITY;
+        s_lse[n] = z == -INFINITY ? INFINITY : z * kLog2e;
+        s_row[n] = live ? grow : 0;
+      }
+    }
+    __syncthreads();
+    const int qmin = s_qp[0], qlast = u.qbase + (int)(min(r0 + QR, (long)tok1 * p.a.group) - 1) / p.a.group;
+    const bool edge = POS || key0 + WK - 1 > qmin || (unsigned)(qlast - key0) >= wlim || r0 + QR > (long)tok1 * p.a.group;
+    const bool band = p.a.E > 0 && (POS ? __any_sync(full, kp_lane != 0x7fffffff && qmin - kp_lane < p.a.E)
+                                        : qmin - (key0 + WK - 1) < p.a.E);
+#pragma unroll 1
+    for (int nt = 0; nt < QR / 8; ++nt) {
+      uint32_t b[16];
+      if (FP4) {
+        const uint32_t rb = sqa + (nt * 8 + g) * 256;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 y = lds128(rb + (((4 * t + i) ^ ((t >> 1) | ((g & 1) << 1))) << 4));
+          b[4 * i] = y.x, b[4 * i + 1] = y.y, b[4 * i + 2] = y.z, b[4 * i + 3] = y.w;
+        }
+      } else {
+        const int row = nt * 8 + (lane & 7);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          ldsm_x4(sqa + row * 256 + (((4 * s + (lane >> 3)) ^ (row & 7)) << 4), b[4 * s], b[4 * s + 1], b[4 * s + 2],
+                  b[4 * s + 3]);
+      }
+      float x[2][4];
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        x[gr][0] = x[gr][1] = x[gr][2] = x[gr][3] = 0.f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) key_mma<FP4>(x[gr], f[gr][s], b[2 * s], b[2 * s + 1]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int m = nt * 8 + 2 * t + c;
+        const float coef = s_coef[m], lse2 = s_lse[m];
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float y = x[gr][2 * hf + c] * coef;
+            if (band || edge) {
+              const unsigned d = (unsigned)s_qp[m] - (unsigned)kp[gr][hf];
+              if (band && d < (unsigned)p.a.E) y = fmaf(p.a.rdec[s_row[m] * p.a.E + d], s_bscale[m], y);
+              if (d >= wlim) y = -INFINITY;
+            }
+            v[2 * gr + hf] += fast_exp2(y - lse2);
+          }
+      }
+    }
+  }
+  const float sum = quad_reduce(v, t);
+  const int key = key0 + (t >> 1) * 16 + (t & 1) * 8 + operand_key<FP4>(g);
+  if (row0 >= 0 && key < u.s.lk) write_weight(p, u, key, row0 + (key - key0), sum);
+}
+
+// ------------------------------------------------------------------ keys out of sight
+
+// Keys that the walk leaves out (past the window of every row, or of a
+// sequence without query rows): w_out = decay * w_in.
+__global__ void __launch_bounds__(256) relattn_key_weights_cold_kernel(const __grid_constant__ KeyWeightArgs p) {
+  Unit u;
+  u.b = blockIdx.y / p.a.Hkv;
+  u.h = blockIdx.y - u.b * p.a.Hkv;
+  const int tiles = unit_tiles(p, u.b, &u.s, &u.lo);
+  if (tiles < 0) return;
+  const int end = tiles == 0 ? u.s.lk : u.lo;
+  for (int key = blockIdx.x * kColdKeys + threadIdx.x; key < min(end, (int)(blockIdx.x + 1) * kColdKeys); key += 256) {
+    const long row = p.pages.row(u.b, u.s.k0, key);
+    if (row < 0) {
+      atomicOr(p.a.err, kDevErrSeqlens);
+      continue;
+    }
+    write_weight(p, u, key, row, 0.f);
+  }
+}
+
+template <int NT, bool POS, bool FP4>
+cudaError_t launch_rows(const KeyWeightArgs &p, cudaLaunchConfig_t cfg) {
+  static std::atomic<bool> done[kMaxDevicesAttr];
+  auto *kernel = relattn_key_weights_rows_kernel<NT, POS, FP4>;
+  const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), KStage<FP4>::ring, done);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(p.a.sms * (FP4 ? 4 : 2)));
+  cfg.blockDim = dim3(WT);
+  cfg.dynamicSmemBytes = KStage<FP4>::ring;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool POS, bool FP4>
+cudaError_t launch_kind(const KeyWeightArgs &p, cudaLaunchConfig_t cfg) {
+  const int rows = p.a.max_q * p.a.group;
+  if (rows <= kFp4Rows && p.a.batch <= kWalkBatch)
+    return rows <= 8 ? launch_rows<1, POS, FP4>(p, cfg) : launch_rows<2, POS, FP4>(p, cfg);
+  cfg.gridDim = dim3((unsigned)((p.a.max_k + kWalkTile - 1) / kWalkTile), (unsigned)(p.a.batch * p.a.Hkv));
+  cfg.blockDim = dim3(WT);
+  return cudaLaunchKernelEx(&cfg, relattn_key_weights_tiles_kernel<POS, FP4>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_key_weights(const KeyWeightArgs &p, cudaStream_t stream) {
+  if ((long)p.a.batch * p.a.Hkv > 65535) return cudaErrorInvalidValue;
+  if (p.a.E > 0) {
+    const cudaError_t e = launch_rel_bias(p.a.r, p.a.P, (long)p.a.total_q * p.a.Hq, p.a.rd, p.a.E,
+                                          const_cast<float *>(p.a.rdec), stream);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.a.E > 0 ? 1 : 0;          // behind the R kernel
+  const bool pos = p.key_pos != nullptr, fp4 = p.k == nullptr;
+  cudaError_t e = pos ? (fp4 ? launch_kind<true, true>(p, cfg) : launch_kind<true, false>(p, cfg))
+                      : (fp4 ? launch_kind<false, true>(p, cfg) : launch_kind<false, false>(p, cfg));
+  if (e != cudaSuccess) return e;
+  // the walk of few rows leaves the keys out of sight alone
+  const bool walked = p.a.max_q * p.a.group <= kFp4Rows && p.a.batch <= kWalkBatch;
+  if (walked) {
+    relattn_key_weights_cold_kernel<<<dim3((unsigned)((p.a.max_k + kColdKeys - 1) / kColdKeys),
+                                           (unsigned)(p.a.batch * p.a.Hkv)), 256, 0, stream>>>(p);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace relattn

@@ -149,4 +149,107 @@ cudaError_t launch_bwd_dq_tc(const BwdArgs &a, cudaStream_t stream);
 cudaError_t launch_prologue(const relattn_prologue_params *p, int *err, int sms, int skip_tile,
                             cudaStream_t stream, const relattn_kv_mxfp8_out *mx = nullptr);
 
+// The 4-bit (NVFP4) K / V cache (nvfp4.cuh): codes [rows, Hkv, 64] (16-byte
+// aligned), scales [rows, Hkv, 8] (8-byte aligned), factors [Hkv] or null (1).
+struct Fp4Cache {
+  const uint8_t *k, *v, *k_scale, *v_scale;
+  const float *k_global, *v_global;
+};
+
+// Physical cache rows: contiguous rows cu_seqlens_k[b] + p, or (with a block
+// table) row block_table[b * max_pages + p / page_size] * page_size + p % page_size.
+struct CachePages {
+  const int32_t *block_table;
+  int page_size, max_pages, num_pages;
+  long rows;   // rows of the cache arrays
+
+  // row of key p of sequence b (k0 = cu_seqlens_k[b]), -1 when it lies outside the arrays
+  __device__ __forceinline__ long row(int b, int k0, int p) const {
+    if (block_table) {
+      const int slot = p / page_size;
+      if (slot >= max_pages) return -1;
+      const int pg = __ldg(block_table + (long)b * max_pages + slot);
+      return (unsigned)pg < (unsigned)num_pages ? (long)pg * page_size + (p - slot * page_size) : -1;
+    }
+    const long r = (long)k0 + p;
+    return r < rows ? r : -1;
+  }
+};
+
+// Chunk rows into / out of the 4-bit cache (cache_fp4.cu): k / v bf16
+// [total_q, Hkv, 128], read by the store and written by the load.
+struct Fp4RowArgs {
+  const __nv_bfloat16 *k, *v;
+  const int32_t *cu_q, *cu_k;
+  int *err;
+  int batch, total_q, Hkv;
+  Fp4Cache kv;
+  CachePages pages;
+};
+cudaError_t launch_store_fp4(const Fp4RowArgs &a, cudaStream_t stream);
+cudaError_t launch_load_fp4(const Fp4RowArgs &a, cudaStream_t stream);
+
+// R = r . P of every query row and distance < E (rel_bias.cu): fp32 [rows][E],
+// any r_dim <= 64 and E.  A kernel launched behind it as its programmatic
+// dependent may start early and waits for it with griddepcontrol.wait.
+cudaError_t launch_rel_bias(const __nv_bfloat16 *r, const __nv_bfloat16 *P, long rows, int r_dim, int E,
+                            float *R, cudaStream_t stream);
+
+// Kernels that stream a cache: q, r, P, lengths, rdec and err in `a`; key_pos
+// [Hkv, pages.rows] / q_pos [batch] are positions, or both null (row indices).
+struct WalkArgs {
+  KernelArgs a;
+  CachePages pages;
+  const int32_t *key_pos, *q_pos;
+};
+constexpr int kWalkTile = 128;        // keys a CTA takes at a time
+
+// Split-KV decode over the 4-bit cache (decode_fp4.cu).
+struct Fp4DecodeArgs : WalkArgs {
+  Fp4Cache kv;
+  int row_blocks;      // 16-row blocks per (sequence, kv head)
+  int splits;          // partial slots of a row; 1 = one CTA per unit, no partials
+  int c_min;           // least tiles a CTA takes (keeps a unit within its slots)
+};
+struct Fp4DecodePlan {
+  int row_blocks, splits, c_min;
+  size_t lse_offset, rel_offset, ws_bytes;
+};
+constexpr int kFp4Rows = 16;          // query rows of a work unit
+constexpr int kFp4PageUnit = 32;      // page sizes are multiples of it
+bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want_splits, Fp4DecodePlan *plan);
+cudaError_t launch_decode_fp4(const Fp4DecodeArgs &a, cudaStream_t stream);
+
+// Attention weight per key (key_weights.cu): w_out[h][row] = decay w_in[h][row]
+// (0 for the newest Lq keys) + sum over query rows and the group's heads of
+// exp(x - lse).  K is bf16 (k) or 4-bit (kv.k, when k is null).
+struct KeyWeightArgs : WalkArgs {
+  const __nv_bfloat16 *k;
+  Fp4Cache kv;
+  const float *lse;    // [Hq, total_q]
+  const float *w_in;   // [Hkv, pages.rows], null: zero
+  float *w_out;
+  float decay;
+};
+cudaError_t launch_key_weights(const KeyWeightArgs &a, cudaStream_t stream);
+
+// Eviction (evict.cu)
+constexpr int kMaxPlanes = 8;
+struct EvictArgs {
+  const float *weights;          // [Hkv, src.rows]
+  const int32_t *cu_k, *cu_keep, *key_pos;
+  CachePages src, dst;
+  int batch, total_keep, max_k, Hkv, sink, recent;
+  float *w_out;                  // [Hkv, dst.rows] or null
+  int32_t *pos_out;              // [Hkv, dst.rows] or null
+  int32_t *src_row;              // workspace [Hkv, total_keep]: cache row of every kept key
+  int32_t *dst_row;              // workspace [total_keep]: its row in the new cache
+  int planes;
+  const void *from[kMaxPlanes];  // [src.rows, Hkv, bytes]
+  void *to[kMaxPlanes];          // [dst.rows, Hkv, bytes]
+  int bytes[kMaxPlanes];
+  int *err;
+};
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream);
+
 }  // namespace relattn

@@ -1,0 +1,659 @@
+"""The compressed K / V cache on the GPU against the fp64 oracle: NVFP4 rows in
+and out, decode over them, the weight each key receives, eviction, and a run
+of them together.  Tolerances count roundings (tests/kvcache_util.py)."""
+import numpy as np
+import pytest
+import torch
+
+import relative_position_biased_gb300 as rpb
+from oracle import kvcache as C
+from relative_position_biased_gb300 import workloads as W
+from tests import kvcache_util as U
+from tests.conftest import gpu_available
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a CUDA GPU")]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    rpb.build()
+    rpb.load_library()
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    if gpu_available():
+        rpb.relattn_get_device_error()
+    yield
+
+
+def ok():
+    torch.cuda.synchronize()
+    st = rpb.relattn_get_device_error()
+    assert st == rpb.RELATTN_OK, rpb.STATUS_NAMES.get(st, st)
+
+
+def host(t):
+    return t.cpu().numpy()
+
+
+# ------------------------------------------------------------------ store and load
+
+@pytest.mark.parametrize("q_lens,k_lens,Hkv,page,factors", [
+    ((1,), (1,), 1, 0, False),
+    ((37, 0, 5), (37, 3, 260), 2, 0, True),
+    ((1,) * 9, (33, 1, 64, 65, 100, 7, 31, 32, 96), 2, 32, True),
+    ((130, 64), (130, 200), 3, 64, False),
+])
+def test_store_writes_the_chunk_rows_and_no_others(q_lens, k_lens, Hkv, page, factors):
+    c = U.Case(q_lens, k_lens, Hkv, Hkv, page=page, factors=factors)
+    d = U.make(c)
+    rows = np.concatenate([w[len(w) - n:] for w, n in zip(d["where"], q_lens)])
+    k, v = d["k"][rows], d["v"][rows]
+    cache = rpb.empty_nvfp4(d["rows"], Hkv, "cuda", *(U.cuda(None if g is None else torch.from_numpy(g))
+                                                     for g in (d["kg"], d["vg"])))
+    for t in cache[:4]:
+        t.fill_(0xA5)
+    kw = dict(block_table=d["table"].cuda(), page_size=page) if page else {}
+    cu = (d["cu_q"].cuda(), d["cu_k"].cuda())
+    rpb.store_nvfp4(k.cuda(), v.cuda(), *cu, cache, **kw)
+    ok()
+    other = np.setdiff1d(np.arange(d["rows"]), rows)
+    for x, codes, scales, g in ((k, cache.k, cache.k_scale, d["kg"]), (v, cache.v, cache.v_scale, d["vg"])):
+        want_c, want_s = C.quantize_nvfp4(x.float().numpy(), g)
+        np.testing.assert_array_equal(host(scales)[rows], want_s)
+        np.testing.assert_array_equal(host(codes)[rows], want_c)
+        assert (host(codes)[other] == 0xA5).all() and (host(scales)[other] == 0xA5).all()
+    lk, lv = rpb.load_nvfp4(cache, *cu, total_q=len(rows), **kw)
+    ok()
+    for x, got, g in ((k, lk, d["kg"]), (v, lv, d["vg"])):
+        ref = C.dequantize_nvfp4(*C.quantize_nvfp4(x.float().numpy(), g), g)
+        # code * scale is exact; the factor's product rounds to fp32, then to bf16
+        assert (np.abs(host(got.double()) - ref) <= np.abs(ref) * (2.0 ** -8 * (1 + 2.0 ** -20) + 2.0 ** -24)).all()
+
+
+def _store_one(x, factor=None):
+    n = x.shape[0]
+    cu = W.cu_seqlens([n]).cuda()
+    g = None if factor is None else torch.from_numpy(factor).cuda()
+    cache = rpb.empty_nvfp4(n, x.shape[1], "cuda", g, g)
+    rpb.store_nvfp4(x.cuda(), x.cuda(), cu, cu, cache)
+    ok()
+    return host(cache.k), host(cache.k_scale), host(cache.v), host(cache.v_scale)
+
+
+@pytest.mark.parametrize("factor", [None, np.float32(0.0123), np.float32(2.0 ** -20), np.float32(3e4)])
+def test_store_rounds_exactly(factor):
+    """Every bf16 magnitude as a block's largest element, and elements next to
+    and on the borders of the codes."""
+    mags = torch.arange(0, 0x7f80, dtype=torch.int16).view(torch.bfloat16).float().numpy()
+    n = (len(mags) + 7) // 8
+    rng = np.random.default_rng(3)
+    x = np.zeros((n, 8, 16), np.float32)
+    x[:, :, 0] = np.resize(mags, n * 8).reshape(n, 8)
+    x[:, :, 1:8] = x[:, :, :1] * np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32) / 6
+    x[:, :, 8:] = x[:, :, :1] * rng.uniform(-1, 1, (n, 8, 8))
+    xb = U.bf16(x.reshape(n, 1, 128))
+    f = None if factor is None else np.array([factor], np.float32)
+    ck, sk, cv, sv = _store_one(xb, f)
+    want_c, want_s = C.quantize_nvfp4(xb.float().numpy(), f)
+    np.testing.assert_array_equal(sk, want_s)
+    np.testing.assert_array_equal(ck, want_c)
+    np.testing.assert_array_equal(cv, want_c)
+    np.testing.assert_array_equal(sv, want_s)
+
+
+def test_store_of_infinities_and_nan():
+    x = np.ones((3, 1, 128), np.float32)
+    x[0, 0, 3] = np.inf
+    x[1, 0, 20] = -np.inf
+    x[2, 0, 127] = np.nan
+    ck, sk, _, _ = _store_one(U.bf16(x))
+    want_c, want_s = C.quantize_nvfp4(x)
+    np.testing.assert_array_equal(sk, want_s)
+    np.testing.assert_array_equal(ck[:2], want_c[:2])
+    assert sk[2, 0, 7] == 0x7F and (sk[2, 0, :7] == want_s[2, 0, :7]).all()
+
+
+def test_store_records_bad_pages_and_lengths():
+    x = U.bf16(np.ones((40, 1, 128)))
+    cache = rpb.empty_nvfp4(64, 1, "cuda")
+    table = torch.tensor([[1, 7]], dtype=torch.int32, device="cuda")      # page 7 is not in the pool
+    cu = W.cu_seqlens([40]).cuda()
+    rpb.store_nvfp4(x.cuda(), x.cuda(), cu, cu, cache, block_table=table, page_size=32)
+    torch.cuda.synchronize()
+    assert rpb.relattn_get_device_error() == 6
+    assert (host(cache.k)[32:] != 0).all() and (host(cache.k)[:32] == 0).all()
+    k, _ = rpb.load_nvfp4(cache, cu, cu, total_q=40, block_table=table, page_size=32)
+    assert rpb.relattn_get_device_error() == 6
+    # a block of ones: 1 / 6 is nearest to the scale 11 / 64, 64 / 11 to the code 6
+    assert (host(k.float())[:32] == 6 * 11 / 64).all() and (host(k.float())[32:] == 0).all()
+    # more chunk rows than keys, and keys past the cache: skipped, recorded
+    for ck in ([8], [100]):
+        cache = rpb.empty_nvfp4(64, 1, "cuda")
+        rpb.store_nvfp4(x.cuda(), x.cuda(), cu, W.cu_seqlens(ck).cuda(), cache)
+        assert rpb.relattn_get_device_error() == 6
+        assert (host(cache.k) == 0).all()
+
+
+# ------------------------------------------------------------------ decode
+
+def run_decode(c, d, qc, cache=None, **kw):
+    out, lse = rpb.decode_nvfp4(d["q"].cuda(), cache or U.device_cache(qc, d), U.cuda(d["r"]), U.cuda(d["P"]),
+                                d["cu_q"].cuda(), d["cu_k"].cuda(), **{**U.call_kw(c, d), **kw})
+    ok()
+    return out, lse
+
+
+DECODE = [
+    U.Case((1,), (1,), 1, 1, E=0, r_dim=0, factors=False),
+    U.Case((1,), (31,), 4, 1),
+    U.Case((1, 1, 1, 1, 1), (32, 33, 127, 128, 129), 8, 1),
+    U.Case((1,), (2900,), 16, 2, r_dim=64, E=1024, base=64.0),
+    U.Case((9, 3, 1), (700, 130, 5), 16, 2, r_dim=64, E=256, base=64.0),       # 72 rows per kv head
+    U.Case((16, 2), (300, 65), 2, 2, E=77, r_dim=24),                          # 16 rows, one head each
+    U.Case((1, 0, 1), (257, 9, 640), 24, 1, E=100, r_dim=5),                   # 24 rows of one token
+    U.Case((1, 1), (1500, 20), 16, 2, window=1),
+    U.Case((4, 1, 2), (1500, 513, 90), 8, 2, window=100, E=64),
+    U.Case((1, 1), (3000, 700), 12, 4, window=512, E=1024, r_dim=64),
+    U.Case((1,) * 7, (33, 1, 64, 65, 1000, 7, 96), 16, 2, page=32),
+    U.Case((5, 2), (1000, 321), 4, 1, page=64, window=200),
+    U.Case((1, 1, 1), (600, 65, 2050), 16, 2, positions=True, base=64.0),
+    U.Case((3, 9), (600, 65), 4, 2, positions=True, E=40, page=32),
+    U.Case((1, 2), (900, 300), 8, 1, positions=True, window=150),
+]
+
+
+@pytest.mark.parametrize("i", range(len(DECODE)))
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_decode(i, splits):
+    c = DECODE[i]
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    out, lse = run_decode(c, d, qc, num_splits=splits)
+    U.check_decode(c, d, qc["k_values"], qc["v_values"], out, lse)
+
+
+@pytest.mark.parametrize("batch", [65, 513])
+def test_decode_of_many_sequences(batch):
+    """Past 512 sequences every unit has a CTA of its own."""
+    rng = np.random.default_rng(batch)
+    c = U.Case((1,) * batch, tuple(int(x) for x in rng.integers(1, 90, batch)), 4, 2, E=64)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    out, lse = run_decode(c, d, qc)
+    U.check_decode(c, d, qc["k_values"], qc["v_values"], out, lse)
+
+
+def test_decode_with_large_and_tiny_queries():
+    """Rows of far apart magnitudes in one unit, and a logit range that moves the
+    running maximum by hundreds."""
+    c = U.Case((1,), (900,), 8, 1, E=64)
+    d = U.make(c)
+    q = d["q"].float()
+    q *= torch.tensor([1e-30, 1e-4, 0.0, 1.0, 30.0, 300.0, 3.0, 1e-38])[None, :, None]
+    d["q"] = q.to(torch.bfloat16)
+    qc = U.quantized(c, d)
+    out, lse = run_decode(c, d, qc)
+    U.check_decode(c, d, qc["k_values"], qc["v_values"], out, lse)
+
+
+def test_rows_that_see_no_key_and_rows_of_no_sequence():
+    c = U.Case((1, 2), (64, 200), 4, 1, positions=True)
+    d = U.make(c)
+    d["key_pos"][:, d["where"][0]] = -1                  # sequence 0: every key hidden
+    d["key_pos"][:, d["where"][1]] = 10                  # sequence 1: every key after its queries
+    d["q_pos"] = torch.tensor([5, 9], dtype=torch.int32)  # ... of row 0, at the second's position
+    qc = U.quantized(c, d)
+    for splits in (0, 1, 2):
+        q = torch.cat([d["q"], d["q"][:2]]).cuda()       # two rows behind the last sequence
+        r = torch.cat([d["r"], d["r"][:2]]).cuda()
+        out = torch.full_like(q, 7.0)
+        lse = torch.full((4, 5), 7.0, device="cuda")
+        rpb.decode_nvfp4(q, U.device_cache(qc, d), r, d["P"].cuda(), d["cu_q"].cuda(), d["cu_k"].cuda(), out=out,
+                         lse=lse, num_splits=splits, **U.call_kw(c, d))
+        ok()
+        assert (out[3:] == 7).all() and (lse[:, 3:] == 7).all()
+        U.check_decode(c, d, qc["k_values"], qc["v_values"], out[:3], lse[:, :3])
+        assert torch.isneginf(lse[:, :2]).all() and torch.isfinite(lse[:, 2]).all()
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_nan_in_masked_places_stays_there(window):
+    """NaN scales in rows that only some query rows see: the others are clean."""
+    c = U.Case((9, 2), (300, 150), 4, 1, window=window, E=64)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    bad = [int(d["where"][0][295]), int(d["where"][1][149])]    # seen by the last rows only
+    if window:
+        bad.append(int(d["where"][0][253]))                     # seen by row 0 and 1 (positions 291, 292)
+        bad.append(int(d["where"][0][100]))                     # seen by none
+    for n in ("k_scale", "v_scale"):
+        qc[n][bad] = 0x7F
+    out, lse = run_decode(c, d, qc)
+    out, lse = host(out.float()), host(lse)
+    sees = {0: [r for r in range(9) if 291 + r >= 295 or (window and r < 2)], 1: [1]}
+    keys = np.where(np.isnan(C.dequantize_nvfp4(qc["k"], qc["k_scale"], d["kg"])), 0, qc["k_values"])
+    values = np.where(np.isnan(C.dequantize_nvfp4(qc["v"], qc["v_scale"], d["vg"])), 0, qc["v_values"])
+    clean = np.ones(11, bool)
+    for b, q0 in ((0, 0), (1, 9)):
+        for r in sees[b]:
+            clean[q0 + r] = False
+    assert np.isnan(out[~clean]).all() and np.isnan(lse[:, ~clean]).all()
+    assert np.isfinite(out[clean]).all() and np.isfinite(lse[:, clean]).all()
+    for b, hq, h, q0, x, mag in U.each_head(c, d, keys):
+        p, z = C.softmax(x)
+        for r in range(x.shape[0]):
+            if clean[q0 + r]:
+                # a rounding of bf16 and one of f16 on sums of magnitude below 1
+                assert np.abs(out[q0 + r, hq] - p[r] @ values[d["where"][b], h]).max() < 2.0 ** -8
+                assert abs(lse[hq, q0 + r] - z[r]) < 1e-3
+
+
+def test_one_nan_value_reaches_its_own_dims_only():
+    c = U.Case((9,), (300,), 4, 1, E=0, r_dim=0)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    qc["v_scale"][295, 0, 3] = 0x7F                     # dims 48 .. 63 of a key that rows 4 .. 8 see
+    out, lse = run_decode(c, d, qc)
+    nan = np.isnan(host(out.float()))
+    want = np.zeros((9, 4, 128), bool)
+    want[4:, :, 48:64] = True
+    np.testing.assert_array_equal(nan, want)
+    assert torch.isfinite(lse).all()
+
+
+def test_decode_reports_bad_pages_positions_and_lengths():
+    c = U.Case((1, 1), (300, 40), 4, 1, page=32)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    good, _ = run_decode(c, d, qc)
+    bad = d["table"].clone()
+    bad[0, 3] = 10 ** 6
+    args = (d["q"].cuda(), U.device_cache(qc, d), d["r"].cuda(), d["P"].cuda(), d["cu_q"].cuda(), d["cu_k"].cuda())
+    kw = U.call_kw(c, d)
+    out, lse = rpb.decode_nvfp4(*args, **{**kw, "block_table": bad.cuda()})
+    torch.cuda.synchronize()
+    assert rpb.relattn_get_device_error() == 6
+    assert torch.isfinite(out.float()).all() and torch.equal(out[1], good[1])
+    # a sequence longer than max_seqlen_k is skipped; the other one is computed
+    out = torch.full_like(out, 7.0)
+    rpb.decode_nvfp4(*args, **{**kw, "max_seqlen_k": 100}, out=out)
+    assert rpb.relattn_get_device_error() == 6
+    assert (out[0] == 7).all()
+    # (its own plan may split it differently: one bf16 rounding apart)
+    assert (out[1].float() - good[1].float()).abs().max() <= 2.0 ** -8 * good[1].float().abs().max()
+    pos = torch.zeros(1, d["rows"], dtype=torch.int32, device="cuda")
+    rpb.decode_nvfp4(*args, **kw, key_pos=pos, q_pos=torch.tensor([-3, 5], dtype=torch.int32, device="cuda"), out=out)
+    assert rpb.relattn_get_device_error() == 6
+    assert (out[0] == 7).all()
+
+
+def test_cache_offsets_past_32_bits():
+    """Pages at the end of a pool whose codes take more than 4 GB."""
+    page, pages, Hkv = 128, (1 << 33) // (128 * 4 * 64) + 4, 4
+    c = U.Case((1, 2), (300, 129), 8, Hkv, E=64)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    small = U.device_cache(qc, d)
+    rows = page * pages
+    big = rpb.KvNvfp4(*(torch.empty(rows, Hkv, t.shape[2], dtype=torch.uint8, device="cuda") for t in small[:4]),
+                      small.k_global, small.v_global)
+    assert big.k.numel() > 1 << 32
+    table = torch.tensor([[pages - 1, 0, pages - 3], [pages - 2, 1, -1]], dtype=torch.int32)
+    where = []
+    for b, n in enumerate(c.k_lens):
+        p = np.arange(n)
+        where.append(table[b].numpy()[p // page].astype(np.int64) * page + p % page)
+        for s, t in zip(small[:4], big[:4]):
+            t[torch.from_numpy(where[b]).cuda()] = s[torch.from_numpy(d["where"][b]).cuda()]
+    kw = {**U.call_kw(c, d), "block_table": table.cuda(), "page_size": page}
+    args = (U.cuda(d["r"]), U.cuda(d["P"]))
+    cu = (d["cu_q"].cuda(), d["cu_k"].cuda())
+    out, lse = rpb.decode_nvfp4(d["q"].cuda(), big, *args, *cu, **kw)
+    ok()
+    U.check_decode(c, d, qc["k_values"], qc["v_values"], out, lse)
+    w = rpb.key_weights(d["q"].cuda(), big, *args, lse, *cu, **kw, decay=0.0,
+                        out=torch.empty(Hkv, rows, device="cuda"))
+    ok()
+    got = torch.zeros(Hkv, d["rows"], device="cuda")
+    for b in range(2):
+        got[:, torch.from_numpy(d["where"][b]).cuda()] = w[:, torch.from_numpy(where[b]).cuda()]
+    U.check_weights(c, d, qc["k_values"], host(lse), None, 0.0, got)
+    # and the rows of its tail come back out of it
+    keep = [100, 60]
+    dst = [torch.empty(160, Hkv, t.shape[2], dtype=torch.uint8, device="cuda") for t in big[:4]]
+    pos, _ = rpb.evict(big[:4], dst, w, cu[1], W.cu_seqlens(keep).cuda(), max_seqlen_k=300, recent=50, sink=2,
+                       total_k=429, total_keep=160, block_table=table.cuda(), page_size=page)
+    ok()
+    for b, o in ((0, 0), (1, 100)):
+        for h in range(Hkv):
+            p = host(pos[h, o:o + keep[b]])
+            np.testing.assert_array_equal(p, C.kept_keys(host(w)[h, where[b]], keep[b], 50, 2))
+            for s, t in zip(small[:4], dst):
+                np.testing.assert_array_equal(host(t)[o:o + keep[b], h], host(s)[d["where"][b][p], h])
+
+
+# ------------------------------------------------------------------ key weights
+
+WEIGHTS = [
+    U.Case((1,), (1,), 1, 1, E=0, r_dim=0),
+    U.Case((1, 1, 1), (33, 1000, 127), 8, 1),
+    U.Case((2, 0, 1), (257, 40, 700), 16, 2, r_dim=64, E=256, base=64.0),      # 16 rows
+    U.Case((9,), (700,), 16, 2, E=64),                                         # 72 rows
+    U.Case((32, 5), (300, 1025), 4, 2, E=77, r_dim=24, base=64.0),             # an observation window
+    U.Case((200, 1, 130), (200, 1, 130), 4, 1, E=64),                          # whole prompts
+    U.Case((300, 40), (300, 90), 8, 2, E=64, window=50),
+    U.Case((1, 1), (1500, 700), 16, 2, window=100, E=1024, r_dim=64),          # keys out of sight decay
+    U.Case((1,) * 4, (33, 64, 500, 7), 8, 2, page=32),
+    U.Case((20, 3), (150, 90), 8, 2, page=64, window=33),
+    U.Case((1, 1), (600, 65), 16, 2, positions=True),
+    U.Case((30, 3), (150, 90), 8, 2, positions=True, page=32, window=60),
+]
+
+
+@pytest.mark.parametrize("i", range(len(WEIGHTS)))
+@pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("decay", [0.0, 0.75])
+def test_key_weights(i, kind, decay):
+    c = WEIGHTS[i]
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    keys = qc["k_values"] if kind == "nvfp4" else d["k"].double().numpy()
+    k = U.device_cache(qc, d) if kind == "nvfp4" else d["k"].cuda()
+    lse = np.zeros((c.Hq, sum(c.q_lens)), np.float32)
+    for b, hq, h, q0, x, mag in U.each_head(c, d, keys):
+        lse[hq, q0:q0 + x.shape[0]] = C.softmax(x)[1]
+    rng = np.random.default_rng(5)
+    w_in = rng.uniform(0, 9, (c.Hkv, d["rows"])).astype(np.float32)
+    given = w_in.copy()
+    if decay == 0:
+        given[:] = np.nan                                # not read
+    for b, (nq, nk) in enumerate(zip(c.q_lens, c.k_lens)):
+        given[:, d["where"][b][nk - nq:]] = np.nan       # the newest rows' are not read either
+    kw = U.call_kw(c, d)
+    args = (d["q"].cuda(), k, U.cuda(d["r"]), U.cuda(d["P"]), torch.from_numpy(lse).cuda(), d["cu_q"].cuda(),
+            d["cu_k"].cuda())
+    out = torch.full((c.Hkv, d["rows"]), 7.0, device="cuda")
+    rpb.key_weights(*args, weights_in=torch.from_numpy(given).cuda(), decay=decay, out=out, **kw)
+    ok()
+    held = U.check_weights(c, d, keys, lse, w_in, decay, out)
+    assert (host(out)[:, ~held] == 7).all()
+    place = torch.from_numpy(given).cuda()               # in place: the same bits
+    rpb.key_weights(*args, weights_in=place, decay=decay, out=place, **kw)
+    ok()
+    assert torch.equal(place[:, torch.from_numpy(held).cuda()], out[:, torch.from_numpy(held).cuda()])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
+def test_rows_without_a_logsumexp_and_nan_keys(kind):
+    """A row with lse = -inf gives nothing, and a NaN key spoils its own weight
+    only where a row sees it."""
+    for q_lens in ((3,), (40,)):
+        c = U.Case(q_lens, (200,), 4, 1, E=0, r_dim=0, window=60)
+        d = U.make(c)
+        qc = U.quantized(c, d)
+        nq = q_lens[0]
+        bad = [20, 199]                                  # out of every window; seen by the last row
+        if kind == "bf16":
+            d["k"][bad] = float("nan")
+            k, keys = d["k"].cuda(), d["k"].double().numpy()
+        else:
+            qc["k_scale"][bad] = 0x7F
+            k, keys = U.device_cache(qc, d), C.dequantize_nvfp4(qc["k"], qc["k_scale"], d["kg"])
+        lse = np.full((4, nq), 5.0, np.float32)
+        lse[:, 0] = -np.inf
+        w = rpb.key_weights(d["q"].cuda(), k, None, None, torch.from_numpy(lse).cuda(), d["cu_q"].cuda(),
+                            d["cu_k"].cuda(), **U.call_kw(c, d))
+        ok()
+        nan = np.isnan(host(w))[0]
+        assert nan.nonzero()[0].tolist() == [199]
+        want = np.zeros(200)
+        for b, hq, h, q0, x, mag in U.each_head(c, d, np.where(np.isnan(keys), 0, keys)):
+            want += np.exp(x - 5.0)[1:].sum(0)
+        # logits of a few units, off by less than 1e-4 (the bound of check_weights)
+        assert np.allclose(host(w)[0, :199], want[:199], rtol=1e-4, atol=1e-30)
+
+
+# ------------------------------------------------------------------ eviction
+
+def _planes(rows, Hkv, kinds, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    out = []
+    for n in kinds:
+        if n == "bf16":
+            out.append(torch.randn(rows, Hkv, 128, generator=g).to(torch.bfloat16))
+        else:
+            out.append(torch.randint(0, 256, (rows, Hkv, n), generator=g, dtype=torch.uint8))
+    return out
+
+
+@pytest.mark.parametrize("k_lens,keep,recent,sink,kinds,page,page_to,ties", [
+    ((1,), (1,), 0, 0, ("bf16",), 0, 0, False),
+    ((50, 7, 0, 33), (20, 7, 0, 1), 4, 2, (64, 64, 8, 8), 0, 0, False),
+    ((50, 64), (3, 10), 16, 4, ("bf16", "bf16"), 0, 0, True),               # fewer kept than recent
+    ((4097, 511), (1000, 510), 0, 0, (128, 128, 4, 4), 0, 0, True),
+    ((4096, 5000), (4096, 4999), 100, 100, (3,), 0, 0, False),              # odd bytes, all kept
+    ((1000, 300), (400, 128), 64, 4, (64, 64, 8, 8), 32, 64, False),        # pages to pages
+    ((17000, 9000), (2000, 8000), 128, 4, (8,), 0, 0, True),                # two CTAs a cluster
+    ((40000,), (5000,), 0, 0, (8,), 128, 0, False),                         # four
+    ((150001,), (75000,), 1024, 4, (8,), 0, 0, True),                       # eight
+])
+def test_evict(k_lens, keep, recent, sink, kinds, page, page_to, ties):
+    Hkv = 2
+    rows, table, where = U.rows_of(k_lens, page, 3)
+    rows_to, table_to, where_to = U.rows_of(keep, page_to, 4)
+    rng = np.random.default_rng(6)
+    w = rng.exponential(1.0, (Hkv, rows)).astype(np.float32)
+    if ties:
+        w = np.round(w, 1)
+        w[:, ::13] = -w[:, ::13]
+        w[:, 5::101] = np.nan
+        w[:, 6::103] = np.inf
+        w[:, 7::107] = -0.0
+    planes = _planes(rows, Hkv, kinds)
+    dst = [torch.full((rows_to, *p.shape[1:]), 3, dtype=p.dtype, device="cuda") for p in planes]
+    kw = {}
+    if page:
+        kw.update(block_table=table.cuda(), page_size=page)
+    if page_to:
+        kw.update(block_table_keep=table_to.cuda(), page_size_keep=page_to)
+    key_pos = torch.from_numpy(rng.integers(0, 1 << 30, (Hkv, rows)).astype(np.int32))
+    for pos_in in (None, key_pos):
+        pos, wk = rpb.evict([p.cuda() for p in planes], dst, torch.from_numpy(w).cuda(), W.cu_seqlens(k_lens).cuda(),
+                            W.cu_seqlens(keep).cuda(), max_seqlen_k=max(k_lens), recent=recent, sink=sink,
+                            total_k=sum(k_lens), total_keep=sum(keep), key_pos=U.cuda(pos_in), **kw)
+        ok()
+        used = np.zeros(rows_to, bool)
+        for b, (n, kk) in enumerate(zip(k_lens, keep)):
+            used[where_to[b]] = True
+            for h in range(Hkv):
+                idx = C.kept_keys(w[h, where[b]], kk, recent, sink)
+                assert len(idx) == kk
+                src = where[b][idx]
+                want = idx if pos_in is None else key_pos[h].numpy()[src]
+                np.testing.assert_array_equal(host(pos)[h, where_to[b]], want)
+                np.testing.assert_array_equal(host(wk)[h, where_to[b]], w[h, src])
+                for p, q in zip(planes, dst):
+                    assert torch.equal(q[torch.from_numpy(where_to[b]).cuda(), h].cpu(), p[torch.from_numpy(src), h])
+        assert (host(pos)[:, ~used] == -1).all()
+        for q in dst:
+            assert (q.cpu().float()[torch.from_numpy(~used)] == 3).all()
+
+
+def test_evict_of_equal_weights_keeps_the_first():
+    n = 20000
+    w = torch.zeros(1, n, device="cuda")
+    pos, _ = rpb.evict([], [], w, W.cu_seqlens([n]).cuda(), W.cu_seqlens([777]).cuda(), max_seqlen_k=n, recent=0,
+                       total_keep=777)
+    ok()
+    assert torch.equal(pos[0].cpu(), torch.arange(777, dtype=torch.int32))
+
+
+def test_evict_skips_and_records_bad_lengths():
+    w = torch.rand(1, 100, device="cuda")
+    p = torch.rand(100, 1, 4, device="cuda")
+    out = torch.full((50, 1, 4), 3.0, device="cuda")
+    cu_k = torch.tensor([0, 20, 100], dtype=torch.int32, device="cuda")
+    cu_keep = torch.tensor([0, 30, 50], dtype=torch.int32, device="cuda")      # 30 of 20
+    pos, _ = rpb.evict([p], [out], w, cu_k, cu_keep, max_seqlen_k=100, recent=5, total_keep=50)
+    torch.cuda.synchronize()
+    assert rpb.relattn_get_device_error() == 6
+    assert (out[:30] == 3).all() and (pos[:, :30] == -1).all()
+    idx = C.kept_keys(host(w)[0, 20:], 20, 5, 0)
+    np.testing.assert_array_equal(host(pos)[0, 30:], idx)
+    assert torch.equal(out[30:, 0], p[20 + torch.from_numpy(idx).cuda(), 0])
+
+
+# ------------------------------------------------------------------ streams, graphs, runs
+
+def test_captured_calls_replay_and_streams_do_not_share():
+    """Two captured decodes with workspaces of their own, replayed together with
+    new inputs; and a call on a side stream."""
+    c = U.Case((1, 2), (700, 300), 8, 2, E=64)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    cache = U.device_cache(qc, d)
+    cu = (d["cu_q"].cuda(), d["cu_k"].cuda())
+    r, P, kw = d["r"].cuda(), d["P"].cuda(), U.call_kw(c, d)
+    qs = [d["q"].cuda(), (d["q"] * 0.5).cuda()]
+    want = [rpb.decode_nvfp4(q, cache, r, P, *cu, **kw) for q in qs]
+    weights = [rpb.key_weights(q, cache, r, P, o[1], *cu, **kw) for q, o in zip(qs, want)]
+    graphs, bufs = [], []
+    for i in range(2):
+        q = torch.zeros_like(qs[i])
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            rpb.decode_nvfp4(q, cache, r, P, *cu, **kw)              # warm up
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o, z = rpb.decode_nvfp4(q, cache, r, P, *cu, **kw)
+            w = rpb.key_weights(q, cache, r, P, z, *cu, **kw)
+        graphs.append(g)
+        bufs.append((q, o, z, w))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for i in range(2):
+            bufs[i][0].copy_(qs[i])
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(bufs[i][1], want[i][0]) and torch.equal(bufs[i][2], want[i][1])
+            assert torch.equal(bufs[i][3], weights[i])
+    side = torch.cuda.Stream()
+    out, lse = rpb.decode_nvfp4(qs[0], cache, r, P, *cu, **kw, stream=side.cuda_stream)
+    w = rpb.key_weights(qs[0], cache, r, P, lse, *cu, **kw, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(out, want[0][0]) and torch.equal(lse, want[0][1]) and torch.equal(w, weights[0])
+    ok()
+
+
+def test_a_prompt_is_cached_weighed_evicted_and_decoded():
+    """The operators in the order a server calls them: a prompt's rows go into a
+    4-bit paged cache, its last rows vote, half of the keys leave, and a
+    token is decoded over the rest at its own position."""
+    page, lens, Hq, Hkv, E = 64, (300, 700), 8, 2, 64
+    c = U.Case(lens, lens, Hq, Hkv, E=E, r_dim=16, base=64.0)
+    d = U.make(c)
+    rows, table, where = U.rows_of([n + 1 for n in lens], page, 9)
+    table = table.cuda()
+    cache = rpb.empty_nvfp4(rows, Hkv, "cuda")
+    cu = W.cu_seqlens(lens).cuda()
+    q, k, v, r, P = (d[n].cuda() for n in ("q", "k", "v", "r", "P"))
+    kw = dict(alpha=c.alpha, log_scale_base=64.0, max_seqlen_k=max(lens))
+    out, lse = rpb.prefill(q, k, v, r, P, cu, cu, max_seqlen_q=max(lens), **kw)
+    rpb.store_nvfp4(k, v, cu, cu, cache, block_table=table, page_size=page)
+    k4, v4 = rpb.load_nvfp4(cache, cu, cu, total_q=sum(lens), block_table=table, page_size=page)
+    # the last 16 rows of each prompt vote, on the cached keys
+    last = torch.cat([torch.arange(sum(lens[:b + 1]) - 16, sum(lens[:b + 1])) for b in range(2)]).cuda()
+    cu_obs = W.cu_seqlens([16, 16]).cuda()
+    w = rpb.key_weights(q[last], cache, r[last], P, lse[:, last].contiguous(), cu_obs, cu, max_seqlen_q=16, decay=0.0,
+                        total_k=sum(lens), block_table=table, page_size=page, **kw)
+    ok()
+    host_k = np.zeros((rows, Hkv, 128))
+    host_v = np.zeros((rows, Hkv, 128))
+    for b in range(2):
+        o = sum(lens[:b])
+        host_k[where[b][:lens[b]]] = k4[o:o + lens[b]].double().cpu().numpy()
+        host_v[where[b][:lens[b]]] = v4[o:o + lens[b]].double().cpu().numpy()
+    c_obs = U.Case((16, 16), lens, Hq, Hkv, E=E, base=64.0)
+    d_obs = dict(d, q=d["q"][last.cpu()], r=d["r"][last.cpu()], where=[where[b][:lens[b]] for b in range(2)])
+    U.check_weights(c_obs, d_obs, host_k, host(lse[:, last]), None, 0.0, w)
+    # half of the keys stay, in contiguous rows with room for one more
+    keep = [n // 2 for n in lens]
+    dst = rpb.empty_nvfp4(sum(keep), Hkv, "cuda")
+    cu_keep = W.cu_seqlens(keep).cuda()
+    pos, wk = rpb.evict(cache[:4], dst[:4], w, cu, cu_keep, max_seqlen_k=max(lens), recent=20, sink=4,
+                        total_k=sum(lens), total_keep=sum(keep), block_table=table, page_size=page)
+    ok()
+    kept = [[C.kept_keys(host(w)[h, where[b][:lens[b]]], keep[b], 20, 4) for h in range(Hkv)] for b in range(2)]
+    # the next token: its row joins each sequence, in pages of its own
+    rows2, table2, where2 = U.rows_of([n + 1 for n in keep], 32, 11)
+    cache2 = rpb.empty_nvfp4(rows2, Hkv, "cuda")
+    pos2 = torch.full((Hkv, rows2), -1, dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(12)
+    new_k, new_v, new_q = (U.bf16(rng.standard_normal((2, H, 128))) for H in (Hkv, Hkv, Hq))
+    new_r = U.bf16(rng.standard_normal((2, Hq, 16)))
+    for b in range(2):
+        a = sum(keep[:b])
+        at = torch.from_numpy(where2[b]).cuda()
+        for s, t in zip(dst[:4], cache2[:4]):
+            t[at[:-1]] = s[a:a + keep[b]]
+        pos2[:, at[:-1]] = pos[:, a:a + keep[b]]
+        pos2[:, at[-1]] = lens[b]
+    cu1, cu2 = W.cu_seqlens([1, 1]).cuda(), W.cu_seqlens([n + 1 for n in keep]).cuda()
+    t2 = table2.cuda()
+    rpb.store_nvfp4(new_k.cuda(), new_v.cuda(), cu1, cu2, cache2, block_table=t2, page_size=32)
+    out, lse2 = rpb.decode_nvfp4(new_q.cuda(), cache2, new_r.cuda(), P, cu1, cu2, max_seqlen_q=1,
+                                 max_seqlen_k=max(keep) + 1, alpha=c.alpha, log_scale_base=64.0, key_pos=pos2,
+                                 q_pos=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                 block_table=t2, page_size=32, total_k=sum(keep) + 2)
+    ok()
+    keys = np.zeros((rows2, Hkv, 128))
+    vals = np.zeros((rows2, Hkv, 128))
+    kp = np.full((Hkv, rows2), -1, np.int32)
+    for b in range(2):
+        for h in range(Hkv):
+            keys[where2[b][:-1], h] = host_k[where[b][kept[b][h]], h]
+            vals[where2[b][:-1], h] = host_v[where[b][kept[b][h]], h]
+            kp[h, where2[b][:-1]] = kept[b][h]
+            kp[h, where2[b][-1]] = lens[b]
+        keys[where2[b][-1]] = C.dequantize_nvfp4(*C.quantize_nvfp4(new_k[b:b + 1].float().numpy()))[0]
+        vals[where2[b][-1]] = C.dequantize_nvfp4(*C.quantize_nvfp4(new_v[b:b + 1].float().numpy()))[0]
+    np.testing.assert_array_equal(host(pos2), kp)
+    c2 = U.Case((1, 1), tuple(n + 1 for n in keep), Hq, Hkv, E=E, base=64.0, positions=True)
+    d2 = dict(q=new_q, r=new_r, P=d["P"], where=where2, key_pos=torch.from_numpy(kp),
+              q_pos=torch.tensor(lens, dtype=torch.int32))
+    U.check_decode(c2, d2, keys, vals, out, lse2)
+
+
+def test_a_thinned_bf16_cache_under_the_plain_decode():
+    """Without a log-scale and with the bias inside the newest keys, the bf16
+    decode reads an evicted cache as it is."""
+    lens, keep, Hq, Hkv, E = (400, 900), (150, 300), 8, 2, 64
+    c = U.Case((1, 1), lens, Hq, Hkv, E=E)
+    d = U.make(c)
+    cu1, cu = W.cu_seqlens([1, 1]).cuda(), W.cu_seqlens(lens).cuda()
+    q, k, v, r, P = (d[n].cuda() for n in ("q", "k", "v", "r", "P"))
+    kw = dict(max_seqlen_q=1, alpha=c.alpha)
+    out, lse = rpb.decode(q, k, v, r, P, cu1, cu, max_seqlen_k=900, **kw)
+    w = rpb.key_weights(q, k, r, P, lse, cu1, cu, max_seqlen_k=900, **kw)
+    ok()
+    dst = [torch.empty(sum(keep), Hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cu_keep = W.cu_seqlens(keep).cuda()
+    pos, _ = rpb.evict([k, v], dst, w, cu, cu_keep, max_seqlen_k=900, recent=E, total_keep=sum(keep))
+    out2, lse2 = rpb.decode(q, *dst, r, P, cu1, cu_keep, max_seqlen_k=300, **kw)
+    ok()
+    for b, hq, h, q0, x, mag in U.each_head(c, d, d["k"].double().numpy()):
+        idx = C.kept_keys(host(w)[h, d["where"][b]], keep[b], E, 0)
+        np.testing.assert_array_equal(host(pos)[h, sum(keep[:b]):sum(keep[:b]) + keep[b]], idx)
+        p, z = C.softmax(x[:, idx])
+        ref = p @ d["v"].double().numpy()[d["where"][b][idx], h]
+        # the framework's own bounds for this decode
+        assert np.abs(out2[q0, hq].double().cpu().numpy() - ref[0]).max() <= 2e-2
+        assert abs(float(lse2[hq, q0]) - z[0]) <= 1e-3
