@@ -653,16 +653,34 @@ def relattn_evict_workspace_size(params: RelattnEvictParams) -> Tuple[int, int]:
     return st, int(n.value)
 
 
-class KvNvfp4(NamedTuple):
-    """A 4-bit (NVFP4) K / V cache: code bytes k / v uint8 [rows, Hkv, 64], E4M3
-    scale bytes k_scale / v_scale uint8 [rows, Hkv, 8], and optional fp32 [Hkv]
-    factors (None: 1)."""
+class _KvTensors(NamedTuple):
     k: "torch.Tensor"            # noqa: F821
     v: "torch.Tensor"            # noqa: F821
     k_scale: "torch.Tensor"      # noqa: F821
     v_scale: "torch.Tensor"      # noqa: F821
     k_global: Optional["torch.Tensor"] = None   # noqa: F821
     v_global: Optional["torch.Tensor"] = None   # noqa: F821
+
+
+class KvNvfp4(_KvTensors):
+    """A 4-bit (NVFP4) K / V cache: code bytes k / v uint8 [rows, Hkv, 64], E4M3
+    scale bytes k_scale / v_scale uint8 [rows, Hkv, 8], and optional fp32 [Hkv]
+    factors (None: 1).  The tensors are checked here, once."""
+
+    def __new__(cls, k, v, k_scale, v_scale, k_global=None, v_global=None):
+        import torch
+        dev = k.device
+        _need(k.dim() == 3, "cache.k must have three dimensions")
+        rows, H = (int(x) for x in k.shape[:2])
+        ptr = {}
+        for n, t, w in (("k", k, 64), ("v", v, 64), ("k_scale", k_scale, 8), ("v_scale", v_scale, 8)):
+            ptr[n] = _tensor(t, f"cache.{n}", torch.uint8, (rows, H, w), dev)
+        for n, t in (("k_global", k_global), ("v_global", v_global)):
+            ptr[n] = None if t is None else _tensor(t, f"cache.{n}", torch.float32, (H,), dev)
+        self = super().__new__(cls, k, v, k_scale, v_scale, k_global, v_global)
+        self.rows, self.num_heads_kv, self.device = rows, H, dev
+        self.c_struct = RelattnKvNvfp4(rows=rows, **ptr)
+        return self
 
 
 def empty_nvfp4(rows: int, num_heads_kv: int, device, k_global=None, v_global=None) -> KvNvfp4:
@@ -678,33 +696,37 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _tensor(t, name: str, dtype, shape, device):
-    """A contiguous tensor of this type and shape (None: any size) on `device`."""
+def _tensor(t, name: str, dtype, shape, device) -> int:
+    """Address of a contiguous tensor of this type and shape on `device`."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _need(t.dim() == len(shape) and all(s is None or int(s) == n for s, n in zip(shape, t.shape)),
-          f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _need(t.shape == shape, f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     _need(t.is_contiguous(), f"{name} must be contiguous")
-    _need(t.device == device, f"{name} is on {t.device}, not {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, not {device}")
 
 
-def _cu(t, name: str, device, batch: Optional[int] = None):
+def _shape(t, name: str, n: int, *want):
+    """t's shape, of n dimensions whose last ones are `want`."""
+    s = t.shape
+    if len(s) != n or (want and s[n - len(want):] != want):
+        raise ValueError(f"{name} must have {n} dimensions{f' ending in {want}' if want else ''}, not shape {tuple(s)}")
+    return s
+
+
+def _lengths(cu_q, cu_k, name_q: str, name_k: str, device):
+    """(batch, addresses) of two cu_seqlens tensors."""
     import torch
-    return _tensor(t, name, torch.int32, [None if batch is None else batch + 1], device)
+    n = cu_q.numel()
+    _need(n >= 1, f"{name_q} needs at least one entry")
+    return n - 1, _tensor(cu_q, name_q, torch.int32, (n,), device), _tensor(cu_k, name_k, torch.int32, (n,), device)
 
 
-def _cache(cache: KvNvfp4, device, num_heads_kv: Optional[int] = None) -> RelattnKvNvfp4:
-    import torch
+def _cache(cache: KvNvfp4, device) -> RelattnKvNvfp4:
     _need(isinstance(cache, KvNvfp4), "cache must be a KvNvfp4")
-    rows = int(cache.k.shape[0])
-    H = int(cache.k.shape[1]) if cache.k.dim() == 3 and num_heads_kv is None else num_heads_kv
-    out = {}
-    for n in ("k", "v"):
-        out[n] = _tensor(getattr(cache, n), f"cache.{n}", torch.uint8, [rows, H, 64], device)
-        out[n + "_scale"] = _tensor(getattr(cache, n + "_scale"), f"cache.{n}_scale", torch.uint8, [rows, H, 8], device)
-        g = getattr(cache, n + "_global")
-        out[n + "_global"] = None if g is None else _tensor(g, f"cache.{n}_global", torch.float32, [H], device)
-    return RelattnKvNvfp4(rows=rows, **out)
+    if cache.device != device:
+        raise ValueError(f"the cache is on {cache.device}, not {device}")
+    return cache.c_struct
 
 
 def _pages(block_table, page_size: int, rows: int, device, batch: int) -> Optional[RelattnPagedKV]:
@@ -712,9 +734,9 @@ def _pages(block_table, page_size: int, rows: int, device, batch: int) -> Option
     if block_table is None:
         return None
     _need(page_size > 0 and rows % page_size == 0, "rows must be a multiple of page_size")
-    return RelattnPagedKV(block_table=_tensor(block_table, "block_table", torch.int32, [batch, None], device),
-                          max_pages_per_seq=int(block_table.shape[1]), page_size=int(page_size),
-                          num_pages=rows // int(page_size))
+    slots = _shape(block_table, "block_table", 2)[1]
+    return RelattnPagedKV(_tensor(block_table, "block_table", torch.int32, (batch, slots), device), slots,
+                          page_size, rows // page_size)
 
 
 def _positions(key_pos, q_pos, num_heads_kv: int, rows: int, batch: int, device) -> Optional[RelattnPositions]:
@@ -722,8 +744,8 @@ def _positions(key_pos, q_pos, num_heads_kv: int, rows: int, batch: int, device)
     if key_pos is None and q_pos is None:
         return None
     _need(key_pos is not None and q_pos is not None, "key_pos and q_pos go together")
-    return RelattnPositions(key_pos=_tensor(key_pos, "key_pos", torch.int32, [num_heads_kv, rows], device),
-                            q_pos=_tensor(q_pos, "q_pos", torch.int32, [batch], device))
+    return RelattnPositions(_tensor(key_pos, "key_pos", torch.int32, (num_heads_kv, rows), device),
+                            _tensor(q_pos, "q_pos", torch.int32, (batch,), device))
 
 
 class _on:
@@ -732,12 +754,17 @@ class _on:
     belongs to the stream it launches on.  Gives the stream to launch on."""
 
     def __init__(self, device, stream: Optional[int]):
-        _need(device.type == "cuda", f"tensors must be on a CUDA device, not {device}")
-        self.device, self.stream, self.stack = device, stream, contextlib.ExitStack()
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, not {device}")
+        self.device, self.stream, self.stack = device, stream, None
 
     def __enter__(self) -> int:
         import torch
-        if self.device.index != torch.cuda.current_device():
+        other = self.device.index != torch.cuda.current_device()
+        if not other and self.stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        self.stack = contextlib.ExitStack()
+        if other:
             self.stack.enter_context(torch.cuda.device(self.device))
         if self.stream is not None:
             self.stack.enter_context(torch.cuda.stream(
@@ -746,34 +773,37 @@ class _on:
         return torch.cuda.current_stream(self.device).cuda_stream
 
     def __exit__(self, *exc):
-        return self.stack.__exit__(*exc)
+        return self.stack.__exit__(*exc) if self.stack is not None else None
 
 
-def _query_args(q, r, P, num_heads_kv: int, device):
-    """Checks q [Tq, Hq, 128], r [Tq, Hq, r_dim], P [r_dim, E]."""
+def _queries(q, r, P, num_heads_kv: int, device):
+    """(total_q, Hq, r_dim, E) and addresses of q [Tq, Hq, 128], r [Tq, Hq,
+    r_dim], P [r_dim, E]."""
     import torch
-    _tensor(q, "q", torch.bfloat16, [None, None, HEAD_DIM], device)
-    _need(q.shape[1] % num_heads_kv == 0, "num_heads_q must be a multiple of num_heads_kv")
-    _need((r is None) == (P is None), "r and P go together")
-    if r is not None:
-        _tensor(r, "r", torch.bfloat16, [q.shape[0], q.shape[1], None], device)
-        _tensor(P, "P", torch.bfloat16, [r.shape[2], None], device)
+    Tq, Hq, _ = _shape(q, "q", 3, HEAD_DIM)
+    if num_heads_kv <= 0 or Hq % num_heads_kv:
+        raise ValueError(f"num_heads_q = {Hq} must be a multiple of num_heads_kv = {num_heads_kv}")
+    qp = _tensor(q, "q", torch.bfloat16, q.shape, device)
+    if r is None or P is None:
+        _need(r is None and P is None, "r and P go together")
+        return Tq, Hq, 0, 0, qp, None, None
+    rd = _shape(r, "r", 3)[2]
+    E = _shape(P, "P", 2)[1]
+    return (Tq, Hq, rd, E, qp, _tensor(r, "r", torch.bfloat16, (Tq, Hq, rd), device),
+            _tensor(P, "P", torch.bfloat16, (rd, E), device))
 
 
 def _cache_rows(k, v, cu_q, cu_k, cache, block_table, page_size):
     import torch
     dev = k.device
     kv = _cache(cache, dev)
-    H = int(cache.k.shape[1])
-    batch = int(cu_q.numel()) - 1
-    _need(batch >= 0, "cu_seqlens_q needs at least one entry")
-    pages = _pages(block_table, page_size, kv.rows, dev, batch)
+    H = cache.num_heads_kv
+    batch, cq, ck = _lengths(cu_q, cu_k, "cu_seqlens_q", "cu_seqlens_k", dev)
+    pages = _pages(block_table, page_size, cache.rows, dev, batch)
+    shape = (k.shape[0], H, HEAD_DIM)
     return RelattnCacheRowsParams(
-        k=_tensor(k, "k", torch.bfloat16, [None, H, HEAD_DIM], dev),
-        v=_tensor(v, "v", torch.bfloat16, [k.shape[0], H, HEAD_DIM], dev),
-        cu_seqlens_q=_cu(cu_q, "cu_seqlens_q", dev), cu_seqlens_k=_cu(cu_k, "cu_seqlens_k", dev, batch),
-        batch=batch, total_q=int(k.shape[0]), num_heads_kv=H, head_dim=HEAD_DIM,
-        cache=ctypes.pointer(kv), pages=None if pages is None else ctypes.pointer(pages))
+        _tensor(k, "k", torch.bfloat16, shape, dev), _tensor(v, "v", torch.bfloat16, shape, dev), cq, ck, batch,
+        shape[0], H, HEAD_DIM, ctypes.pointer(kv), None if pages is None else ctypes.pointer(pages))
 
 
 def store_nvfp4(k, v, cu_seqlens_q, cu_seqlens_k, cache: KvNvfp4, *, block_table=None, page_size: int = 0,
@@ -791,24 +821,14 @@ def load_nvfp4(cache: KvNvfp4, cu_seqlens_q, cu_seqlens_k, *, total_q: int, bloc
     """The last cu_seqlens_q rows of every sequence as bf16 (k, v) [total_q, Hkv,
     128] (pass cu_seqlens_k twice for all of them)."""
     import torch
-    with _on(cache.k.device, stream) as st:
-        shape = (int(total_q), int(cache.k.shape[1]), HEAD_DIM)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if v is None else v
+    with _on(cache.device, stream) as st:
+        shape = (int(total_q), cache.num_heads_kv, HEAD_DIM)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
         _need(k.shape[0] == total_q, "k must have total_q rows")
         prm = _cache_rows(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table, page_size)
         _check(relattn_load_nvfp4(prm, st), "relattn_load_nvfp4")
         return k, v
-
-
-def _forward_params(q, k, r, P, cu_q, cu_k, *, total_k, num_heads_kv, **kw) -> RelattnParams:
-    r_dim = 0 if r is None else int(r.shape[2])
-    return RelattnParams(
-        q=q.data_ptr(), k=None if k is None else k.data_ptr(),
-        r=None if r is None else r.data_ptr(), P=None if P is None else P.data_ptr(),
-        cu_seqlens_q=cu_q.data_ptr(), cu_seqlens_k=cu_k.data_ptr(), batch=int(cu_q.numel()) - 1,
-        total_q=int(q.shape[0]), total_k=int(total_k), num_heads_q=int(q.shape[1]), num_heads_kv=int(num_heads_kv),
-        head_dim=int(q.shape[2]), r_dim=r_dim, rel_extent=0 if P is None else int(P.shape[1]), **kw)
 
 
 def _total_k(total_k: Optional[int], block_table, cu_k, rows: int) -> int:
@@ -840,22 +860,18 @@ def decode_nvfp4(q, cache: KvNvfp4, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seq
     import torch
     dev = q.device
     with _on(dev, stream) as st:
-        H = int(cache.k.shape[1])
         kv = _cache(cache, dev)
-        _query_args(q, r, P, H, dev)
-        batch = int(cu_seqlens_q.numel()) - 1
-        _cu(cu_seqlens_q, "cu_seqlens_q", dev)
-        _cu(cu_seqlens_k, "cu_seqlens_k", dev, batch)
-        pages = _pages(block_table, page_size, kv.rows, dev, batch)
-        pos = _positions(key_pos, q_pos, H, kv.rows, batch, dev)
+        H, rows = cache.num_heads_kv, cache.rows
+        Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
+        batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
+        pages = _pages(block_table, page_size, rows, dev, batch)
+        pos = _positions(key_pos, q_pos, H, rows, batch, dev)
         out, lse = _outputs(q, out, lse)
-        _tensor(out, "out", torch.bfloat16, q.shape, dev)
-        _tensor(lse, "lse", torch.float32, [q.shape[1], q.shape[0]], dev)
-        prm = _forward_params(q, None, r, P, cu_seqlens_q, cu_seqlens_k,
-                              total_k=_total_k(total_k, block_table, cu_seqlens_k, kv.rows), num_heads_kv=H,
-                              max_seqlen_q=int(max_seqlen_q), max_seqlen_k=int(max_seqlen_k), alpha=float(alpha),
-                              window=int(window), log_scale_base=float(log_scale_base), out=out.data_ptr(),
-                              lse=lse.data_ptr(), num_splits=int(num_splits))
+        prm = RelattnParams(
+            qp, None, None, rp, Pp, cq, ck, batch, Tq, _total_k(total_k, block_table, cu_seqlens_k, rows),
+            max_seqlen_q, max_seqlen_k, Hq, H, HEAD_DIM, rd, E, window, alpha, log_scale_base,
+            _tensor(out, "out", torch.bfloat16, (Tq, Hq, HEAD_DIM), dev),
+            _tensor(lse, "lse", torch.float32, (Hq, Tq), dev), None, 0, num_splits)
         status, need = relattn_decode_nvfp4_workspace_size(prm, pos)
         _check(status, "relattn_decode_nvfp4_workspace_size")
         keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
@@ -877,31 +893,29 @@ def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: in
     dev = q.device
     with _on(dev, stream) as st:
         fp4 = isinstance(k, KvNvfp4)
-        kv = _cache(k, dev) if fp4 else None
-        if not fp4:
-            _tensor(k, "k", torch.bfloat16, [None, None, HEAD_DIM], dev)
-        rows, H = (int(x) for x in (k.k if fp4 else k).shape[:2])
-        _query_args(q, r, P, H, dev)
-        _tensor(lse, "lse", torch.float32, [q.shape[1], q.shape[0]], dev)
-        batch = int(cu_seqlens_q.numel()) - 1
-        _cu(cu_seqlens_q, "cu_seqlens_q", dev)
-        _cu(cu_seqlens_k, "cu_seqlens_k", dev, batch)
+        if fp4:
+            kv, rows, H = _cache(k, dev), k.rows, k.num_heads_kv
+        else:
+            rows, H, _ = _shape(k, "k", 3, HEAD_DIM)
+            kp = _tensor(k, "k", torch.bfloat16, k.shape, dev)
+        Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
+        batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
         pages = _pages(block_table, page_size, rows, dev, batch)
         pos = _positions(key_pos, q_pos, H, rows, batch, dev)
-        w_in = None if weights_in is None else _tensor(weights_in, "weights_in", torch.float32, [H, rows], dev)
+        w_in = None if weights_in is None else _tensor(weights_in, "weights_in", torch.float32, (H, rows), dev)
         if out is None:
             out = torch.zeros(H, rows, dtype=torch.float32, device=dev)
-        _tensor(out, "out", torch.float32, [H, rows], dev)
         total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
         if not fp4 and block_table is None:
             _need(total_k == rows, "a contiguous k has total_k rows")
-        fwd = _forward_params(q, None if fp4 else k, r, P, cu_seqlens_q, cu_seqlens_k, total_k=total_k, num_heads_kv=H,
-                              max_seqlen_q=int(max_seqlen_q), max_seqlen_k=int(max_seqlen_k), alpha=float(alpha),
-                              window=int(window), log_scale_base=float(log_scale_base), lse=lse.data_ptr())
+        fwd = RelattnParams(
+            qp, None if fp4 else kp, None, rp, Pp, cq, ck, batch, Tq, total_k, max_seqlen_q, max_seqlen_k, Hq, H,
+            HEAD_DIM, rd, E, window, alpha, log_scale_base, None,
+            _tensor(lse, "lse", torch.float32, (Hq, Tq), dev), None, 0, 0)
         prm = RelattnKeyWeightsParams(
-            fwd=fwd, cache=ctypes.pointer(kv) if fp4 else None, positions=None if pos is None else ctypes.pointer(pos),
-            pages=None if pages is None else ctypes.pointer(pages), weights_in=w_in, weights_out=out.data_ptr(),
-            decay=float(decay))
+            fwd, ctypes.pointer(kv) if fp4 else None, None if pos is None else ctypes.pointer(pos),
+            None if pages is None else ctypes.pointer(pages), w_in,
+            _tensor(out, "out", torch.float32, (H, rows), dev), decay)
         status, need = relattn_key_weights_workspace_size(prm)
         _check(status, "relattn_key_weights_workspace_size")
         keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
@@ -922,40 +936,37 @@ def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seq
     import torch
     dev = weights.device
     with _on(dev, stream) as st:
-        _need(len(planes) == len(dst_planes) <= MAX_PLANES, f"as many dst_planes as planes, at most {MAX_PLANES}")
-        _tensor(weights, "weights", torch.float32, [None, None], dev)
-        H, rows = (int(x) for x in weights.shape)
-        batch = int(cu_seqlens_k.numel()) - 1
-        _cu(cu_seqlens_k, "cu_seqlens_k", dev)
-        _cu(cu_seqlens_keep, "cu_seqlens_keep", dev, batch)
-        rows_keep = int(dst_planes[0].shape[0]) if len(dst_planes) else int(total_keep)
-        prm = RelattnEvictParams(num_planes=len(planes))
-        for i, (a, b) in enumerate(zip(planes, dst_planes)):
-            _need(a.dim() >= 2 and tuple(a.shape[:2]) == (rows, H) and tuple(b.shape) == (rows_keep, *a.shape[1:]),
-                  f"plane {i} must be [rows, Hkv, ...] and its destination [rows_keep, Hkv, ...]")
-            _tensor(a, f"plane {i}", a.dtype, a.shape, dev)
-            _tensor(b, f"destination {i}", a.dtype, b.shape, dev)
-            n = a.element_size()
-            for s in a.shape[2:]:
-                n *= int(s)
-            prm.planes[i] = RelattnPlane(src=a.data_ptr(), dst=b.data_ptr(), bytes=n)
+        n = len(planes)
+        if not n == len(dst_planes) <= MAX_PLANES:
+            raise ValueError(f"as many dst_planes as planes, at most {MAX_PLANES}")
+        H, rows = _shape(weights, "weights", 2)
+        batch, ck, ckeep = _lengths(cu_seqlens_k, cu_seqlens_keep, "cu_seqlens_k", "cu_seqlens_keep", dev)
+        rows_keep = dst_planes[0].shape[0] if n else int(total_keep)
+        prm = RelattnEvictParams(_tensor(weights, "weights", torch.float32, (H, rows), dev), ck, ckeep)
+        for i in range(n):
+            a, b = planes[i], dst_planes[i]
+            rest = a.shape[2:]
+            if a.shape[:2] != (rows, H) or b.shape != (rows_keep, H, *rest):
+                raise ValueError(f"plane {i} must be [rows, Hkv, ...] and its destination [rows_keep, Hkv, ...]")
+            prm.planes[i] = RelattnPlane(_tensor(a, f"plane {i}", a.dtype, a.shape, dev),
+                                         _tensor(b, f"destination {i}", a.dtype, b.shape, dev),
+                                         a.element_size() * rest.numel())
         pages = _pages(block_table, page_size, rows, dev, batch)
         pages_keep = _pages(block_table_keep, page_size_keep, rows_keep, dev, batch)
         if key_pos_out is None:
             key_pos_out = torch.full((H, rows_keep), -1, dtype=torch.int32, device=dev)
         if weights_out is None:
             weights_out = torch.zeros(H, rows_keep, dtype=torch.float32, device=dev)
-        prm.weights, prm.cu_seqlens_k, prm.cu_seqlens_keep = (weights.data_ptr(), cu_seqlens_k.data_ptr(),
-                                                              cu_seqlens_keep.data_ptr())
-        prm.key_pos = None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, [H, rows], dev)
-        prm.batch, prm.total_keep, prm.num_heads_kv = batch, int(total_keep), H
+        prm.key_pos = None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, (H, rows), dev)
+        prm.batch, prm.total_keep, prm.num_heads_kv, prm.num_planes = batch, total_keep, H, n
         prm.total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
-        prm.max_seqlen_k, prm.sink, prm.recent, prm.rows, prm.rows_keep = (int(max_seqlen_k), int(sink), int(recent), rows,
-                                                                           rows_keep)
-        prm.pages = None if pages is None else ctypes.pointer(pages)
-        prm.pages_keep = None if pages_keep is None else ctypes.pointer(pages_keep)
-        prm.weights_out = _tensor(weights_out, "weights_out", torch.float32, [H, rows_keep], dev)
-        prm.key_pos_out = _tensor(key_pos_out, "key_pos_out", torch.int32, [H, rows_keep], dev)
+        prm.max_seqlen_k, prm.sink, prm.recent, prm.rows, prm.rows_keep = max_seqlen_k, sink, recent, rows, rows_keep
+        if pages is not None:
+            prm.pages = ctypes.pointer(pages)
+        if pages_keep is not None:
+            prm.pages_keep = ctypes.pointer(pages_keep)
+        prm.weights_out = _tensor(weights_out, "weights_out", torch.float32, (H, rows_keep), dev)
+        prm.key_pos_out = _tensor(key_pos_out, "key_pos_out", torch.int32, (H, rows_keep), dev)
         status, need = relattn_evict_workspace_size(prm)
         _check(status, "relattn_evict_workspace_size")
         keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)

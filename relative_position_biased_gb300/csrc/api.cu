@@ -409,9 +409,16 @@ relattn_status validate_cached(const relattn_params *p, bool decode, const void 
   return (long)p->batch * p->num_heads_kv > 65535 ? RELATTN_ERR_UNSUPPORTED : RELATTN_OK;
 }
 
-size_t key_weights_bytes(const relattn_params &f) {
-  if (!(f.r_dim > 0 && f.rel_extent > 0) || f.batch == 0) return 0;
-  return (size_t)f.total_q * f.num_heads_q * f.rel_extent * sizeof(float);
+// the sizes that the key weights' workspace depends on
+KernelArgs key_weight_sizes(const relattn_params &f) {
+  KernelArgs a = {};
+  a.batch = f.batch;
+  a.total_q = f.total_q;
+  a.max_q = f.max_seqlen_q;
+  a.Hq = f.num_heads_q;
+  a.group = f.num_heads_q / f.num_heads_kv;
+  a.E = f.r_dim > 0 ? f.rel_extent : 0;
+  return a;
 }
 
 size_t evict_bytes(const relattn_evict_params &p) {
@@ -799,9 +806,10 @@ relattn_status relattn_decode_nvfp4(const relattn_params *p, const relattn_kv_nv
 
 relattn_status relattn_key_weights_workspace_size(const relattn_key_weights_params *p, size_t *bytes) {
   if (!p || !bytes) return RELATTN_ERR_INVALID_ARG;
-  const relattn_status st = validate_cached(&p->fwd, false, p->fwd.q, p->fwd.q, p->fwd.q);
+  const relattn_params &f = p->fwd;
+  const relattn_status st = validate_cached(&f, false, f.q, f.q, f.q);
   if (st != RELATTN_OK) return st;
-  *bytes = key_weights_bytes(p->fwd);
+  *bytes = f.batch == 0 || f.total_q == 0 ? 0 : key_weights_workspace(key_weight_sizes(f), p->positions != nullptr);
   return RELATTN_OK;
 }
 
@@ -828,7 +836,7 @@ relattn_status relattn_key_weights(const relattn_key_weights_params *p, void *st
   const size_t n = (size_t)rows * f.num_heads_kv * sizeof(float);
   if (p->weights_in && p->weights_in != p->weights_out && overlaps(p->weights_in, n, p->weights_out, n))
     return RELATTN_ERR_INVALID_ARG;
-  const size_t need = key_weights_bytes(f);
+  const size_t need = key_weights_workspace(key_weight_sizes(f), p->positions != nullptr);
   if (need > 0 && (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < need)) return RELATTN_ERR_WORKSPACE;
   if ((st = make_args(&f, &x.a)) != RELATTN_OK) return st;
   x.a.rdec = static_cast<const float *>(p->workspace);

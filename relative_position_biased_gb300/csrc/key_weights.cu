@@ -16,10 +16,17 @@
 //     a warp streams 32 keys at a time through its own ring; bound by K's bytes.
 //   many rows: a CTA holds 128 keys as operands in registers and takes the
 //     rows that see them 32 at a time through shared memory; bound by the
-//     matrix instruction and the exponentials.
+//     matrix instruction and the exponentials.  The bias is a product too:
+//     key j and a row at position i meet column i - j of P, so a table of P's
+//     columns in falling order makes the 16 keys' bias columns 16 consecutive
+//     rows, and P^T r^T of one token's rows is 4 more instructions of the
+//     same shape, its operand read from shared memory at the token's offset.
+//     Nothing of size rows x E is ever stored.
+//   rows past the bias band (distance >= E for all 128 keys): the tcgen05
+//     kernel of key_weights_tc.cu, which adds to these sums.
 #include <algorithm>
 
-#include "cache_walk.cuh"
+#include "key_weights.cuh"
 
 namespace relattn {
 namespace {
@@ -117,13 +124,6 @@ __device__ __forceinline__ float quad_reduce(const float (&v)[4], int t) {
   const float x = ((t & 1) ? v[1] : v[0]) + __shfl_xor_sync(full, a, 1);
   const float y = ((t & 1) ? v[3] : v[2]) + __shfl_xor_sync(full, b, 1);
   return ((t & 2) ? y : x) + __shfl_xor_sync(full, (t & 2) ? x : y, 2);
-}
-
-// w_out of key `key` (cache row `row`) with the new weight `sum`.
-__device__ __forceinline__ void write_weight(const KeyWeightArgs &p, const Unit &u, int key, long row, float sum) {
-  const long at = (long)u.h * p.pages.rows + row;
-  if (p.w_in && p.decay != 0.f && key < u.s.lk - u.s.lq) sum = fmaf(p.decay, __ldg(p.w_in + at), sum);
-  p.w_out[at] = sum;
 }
 
 // ------------------------------------------------------------------ few rows
@@ -316,15 +316,15 @@ __global__ void __launch_bounds__(WT) relattn_key_weights_rows_kernel(const __gr
 // ------------------------------------------------------------------ many rows
 
 constexpr int QR = 32;                       // query rows staged at a time
+constexpr int TR = 256;                      // rows of the bias table in shared memory, a ring
+// shared memory: K as operands, then (its place) the ring; two stages of q and r rows
+constexpr int ST_Q = WW * WK * 256, ST_R = ST_Q + 2 * QR * 256, ST_C = ST_R + 2 * QR * 128;
+constexpr int ST_BYTES = ST_C + 2 * QR * 5 * 4;
+static_assert(TR * 128 <= ST_Q && TR >= 128 + 2 * QR, "two stages' table rows fit the ring");
 
-template <bool POS, bool FP4>
-__global__ void __launch_bounds__(WT) relattn_key_weights_tiles_kernel(const __grid_constant__ KeyWeightArgs p) {
-  // K first (its stage layout, one per warp), then the staged rows
-  __shared__ __align__(128) uint8_t sk[WW * KStage<FP4>::bytes];
-  __shared__ __align__(128) uint8_t sq[QR * 256];
-  __shared__ float s_coef[QR], s_bscale[QR], s_lse[QR];
-  __shared__ int s_qp[QR];
-  __shared__ long s_row[QR];
+template <bool POS>
+__global__ void __launch_bounds__(WT, 3) relattn_key_weights_tiles_kernel(const __grid_constant__ KeyWeightArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const unsigned full = 0xffffffffu;
   Unit u;
@@ -338,26 +338,30 @@ __global__ void __launch_bounds__(WT) relattn_key_weights_tiles_kernel(const __g
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  u.nrows = u.s.lq * p.a.group;
   u.qbase = u.s.lq > 0 ? first_query_pos(u.s, p.q_pos, u.b) : 0;
   const unsigned wlim = p.a.window > 0 ? (unsigned)p.a.window : 0x80000000u;
-  // tokens that may see a key of the tile
+  // tokens that may see a key of the tile, less those the tcgen05 kernel takes
   int tok0 = 0, tok1 = u.s.lq;
   if (!POS) {
     tok0 = max(0, tile0 - u.qbase);
     const long last = (long)min(tile0 + kWalkTile, u.s.lk) - 1 + wlim - u.qbase;   // first token past the window
     if (last < tok1) tok1 = (int)max(last, 0L);
+    if (p.tc) tok1 = min(tok1, tc_first_token(p, u.qbase, tile0));
   }
   const long row0 = group_row(p, u, key0);
-  const uint32_t st = smem_addr(sk) + warp * KStage<FP4>::bytes;
   uint32_t f[2][8][4];
   if (tok0 < tok1) {
-    issue_keys<FP4>(p, u, st, key0, row0, lane);
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncwarp();
-    key_operands<FP4>(st, 0, lane, f[0]);
-    key_operands<FP4>(st, 1, lane, f[1]);
+    load_key_tile(p, u, tile0, tid, WT, [&](int k, int c) { return smem + k * 256 + ((c ^ (k & 7)) << 4); });
+    __syncthreads();
+    const uint32_t sk = smem_addr(smem) + warp * WK * 256;
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      const int row = gr * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        ldsm_x4(sk + row * 256 + (((2 * s + (lane >> 4)) ^ (row & 7)) << 4), f[gr][s][0], f[gr][s][1], f[gr][s][2], f[gr][s][3]);
+    }
+    __syncthreads();                         // the table ring takes K's place
   }
   int kp[2][2], kp_lane = 0x7fffffff;
   if (POS && row0 >= 0 && key0 + lane < u.s.lk) {
@@ -368,113 +372,182 @@ __global__ void __launch_bounds__(WT) relattn_key_weights_tiles_kernel(const __g
   for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const int k = gr * 16 + hf * 8 + operand_key<FP4>(g);
+      const int k = gr * 16 + hf * 8 + g;
       kp[gr][hf] = POS ? __shfl_sync(full, kp_lane, k) : key0 + k;
     }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float kg = FP4 && p.kv.k_global ? __ldg(p.kv.k_global + u.h) : 1.f;
-  const uint32_t sqa = smem_addr(sq);
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  for (long r0 = (long)tok0 * p.a.group; r0 < (long)tok1 * p.a.group; r0 += QR) {
-    __syncthreads();                         // the rows before these are read
-    {
-      // four threads a row, 32 dims each
-      const int n = tid >> 2, part = tid & 3;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the table, or R
+
+  const uint32_t ring = smem_addr(smem), sq = ring + ST_Q, sr = ring + ST_R;
+  float *sc = reinterpret_cast<float *>(smem + ST_C);  // [stage][coef, bias scale, lse, position, row][QR]
+  const float kg = p.k == nullptr && p.kv.k_global ? __ldg(p.kv.k_global + u.h) : 1.f;
+  const int ks = p.a.E > 0 && !POS ? (p.a.rd + 15) / 16 : 0;   // 16-channel steps of the bias product
+  const bool r_vec = (p.a.rd & 7) == 0 && (reinterpret_cast<uintptr_t>(p.a.r) & 15u) == 0;
+  const long rbeg = (long)tok0 * p.a.group, rend = (long)tok1 * p.a.group;
+  const int m0 = rel_table_origin(p.a.E);
+  int table_lo = 0x7fffffff;                 // table rows from here on have been copied
+  auto stage = [&](long r0, int buf) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = (tid >> 4) + 8 * i, c = tid & 15;
       const long rr = r0 + n;
-      const bool live = rr < (long)tok1 * p.a.group;
-      const int tok = (int)(rr / p.a.group), hh = (int)(rr - (long)tok * p.a.group);
-      const int head = u.h * p.a.group + hh;
-      const long grow = (long)(u.s.q0 + tok) * p.a.Hq + head;
-      uint32_t w[16];
-      float back = 1.f;
+      const bool live = rr < rend;
+      const int tok = (int)((live ? rr : rbeg) / p.a.group), hh = (int)((live ? rr : rbeg) - (long)tok * p.a.group);
+      const __nv_bfloat16 *src = p.a.q + ((long)(u.s.q0 + tok) * p.a.Hq + u.h * p.a.group + hh) * kHeadDim + c * 8;
+      cp_async16(sq + buf * QR * 256 + n * 256 + ((c ^ (n & 7)) << 4), src, live);
+    }
+    const int last = (int)((min(r0 + QR, rend) - 1) / p.a.group), first = (int)(r0 / p.a.group);
+    if (ks > 0 && u.qbase + first - (tile0 + kWalkTile - 1) < p.a.E) {
+      // r rows (zero past r_dim), and the table rows that these tokens add
+      for (int i = tid; i < QR * 2 * ks; i += WT) {
+        const int n = i / (2 * ks), c = i - n * 2 * ks;
+        const long rr = r0 + n;
+        const bool live = rr < rend;
+        const int tok = (int)((live ? rr : rbeg) / p.a.group), hh = (int)((live ? rr : rbeg) - (long)tok * p.a.group);
+        const __nv_bfloat16 *src = p.a.r + ((long)(u.s.q0 + tok) * p.a.Hq + u.h * p.a.group + hh) * p.a.rd;
+        const uint32_t dst = sr + buf * QR * 128 + n * 128 + ((c ^ (n & 7)) << 4);
+        if (r_vec) {
+          cp_async16(dst, src + (c * 8 < p.a.rd ? c * 8 : 0), live && c * 8 < p.a.rd);
+        } else {
+          uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = 0;
-      if (live) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + grow * kHeadDim + part * 32);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 y = __ldg(src + i);
-          w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
+          for (int j = 0; j < 4; ++j) {
+            const int e = c * 8 + 2 * j;
+            const uint32_t lo = live && e < p.a.rd ? __bfloat16_as_ushort(src[e]) : 0;
+            const uint32_t hi = live && e + 1 < p.a.rd ? __bfloat16_as_ushort(src[e + 1]) : 0;
+            w[j] = lo | (hi << 16);
+          }
+          st_shared_v4(dst, w[0], w[1], w[2], w[3]);
         }
       }
-      if (FP4) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
-        top = max(top, __shfl_xor_sync(full, top, 1));
-        top = max(top, __shfl_xor_sync(full, top, 2));
-        const float up = f16_row_scale(top, &back);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+      const int lo = m0 - (u.qbase + last) + tile0;
+      const int hi = min(table_lo, m0 - (u.qbase + first) + tile0 + kWalkTile);
+      for (int i = tid; i < (hi - lo) * 8; i += WT) {
+        const int m = lo + (i >> 3), c = i & 7, slot = m & (TR - 1);
+        const bool in = m >= 0 && m < rel_table_rows(p.a.E);
+        cp_async16(ring + slot * 128 + ((c ^ (slot & 7)) << 4), p.table + (in ? (long)m * 64 + c * 8 : 0), in);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // 16-byte chunks exchanged so that each operand read meets every bank once
-        const int c = part * 4 + i, at = FP4 ? c ^ ((part >> 1) | ((n & 1) << 1)) : c ^ (n & 7);
-        st_shared_v4(sqa + n * 256 + at * 16, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      }
-      if (part == 0) {
-        const float s = live ? log_scale(u.qbase + tok, p.a.inv_ln_base) : 0.f;
-        s_qp[n] = live ? u.qbase + tok : -1;
-        s_coef[n] = p.a.alpha_log2e * s * kg * back;
-        s_bscale[n] = s * kLog2e;
-        const float z = live ? __ldg(p.lse + (long)head * p.a.total_q + u.s.q0 + tok) : -INFINITY;
-        s_lse[n] = z == -INFINITY ? INFINITY : z * kLog2e;
-        s_row[n] = live ? grow : 0;
-      }
+      table_lo = lo;
     }
-    __syncthreads();
-    const int qmin = s_qp[0], qlast = u.qbase + (int)(min(r0 + QR, (long)tok1 * p.a.group) - 1) / p.a.group;
-    const bool edge = POS || key0 + WK - 1 > qmin || (unsigned)(qlast - key0) >= wlim || r0 + QR > (long)tok1 * p.a.group;
+    if (tid < QR) {
+      const long rr = r0 + tid;
+      const bool live = rr < rend;
+      const int tok = (int)((live ? rr : rbeg) / p.a.group), hh = (int)((live ? rr : rbeg) - (long)tok * p.a.group);
+      const int head = u.h * p.a.group + hh;
+      float *o = sc + buf * 5 * QR + tid;
+      const float s = live ? log_scale(u.qbase + tok, p.a.inv_ln_base) : 0.f;
+      const float z = live ? __ldg(p.lse + (long)head * p.a.total_q + u.s.q0 + tok) : -INFINITY;
+      o[0] = p.a.alpha_log2e * s * kg;
+      o[QR] = s * kLog2e;
+      o[2 * QR] = z == -INFINITY ? INFINITY : z * kLog2e;
+      o[3 * QR] = __int_as_float(live ? u.qbase + tok : -1);
+      o[4 * QR] = __int_as_float(tok * p.a.group + hh);
+    }
+    cp_async_commit();
+  };
+
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  int buf = 0;
+  if (rbeg < rend) stage(rbeg, 0);
+  for (long r0 = rbeg; r0 < rend; r0 += QR, buf ^= 1) {
+    cp_async_wait<0>();
+    __syncthreads();                         // this stage has landed, the other one is read
+    if (r0 + QR < rend) stage(r0 + QR, buf ^ 1);
+    const float *c_coef = sc + buf * 5 * QR;
+    const int qmin = __float_as_int(c_coef[3 * QR]);
+    const int qlast = u.qbase + (int)((min(r0 + QR, rend) - 1) / p.a.group);
+    const bool edge = POS || key0 + WK - 1 > qmin || (unsigned)(qlast - key0) >= wlim || r0 + QR > rend;
     const bool band = p.a.E > 0 && (POS ? __any_sync(full, kp_lane != 0x7fffffff && qmin - kp_lane < p.a.E)
                                         : qmin - (key0 + WK - 1) < p.a.E);
 #pragma unroll 1
     for (int nt = 0; nt < QR / 8; ++nt) {
       uint32_t b[16];
-      if (FP4) {
-        const uint32_t rb = sqa + (nt * 8 + g) * 256;
+      const int brow = nt * 8 + (lane & 7);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 y = lds128(rb + (((4 * t + i) ^ ((t >> 1) | ((g & 1) << 1))) << 4));
-          b[4 * i] = y.x, b[4 * i + 1] = y.y, b[4 * i + 2] = y.z, b[4 * i + 3] = y.w;
-        }
-      } else {
-        const int row = nt * 8 + (lane & 7);
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          ldsm_x4(sqa + row * 256 + (((4 * s + (lane >> 3)) ^ (row & 7)) << 4), b[4 * s], b[4 * s + 1], b[4 * s + 2],
-                  b[4 * s + 3]);
-      }
-      float x[2][4];
+      for (int s = 0; s < 4; ++s)
+        ldsm_x4(sq + buf * QR * 256 + brow * 256 + (((4 * s + (lane >> 3)) ^ (brow & 7)) << 4), b[4 * s], b[4 * s + 1],
+                b[4 * s + 2], b[4 * s + 3]);
+      float x[2][4], y[2][4];
 #pragma unroll
       for (int gr = 0; gr < 2; ++gr) {
         x[gr][0] = x[gr][1] = x[gr][2] = x[gr][3] = 0.f;
+        y[gr][0] = y[gr][1] = y[gr][2] = y[gr][3] = 0.f;
 #pragma unroll
-        for (int s = 0; s < 8; ++s) key_mma<FP4>(x[gr], f[gr][s], b[2 * s], b[2 * s + 1]);
+        for (int s = 0; s < 8; ++s)
+          mma_bf16_16816(x[gr], f[gr][s][0], f[gr][s][1], f[gr][s][2], f[gr][s][3], b[2 * s], b[2 * s + 1]);
+      }
+      if (band && !POS) {
+        // y = P^T r^T, one token's rows at a time: key j is table row m0 - i + j
+        uint32_t rbf[8];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          ldsm_x4(sr + buf * QR * 128 + brow * 128 + (((4 * s + (lane >> 3)) ^ (brow & 7)) << 4), rbf[4 * s],
+                  rbf[4 * s + 1], rbf[4 * s + 2], rbf[4 * s + 3]);
+        const int my_pos = __float_as_int(c_coef[3 * QR + nt * 8 + g]);       // of the row this lane holds
+        const int lo_pos = __float_as_int(c_coef[3 * QR + nt * 8]);
+        const int hi_pos = min(qlast, __shfl_sync(full, my_pos, 28) < 0 ? qlast : __shfl_sync(full, my_pos, 28));
+        for (int pos = lo_pos; pos >= 0 && pos <= hi_pos; ++pos) {
+          const bool mine = my_pos == pos;
+#pragma unroll
+          for (int gr = 0; gr < 2; ++gr) {
+            const int m = m0 - pos + key0 + gr * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
+            const uint32_t slot = (uint32_t)m & (TR - 1);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              if (s < ks) {
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4(ring + slot * 128 + (((2 * s + (lane >> 4)) ^ (slot & 7)) << 4), a0, a1, a2, a3);
+                mma_bf16_16816(y[gr], a0, a1, a2, a3, mine ? rbf[2 * s] : 0u, mine ? rbf[2 * s + 1] : 0u);
+              }
+          }
+        }
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int m = nt * 8 + 2 * t + c;
-        const float coef = s_coef[m], lse2 = s_lse[m];
+        const float coef = c_coef[m], bs = c_coef[QR + m], lse2 = c_coef[2 * QR + m];
+        const int qp = __float_as_int(c_coef[3 * QR + m]);
 #pragma unroll
         for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            float y = x[gr][2 * hf + c] * coef;
-            if (band || edge) {
-              const unsigned d = (unsigned)s_qp[m] - (unsigned)kp[gr][hf];
-              if (band && d < (unsigned)p.a.E) y = fmaf(p.a.rdec[s_row[m] * p.a.E + d], s_bscale[m], y);
-              if (d >= wlim) y = -INFINITY;
+            float l = fmaf(x[gr][2 * hf + c], coef, -lse2);
+            const unsigned d = (unsigned)qp - (unsigned)kp[gr][hf];
+            if (POS) {
+              if (band && d < (unsigned)p.a.E) {
+                const int rr = __float_as_int(c_coef[4 * QR + m]), tok = rr / p.a.group;
+                const long grow = (long)(u.s.q0 + tok) * p.a.Hq + u.h * p.a.group + (rr - tok * p.a.group);
+                l = fmaf(p.a.rdec[grow * p.a.E + d], bs, l);
+              }
+            } else if (band) {
+              l = fmaf(y[gr][2 * hf + c], bs, l);
             }
-            v[2 * gr + hf] += fast_exp2(y - lse2);
+            if (edge && d >= wlim) l = -INFINITY;
+            v[2 * gr + hf] += fast_exp2(l);
           }
       }
     }
   }
   const float sum = quad_reduce(v, t);
-  const int key = key0 + (t >> 1) * 16 + (t & 1) * 8 + operand_key<FP4>(g);
+  const int key = key0 + (t >> 1) * 16 + (t & 1) * 8 + g;
   if (row0 >= 0 && key < u.s.lk) write_weight(p, u, key, row0 + (key - key0), sum);
+}
+
+// The bias table: row m holds P[:, d] for d = origin - m, zero outside [0, E)
+// and past r_dim.
+__global__ void __launch_bounds__(256) relattn_rel_table_kernel(const __nv_bfloat16 *__restrict__ P, int rd, int E,
+                                                                __nv_bfloat16 *__restrict__ table) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ __nv_bfloat16 tile[64][33];
+  const int m0 = blockIdx.x * 32, rows = rel_table_rows(E), org = rel_table_origin(E);
+  for (int i = threadIdx.x; i < 64 * 32; i += 256) {
+    const int c = i >> 5, m = m0 + (i & 31), d = org - m;
+    tile[c][i & 31] = c < rd && d >= 0 && d < E ? P[(size_t)c * E + d] : __float2bfloat16_rn(0.f);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * 32; i += 256) {
+    const int m = m0 + (i >> 6), c = i & 63;
+    if (m < rows) table[(long)m * 64 + c] = tile[c][i >> 6];
+  }
 }
 
 // ------------------------------------------------------------------ keys out of sight
@@ -511,22 +584,48 @@ cudaError_t launch_rows(const KeyWeightArgs &p, cudaLaunchConfig_t cfg) {
 }
 
 template <bool POS, bool FP4>
-cudaError_t launch_kind(const KeyWeightArgs &p, cudaLaunchConfig_t cfg) {
-  const int rows = p.a.max_q * p.a.group;
-  if (rows <= kFp4Rows && p.a.batch <= kWalkBatch)
-    return rows <= 8 ? launch_rows<1, POS, FP4>(p, cfg) : launch_rows<2, POS, FP4>(p, cfg);
+cudaError_t launch_few(const KeyWeightArgs &p, cudaLaunchConfig_t cfg) {
+  return p.a.max_q * p.a.group <= 8 ? launch_rows<1, POS, FP4>(p, cfg) : launch_rows<2, POS, FP4>(p, cfg);
+}
+
+template <bool POS>
+cudaError_t launch_tiles(const KeyWeightArgs &p, cudaLaunchConfig_t cfg) {
+  static std::atomic<bool> done[kMaxDevicesAttr];
+  auto *kernel = relattn_key_weights_tiles_kernel<POS>;
+  const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), ST_BYTES, done);
+  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)((p.a.max_k + kWalkTile - 1) / kWalkTile), (unsigned)(p.a.batch * p.a.Hkv));
   cfg.blockDim = dim3(WT);
-  return cudaLaunchKernelEx(&cfg, relattn_key_weights_tiles_kernel<POS, FP4>, p);
+  cfg.dynamicSmemBytes = ST_BYTES;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
 
-cudaError_t launch_key_weights(const KeyWeightArgs &p, cudaStream_t stream) {
-  if ((long)p.a.batch * p.a.Hkv > 65535) return cudaErrorInvalidValue;
+// A call is walked (few rows) or takes tiles of keys; with positions, and when
+// walked, the bias comes from R in the workspace, else from the bias table.
+bool key_weights_walked(const KernelArgs &a) { return (long)a.max_q * a.group <= kFp4Rows && a.batch <= kWalkBatch; }
+
+size_t key_weights_workspace(const KernelArgs &a, bool positions) {
+  if (a.E <= 0) return 0;
+  if (positions || key_weights_walked(a)) return (size_t)a.total_q * a.Hq * a.E * sizeof(float);
+  return (size_t)rel_table_rows(a.E) * 64 * sizeof(__nv_bfloat16);
+}
+
+cudaError_t launch_key_weights(const KeyWeightArgs &args, cudaStream_t stream) {
+  KeyWeightArgs p = args;
+  const bool pos = p.key_pos != nullptr, fp4 = p.k == nullptr, walked = key_weights_walked(p.a);
+  p.table = nullptr;
   if (p.a.E > 0) {
-    const cudaError_t e = launch_rel_bias(p.a.r, p.a.P, (long)p.a.total_q * p.a.Hq, p.a.rd, p.a.E,
-                                          const_cast<float *>(p.a.rdec), stream);
+    cudaError_t e;
+    if (pos || walked) {
+      e = launch_rel_bias(p.a.r, p.a.P, (long)p.a.total_q * p.a.Hq, p.a.rd, p.a.E, const_cast<float *>(p.a.rdec), stream);
+    } else {
+      p.table = reinterpret_cast<const __nv_bfloat16 *>(p.a.rdec);
+      relattn_rel_table_kernel<<<(rel_table_rows(p.a.E) + 31) / 32, 256, 0, stream>>>(
+          p.a.P, p.a.rd, p.a.E, const_cast<__nv_bfloat16 *>(p.table));
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -535,19 +634,22 @@ cudaError_t launch_key_weights(const KeyWeightArgs &p, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = p.a.E > 0 ? 1 : 0;          // behind the R kernel
-  const bool pos = p.key_pos != nullptr, fp4 = p.k == nullptr;
-  cudaError_t e = pos ? (fp4 ? launch_kind<true, true>(p, cfg) : launch_kind<true, false>(p, cfg))
-                      : (fp4 ? launch_kind<false, true>(p, cfg) : launch_kind<false, false>(p, cfg));
-  if (e != cudaSuccess) return e;
-  // the walk of few rows leaves the keys out of sight alone
-  const bool walked = p.a.max_q * p.a.group <= kFp4Rows && p.a.batch <= kWalkBatch;
+  cfg.numAttrs = p.a.E > 0 ? 1 : 0;          // behind the R or table kernel
   if (walked) {
+    const cudaError_t e = pos ? (fp4 ? launch_few<true, true>(p, cfg) : launch_few<true, false>(p, cfg))
+                              : (fp4 ? launch_few<false, true>(p, cfg) : launch_few<false, false>(p, cfg));
+    if (e != cudaSuccess) return e;
+    // the walk leaves the keys out of sight alone
     relattn_key_weights_cold_kernel<<<dim3((unsigned)((p.a.max_k + kColdKeys - 1) / kColdKeys),
                                            (unsigned)(p.a.batch * p.a.Hkv)), 256, 0, stream>>>(p);
-    e = cudaGetLastError();
+    return cudaGetLastError();
   }
-  return e;
+  p.tc = !pos && key_weights_tc_supported(p);
+  cudaError_t e = cudaSuccess;
+  // the tcgen05 kernel takes every row without a bias, and the rows past the band with one
+  if (!p.tc || p.a.E > 0) e = pos ? launch_tiles<true>(p, cfg) : launch_tiles<false>(p, cfg);
+  if (e != cudaSuccess || !p.tc) return e;
+  return launch_key_weights_tc(p, stream);
 }
 
 }  // namespace relattn

@@ -230,8 +230,17 @@ struct KeyWeightArgs : WalkArgs {
   const float *w_in;   // [Hkv, pages.rows], null: zero
   float *w_out;
   float decay;
+  const __nv_bfloat16 *table;   // bias table in the workspace (set by the launcher)
+  int tc;                       // 1: rows past the bias band go to key_weights_tc.cu
 };
+bool key_weights_walked(const KernelArgs &a);
+size_t key_weights_workspace(const KernelArgs &a, bool positions);
 cudaError_t launch_key_weights(const KeyWeightArgs &a, cudaStream_t stream);
+// Many rows on tcgen05 (key_weights_tc.cu): the rows whose every distance to a
+// tile's 128 keys is at least E, added to the sums of the kernel before it;
+// without a bias every row.
+bool key_weights_tc_supported(const KeyWeightArgs &a);
+cudaError_t launch_key_weights_tc(const KeyWeightArgs &a, cudaStream_t stream);
 
 // Eviction (evict.cu)
 constexpr int kMaxPlanes = 8;

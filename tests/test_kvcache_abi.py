@@ -186,6 +186,12 @@ def test_python_checks_name_the_argument():
         rpb.store_nvfp4(k, k, cu, cu[:1], c)
     with pytest.raises(ValueError, match="contiguous"):
         rpb.store_nvfp4(torch.zeros(4, 2, 256, dtype=torch.bfloat16)[..., ::2], k, cu, cu, c)
+    with pytest.raises(ValueError, match="cache.v must be torch.uint8"):
+        rpb.KvNvfp4(c.k, c.v.float(), c.k_scale, c.v_scale)
+    with pytest.raises(ValueError, match="cache.k_scale must have shape"):
+        rpb.KvNvfp4(c.k, c.v, c.k_scale[:, :1], c.v_scale)
+    with pytest.raises(ValueError, match="cache.v_global must have shape"):
+        rpb.KvNvfp4(*c[:4], None, torch.ones(3))
     with pytest.raises(ValueError, match="KvNvfp4"):
         rpb.store_nvfp4(k, k, cu, cu, tuple(c))
     with pytest.raises(ValueError, match="page_size"):

@@ -349,6 +349,13 @@ WEIGHTS = [
     U.Case((20, 3), (150, 90), 8, 2, page=64, window=33),
     U.Case((1, 1), (600, 65), 16, 2, positions=True),
     U.Case((30, 3), (150, 90), 8, 2, positions=True, page=32, window=60),
+    # rows past the bias band, several steps of 256 rows, ragged ends
+    U.Case((700, 33, 1), (700, 33, 1), 6, 2, E=64, window=300, base=64.0),
+    U.Case((500, 90), (777, 90), 4, 2, E=0, r_dim=0),
+    U.Case((300,), (900,), 8, 1, E=0, r_dim=0, window=200, page=32),
+    U.Case((520, 17), (520, 300), 2, 2, E=64, r_dim=16, page=64, base=64.0),   # 32 tokens in 32 rows
+    U.Case((400,), (400,), 16, 1, E=100, r_dim=5),                             # unaligned r and P
+    U.Case((31,), (2000,), 8, 1, E=64),                                        # too few rows for a 32-token box
 ]
 
 
