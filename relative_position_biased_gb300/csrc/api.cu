@@ -791,6 +791,7 @@ relattn_status relattn_decode_nvfp4(const relattn_params *p, const relattn_kv_nv
   if ((st = make_args(p, &x.a)) != RELATTN_OK) return st;
   Fp4DecodePlan plan;
   if (!plan_decode_fp4(x.a, p->total_k, positions != nullptr, p->num_splits, &plan)) return RELATTN_ERR_UNSUPPORTED;
+  x.hp = plan.hp;
   x.row_blocks = plan.row_blocks;
   x.splits = plan.splits;
   x.c_min = plan.c_min;

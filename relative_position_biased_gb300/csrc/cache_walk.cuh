@@ -24,7 +24,8 @@ __device__ __forceinline__ int unit_tiles(const WalkArgs &p, int b, SeqRows *sp,
   if (!s.ok || s.lq > p.a.max_q || s.lk > p.a.max_k || first_query_pos(s, p.q_pos, b) < 0) return -1;
   if (s.lq == 0) return 0;
   if (p.a.window > 0 && !p.key_pos) *lo = max(0, s.lk - s.lq - p.a.window + 1) & ~31;
-  return (s.lk - *lo + kWalkTile - 1) / kWalkTile;
+  const int tile = kWalkTile / p.hp;
+  return (s.lk - *lo + tile - 1) / tile;
 }
 
 // Row n of the unit's block: its index among all (token, head) rows, and token.

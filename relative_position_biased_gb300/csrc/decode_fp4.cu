@@ -37,11 +37,13 @@
 // copies: no barrier among warps until the end of a piece.  The running
 // maximum is raised only when a logit passes it by more than 8 (base 2).
 //
-// Work split: the units (sequence, kv head, 16-row block) hold ceil(keys/128)
-// tiles each; they are laid end to end, head and row block outermost so that
-// the heads of one key range are read at the same time, and CTA c takes tiles
-// [c C, (c+1) C).  A piece of a unit writes its partial to slot c - (first
-// CTA of the unit); the unit's first piece marks the slots no piece fills.
+// Work split: the units (sequence, kv heads of a CTA, 16-row block) hold
+// ceil(keys / tile) tiles each; they are laid end to end, and CTA c takes
+// tiles [c C, (c+1) C).  A piece of a unit writes its partial to slot c -
+// (first CTA of the unit); the unit's first piece marks the slots no piece
+// fills.  With an even number of kv heads a CTA takes two of them, two warps
+// each, over the same 64 keys: their rows share 128-byte lines, and lines
+// fetched for one head only were read twice (538 MB for 311 MB of cache).
 #include <algorithm>
 
 #include "cache_walk.cuh"
@@ -70,30 +72,36 @@ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }
 // of keys (a half warp reads keys t = 0..3 from distinct banks).
 __device__ __forceinline__ void issue_group(const Fp4DecodeArgs &p, const Unit &u, uint32_t st, int key0, long row0,
                                             int lane) {
-  const long rb = (long)p.a.Hkv * kFp4RowBytes;
+  const int n = row0 >= 0 ? u.s.lk - key0 : 0;          // keys to copy; the rest is zeroed
+  const int k0 = lane >> 2, c = lane & 3;
+  const long rb = (long)p.a.Hkv * kFp4RowBytes, step = 8 * rb;
+  long off = (max(row0, 0L) + k0) * rb + u.h * kFp4RowBytes + c * 16;
+  // rows 8 apart keep their place within 16 keys: 8 more, whole groups
+  const uint32_t kdst = st + (2 * (k0 & 3) + (k0 >> 2)) * kFp4RowBytes + c * 16;
+  const uint32_t vdst = st + FS_V + k0 * kFp4RowBytes + ((c ^ (((k0 >> 1) & 1) << 1)) << 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int k = (lane >> 2) + 8 * i, c = lane & 3;
-    const bool ok = row0 >= 0 && key0 + k < u.s.lk;
-    const long off = ok ? (row0 + k) * rb + u.h * kFp4RowBytes + c * 16 : 0;
-    const int k16 = k & 15, slot = (k & 16) + (k16 & 8) + 2 * (k16 & 3) + ((k16 >> 2) & 1);
-    cp_async16(st + slot * kFp4RowBytes + c * 16, p.kv.k + off, ok);
-    cp_async16(st + FS_V + k * kFp4RowBytes + ((c ^ (((k >> 1) & 1) << 1)) << 4), p.kv.v + off, ok);
+    const bool ok = k0 + 8 * i < n;
+    const long o = ok ? off : 0;
+    cp_async16(kdst + 8 * i * kFp4RowBytes, p.kv.k + o, ok);
+    cp_async16(vdst + 8 * i * kFp4RowBytes, p.kv.v + o, ok);
+    off += step;
   }
-  const bool ok = row0 >= 0 && key0 + lane < u.s.lk;
+  const bool ok = lane < n;
   const long soff = ok ? ((row0 + lane) * p.a.Hkv + u.h) * kFp4Blocks : 0;
   cp_async8(st + FS_KS + lane * kFp4Blocks, p.kv.k_scale + soff, ok);
   cp_async8(st + FS_VS + lane * kFp4Blocks, p.kv.v_scale + soff, ok);
 }
 
-// One piece: tiles [t0, t0 + n) of unit u, partial into `slot` (or the result
-// itself when there is one slot).
+// One piece: tiles [t0, t0 + n) of unit u, whose u.h is the warp's head;
+// partial into `slot` (or the result itself when there is one slot).
 template <int NT, bool POS>
 __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u, int t0, int n, int slot,
-                                          bool first_piece, uint8_t *smem) {
+                                          uint8_t *smem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * (F_STAGES * FS_BYTES);
-  const int k_first = u.lo + t0 * kWalkTile + warp * FK;
+  const int tile = kWalkTile / p.hp;        // keys of a tile
+  const int k_first = u.lo + t0 * tile + warp / p.hp * FK;
   const unsigned full = 0xffffffffu;
 
   // ---- the first copies, then the query rows while they fly
@@ -112,7 +120,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
   for (int i = 0; i < F_STAGES - 1; ++i) {
     pos_q[i] = 0x7fffffff;
     if (i < n) {
-      const int key0 = k_first + i * kWalkTile;
+      const int key0 = k_first + i * tile;
       const long row = group_row(p, u, key0);
       if (POS) pos_q[i] = fetch_pos(key0, row);
       issue_group(p, u, ring + i * FS_BYTES, key0, row, lane);
@@ -120,14 +128,14 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
     cp_async_commit();
   }
   if (F_STAGES - 1 < n) {
-    next_row = group_row(p, u, k_first + (F_STAGES - 1) * kWalkTile);
-    if (POS) pos_next = fetch_pos(k_first + (F_STAGES - 1) * kWalkTile, next_row);
+    next_row = group_row(p, u, k_first + (F_STAGES - 1) * tile);
+    if (POS) pos_next = fetch_pos(k_first + (F_STAGES - 1) * tile, next_row);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // R, where it was launched before this kernel
 
   uint32_t qf[NT][16];                      // row 8 nt + g, dims 32 t .. 32 t + 31
   float coef[NT][2], bscale[NT][2];         // of rows 8 nt + 2 t, + 1
-  int qp[NT][2];
+  int qp[NT][2], gr_[NT][2];                // position, row of R
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int nrow = nt * 8 + g;
@@ -166,8 +174,8 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
       const int m = nt * 8 + 2 * t + c;
       const float bk = __shfl_sync(full, back, (2 * t + c) * 4);
       int tk;
-      unit_row(p, u, m, &tk);
       const bool live = m < u.nrows;
+      gr_[nt][c] = (int)unit_row(p, u, live ? m : 0, &tk);
       const float s = live ? log_scale(u.qbase + tk, p.a.inv_ln_base) : 0.f;
       qp[nt][c] = live ? u.qbase + tk : -1;   // rows past the block see no key
       coef[nt][c] = p.a.alpha_log2e * s * kg * bk;
@@ -196,12 +204,12 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
 
   int buf = 0;
   for (int it = 0; it < n; ++it) {
-    const int key0 = k_first + it * kWalkTile;
+    const int key0 = k_first + it * tile;
     cp_async_wait<F_STAGES - 2>();
     __syncwarp();                            // the stage has landed; the one before it is read
     {
       const int nb = buf == 0 ? F_STAGES - 1 : buf - 1;
-      if (it + F_STAGES - 1 < n) issue_group(p, u, ring + nb * FS_BYTES, key0 + (F_STAGES - 1) * kWalkTile, next_row, lane);
+      if (it + F_STAGES - 1 < n) issue_group(p, u, ring + nb * FS_BYTES, key0 + (F_STAGES - 1) * tile, next_row, lane);
       cp_async_commit();
     }
     const int pos_lane = POS ? pos_q[0] : 0;
@@ -211,134 +219,120 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
       pos_q[F_STAGES - 2] = pos_next;
     }
     if (it + F_STAGES < n) {
-      next_row = group_row(p, u, key0 + F_STAGES * kWalkTile);
-      if (POS) pos_next = fetch_pos(key0 + F_STAGES * kWalkTile, next_row);
+      next_row = group_row(p, u, key0 + F_STAGES * tile);
+      if (POS) pos_next = fetch_pos(key0 + F_STAGES * tile, next_row);
     }
     const uint32_t st = ring + buf * FS_BYTES;
     buf = buf == F_STAGES - 1 ? 0 : buf + 1;
     if (key0 >= u.s.lk) continue;            // past the sequence: nothing for this warp
 
-    // ---- S^T = K q^T
-    float x[2][NT][4];
-#pragma unroll
+    const bool edge = POS || key0 + FK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
+    const bool band = p.a.E > 0 && (POS ? __any_sync(full, pos_lane != 0x7fffffff && qmin - pos_lane < p.a.E)
+                                        : qmin - (key0 + FK - 1) < p.a.E);
+#pragma unroll 1
     for (int gr = 0; gr < 2; ++gr) {
+      // ---- S^T = K q^T, two chains of four products
+      float x[NT][4], x2[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[gr][nt][0] = x[gr][nt][1] = x[gr][nt][2] = x[gr][nt][3] = 0.f;
-      const uint32_t kb = st + gr * 16 * kFp4RowBytes + t * 16;
-      const uint4 w0 = lds128(kb + g * kFp4RowBytes), w1 = lds128(kb + (g + 8) * kFp4RowBytes);
-      const int kg16 = (g >> 1) + 4 * (g & 1);
-      const uint32_t sb = st + FS_KS + (gr * 16 + kg16) * kFp4Blocks + 2 * t;
-      const uint32_t s0 = e4m3x2_to_f16(lds_u16(sb)), s1 = e4m3x2_to_f16(lds_u16(sb + 8 * kFp4Blocks));
-      const uint32_t ww0[4] = {w0.x, w0.y, w0.z, w0.w}, ww1[4] = {w1.x, w1.y, w1.z, w1.w};
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t m0 = __byte_perm(s0, 0, w < 2 ? 0x1010 : 0x3232);
-        const uint32_t m1 = __byte_perm(s1, 0, w < 2 ? 0x1010 : 0x3232);
-        uint32_t f0[4], f1[4];
-        e2m1x8_to_f16(ww0[w], f0);
-        e2m1x8_to_f16(ww1[w], f1);
+        for (int i = 0; i < 4; ++i) x[nt][i] = x2[nt][i] = 0.f;
+      {
+        const uint32_t kb = st + gr * 16 * kFp4RowBytes + t * 16;
+        const uint4 w0 = lds128(kb + g * kFp4RowBytes), w1 = lds128(kb + (g + 8) * kFp4RowBytes);
+        const int kg16 = (g >> 1) + 4 * (g & 1);
+        const uint32_t sb = st + FS_KS + (gr * 16 + kg16) * kFp4Blocks + 2 * t;
+        const uint32_t s0 = e4m3x2_to_f16(lds_u16(sb)), s1 = e4m3x2_to_f16(lds_u16(sb + 8 * kFp4Blocks));
+        const uint32_t ww0[4] = {w0.x, w0.y, w0.z, w0.w}, ww1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f0[i] = hmul2(f0[i], m0), f1[i] = hmul2(f1[i], m1);
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t m0 = __byte_perm(s0, 0, w < 2 ? 0x1010 : 0x3232);
+          const uint32_t m1 = __byte_perm(s1, 0, w < 2 ? 0x1010 : 0x3232);
+          uint32_t f0[4], f1[4];
+          e2m1x8_to_f16(ww0[w], f0);
+          e2m1x8_to_f16(ww1[w], f1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_16816(x[gr][nt], f0[0], f1[0], f0[1], f1[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
-          mma_f16_16816(x[gr][nt], f0[2], f1[2], f0[3], f1[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+          for (int i = 0; i < 4; ++i) f0[i] = hmul2(f0[i], m0), f1[i] = hmul2(f1[i], m1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_16816(x[nt], f0[0], f1[0], f0[1], f1[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
+            mma_f16_16816(x2[nt], f0[2], f1[2], f0[3], f1[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+          }
         }
       }
-    }
 
-    // ---- logits: scale, bias, mask
-    const bool edge = POS || key0 + FK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
-    int kp[2][2];                            // positions of the lane's keys
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr)
+      // ---- logits: scale, bias, mask
+      int kp[2];                             // positions of the lane's keys
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int k = gr * 16 + hf * 8 + (g >> 1) + 4 * (g & 1);
-        kp[gr][hf] = POS ? __shfl_sync(full, pos_lane, k) : key0 + k;
+        kp[hf] = POS ? __shfl_sync(full, pos_lane, k) : key0 + k;
       }
-    const bool band = p.a.E > 0 && (POS ? __any_sync(full, pos_lane != 0x7fffffff && qmin - pos_lane < p.a.E)
-                                        : qmin - (key0 + FK - 1) < p.a.E);
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[gr][nt][i] *= coef[nt][i & 1];
-    if (band) {
+        for (int i = 0; i < 4; ++i) x[nt][i] = (x[nt][i] + x2[nt][i]) * coef[nt][i & 1];
+      if (band) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int m = nt * 8 + 2 * t + c;
-          int tk;
-          const float *R = p.a.rdec + unit_row(p, u, min(m, u.nrows - 1), &tk) * p.a.E;
-#pragma unroll
-          for (int gr = 0; gr < 2; ++gr)
+          for (int c = 0; c < 2; ++c) {
+            const float *R = p.a.rdec + (long)gr_[nt][c] * p.a.E;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const unsigned d = (unsigned)qp[nt][c] - (unsigned)kp[gr][hf];
-              if (d < (unsigned)p.a.E) x[gr][nt][hf * 2 + c] = fmaf(R[d], bscale[nt][c], x[gr][nt][hf * 2 + c]);
+              const unsigned d = (unsigned)qp[nt][c] - (unsigned)kp[hf];
+              if (d < (unsigned)p.a.E) x[nt][hf * 2 + c] = fmaf(R[d], bscale[nt][c], x[nt][hf * 2 + c]);
             }
-        }
-    }
-    if (edge) {
-#pragma unroll
-      for (int gr = 0; gr < 2; ++gr)
+          }
+      }
+      if (edge) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if ((unsigned)qp[nt][i & 1] - (unsigned)kp[gr][i >> 1] >= wlim) x[gr][nt][i] = -INFINITY;
-    }
+            if ((unsigned)qp[nt][i & 1] - (unsigned)kp[i >> 1] >= wlim) x[nt][i] = -INFINITY;
+      }
 
-    // ---- the running maximum, raised only when a logit passes it by more than kRaise
-    bool need = false;
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr)
+      // ---- the running maximum, raised only when a logit passes it by more than kRaise
+      bool need = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) need |= x[gr][nt][i] > mref[nt][i & 1] + kRaise;
-    if (__any_sync(full, need)) {
+        for (int c = 0; c < 2; ++c) need |= fmaxf(x[nt][c], x[nt][c + 2]) > mref[nt][c] + kRaise;
+      if (__any_sync(full, need)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = fmaxf(fmaxf(x[0][nt][c], x[0][nt][c + 2]), fmaxf(x[1][nt][c], x[1][nt][c + 2]));
-          m = fmaxf(m, __shfl_xor_sync(full, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(full, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(full, m, 16));
-          m = fmaxf(m, mref[nt][c]);
-          const float f = m == -INFINITY ? 1.f : fast_exp2(mref[nt][c] - m);
-          mref[nt][c] = m;
-          l[nt][c] *= f;
+          for (int c = 0; c < 2; ++c) {
+            float m = fmaxf(x[nt][c], x[nt][c + 2]);
+            m = fmaxf(m, __shfl_xor_sync(full, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(full, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(full, m, 16));
+            m = fmaxf(m, mref[nt][c]);
+            const float f = m == -INFINITY ? 1.f : fast_exp2(mref[nt][c] - m);
+            mref[nt][c] = m;
+            l[nt][c] *= f;
 #pragma unroll
-          for (int d = 0; d < 8; ++d) acc[d][nt][c] *= f, acc[d][nt][c + 2] *= f;
-        }
-    }
-    uint32_t pb[2][NT][2];
+            for (int d = 0; d < 8; ++d) acc[d][nt][c] *= f, acc[d][nt][c + 2] *= f;
+          }
+      }
+      uint32_t pb[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float mo[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) mo[c] = (mref[nt][c] == -INFINITY ? 0.f : mref[nt][c]) - kPShift;
-#pragma unroll
-      for (int gr = 0; gr < 2; ++gr) {
+      for (int nt = 0; nt < NT; ++nt) {
         float e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = fast_exp2(x[gr][nt][i] - mo[i & 1]);
+        for (int i = 0; i < 4; ++i) {
+          const float m = mref[nt][i & 1];
+          e[i] = fast_exp2(x[nt][i] - (m == -INFINITY ? -kPShift : m - kPShift));
+        }
         l[nt][0] += e[0] + e[2];
         l[nt][1] += e[1] + e[3];
         // key g x rows 2t, 2t+1  ->  row g x keys 2t, 2t+1
-        pb[gr][nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
-        pb[gr][nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
+        pb[nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+        pb[nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
       }
-    }
 
-    // ---- O^T += V^T P^T
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
+      // ---- O^T += V^T P^T
       // the lane's keys, in operand order 2t, 2t+1, 2t+8, 2t+9: t, 4+t, 8+t, 12+t; dims 16 g ..
       const uint32_t vb = st + FS_V + (gr * 16 + t) * kFp4RowBytes + ((((g >> 1) ^ (((t >> 1) & 1) << 1))) << 4) + (g & 1) * 8;
       const uint32_t sb = st + FS_VS + (gr * 16 + t) * kFp4Blocks + g;
@@ -390,7 +384,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
                  [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
                    for (int nt = 0; nt < NT; ++nt)
-                     mma_f16_16816(acc[m][nt], a0, a1, a2, a3, pb[gr][nt][0], pb[gr][nt][1]);
+                     mma_f16_16816(acc[m][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
                  });
       } else {
         // one row at a time, without the keys that it does not see; a NaN
@@ -411,7 +405,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float o[4] = {acc[m][nt][0], acc[m][nt][1], acc[m][nt][2], acc[m][nt][3]};
-              mma_f16_16816(o, a0, a1, a2, a3, pb[gr][nt][0], pb[gr][nt][1]);
+              mma_f16_16816(o, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (nt * 8 + 2 * t + (i & 1) == only) acc[m][nt][i] = o[i];
@@ -446,25 +440,26 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
             make_float2(acc[m][nt][c], acc[m][nt][c + 2]);
     }
   __syncthreads();
-  const float vg = p.kv.v_global ? __ldg(p.kv.v_global + u.h) : 1.f;
   const long rows_all = (long)p.a.total_q * p.a.Hq;
-  for (int row = 0; row < u.nrows; ++row) {
+  for (int i = 0; i < u.nrows * p.hp; ++i) {
+    const int hs = i / u.nrows, row = i - hs * u.nrows;
     float m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < FW; ++w) m = fmaxf(m, sm[w * kFp4Rows + row]);
+    for (int w = hs; w < FW; w += p.hp) m = fmaxf(m, sm[w * kFp4Rows + row]);
     float o = 0.f, z = 0.f;
-#pragma unroll
-    for (int w = 0; w < FW; ++w) {
+    for (int w = hs; w < FW; w += p.hp) {
       const float mw = sm[w * kFp4Rows + row], zw = sl[w * kFp4Rows + row];
       // a warp without a visible key has an empty sum; a NaN sum stays one
       const float f = mw == -INFINITY ? (zw == 0.f ? 0.f : 1.f) : fast_exp2(mw - m);
       z = fmaf(zw, f, z);
       o = fmaf(so[(w * kFp4Rows + row) * kHeadDim + tid], f, o);
     }
+    Unit uh = u;
+    uh.h = u.h - warp % p.hp + hs;
+    const float vg = p.kv.v_global ? __ldg(p.kv.v_global + uh.h) : 1.f;
     const float out = z == 0.f ? 0.f : o / z * vg;
     const float lse = z == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) - kPShift + log2f(z)) * kLn2;
     int tk;
-    const long grow = unit_row(p, u, row, &tk);
+    const long grow = unit_row(p, uh, row, &tk);
     if (p.splits == 1) {
       p.a.out[grow * kHeadDim + tid] = __float2bfloat16_rn(out);
       if (tid == 0) p.a.lse[(grow % p.a.Hq) * p.a.total_q + grow / p.a.Hq] = lse;
@@ -481,50 +476,53 @@ __global__ void __launch_bounds__(FT, ctas_per_sm(NT)) relattn_decode_fp4_kernel
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int prefix[kWalkBatch + 1];
   __shared__ int wsum[FW];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, hsub = (tid >> 5) % p.hp;
   Unit u;
-  if (p.splits == 1) {                       // one CTA per unit
-    const int unit = blockIdx.x;
-    const int hr = unit / p.a.batch;
-    u.b = unit - hr * p.a.batch;
-    u.h = hr / p.row_blocks;
-    u.rb = hr - u.h * p.row_blocks;
-    const int n = unit_tiles(p, u.b, &u.s, &u.lo);
+  // head group and row block of unit group hr; the warp's head
+  auto place = [&](int hr) {
+    u.rb = hr % p.row_blocks;
+    u.h = hr / p.row_blocks * p.hp + hsub;
     u.nrows = min(kFp4Rows, u.s.lq * p.a.group - u.rb * kFp4Rows);
+    u.qbase = first_query_pos(u.s, p.q_pos, u.b);
+  };
+  if (p.splits == 1) {                       // one CTA per unit
+    const int hr = blockIdx.x / p.a.batch;
+    u.b = blockIdx.x - hr * p.a.batch;
+    const int n = unit_tiles(p, u.b, &u.s, &u.lo);
     if (n < 0 && tid == 0) atomicOr(p.a.err, kDevErrSeqlens);
-    if (n > 0 && u.nrows > 0) {
-      u.qbase = first_query_pos(u.s, p.q_pos, u.b);
-      run_piece<NT, POS>(p, u, 0, n, 0, true, smem);
+    if (n > 0) {
+      place(hr);
+      if (u.nrows > 0) run_piece<NT, POS>(p, u, 0, n, 0, smem);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   const int base = tile_prefix<FT>(p, prefix, wsum);
-  const long per = base, total = per * p.a.Hkv * p.row_blocks;
+  const long per = base, total = per * (p.a.Hkv / p.hp) * p.row_blocks;
   const long C = max((total + gridDim.x - 1) / gridDim.x, (long)p.c_min);
   long x = blockIdx.x * C;
   const long end = min(total, x + C);
   while (x < end) {
     const int hr = (int)(x / per), xb = (int)(x - hr * per);
     u.b = last_not_above(prefix, p.a.batch, xb);   // it holds tile xb
-    u.h = hr / p.row_blocks;
-    u.rb = hr - u.h * p.row_blocks;
     const int tiles = unit_tiles(p, u.b, &u.s, &u.lo), t0 = xb - prefix[u.b];
     const int n = (int)min((long)(tiles - t0), end - x);
-    u.nrows = min(kFp4Rows, u.s.lq * p.a.group - u.rb * kFp4Rows);
+    place(hr);
     if (u.nrows > 0) {
-      u.qbase = first_query_pos(u.s, p.q_pos, u.b);
       const long ustart = hr * per + prefix[u.b], first = ustart / C;
       if (t0 == 0) {                         // mark the slots that no piece fills
         const int used = (int)((ustart + tiles - 1) / C - first) + 1;
-        const int empty = (p.splits - used) * u.nrows;
+        const int cells = u.nrows * p.hp, empty = (p.splits - used) * cells;
         for (int i = tid; i < empty; i += FT) {
           int tk;
-          const long grow = unit_row(p, u, i % u.nrows, &tk);
-          p.a.lse_part[(long)(used + i / u.nrows) * p.a.total_q * p.a.Hq + grow] = -INFINITY;
+          Unit uh = u;
+          const int cell = i % cells;
+          uh.h = u.h - hsub + cell / u.nrows;
+          const long grow = unit_row(p, uh, cell % u.nrows, &tk);
+          p.a.lse_part[(long)(used + i / cells) * p.a.total_q * p.a.Hq + grow] = -INFINITY;
         }
       }
-      run_piece<NT, POS>(p, u, t0, n, (int)(blockIdx.x - first), t0 == 0, smem);
+      run_piece<NT, POS>(p, u, t0, n, (int)(blockIdx.x - first), smem);
     }
     x += n;
   }
@@ -596,7 +594,7 @@ cudaError_t launch_main(const Fp4DecodeArgs &p, cudaStream_t stream) {
   auto *kernel = relattn_decode_fp4_kernel<NT, POS>;
   const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), F_RING, done);
   if (e != cudaSuccess) return e;
-  const long grid = p.splits == 1 ? (long)p.a.batch * p.a.Hkv * p.row_blocks : (long)p.a.sms * ctas_per_sm(NT);
+  const long grid = p.splits == 1 ? (long)p.a.batch * (p.a.Hkv / p.hp) * p.row_blocks : (long)p.a.sms * ctas_per_sm(NT);
   if (grid > 0x7fffffffL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -624,10 +622,12 @@ bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want
   plan->row_blocks = (rows + kFp4Rows - 1) / kFp4Rows;
   long vis = a.max_k;
   if (a.window > 0 && !positions) vis = std::min<long>(vis, (long)a.window + a.max_q - 1 + FK - 1);
-  const long U = (vis + kWalkTile - 1) / kWalkTile;
+  plan->hp = a.Hkv % 2 == 0 ? 2 : 1;
+  const long tile = kWalkTile / plan->hp;
+  const long U = (vis + tile - 1) / tile;
   const long keys = std::min<long>(total_k, (long)a.batch * vis);
-  const long heads = (long)a.Hkv * plan->row_blocks;
-  const long total = (keys / kWalkTile + a.batch) * heads;
+  const long heads = (long)(a.Hkv / plan->hp) * plan->row_blocks;
+  const long total = (keys / tile + a.batch) * heads;
   const long grid = (long)a.sms * ctas_per_sm(two_columns(a) ? 2 : 1);
   constexpr long kMinTiles = 4;              // a piece's fixed cost is that of a few tiles
   long C = std::max<long>((total + grid - 1) / grid, kMinTiles);

@@ -133,14 +133,15 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
   constexpr int SB = KStage<FP4>::bytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * (W_STAGES * SB);
-  const int k_first = u.lo + t0 * kWalkTile + warp * WK;
+  const int tile = kWalkTile / p.hp;        // keys of a tile
+  const int k_first = u.lo + t0 * tile + warp / p.hp * WK;
   const unsigned full = 0xffffffffu;
   long rows_q[W_STAGES];                    // cache rows of the groups in flight, then the next to copy
 #pragma unroll
   for (int i = 0; i < W_STAGES; ++i) {
-    rows_q[i] = i < n ? group_row(p, u, k_first + i * kWalkTile) : -1;
+    rows_q[i] = i < n ? group_row(p, u, k_first + i * tile) : -1;
     if (i < W_STAGES - 1) {
-      if (i < n) issue_keys<FP4>(p, u, ring + i * SB, k_first + i * kWalkTile, rows_q[i], lane);
+      if (i < n) issue_keys<FP4>(p, u, ring + i * SB, k_first + i * tile, rows_q[i], lane);
       cp_async_commit();
     }
   }
@@ -214,18 +215,18 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
 
   int buf = 0;
   for (int it = 0; it < n; ++it) {
-    const int key0 = k_first + it * kWalkTile;
+    const int key0 = k_first + it * tile;
     cp_async_wait<W_STAGES - 2>();
     __syncwarp();
     const long row0 = rows_q[0];
     {
       const int nb = buf == 0 ? W_STAGES - 1 : buf - 1;
-      if (it + W_STAGES - 1 < n) issue_keys<FP4>(p, u, ring + nb * SB, key0 + (W_STAGES - 1) * kWalkTile, rows_q[W_STAGES - 1], lane);
+      if (it + W_STAGES - 1 < n) issue_keys<FP4>(p, u, ring + nb * SB, key0 + (W_STAGES - 1) * tile, rows_q[W_STAGES - 1], lane);
       cp_async_commit();
     }
 #pragma unroll
     for (int i = 0; i + 1 < W_STAGES; ++i) rows_q[i] = rows_q[i + 1];
-    rows_q[W_STAGES - 1] = it + W_STAGES < n ? group_row(p, u, key0 + W_STAGES * kWalkTile) : -1;
+    rows_q[W_STAGES - 1] = it + W_STAGES < n ? group_row(p, u, key0 + W_STAGES * tile) : -1;
     const uint32_t st = ring + buf * SB;
     buf = buf == W_STAGES - 1 ? 0 : buf + 1;
     if (key0 >= u.s.lk) continue;
@@ -293,15 +294,15 @@ __global__ void __launch_bounds__(WT) relattn_key_weights_rows_kernel(const __gr
   __shared__ int prefix[kWalkBatch + 1];
   __shared__ int wsum[WW];
   const int base = tile_prefix<WT>(p, prefix, wsum);
-  const long per = base, total = per * p.a.Hkv;
+  const long per = base, total = per * (p.a.Hkv / p.hp);
   const long C = (total + gridDim.x - 1) / gridDim.x;
   long x = blockIdx.x * C;
   const long end = min(total, x + C);
   Unit u;
   u.rb = 0;
   while (x < end) {
-    u.h = (int)(x / per);
-    const int xb = (int)(x - u.h * per);
+    const int hg = (int)(x / per), xb = (int)(x - hg * per);
+    u.h = hg * p.hp + (int)(threadIdx.x >> 5) % p.hp;
     u.b = last_not_above(prefix, p.a.batch, xb);
     const int tiles = unit_tiles(p, u.b, &u.s, &u.lo), t0 = xb - prefix[u.b];
     const int n = (int)min((long)(tiles - t0), end - x);
@@ -616,6 +617,7 @@ cudaError_t launch_key_weights(const KeyWeightArgs &args, cudaStream_t stream) {
   KeyWeightArgs p = args;
   const bool pos = p.key_pos != nullptr, fp4 = p.k == nullptr, walked = key_weights_walked(p.a);
   p.table = nullptr;
+  p.hp = walked && p.a.Hkv % 2 == 0 ? 2 : 1;   // two heads share their rows' lines
   if (p.a.E > 0) {
     cudaError_t e;
     if (pos || walked) {

@@ -201,8 +201,9 @@ struct WalkArgs {
   KernelArgs a;
   CachePages pages;
   const int32_t *key_pos, *q_pos;
+  int hp;                             // kv heads a walking CTA takes (1 or 2)
 };
-constexpr int kWalkTile = 128;        // keys a CTA takes at a time
+constexpr int kWalkTile = 128;        // keys a CTA takes at a time, over its kv heads
 
 // Split-KV decode over the 4-bit cache (decode_fp4.cu).
 struct Fp4DecodeArgs : WalkArgs {
@@ -212,7 +213,7 @@ struct Fp4DecodeArgs : WalkArgs {
   int c_min;           // least tiles a CTA takes (keeps a unit within its slots)
 };
 struct Fp4DecodePlan {
-  int row_blocks, splits, c_min;
+  int hp, row_blocks, splits, c_min;
   size_t lse_offset, rel_offset, ws_bytes;
 };
 constexpr int kFp4Rows = 16;          // query rows of a work unit

@@ -14,8 +14,9 @@ namespace relattn {
 constexpr int kFp4RowBytes = kHeadDim / 2;    // code bytes of a (row, head)
 constexpr int kFp4Blocks = kHeadDim / 16;     // scale bytes of a (row, head)
 
-// Sequences up to this many are laid end to end by the walking kernels.
-constexpr int kWalkBatch = 512;
+// Sequences up to this many are laid end to end by the walking kernels (their
+// table leaves room for four decode CTAs per SM).
+constexpr int kWalkBatch = 384;
 
 // Four code bytes (one word, lowest byte first) as four f16 pairs, the low
 // nibble of each byte in the low half.  Exact.
