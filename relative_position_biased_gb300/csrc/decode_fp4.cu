@@ -59,7 +59,7 @@ constexpr int F_STAGES = 3;
 constexpr int FS_V = FK * kFp4RowBytes, FS_KS = 2 * FS_V, FS_VS = FS_KS + FK * kFp4Blocks;
 constexpr int FS_BYTES = FS_VS + FK * kFp4Blocks;
 constexpr int F_RING = FW * F_STAGES * FS_BYTES;
-static_assert(F_RING >= FW * kFp4Rows * kHeadDim * 4 + 2 * FW * kFp4Rows * 4, "the merge reuses the ring");
+static_assert(F_RING >= FW * kFp4Rows * kHeadDim * 4 + 2 * FW * kFp4Rows * 4 + 2 * kFp4Rows * 8, "the merge reuses the ring");
 constexpr float kPShift = 7.f;               // P is held times 2^7
 constexpr float kRaise = 8.f;                // the maximum is raised past this excess
 
@@ -343,74 +343,60 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
         w[j] = lds64(vb + 4 * j * kFp4RowBytes);
         sc[j] = lds_u8(sb + 4 * j * kFp4Blocks);
       }
-      bool split_rows = false;               // a NaN scale that only some rows may see
-      int vk[4];
       if (edge) {
-        // scales of keys that no row sees become zero: their values (a NaN
-        // scale, an unwritten row) do not reach the sum
+        // Keys that no row sees: scale zero, so that their values (a NaN scale,
+        // an unwritten row) do not reach the sum.  A NaN scale that some rows
+        // see spoils its 16 dims of those rows, which the lane's quad holds; as
+        // an operand it would spoil every row (0 * NaN).
         bool bad = false;
+        int vk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int k = gr * 16 + 4 * j + t;
           vk[j] = POS ? __shfl_sync(full, pos_lane, k) : key0 + k;
-          const bool any = vk[j] <= qmax && (unsigned)max(qmin - vk[j], 0) < wlim;
-          const bool all = vk[j] <= qmin && (unsigned)(qmax - vk[j]) < wlim;
-          if (!any) sc[j] = 0;
-          bad |= any && !all && (sc[j] & 0x7f) == 0x7f;
+          if (vk[j] > qmax || (unsigned)max(qmin - vk[j], 0) >= wlim) sc[j] = 0;
+          bad |= (sc[j] & 0x7f) == 0x7f;
         }
-        split_rows = __any_sync(full, bad);
-      }
-      // the operand's two f16 scale pairs from four scale bytes
-      auto products = [&](uint32_t s0, uint32_t s1, auto &&use) {
-        s0 = e4m3x2_to_f16(s0);
-        s1 = e4m3x2_to_f16(s1);
-#pragma unroll
-        for (int hw = 0; hw < 2; ++hw) {
-          const uint32_t A = hw ? w[0].y : w[0].x, B = hw ? w[1].y : w[1].x;
-          const uint32_t C = hw ? w[2].y : w[2].x, E = hw ? w[3].y : w[3].x;
-          const uint32_t nib = 0x0f0f0f0fu;
-          uint32_t f0[4], f1[4], f2[4], f3[4];
-          e2m1x8_to_f16((A & nib) | ((B << 4) & ~nib), f0);
-          e2m1x8_to_f16(((A >> 4) & nib) | (B & ~nib), f1);
-          e2m1x8_to_f16((C & nib) | ((E << 4) & ~nib), f2);
-          e2m1x8_to_f16(((C >> 4) & nib) | (E & ~nib), f3);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            use(4 * hw + i, hmul2(f0[i], s0), hmul2(f1[i], s0), hmul2(f2[i], s1), hmul2(f3[i], s1));
-        }
-      };
-      if (!split_rows) {
-        products(sc[0] | (sc[1] << 8), sc[2] | (sc[3] << 8),
-                 [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-                   for (int nt = 0; nt < NT; ++nt)
-                     mma_f16_16816(acc[m][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-                 });
-      } else {
-        // one row at a time, without the keys that it does not see; a NaN
-        // operand spoils every column of a product, so only the row's is kept
+        if (__any_sync(full, bad)) {
 #pragma unroll 1
-        for (int only = 0; only < u.nrows; ++only) {
-          int tk;
-          unit_row(p, u, only, &tk);
-          const int qr = u.qbase + tk;
-          uint32_t s0 = 0, s1 = 0;
+          for (int src = 0; src < 4; ++src)
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+              const int mine = j == 0 ? vk[0] : j == 1 ? vk[1] : j == 2 ? vk[2] : vk[3];
+              const uint32_t sj = j == 0 ? sc[0] : j == 1 ? sc[1] : j == 2 ? sc[2] : sc[3];
+              const int v = __shfl_sync(full, mine, src, 4);
+              const bool nan = (__shfl_sync(full, sj, src, 4) & 0x7f) == 0x7f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t v = (unsigned)qr - (unsigned)vk[j] < wlim ? sc[j] : 0u;
-            if (j < 2) s0 |= v << (8 * j);
-            else s1 |= v << (8 * (j - 2));
-          }
-          products(s0, s1, [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float o[4] = {acc[m][nt][0], acc[m][nt][1], acc[m][nt][2], acc[m][nt][3]};
-              mma_f16_16816(o, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                for (int c = 0; c < 2; ++c)
+                  if (nan && (unsigned)qp[nt][c] - (unsigned)v < wlim)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (nt * 8 + 2 * t + (i & 1) == only) acc[m][nt][i] = o[i];
+                    for (int m = 0; m < 8; ++m) acc[m][nt][c] = acc[m][nt][c + 2] = __int_as_float(0x7fffffff);
             }
-          });
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((sc[j] & 0x7f) == 0x7f) sc[j] = 0;
+        }
+      }
+      const uint32_t s0 = e4m3x2_to_f16(sc[0] | (sc[1] << 8)), s1 = e4m3x2_to_f16(sc[2] | (sc[3] << 8));
+#pragma unroll
+      for (int hw = 0; hw < 2; ++hw) {
+        const uint32_t A = hw ? w[0].y : w[0].x, B = hw ? w[1].y : w[1].x;
+        const uint32_t C = hw ? w[2].y : w[2].x, E = hw ? w[3].y : w[3].x;
+        const uint32_t nib = 0x0f0f0f0fu;
+        uint32_t f0[4], f1[4], f2[4], f3[4];
+        e2m1x8_to_f16((A & nib) | ((B << 4) & ~nib), f0);
+        e2m1x8_to_f16(((A >> 4) & nib) | (B & ~nib), f1);
+        e2m1x8_to_f16((C & nib) | ((E << 4) & ~nib), f2);
+        e2m1x8_to_f16(((C >> 4) & nib) | (E & ~nib), f3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f0[i] = hmul2(f0[i], s0), f1[i] = hmul2(f1[i], s0);
+          f2[i] = hmul2(f2[i], s1), f3[i] = hmul2(f3[i], s1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16_16816(acc[4 * hw + i][nt], f0[i], f1[i], f2[i], f3[i], pb[nt][0], pb[nt][1]);
         }
       }
     }
@@ -421,6 +407,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
   __syncthreads();                           // every ring is idle
   float *so = reinterpret_cast<float *>(smem);                   // [warp][row][128]
   float *sm = so + FW * kFp4Rows * kHeadDim, *sl = sm + FW * kFp4Rows;
+  long *sg = reinterpret_cast<long *>(sl + FW * kFp4Rows);       // [head of the CTA][row]: output row
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -440,34 +427,50 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
             make_float2(acc[m][nt][c], acc[m][nt][c + 2]);
     }
   __syncthreads();
+  // a thread per (head, row): the warps' factors, lse and the output row
   const long rows_all = (long)p.a.total_q * p.a.Hq;
-  for (int i = 0; i < u.nrows * p.hp; ++i) {
-    const int hs = i / u.nrows, row = i - hs * u.nrows;
-    float m = -INFINITY;
-    for (int w = hs; w < FW; w += p.hp) m = fmaxf(m, sm[w * kFp4Rows + row]);
-    float o = 0.f, z = 0.f;
-    for (int w = hs; w < FW; w += p.hp) {
-      const float mw = sm[w * kFp4Rows + row], zw = sl[w * kFp4Rows + row];
-      // a warp without a visible key has an empty sum; a NaN sum stays one
-      const float f = mw == -INFINITY ? (zw == 0.f ? 0.f : 1.f) : fast_exp2(mw - m);
-      z = fmaf(zw, f, z);
-      o = fmaf(so[(w * kFp4Rows + row) * kHeadDim + tid], f, o);
+  if (tid < kFp4Rows * p.hp) {
+    const int hs = tid / kFp4Rows, row = tid % kFp4Rows, h = u.h - warp % p.hp + hs;
+    float m = -INFINITY, z = 0.f, f[FW];
+#pragma unroll
+    for (int w = 0; w < FW; ++w)
+      if (w % p.hp == hs) m = fmaxf(m, sm[w * kFp4Rows + row]);
+#pragma unroll
+    for (int w = 0; w < FW; ++w) {
+      f[w] = 0.f;
+      if (w % p.hp == hs) {
+        const float mw = sm[w * kFp4Rows + row], zw = sl[w * kFp4Rows + row];
+        // a warp without a visible key has an empty sum; a NaN sum stays one
+        f[w] = mw == -INFINITY ? (zw == 0.f ? 0.f : 1.f) : fast_exp2(mw - m);
+        z = fmaf(zw, f[w], z);
+      }
     }
-    Unit uh = u;
-    uh.h = u.h - warp % p.hp + hs;
-    const float vg = p.kv.v_global ? __ldg(p.kv.v_global + uh.h) : 1.f;
-    const float out = z == 0.f ? 0.f : o / z * vg;
+    const float scale = z == 0.f ? 0.f : (p.kv.v_global ? __ldg(p.kv.v_global + h) : 1.f) / z;
+#pragma unroll
+    for (int w = 0; w < FW; ++w)
+      if (w % p.hp == hs) sl[w * kFp4Rows + row] = f[w] * scale;
     const float lse = z == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) - kPShift + log2f(z)) * kLn2;
-    int tk;
-    const long grow = unit_row(p, uh, row, &tk);
-    if (p.splits == 1) {
-      p.a.out[grow * kHeadDim + tid] = __float2bfloat16_rn(out);
-      if (tid == 0) p.a.lse[(grow % p.a.Hq) * p.a.total_q + grow / p.a.Hq] = lse;
-    } else {
-      p.a.o_part[((long)slot * rows_all + grow) * kHeadDim + tid] = out;
-      if (tid == 0) p.a.lse_part[(long)slot * rows_all + grow] = lse;
+    if (row < u.nrows) {
+      const int rr = u.rb * kFp4Rows + row, tok = u.s.q0 + rr / p.a.group;
+      const int head = h * p.a.group + rr % p.a.group;
+      const long grow = (long)tok * p.a.Hq + head;
+      sg[tid] = grow;
+      if (p.splits == 1) p.a.lse[(long)head * p.a.total_q + tok] = lse;
+      else p.a.lse_part[(long)slot * rows_all + grow] = lse;
     }
   }
+  __syncthreads();
+  for (int hs = 0; hs < p.hp; ++hs)
+#pragma unroll 4
+    for (int row = 0; row < u.nrows; ++row) {
+      float o = 0.f;
+#pragma unroll
+      for (int w = 0; w < FW; ++w)
+        if (w % p.hp == hs) o = fmaf(so[(w * kFp4Rows + row) * kHeadDim + tid], sl[w * kFp4Rows + row], o);
+      const long grow = sg[hs * kFp4Rows + row];
+      if (p.splits == 1) p.a.out[grow * kHeadDim + tid] = __float2bfloat16_rn(o);
+      else p.a.o_part[((long)slot * rows_all + grow) * kHeadDim + tid] = o;
+    }
   __syncthreads();                           // the merge buffers become rings again
 }
 
@@ -498,31 +501,29 @@ __global__ void __launch_bounds__(FT, ctas_per_sm(NT)) relattn_decode_fp4_kernel
     return;
   }
   const int base = tile_prefix<FT>(p, prefix, wsum);
-  const long per = base, total = per * (p.a.Hkv / p.hp) * p.row_blocks;
-  const long C = max((total + gridDim.x - 1) / gridDim.x, (long)p.c_min);
-  long x = blockIdx.x * C;
-  const long end = min(total, x + C);
+  // (the plan keeps the number of tiles below 2^31)
+  const unsigned per = base, total = per * (unsigned)(p.a.Hkv / p.hp * p.row_blocks);
+  const unsigned C = max((total + gridDim.x - 1) / gridDim.x, (unsigned)p.c_min);
+  unsigned x = (unsigned)min((unsigned long long)blockIdx.x * C, (unsigned long long)total);
+  const unsigned end = x + min(total - x, C);
   while (x < end) {
-    const int hr = (int)(x / per), xb = (int)(x - hr * per);
+    const unsigned hr = x / per;
+    const int xb = (int)(x - hr * per);
     u.b = last_not_above(prefix, p.a.batch, xb);   // it holds tile xb
     const int tiles = unit_tiles(p, u.b, &u.s, &u.lo), t0 = xb - prefix[u.b];
-    const int n = (int)min((long)(tiles - t0), end - x);
-    place(hr);
+    const int n = (int)min((unsigned)(tiles - t0), end - x);
+    place((int)hr);
     if (u.nrows > 0) {
-      const long ustart = hr * per + prefix[u.b], first = ustart / C;
+      const unsigned ustart = hr * per + prefix[u.b], first = ustart / C;
+      run_piece<NT, POS>(p, u, t0, n, (int)(blockIdx.x - first), smem);
       if (t0 == 0) {                         // mark the slots that no piece fills
         const int used = (int)((ustart + tiles - 1) / C - first) + 1;
-        const int cells = u.nrows * p.hp, empty = (p.splits - used) * cells;
-        for (int i = tid; i < empty; i += FT) {
-          int tk;
-          Unit uh = u;
-          const int cell = i % cells;
-          uh.h = u.h - hsub + cell / u.nrows;
-          const long grow = unit_row(p, uh, cell % u.nrows, &tk);
-          p.a.lse_part[(long)(used + i / cells) * p.a.total_q * p.a.Hq + grow] = -INFINITY;
+        for (int i = tid; i < u.nrows * p.hp; i += FT) {
+          const int hs = i / u.nrows, rr = u.rb * kFp4Rows + i % u.nrows;
+          const long grow = (long)(u.s.q0 + rr / p.a.group) * p.a.Hq + (u.h - hsub + hs) * p.a.group + rr % p.a.group;
+          for (int k = used; k < p.splits; ++k) p.a.lse_part[(long)k * p.a.total_q * p.a.Hq + grow] = -INFINITY;
         }
       }
-      run_piece<NT, POS>(p, u, t0, n, (int)(blockIdx.x - first), smem);
     }
     x += n;
   }
@@ -645,7 +646,8 @@ bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want
   }
   plan->rel_offset = (end + 255) / 256 * 256;
   plan->ws_bytes = a.E > 0 ? plan->rel_offset + rows_all * a.E * sizeof(float) : end;
-  return splits <= 65535 && rows_all <= 0x7fffffffUL && (long)a.batch * heads <= 0x7fffffffL;
+  return splits <= 65535 && rows_all <= 0x7fffffffUL && (long)a.batch * heads <= 0x7fffffffL &&
+         ((long)a.batch * U + grid) * heads <= 0x7fffffffL;
 }
 
 cudaError_t launch_decode_fp4(const Fp4DecodeArgs &p, cudaStream_t stream) {
