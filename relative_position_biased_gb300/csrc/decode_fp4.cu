@@ -127,11 +127,11 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
     }
     cp_async_commit();
   }
+  bool waited = false;                      // for the kernel before this one: R
   if (F_STAGES - 1 < n) {
     next_row = group_row(p, u, k_first + (F_STAGES - 1) * tile);
     if (POS) pos_next = fetch_pos(k_first + (F_STAGES - 1) * tile, next_row);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // R, where it was launched before this kernel
 
   uint32_t qf[NT][16];                      // row 8 nt + g, dims 32 t .. 32 t + 31
   float coef[NT][2], bscale[NT][2];         // of rows 8 nt + 2 t, + 1
@@ -231,6 +231,30 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
                                         : qmin - (key0 + FK - 1) < p.a.E);
 #pragma unroll 1
     for (int gr = 0; gr < 2; ++gr) {
+      int kp[2];                             // positions of the lane's keys
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int k = gr * 16 + hf * 8 + (g >> 1) + 4 * (g & 1);
+        kp[hf] = POS ? __shfl_sync(full, pos_lane, k) : key0 + k;
+      }
+      // With 8 rows the bias is loaded ahead of the products, which hide its
+      // latency (106 -> 102 us on 64 x 1 rows); with 16 that costs more in
+      // spilled registers than it gives (457 -> 482 us on 9 rows x 1M keys).
+      float bias[4];
+      auto load_bias = [&](int nt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned d = (unsigned)qp[nt][i & 1] - (unsigned)kp[i >> 1];
+          bias[i] = d < (unsigned)p.a.E ? p.a.rdec[(long)gr_[nt][i & 1] * p.a.E + d] : 0.f;
+        }
+      };
+      if (band) {
+        if (!waited) {
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          waited = true;
+        }
+        if (NT == 1) load_bias(0);
+      }
       // ---- S^T = K q^T, two chains of four products
       float x[NT][4], x2[NT][4];
 #pragma unroll
@@ -262,28 +286,17 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
       }
 
       // ---- logits: scale, bias, mask
-      int kp[2];                             // positions of the lane's keys
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int k = gr * 16 + hf * 8 + (g >> 1) + 4 * (g & 1);
-        kp[hf] = POS ? __shfl_sync(full, pos_lane, k) : key0 + k;
-      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[nt][i] = (x[nt][i] + x2[nt][i]) * coef[nt][i & 1];
       if (band) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          if (NT > 1) load_bias(nt);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float *R = p.a.rdec + (long)gr_[nt][c] * p.a.E;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const unsigned d = (unsigned)qp[nt][c] - (unsigned)kp[hf];
-              if (d < (unsigned)p.a.E) x[nt][hf * 2 + c] = fmaf(R[d], bscale[nt][c], x[nt][hf * 2 + c]);
-            }
-          }
+          for (int i = 0; i < 4; ++i) x[nt][i] = fmaf(bias[i], bscale[nt][i & 1], x[nt][i]);
+        }
       }
       if (edge) {
 #pragma unroll
@@ -480,6 +493,8 @@ __global__ void __launch_bounds__(FT, ctas_per_sm(NT)) relattn_decode_fp4_kernel
   __shared__ int prefix[kWalkBatch + 1];
   __shared__ int wsum[FW];
   const int tid = threadIdx.x, hsub = (tid >> 5) % p.hp;
+  // the merge kernel may take its place beside the last CTAs; it waits for this grid
+  asm volatile("griddepcontrol.launch_dependents;");
   Unit u;
   // head group and row block of unit group hr; the warp's head
   auto place = [&](int hr) {
