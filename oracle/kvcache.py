@@ -99,6 +99,8 @@ def kept_keys(weights, keep, recent, sink):
     n = len(w)
     recent = min(recent, keep)
     sink = min(sink, keep - recent, n - recent)
-    mid = list(range(sink, n - recent))
-    mid.sort(key=lambda p: (np.isnan(w[p]), -w[p] if not np.isnan(w[p]) else 0.0, p))
-    return np.array(sorted(list(range(sink)) + mid[:keep - recent - sink] + list(range(n - recent, n))), dtype=np.int64)
+    mid = np.arange(sink, n - recent)
+    v = w[mid]
+    nan = np.isnan(v)
+    mid = mid[np.lexsort((mid, -np.where(nan, 0.0, v), nan))]      # numbers first, heaviest first, lower index first
+    return np.sort(np.concatenate([np.arange(sink), mid[:keep - recent - sink], np.arange(n - recent, n)])).astype(np.int64)

@@ -9,11 +9,10 @@
 // the top) over distributed shared memory find the exact smallest kept key
 // and how many of its equals are kept; a last pass ranks the kept keys by
 // ballots and writes their rows.  Nothing is sorted, and every count is an
-// integer, so the result does not depend on any order.  Bound by the latency
-// of four dependent passes over the weights (which stay in L2): the cluster
-// is as wide as the longest sequence asks for.
-// Move: a flat copy of the kept rows' bytes, any number of planes (codes,
-// scales, bf16 rows); bound by memory.
+// integer, so the result does not depend on any order.  The keys are read
+// once where a CTA's share fits its shared memory, else from L2 in each pass.
+// Move: the kept rows' bytes, any number of planes (codes, scales, bf16 rows);
+// bound by memory.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -25,16 +24,16 @@ namespace cg = cooperative_groups;
 namespace relattn {
 namespace {
 
-constexpr int ET = 512, EW = ET / 32;
 constexpr int EB = 8;                        // keys of a lane in a tile
-constexpr int ETILE = ET * EB;
 constexpr int EBINS = 2048;
+constexpr int ECOPY = 4;                     // copies of a histogram: equal digits of a warp collide less
+constexpr int kMaxCluster = 16;              // CTAs of a cluster (above 8: opted into)
+constexpr int kCacheKeys = 46 * 1024;        // keys of a CTA that shared memory holds
 
 // Order-preserving bits: larger weight, larger key; -0 as 0, NaN below -inf.
 __device__ __forceinline__ uint32_t rank_bits(float w) {
-  if (w != w) return 0;
-  const uint32_t b = __float_as_uint(w == 0.f ? 0.f : w);
-  return (b >> 31) ? ~b : b | 0x80000000u;
+  const uint32_t b = __float_as_uint(w + 0.f);
+  return w != w ? 0u : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
 
 struct Segment {
@@ -62,17 +61,56 @@ __device__ __forceinline__ Segment segment(const EvictArgs &a, int unit) {
   return s;
 }
 
-__device__ __forceinline__ uint32_t weight_key(const EvictArgs &a, const Segment &s, int p, long *row) {
-  *row = a.src.row(s.b, s.k0, p);
-  return *row >= 0 ? rank_bits(__ldg(a.weights + (long)s.h * a.src.rows + *row)) : 0;
+// A warp takes 32 EB keys from p0 (a multiple of 32) at a time, key 32 i + lane
+// in [i].  32 keys share a page, so lane i looks up row i's page: base[i] is
+// the cache row of key 32 i, -1 outside the cache.
+__device__ __forceinline__ void rows_of(const EvictArgs &a, const Segment &s, int p0, int hi, int lane, int (&base)[EB]) {
+  if (!a.src.block_table) {                  // (the segment's rows lie inside the cache)
+#pragma unroll
+    for (int i = 0; i < EB; ++i) base[i] = s.k0 + p0 + 32 * i;
+    return;
+  }
+  int r = -1;
+  if (lane < EB && p0 + 32 * lane < hi) r = (int)a.src.row(s.b, s.k0, p0 + 32 * lane);
+#pragma unroll
+  for (int i = 0; i < EB; ++i) base[i] = __shfl_sync(0xffffffffu, r, i);
 }
 
+template <bool CACHED>
+__device__ __forceinline__ void load_keys(const EvictArgs &a, const Segment &s, int p0, int hi, int lane,
+                                          const uint32_t *cache, int lo, uint32_t (&key)[EB]) {
+  if (CACHED) {
+#pragma unroll
+    for (int i = 0; i < EB; ++i) {
+      const int p = p0 + 32 * i + lane;
+      key[i] = p < hi ? cache[p - lo] : 0;
+    }
+    return;
+  }
+  int base[EB];
+  rows_of(a, s, p0, hi, lane, base);
+  const float *w0 = a.weights + (long)s.h * a.src.rows + lane;
+  float w[EB];
+#pragma unroll
+  for (int i = 0; i < EB; ++i) {
+    const bool in = p0 + 32 * i + lane < hi && base[i] >= 0;
+    w[i] = in ? __ldg(w0 + base[i]) : __int_as_float(0x7fffffff);
+  }
+#pragma unroll
+  for (int i = 0; i < EB; ++i) key[i] = rank_bits(w[i]);
+}
+
+// Dynamic shared memory: the CTA's keys when CACHED.
+template <int ET, bool CACHED>
 __global__ void __launch_bounds__(ET) relattn_evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ unsigned hist[EBINS];
-  __shared__ unsigned scan[EW];
-  __shared__ int counts[2];                  // kept above the border / equal to it, in this CTA's keys
+  constexpr int EW = ET / 32, ETILE = ET * EB, EPT = EBINS / ET;      // EPT: bins of a thread
+  extern __shared__ uint32_t cache[];
+  __shared__ __align__(16) unsigned hist[EBINS * ECOPY];              // this CTA's counts of the pass
+  __shared__ unsigned scan[EW], lscan[EW];
   __shared__ unsigned found[2];              // digit, places left below it
+  __shared__ int counts[2];                  // kept above the border / equal to it, in this CTA's keys
   __shared__ int wabove[EW], wequal[EW];
+  __shared__ unsigned total[EBINS];          // the cluster's counts of the pass
   cg::cluster_group cl = cg::this_cluster();
   const int cs = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -80,7 +118,7 @@ __global__ void __launch_bounds__(ET) relattn_evict_select_kernel(const __grid_c
   const unsigned full = 0xffffffffu;
   if (!s.ok) {                               // the same for every CTA of the cluster
     if (rank == 0 && tid == 0) atomicOr(a.err, kDevErrSeqlens);
-    if (s.d0 >= 0 && s.d0 + (long)s.keep <= a.total_keep)
+    if (rank == 0 && s.d0 >= 0 && s.keep >= 0 && s.d0 + (long)s.keep <= a.total_keep)
       for (int i = tid; i < s.keep; i += ET) {
         a.src_row[(long)s.h * a.total_keep + s.d0 + i] = -1;
         if (s.h == 0) a.dst_row[s.d0 + i] = -1;
@@ -90,162 +128,158 @@ __global__ void __launch_bounds__(ET) relattn_evict_select_kernel(const __grid_c
   // this CTA's keys, a multiple of 32 each
   const int chunk = ((s.n + cs - 1) / cs + 31) & ~31;
   const int lo = min(s.n, rank * chunk), hi = min(s.n, lo + chunk);
-  const int mlo = max(lo, s.sink), mhi = min(hi, s.n - s.recent);   // its competing keys
+  const int m0 = s.sink, m1 = s.n - s.recent;                       // the competing keys
+  const int mlo = max(lo, m0 & ~31), mhi = min(hi, m1);             // from a multiple of 32 (or none)
 
-  // the border: keys above it are kept, and `equal` of those on it
+  if (CACHED) {
+    for (int p0 = lo + warp * 32 * EB; p0 < hi; p0 += ETILE) {
+      uint32_t key[EB];
+      load_keys<false>(a, s, p0, hi, lane, nullptr, 0, key);
+#pragma unroll
+      for (int i = 0; i < EB; ++i) {
+        const int p = p0 + 32 * i + lane;
+        if (p < hi) cache[p - lo] = key[i];
+      }
+    }
+    __syncthreads();
+  }
+
+  // the border: keys above it are kept, and `left` of those on it
   uint32_t border = 0, mask = 0;
-  int left = s.rest;
-  if (s.rest > 0 && s.rest < s.mid) {
+  int left = s.rest, na = 0, ne = 0;         // na / ne: this CTA's keys above / on the border
+  const bool choose = s.rest > 0 && s.rest < s.mid;
+  if (choose) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const int bins = pass == 2 ? 1024 : 2048;
-      for (int i = tid; i < bins; i += ET) hist[i] = 0;
+      for (int i = tid; i < bins; i += ET) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
       for (int p0 = mlo + warp * 32 * EB; p0 < mhi; p0 += ETILE) {
         uint32_t key[EB];
-        long row;
+        load_keys<CACHED>(a, s, p0, mhi, lane, cache, lo, key);
 #pragma unroll
         for (int i = 0; i < EB; ++i) {
           const int p = p0 + 32 * i + lane;
-          key[i] = p < mhi ? weight_key(a, s, p, &row) : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < EB; ++i) {
-          const bool in = p0 + 32 * i + lane < mhi && (key[i] & mask) == border;
-          const unsigned bin = (key[i] >> shift) & (bins - 1);
-          const unsigned who = __ballot_sync(full, in);
-          if (!who) continue;
-          // a warp of equal digits (ties are common) adds once
-          const unsigned lead = __shfl_sync(full, bin, __ffs(who) - 1);
-          if (__all_sync(full, !in || bin == lead)) {
-            if (lane == 0) atomicAdd(&hist[lead], (unsigned)__popc(who));
-          } else if (in) {
-            atomicAdd(&hist[bin], 1u);
-          }
+          const bool in = p >= m0 && p < mhi && (key[i] & mask) == border;
+          if (in) atomicAdd(&hist[((key[i] >> shift) & (bins - 1)) * ECOPY + (lane & (ECOPY - 1))], 1u);
         }
       }
       cl.sync();
-      // every CTA adds the cluster's histograms; thread t holds bins from the top
-      unsigned c[4], mine = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int bin = bins - 1 - (4 * tid + j);
-        c[j] = 0;
-        if (bin >= 0)
-          for (int r = 0; r < cs; ++r) c[j] += cl.map_shared_rank(hist, r)[bin];
-        mine += c[j];
+      // every CTA adds one slice of the bins over the cluster and hands the
+      // sums to all
+      const int slice = bins / cs;
+      for (int i = tid; i < slice; i += ET) {
+        const int bin = rank * slice + i;
+        unsigned c = 0;
+        for (int r = 0; r < cs; ++r) {
+          const uint4 x = reinterpret_cast<const uint4 *>(cl.map_shared_rank(hist, r))[bin];
+          c += x.x + x.y + x.z + x.w;
+        }
+        for (int r = 0; r < cs; ++r) cl.map_shared_rank(total, r)[bin] = c;
       }
-      unsigned inc = mine;
+      cl.sync();
+      // thread t holds EPT bins, from the top
+      unsigned c[EPT], own[EPT], mine = 0, lmine = 0;
+#pragma unroll
+      for (int j = 0; j < EPT; ++j) {
+        const int bin = bins - 1 - (EPT * tid + j);
+        c[j] = own[j] = 0;
+        if (bin >= 0) {
+          const uint4 x = reinterpret_cast<const uint4 *>(hist)[bin];
+          c[j] = total[bin];
+          own[j] = x.x + x.y + x.z + x.w;
+        }
+        mine += c[j];
+        lmine += own[j];
+      }
+      unsigned inc = mine, linc = lmine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(full, inc, o);
-        if (lane >= o) inc += y;
+        const unsigned y = __shfl_up_sync(full, inc, o), ly = __shfl_up_sync(full, linc, o);
+        if (lane >= o) inc += y, linc += ly;
       }
-      if (lane == 31) scan[warp] = inc;
+      if (lane == 31) scan[warp] = inc, lscan[warp] = linc;
       __syncthreads();
-      unsigned before = inc - mine;
-      for (int w = 0; w < warp; ++w) before += scan[w];
+      unsigned before = inc - mine, lbefore = linc - lmine;
+      before += __reduce_add_sync(full, lane < warp && lane < EW ? scan[lane] : 0u);
+      lbefore += __reduce_add_sync(full, lane < warp && lane < EW ? lscan[lane] : 0u);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < EPT; ++j) {
         if (before < (unsigned)left && before + c[j] >= (unsigned)left) {
-          found[0] = bins - 1 - (4 * tid + j);
+          found[0] = bins - 1 - (EPT * tid + j);
           found[1] = left - before;
+          counts[0] = (int)lbefore;          // this CTA's keys above the digit
+          counts[1] = (int)own[j];           // and on it
         }
         before += c[j];
+        lbefore += own[j];
       }
-      cl.sync();                             // histograms are read, and `found` is written
+      __syncthreads();
       border |= found[0] << shift;
       mask |= (uint32_t)(bins - 1) << shift;
       left = (int)found[1];
+      na += counts[0];
+      ne = counts[1];
+      __syncthreads();
     }
   }
-  const bool all = s.rest == s.mid, none = s.rest == 0;
-  // kept / equal keys of this CTA, then of the CTAs before it
-  auto kind = [&](int p, uint32_t key) {     // 0 dropped, 1 kept, 2 on the border
-    if (p < s.sink || p >= s.n - s.recent) return 1;
-    if (all) return 1;
-    if (none) return 0;
-    return key > border ? 1 : key == border ? 2 : 0;
-  };
-  if (tid < 2) counts[tid] = 0;
-  __syncthreads();
-  int na = 0, ne = 0;
-  for (int p0 = lo + warp * 32 * EB; p0 < hi; p0 += ETILE) {
-    long row;
-    uint32_t key[EB];
-#pragma unroll
-    for (int i = 0; i < EB; ++i) {
-      const int p = p0 + 32 * i + lane;
-      key[i] = p < hi ? weight_key(a, s, p, &row) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < EB; ++i) {
-      const int p = p0 + 32 * i + lane, k = p < hi ? kind(p, key[i]) : 0;
-      na += k == 1;
-      ne += k == 2;
-    }
-  }
-  na = __reduce_add_sync(full, na);
-  ne = __reduce_add_sync(full, ne);
-  if (lane == 0) {
-    atomicAdd(&counts[0], na);
-    atomicAdd(&counts[1], ne);
-  }
+  const bool all = s.rest == s.mid;
+  const int places = choose ? left : 0;      // border keys kept, lowest index first
+  // kept outright: protected keys of this CTA, all competing ones, or those above the border
+  auto overlap = [&](int x0, int x1) { return max(0, min(hi, x1) - max(lo, x0)); };
+  if (all) na = overlap(m0, m1);
+  na += overlap(0, m0) + overlap(m1, s.n);
+  if (!choose) ne = 0;
+  if (tid == 0) counts[0] = na, counts[1] = ne;
   cl.sync();
   int above = 0, equal = 0;                  // before the tile at hand
   for (int r = 0; r < rank; ++r) {
     above += cl.map_shared_rank(counts, r)[0];
     equal += cl.map_shared_rank(counts, r)[1];
   }
-  const int places = all || none ? 0 : left; // border keys kept, lowest index first
   for (int t0 = lo; t0 < hi; t0 += ETILE) {
     const int p0 = t0 + warp * 32 * EB;
     uint32_t key[EB];
-    long row[EB];
-#pragma unroll
-    for (int i = 0; i < EB; ++i) {
-      const int p = p0 + 32 * i + lane;
-      row[i] = -1;
-      key[i] = p < hi ? weight_key(a, s, p, &row[i]) : 0;
-    }
+    load_keys<CACHED>(a, s, p0, hi, lane, cache, lo, key);
     unsigned ba[EB], be[EB];
     int wa = 0, we = 0;
 #pragma unroll
     for (int i = 0; i < EB; ++i) {
-      const int p = p0 + 32 * i + lane, k = p < hi ? kind(p, key[i]) : 0;
-      ba[i] = __ballot_sync(full, k == 1);
-      be[i] = __ballot_sync(full, k == 2);
+      const int p = p0 + 32 * i + lane;
+      const bool in = p < hi, safe = p < m0 || p >= m1;
+      ba[i] = __ballot_sync(full, in && (safe || all || (choose && key[i] > border)));
+      be[i] = __ballot_sync(full, in && !safe && choose && key[i] == border);
       wa += __popc(ba[i]);
       we += __popc(be[i]);
     }
     __syncthreads();                         // the previous tile's counts are read
     if (lane == 0) wabove[warp] = wa, wequal[warp] = we;
     __syncthreads();
-    int a0 = above, e0 = equal;
-    for (int w = 0; w < EW; ++w) {
-      if (w < warp) a0 += wabove[w], e0 += wequal[w];
-      above += wabove[w];
-      equal += wequal[w];
-    }
+    const int va = lane < EW ? wabove[lane] : 0, ve = lane < EW ? wequal[lane] : 0;
+    int a0 = above + __reduce_add_sync(full, lane < warp ? va : 0);
+    int e0 = equal + __reduce_add_sync(full, lane < warp ? ve : 0);
+    above += __reduce_add_sync(full, va);
+    equal += __reduce_add_sync(full, ve);
+    if (wa + we == 0) continue;              // the same for the whole warp
+    int base[EB];
+    rows_of(a, s, p0, hi, lane, base);
     const unsigned below = (1u << lane) - 1;
 #pragma unroll
     for (int i = 0; i < EB; ++i) {
-      const int p = p0 + 32 * i + lane;
       const bool on = be[i] >> lane & 1;
       const int eb = e0 + __popc(be[i] & below);
       if ((ba[i] >> lane & 1) || (on && eb < places)) {
+        const int p = p0 + 32 * i + lane;
         const int j = a0 + __popc(ba[i] & below) + min(eb, places);
-        const long at = (long)s.d0 + j;
-        long dst = a.dst.row(s.b, s.d0, j);
-        if (row[i] < 0 || dst < 0) atomicOr(a.err, kDevErrSeqlens);
-        a.src_row[(long)s.h * a.total_keep + at] = (int)row[i];
+        const long at = (long)s.d0 + j, row = base[i] >= 0 ? base[i] + lane : -1, dst = a.dst.row(s.b, s.d0, j);
+        if (row < 0 || dst < 0) atomicOr(a.err, kDevErrSeqlens);
+        a.src_row[(long)s.h * a.total_keep + at] = (int)row;
         if (s.h == 0) a.dst_row[at] = (int)dst;
         if (dst >= 0) {
-          const long o = (long)s.h * a.dst.rows + dst;
-          const long src = (long)s.h * a.src.rows + row[i];
-          if (a.pos_out) a.pos_out[o] = a.key_pos ? (row[i] >= 0 ? __ldg(a.key_pos + src) : -1) : p;
-          if (a.w_out) a.w_out[o] = row[i] >= 0 ? __ldg(a.weights + src) : 0.f;
+          const long o = (long)s.h * a.dst.rows + dst, src = (long)s.h * a.src.rows + row;
+          if (a.pos_out) a.pos_out[o] = a.key_pos ? (row >= 0 ? __ldg(a.key_pos + src) : -1) : p;
+          if (a.w_out) a.w_out[o] = row >= 0 ? __ldg(a.weights + src) : 0.f;
         }
       }
       a0 += __popc(ba[i]);
@@ -255,69 +289,91 @@ __global__ void __launch_bounds__(ET) relattn_evict_select_kernel(const __grid_c
   cl.sync();                                 // no CTA leaves while another reads its counts
 }
 
-// Copy units: 16 bytes where a plane's rows and addresses allow, else 8, 4 or 1.
+// Copies the kept rows: a CTA takes MR rows of one head, plane by plane, in
+// units of 16 bytes where a plane's rows and addresses allow, else 8, 4 or 1.
+// The head is the fastest block index: the heads of a row share lines.
 struct MoveArgs {
   const int32_t *src_row, *dst_row, *cu_keep;
-  int batch, total_keep, Hkv, planes, units;
+  int batch, total_keep, Hkv, planes;
   long src_rows, dst_rows;
   const uint8_t *from[kMaxPlanes];
   uint8_t *to[kMaxPlanes];
-  int bytes[kMaxPlanes], width[kMaxPlanes], first[kMaxPlanes + 1];
+  int bytes[kMaxPlanes], width[kMaxPlanes];
 };
 
-constexpr int MT = 256, MU = 4;              // units in flight per thread
+constexpr int MT = 256, MR = 128, MU = 4;    // MU: units in flight per thread
 
-__global__ void __launch_bounds__(MT) relattn_evict_move_kernel(const __grid_constant__ MoveArgs a) {
-  const long per_row = (long)a.Hkv * a.units, total = a.total_keep * per_row;
-  const int used0 = a.cu_keep[0], used1 = a.cu_keep[a.batch];
-  for (long i0 = (long)blockIdx.x * MT * MU + threadIdx.x; i0 < total; i0 += (long)gridDim.x * MT * MU) {
-    uint4 v[MU];
-    uint8_t *to[MU];
-    int width[MU];
+template <typename V>
+__device__ __forceinline__ void move_plane(const MoveArgs &a, int pl, int h, int n, const int *src, const int *dst) {
+  const int bytes = a.bytes[pl], units = bytes / (int)sizeof(V), total = n * units;
+  const uint8_t *from = a.from[pl] + (long)h * bytes;
+  uint8_t *to = a.to[pl] + (long)h * bytes;
+  const long pitch = (long)a.Hkv * bytes;
+  const int shift = (units & (units - 1)) == 0 ? 31 - __clz(units) : -1;
+  for (int i0 = threadIdx.x; i0 < total; i0 += MT * MU) {
+    V v[MU];
+    long o[MU];
 #pragma unroll
     for (int k = 0; k < MU; ++k) {
-      const long i = i0 + (long)k * MT;
-      width[k] = 0;
+      const int i = i0 + k * MT;
+      o[k] = -1;
       if (i >= total) continue;
-      const int j = (int)(i / per_row), hu = (int)(i - j * per_row), h = hu / a.units, un = hu - h * a.units;
-      if (j < used0 || j >= used1) continue;   // rows of no sequence
-      const long src = __ldg(a.src_row + (long)h * a.total_keep + j), dst = __ldg(a.dst_row + j);
-      if (src < 0 || dst < 0 || src >= a.src_rows || dst >= a.dst_rows) continue;
-      int pl = 0;
-#pragma unroll
-      for (int q = 1; q < kMaxPlanes; ++q) pl += q < a.planes && un >= a.first[q];
-      const int w = a.width[pl], off = (un - a.first[pl]) * w;
-      const uint8_t *from = a.from[pl] + (src * a.Hkv + h) * a.bytes[pl] + off;
-      to[k] = a.to[pl] + (dst * a.Hkv + h) * a.bytes[pl] + off;
-      width[k] = w;
-      if (w == 16) v[k] = __ldg(reinterpret_cast<const uint4 *>(from));
-      else if (w == 8) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(from));
-        v[k].x = x.x, v[k].y = x.y;
-      } else if (w == 4) v[k].x = __ldg(reinterpret_cast<const unsigned *>(from));
-      else v[k].x = __ldg(from);
+      const int j = shift >= 0 ? i >> shift : i / units, off = (i - j * units) * (int)sizeof(V);
+      if (src[j] < 0) continue;
+      v[k] = __ldg(reinterpret_cast<const V *>(from + src[j] * pitch + off));
+      o[k] = dst[j] * pitch + off;
     }
 #pragma unroll
-    for (int k = 0; k < MU; ++k) {
-      if (width[k] == 16) *reinterpret_cast<uint4 *>(to[k]) = v[k];
-      else if (width[k] == 8) *reinterpret_cast<uint2 *>(to[k]) = make_uint2(v[k].x, v[k].y);
-      else if (width[k] == 4) *reinterpret_cast<unsigned *>(to[k]) = v[k].x;
-      else if (width[k] == 1) *to[k] = (uint8_t)v[k].x;
-    }
+    for (int k = 0; k < MU; ++k)
+      if (o[k] >= 0) *reinterpret_cast<V *>(to + o[k]) = v[k];
   }
 }
 
-}  // namespace
+__global__ void __launch_bounds__(MT) relattn_evict_move_kernel(const __grid_constant__ MoveArgs a) {
+  __shared__ int src[MR], dst[MR];
+  const int h = blockIdx.x % a.Hkv;
+  const int j0 = (int)(blockIdx.x / a.Hkv) * MR, n = min(MR, a.total_keep - j0);
+  for (int i = threadIdx.x; i < n; i += MT) {
+    const int j = j0 + i;
+    int s = -1, d = -1;
+    if (j >= __ldg(a.cu_keep) && j < __ldg(a.cu_keep + a.batch)) {      // else a row of no sequence
+      s = __ldg(a.src_row + (long)h * a.total_keep + j);
+      d = __ldg(a.dst_row + j);
+    }
+    if (d < 0 || s >= a.src_rows || d >= a.dst_rows) s = -1;
+    src[i] = s;
+    dst[i] = d;
+  }
+  __syncthreads();
+  for (int pl = 0; pl < a.planes; ++pl) {
+    if (a.width[pl] == 16) move_plane<uint4>(a, pl, h, n, src, dst);
+    else if (a.width[pl] == 8) move_plane<uint2>(a, pl, h, n, src, dst);
+    else if (a.width[pl] == 4) move_plane<unsigned>(a, pl, h, n, src, dst);
+    else move_plane<unsigned char>(a, pl, h, n, src, dst);
+  }
+}
 
-cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream) {
-  // CTAs per (sequence, kv head): one per 16K keys, at most the portable 8
-  int cs = 1;
-  while (cs < 8 && a.max_k > cs * 16384) cs *= 2;
-  const long units = (long)a.batch * a.Hkv;
-  if (units * cs > 0x7fffffffL) return cudaErrorInvalidValue;
+template <int ET, bool CACHED>
+cudaError_t launch_select(const EvictArgs &a, long units, int cs, int smem, cudaStream_t stream) {
+  auto *kernel = relattn_evict_select_kernel<ET, CACHED>;
+  static std::atomic<bool> done[kMaxDevicesAttr], wide[kMaxDevicesAttr];
+  if (CACHED) {
+    const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), kCacheKeys * 4, done);
+    if (e != cudaSuccess) return e;
+  }
+  if (cs > 8) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return cudaErrorInvalidDevice;
+    if (!wide[dev].load(std::memory_order_acquire)) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      wide[dev].store(true, std::memory_order_release);
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cs));
   cfg.blockDim = dim3(ET);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -326,7 +382,22 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, relattn_evict_select_kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream) {
+  // CTAs per (sequence, kv head): one per 16K keys, up to 16; of 512 threads
+  // while 16K keys are enough, else of 1024
+  int cs = 1;
+  while (cs < kMaxCluster && a.max_k > cs * 16384) cs *= 2;
+  const long units = (long)a.batch * a.Hkv;
+  if (units * cs > 0x7fffffffL) return cudaErrorInvalidValue;
+  const long chunk = ((a.max_k + cs - 1) / cs + 31) & ~31L;
+  cudaError_t e = chunk <= 16384       ? launch_select<512, true>(a, units, cs, (int)chunk * 4, stream)
+                  : chunk <= kCacheKeys ? launch_select<1024, true>(a, units, cs, (int)chunk * 4, stream)
+                                        : launch_select<1024, false>(a, units, cs, 0, stream);
   if (e != cudaSuccess) return e;
   if (a.planes == 0 || a.total_keep == 0) return cudaSuccess;
   MoveArgs m = {};
@@ -345,12 +416,9 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream) {
     m.bytes[i] = a.bytes[i];
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.from[i]) | reinterpret_cast<uintptr_t>(a.to[i]) | (uintptr_t)a.bytes[i];
     m.width[i] = !(bits & 15) ? 16 : !(bits & 7) ? 8 : !(bits & 3) ? 4 : 1;
-    m.first[i] = m.units;
-    m.units += a.bytes[i] / m.width[i];
   }
-  m.first[a.planes] = m.units;
-  const long total = (long)a.total_keep * a.Hkv * m.units;
-  const long grid = std::min<long>((total + MT * MU - 1) / (MT * MU), 1L << 20);
+  const long grid = ((long)a.total_keep + MR - 1) / MR * a.Hkv;
+  if (grid > 0x7fffffffL) return cudaErrorInvalidValue;
   relattn_evict_move_kernel<<<(unsigned)grid, MT, 0, stream>>>(m);
   return cudaGetLastError();
 }

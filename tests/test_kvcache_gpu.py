@@ -442,9 +442,12 @@ def _planes(rows, Hkv, kinds, seed=0):
     ((4097, 511), (1000, 510), 0, 0, (128, 128, 4, 4), 0, 0, True),
     ((4096, 5000), (4096, 4999), 100, 100, (3,), 0, 0, False),              # odd bytes, all kept
     ((1000, 300), (400, 128), 64, 4, (64, 64, 8, 8), 32, 64, False),        # pages to pages
-    ((17000, 9000), (2000, 8000), 128, 4, (8,), 0, 0, True),                # two CTAs a cluster
-    ((40000,), (5000,), 0, 0, (8,), 128, 0, False),                         # four
+    ((17000, 9000), (2000, 8000), 128, 4, (8,), 0, 0, True),
+    ((40000,), (5000,), 0, 0, (8,), 128, 0, False),                         # two CTAs a cluster
     ((150001,), (75000,), 1024, 4, (8,), 0, 0, True),                       # eight
+    ((300001, 40), (290000, 7), 5, 1, (16, 1), 0, 0, True),                 # sixteen
+    ((800000,), (1234,), 100, 3, (8,), 0, 0, False),                        # more keys than shared memory holds
+    ((790000, 100), (400000, 99), 0, 0, (4,), 64, 32, True),
 ])
 def test_evict(k_lens, keep, recent, sink, kinds, page, page_to, ties):
     Hkv = 2
