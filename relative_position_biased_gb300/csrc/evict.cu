@@ -102,7 +102,7 @@ __device__ __forceinline__ void load_keys(const EvictArgs &a, const Segment &s, 
 
 // Dynamic shared memory: the CTA's keys when CACHED.
 template <int ET, bool CACHED>
-__global__ void __launch_bounds__(ET) relattn_evict_select_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int EW = ET / 32, ETILE = ET * EB, EPT = EBINS / ET;      // EPT: bins of a thread
   extern __shared__ uint32_t cache[];
   __shared__ __align__(16) unsigned hist[EBINS * ECOPY];              // this CTA's counts of the pass
@@ -238,6 +238,11 @@ __global__ void __launch_bounds__(ET) relattn_evict_select_kernel(const __grid_c
     above += cl.map_shared_rank(counts, r)[0];
     equal += cl.map_shared_rank(counts, r)[1];
   }
+  static_assert(EBINS * ECOPY >= ETILE, "a tile's kept keys fit the histograms' place");
+  int *list = reinterpret_cast<int *>(hist);
+  int32_t *src_row = a.src_row + (long)s.h * a.total_keep + s.d0, *dst_row = a.dst_row + s.d0;
+  int32_t *pos_out = a.pos_out ? a.pos_out + (long)s.h * a.dst.rows : nullptr;
+  float *w_out = a.w_out ? a.w_out + (long)s.h * a.dst.rows : nullptr;
   for (int t0 = lo; t0 < hi; t0 += ETILE) {
     const int p0 = t0 + warp * 32 * EB;
     uint32_t key[EB];
@@ -259,56 +264,60 @@ __global__ void __launch_bounds__(ET) relattn_evict_select_kernel(const __grid_c
     const int va = lane < EW ? wabove[lane] : 0, ve = lane < EW ? wequal[lane] : 0;
     int a0 = above + __reduce_add_sync(full, lane < warp ? va : 0);
     int e0 = equal + __reduce_add_sync(full, lane < warp ? ve : 0);
+    const int first = above + min(equal, places);
     above += __reduce_add_sync(full, va);
     equal += __reduce_add_sync(full, ve);
-    if (wa + we == 0) continue;              // the same for the whole warp
-    int base[EB];
-    rows_of(a, s, p0, hi, lane, base);
+    const int kept = above + min(equal, places) - first;      // of this tile
+    // the tile's kept keys, in order, into shared memory (the histograms' place) ...
     const unsigned below = (1u << lane) - 1;
+    if (wa + we > 0) {                       // the same for the whole warp
 #pragma unroll
-    for (int i = 0; i < EB; ++i) {
-      const bool on = be[i] >> lane & 1;
-      const int eb = e0 + __popc(be[i] & below);
-      if ((ba[i] >> lane & 1) || (on && eb < places)) {
-        const int p = p0 + 32 * i + lane;
-        const int j = a0 + __popc(ba[i] & below) + min(eb, places);
-        const long at = (long)s.d0 + j, row = base[i] >= 0 ? base[i] + lane : -1, dst = a.dst.row(s.b, s.d0, j);
-        if (row < 0 || dst < 0) atomicOr(a.err, kDevErrSeqlens);
-        a.src_row[(long)s.h * a.total_keep + at] = (int)row;
-        if (s.h == 0) a.dst_row[at] = (int)dst;
-        if (dst >= 0) {
-          const long o = (long)s.h * a.dst.rows + dst, src = (long)s.h * a.src.rows + row;
-          if (a.pos_out) a.pos_out[o] = a.key_pos ? (row >= 0 ? __ldg(a.key_pos + src) : -1) : p;
-          if (a.w_out) a.w_out[o] = row >= 0 ? __ldg(a.weights + src) : 0.f;
-        }
+      for (int i = 0; i < EB; ++i) {
+        const int eb = e0 + __popc(be[i] & below);
+        if ((ba[i] >> lane & 1) || ((be[i] >> lane & 1) && eb < places))
+          list[a0 + __popc(ba[i] & below) + min(eb, places) - first] = p0 + 32 * i + lane;
+        a0 += __popc(ba[i]);
+        e0 += __popc(be[i]);
       }
-      a0 += __popc(ba[i]);
-      e0 += __popc(be[i]);
+    }
+    __syncthreads();
+    // ... and out from there with every lane at work (few keys of a warp are
+    // kept: stores from the ranking itself took 4 us a tile)
+    for (int k = tid; k < kept; k += ET) {
+      const int p = list[k], j = first + k;
+      const int row = a.src.block_table ? (int)a.src.row(s.b, s.k0, p) : s.k0 + p;
+      const int dst = a.dst.block_table ? (int)a.dst.row(s.b, s.d0, j) : s.d0 + j;
+      if (row < 0 || dst < 0) atomicOr(a.err, kDevErrSeqlens);
+      src_row[j] = row;
+      if (s.h == 0) dst_row[j] = dst;
+      if (dst >= 0) {
+        if (pos_out) pos_out[dst] = !a.key_pos ? p : row >= 0 ? __ldg(a.key_pos + (long)s.h * a.src.rows + row) : -1;
+        if (w_out) w_out[dst] = row >= 0 ? __ldg(a.weights + (long)s.h * a.src.rows + row) : 0.f;
+      }
     }
   }
   cl.sync();                                 // no CTA leaves while another reads its counts
 }
 
-// Copies the kept rows: a CTA takes MR rows of one head, plane by plane, in
-// units of 16 bytes where a plane's rows and addresses allow, else 8, 4 or 1.
-// The head is the fastest block index: the heads of a row share lines.
+// Copies the kept rows of one plane (blockIdx.y) and head, in units of 16 bytes
+// where the plane's rows and addresses allow, else 8, 4 or 1: a CTA takes as
+// many rows as give each thread MU units, all in flight together.  The head is
+// the fastest block index: the heads of a row share lines.
 struct MoveArgs {
   const int32_t *src_row, *dst_row, *cu_keep;
   int batch, total_keep, Hkv, planes;
   long src_rows, dst_rows;
   const uint8_t *from[kMaxPlanes];
   uint8_t *to[kMaxPlanes];
-  int bytes[kMaxPlanes], width[kMaxPlanes];
+  int bytes[kMaxPlanes], width[kMaxPlanes], rows[kMaxPlanes];         // rows: of a CTA
 };
 
-constexpr int MT = 256, MR = 128, MU = 4;    // MU: units in flight per thread
+constexpr int MT = 256, MU = 4, MROWS = MT * MU;
 
 template <typename V>
-__device__ __forceinline__ void move_plane(const MoveArgs &a, int pl, int h, int n, const int *src, const int *dst) {
-  const int bytes = a.bytes[pl], units = bytes / (int)sizeof(V), total = n * units;
-  const uint8_t *from = a.from[pl] + (long)h * bytes;
-  uint8_t *to = a.to[pl] + (long)h * bytes;
-  const long pitch = (long)a.Hkv * bytes;
+__device__ __forceinline__ void move_rows(const uint8_t *from, uint8_t *to, long pitch, int units, int n, const int *src,
+                                          const int *dst) {
+  const int total = n * units;
   const int shift = (units & (units - 1)) == 0 ? 31 - __clz(units) : -1;
   for (int i0 = threadIdx.x; i0 < total; i0 += MT * MU) {
     V v[MU];
@@ -330,27 +339,29 @@ __device__ __forceinline__ void move_plane(const MoveArgs &a, int pl, int h, int
 }
 
 __global__ void __launch_bounds__(MT) relattn_evict_move_kernel(const __grid_constant__ MoveArgs a) {
-  __shared__ int src[MR], dst[MR];
+  __shared__ int src[MROWS], dst[MROWS];
+  const int pl = blockIdx.y, rows = a.rows[pl];
   const int h = blockIdx.x % a.Hkv;
-  const int j0 = (int)(blockIdx.x / a.Hkv) * MR, n = min(MR, a.total_keep - j0);
+  const long j0 = (long)(blockIdx.x / a.Hkv) * rows;
+  if (j0 >= a.total_keep) return;
+  const int n = (int)min((long)rows, a.total_keep - j0);
+  const int used0 = __ldg(a.cu_keep), used1 = __ldg(a.cu_keep + a.batch);
   for (int i = threadIdx.x; i < n; i += MT) {
-    const int j = j0 + i;
-    int s = -1, d = -1;
-    if (j >= __ldg(a.cu_keep) && j < __ldg(a.cu_keep + a.batch)) {      // else a row of no sequence
-      s = __ldg(a.src_row + (long)h * a.total_keep + j);
-      d = __ldg(a.dst_row + j);
-    }
-    if (d < 0 || s >= a.src_rows || d >= a.dst_rows) s = -1;
+    const int j = (int)j0 + i;
+    int s = __ldg(a.src_row + (long)h * a.total_keep + j), d = __ldg(a.dst_row + j);
+    if (j < used0 || j >= used1 || d < 0 || s >= a.src_rows || d >= a.dst_rows) s = -1;   // a row of no sequence
     src[i] = s;
     dst[i] = d;
   }
   __syncthreads();
-  for (int pl = 0; pl < a.planes; ++pl) {
-    if (a.width[pl] == 16) move_plane<uint4>(a, pl, h, n, src, dst);
-    else if (a.width[pl] == 8) move_plane<uint2>(a, pl, h, n, src, dst);
-    else if (a.width[pl] == 4) move_plane<unsigned>(a, pl, h, n, src, dst);
-    else move_plane<unsigned char>(a, pl, h, n, src, dst);
-  }
+  const int bytes = a.bytes[pl], width = a.width[pl];
+  const uint8_t *from = a.from[pl] + (long)h * bytes;
+  uint8_t *to = a.to[pl] + (long)h * bytes;
+  const long pitch = (long)a.Hkv * bytes;
+  if (width == 16) move_rows<uint4>(from, to, pitch, bytes / 16, n, src, dst);
+  else if (width == 8) move_rows<uint2>(from, to, pitch, bytes / 8, n, src, dst);
+  else if (width == 4) move_rows<unsigned>(from, to, pitch, bytes / 4, n, src, dst);
+  else move_rows<unsigned char>(from, to, pitch, bytes, n, src, dst);
 }
 
 template <int ET, bool CACHED>
@@ -410,16 +421,19 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream) {
   m.planes = a.planes;
   m.src_rows = a.src.rows;
   m.dst_rows = a.dst.rows;
+  long grid = 0;
   for (int i = 0; i < a.planes; ++i) {
     m.from[i] = static_cast<const uint8_t *>(a.from[i]);
     m.to[i] = static_cast<uint8_t *>(a.to[i]);
     m.bytes[i] = a.bytes[i];
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.from[i]) | reinterpret_cast<uintptr_t>(a.to[i]) | (uintptr_t)a.bytes[i];
     m.width[i] = !(bits & 15) ? 16 : !(bits & 7) ? 8 : !(bits & 3) ? 4 : 1;
+    const int units = a.bytes[i] / m.width[i];
+    m.rows[i] = std::max(16, std::min(MROWS, MROWS / units));
+    grid = std::max(grid, ((long)a.total_keep + m.rows[i] - 1) / m.rows[i] * a.Hkv);
   }
-  const long grid = ((long)a.total_keep + MR - 1) / MR * a.Hkv;
   if (grid > 0x7fffffffL) return cudaErrorInvalidValue;
-  relattn_evict_move_kernel<<<(unsigned)grid, MT, 0, stream>>>(m);
+  relattn_evict_move_kernel<<<dim3((unsigned)grid, (unsigned)a.planes), MT, 0, stream>>>(m);
   return cudaGetLastError();
 }
 
