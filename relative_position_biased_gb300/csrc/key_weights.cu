@@ -22,8 +22,9 @@
 //     rows, and P^T r^T of one token's rows is 4 more instructions of the
 //     same shape, its operand read from shared memory at the token's offset.
 //     Nothing of size rows x E is ever stored.
-//   rows past the bias band (distance >= E for all 128 keys): the tcgen05
-//     kernel of key_weights_tc.cu, which adds to these sums.
+//   many rows of the usual shapes: the tcgen05 kernel of key_weights_tc.cu
+//     takes them all, or (r rows that TMA cannot read) those past the bias
+//     band and adds to these sums.
 #include <algorithm>
 
 #include "key_weights.cuh"
@@ -646,10 +647,9 @@ cudaError_t launch_key_weights(const KeyWeightArgs &args, cudaStream_t stream) {
                                            (unsigned)(p.a.batch * p.a.Hkv)), 256, 0, stream>>>(p);
     return cudaGetLastError();
   }
-  p.tc = !pos && key_weights_tc_supported(p);
+  p.tc = pos ? 0 : key_weights_tc_kind(p);
   cudaError_t e = cudaSuccess;
-  // the tcgen05 kernel takes every row without a bias, and the rows past the band with one
-  if (!p.tc || p.a.E > 0) e = pos ? launch_tiles<true>(p, cfg) : launch_tiles<false>(p, cfg);
+  if (p.tc != 2) e = pos ? launch_tiles<true>(p, cfg) : launch_tiles<false>(p, cfg);
   if (e != cudaSuccess || !p.tc) return e;
   return launch_key_weights_tc(p, stream);
 }

@@ -232,15 +232,14 @@ struct KeyWeightArgs : WalkArgs {
   float *w_out;
   float decay;
   const __nv_bfloat16 *table;   // bias table in the workspace (set by the launcher)
-  int tc;                       // 1: rows past the bias band go to key_weights_tc.cu
+  int tc;                       // tcgen05 kernel (key_weights_tc.cu): 0 no, 1 the rows past the bias band, 2 all rows
 };
 bool key_weights_walked(const KernelArgs &a);
 size_t key_weights_workspace(const KernelArgs &a, bool positions);
 cudaError_t launch_key_weights(const KeyWeightArgs &a, cudaStream_t stream);
-// Many rows on tcgen05 (key_weights_tc.cu): the rows whose every distance to a
-// tile's 128 keys is at least E, added to the sums of the kernel before it;
-// without a bias every row.
-bool key_weights_tc_supported(const KeyWeightArgs &a);
+// Many rows on tcgen05 (key_weights_tc.cu), by p.tc: the value it supports for
+// these arguments, and the launch (with 1 it adds to the tiles kernel's sums).
+int key_weights_tc_kind(const KeyWeightArgs &a);
 cudaError_t launch_key_weights_tc(const KeyWeightArgs &a, cudaStream_t stream);
 
 // Eviction (evict.cu)

@@ -355,7 +355,14 @@ WEIGHTS = [
     U.Case((300,), (900,), 8, 1, E=0, r_dim=0, window=200, page=32),
     U.Case((520, 17), (520, 300), 2, 2, E=64, r_dim=16, page=64, base=64.0),   # 32 tokens in 32 rows
     U.Case((400,), (400,), 16, 1, E=100, r_dim=5),                             # unaligned r and P
-    U.Case((31,), (2000,), 8, 1, E=64),                                        # too few rows for a 32-token box
+    U.Case((31,), (2000,), 8, 1, E=64),
+    U.Case((5,), (2000,), 16, 1, E=64),                                        # too few tokens for the tcgen05 kernel
+    U.Case((330, 130), (330, 200), 1, 1, E=100, r_dim=16),                     # 128 tokens a step
+    U.Case((300,), (400,), 4, 2, E=300, r_dim=64, window=250),                 # 64
+    U.Case((150, 70), (190, 70), 8, 2, E=64, r_dim=8, base=64.0),              # 32
+    U.Case((270,), (270,), 24, 2, E=128, r_dim=32),                            # group 12: unused row slots
+    U.Case((140,), (300,), 40, 1, E=64, r_dim=16, page=32),                    # group 40: 3 tokens
+    U.Case((40, 3), (90, 33), 64, 1, E=32, r_dim=16),
 ]
 
 
