@@ -748,32 +748,30 @@ def _positions(key_pos, q_pos, num_heads_kv: int, rows: int, batch: int, device)
                             _tensor(q_pos, "q_pos", torch.int32, (batch,), device))
 
 
-class _on:
-    """Runs a block with the tensors' device current and, where a stream is
-    given, with that stream current too, so that what the block allocates
-    belongs to the stream it launches on.  Gives the stream to launch on."""
+def _stream_here(device, stream: Optional[int]) -> Optional[int]:
+    """The current stream of `device` when a call may launch on it as things
+    are: no stream given and the device current.  Else None (see _switched)."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    index = device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return None
+    return torch._C._cuda_getCurrentRawStream(index)
 
-    def __init__(self, device, stream: Optional[int]):
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, not {device}")
-        self.device, self.stream, self.stack = device, stream, None
 
-    def __enter__(self) -> int:
-        import torch
-        other = self.device.index != torch.cuda.current_device()
-        if not other and self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        self.stack = contextlib.ExitStack()
-        if other:
-            self.stack.enter_context(torch.cuda.device(self.device))
-        if self.stream is not None:
-            self.stack.enter_context(torch.cuda.stream(
-                torch.cuda.ExternalStream(self.stream, device=self.device) if self.stream
-                else torch.cuda.default_stream(self.device)))
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        return self.stack.__exit__(*exc) if self.stack is not None else None
+@contextlib.contextmanager
+def _switched(device, stream: Optional[int]):
+    """With the tensors' device current and, where a stream is given, that stream
+    too, so that what the block allocates belongs to the stream it launches on."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                                   else torch.cuda.default_stream(device)):
+                yield
 
 
 def _queries(q, r, P, num_heads_kv: int, device):
@@ -812,8 +810,11 @@ def store_nvfp4(k, v, cu_seqlens_q, cu_seqlens_k, cache: KvNvfp4, *, block_table
     of every sequence) into the 4-bit cache; with ``block_table`` int32 [batch,
     max_pages_per_seq] the cache's rows are pages of ``page_size`` keys."""
     prm = _cache_rows(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table, page_size)
-    with _on(k.device, stream) as st:
-        _check(relattn_store_nvfp4(prm, st), "relattn_store_nvfp4")
+    st = _stream_here(k.device, stream)
+    if st is None:
+        with _switched(k.device, stream):
+            return store_nvfp4(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table=block_table, page_size=page_size)
+    _check(relattn_store_nvfp4(prm, st), "relattn_store_nvfp4")
 
 
 def load_nvfp4(cache: KvNvfp4, cu_seqlens_q, cu_seqlens_k, *, total_q: int, block_table=None, page_size: int = 0,
@@ -821,14 +822,18 @@ def load_nvfp4(cache: KvNvfp4, cu_seqlens_q, cu_seqlens_k, *, total_q: int, bloc
     """The last cu_seqlens_q rows of every sequence as bf16 (k, v) [total_q, Hkv,
     128] (pass cu_seqlens_k twice for all of them)."""
     import torch
-    with _on(cache.device, stream) as st:
-        shape = (int(total_q), cache.num_heads_kv, HEAD_DIM)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
-        _need(k.shape[0] == total_q, "k must have total_q rows")
-        prm = _cache_rows(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table, page_size)
-        _check(relattn_load_nvfp4(prm, st), "relattn_load_nvfp4")
-        return k, v
+    st = _stream_here(cache.device, stream)
+    if st is None:
+        with _switched(cache.device, stream):
+            return load_nvfp4(cache, cu_seqlens_q, cu_seqlens_k, total_q=total_q, block_table=block_table,
+                              page_size=page_size, k=k, v=v)
+    shape = (int(total_q), cache.num_heads_kv, HEAD_DIM)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    _need(k.shape[0] == total_q, "k must have total_q rows")
+    prm = _cache_rows(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table, page_size)
+    _check(relattn_load_nvfp4(prm, st), "relattn_load_nvfp4")
+    return k, v
 
 
 def _total_k(total_k: Optional[int], block_table, cu_k, rows: int) -> int:
@@ -859,24 +864,30 @@ def decode_nvfp4(q, cache: KvNvfp4, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seq
     from cu_seqlens_k, which waits for the stream.  Returns (out, lse)."""
     import torch
     dev = q.device
-    with _on(dev, stream) as st:
-        kv = _cache(cache, dev)
-        H, rows = cache.num_heads_kv, cache.rows
-        Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
-        batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
-        pages = _pages(block_table, page_size, rows, dev, batch)
-        pos = _positions(key_pos, q_pos, H, rows, batch, dev)
-        out, lse = _outputs(q, out, lse)
-        prm = RelattnParams(
-            qp, None, None, rp, Pp, cq, ck, batch, Tq, _total_k(total_k, block_table, cu_seqlens_k, rows),
-            max_seqlen_q, max_seqlen_k, Hq, H, HEAD_DIM, rd, E, window, alpha, log_scale_base,
-            _tensor(out, "out", torch.bfloat16, (Tq, Hq, HEAD_DIM), dev),
-            _tensor(lse, "lse", torch.float32, (Hq, Tq), dev), None, 0, num_splits)
-        status, need = relattn_decode_nvfp4_workspace_size(prm, pos)
-        _check(status, "relattn_decode_nvfp4_workspace_size")
-        keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
-        _check(relattn_decode_nvfp4(prm, kv, pos, pages, st), "relattn_decode_nvfp4")
-        return out, lse
+    st = _stream_here(dev, stream)
+    if st is None:
+        with _switched(dev, stream):
+            return decode_nvfp4(q, cache, r, P, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
+                                max_seqlen_k=max_seqlen_k, alpha=alpha, window=window, log_scale_base=log_scale_base,
+                                key_pos=key_pos, q_pos=q_pos, block_table=block_table, page_size=page_size,
+                                total_k=total_k, num_splits=num_splits, out=out, lse=lse, workspace=workspace)
+    kv = _cache(cache, dev)
+    H, rows = cache.num_heads_kv, cache.rows
+    Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
+    batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
+    pages = _pages(block_table, page_size, rows, dev, batch)
+    pos = _positions(key_pos, q_pos, H, rows, batch, dev)
+    out, lse = _outputs(q, out, lse)
+    prm = RelattnParams(
+        qp, None, None, rp, Pp, cq, ck, batch, Tq, _total_k(total_k, block_table, cu_seqlens_k, rows),
+        max_seqlen_q, max_seqlen_k, Hq, H, HEAD_DIM, rd, E, window, alpha, log_scale_base,
+        _tensor(out, "out", torch.bfloat16, (Tq, Hq, HEAD_DIM), dev),
+        _tensor(lse, "lse", torch.float32, (Hq, Tq), dev), None, 0, num_splits)
+    status, need = relattn_decode_nvfp4_workspace_size(prm, pos)
+    _check(status, "relattn_decode_nvfp4_workspace_size")
+    keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
+    _check(relattn_decode_nvfp4(prm, kv, pos, pages, st), "relattn_decode_nvfp4")
+    return out, lse
 
 
 def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int, max_seqlen_k: int, alpha: float,
@@ -891,36 +902,43 @@ def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: in
     not written."""
     import torch
     dev = q.device
-    with _on(dev, stream) as st:
-        fp4 = isinstance(k, KvNvfp4)
-        if fp4:
-            kv, rows, H = _cache(k, dev), k.rows, k.num_heads_kv
-        else:
-            rows, H, _ = _shape(k, "k", 3, HEAD_DIM)
-            kp = _tensor(k, "k", torch.bfloat16, k.shape, dev)
-        Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
-        batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
-        pages = _pages(block_table, page_size, rows, dev, batch)
-        pos = _positions(key_pos, q_pos, H, rows, batch, dev)
-        w_in = None if weights_in is None else _tensor(weights_in, "weights_in", torch.float32, (H, rows), dev)
-        if out is None:
-            out = torch.zeros(H, rows, dtype=torch.float32, device=dev)
-        total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
-        if not fp4 and block_table is None:
-            _need(total_k == rows, "a contiguous k has total_k rows")
-        fwd = RelattnParams(
-            qp, None if fp4 else kp, None, rp, Pp, cq, ck, batch, Tq, total_k, max_seqlen_q, max_seqlen_k, Hq, H,
-            HEAD_DIM, rd, E, window, alpha, log_scale_base, None,
-            _tensor(lse, "lse", torch.float32, (Hq, Tq), dev), None, 0, 0)
-        prm = RelattnKeyWeightsParams(
-            fwd, ctypes.pointer(kv) if fp4 else None, None if pos is None else ctypes.pointer(pos),
-            None if pages is None else ctypes.pointer(pages), w_in,
-            _tensor(out, "out", torch.float32, (H, rows), dev), decay)
-        status, need = relattn_key_weights_workspace_size(prm)
-        _check(status, "relattn_key_weights_workspace_size")
-        keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
-        _check(relattn_key_weights(prm, st), "relattn_key_weights")
-        return out
+    st = _stream_here(dev, stream)
+    if st is None:
+        with _switched(dev, stream):
+            return key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
+                               max_seqlen_k=max_seqlen_k, alpha=alpha, window=window, log_scale_base=log_scale_base,
+                               weights_in=weights_in, decay=decay, key_pos=key_pos, q_pos=q_pos,
+                               block_table=block_table, page_size=page_size, total_k=total_k, out=out,
+                               workspace=workspace)
+    fp4 = isinstance(k, KvNvfp4)
+    if fp4:
+        kv, rows, H = _cache(k, dev), k.rows, k.num_heads_kv
+    else:
+        rows, H, _ = _shape(k, "k", 3, HEAD_DIM)
+        kp = _tensor(k, "k", torch.bfloat16, k.shape, dev)
+    Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
+    batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
+    pages = _pages(block_table, page_size, rows, dev, batch)
+    pos = _positions(key_pos, q_pos, H, rows, batch, dev)
+    w_in = None if weights_in is None else _tensor(weights_in, "weights_in", torch.float32, (H, rows), dev)
+    if out is None:
+        out = torch.zeros(H, rows, dtype=torch.float32, device=dev)
+    total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
+    if not fp4 and block_table is None:
+        _need(total_k == rows, "a contiguous k has total_k rows")
+    fwd = RelattnParams(
+        qp, None if fp4 else kp, None, rp, Pp, cq, ck, batch, Tq, total_k, max_seqlen_q, max_seqlen_k, Hq, H,
+        HEAD_DIM, rd, E, window, alpha, log_scale_base, None,
+        _tensor(lse, "lse", torch.float32, (Hq, Tq), dev), None, 0, 0)
+    prm = RelattnKeyWeightsParams(
+        fwd, ctypes.pointer(kv) if fp4 else None, None if pos is None else ctypes.pointer(pos),
+        None if pages is None else ctypes.pointer(pages), w_in,
+        _tensor(out, "out", torch.float32, (H, rows), dev), decay)
+    status, need = relattn_key_weights_workspace_size(prm)
+    _check(status, "relattn_key_weights_workspace_size")
+    keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
+    _check(relattn_key_weights(prm, st), "relattn_key_weights")
+    return out
 
 
 def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seqlen_k: int, recent: int, sink: int = 0,
@@ -935,40 +953,47 @@ def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seq
     of the new cache."""
     import torch
     dev = weights.device
-    with _on(dev, stream) as st:
-        n = len(planes)
-        if not n == len(dst_planes) <= MAX_PLANES:
-            raise ValueError(f"as many dst_planes as planes, at most {MAX_PLANES}")
-        H, rows = _shape(weights, "weights", 2)
-        batch, ck, ckeep = _lengths(cu_seqlens_k, cu_seqlens_keep, "cu_seqlens_k", "cu_seqlens_keep", dev)
-        rows_keep = dst_planes[0].shape[0] if n else int(total_keep)
-        prm = RelattnEvictParams(_tensor(weights, "weights", torch.float32, (H, rows), dev), ck, ckeep)
-        for i in range(n):
-            a, b = planes[i], dst_planes[i]
-            rest = a.shape[2:]
-            if a.shape[:2] != (rows, H) or b.shape != (rows_keep, H, *rest):
-                raise ValueError(f"plane {i} must be [rows, Hkv, ...] and its destination [rows_keep, Hkv, ...]")
-            prm.planes[i] = RelattnPlane(_tensor(a, f"plane {i}", a.dtype, a.shape, dev),
-                                         _tensor(b, f"destination {i}", a.dtype, b.shape, dev),
-                                         a.element_size() * rest.numel())
-        pages = _pages(block_table, page_size, rows, dev, batch)
-        pages_keep = _pages(block_table_keep, page_size_keep, rows_keep, dev, batch)
-        if key_pos_out is None:
-            key_pos_out = torch.full((H, rows_keep), -1, dtype=torch.int32, device=dev)
-        if weights_out is None:
-            weights_out = torch.zeros(H, rows_keep, dtype=torch.float32, device=dev)
-        prm.key_pos = None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, (H, rows), dev)
-        prm.batch, prm.total_keep, prm.num_heads_kv, prm.num_planes = batch, total_keep, H, n
-        prm.total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
-        prm.max_seqlen_k, prm.sink, prm.recent, prm.rows, prm.rows_keep = max_seqlen_k, sink, recent, rows, rows_keep
-        if pages is not None:
-            prm.pages = ctypes.pointer(pages)
-        if pages_keep is not None:
-            prm.pages_keep = ctypes.pointer(pages_keep)
-        prm.weights_out = _tensor(weights_out, "weights_out", torch.float32, (H, rows_keep), dev)
-        prm.key_pos_out = _tensor(key_pos_out, "key_pos_out", torch.int32, (H, rows_keep), dev)
-        status, need = relattn_evict_workspace_size(prm)
-        _check(status, "relattn_evict_workspace_size")
-        keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
-        _check(relattn_evict(prm, st), "relattn_evict")
-        return key_pos_out, weights_out
+    st = _stream_here(dev, stream)
+    if st is None:
+        with _switched(dev, stream):
+            return evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, max_seqlen_k=max_seqlen_k,
+                         recent=recent, sink=sink, total_keep=total_keep, total_k=total_k, key_pos=key_pos,
+                         block_table=block_table, page_size=page_size, block_table_keep=block_table_keep,
+                         page_size_keep=page_size_keep, key_pos_out=key_pos_out, weights_out=weights_out,
+                         workspace=workspace)
+    n = len(planes)
+    if not n == len(dst_planes) <= MAX_PLANES:
+        raise ValueError(f"as many dst_planes as planes, at most {MAX_PLANES}")
+    H, rows = _shape(weights, "weights", 2)
+    batch, ck, ckeep = _lengths(cu_seqlens_k, cu_seqlens_keep, "cu_seqlens_k", "cu_seqlens_keep", dev)
+    rows_keep = dst_planes[0].shape[0] if n else int(total_keep)
+    prm = RelattnEvictParams(_tensor(weights, "weights", torch.float32, (H, rows), dev), ck, ckeep)
+    for i in range(n):
+        a, b = planes[i], dst_planes[i]
+        rest = a.shape[2:]
+        if a.shape[:2] != (rows, H) or b.shape != (rows_keep, H, *rest):
+            raise ValueError(f"plane {i} must be [rows, Hkv, ...] and its destination [rows_keep, Hkv, ...]")
+        prm.planes[i] = RelattnPlane(_tensor(a, f"plane {i}", a.dtype, a.shape, dev),
+                                     _tensor(b, f"destination {i}", a.dtype, b.shape, dev),
+                                     a.element_size() * rest.numel())
+    pages = _pages(block_table, page_size, rows, dev, batch)
+    pages_keep = _pages(block_table_keep, page_size_keep, rows_keep, dev, batch)
+    if key_pos_out is None:
+        key_pos_out = torch.full((H, rows_keep), -1, dtype=torch.int32, device=dev)
+    if weights_out is None:
+        weights_out = torch.zeros(H, rows_keep, dtype=torch.float32, device=dev)
+    prm.key_pos = None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, (H, rows), dev)
+    prm.batch, prm.total_keep, prm.num_heads_kv, prm.num_planes = batch, total_keep, H, n
+    prm.total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
+    prm.max_seqlen_k, prm.sink, prm.recent, prm.rows, prm.rows_keep = max_seqlen_k, sink, recent, rows, rows_keep
+    if pages is not None:
+        prm.pages = ctypes.pointer(pages)
+    if pages_keep is not None:
+        prm.pages_keep = ctypes.pointer(pages_keep)
+    prm.weights_out = _tensor(weights_out, "weights_out", torch.float32, (H, rows_keep), dev)
+    prm.key_pos_out = _tensor(key_pos_out, "key_pos_out", torch.int32, (H, rows_keep), dev)
+    status, need = relattn_evict_workspace_size(prm)
+    _check(status, "relattn_evict_workspace_size")
+    keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
+    _check(relattn_evict(prm, st), "relattn_evict")
+    return key_pos_out, weights_out

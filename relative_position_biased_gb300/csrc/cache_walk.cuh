@@ -22,7 +22,7 @@ __device__ __forceinline__ int unit_tiles(const WalkArgs &p, int b, SeqRows *sp,
   *sp = s;
   *lo = 0;
   if (!s.ok || s.lq > p.a.max_q || s.lk > p.a.max_k || first_query_pos(s, p.q_pos, b) < 0) return -1;
-  if (s.lq == 0) return 0;
+  if (s.lq == 0 && !p.idle) return 0;
   if (p.a.window > 0 && !p.key_pos) *lo = max(0, s.lk - s.lq - p.a.window + 1) & ~31;
   const int tile = kWalkTile / p.hp;
   return (s.lk - *lo + tile - 1) / tile;

@@ -146,11 +146,11 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
       cp_async_commit();
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  bool waited = false;                      // for the kernel before this one: R
 
   uint32_t qf[NT][16];
   float coef[NT][2], bscale[NT][2], lse2[NT][2];
-  int qp[NT][2];
+  int qp[NT][2], rrow[NT][2];               // position, row of R
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int nrow = nt * 8 + g;
@@ -196,8 +196,9 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
       const int m = nt * 8 + 2 * t + c;
       const float bk = __shfl_sync(full, back, (2 * t + c) * 4);
       int tk;
-      const long grow = unit_row(p, u, m, &tk);
       const bool live = m < u.nrows;
+      const long grow = unit_row(p, u, live ? m : 0, &tk);
+      rrow[nt][c] = (int)grow;
       const float s = live ? log_scale(u.qbase + tk, p.a.inv_ln_base) : 0.f;
       qp[nt][c] = live ? u.qbase + tk : -1;
       coef[nt][c] = p.a.alpha_log2e * s * kg * bk;
@@ -236,51 +237,54 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
       kp_lane = __ldg(p.key_pos + (long)u.h * p.pages.rows + row0 + lane);
       if (kp_lane < 0) kp_lane = 0x7fffffff;
     }
-    float x[2][NT][4];
+    const bool edge = POS || key0 + WK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
+    const bool band = p.a.E > 0 && (POS ? __any_sync(full, kp_lane != 0x7fffffff && qmin - kp_lane < p.a.E)
+                                        : qmin - (key0 + WK - 1) < p.a.E);
+    if (band && !waited) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+    }
+    float v[4];                              // keys operand_key(g) + 8 hf + 16 gr at 2 gr + hf
 #pragma unroll
     for (int gr = 0; gr < 2; ++gr) {
-      uint32_t f[8][4];
-      key_operands<FP4>(st, gr, lane, f);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        x[gr][nt][0] = x[gr][nt][1] = x[gr][nt][2] = x[gr][nt][3] = 0.f;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) key_mma<FP4>(x[gr][nt], f[s], qf[nt][2 * s], qf[nt][2 * s + 1]);
-      }
-    }
-    const bool edge = POS || key0 + WK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
-    int kp[2][2];
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr)
+      int kp[2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int k = gr * 16 + hf * 8 + operand_key<FP4>(g);
-        kp[gr][hf] = POS ? __shfl_sync(full, kp_lane, k) : key0 + k;
+        kp[hf] = POS ? __shfl_sync(full, kp_lane, k) : key0 + k;
+        v[2 * gr + hf] = 0.f;
       }
-    const bool band = p.a.E > 0 && (POS ? __any_sync(full, kp_lane != 0x7fffffff && qmin - kp_lane < p.a.E)
-                                        : qmin - (key0 + WK - 1) < p.a.E);
-    float v[4] = {0.f, 0.f, 0.f, 0.f};      // keys operand_key(g) + 8 hf + 16 gr at 2 gr + hf
+      float x[NT][4], bias[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float *R = nullptr;
-        if (band) {
-          int tk;
-          R = p.a.rdec + unit_row(p, u, min(nt * 8 + 2 * t + c, u.nrows - 1), &tk) * p.a.E;
-        }
+        for (int i = 0; i < 4; ++i) x[nt][i] = bias[nt][i] = 0.f;
+      if (band) {                            // ahead of the products, which hide its latency
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float y = x[gr][nt][2 * hf + c] * coef[nt][c];
-            const unsigned d = (unsigned)qp[nt][c] - (unsigned)kp[gr][hf];
-            if (band && d < (unsigned)p.a.E) y = fmaf(R[d], bscale[nt][c], y);
-            float e = fast_exp2(y - lse2[nt][c]);
-            if (edge && d >= wlim) e = 0.f;
-            v[2 * gr + hf] += e;
+          for (int i = 0; i < 4; ++i) {
+            const unsigned d = (unsigned)qp[nt][i & 1] - (unsigned)kp[i >> 1];
+            if (d < (unsigned)p.a.E) bias[nt][i] = p.a.rdec[(long)rrow[nt][i & 1] * p.a.E + d];
           }
       }
+      uint32_t f[8][4];
+      key_operands<FP4>(st, gr, lane, f);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) key_mma<FP4>(x[nt], f[s], qf[nt][2 * s], qf[nt][2 * s + 1]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y = fmaf(x[nt][i], coef[nt][i & 1], -lse2[nt][i & 1]);
+          if (band) y = fmaf(bias[nt][i], bscale[nt][i & 1], y);
+          float e = fast_exp2(y);
+          if (edge && (unsigned)qp[nt][i & 1] - (unsigned)kp[i >> 1] >= wlim) e = 0.f;
+          v[2 * gr + (i >> 1)] += e;
+        }
+    }
     const float sum = quad_reduce(v, t);
     const int key = key0 + (t >> 1) * 16 + (t & 1) * 8 + operand_key<FP4>(g);
     if (row0 >= 0 && key < u.s.lk) write_weight(p, u, key, row0 + (key - key0), sum);
@@ -289,8 +293,11 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
   __syncwarp();
 }
 
+// CTAs of an SM: bounded by registers (4-bit keys) or the ring (bf16 keys).
+constexpr int rows_ctas(int nt, bool fp4) { return fp4 ? (nt == 1 ? 5 : 3) : 2; }
+
 template <int NT, bool POS, bool FP4>
-__global__ void __launch_bounds__(WT) relattn_key_weights_rows_kernel(const __grid_constant__ KeyWeightArgs p) {
+__global__ void __launch_bounds__(WT, rows_ctas(NT, FP4)) relattn_key_weights_rows_kernel(const __grid_constant__ KeyWeightArgs p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int prefix[kWalkBatch + 1];
   __shared__ int wsum[WW];
@@ -554,15 +561,15 @@ __global__ void __launch_bounds__(256) relattn_rel_table_kernel(const __nv_bfloa
 
 // ------------------------------------------------------------------ keys out of sight
 
-// Keys that the walk leaves out (past the window of every row, or of a
-// sequence without query rows): w_out = decay * w_in.
+// Keys that the walk leaves out (past the window of every row): w_out = decay *
+// w_in.
 __global__ void __launch_bounds__(256) relattn_key_weights_cold_kernel(const __grid_constant__ KeyWeightArgs p) {
   Unit u;
   u.b = blockIdx.y / p.a.Hkv;
   u.h = blockIdx.y - u.b * p.a.Hkv;
   const int tiles = unit_tiles(p, u.b, &u.s, &u.lo);
   if (tiles < 0) return;
-  const int end = tiles == 0 ? u.s.lk : u.lo;
+  const int end = u.lo;
   for (int key = blockIdx.x * kColdKeys + threadIdx.x; key < min(end, (int)(blockIdx.x + 1) * kColdKeys); key += 256) {
     const long row = p.pages.row(u.b, u.s.k0, key);
     if (row < 0) {
@@ -579,7 +586,7 @@ cudaError_t launch_rows(const KeyWeightArgs &p, cudaLaunchConfig_t cfg) {
   auto *kernel = relattn_key_weights_rows_kernel<NT, POS, FP4>;
   const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), KStage<FP4>::ring, done);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(p.a.sms * (FP4 ? 4 : 2)));
+  cfg.gridDim = dim3((unsigned)(p.a.sms * rows_ctas(NT, FP4)));
   cfg.blockDim = dim3(WT);
   cfg.dynamicSmemBytes = KStage<FP4>::ring;
   return cudaLaunchKernelEx(&cfg, kernel, p);
@@ -619,6 +626,7 @@ cudaError_t launch_key_weights(const KeyWeightArgs &args, cudaStream_t stream) {
   const bool pos = p.key_pos != nullptr, fp4 = p.k == nullptr, walked = key_weights_walked(p.a);
   p.table = nullptr;
   p.hp = walked && p.a.Hkv % 2 == 0 ? 2 : 1;   // two heads share their rows' lines
+  p.idle = 1;                                 // their keys' weights decay
   if (p.a.E > 0) {
     cudaError_t e;
     if (pos || walked) {
@@ -641,8 +649,8 @@ cudaError_t launch_key_weights(const KeyWeightArgs &args, cudaStream_t stream) {
   if (walked) {
     const cudaError_t e = pos ? (fp4 ? launch_few<true, true>(p, cfg) : launch_few<true, false>(p, cfg))
                               : (fp4 ? launch_few<false, true>(p, cfg) : launch_few<false, false>(p, cfg));
-    if (e != cudaSuccess) return e;
-    // the walk leaves the keys out of sight alone
+    // the walk leaves the keys past every row's window alone
+    if (e != cudaSuccess || p.a.window <= 0 || pos || p.a.max_k <= p.a.window) return e;
     relattn_key_weights_cold_kernel<<<dim3((unsigned)((p.a.max_k + kColdKeys - 1) / kColdKeys),
                                            (unsigned)(p.a.batch * p.a.Hkv)), 256, 0, stream>>>(p);
     return cudaGetLastError();

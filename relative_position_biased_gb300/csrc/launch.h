@@ -202,6 +202,7 @@ struct WalkArgs {
   CachePages pages;
   const int32_t *key_pos, *q_pos;
   int hp;                             // kv heads a walking CTA takes (1 or 2)
+  int idle;                           // 1: sequences without query rows are walked too
 };
 constexpr int kWalkTile = 128;        // keys a CTA takes at a time, over its kv heads
 
