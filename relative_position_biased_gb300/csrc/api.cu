@@ -380,6 +380,7 @@ relattn_status cache_rows_args(const relattn_cache_rows_params *p, Fp4RowArgs *a
   if (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v) || !p->cu_seqlens_q || !p->cu_seqlens_k)
     return RELATTN_ERR_INVALID_ARG;
   if ((st = cache_fp4(p->cache, &a->kv)) != RELATTN_OK) return st;
+  if ((size_t)p->total_q * p->num_heads_kv * 8 > 0xfffff000UL) return RELATTN_ERR_UNSUPPORTED;
   const size_t in = (size_t)p->total_q * p->num_heads_kv * kHeadDim * 2;
   const size_t codes = (size_t)p->cache->rows * p->num_heads_kv * 64;
   const void *arrays[] = {a->kv.k, a->kv.v, a->kv.k_scale, a->kv.v_scale};

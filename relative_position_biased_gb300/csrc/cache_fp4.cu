@@ -17,9 +17,9 @@
 // function takes about ten (store of 4 x 8192 x 2 rows: 23 -> XX us).  Outside the range
 // where residuals are exact, and for infinities, the divide function is called.
 //
-// One thread takes 16 dims: 32 bytes of bf16 on one side, 8 bytes of codes
-// and a scale byte on the other, so a warp touches 1 KB and 256 + 32 bytes
-// without gaps.  Bound by memory.
+// One thread takes 16 dims of K and of V: 32 bytes of bf16 on one side, 8 bytes
+// of codes and a scale byte on the other, so a warp touches 1 KB and 256 + 32
+// bytes without gaps.
 #include "nvfp4.cuh"
 
 namespace relattn {
@@ -36,12 +36,22 @@ struct Divisor {
     y = __frcp_rn(b);
     plain = !(b > 0x1p-60f && b < 0x1p60f && top < 0x1p60f);
   }
-  __device__ __forceinline__ float operator()(float a) const {
-    if (plain) return __fdiv_rn(a, b);
-    // (elements below 2^-60 may lose residual bits to underflow: they are far
-    // below every border, the smallest being 2^-12)
+  // (elements below 2^-60 may lose residual bits to underflow: they are far
+  // below every border, the smallest being 2^-12)
+  __device__ __forceinline__ float quick(float a) const {
     const float q = __fmul_rn(a, y);
     return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+  }
+  __device__ __forceinline__ void operator()(float (&x)[16], float &top) const {
+    if (!plain) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = quick(x[i]);
+      top = quick(top);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], b);
+      top = __fdiv_rn(top, b);
+    }
   }
 };
 
@@ -73,17 +83,21 @@ __device__ __forceinline__ bool place_row(const Fp4RowArgs &a, int t, long *row)
   return true;
 }
 
-__global__ void __launch_bounds__(kRowThreads) relattn_store_fp4_kernel(const Fp4RowArgs a) {
-  const long idx = (long)blockIdx.x * kRowThreads + threadIdx.x;
-  const int per_row = a.Hkv * kFp4Blocks;
-  const long t = idx / per_row;
-  if (t >= a.total_q) return;
-  const int hb = (int)(idx - t * per_row), h = hb / kFp4Blocks;
-  long row;
-  if (!place_row(a, (int)t, &row) || row < 0) return;
-  const bool is_v = blockIdx.y != 0;
-  const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? a.v : a.k) + (t * per_row + hb) * 16);
-  const float *gp = is_v ? a.kv.v_global : a.kv.k_global;
+// What a thread takes of a call: block hb of a (row, head) grid of per_row.
+// (32-bit: 2^32 blocks of K and V alone would fill the device's memory; the
+// host refuses more.)
+struct BlockPlace {
+  unsigned t, hb;
+  int h;
+  __device__ __forceinline__ BlockPlace(int Hkv) {
+    const unsigned idx = blockIdx.x * kRowThreads + threadIdx.x, per_row = Hkv * kFp4Blocks;
+    t = idx / per_row;
+    hb = idx - t * per_row;
+    h = hb / kFp4Blocks;
+  }
+};
+
+__device__ __forceinline__ void store_block(const uint4 *src, const float *gp, int h, uint8_t *codes_at, uint8_t *scale_at) {
   const float g = gp ? __ldg(gp + h) : 1.f;
   const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
   const uint32_t ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -97,52 +111,40 @@ __global__ void __launch_bounds__(kRowThreads) relattn_store_fp4_kernel(const Fp
     top = max(top, max((ws[i] << 16) & 0x7fff0000u, ws[i] & 0x7fff0000u));
   }
   float amax = __uint_as_float(top);
-  if (gp) {
-    const Divisor by_g(g, amax);
-    amax = by_g(amax);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = by_g(x[i]);
-  }
+  if (gp) Divisor(g, amax)(x, amax);
   const uint32_t sb = e4m3x2(0.f, __fdiv_rn(amax, 6.f)) & 0xffu;
   const uint32_t sh = e4m3x2_to_f16(sb);
   float s;
   asm("cvt.f32.f16 %0, %1;" : "=f"(s) : "h"((uint16_t)sh));
   uint32_t codes[2] = {0, 0};
   if (s > 0.f) {
-    const Divisor by_s(s, amax);
+    Divisor(s, amax)(x, amax);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
-      const float lo = by_s(x[i]), hi = by_s(x[i + 1]);
       uint32_t c;
       asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\tmov.b32 %0, {c, 0, 0, 0};\n\t}"
-          : "=r"(c) : "f"(hi), "f"(lo));
+          : "=r"(c) : "f"(x[i + 1]), "f"(x[i]));
       codes[i / 8] |= c << (4 * (i & 7));
     }
   }
-  uint8_t *cp = const_cast<uint8_t *>(is_v ? a.kv.v : a.kv.k);
-  uint8_t *sp = const_cast<uint8_t *>(is_v ? a.kv.v_scale : a.kv.k_scale);
-  *reinterpret_cast<uint2 *>(cp + (row * per_row + hb) * 8) = make_uint2(codes[0], codes[1]);
-  sp[row * per_row + hb] = (uint8_t)sb;
+  *reinterpret_cast<uint2 *>(codes_at) = make_uint2(codes[0], codes[1]);
+  *scale_at = (uint8_t)sb;
 }
 
-__global__ void __launch_bounds__(kRowThreads) relattn_load_fp4_kernel(const Fp4RowArgs a) {
-  const long idx = (long)blockIdx.x * kRowThreads + threadIdx.x;
-  const int per_row = a.Hkv * kFp4Blocks;
-  const long t = idx / per_row;
-  if (t >= a.total_q) return;
-  const int hb = (int)(idx - t * per_row), h = hb / kFp4Blocks;
+__global__ void __launch_bounds__(kRowThreads) relattn_store_fp4_kernel(const __grid_constant__ Fp4RowArgs a) {
+  const BlockPlace x(a.Hkv);
+  if (x.t >= (unsigned)a.total_q) return;
   long row;
-  if (!place_row(a, (int)t, &row)) return;
-  const bool is_v = blockIdx.y != 0;
-  const uint8_t *cp = is_v ? a.kv.v : a.kv.k, *sp = is_v ? a.kv.v_scale : a.kv.k_scale;
-  const float *gp = is_v ? a.kv.v_global : a.kv.k_global;
+  if (!place_row(a, (int)x.t, &row) || row < 0) return;
+  const long per_row = a.Hkv * kFp4Blocks, from = ((long)x.t * per_row + x.hb) * 16, to = row * per_row + x.hb;
+  store_block(reinterpret_cast<const uint4 *>(a.k + from), a.kv.k_global, x.h, const_cast<uint8_t *>(a.kv.k) + to * 8,
+              const_cast<uint8_t *>(a.kv.k_scale) + to);
+  store_block(reinterpret_cast<const uint4 *>(a.v + from), a.kv.v_global, x.h, const_cast<uint8_t *>(a.kv.v) + to * 8,
+              const_cast<uint8_t *>(a.kv.v_scale) + to);
+}
+
+__device__ __forceinline__ void load_block(uint2 c, uint32_t sb, const float *gp, int h, uint4 *dst) {
   const float g = gp ? __ldg(gp + h) : 1.f;
-  uint2 c = make_uint2(0, 0);
-  uint32_t sb = 0;
-  if (row >= 0) {                 // a row outside the cache reads as zero
-    c = __ldg(reinterpret_cast<const uint2 *>(cp + (row * per_row + hb) * 8));
-    sb = __ldg(sp + row * per_row + hb);
-  }
   const uint32_t sh = e4m3x2_to_f16(sb);
   float s;
   asm("cvt.f32.f16 %0, %1;" : "=f"(s) : "h"((uint16_t)sh));
@@ -160,15 +162,32 @@ __global__ void __launch_bounds__(kRowThreads) relattn_load_fp4_kernel(const Fp4
       o[4 * w + i] = pack_bf16x2(lo * s * g, hi * s * g);
     }
   }
-  uint4 *dst = reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(is_v ? a.v : a.k) + (t * per_row + hb) * 16);
   dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
   dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+__global__ void __launch_bounds__(kRowThreads) relattn_load_fp4_kernel(const __grid_constant__ Fp4RowArgs a) {
+  const BlockPlace x(a.Hkv);
+  if (x.t >= (unsigned)a.total_q) return;
+  long row;
+  if (!place_row(a, (int)x.t, &row)) return;
+  const long per_row = a.Hkv * kFp4Blocks, to = ((long)x.t * per_row + x.hb) * 16, from = row * per_row + x.hb;
+  uint2 ck = make_uint2(0, 0), cv = ck;
+  uint32_t sk = 0, sv = 0;
+  if (row >= 0) {                 // a row outside the cache reads as zero
+    ck = __ldg(reinterpret_cast<const uint2 *>(a.kv.k + from * 8));
+    cv = __ldg(reinterpret_cast<const uint2 *>(a.kv.v + from * 8));
+    sk = __ldg(a.kv.k_scale + from);
+    sv = __ldg(a.kv.v_scale + from);
+  }
+  load_block(ck, sk, a.kv.k_global, x.h, reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(a.k) + to));
+  load_block(cv, sv, a.kv.v_global, x.h, reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(a.v) + to));
+}
+
 cudaError_t row_grid(const Fp4RowArgs &a, dim3 *grid) {
-  const long n = ((long)a.total_q * a.Hkv * kFp4Blocks + kRowThreads - 1) / kRowThreads;
-  if (n > 0x7fffffffL) return cudaErrorInvalidValue;
-  *grid = dim3((unsigned)n, 2);
+  const unsigned long n = (unsigned long)a.total_q * a.Hkv * kFp4Blocks;
+  if (n > 0xffffffffUL - kRowThreads) return cudaErrorInvalidValue;
+  *grid = dim3((unsigned)((n + kRowThreads - 1) / kRowThreads));
   return cudaSuccess;
 }
 

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(WT, 3) relattn_key_weights_tiles_kernel(const 
   const long row0 = group_row(p, u, key0);
   uint32_t f[2][8][4];
   if (tok0 < tok1) {
-    load_key_tile(p, u, tile0, tid, WT, [&](int k, int c) { return smem + k * 256 + ((c ^ (k & 7)) << 4); });
+    load_key_tile<WT>(p, u, tile0, tid, [&](int k, int c) { return smem + k * 256 + ((c ^ (k & 7)) << 4); });
     __syncthreads();
     const uint32_t sk = smem_addr(smem) + warp * WK * 256;
 #pragma unroll

@@ -275,7 +275,7 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
   } else if (warp >= 4) {
     // ======================================================== the warpgroups
     const int wg = (warp - 4) >> 2, wq = warp & 3, slot = wq * 32 + lane;   // slot = row of the step
-    load_key_tile(p, u, tile0, tid - 128, KWC, [&](int k, int c) {
+    load_key_tile<KWC>(p, u, tile0, tid - 128, [&](int k, int c) {
       return smem + KW_K + (c >> 3) * 16384 + k * 128 + (((c & 7) ^ (k & 7)) << 4);
     });
     fence_proxy_async_smem();
