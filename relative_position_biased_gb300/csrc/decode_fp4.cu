@@ -61,6 +61,8 @@ constexpr int FS_BYTES = FS_VS + FK * kFp4Blocks;
 constexpr int F_RING = FW * F_STAGES * FS_BYTES;
 static_assert(F_RING >= FW * kFp4Rows * kHeadDim * 4 + 2 * FW * kFp4Rows * 4 + 2 * kFp4Rows * 8, "the merge reuses the ring");
 constexpr float kPShift = 7.f;               // P is held times 2^7
+constexpr float kNone = -3.402823466e38f;    // running maximum before any visible key: finite, so that
+                                             // differences from it are never NaN
 constexpr float kRaise = 8.f;                // the maximum is raised past this excess
 
 constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }
@@ -197,7 +199,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) mref[nt][c] = -INFINITY, l[nt][c] = 0.f;
+    for (int c = 0; c < 2; ++c) mref[nt][c] = kNone, l[nt][c] = 0.f;
 #pragma unroll
     for (int m = 0; m < 8; ++m) acc[m][nt][0] = acc[m][nt][1] = acc[m][nt][2] = acc[m][nt][3] = 0.f;
   }
@@ -256,11 +258,11 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
         if (NT == 1) load_bias(0);
       }
       // ---- S^T = K q^T, two chains of four products
-      float x[NT][4], x2[NT][4];
+      float x[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[nt][i] = x2[nt][i] = 0.f;
+        for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
       {
         const uint32_t kb = st + gr * 16 * kFp4RowBytes + t * 16;
         const uint4 w0 = lds128(kb + g * kFp4RowBytes), w1 = lds128(kb + (g + 8) * kFp4RowBytes);
@@ -280,7 +282,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_f16_16816(x[nt], f0[0], f1[0], f0[1], f1[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
-            mma_f16_16816(x2[nt], f0[2], f1[2], f0[3], f1[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+            mma_f16_16816(x[nt], f0[2], f1[2], f0[3], f1[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
           }
         }
       }
@@ -289,7 +291,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[nt][i] = (x[nt][i] + x2[nt][i]) * coef[nt][i & 1];
+        for (int i = 0; i < 4; ++i) x[nt][i] = x[nt][i] * coef[nt][i & 1];
       if (band) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -322,7 +324,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
             m = fmaxf(m, __shfl_xor_sync(full, m, 8));
             m = fmaxf(m, __shfl_xor_sync(full, m, 16));
             m = fmaxf(m, mref[nt][c]);
-            const float f = m == -INFINITY ? 1.f : fast_exp2(mref[nt][c] - m);
+            const float f = fast_exp2(mref[nt][c] - m);
             mref[nt][c] = m;
             l[nt][c] *= f;
 #pragma unroll
@@ -334,10 +336,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
       for (int nt = 0; nt < NT; ++nt) {
         float e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float m = mref[nt][i & 1];
-          e[i] = fast_exp2(x[nt][i] - (m == -INFINITY ? -kPShift : m - kPShift));
-        }
+        for (int i = 0; i < 4; ++i) e[i] = fast_exp2(x[nt][i] - (mref[nt][i & 1] - kPShift));
         l[nt][0] += e[0] + e[2];
         l[nt][1] += e[1] + e[3];
         // key g x rows 2t, 2t+1  ->  row g x keys 2t, 2t+1
@@ -444,7 +443,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
   const long rows_all = (long)p.a.total_q * p.a.Hq;
   if (tid < kFp4Rows * p.hp) {
     const int hs = tid / kFp4Rows, row = tid % kFp4Rows, h = u.h - warp % p.hp + hs;
-    float m = -INFINITY, z = 0.f, f[FW];
+    float m = kNone, z = 0.f, f[FW];
 #pragma unroll
     for (int w = 0; w < FW; ++w)
       if (w % p.hp == hs) m = fmaxf(m, sm[w * kFp4Rows + row]);
@@ -453,8 +452,8 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
       f[w] = 0.f;
       if (w % p.hp == hs) {
         const float mw = sm[w * kFp4Rows + row], zw = sl[w * kFp4Rows + row];
-        // a warp without a visible key has an empty sum; a NaN sum stays one
-        f[w] = mw == -INFINITY ? (zw == 0.f ? 0.f : 1.f) : fast_exp2(mw - m);
+        // (a warp without a visible key has an empty sum; a NaN sum stays one)
+        f[w] = fast_exp2(mw - m);
         z = fmaf(zw, f[w], z);
       }
     }
@@ -462,7 +461,7 @@ __device__ __forceinline__ void run_piece(const Fp4DecodeArgs &p, const Unit &u,
 #pragma unroll
     for (int w = 0; w < FW; ++w)
       if (w % p.hp == hs) sl[w * kFp4Rows + row] = f[w] * scale;
-    const float lse = z == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) - kPShift + log2f(z)) * kLn2;
+    const float lse = z == 0.f ? -INFINITY : (m - kPShift + log2f(z)) * kLn2;
     if (row < u.nrows) {
       const int rr = u.rb * kFp4Rows + row, tok = u.s.q0 + rr / p.a.group;
       const int head = h * p.a.group + rr % p.a.group;

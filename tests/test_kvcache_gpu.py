@@ -176,7 +176,7 @@ def test_decode(i, splits):
 
 @pytest.mark.parametrize("batch", [65, 513])
 def test_decode_of_many_sequences(batch):
-    """Past 512 sequences every unit has a CTA of its own."""
+    """Past 384 sequences every unit has a CTA of its own."""
     rng = np.random.default_rng(batch)
     c = U.Case((1,) * batch, tuple(int(x) for x in rng.integers(1, 90, batch)), 4, 2, E=64)
     d = U.make(c)
@@ -397,6 +397,30 @@ def test_key_weights(i, kind, decay):
     rpb.key_weights(*args, weights_in=place, decay=decay, out=place, **kw)
     ok()
     assert torch.equal(place[:, torch.from_numpy(held).cuda()], out[:, torch.from_numpy(held).cuda()])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("E,page,window", [(64, 0, 0), (0, 32, 0), (200, 96, 3000)])
+def test_key_weights_of_more_tiles_than_sms(kind, E, page, window):
+    """Every SM takes several tiles of 128 keys, of sequences of all lengths, some
+    without a tile or without a row that sees it."""
+    c = U.Case((20, 0, 17, 40, 1, 33), (5000, 700, 17, 9000, 1, 2049), 6, 6, E=E, r_dim=16 if E else 0, page=page,
+               window=window, base=64.0)
+    assert sum(-(-n // 128) for n in c.k_lens) * c.Hkv > 5 * 152
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    keys = qc["k_values"] if kind == "nvfp4" else d["k"].double().numpy()
+    k = U.device_cache(qc, d) if kind == "nvfp4" else d["k"].cuda()
+    lse = np.zeros((c.Hq, sum(c.q_lens)), np.float32)
+    for b, hq, h, q0, x, mag in U.each_head(c, d, keys):
+        lse[hq, q0:q0 + x.shape[0]] = C.softmax(x)[1]
+    w_in = np.random.default_rng(6).uniform(0, 9, (c.Hkv, d["rows"])).astype(np.float32)
+    out = torch.full((c.Hkv, d["rows"]), 7.0, device="cuda")
+    rpb.key_weights(d["q"].cuda(), k, U.cuda(d["r"]), U.cuda(d["P"]), torch.from_numpy(lse).cuda(), d["cu_q"].cuda(),
+                    d["cu_k"].cuda(), weights_in=torch.from_numpy(w_in).cuda(), decay=0.5, out=out, **U.call_kw(c, d))
+    ok()
+    held = U.check_weights(c, d, keys, lse, w_in, 0.5, out)
+    assert (host(out)[:, ~held] == 7).all()
 
 
 @pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
