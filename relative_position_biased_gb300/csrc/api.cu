@@ -796,6 +796,8 @@ relattn_status relattn_decode_nvfp4(const relattn_params *p, const relattn_kv_nv
   x.row_blocks = plan.row_blocks;
   x.splits = plan.splits;
   x.c_min = plan.c_min;
+  x.tc = plan.tc;
+  x.band_extra = plan.band_extra;
   if (plan.ws_bytes > 0) {
     if (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < plan.ws_bytes) return RELATTN_ERR_WORKSPACE;
     char *ws = static_cast<char *>(p->workspace);

@@ -28,6 +28,14 @@ __device__ __forceinline__ int unit_tiles(const WalkArgs &p, int b, SeqRows *sp,
   return (s.lk - *lo + tile - 1) / tile;
 }
 
+// Tiles before the first one that meets the bias band, where those count more
+// (band_extra > 0).
+__device__ __forceinline__ int plain_tiles(const WalkArgs &p, const SeqRows &s, int lo, int tiles) {
+  if (p.band_extra == 0) return tiles;
+  const int first = s.lk - s.lq - p.a.E + 1 - lo;       // the first key of the band, from lo
+  return min(max(first, 0) / (kWalkTile / p.hp), tiles);
+}
+
 // Row n of the unit's block: its index among all (token, head) rows, and token.
 __device__ __forceinline__ long unit_row(const WalkArgs &p, const Unit &u, int n, int *tok) {
   const int rr = u.rb * kFp4Rows + n;
@@ -55,7 +63,7 @@ __device__ __forceinline__ int last_not_above(const int *v, int n, int x) {
   return lo;
 }
 
-// Running tile counts of the sequences into prefix[0 .. batch] (batch <=
+// Running (weighted) tile counts of the sequences into prefix[0 .. batch] (batch <=
 // kWalkBatch), by a CTA of THREADS; returns the total.  Inconsistent sequences
 // hold no tile and are recorded once.
 template <int THREADS>
@@ -72,6 +80,8 @@ __device__ __forceinline__ int tile_prefix(const WalkArgs &p, int *prefix, int *
       if (n < 0) {
         n = 0;
         if (blockIdx.x == 0) atomicOr(p.a.err, kDevErrSeqlens);
+      } else {
+        n += p.band_extra * (n - plain_tiles(p, s, lo, n));
       }
     }
     int inc = n;

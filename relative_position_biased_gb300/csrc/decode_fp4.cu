@@ -14,9 +14,9 @@
 // and a conversion (two values a lane) runs at about 1.2 warp instructions a
 // clock and SM against 2 for the f16 multiply by the scale and 0.5 for the
 // matrix instruction.  So the kernel is written around few instructions a
-// key, on warp-level matrix instructions fed from registers: the tcgen05 path
-// would need the values in shared memory, 2 bytes each, which costs more than
-// the products.
+// key, on warp-level matrix instructions fed from registers: with few rows the
+// tcgen05 path's way through shared memory, 2 bytes a value, costs more than the
+// products (decode_fp4_tc.cu takes it for many).
 //   - Keys go along the matrix instruction's 16 rows, query rows along its 8
 //     columns: S^T = K q^T, O^T += V^T P^T.  One token of a GQA-8 group fills
 //     it; with 16 rows a unit takes two columns sets.
@@ -624,6 +624,16 @@ cudaError_t launch_main(const Fp4DecodeArgs &p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Rows of a kv head past which the tcgen05 kernel is taken.  It costs the same
+// for 1 and 128 rows; here every 16 rows convert the cache again.  Measured (us,
+// this / that; 2 kv heads, E = 1024), 32, 40 and 128 rows: one sequence of 16384
+// keys 27 / 27, 28 / 27, 40 / 31; of 131072 64 / 43, 71 / 43, 111 / 48; 64
+// of 8192 137 / 155, 177 / 158, 478 / 195.
+constexpr int kTcMinRows = 32;
+// Its tiles that meet the bias band take some seven times as long as the others:
+// 175 us for 72 rows of a million keys and E = 1024, 208 with a weight of four.
+constexpr int kTcBandExtra = 6;
+
 bool two_columns(const KernelArgs &a) { return a.max_q * a.group > 8; }
 
 }  // namespace
@@ -634,16 +644,21 @@ bool two_columns(const KernelArgs &a) { return a.max_q * a.group > 8; }
 // fit the kernel's index types.
 bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want_splits, Fp4DecodePlan *plan) {
   const int rows = a.max_q * a.group;
-  plan->row_blocks = (rows + kFp4Rows - 1) / kFp4Rows;
+  plan->tc = rows > kTcMinRows && !positions;
+  const int block = plan->tc ? kFp4TcRows : kFp4Rows;
+  plan->row_blocks = (rows + block - 1) / block;
   long vis = a.max_k;
   if (a.window > 0 && !positions) vis = std::min<long>(vis, (long)a.window + a.max_q - 1 + FK - 1);
-  plan->hp = a.Hkv % 2 == 0 ? 2 : 1;
+  plan->hp = a.Hkv % 2 == 0 && !plan->tc ? 2 : 1;
   const long tile = kWalkTile / plan->hp;
-  const long U = (vis + tile - 1) / tile;
+  long U = (vis + tile - 1) / tile;
+  const long band = plan->tc && a.E > 0 ? std::min<long>(U, ((long)a.E + a.max_q) / tile + 2) : 0;
+  plan->band_extra = plan->tc && a.E > 0 ? kTcBandExtra : 0;
+  U += plan->band_extra * band;              // (tiles of the band are weighted)
   const long keys = std::min<long>(total_k, (long)a.batch * vis);
   const long heads = (long)(a.Hkv / plan->hp) * plan->row_blocks;
-  const long total = (keys / tile + a.batch) * heads;
-  const long grid = (long)a.sms * ctas_per_sm(two_columns(a) ? 2 : 1);
+  const long total = (keys / tile + a.batch * (1 + plan->band_extra * band)) * heads;
+  const long grid = (long)a.sms * (plan->tc ? 1 : ctas_per_sm(two_columns(a) ? 2 : 1));
   constexpr long kMinTiles = 4;              // a piece's fixed cost is that of a few tiles
   long C = std::max<long>((total + grid - 1) / grid, kMinTiles);
   long splits = want_splits > 0 ? want_splits : U <= C ? 1 : (U + C - 1) / C + 1;
@@ -671,7 +686,8 @@ cudaError_t launch_decode_fp4(const Fp4DecodeArgs &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   cudaError_t e;
-  if (two_columns(p.a)) e = p.key_pos ? launch_main<2, true>(p, stream) : launch_main<2, false>(p, stream);
+  if (p.tc) e = launch_decode_fp4_tc(p, stream);
+  else if (two_columns(p.a)) e = p.key_pos ? launch_main<2, true>(p, stream) : launch_main<2, false>(p, stream);
   else e = p.key_pos ? launch_main<1, true>(p, stream) : launch_main<1, false>(p, stream);
   if (e != cudaSuccess || p.splits == 1) return e;
   cudaLaunchConfig_t cfg = {};

@@ -203,24 +203,28 @@ struct WalkArgs {
   const int32_t *key_pos, *q_pos;
   int hp;                             // kv heads a walking CTA takes (1 or 2)
   int idle;                           // 1: sequences without query rows are walked too
+  int band_extra;                     // a tile that meets the bias band counts as this many more
 };
 constexpr int kWalkTile = 128;        // keys a CTA takes at a time, over its kv heads
 
-// Split-KV decode over the 4-bit cache (decode_fp4.cu).
+// Split-KV decode over the 4-bit cache (decode_fp4.cu, decode_fp4_tc.cu).
 struct Fp4DecodeArgs : WalkArgs {
   Fp4Cache kv;
-  int row_blocks;      // 16-row blocks per (sequence, kv head)
+  int row_blocks;      // row blocks per (sequence, kv head)
   int splits;          // partial slots of a row; 1 = one CTA per unit, no partials
   int c_min;           // least tiles a CTA takes (keeps a unit within its slots)
+  int tc;              // 1: the tcgen05 kernel (decode_fp4_tc.cu)
 };
 struct Fp4DecodePlan {
-  int hp, row_blocks, splits, c_min;
+  int hp, row_blocks, splits, c_min, tc, band_extra;
   size_t lse_offset, rel_offset, ws_bytes;
 };
 constexpr int kFp4Rows = 16;          // query rows of a work unit
+constexpr int kFp4TcRows = 128;       // and of one of the tcgen05 kernel
 constexpr int kFp4PageUnit = 32;      // page sizes are multiples of it
 bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want_splits, Fp4DecodePlan *plan);
 cudaError_t launch_decode_fp4(const Fp4DecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_decode_fp4_tc(const Fp4DecodeArgs &a, cudaStream_t stream);
 
 // Attention weight per key (key_weights.cu): w_out[h][row] = decay w_in[h][row]
 // (0 for the newest Lq keys) + sum over query rows and the group's heads of

@@ -24,11 +24,12 @@ class Case:
     page: int = 0
     positions: bool = False
     factors: bool = True
+    sign: float = 1.0        # of the logit scale
     seed: int = 0
 
     @property
     def alpha(self):
-        return 1 / np.sqrt(128)
+        return self.sign * (1 / np.sqrt(128))
 
 
 def rows_of(lens, page, seed):

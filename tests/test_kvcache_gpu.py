@@ -161,6 +161,12 @@ DECODE = [
     U.Case((1, 1, 1), (600, 65, 2050), 16, 2, positions=True, base=64.0),
     U.Case((3, 9), (600, 65), 4, 2, positions=True, E=40, page=32),
     U.Case((1, 2), (900, 300), 8, 1, positions=True, window=150),
+    # more than 32 rows of a kv head
+    U.Case((16, 9), (1700, 300), 32, 2, E=300, r_dim=64, base=64.0),           # 256: two blocks of rows
+    U.Case((7, 16, 0, 1), (900, 16, 5, 2050), 24, 2, page=32, window=130, E=64),
+    U.Case((3,), (20000,), 16, 1, E=1024, r_dim=16),
+    U.Case((5, 16), (129, 400), 8, 1, E=0, r_dim=0, window=1, factors=False),
+    U.Case((9, 11, 12), (640, 96, 4097), 16, 2, E=1500, r_dim=8, page=96, sign=-1.0),
 ]
 
 
@@ -185,10 +191,11 @@ def test_decode_of_many_sequences(batch):
     U.check_decode(c, d, qc["k_values"], qc["v_values"], out, lse)
 
 
-def test_decode_with_large_and_tiny_queries():
+@pytest.mark.parametrize("q_len", [1, 5])
+def test_decode_with_large_and_tiny_queries(q_len):
     """Rows of far apart magnitudes in one unit, and a logit range that moves the
     running maximum by hundreds."""
-    c = U.Case((1,), (900,), 8, 1, E=64)
+    c = U.Case((q_len,), (900,), 8, 1, E=64)
     d = U.make(c)
     q = d["q"].float()
     q *= torch.tensor([1e-30, 1e-4, 0.0, 1.0, 30.0, 300.0, 3.0, 1e-38])[None, :, None]
@@ -219,9 +226,10 @@ def test_rows_that_see_no_key_and_rows_of_no_sequence():
 
 
 @pytest.mark.parametrize("window", [0, 40])
-def test_nan_in_masked_places_stays_there(window):
+@pytest.mark.parametrize("Hq", [1, 3, 4])                # up to 9, 27 and 36 rows
+def test_nan_in_masked_places_stays_there(window, Hq):
     """NaN scales in rows that only some query rows see: the others are clean."""
-    c = U.Case((9, 2), (300, 150), 4, 1, window=window, E=64)
+    c = U.Case((9, 2), (300, 150), Hq, 1, window=window, E=64)
     d = U.make(c)
     qc = U.quantized(c, d)
     bad = [int(d["where"][0][295]), int(d["where"][1][149])]    # seen by the last rows only
@@ -250,14 +258,15 @@ def test_nan_in_masked_places_stays_there(window):
                 assert abs(lse[hq, q0 + r] - z[r]) < 1e-3
 
 
-def test_one_nan_value_reaches_its_own_dims_only():
-    c = U.Case((9,), (300,), 4, 1, E=0, r_dim=0)
+@pytest.mark.parametrize("Hq", [1, 3, 4])
+def test_one_nan_value_reaches_its_own_dims_only(Hq):
+    c = U.Case((9,), (300,), Hq, 1, E=0, r_dim=0)
     d = U.make(c)
     qc = U.quantized(c, d)
     qc["v_scale"][295, 0, 3] = 0x7F                     # dims 48 .. 63 of a key that rows 4 .. 8 see
     out, lse = run_decode(c, d, qc)
     nan = np.isnan(host(out.float()))
-    want = np.zeros((9, 4, 128), bool)
+    want = np.zeros((9, Hq, 128), bool)
     want[4:, :, 48:64] = True
     np.testing.assert_array_equal(nan, want)
     assert torch.isfinite(lse).all()
