@@ -659,9 +659,12 @@ bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want
   const long heads = (long)(a.Hkv / plan->hp) * plan->row_blocks;
   const long total = (keys / tile + a.batch * (1 + plan->band_extra * band)) * heads;
   const long grid = (long)a.sms * (plan->tc ? 1 : ctas_per_sm(two_columns(a) ? 2 : 1));
-  constexpr long kMinTiles = 4;              // a piece's fixed cost is that of a few tiles
+  // A piece's fixed cost is that of a few tiles, and partials cost a second
+  // kernel: up to 8 tiles stay whole (one sequence of 8 tiles, caches cold: 18.6 us
+  // whole, 22.7 in pieces of two; 12 tiles 25.7 and 24.7).
+  const long kMinTiles = plan->tc ? 4 : 2, kWhole = plan->tc ? 0 : 8;
   long C = std::max<long>((total + grid - 1) / grid, kMinTiles);
-  long splits = want_splits > 0 ? want_splits : U <= C ? 1 : (U + C - 1) / C + 1;
+  long splits = want_splits > 0 ? want_splits : U <= std::max(C, kWhole) ? 1 : (U + C - 1) / C + 1;
   if (a.batch > kWalkBatch) splits = 1;
   if (splits > 1) splits = std::min<long>(splits, U + 1);
   plan->splits = (int)splits;
