@@ -31,9 +31,20 @@ __device__ __forceinline__ int unit_tiles(const WalkArgs &p, int b, SeqRows *sp,
 // Tiles before the first one that meets the bias band, where those count more
 // (band_extra > 0).
 __device__ __forceinline__ int plain_tiles(const WalkArgs &p, const SeqRows &s, int lo, int tiles) {
-  if (p.band_extra == 0) return tiles;
+  if (p.band_extra == 0 || s.lq == 0) return tiles;
   const int first = s.lk - s.lq - p.a.E + 1 - lo;       // the first key of the band, from lo
   return min(max(first, 0) / (kWalkTile / p.hp), tiles);
+}
+
+// A unit's tiles with their weights: a tile of the band counts 1 + band_extra
+// times and belongs to the range that holds its first.
+struct Weighted {
+  int plain, extra, total;
+  __device__ __forceinline__ int tile(int v) const { return v <= plain ? v : plain + (v - plain + extra) / (extra + 1); }
+};
+__device__ __forceinline__ Weighted weighted_tiles(const WalkArgs &p, const SeqRows &s, int lo, int tiles) {
+  const int plain = plain_tiles(p, s, lo, tiles);
+  return {plain, p.band_extra, tiles + p.band_extra * (tiles - plain)};
 }
 
 // Row n of the unit's block: its index among all (token, head) rows, and token.

@@ -524,18 +524,21 @@ __global__ void __launch_bounds__(FT, ctas_per_sm(NT)) relattn_decode_fp4_kernel
     const unsigned hr = x / per;
     const int xb = (int)(x - hr * per);
     u.b = last_not_above(prefix, p.a.batch, xb);   // it holds tile xb
-    const int tiles = unit_tiles(p, u.b, &u.s, &u.lo), t0 = xb - prefix[u.b];
-    const int n = (int)min((unsigned)(tiles - t0), end - x);
+    const int real = unit_tiles(p, u.b, &u.s, &u.lo), v0 = xb - prefix[u.b];
+    const Weighted w = weighted_tiles(p, u.s, u.lo, real);
+    const int n = (int)min((unsigned)(w.total - v0), end - x);
     place((int)hr);
     if (u.nrows > 0) {
       const unsigned ustart = hr * per + prefix[u.b], first = ustart / C;
-      run_piece<NT, POS>(p, u, t0, n, (int)(blockIdx.x - first), smem);
-      if (t0 == 0) {                         // mark the slots that no piece fills
-        const int used = (int)((ustart + tiles - 1) / C - first) + 1;
+      const int t0 = w.tile(v0), tiles = w.tile(v0 + n) - t0, slot = (int)(blockIdx.x - first);
+      if (tiles > 0) run_piece<NT, POS>(p, u, t0, tiles, slot, smem);
+      // mark slots without a piece: the first piece those past the last, a range within a tile its own
+      const int from = tiles > 0 ? (int)((ustart + w.total - 1) / C - first) + 1 : slot, to = tiles > 0 ? p.splits : slot + 1;
+      if (t0 == 0 || tiles == 0) {
         for (int i = tid; i < u.nrows * p.hp; i += FT) {
           const int hs = i / u.nrows, rr = u.rb * kFp4Rows + i % u.nrows;
           const long grow = (long)(u.s.q0 + rr / p.a.group) * p.a.Hq + (u.h - hsub + hs) * p.a.group + rr % p.a.group;
-          for (int k = used; k < p.splits; ++k) p.a.lse_part[(long)k * p.a.total_q * p.a.Hq + grow] = -INFINITY;
+          for (int k = from; k < to; ++k) p.a.lse_part[(long)k * p.a.total_q * p.a.Hq + grow] = -INFINITY;
         }
       }
     }
@@ -633,6 +636,9 @@ constexpr int kTcMinRows = 32;
 // Its tiles that meet the bias band take some seven times as long as the others:
 // 175 us for 72 rows of a million keys and E = 1024, 208 with a weight of four.
 constexpr int kTcBandExtra = 6;
+// And of this kernel about twice as long (64 sequences of 1 to 32 thousand keys:
+// 97 us, 104 without weights, 100 with three times).
+constexpr int kBandExtra = 1;
 
 bool two_columns(const KernelArgs &a) { return a.max_q * a.group > 8; }
 
@@ -652,8 +658,8 @@ bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want
   plan->hp = a.Hkv % 2 == 0 && !plan->tc ? 2 : 1;
   const long tile = kWalkTile / plan->hp;
   long U = (vis + tile - 1) / tile;
-  const long band = plan->tc && a.E > 0 ? std::min<long>(U, ((long)a.E + a.max_q) / tile + 2) : 0;
-  plan->band_extra = plan->tc && a.E > 0 ? kTcBandExtra : 0;
+  const long band = a.E > 0 ? std::min<long>(U, ((long)a.E + a.max_q) / tile + 2) : 0;
+  plan->band_extra = a.E == 0 ? 0 : plan->tc ? kTcBandExtra : kBandExtra;
   U += plan->band_extra * band;              // (tiles of the band are weighted)
   const long keys = std::min<long>(total_k, (long)a.batch * vis);
   const long heads = (long)(a.Hkv / plan->hp) * plan->row_blocks;

@@ -119,16 +119,14 @@ __device__ __forceinline__ void for_pieces(const Fp4DecodeArgs &p, const int *pr
     const unsigned hr = x / per;
     const int xb = (int)(x - hr * per);
     u.b = last_not_above(prefix, p.a.batch, xb);   // it holds tile xb
-    const int real = unit_tiles(p, u.b, &u.s, &u.lo), plain = plain_tiles(p, u.s, u.lo, real);
-    const int tiles = real + p.band_extra * (real - plain), v0 = xb - prefix[u.b];
-    const int n = (int)min((unsigned)(tiles - v0), end - x);
-    // a tile of the band counts 1 + band_extra times, and is its first time's
-    auto tile_of = [&](int v) { return v <= plain ? v : plain + (v - plain + p.band_extra) / (p.band_extra + 1); };
+    const int real = unit_tiles(p, u.b, &u.s, &u.lo), v0 = xb - prefix[u.b];
+    const Weighted w = weighted_tiles(p, u.s, u.lo, real);
+    const int n = (int)min((unsigned)(w.total - v0), end - x);
     place((int)hr);
     if (u.nrows > 0) {
       const unsigned ustart = hr * per + prefix[u.b], first = ustart / C;
-      const int t0 = tile_of(v0);
-      if (!body(u, t0, tile_of(v0 + n) - t0, (int)(blockIdx.x - first), (int)((ustart + tiles - 1) / C - first) + 1)) return;
+      const int t0 = w.tile(v0);
+      if (!body(u, t0, w.tile(v0 + n) - t0, (int)(blockIdx.x - first), (int)((ustart + w.total - 1) / C - first) + 1)) return;
     }
     x += n;
   }

@@ -312,11 +312,12 @@ __global__ void __launch_bounds__(WT, rows_ctas(NT, FP4)) relattn_key_weights_ro
     const int hg = (int)(x / per), xb = (int)(x - hg * per);
     u.h = hg * p.hp + (int)(threadIdx.x >> 5) % p.hp;
     u.b = last_not_above(prefix, p.a.batch, xb);
-    const int tiles = unit_tiles(p, u.b, &u.s, &u.lo), t0 = xb - prefix[u.b];
-    const int n = (int)min((long)(tiles - t0), end - x);
+    const int real = unit_tiles(p, u.b, &u.s, &u.lo), v0 = xb - prefix[u.b];
+    const Weighted w = weighted_tiles(p, u.s, u.lo, real);
+    const int n = (int)min((long)(w.total - v0), end - x), t0 = w.tile(v0), tiles = w.tile(v0 + n) - t0;
     u.nrows = u.s.lq * p.a.group;
     u.qbase = first_query_pos(u.s, p.q_pos, u.b);
-    weigh_piece<NT, POS, FP4>(p, u, t0, n, smem);
+    if (tiles > 0) weigh_piece<NT, POS, FP4>(p, u, t0, tiles, smem);
     x += n;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -613,6 +614,8 @@ cudaError_t launch_tiles(const KeyWeightArgs &p, cudaLaunchConfig_t cfg) {
 
 // A call is walked (few rows) or takes tiles of keys; with positions, and when
 // walked, the bias comes from R in the workspace, else from the bias table.
+constexpr int kBandExtra = 1;                // a walked tile with a bias counts twice (64 sequences, 1 to 32 thousand
+                                            // keys: 69 us; 75 counted once, 72 three times)
 bool key_weights_walked(const KernelArgs &a) { return (long)a.max_q * a.group <= kFp4Rows && a.batch <= kWalkBatch; }
 
 size_t key_weights_workspace(const KernelArgs &a, bool positions) {
@@ -627,6 +630,7 @@ cudaError_t launch_key_weights(const KeyWeightArgs &args, cudaStream_t stream) {
   p.table = nullptr;
   p.hp = walked && p.a.Hkv % 2 == 0 ? 2 : 1;   // two heads share their rows' lines
   p.idle = 1;                                 // their keys' weights decay
+  p.band_extra = walked && p.a.E > 0 ? kBandExtra : 0;
   if (p.a.E > 0) {
     cudaError_t e;
     if (pos || walked) {
