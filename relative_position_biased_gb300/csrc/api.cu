@@ -422,8 +422,14 @@ KernelArgs key_weight_sizes(const relattn_params &f) {
   return a;
 }
 
-size_t evict_bytes(const relattn_evict_params &p) {
+size_t evict_rows_bytes(const relattn_evict_params &p) {
   return (size_t)p.total_keep * ((size_t)p.num_heads_kv + 1) * sizeof(int32_t);
+}
+// the kept keys' rows, then a wide selection's histograms
+size_t evict_wide_at(const relattn_evict_params &p) { return (evict_rows_bytes(p) + 255) / 256 * 256; }
+size_t evict_bytes(const relattn_evict_params &p) {
+  const size_t wide = evict_wide_bytes(p.batch, p.num_heads_kv, p.max_seqlen_k);
+  return wide > 0 ? evict_wide_at(p) + wide : evict_rows_bytes(p);
 }
 
 relattn_status validate_evict(const relattn_evict_params *p, EvictArgs *a) {
@@ -480,8 +486,10 @@ relattn_status validate_evict(const relattn_evict_params *p, EvictArgs *a) {
   a->pos_out = p->key_pos_out;
   a->src_row = static_cast<int32_t *>(p->workspace);
   a->dst_row = a->src_row + (size_t)p->total_keep * p->num_heads_kv;
+  if (evict_wide_bytes(p->batch, p->num_heads_kv, p->max_seqlen_k) > 0)
+    a->wide = reinterpret_cast<unsigned *>(static_cast<char *>(p->workspace) + evict_wide_at(*p));
   a->planes = n;
-  return device_state(nullptr, &a->err, nullptr);
+  return device_state(nullptr, &a->err, &a->sms);
 }
 
 }  // namespace

@@ -9,7 +9,9 @@
 // the top) over distributed shared memory find the exact smallest kept key
 // and how many of its equals are kept; a last pass ranks the kept keys by
 // ballots and writes their rows.  Nothing is sorted, and every count is an
-// integer, so the result does not depend on any order.  The keys are read
+// integer, so the result does not depend on any order.  Few long sequences are
+// selected by all SMs instead (a million keys of two heads: 128 us of the call
+// to 81): the same passes, with the counts in global memory.  The keys are read
 // once where a CTA's share fits its shared memory, else from L2 in each pass.
 // Move: the kept rows' bytes, any number of planes (codes, scales, bf16 rows);
 // bound by memory.
@@ -29,6 +31,7 @@ constexpr int EBINS = 2048;
 constexpr int ECOPY = 4;                     // copies of a histogram: equal digits of a warp collide less
 constexpr int kMaxCluster = 16;              // CTAs of a cluster (above 8: opted into)
 constexpr int kCacheKeys = 46 * 1024;        // keys of a CTA that shared memory holds
+constexpr int kWideUnits = 8, kWideKeys = 32 * 1024;         // (evict_wide_bytes)
 
 // Order-preserving bits: larger weight, larger key; -0 as 0, NaN below -inf.
 __device__ __forceinline__ uint32_t rank_bits(float w) {
@@ -100,8 +103,34 @@ __device__ __forceinline__ void load_keys(const EvictArgs &a, const Segment &s, 
   for (int i = 0; i < EB; ++i) key[i] = rank_bits(w[i]);
 }
 
+// A wide selection: words of workspace per (sequence, kv head): the barrier's
+// counter, three passes' histograms, two counts of every CTA.
+constexpr int kWideHist = 32, kWideCounts = kWideHist + 3 * EBINS, kWideCtas = 512, kWideWords = kWideCounts + 2 * kWideCtas;
+
+// All CTAs of a (sequence, kv head), which a cooperative launch keeps resident
+// together; false after a timeout.
+__device__ __forceinline__ bool unit_barrier(unsigned *counter, unsigned target, int *err, int *failed) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(counter, 1u);
+    const long long t0 = clock64();
+    int bad = 0;
+    while (*reinterpret_cast<volatile unsigned *>(counter) < target)
+      if (clock64() - t0 > 2000000000ll) {
+        record_timeout(err, 60);
+        bad = 1;
+        break;
+      }
+    __threadfence();
+    *failed = bad;
+  }
+  __syncthreads();
+  return *failed == 0;
+}
+
 // Dynamic shared memory: the CTA's keys when CACHED.
-template <int ET, bool CACHED>
+template <int ET, bool CACHED, bool WIDE>
 __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int EW = ET / 32, ETILE = ET * EB, EPT = EBINS / ET;      // EPT: bins of a thread
   extern __shared__ uint32_t cache[];
@@ -111,10 +140,20 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
   __shared__ int counts[2];                  // kept above the border / equal to it, in this CTA's keys
   __shared__ int wabove[EW], wequal[EW];
   __shared__ unsigned total[EBINS];          // the cluster's counts of the pass
+  __shared__ int failed;
   cg::cluster_group cl = cg::this_cluster();
-  const int cs = cl.num_blocks(), rank = cl.block_rank();
+  const int cs = WIDE ? a.ctas : (int)cl.num_blocks(), rank = WIDE ? (int)(blockIdx.x % cs) : (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Segment s = segment(a, blockIdx.x / cs);
+  unsigned *wide = WIDE ? a.wide + (long)(blockIdx.x / cs) * kWideWords : nullptr;
+  unsigned arrivals = 0;
+  auto meet = [&]() {                        // the CTAs of the (sequence, kv head)
+    if (!WIDE) {
+      cl.sync();
+      return true;
+    }
+    return unit_barrier(wide, arrivals += cs, a.err, &failed);
+  };
   const unsigned full = 0xffffffffu;
   if (!s.ok) {                               // the same for every CTA of the cluster
     if (rank == 0 && tid == 0) atomicOr(a.err, kDevErrSeqlens);
@@ -165,20 +204,34 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
           if (in) atomicAdd(&hist[((key[i] >> shift) & (bins - 1)) * ECOPY + (lane & (ECOPY - 1))], 1u);
         }
       }
-      cl.sync();
-      // every CTA adds one slice of the bins over the cluster and hands the
-      // sums to all
-      const int slice = bins / cs;
-      for (int i = tid; i < slice; i += ET) {
-        const int bin = rank * slice + i;
-        unsigned c = 0;
-        for (int r = 0; r < cs; ++r) {
-          const uint4 x = reinterpret_cast<const uint4 *>(cl.map_shared_rank(hist, r))[bin];
-          c += x.x + x.y + x.z + x.w;
+      const unsigned *sums = total;
+      if (WIDE) {
+        // the CTAs' counts meet in global memory (integers: in any order)
+        unsigned *g = wide + kWideHist + pass * EBINS;
+        sums = g;
+        __syncthreads();
+        for (int i = tid; i < bins; i += ET) {
+          const uint4 x = reinterpret_cast<const uint4 *>(hist)[i];
+          const unsigned c = x.x + x.y + x.z + x.w;
+          if (c) atomicAdd(g + i, c);
         }
-        for (int r = 0; r < cs; ++r) cl.map_shared_rank(total, r)[bin] = c;
+        if (!meet()) return;
+      } else {
+        cl.sync();
+        // every CTA adds one slice of the bins over the cluster and hands the
+        // sums to all
+        const int slice = bins / cs;
+        for (int i = tid; i < slice; i += ET) {
+          const int bin = rank * slice + i;
+          unsigned c = 0;
+          for (int r = 0; r < cs; ++r) {
+            const uint4 x = reinterpret_cast<const uint4 *>(cl.map_shared_rank(hist, r))[bin];
+            c += x.x + x.y + x.z + x.w;
+          }
+          for (int r = 0; r < cs; ++r) cl.map_shared_rank(total, r)[bin] = c;
+        }
+        cl.sync();
       }
-      cl.sync();
       // thread t holds EPT bins, from the top
       unsigned c[EPT], own[EPT], mine = 0, lmine = 0;
 #pragma unroll
@@ -187,7 +240,7 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
         c[j] = own[j] = 0;
         if (bin >= 0) {
           const uint4 x = reinterpret_cast<const uint4 *>(hist)[bin];
-          c[j] = total[bin];
+          c[j] = WIDE ? __ldcg(sums + bin) : sums[bin];
           own[j] = x.x + x.y + x.z + x.w;
         }
         mine += c[j];
@@ -231,12 +284,21 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
   if (all) na = overlap(m0, m1);
   na += overlap(0, m0) + overlap(m1, s.n);
   if (!choose) ne = 0;
-  if (tid == 0) counts[0] = na, counts[1] = ne;
-  cl.sync();
   int above = 0, equal = 0;                  // before the tile at hand
-  for (int r = 0; r < rank; ++r) {
-    above += cl.map_shared_rank(counts, r)[0];
-    equal += cl.map_shared_rank(counts, r)[1];
+  if (WIDE) {
+    int *all_counts = reinterpret_cast<int *>(wide + kWideCounts);
+    if (tid == 0) all_counts[2 * rank] = na, all_counts[2 * rank + 1] = ne;
+    if (!meet()) return;
+    for (int r = lane; r < rank; r += 32) above += __ldcg(all_counts + 2 * r), equal += __ldcg(all_counts + 2 * r + 1);
+    above = __reduce_add_sync(full, above);
+    equal = __reduce_add_sync(full, equal);
+  } else {
+    if (tid == 0) counts[0] = na, counts[1] = ne;
+    cl.sync();
+    for (int r = 0; r < rank; ++r) {
+      above += cl.map_shared_rank(counts, r)[0];
+      equal += cl.map_shared_rank(counts, r)[1];
+    }
   }
   static_assert(EBINS * ECOPY >= ETILE, "a tile's kept keys fit the histograms' place");
   int *list = reinterpret_cast<int *>(hist);
@@ -296,7 +358,7 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
       }
     }
   }
-  cl.sync();                                 // no CTA leaves while another reads its counts
+  if (!WIDE) cl.sync();                      // no CTA leaves while another reads its counts
 }
 
 // Copies the kept rows of one plane (blockIdx.y) and head, in units of 16 bytes
@@ -364,15 +426,15 @@ __global__ void __launch_bounds__(MT) relattn_evict_move_kernel(const __grid_con
   else move_rows<unsigned char>(from, to, pitch, bytes, n, src, dst);
 }
 
-template <int ET, bool CACHED>
+template <int ET, bool CACHED, bool WIDE>
 cudaError_t launch_select(const EvictArgs &a, long units, int cs, int smem, cudaStream_t stream) {
-  auto *kernel = relattn_evict_select_kernel<ET, CACHED>;
+  auto *kernel = relattn_evict_select_kernel<ET, CACHED, WIDE>;
   static std::atomic<bool> done[kMaxDevicesAttr], wide[kMaxDevicesAttr];
   if (CACHED) {
     const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), kCacheKeys * 4, done);
     if (e != cudaSuccess) return e;
   }
-  if (cs > 8) {
+  if (!WIDE && cs > 8) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return cudaErrorInvalidDevice;
     if (!wide[dev].load(std::memory_order_acquire)) {
@@ -387,10 +449,15 @@ cudaError_t launch_select(const EvictArgs &a, long units, int cs, int smem, cuda
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cs;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
+  if (WIDE) {
+    attr.id = cudaLaunchAttributeCooperative;          // its CTAs wait for one another
+    attr.val.cooperative = 1;
+  } else {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cs;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+  }
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
@@ -398,7 +465,19 @@ cudaError_t launch_select(const EvictArgs &a, long units, int cs, int smem, cuda
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream) {
+// Few long sequences: clusters would leave most SMs idle, so all of them work
+// on the selection, in a cooperative launch, and meet in global memory.
+// Measured (us, this / clusters, of the whole call with half of the keys kept
+// and one plane of 8 bytes): one head of 8 thousand keys 44 / 36, of 33 thousand 42 /
+// 46, of a million 52 / 106; eight heads of 33 thousand 36 / 46, of a million 120 /
+// 214.
+size_t evict_wide_bytes(int batch, int Hkv, int max_k) {
+  const long units = (long)batch * Hkv;
+  return units <= kWideUnits && max_k >= kWideKeys ? (size_t)units * kWideWords * sizeof(unsigned) : 0;
+}
+
+cudaError_t launch_evict(const EvictArgs &args, cudaStream_t stream) {
+  EvictArgs a = args;
   // CTAs per (sequence, kv head): one per 16K keys, up to 16; of 512 threads
   // while 16K keys are enough, else of 1024
   int cs = 1;
@@ -406,9 +485,19 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream) {
   const long units = (long)a.batch * a.Hkv;
   if (units * cs > 0x7fffffffL) return cudaErrorInvalidValue;
   const long chunk = ((a.max_k + cs - 1) / cs + 31) & ~31L;
-  cudaError_t e = chunk <= 16384       ? launch_select<512, true>(a, units, cs, (int)chunk * 4, stream)
-                  : chunk <= kCacheKeys ? launch_select<1024, true>(a, units, cs, (int)chunk * 4, stream)
-                                        : launch_select<1024, false>(a, units, cs, 0, stream);
+  cudaError_t e;
+  if (a.wide) {
+    a.ctas = std::min(kWideCtas, a.sms / (int)units);
+    const long own = ((a.max_k + a.ctas - 1) / a.ctas + 31) & ~31L;
+    e = cudaMemsetAsync(a.wide, 0, (size_t)units * kWideWords * sizeof(unsigned), stream);
+    if (e != cudaSuccess) return e;
+    e = own <= kCacheKeys ? launch_select<1024, true, true>(a, units, a.ctas, (int)own * 4, stream)
+                          : launch_select<1024, false, true>(a, units, a.ctas, 0, stream);
+  } else {
+    e = chunk <= 16384       ? launch_select<512, true, false>(a, units, cs, (int)chunk * 4, stream)
+        : chunk <= kCacheKeys ? launch_select<1024, true, false>(a, units, cs, (int)chunk * 4, stream)
+                              : launch_select<1024, false, false>(a, units, cs, 0, stream);
+  }
   if (e != cudaSuccess) return e;
   if (a.planes == 0 || a.total_keep == 0) return cudaSuccess;
   MoveArgs m = {};

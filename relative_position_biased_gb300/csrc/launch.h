@@ -262,8 +262,12 @@ struct EvictArgs {
   const void *from[kMaxPlanes];  // [src.rows, Hkv, bytes]
   void *to[kMaxPlanes];          // [dst.rows, Hkv, bytes]
   int bytes[kMaxPlanes];
+  unsigned *wide;                // workspace of a wide selection (evict_wide_bytes), zeroed by the launcher
+  int ctas;                      // CTAs per (sequence, kv head) in a wide selection (set by the launcher)
+  int sms;
   int *err;
 };
+size_t evict_wide_bytes(int batch, int Hkv, int max_k);       // 0: one cluster per (sequence, kv head)
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream);
 
 }  // namespace relattn

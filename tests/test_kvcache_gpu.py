@@ -488,6 +488,11 @@ def _planes(rows, Hkv, kinds, seed=0):
     ((300001, 40), (290000, 7), 5, 1, (16, 1), 0, 0, True),                 # sixteen
     ((800000,), (1234,), 100, 3, (8,), 0, 0, False),                        # more keys than shared memory holds
     ((790000, 100), (400000, 99), 0, 0, (4,), 64, 32, True),
+    # and of more (sequence, head) pairs than the selection by all SMs takes
+    ((150001, 20, 0, 9, 1), (75000, 3, 0, 9, 1), 1024, 4, (8,), 0, 0, True),
+    ((300001, 40, 33, 8, 7), (290000, 7, 33, 1, 2), 5, 1, (16, 1), 32, 0, True),
+    ((800000, 5, 6, 0, 2), (1234, 5, 1, 0, 2), 100, 3, (8,), 0, 0, False),
+    ((1900000, 70000), (3000, 69999), 10, 4, (4,), 0, 0, True),             # more than all SMs' shared memory holds
 ])
 def test_evict(k_lens, keep, recent, sink, kinds, page, page_to, ties):
     Hkv = 2
