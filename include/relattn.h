@@ -294,8 +294,9 @@ typedef struct relattn_positions {
  * not quantised; products are exact, sums fp32, the softmax weights f16.  A
  * row that sees no key gives out = 0, lse = -inf.  positions and pages may be
  * NULL.  Any max_seqlen_q <= 16, group, r_dim <= 64 and rel_extent; speed is
- * best with at most 8 rows per kv head (max_seqlen_q x group), 16 rows share
- * one pass over the keys and more take a pass per 16.  num_splits: 0 chooses,
+ * best with at most 8 rows per kv head (max_seqlen_q x group); 16 rows share
+ * one pass over the keys, and past 32 rows 128 do (with positions every 16
+ * take one of their own).  num_splits: 0 chooses,
  * n > 0 allows at most n partials per row.  Rows of no sequence keep their out
  * and lse.  The workspace size depends on params and on whether positions are
  * given.
@@ -314,15 +315,19 @@ relattn_status relattn_decode_nvfp4_workspace_size(const relattn_params *params,
  * The newest Lq_b keys of a sequence start from 0 (their rows were just
  * written); weights_in = NULL or decay = 0 starts every key from 0 and reads
  * nothing.  Rows that hold no key keep their weights_out.  A query row with
- * lse = -inf gives nothing; a call with total_q = 0 writes nothing.  fp32 throughout.  Which rows vote is the
- * caller's choice: a decode step's, all rows of a prompt, or (cu_seqlens_q
- * over the last n rows of q and lse) an observation window.
+ * lse = -inf gives nothing; a call with total_q = 0 writes nothing.  Sums are
+ * fp32.  Which rows vote is the caller's choice: a decode step's, all rows of a
+ * prompt, or (cu_seqlens_q over the last n rows of q and lse) an observation
+ * window.  A cache row belongs to one sequence: a page that two block tables
+ * share would receive the weights of either.
  * fwd: q, k, r, P, lengths, masks and lse (an input) as in relattn_prefill;
  * v, out, workspace and num_splits are ignored.  cache = NULL reads the keys
  * from fwd.k (bf16 rows, contiguous or paged).  weights_out may equal
  * weights_in and must not overlap anything else.  workspace:
  * relattn_key_weights_workspace_size() bytes, 16-byte aligned (with a bias: R
- * = r . P, fp32 total_q x num_heads_q x rel_extent).
+ * = r . P, fp32 total_q x num_heads_q x rel_extent, where positions are given
+ * or at most 16 rows per kv head vote in a batch of at most 384; else a table
+ * of (rel_extent + 320) x 64 bf16).
  */
 typedef struct relattn_key_weights_params {
   relattn_params fwd;
@@ -350,7 +355,8 @@ relattn_status relattn_key_weights_workspace_size(const relattn_key_weights_para
  * (key_pos, or their indices when it is NULL) and weights_out their weights;
  * either may be NULL.  rows / rows_keep: rows of the source / new arrays
  * (< 2^31); pages / pages_keep: NULL for contiguous rows cu_seqlens_k[b] + p /
- * cu_seqlens_keep[b] + j.  Sources and destinations must not overlap.
+ * cu_seqlens_keep[b] + j.  Sources and destinations must not overlap, and no
+ * page of pages_keep may be listed twice.
  * With no log-scale and every row's bias and window inside the newest
  * `recent` keys, the other decodes read the new bf16 or MXFP8 cache as it is;
  * otherwise pass the positions to relattn_decode_nvfp4.

@@ -267,10 +267,26 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + KW_SLOT);
+  // A wait that may last a tile: it gives up a second after the issuer's last step.
+  auto wait_long = [&](int b, uint32_t parity, int site) {
+    long long t0 = clock64();
+    int seen = *begun;
+    while (!mbar_try_wait(bar(b), parity, 2000u)) {
+      if (*abort_flag) return false;
+      if (*begun != seen) {
+        seen = *begun;
+        t0 = clock64();
+      } else if (clock64() - t0 > 2000000000ll) {
+        *abort_flag = site;
+        return false;
+      }
+    }
+    return true;
+  };
   // The k-th tile of this CTA, by a whole warp, or by one lane; false: there is none.
   auto next_tile = [&](int k, bool one_lane, Tile &t) {
     const int s = k % UST;
-    bool got = mbar_wait_suspend(bar(BU_FULL + s), (k / UST) & 1, abort_flag, 30);
+    bool got = wait_long(BU_FULL + s, (k / UST) & 1, 30);
     if (!one_lane) got = __all_sync(0xffffffffu, got);
     if (!got) return false;
     const uint4 *src = reinterpret_cast<const uint4 *>(smem + KW_UNIT + 64 * s);
@@ -376,15 +392,20 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
       int asked = 0, steps = 0;
       for (int k = 0; more; ++k) {
         const int s = k % UST;
-        if (k >= UST && !mbar_wait_suspend(bar(BU_EMPTY + s), ((k / UST) - 1) & 1, abort_flag, 31)) break;
+        if (k >= UST && !wait_long(BU_EMPTY + s, ((k / UST) - 1) & 1, 31)) break;
         Tile t = {};
         do {
           if (!own) {
             // a tile taken early is one that an idler CTA cannot take
-            const long long t0 = clock64();
-            while (steps - *begun > kStepsAhead && !*abort_flag) {
+            long long t0 = clock64();
+            for (int seen = *begun; steps - *begun > kStepsAhead && !*abort_flag;) {
               __nanosleep(100);
-              if (clock64() - t0 > 2000000000ll) *abort_flag = 36;
+              if (*begun != seen) {
+                seen = *begun;
+                t0 = clock64();
+              } else if (clock64() - t0 > 2000000000ll) {
+                *abort_flag = 36;
+              }
             }
             if (*abort_flag) {
               more = false;
@@ -416,7 +437,7 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
       for (int k = 0; next_tile(k, true, t); ++k) {
         if (t.steps == 0 || !p.k) continue;
         const int ks = kt % KST;
-        if (kt >= KST && !mbar_wait_suspend(bar(BK_EMPTY + ks), ((kt / KST) - 1) & 1, abort_flag, 33)) break;
+        if (kt >= KST && !wait_long(BK_EMPTY + ks, ((kt / KST) - 1) & 1, 33)) break;
         ++kt;
         mbar_arrive_expect_tx(bar(BK_FULL + ks), 32768);
 #pragma unroll
@@ -636,7 +657,8 @@ cudaError_t launch_nb(const KeyWeightArgs &p, cudaStream_t stream, const CUtenso
 int key_weights_tc_kind(const KeyWeightArgs &p) {
   const KernelArgs &a = p.a;
   if (a.group > 128 || a.max_q < 16 || a.total_q < step_tokens(a.group) || !encoder()) return 0;
-  if (p.k && p.pages.rows > 0x7fffffffL) return 0;       // rows are coordinates of the key loads
+  // rows are coordinates of the key loads, 32 of them a box
+  if (p.k && (p.pages.rows > 0x7fffffffL || p.pages.rows < 32)) return 0;
   if (a.E == 0) return 2;
   return a.rd % 8 == 0 && (reinterpret_cast<uintptr_t>(a.r) & 15u) == 0 ? 2 : 1;
 }
