@@ -577,16 +577,28 @@ __global__ void __launch_bounds__(FT) relattn_decode_fp4_combine_kernel(const __
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float z = 0.f;
   if (m != -INFINITY)
-    for (int i = warp; i < p.splits; i += FW) {
-      const float ls = p.a.lse_part[i * rows + row];
-      if (ls == -INFINITY) continue;
-      const float4 v = *reinterpret_cast<const float4 *>(p.a.o_part + (i * rows + row) * kHeadDim + lane * 4);
-      const float f = exp2f((ls - m) * kLog2e);
-      z += f;
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+    for (int i0 = warp; i0 < p.splits; i0 += 4 * FW) {       // four slots' loads in flight together
+      float ls[4];
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * FW;
+        ls[k] = i < p.splits ? p.a.lse_part[i * rows + row] : -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (ls[k] != -INFINITY)
+          v[k] = *reinterpret_cast<const float4 *>(p.a.o_part + ((i0 + k * FW) * rows + row) * kHeadDim + lane * 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (ls[k] == -INFINITY) continue;
+        const float f = exp2f((ls[k] - m) * kLog2e);
+        z += f;
+        acc.x = fmaf(f, v[k].x, acc.x);
+        acc.y = fmaf(f, v[k].y, acc.y);
+        acc.z = fmaf(f, v[k].z, acc.z);
+        acc.w = fmaf(f, v[k].w, acc.w);
+      }
     }
   red_o[warp][lane] = acc;
   if (lane == 0) red_z[warp] = z;
