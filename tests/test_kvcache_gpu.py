@@ -608,6 +608,57 @@ def test_captured_calls_replay_and_streams_do_not_share():
     ok()
 
 
+def test_calls_of_many_rows_and_long_sequences_replay_side_by_side():
+    """Decodes of 40 rows, key weights of 160 rows and selections by all SMs, in
+    two graphs that replay on two streams at once."""
+    c = U.Case((5, 4), (40000, 300), 16, 2, E=64)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    cache = U.device_cache(qc, d)
+    cu = (d["cu_q"].cuda(), d["cu_k"].cuda())
+    r, P, kw = d["r"].cuda(), d["P"].cuda(), U.call_kw(c, d)
+    c2 = U.Case((20, 3), c.k_lens, 16, 2, E=64, seed=3)
+    d2 = U.make(c2)
+    q2, r2, P2, cu2, kw2 = d2["q"].cuda(), d2["r"].cuda(), d2["P"].cuda(), d2["cu_q"].cuda(), U.call_kw(c2, d2)
+    lse2 = torch.full((16, 23), 8.0, device="cuda")
+    cu_keep = W.cu_seqlens([9000, 200]).cuda()
+
+    def step(q, w):
+        o, z = rpb.decode_nvfp4(q, cache, r, P, *cu, **kw)
+        w = rpb.key_weights(q2, cache, r2, P2, lse2, cu2, cu[1], weights_in=w, decay=0.5, **kw2)
+        to = torch.zeros(9200, 2, 8, dtype=torch.uint8, device="cuda")
+        pos, wk = rpb.evict([cache.k_scale], [to], w, cu[1], cu_keep, max_seqlen_k=40000, recent=64, sink=4,
+                            total_k=40300, total_keep=9200)
+        return o, z, w, to, pos, wk
+
+    rng = torch.Generator(device="cuda").manual_seed(1)
+    ins = [(d["q"].cuda() * f, torch.rand(2, 40300, device="cuda", generator=rng)) for f in (1.0, 0.5)]
+    want = [step(q, w) for q, w in ins]
+    ok()
+    graphs, held = [], []
+    for q, w in ins:
+        g, q0, w0 = torch.cuda.CUDAGraph(), torch.zeros_like(q), torch.zeros_like(w)
+        with torch.cuda.graph(g):
+            got = step(q0, w0)
+        graphs.append(g)
+        held.append((q0, w0, got))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for (q, w), (q0, w0, _) in zip(ins, held):
+            q0.copy_(q)
+            w0.copy_(w)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        ok()
+        for x, (_, _, got) in zip(want, held):
+            for a, b in zip(x, got):
+                assert torch.equal(a, b)
+
+
 def test_a_prompt_is_cached_weighed_evicted_and_decoded():
     """The operators in the order a server calls them: a prompt's rows go into a
     4-bit paged cache, its last rows vote, half of the keys leave, and a
