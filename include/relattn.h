@@ -232,7 +232,8 @@ relattn_status relattn_decode_mxfp8(const relattn_params *params, const relattn_
  * A cache holds `rows` rows: contiguous, row cu_seqlens_k[b] + p for key p of
  * sequence b (rows >= total_k), or, where a call is given a relattn_paged_kv,
  * pool rows as in relattn_decode_paged (rows = num_pages * page_size; here any
- * page_size that is a multiple of 32).  rows < 2^31.
+ * page_size that is a multiple of 32).  rows < 2^31; the calls below take
+ * max_seqlen_k up to 2^31 - 2^16.
  */
 typedef struct relattn_kv_nvfp4 {
   void *k;                     /* uint8 [rows, num_heads_kv, 64], 16-byte aligned          */

@@ -326,6 +326,7 @@ relattn_status validate_prologue(const relattn_prologue_params *p, const relattn
 // ---- the 4-bit cache, key weights and eviction
 
 constexpr long kMaxRows = 0x7fffffffL;
+constexpr long kMaxKeys = 0x7fff0000L;      // of a sequence: the walks step past its end by less than the rest
 
 // Checks a page table and fills the row addressing; max_k: the longest
 // sequence it has to hold (0: checked on the device).
@@ -407,7 +408,7 @@ relattn_status validate_cached(const relattn_params *p, bool decode, const void 
   f.out = const_cast<void *>(out);
   const relattn_status st = validate(&f, decode);
   if (st != RELATTN_OK) return st;
-  return (long)p->batch * p->num_heads_kv > 65535 ? RELATTN_ERR_UNSUPPORTED : RELATTN_OK;
+  return (long)p->batch * p->num_heads_kv > 65535 || p->max_seqlen_k > kMaxKeys ? RELATTN_ERR_UNSUPPORTED : RELATTN_OK;
 }
 
 // the sizes that the key weights' workspace depends on
@@ -438,7 +439,7 @@ relattn_status validate_evict(const relattn_evict_params *p, EvictArgs *a) {
       p->sink < 0 || p->recent < 0 || p->num_planes < 0 || p->num_planes > RELATTN_MAX_PLANES ||
       p->total_keep > p->total_k)
     return RELATTN_ERR_INVALID_ARG;
-  if ((long)p->batch * p->num_heads_kv > 0x0fffffffL) return RELATTN_ERR_UNSUPPORTED;
+  if ((long)p->batch * p->num_heads_kv > 0x0fffffffL || p->max_seqlen_k > kMaxKeys) return RELATTN_ERR_UNSUPPORTED;
   *a = EvictArgs{};
   relattn_status st = cache_pages(p->pages, p->rows, p->max_seqlen_k, &a->src);
   if (st == RELATTN_OK) st = cache_pages(p->pages_keep, p->rows_keep, 0, &a->dst);

@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
     return;
   }
   // this CTA's keys, a multiple of 32 each
-  const int chunk = ((s.n + cs - 1) / cs + 31) & ~31;
-  const int lo = min(s.n, rank * chunk), hi = min(s.n, lo + chunk);
+  const long chunk = (((long)s.n + cs - 1) / cs + 31) & ~31L;
+  const int lo = (int)min((long)s.n, rank * chunk), hi = (int)min((long)s.n, lo + chunk);
   const int m0 = s.sink, m1 = s.n - s.recent;                       // the competing keys
   const int mlo = max(lo, m0 & ~31), mhi = min(hi, m1);             // from a multiple of 32 (or none)
 

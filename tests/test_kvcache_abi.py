@@ -43,6 +43,7 @@ def pages(**kw):
     (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(lse=None), INVALID), (dict(q=A + 2), INVALID),
     (dict(r=None), INVALID), (dict(total_k=601), INVALID), (dict(batch=-1), INVALID),
     (dict(batch=40000), UNSUPPORTED), (dict(max_seqlen_k=0), INVALID),
+    (dict(max_seqlen_k=(1 << 31) - (1 << 16) + 1, total_k=(1 << 31) - 1), UNSUPPORTED),
 ])
 def test_decode_refuses_parameters(kw, want):
     assert rpb.relattn_decode_nvfp4(fwd(**kw), cache()) == want
@@ -132,7 +133,9 @@ def evict(**kw):
     (dict(weights_out=A), INVALID), (dict(weights_out=5 * A), INVALID), (dict(key_pos=5 * A), INVALID),
     (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=100 * 3 * 4 - 1), WORKSPACE), (dict(workspace=A + 8), WORKSPACE),
     (dict(pages=ctypes.pointer(pages(page_size=16, num_pages=40)), rows=640), UNSUPPORTED),
-    (dict(rows=1 << 31), UNSUPPORTED),
+    (dict(rows=1 << 31), UNSUPPORTED), (dict(max_seqlen_k=(1 << 31) - (1 << 16) + 1), UNSUPPORTED),
+    # few long sequences need more than the kept rows' numbers
+    (dict(max_seqlen_k=40000, rows=40000, total_k=40000, workspace_bytes=100 * 3 * 4), WORKSPACE),
 ])
 def test_evict_refuses(kw, want):
     assert rpb.relattn_evict(evict(**kw)) == want
@@ -166,6 +169,9 @@ def test_workspace_sizes():
     assert (st, n) == (0, 2 * 8 * 64 * 4)
     assert rpb.relattn_key_weights_workspace_size(weights(f=fwd(r_dim=0, rel_extent=0))) == (0, 0)
     assert rpb.relattn_evict_workspace_size(evict()) == (0, 100 * 3 * 4)
+    st, n = rpb.relattn_evict_workspace_size(evict(max_seqlen_k=40000))
+    assert st == 0 and n > 4 * 3 * 2048 * 4                # three histograms of every (sequence, head)
+    assert rpb.relattn_evict_workspace_size(evict(max_seqlen_k=40000, batch=5)) == (0, 100 * 3 * 4)
 
 
 def test_python_checks_name_the_argument():
