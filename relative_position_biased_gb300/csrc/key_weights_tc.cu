@@ -21,7 +21,8 @@
 // What bounds it: the issue of N = 128 products (about 70 cycles each, 8 a
 // step and 4 more in the band) outside the band, the consumers inside it; with
 // a tile of only two steps (32 observing tokens of a group of 8) the consumers'
-// turn from tile to tile, of which the lanes' shuffles are half.
+// turn from tile to tile, of which the lanes' shuffles are a third.  Measured: all
+// rows of a 4 x 8192 prompt, window 4096, group 8: 575 us, 717 TFLOP/s.
 //
 // A CTA is given tiles until there are none left (cluster launch control), in
 // the order in which CTAs would start, longest first: early keys are seen by

@@ -5,7 +5,8 @@
 // Positional Embedding".
 //
 // A [rows, r_dim] x [r_dim, E] product with r_dim <= 64: what it writes (4
-// bytes a value) is many times what it reads, so it is bound by that.  A CTA
+// bytes a value) is many times what it reads, so it is bound by that and, at a
+// decode step's sizes, by its launch (1024 rows x 1024 distances: 7 us).  A CTA
 // takes 64 rows x 128 distances, a warp 16 rows; both operands are staged in
 // shared memory, zero past r_dim, the rows and E, with 16-byte loads where the
 // addresses allow and 2-byte ones elsewhere.
