@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(TDT, 1) relattn_decode_fp4_tc_kernel(const __g
                         lds_u16(sat + 8 * kFp4Blocks * j));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(DB_KF + ks));
+        if (lane == 0 && g != p.a.test_skip_k_tile) mbar_arrive(bar(DB_KF + ks));    // (test hook: never told)
         if (g >= VST && !wait_warp(bar(DB_VE + vs), ((g / VST) - 1) & 1, abort_flag, 46)) return false;
 #pragma unroll 1
         for (int j = 0; j < DJ; ++j)

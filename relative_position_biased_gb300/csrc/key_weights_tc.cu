@@ -439,7 +439,7 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
         if (t.steps == 0 || !p.k) continue;
         const int ks = kt % KST;
         if (kt >= KST && !wait_long(BK_EMPTY + ks, ((kt / KST) - 1) & 1, 33)) break;
-        ++kt;
+        if (kt++ == p.a.test_skip_k_tile) continue;     // (test hook: a skipped tile is never loaded)
         mbar_arrive_expect_tx(bar(BK_FULL + ks), 32768);
 #pragma unroll
         for (int i = 0; i < kWalkTile / 32; ++i) {
