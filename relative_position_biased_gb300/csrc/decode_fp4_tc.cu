@@ -11,14 +11,15 @@
 //
 // What bounds it: no pipe (tensor a quarter, issue two fifths busy) but the way
 // of a tile through its steps, 1.3 us: conversion, product, a softmax warp of
-// each scheduler that walks 128 columns alone, second product.  Of 178 us for
-// that case without a bias, 60 conversion (118 without it), 51 the softmax.  So
-// two groups of conversion warps take tiles in turn, the two products queue
-// behind each other without a wait, and loops are kept short: unrolled, with P
-// in registers, the same softmax took 183 to 193 us, as the roles' code then
-// no longer fits the instruction cache together; with eight softmax warps, 64 keys
-// and dims each, 205.  Tiles of the bias band are slow (a warp fetches 32 windows
-// of R) and weigh more in the split of the work.
+// each scheduler that walks 128 columns alone, second product.  (An earlier form
+// took 193 us for that case without a bias, 166 without the conversion, 142
+// without the softmax, 117 without both.)  So two groups of conversion warps
+// take tiles in turn, the next logits are made while these are worked on, and
+// loops are kept short: unrolled, with P in registers, the softmax took 183 to
+// 193 us instead of 178, as the roles' code then no longer fits the instruction
+// cache together; with eight softmax warps, 64 keys and dims each, 205.  Tiles of
+// the bias band are slow (a warp fetches 32 windows of R) and weigh more in the
+// split of the work.
 //
 // q is f16 after a power-of-two scaling per row, P is rounded to f16 and held
 // times 2^7, the factors of the head are folded into the logit scale and the
@@ -29,10 +30,10 @@
 //
 // Roles (16 warps): 0-3 softmax and the output (a thread a row), 4-11
 // conversion (two groups, 32 keys of every other tile each, raw bytes in a ring
-// of asynchronous copies of their own), 12 the products.  TMEM: S twice 128 columns, P over
-// the S it came from, O 128, Q 64.  Work is split as in the other kernel:
-// units (sequence, kv head, 128-row block) of tiles laid end to end.  Every
-// wait is bounded: a timeout sets the device error word and the roles stop.
+// of asynchronous copies of their own), 12 the products.  TMEM: S twice 128
+// columns, O 128, Q 64, P 64.  Work is split as in the other kernel: units
+// (sequence, kv head, 128-row block) of tiles laid end to end.  Every wait is
+// bounded: a timeout sets the device error word and the roles stop.
 #include <algorithm>
 
 #include "cache_walk.cuh"
@@ -63,7 +64,7 @@ enum { DB_QF = 0, DB_KF, DB_KE = DB_KF + KST, DB_VF = DB_KE + KST, DB_VE = DB_VF
 constexpr uint32_t TD_SLOT = TD_BAR + DB_COUNT * 8, TD_ABORT = TD_SLOT + 8;
 constexpr uint32_t TD_SMEM = TD_ABORT + 8 + 1024;
 static_assert(TD_SMEM + (kWalkBatch + 1 + 16) * 4 <= 227 * 1024, "shared memory budget");
-constexpr uint32_t TM_S = 0, TM_O = 256, TM_Q = 384;               // TMEM columns
+constexpr uint32_t TM_S = 0, TM_O = 256, TM_Q = 384, TM_P = 448;   // TMEM columns
 constexpr float kPShift = 7.f;               // P is held times 2^7
 constexpr float kNone = -3.402823466e38f;    // running maximum before any visible key: finite
 constexpr float kRaise = 8.f;                // the maximum is raised past this excess
@@ -331,61 +332,58 @@ __global__ void __launch_bounds__(TDT, 1) relattn_decode_fp4_tc_kernel(const __g
             }
             tmem_wait_st();
           }
-          // ---- the tile's largest logit
-          float mx = -INFINITY;
+          // ---- P of the maximum so far; again, with a raised one, where a logit
+          // passes it by too much (S stays as it is, P has its own columns)
+          float z0, z1;
+          bool free = i == 0;                // P's last product is through
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            float x[64];
-            tmem_ld32f<0>(sa + 64 * h, x);
-            tmem_ld32f<32>(sa + 64 * h + 32, x);
-            tmem_wait_ld_f<0>(x);
-            reg_dep_f<32>(x);
-            float a = -INFINITY;
+          for (;;) {
+            const float c = kPShift - m;
+            float mx = -INFINITY;
+            z0 = l0, z1 = l1;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              float x[64];
+              uint32_t y[32];
+              tmem_ld32f<0>(sa + 64 * h, x);
+              tmem_ld32f<32>(sa + 64 * h + 32, x);
+              tmem_wait_ld_f<0>(x);
+              reg_dep_f<32>(x);
 #pragma unroll
-            for (int k = 0; k < 64; k += 4) a = fmax3(a, x[k], x[k + 1]), mx = fmax3(mx, x[k + 2], x[k + 3]);
-            mx = fmaxf(mx, a);
-          }
-          mx *= cm;
-          if (__any_sync(full, mx > m + kRaise)) {
+              for (int k = 0; k < 32; ++k) {
+                float e0, e1;
+                mx = fmax3(mx, x[2 * k], x[2 * k + 1]);
+                ffma2(e0, e1, x[2 * k], x[2 * k + 1], cm, cm, c, c);
+                e0 = fast_exp2(e0), e1 = fast_exp2(e1);
+                add2(z0, z1, e0, e1);
+                y[k] = pack_f16x2(e0, e1);
+              }
+              if (!free) {
+                if (!__all_sync(full, mbar_wait(bar(DB_OD), (g - 1) & 1, abort_flag, 42))) return false;
+                tc_fence_after();
+                free = true;
+              }
+              tmem_st32(lanes + TM_P + 32 * h, y);
+            }
+            mx *= cm;
+            if (!__any_sync(full, mx > m + kRaise)) break;
             const float to = fmaxf(m, mx), f = fast_exp2(m - to);
             m = to;
             l0 *= f, l1 *= f;
-            if (i > 0) {
-              // O as it stands, after the last tile's product
-              if (!__all_sync(full, mbar_wait(bar(DB_OD), (g - 1) & 1, abort_flag, 42))) return false;
-              tc_fence_after();
+            if (i == 0) continue;
+            // O as it stands, after the last tile's product
 #pragma unroll 1
-              for (int ch = 0; ch < 4; ++ch) {
-                float x[32];
-                uint32_t w[32];
-                tmem_ld32f<0>(lanes + TM_O + 32 * ch, x);
-                tmem_wait_ld_f<0>(x);
+            for (int ch = 0; ch < 4; ++ch) {
+              float x[32];
+              uint32_t w[32];
+              tmem_ld32f<0>(lanes + TM_O + 32 * ch, x);
+              tmem_wait_ld_f<0>(x);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(x[k] * f);
-                tmem_st32(lanes + TM_O + 32 * ch, w);
-              }
+              for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(x[k] * f);
+              tmem_st32(lanes + TM_O + 32 * ch, w);
             }
           }
-          // ---- P over S, behind the columns that are still to be read
-          const float c = kPShift - m;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            float x[64];
-            uint32_t y[32];
-            tmem_ld32f<0>(sa + 64 * h, x);
-            tmem_ld32f<32>(sa + 64 * h + 32, x);
-            tmem_wait_ld_f<0>(x);
-            reg_dep_f<32>(x);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float e0, e1;
-              ffma2(e0, e1, x[2 * k], x[2 * k + 1], cm, cm, c, c);
-              e0 = fast_exp2(e0), e1 = fast_exp2(e1);
-              add2(l0, l1, e0, e1);
-              y[k] = pack_f16x2(e0, e1);
-            }
-            tmem_st32(sa + 32 * h, y);
-          }
+          l0 = z0, l1 = z1;
           tmem_wait_st();
         }
         // ---- NaN blocks of V that the row sees
@@ -529,7 +527,7 @@ __global__ void __launch_bounds__(TDT, 1) relattn_decode_fp4_tc_kernel(const __g
         if (!(run = mbar_wait_warp(bar(DB_VF + vs), (t / VST) & 1, abort_flag, 49))) return false;
         tc_fence_after();
         const uint64_t vd = vd0 + (uint64_t)(vs * (TILE >> 4));
-        const uint32_t pa = tmem + TM_S + 128u * (t & 1);
+        const uint32_t pa = tmem + TM_P;
         if (acc) mma_ts_e<1>(o, pa, vd, id_o);
         else mma_ts_e<0>(o, pa, vd, id_o);
         mma_ts_e<1>(o, pa + 8, vd + 128, id_o);
@@ -546,7 +544,6 @@ __global__ void __launch_bounds__(TDT, 1) relattn_decode_fp4_tc_kernel(const __g
       for (int i = 0; i < n; ++i, ++g) {
         const int ks = g % KST;
         if (!(run = mbar_wait_warp(bar(DB_KF + ks), (g / KST) & 1, abort_flag, 50))) return false;
-        // (P of two tiles ago lies where S goes now; its product is before this one in the same queue)
         tc_fence_after();
         const uint64_t kd = kd0 + (uint64_t)(ks * (TILE >> 4));
         const uint32_t d = tmem + TM_S + 128u * (g & 1);
