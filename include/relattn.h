@@ -394,6 +394,8 @@ typedef struct relattn_evict_params {
   int32_t *key_pos_out;              /* int32 [num_heads_kv, rows_keep] or NULL            */
   void *workspace;
   size_t workspace_bytes;
+  int32_t clear_out;                 /* not 0: weights_out is set to 0 and key_pos_out to -1
+                                      * first; 0: rows that take no key keep theirs */
 } relattn_evict_params;
 
 relattn_status relattn_evict(const relattn_evict_params *params, void *stream);

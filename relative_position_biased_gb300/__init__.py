@@ -141,6 +141,7 @@ class RelattnEvictParams(ctypes.Structure):
         ("num_planes", ctypes.c_int32), ("planes", RelattnPlane * MAX_PLANES),
         ("weights_out", ctypes.c_void_p), ("key_pos_out", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("clear_out", ctypes.c_int32),
     ]
 
 
@@ -941,6 +942,9 @@ def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: in
     return out
 
 
+_NO_PLANES = RelattnPlane * MAX_PLANES
+
+
 def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seqlen_k: int, recent: int, sink: int = 0,
           total_keep: int, total_k: Optional[int] = None, key_pos=None, block_table=None, page_size: int = 0,
           block_table_keep=None, page_size_keep: int = 0, key_pos_out=None, weights_out=None, workspace=None,
@@ -967,31 +971,29 @@ def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seq
     H, rows = _shape(weights, "weights", 2)
     batch, ck, ckeep = _lengths(cu_seqlens_k, cu_seqlens_keep, "cu_seqlens_k", "cu_seqlens_keep", dev)
     rows_keep = dst_planes[0].shape[0] if n else int(total_keep)
-    prm = RelattnEvictParams(_tensor(weights, "weights", torch.float32, (H, rows), dev), ck, ckeep)
+    wp = _tensor(weights, "weights", torch.float32, (H, rows), dev)
+    table = _NO_PLANES()
     for i in range(n):
         a, b = planes[i], dst_planes[i]
-        rest = a.shape[2:]
-        if a.shape[:2] != (rows, H) or b.shape != (rows_keep, H, *rest):
+        sa, sb = a.shape, b.shape
+        if len(sa) < 2 or sa[0] != rows or sa[1] != H or len(sb) < 2 or sb[0] != rows_keep or sb[1:] != sa[1:]:
             raise ValueError(f"plane {i} must be [rows, Hkv, ...] and its destination [rows_keep, Hkv, ...]")
-        prm.planes[i] = RelattnPlane(_tensor(a, f"plane {i}", a.dtype, a.shape, dev),
-                                     _tensor(b, f"destination {i}", a.dtype, b.shape, dev),
-                                     a.element_size() * rest.numel())
+        table[i] = (_tensor(a, f"plane {i}", a.dtype, sa, dev), _tensor(b, f"destination {i}", a.dtype, sb, dev),
+                    a.element_size() * sa[2:].numel())
     pages = _pages(block_table, page_size, rows, dev, batch)
     pages_keep = _pages(block_table_keep, page_size_keep, rows_keep, dev, batch)
-    if key_pos_out is None:
-        key_pos_out = torch.full((H, rows_keep), -1, dtype=torch.int32, device=dev)
-    if weights_out is None:
-        weights_out = torch.zeros(H, rows_keep, dtype=torch.float32, device=dev)
-    prm.key_pos = None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, (H, rows), dev)
-    prm.batch, prm.total_keep, prm.num_heads_kv, prm.num_planes = batch, total_keep, H, n
-    prm.total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
-    prm.max_seqlen_k, prm.sink, prm.recent, prm.rows, prm.rows_keep = max_seqlen_k, sink, recent, rows, rows_keep
-    if pages is not None:
-        prm.pages = ctypes.pointer(pages)
-    if pages_keep is not None:
-        prm.pages_keep = ctypes.pointer(pages_keep)
-    prm.weights_out = _tensor(weights_out, "weights_out", torch.float32, (H, rows_keep), dev)
-    prm.key_pos_out = _tensor(key_pos_out, "key_pos_out", torch.int32, (H, rows_keep), dev)
+    new_pos, new_w = key_pos_out is None, weights_out is None
+    if new_pos:                                  # (both new: cleared by the call)
+        key_pos_out = (torch.empty(H, rows_keep, dtype=torch.int32, device=dev) if new_w
+                       else torch.full((H, rows_keep), -1, dtype=torch.int32, device=dev))
+    if new_w:
+        weights_out = (torch.empty if new_pos else torch.zeros)(H, rows_keep, dtype=torch.float32, device=dev)
+    prm = RelattnEvictParams(
+        wp, ck, ckeep, None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, (H, rows), dev), batch,
+        _total_k(total_k, block_table, cu_seqlens_k, rows), total_keep, max_seqlen_k, H, sink, recent, rows, rows_keep,
+        None if pages is None else ctypes.pointer(pages), None if pages_keep is None else ctypes.pointer(pages_keep),
+        n, table, _tensor(weights_out, "weights_out", torch.float32, (H, rows_keep), dev),
+        _tensor(key_pos_out, "key_pos_out", torch.int32, (H, rows_keep), dev), None, 0, new_pos and new_w)
     status, need = relattn_evict_workspace_size(prm)
     _check(status, "relattn_evict_workspace_size")
     keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)

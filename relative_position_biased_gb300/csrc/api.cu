@@ -485,6 +485,7 @@ relattn_status validate_evict(const relattn_evict_params *p, EvictArgs *a) {
   a->recent = p->recent;
   a->w_out = p->weights_out;
   a->pos_out = p->key_pos_out;
+  a->clear = p->clear_out != 0;
   a->src_row = static_cast<int32_t *>(p->workspace);
   a->dst_row = a->src_row + (size_t)p->total_keep * p->num_heads_kv;
   if (evict_wide_bytes(p->batch, p->num_heads_kv, p->max_seqlen_k) > 0)
@@ -869,7 +870,15 @@ relattn_status relattn_evict_workspace_size(const relattn_evict_params *p, size_
 relattn_status relattn_evict(const relattn_evict_params *p, void *stream) {
   EvictArgs a;
   const relattn_status st = validate_evict(p, &a);
-  if (st != RELATTN_OK || a.batch == 0) return st;
+  if (st != RELATTN_OK) return st;
+  if (a.batch == 0) {                        // nothing is kept
+    EvictArgs none{};
+    none.Hkv = p->num_heads_kv;
+    none.dst.rows = p->rows_keep;
+    none.w_out = p->clear_out ? p->weights_out : nullptr;
+    none.pos_out = p->clear_out ? p->key_pos_out : nullptr;
+    return cuda_status(clear_evicted(none, static_cast<cudaStream_t>(stream)));
+  }
   return cuda_status(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 

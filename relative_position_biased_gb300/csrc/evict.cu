@@ -477,8 +477,22 @@ size_t evict_wide_bytes(int batch, int Hkv, int max_k) {
   return units <= kWideUnits && max_k >= kWideKeys ? (size_t)units * kWideWords * sizeof(unsigned) : 0;
 }
 
+cudaError_t clear_evicted(const EvictArgs &a, cudaStream_t stream) {
+  const size_t bytes = (size_t)a.Hkv * a.dst.rows * 4;
+  if (bytes == 0) return cudaSuccess;
+  if (a.w_out) {
+    const cudaError_t e = cudaMemsetAsync(a.w_out, 0, bytes, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return a.pos_out ? cudaMemsetAsync(a.pos_out, 0xff, bytes, stream) : cudaSuccess;
+}
+
 cudaError_t launch_evict(const EvictArgs &args, cudaStream_t stream) {
   EvictArgs a = args;
+  if (a.clear) {
+    const cudaError_t e = clear_evicted(a, stream);
+    if (e != cudaSuccess) return e;
+  }
   // CTAs per (sequence, kv head): one per 16K keys, up to 16; of 512 threads
   // while 16K keys are enough, else of 1024
   int cs = 1;

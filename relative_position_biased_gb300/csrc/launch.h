@@ -256,6 +256,7 @@ struct EvictArgs {
   int batch, total_keep, max_k, Hkv, sink, recent;
   float *w_out;                  // [Hkv, dst.rows] or null
   int32_t *pos_out;              // [Hkv, dst.rows] or null
+  int clear;                     // both are cleared first
   int32_t *src_row;              // workspace [Hkv, total_keep]: cache row of every kept key
   int32_t *dst_row;              // workspace [total_keep]: its row in the new cache
   int planes;
@@ -268,6 +269,7 @@ struct EvictArgs {
   int *err;
 };
 size_t evict_wide_bytes(int batch, int Hkv, int max_k);       // 0: one cluster per (sequence, kv head)
+cudaError_t clear_evicted(const EvictArgs &a, cudaStream_t stream);     // w_out to 0, pos_out to -1
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream);
 
 }  // namespace relattn

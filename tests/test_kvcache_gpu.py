@@ -531,7 +531,7 @@ def test_evict(k_lens, keep, recent, sink, kinds, page, page_to, ties):
                 np.testing.assert_array_equal(host(wk)[h, where_to[b]], w[h, src])
                 for p, q in zip(planes, dst):
                     assert torch.equal(q[torch.from_numpy(where_to[b]).cuda(), h].cpu(), p[torch.from_numpy(src), h])
-        assert (host(pos)[:, ~used] == -1).all()
+        assert (host(pos)[:, ~used] == -1).all() and (host(wk)[:, ~used] == 0).all()
         for q in dst:
             assert (q.cpu().float()[torch.from_numpy(~used)] == 3).all()
 
@@ -543,6 +543,29 @@ def test_evict_of_equal_weights_keeps_the_first():
                        total_keep=777)
     ok()
     assert torch.equal(pos[0].cpu(), torch.arange(777, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("given", [(True, True), (True, False), (False, True)])
+def test_evict_keeps_what_given_outputs_hold_elsewhere(given):
+    w = torch.rand(2, 300, device="cuda")
+    p = torch.rand(300, 2, 4, device="cuda")
+    to = torch.zeros(100, 2, 4, device="cuda")
+    pos = torch.full((2, 100), 7, dtype=torch.int32, device="cuda") if given[0] else None
+    wk = torch.full((2, 100), 7.0, device="cuda") if given[1] else None
+    pos, wk = rpb.evict([p], [to], w, W.cu_seqlens([300]).cuda(), W.cu_seqlens([60]).cuda(), max_seqlen_k=300, recent=5,
+                        total_keep=60, key_pos_out=pos, weights_out=wk)
+    ok()
+    assert (pos[:, 60:] == (7 if given[0] else -1)).all() and (wk[:, 60:] == (7 if given[1] else 0)).all()
+    assert (pos[:, :60] >= 0).all() and torch.equal(wk[0, :60], w[0][pos[0, :60].long()])
+
+
+def test_evict_of_nothing_clears_new_outputs():
+    p = torch.rand(30, 1, 4, device="cuda")
+    to = torch.zeros(10, 1, 4, device="cuda")
+    pos, wk = rpb.evict([p], [to], torch.rand(1, 30, device="cuda"), W.cu_seqlens([30]).cuda(), W.cu_seqlens([0]).cuda(),
+                        max_seqlen_k=30, recent=0, total_keep=0)
+    ok()
+    assert (pos == -1).all() and (wk == 0).all() and pos.shape == (1, 10)
 
 
 def test_evict_skips_and_records_bad_lengths():
