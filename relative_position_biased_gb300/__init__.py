@@ -681,6 +681,7 @@ class KvNvfp4(_KvTensors):
         self = super().__new__(cls, k, v, k_scale, v_scale, k_global, v_global)
         self.rows, self.num_heads_kv, self.device = rows, H, dev
         self.c_struct = RelattnKvNvfp4(rows=rows, **ptr)
+        self.c_pointer = ctypes.pointer(self.c_struct)
         return self
 
 
@@ -707,6 +708,15 @@ def _tensor(t, name: str, dtype, shape, device) -> int:
     raise ValueError(f"{name} is on {t.device}, not {device}")
 
 
+def _address(t, name: str, dtype, device) -> int:
+    """Address of a contiguous tensor of this type on `device` whose shape has
+    been looked at.  (These checks are most of a short call's host time: they
+    format nothing and look at nothing twice.)"""
+    if t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    return _tensor(t, name, dtype, t.shape, device)
+
+
 def _shape(t, name: str, n: int, *want):
     """t's shape, of n dimensions whose last ones are `want`."""
     s = t.shape
@@ -718,16 +728,19 @@ def _shape(t, name: str, n: int, *want):
 def _lengths(cu_q, cu_k, name_q: str, name_k: str, device):
     """(batch, addresses) of two cu_seqlens tensors."""
     import torch
-    n = cu_q.numel()
-    _need(n >= 1, f"{name_q} needs at least one entry")
-    return n - 1, _tensor(cu_q, name_q, torch.int32, (n,), device), _tensor(cu_k, name_k, torch.int32, (n,), device)
+    n, int32 = cu_q.numel(), torch.int32
+    if n < 1:
+        raise ValueError(f"{name_q} needs at least one entry")
+    if cu_q.dim() == 1 and cu_k.dim() == 1 and cu_k.numel() == n:
+        return n - 1, _address(cu_q, name_q, int32, device), _address(cu_k, name_k, int32, device)
+    return n - 1, _tensor(cu_q, name_q, int32, (n,), device), _tensor(cu_k, name_k, int32, (n,), device)
 
 
-def _cache(cache: KvNvfp4, device) -> RelattnKvNvfp4:
-    _need(isinstance(cache, KvNvfp4), "cache must be a KvNvfp4")
+def _cache(cache: KvNvfp4, device) -> None:
+    if not isinstance(cache, KvNvfp4):
+        raise ValueError("cache must be a KvNvfp4")
     if cache.device != device:
         raise ValueError(f"the cache is on {cache.device}, not {device}")
-    return cache.c_struct
 
 
 def _pages(block_table, page_size: int, rows: int, device, batch: int) -> Optional[RelattnPagedKV]:
@@ -735,9 +748,11 @@ def _pages(block_table, page_size: int, rows: int, device, batch: int) -> Option
     if block_table is None:
         return None
     _need(page_size > 0 and rows % page_size == 0, "rows must be a multiple of page_size")
-    slots = _shape(block_table, "block_table", 2)[1]
-    return RelattnPagedKV(_tensor(block_table, "block_table", torch.int32, (batch, slots), device), slots,
-                          page_size, rows // page_size)
+    seqs, slots = _shape(block_table, "block_table", 2)
+    if seqs != batch:
+        _tensor(block_table, "block_table", torch.int32, (batch, slots), device)
+    return RelattnPagedKV(_address(block_table, "block_table", torch.int32, device), slots, page_size,
+                          rows // page_size)
 
 
 def _positions(key_pos, q_pos, num_heads_kv: int, rows: int, batch: int, device) -> Optional[RelattnPositions]:
@@ -755,8 +770,8 @@ def _stream_here(device, stream: Optional[int]) -> Optional[int]:
     import torch
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, not {device}")
-    index = device.index
-    if stream is not None or index != torch.cuda.current_device():
+    index = device.index                     # (a tensor on it: CUDA is initialised)
+    if stream is not None or index != torch._C._cuda_getDevice():
         return None
     return torch._C._cuda_getCurrentRawStream(index)
 
@@ -779,30 +794,34 @@ def _queries(q, r, P, num_heads_kv: int, device):
     """(total_q, Hq, r_dim, E) and addresses of q [Tq, Hq, 128], r [Tq, Hq,
     r_dim], P [r_dim, E]."""
     import torch
+    bf16 = torch.bfloat16
     Tq, Hq, _ = _shape(q, "q", 3, HEAD_DIM)
     if num_heads_kv <= 0 or Hq % num_heads_kv:
         raise ValueError(f"num_heads_q = {Hq} must be a multiple of num_heads_kv = {num_heads_kv}")
-    qp = _tensor(q, "q", torch.bfloat16, q.shape, device)
+    qp = _address(q, "q", bf16, device)
     if r is None or P is None:
         _need(r is None and P is None, "r and P go together")
         return Tq, Hq, 0, 0, qp, None, None
-    rd = _shape(r, "r", 3)[2]
-    E = _shape(P, "P", 2)[1]
-    return (Tq, Hq, rd, E, qp, _tensor(r, "r", torch.bfloat16, (Tq, Hq, rd), device),
-            _tensor(P, "P", torch.bfloat16, (rd, E), device))
+    rs, Ps = r.shape, P.shape
+    if len(rs) == 3 and len(Ps) == 2 and rs[0] == Tq and rs[1] == Hq and Ps[0] == rs[2]:
+        return Tq, Hq, rs[2], Ps[1], qp, _address(r, "r", bf16, device), _address(P, "P", bf16, device)
+    rd, E = _shape(r, "r", 3)[2], _shape(P, "P", 2)[1]
+    _tensor(r, "r", bf16, (Tq, Hq, rd), device)
+    _tensor(P, "P", bf16, (rd, E), device)
+    raise AssertionError("one of them was refused")
 
 
 def _cache_rows(k, v, cu_q, cu_k, cache, block_table, page_size):
     import torch
-    dev = k.device
-    kv = _cache(cache, dev)
+    dev, bf16 = k.device, torch.bfloat16
+    _cache(cache, dev)
     H = cache.num_heads_kv
     batch, cq, ck = _lengths(cu_q, cu_k, "cu_seqlens_q", "cu_seqlens_k", dev)
     pages = _pages(block_table, page_size, cache.rows, dev, batch)
     shape = (k.shape[0], H, HEAD_DIM)
     return RelattnCacheRowsParams(
-        _tensor(k, "k", torch.bfloat16, shape, dev), _tensor(v, "v", torch.bfloat16, shape, dev), cq, ck, batch,
-        shape[0], H, HEAD_DIM, ctypes.pointer(kv), None if pages is None else ctypes.pointer(pages))
+        _tensor(k, "k", bf16, shape, dev), _tensor(v, "v", bf16, shape, dev), cq, ck, batch,
+        shape[0], H, HEAD_DIM, cache.c_pointer, None if pages is None else ctypes.pointer(pages))
 
 
 def store_nvfp4(k, v, cu_seqlens_q, cu_seqlens_k, cache: KvNvfp4, *, block_table=None, page_size: int = 0,
@@ -815,7 +834,7 @@ def store_nvfp4(k, v, cu_seqlens_q, cu_seqlens_k, cache: KvNvfp4, *, block_table
     if st is None:
         with _switched(k.device, stream):
             return store_nvfp4(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table=block_table, page_size=page_size)
-    _check(relattn_store_nvfp4(prm, st), "relattn_store_nvfp4")
+    _check((_lib or load_library()).relattn_store_nvfp4(ctypes.byref(prm), st), "relattn_store_nvfp4")
 
 
 def load_nvfp4(cache: KvNvfp4, cu_seqlens_q, cu_seqlens_k, *, total_q: int, block_table=None, page_size: int = 0,
@@ -833,7 +852,7 @@ def load_nvfp4(cache: KvNvfp4, cu_seqlens_q, cu_seqlens_k, *, total_q: int, bloc
     v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
     _need(k.shape[0] == total_q, "k must have total_q rows")
     prm = _cache_rows(k, v, cu_seqlens_q, cu_seqlens_k, cache, block_table, page_size)
-    _check(relattn_load_nvfp4(prm, st), "relattn_load_nvfp4")
+    _check((_lib or load_library()).relattn_load_nvfp4(ctypes.byref(prm), st), "relattn_load_nvfp4")
     return k, v
 
 
@@ -845,11 +864,13 @@ def _total_k(total_k: Optional[int], block_table, cu_k, rows: int) -> int:
 
 def _workspace(nbytes: int, workspace, device):
     """(tensor kept alive, pointer, bytes) of a workspace of at least nbytes."""
-    import torch
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device)
+        import torch
+        words = (nbytes + 3) // 4
+        workspace = torch.empty(words, dtype=torch.float32, device=device)
+        return workspace, workspace.data_ptr(), 4 * words
     _need(workspace.device == device, "workspace is on another device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -872,22 +893,30 @@ def decode_nvfp4(q, cache: KvNvfp4, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seq
                                 max_seqlen_k=max_seqlen_k, alpha=alpha, window=window, log_scale_base=log_scale_base,
                                 key_pos=key_pos, q_pos=q_pos, block_table=block_table, page_size=page_size,
                                 total_k=total_k, num_splits=num_splits, out=out, lse=lse, workspace=workspace)
-    kv = _cache(cache, dev)
+    _cache(cache, dev)
     H, rows = cache.num_heads_kv, cache.rows
     Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
     batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
     pages = _pages(block_table, page_size, rows, dev, batch)
     pos = _positions(key_pos, q_pos, H, rows, batch, dev)
-    out, lse = _outputs(q, out, lse)
+    if out is None:
+        out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _tensor(out, "out", torch.bfloat16, (Tq, Hq, HEAD_DIM), dev)
+    if lse is None:
+        lse = torch.empty(Hq, Tq, dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    else:
+        lp = _tensor(lse, "lse", torch.float32, (Hq, Tq), dev)
     prm = RelattnParams(
         qp, None, None, rp, Pp, cq, ck, batch, Tq, _total_k(total_k, block_table, cu_seqlens_k, rows),
-        max_seqlen_q, max_seqlen_k, Hq, H, HEAD_DIM, rd, E, window, alpha, log_scale_base,
-        _tensor(out, "out", torch.bfloat16, (Tq, Hq, HEAD_DIM), dev),
-        _tensor(lse, "lse", torch.float32, (Hq, Tq), dev), None, 0, num_splits)
-    status, need = relattn_decode_nvfp4_workspace_size(prm, pos)
-    _check(status, "relattn_decode_nvfp4_workspace_size")
-    keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
-    _check(relattn_decode_nvfp4(prm, kv, pos, pages, st), "relattn_decode_nvfp4")
+        max_seqlen_q, max_seqlen_k, Hq, H, HEAD_DIM, rd, E, window, alpha, log_scale_base, op, lp, None, 0, num_splits)
+    lib, need = _lib or load_library(), ctypes.c_size_t()
+    ref, pos = ctypes.byref(prm), _ref(pos)
+    _check(lib.relattn_decode_nvfp4_workspace_size(ref, pos, ctypes.byref(need)), "relattn_decode_nvfp4_workspace_size")
+    keep, prm.workspace, prm.workspace_bytes = _workspace(need.value, workspace, dev)
+    _check(lib.relattn_decode_nvfp4(ref, cache.c_pointer, pos, _ref(pages), st), "relattn_decode_nvfp4")
     return out, lse
 
 
@@ -913,10 +942,11 @@ def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: in
                                workspace=workspace)
     fp4 = isinstance(k, KvNvfp4)
     if fp4:
-        kv, rows, H = _cache(k, dev), k.rows, k.num_heads_kv
+        _cache(k, dev)
+        rows, H = k.rows, k.num_heads_kv
     else:
         rows, H, _ = _shape(k, "k", 3, HEAD_DIM)
-        kp = _tensor(k, "k", torch.bfloat16, k.shape, dev)
+        kp = _address(k, "k", torch.bfloat16, dev)
     Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
     batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
     pages = _pages(block_table, page_size, rows, dev, batch)
@@ -924,6 +954,7 @@ def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: in
     w_in = None if weights_in is None else _tensor(weights_in, "weights_in", torch.float32, (H, rows), dev)
     if out is None:
         out = torch.zeros(H, rows, dtype=torch.float32, device=dev)
+    w_out = w_in if out is weights_in else _tensor(out, "out", torch.float32, (H, rows), dev)
     total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
     if not fp4 and block_table is None:
         _need(total_k == rows, "a contiguous k has total_k rows")
@@ -932,13 +963,12 @@ def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: in
         HEAD_DIM, rd, E, window, alpha, log_scale_base, None,
         _tensor(lse, "lse", torch.float32, (Hq, Tq), dev), None, 0, 0)
     prm = RelattnKeyWeightsParams(
-        fwd, ctypes.pointer(kv) if fp4 else None, None if pos is None else ctypes.pointer(pos),
-        None if pages is None else ctypes.pointer(pages), w_in,
-        _tensor(out, "out", torch.float32, (H, rows), dev), decay)
-    status, need = relattn_key_weights_workspace_size(prm)
-    _check(status, "relattn_key_weights_workspace_size")
-    keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
-    _check(relattn_key_weights(prm, st), "relattn_key_weights")
+        fwd, k.c_pointer if fp4 else None, None if pos is None else ctypes.pointer(pos),
+        None if pages is None else ctypes.pointer(pages), w_in, w_out, decay)
+    lib, need, ref = _lib or load_library(), ctypes.c_size_t(), ctypes.byref(prm)
+    _check(lib.relattn_key_weights_workspace_size(ref, ctypes.byref(need)), "relattn_key_weights_workspace_size")
+    keep, prm.workspace, prm.workspace_bytes = _workspace(need.value, workspace, dev)
+    _check(lib.relattn_key_weights(ref, st), "relattn_key_weights")
     return out
 
 
@@ -978,8 +1008,11 @@ def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seq
         sa, sb = a.shape, b.shape
         if len(sa) < 2 or sa[0] != rows or sa[1] != H or len(sb) < 2 or sb[0] != rows_keep or sb[1:] != sa[1:]:
             raise ValueError(f"plane {i} must be [rows, Hkv, ...] and its destination [rows_keep, Hkv, ...]")
-        table[i] = (_tensor(a, f"plane {i}", a.dtype, sa, dev), _tensor(b, f"destination {i}", a.dtype, sb, dev),
-                    a.element_size() * sa[2:].numel())
+        dtype = a.dtype
+        if not (b.dtype is dtype and a.device == dev and b.device == dev and a.is_contiguous() and b.is_contiguous()):
+            _tensor(a, f"plane {i}", dtype, sa, dev)
+            _tensor(b, f"destination {i}", dtype, sb, dev)
+        table[i] = (a.data_ptr(), b.data_ptr(), a.element_size() * sa[2:].numel())
     pages = _pages(block_table, page_size, rows, dev, batch)
     pages_keep = _pages(block_table_keep, page_size_keep, rows_keep, dev, batch)
     new_pos, new_w = key_pos_out is None, weights_out is None
@@ -992,10 +1025,11 @@ def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seq
         wp, ck, ckeep, None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, (H, rows), dev), batch,
         _total_k(total_k, block_table, cu_seqlens_k, rows), total_keep, max_seqlen_k, H, sink, recent, rows, rows_keep,
         None if pages is None else ctypes.pointer(pages), None if pages_keep is None else ctypes.pointer(pages_keep),
-        n, table, _tensor(weights_out, "weights_out", torch.float32, (H, rows_keep), dev),
-        _tensor(key_pos_out, "key_pos_out", torch.int32, (H, rows_keep), dev), None, 0, new_pos and new_w)
-    status, need = relattn_evict_workspace_size(prm)
-    _check(status, "relattn_evict_workspace_size")
-    keep, prm.workspace, prm.workspace_bytes = _workspace(need, workspace, dev)
-    _check(relattn_evict(prm, st), "relattn_evict")
+        n, table, weights_out.data_ptr() if new_w else _tensor(weights_out, "weights_out", torch.float32, (H, rows_keep), dev),
+        key_pos_out.data_ptr() if new_pos else _tensor(key_pos_out, "key_pos_out", torch.int32, (H, rows_keep), dev),
+        None, 0, new_pos and new_w)
+    lib, need, ref = _lib or load_library(), ctypes.c_size_t(), ctypes.byref(prm)
+    _check(lib.relattn_evict_workspace_size(ref, ctypes.byref(need)), "relattn_evict_workspace_size")
+    keep, prm.workspace, prm.workspace_bytes = _workspace(need.value, workspace, dev)
+    _check(lib.relattn_evict(ref, st), "relattn_evict")
     return key_pos_out, weights_out
