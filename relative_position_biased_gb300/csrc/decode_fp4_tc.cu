@@ -385,6 +385,9 @@ __global__ void __launch_bounds__(TDT, 1) relattn_decode_fp4_tc_kernel(const __g
           }
           l0 = z0, l1 = z1;
           tmem_wait_st();
+        } else if (i > 0) {
+          // (a warp without rows follows the products too, one phase at a time)
+          if (!__all_sync(full, mbar_wait(bar(DB_OD), (g - 1) & 1, abort_flag, 43))) return false;
         }
         // ---- NaN blocks of V that the row sees
         if (fa.x | fa.y | fa.z | fa.w) {
@@ -403,10 +406,11 @@ __global__ void __launch_bounds__(TDT, 1) relattn_decode_fp4_tc_kernel(const __g
         mbar_arrive(bar(DB_PF + buf));
       }
       // ---- the piece's result
-      // (the product before the last may be under way too: a wait tells two phases apart)
-      if (!__all_sync(full, mbar_wait(bar(DB_OD), (g - 2) & 1, abort_flag, 44) &&
-                                mbar_wait(bar(DB_OD), (g - 1) & 1, abort_flag, 44)))
-        return false;
+      // (Every warp has seen the product before the last: in this piece's last tile, or
+      // at the end of the piece before.  A parity wait tells only neighbouring
+      // phases apart: one for that product, first polled after the last one too
+      // has completed, would never pass.)
+      if (!__all_sync(full, mbar_wait(bar(DB_OD), (g - 1) & 1, abort_flag, 44))) return false;
       tc_fence_after();
       const float z = l0 + l1;
       const float scale = z == 0.f ? 0.f : (p.kv.v_global ? __ldg(p.kv.v_global + u.h) : 1.f) / z;
