@@ -158,10 +158,13 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
   const unsigned full = 0xffffffffu;
   if (!s.ok) {                               // the same for every CTA of the cluster
     if (rank == 0 && tid == 0) atomicOr(a.err, kDevErrSeqlens);
-    if (rank == 0 && s.d0 >= 0 && s.keep >= 0 && s.d0 + (long)s.keep <= a.total_keep)
-      for (int i = tid; i < s.keep; i += ET) {
-        a.src_row[(long)s.h * a.total_keep + s.d0 + i] = -1;
-        if (s.h == 0) a.dst_row[s.d0 + i] = -1;
+    // Nothing of it is moved: each of its places among the kept rows says so.
+    // (Every place lies in a sequence whose start is not above and whose end is
+    // above it, so none keeps what the workspace held.)
+    if (rank == 0)
+      for (int j = max(s.d0, 0) + tid; j < min(a.cu_keep[s.b + 1], a.total_keep); j += ET) {
+        a.src_row[(long)s.h * a.total_keep + j] = -1;
+        if (s.h == 0) a.dst_row[j] = -1;
       }
     return;
   }

@@ -583,6 +583,26 @@ def test_evict_skips_and_records_bad_lengths():
     assert torch.equal(out[30:, 0], p[20 + torch.from_numpy(idx).cuda(), 0])
 
 
+@pytest.mark.parametrize("max_k", [100, 40000])           # selected by clusters, and by all SMs
+@pytest.mark.parametrize("cu_keep,bad", [([0, 10, 40], 1), ([-5, 10, 30], 0)])
+def test_evict_moves_nothing_of_a_sequence_partly_outside(max_k, cu_keep, bad):
+    """A sequence whose kept rows start before the first or end behind the last
+    place moves no row, whatever the workspace held (here, numbers of rows)."""
+    w = torch.rand(2, 100, device="cuda")
+    p = torch.rand(100, 2, 4, device="cuda")
+    out = torch.full((30, 2, 4), 3.0, device="cuda")
+    cu_k = torch.tensor([0, 20, 100], dtype=torch.int32, device="cuda")
+    work = torch.full((1 << 20,), 3, dtype=torch.int32, device="cuda")
+    pos, wk = rpb.evict([p], [out], w, cu_k, torch.tensor(cu_keep, dtype=torch.int32, device="cuda"), max_seqlen_k=max_k,
+                        recent=30, total_keep=30, workspace=work)
+    torch.cuda.synchronize()
+    assert rpb.relattn_get_device_error() == 6
+    good, skipped = (slice(0, 10), slice(10, 30)) if bad == 1 else (slice(10, 30), slice(0, 10))
+    end = 20 if bad == 1 else 100
+    assert torch.equal(out[good], p[end - (good.stop - good.start):end])      # the newest
+    assert (out[skipped] == 3).all() and (pos[:, skipped] == -1).all() and (wk[:, skipped] == 0).all()
+
+
 # ------------------------------------------------------------------ streams, graphs, runs
 
 def test_captured_calls_replay_and_streams_do_not_share():
