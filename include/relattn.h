@@ -601,6 +601,8 @@ relattn_status relattn_prologue_mxfp8(const relattn_prologue_params *params,
  * bounded limit (about a second): the CTA gives up, drains its own copies and
  * MMAs, frees its tensor memory and exits, and relattn_get_device_error()
  * then returns RELATTN_ERR_TIMEOUT (outputs of affected rows are undefined).
+ * In an eviction whose keys all SMs select, CTA `tile` of each (sequence, kv
+ * head) never arrives where they meet: nothing is moved.
  * tile = -1 restores normal operation; tile < -1 -> RELATTN_ERR_INVALID_ARG. */
 relattn_status relattn_test_skip_k_tile(int32_t tile);
 

@@ -486,6 +486,7 @@ relattn_status validate_evict(const relattn_evict_params *p, EvictArgs *a) {
   a->w_out = p->weights_out;
   a->pos_out = p->key_pos_out;
   a->clear = p->clear_out != 0;
+  a->test_skip_cta = g_test_skip_k_tile;
   a->src_row = static_cast<int32_t *>(p->workspace);
   a->dst_row = a->src_row + (size_t)p->total_keep * p->num_heads_kv;
   if (evict_wide_bytes(p->batch, p->num_heads_kv, p->max_seqlen_k) > 0)

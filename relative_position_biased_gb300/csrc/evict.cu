@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
     // (Every place lies in a sequence whose start is not above and whose end is
     // above it, so none keeps what the workspace held.)
     if (rank == 0)
-      for (int j = max(s.d0, 0) + tid; j < min(a.cu_keep[s.b + 1], a.total_keep); j += ET) {
+      for (long j = max(s.d0, 0) + (long)tid; j < min(a.cu_keep[s.b + 1], a.total_keep); j += ET) {
         a.src_row[(long)s.h * a.total_keep + j] = -1;
         if (s.h == 0) a.dst_row[j] = -1;
       }
@@ -185,6 +185,15 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
       }
     }
     __syncthreads();
+  }
+
+  if (WIDE) {
+    // Should a barrier give up, rows that no CTA got to list are not moved.
+    for (long j = s.d0 + (long)rank * ET + tid; j < s.d0 + s.keep; j += (long)cs * ET) {
+      a.src_row[(long)s.h * a.total_keep + j] = -1;
+      if (s.h == 0) a.dst_row[j] = -1;
+    }
+    if (rank == a.test_skip_cta) return;     // (test hook: never arrives)
   }
 
   // the border: keys above it are kept, and `left` of those on it

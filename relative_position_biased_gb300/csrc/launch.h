@@ -266,6 +266,7 @@ struct EvictArgs {
   unsigned *wide;                // workspace of a wide selection (evict_wide_bytes), zeroed by the launcher
   int ctas;                      // CTAs per (sequence, kv head) in a wide selection (set by the launcher)
   int sms;
+  int test_skip_cta;             // test hook: CTA of a wide selection that never arrives (-1: none)
   int *err;
 };
 size_t evict_wide_bytes(int batch, int Hkv, int max_k);       // 0: one cluster per (sequence, kv head)

@@ -1,12 +1,16 @@
-"""Failure path of the compressed cache's tensor-core kernels, without faulting
-the GPU: a hook of the test build leaves one key tile out, the bounded waits
-behind it run out after about a second, every role stops, tensor memory is
-freed, the host reads RELATTN_ERR_TIMEOUT, and the next call is right."""
+"""Failure paths of the compressed cache's kernels that wait, without faulting
+the GPU: a hook of the test build leaves one key tile out of the tensor-core
+kernels, the bounded waits behind it run out after about a second, every role
+stops, tensor memory is freed, the host reads RELATTN_ERR_TIMEOUT, and the next
+call is right.  In the same way a CTA stays away from an eviction's grid-wide
+selection."""
 import numpy as np
 import pytest
 import torch
 
 import relative_position_biased_gb300 as rpb
+from oracle import kvcache as C
+from relative_position_biased_gb300 import workloads as W
 from tests import kvcache_util as U
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +65,28 @@ def test_key_weights_of_many_rows_give_up_and_recover():
     out = call()
     assert rpb.relattn_get_device_error() == rpb.RELATTN_OK
     U.check_weights(c, d, keys, lse, w_in, 0.0, out)
+
+
+@pytest.mark.parametrize("cta", [0, 5])
+def test_eviction_by_all_sms_gives_up_moves_nothing_and_recovers(cta):
+    """The workspace holds numbers of rows, which nobody takes for a selection's."""
+    lens, keep = [40000, 70], [9000, 40]
+    w = torch.rand(2, sum(lens), device="cuda")
+    p = torch.rand(sum(lens), 2, 4, device="cuda")
+    out = torch.full((sum(keep), 2, 4), 3.0, device="cuda")
+    work = torch.full((1 << 20,), 7, dtype=torch.int32, device="cuda")
+
+    def call():
+        return rpb.evict([p], [out], w, W.cu_seqlens(lens).cuda(), W.cu_seqlens(keep).cuda(), max_seqlen_k=40000,
+                         recent=16, sink=2, total_keep=sum(keep), workspace=work)
+
+    times_out(call, cta)
+    assert (out == 3).all()
+    pos, wk = call()
+    assert rpb.relattn_get_device_error() == rpb.RELATTN_OK
+    for b in range(2):
+        a, o = sum(lens[:b]), sum(keep[:b])
+        for h in range(2):
+            idx = C.kept_keys(w[h, a:a + lens[b]].cpu().numpy(), keep[b], 16, 2)
+            np.testing.assert_array_equal(pos[h, o:o + keep[b]].cpu().numpy(), idx)
+            assert torch.equal(out[o:o + keep[b], h], p[a + torch.from_numpy(idx).cuda(), h])
