@@ -37,11 +37,12 @@ struct Divisor {
     y = __frcp_rn(b);
     plain = !(b > 0x1p-60f && b < 0x1p60f && top < 0x1p60f);
   }
-  // (elements below 2^-60 may lose residual bits to underflow: they are far
-  // below every border, the smallest being 2^-12)
+  // (Elements below 2^-60 may lose residual bits to underflow: they are far
+  // below every border, the smallest being 2^-12.  The residual is taken as b q -
+  // a: of a -0 it is +0, and -0 y - 0 stays -0; a - b q would end as +0.)
   __device__ __forceinline__ float quick(float a) const {
     const float q = __fmul_rn(a, y);
-    return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+    return __fmaf_rn(-__fmaf_rn(q, b, -a), y, q);
   }
   __device__ __forceinline__ void operator()(float (&x)[16], float &top) const {
     if (!plain) {

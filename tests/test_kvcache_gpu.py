@@ -103,6 +103,26 @@ def test_store_rounds_exactly(factor):
     np.testing.assert_array_equal(sv, want_s)
 
 
+@pytest.mark.parametrize("factor", [None, 0.0123, 2.0 ** -20, 3e4, 1e-25])
+def test_store_keeps_the_sign_of_zero(factor):
+    """-0 (and magnitudes that round to it) beside nonzero elements, whichever way
+    the quotient is made."""
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((40, 2, 128)).astype(np.float32)
+    x *= (2.0 ** rng.integers(-60, 60, (40, 2, 8, 1))).repeat(16, 3).reshape(x.shape)
+    x[rng.random(x.shape) < 0.3] = -0.0
+    x[rng.random(x.shape) < 0.2] = 0.0
+    x[rng.random(x.shape) < 0.1] = -1e-38
+    xb = U.bf16(x)
+    f = None if factor is None else np.full(2, factor, np.float32)
+    ck, sk, cv, sv = _store_one(xb, f)
+    want_c, want_s = C.quantize_nvfp4(xb.float().numpy(), f)
+    assert ((want_c & 15) == 8).any() and (want_s > 0).any()
+    for c, s in ((ck, sk), (cv, sv)):
+        np.testing.assert_array_equal(s, want_s)
+        np.testing.assert_array_equal(c, want_c)
+
+
 def test_store_of_infinities_and_nan():
     x = np.ones((3, 1, 128), np.float32)
     x[0, 0, 3] = np.inf
