@@ -153,7 +153,8 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
 
   uint32_t qf[NT][16];
   float coef[NT][2], bscale[NT][2], lse2[NT][2];
-  int qp[NT][2], rrow[NT][2];               // position, row of R
+  int qp[NT][2], rrow[NT][2];               // position (-1: no row, or one that gives nothing), row of R
+  bool whole = true;                        // every slot holds a row that gives something
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int nrow = nt * 8 + g;
@@ -203,12 +204,15 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
       const long grow = unit_row(p, u, live ? m : 0, &tk);
       rrow[nt][c] = (int)grow;
       const float s = live ? log_scale(u.qbase + tk, p.a.inv_ln_base) : 0.f;
-      qp[nt][c] = live ? u.qbase + tk : -1;
       coef[nt][c] = p.a.alpha_log2e * s * kg * bk;
       bscale[nt][c] = s * kLog2e;
-      // a row that saw nothing (lse -inf), and one past the block, give nothing
+      // A row that saw nothing (lse -inf), and one past the block, give nothing:
+      // masked, since 0 times an infinite or NaN key is not 0.
       const float z = live ? __ldg(p.lse + (grow % p.a.Hq) * p.a.total_q + grow / p.a.Hq) : -INFINITY;
-      lse2[nt][c] = z == -INFINITY ? INFINITY : z * kLog2e;
+      const bool gives = z != -INFINITY;
+      whole = whole && gives;
+      qp[nt][c] = gives ? u.qbase + tk : -1;
+      lse2[nt][c] = gives ? z * kLog2e : INFINITY;
     }
   }
   int qmin, qmax, tk_;
@@ -217,6 +221,7 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
   unit_row(p, u, u.nrows - 1, &tk_);
   qmax = u.qbase + tk_;
   const unsigned wlim = p.a.window > 0 ? (unsigned)p.a.window : 0x80000000u;
+  const bool part = !__all_sync(full, whole);
 
   int buf = 0;
   for (int it = 0; it < n; ++it) {
@@ -240,7 +245,7 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
       kp_lane = __ldg(p.key_pos + (long)u.h * p.pages.rows + row0 + lane);
       if (kp_lane < 0) kp_lane = 0x7fffffff;
     }
-    const bool edge = POS || key0 + WK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
+    const bool edge = POS || part || key0 + WK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
     const bool band = p.a.E > 0 && (POS ? __any_sync(full, kp_lane != 0x7fffffff && qmin - kp_lane < p.a.E)
                                         : qmin - (key0 + WK - 1) < p.a.E);
     if (band && !waited) {
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(WT, 3) relattn_key_weights_tiles_kernel(const 
             } else if (band) {
               l = fmaf(y[gr][2 * hf + c], bs, l);
             }
-            if (edge && d >= wlim) l = -INFINITY;
+            if ((edge && d >= wlim) || lse2 == INFINITY) l = -INFINITY;   // (0 times a NaN key is not 0)
             v[2 * gr + hf] += fast_exp2(l);
           }
       }

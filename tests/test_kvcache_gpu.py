@@ -482,6 +482,50 @@ def test_rows_without_a_logsumexp_and_nan_keys(kind):
         assert np.allclose(host(w)[0, :199], want[:199], rtol=1e-4, atol=1e-30)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("q_len,Hq,positions", [(0, 4, False), (1, 1, False), (1, 4, False), (2, 8, False), (3, 4, False),
+                                                (9, 4, False), (40, 4, False), (1, 4, True), (40, 4, True)])
+def test_nan_keys_that_only_silent_rows_see(kind, q_len, Hq, positions):
+    """NaN keys in the sight of nobody but rows with lse = -inf, slots without a row
+    and a sequence without rows: their weights decay like all others."""
+    c = U.Case((q_len, 1), (700, 300), Hq, 1, E=0, r_dim=0, positions=positions)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    bad = [3, 150, 699 - q_len]                          # of the first sequence
+    if kind == "bf16":
+        d["k"][bad] = float("nan")
+        d["k"][200] = float("inf")
+        bad.append(200)
+        k = d["k"].cuda()
+    else:
+        qc["k_scale"][bad] = 0x7F
+        k = U.device_cache(qc, d)
+    lse = np.full((Hq, q_len + 1), -np.inf, np.float32)
+    lse[:, q_len:] = 5.0                                 # the second sequence's row votes
+    w_in = np.random.default_rng(9).uniform(1, 9, (1, 1000)).astype(np.float32)
+    w = rpb.key_weights(d["q"].cuda(), k, None, None, torch.from_numpy(lse).cuda(), d["cu_q"].cuda(), d["cu_k"].cuda(),
+                        weights_in=torch.from_numpy(w_in).cuda(), decay=0.5, **U.call_kw(c, d))
+    ok()
+    want = 0.5 * w_in[0, :700]
+    want[700 - q_len:] = 0
+    np.testing.assert_array_equal(host(w)[0, :700], want)
+    assert np.isfinite(host(w)[0, 700:]).all() and (host(w)[0, 700:] > 0).any()
+
+
+@pytest.mark.parametrize("Hq", [1, 3, 8])
+def test_a_key_of_logit_minus_infinity_has_no_weight(Hq):
+    """An infinite element that every row answers with -inf: weight 0, in slots
+    without a row too."""
+    c = U.Case((1,), (300,), Hq, 1, E=0, r_dim=0)
+    d = U.make(c)
+    d["k"][40, 0, 7] = float("inf")
+    d["q"][:, :, 7] = -1.0
+    w = rpb.key_weights(d["q"].cuda(), d["k"].cuda(), None, None, torch.full((Hq, 1), 5.0, device="cuda"),
+                        d["cu_q"].cuda(), d["cu_k"].cuda(), **U.call_kw(c, d))
+    ok()
+    assert host(w)[0, 40] == 0 and np.isfinite(host(w)).all() and (np.delete(host(w)[0], 40) > 0).all()
+
+
 # ------------------------------------------------------------------ eviction
 
 def _planes(rows, Hkv, kinds, seed=0):
