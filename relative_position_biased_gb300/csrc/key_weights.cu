@@ -221,7 +221,7 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
   unit_row(p, u, u.nrows - 1, &tk_);
   qmax = u.qbase + tk_;
   const unsigned wlim = p.a.window > 0 ? (unsigned)p.a.window : 0x80000000u;
-  const bool part = !__all_sync(full, whole);
+  if (!__all_sync(full, whole)) qmax = -1;   // every key needs the mask
 
   int buf = 0;
   for (int it = 0; it < n; ++it) {
@@ -245,7 +245,7 @@ __device__ __forceinline__ void weigh_piece(const KeyWeightArgs &p, const Unit &
       kp_lane = __ldg(p.key_pos + (long)u.h * p.pages.rows + row0 + lane);
       if (kp_lane < 0) kp_lane = 0x7fffffff;
     }
-    const bool edge = POS || part || key0 + WK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
+    const bool edge = POS || key0 + WK - 1 > qmin || (unsigned)(qmax - key0) >= wlim;
     const bool band = p.a.E > 0 && (POS ? __any_sync(full, kp_lane != 0x7fffffff && qmin - kp_lane < p.a.E)
                                         : qmin - (key0 + WK - 1) < p.a.E);
     if (band && !waited) {
