@@ -321,6 +321,9 @@ relattn_status relattn_decode_nvfp4_workspace_size(const relattn_params *params,
  * prompt, or (cu_seqlens_q over the last n rows of q and lse) an observation
  * window.  A cache row belongs to one sequence: a page that two block tables
  * share would receive the weights of either.
+ * With more than 16 rows per kv head, or a batch above 384, max_seqlen_k / 128 x
+ * batch x num_heads_kv must stay below 2^31 (of a contiguous cache, its rows
+ * count where max_seqlen_k is larger).
  * fwd: q, k, r, P, lengths, masks and lse (an input) as in relattn_prefill;
  * v, out, workspace and num_splits are ignored.  cache = NULL reads the keys
  * from fwd.k (bf16 rows, contiguous or paged).  weights_out may equal

@@ -3,6 +3,7 @@
 // relattn_get_device_error), no host fallback.
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -851,9 +852,16 @@ relattn_status relattn_key_weights(const relattn_key_weights_params *p, void *st
   const size_t n = (size_t)rows * f.num_heads_kv * sizeof(float);
   if (p->weights_in && p->weights_in != p->weights_out && overlaps(p->weights_in, n, p->weights_out, n))
     return RELATTN_ERR_INVALID_ARG;
+  // no sequence is longer than the cache (checked on the device): a bound far above
+  // the lengths would only make units of work without a key
+  const long max_k = p->pages ? f.max_seqlen_k : std::min<int64_t>(f.max_seqlen_k, rows);
+  if (!key_weights_walked(key_weight_sizes(f)) &&
+      (max_k + kWalkTile - 1) / kWalkTile * f.batch * f.num_heads_kv > 0x7fffffffL)
+    return RELATTN_ERR_UNSUPPORTED;
   const size_t need = key_weights_workspace(key_weight_sizes(f), p->positions != nullptr);
   if (need > 0 && (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < need)) return RELATTN_ERR_WORKSPACE;
   if ((st = make_args(&f, &x.a)) != RELATTN_OK) return st;
+  x.a.max_k = (int)max_k;
   x.a.rdec = static_cast<const float *>(p->workspace);
   x.lse = f.lse;
   x.w_in = p->weights_in;

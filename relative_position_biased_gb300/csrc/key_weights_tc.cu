@@ -78,6 +78,12 @@ constexpr uint32_t KW_DONE = KW_ABORT + 4;   // steps that the issuer has begun
 constexpr uint32_t KW_SMEM = KW_ABORT + 8 + 1024;
 static_assert(KW_SMEM <= 227 * 1024, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_R = 256;     // TMEM columns
+// Waits for a planned tile last as long as the scheduler passes over units that
+// have none: max_seqlen_k may be far above the lengths, a grid has up to 2^31
+// units, and one takes 0.9 us of an SM (400 million: 2.4 s).  The scheduler's own
+// waits are short, and one that gives up ends these too, so this is only the last
+// resort: 40 s.
+constexpr long long kPlanCycles = 80000000000ll;
 
 __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -269,7 +275,7 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + KW_SLOT);
   // A wait that may last a tile: it gives up a second after the issuer's last step.
-  auto wait_long = [&](int b, uint32_t parity, int site) {
+  auto wait_long = [&](int b, uint32_t parity, int site, long long limit = 2000000000ll) {
     long long t0 = clock64();
     int seen = *begun;
     while (!mbar_try_wait(bar(b), parity, 2000u)) {
@@ -277,7 +283,7 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
       if (*begun != seen) {
         seen = *begun;
         t0 = clock64();
-      } else if (clock64() - t0 > 2000000000ll) {
+      } else if (clock64() - t0 > limit) {
         *abort_flag = site;
         return false;
       }
@@ -287,7 +293,7 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
   // The k-th tile of this CTA, by a whole warp, or by one lane; false: there is none.
   auto next_tile = [&](int k, bool one_lane, Tile &t) {
     const int s = k % UST;
-    bool got = wait_long(BU_FULL + s, (k / UST) & 1, 30);
+    bool got = wait_long(BU_FULL + s, (k / UST) & 1, 30, kPlanCycles);
     if (!one_lane) got = __all_sync(0xffffffffu, got);
     if (!got) return false;
     const uint4 *src = reinterpret_cast<const uint4 *>(smem + KW_UNIT + 64 * s);
@@ -471,7 +477,8 @@ relattn_key_weights_tc_kernel(const __grid_constant__ KeyWeightArgs p, const __g
     // The k-th tile stays in its slot until this warp is done with it.
     auto tile_at = [&](int k) { return reinterpret_cast<const volatile Tile *>(smem + KW_UNIT + 64 * (k % UST)); };
     auto wait_tile = [&](int k) {
-      return __all_sync(0xffffffffu, mbar_wait(bar(BU_FULL + k % UST), (k / UST) & 1, abort_flag, 30)) && tile_at(k)->more;
+      return __all_sync(0xffffffffu, mbar_wait(bar(BU_FULL + k % UST), (k / UST) & 1, abort_flag, 30, kPlanCycles)) &&
+             tile_at(k)->more;
     };
     auto unit_at = [&](const volatile Tile *t) {
       Unit u = {};
@@ -636,8 +643,7 @@ cudaError_t launch_nb(const KeyWeightArgs &p, cudaStream_t stream, const CUtenso
   const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), (int)KW_SMEM, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const long grid = ((long)p.a.max_k + kWalkTile - 1) / kWalkTile * p.a.batch * p.a.Hkv;
-  if (grid > 0x7fffffffL) return cudaErrorInvalidValue;
+  const long grid = ((long)p.a.max_k + kWalkTile - 1) / kWalkTile * p.a.batch * p.a.Hkv;      // (the host keeps it below 2^31)
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(KWT);
   cfg.dynamicSmemBytes = KW_SMEM;

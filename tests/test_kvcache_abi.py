@@ -112,6 +112,21 @@ def test_key_weights_refuse(p, want):
     assert rpb.relattn_key_weights(p()) == want
 
 
+def test_key_weights_refuse_more_units_than_a_grid_holds():
+    """2^24 tiles of 128 keys for each of 130 heads; of a contiguous cache its rows
+    count, and few rows are walked whatever the bound."""
+    many = dict(out=None, v=None, batch=65, total_q=65 * 20, max_seqlen_q=20, max_seqlen_k=(1 << 31) - (1 << 16))
+    wide = ctypes.pointer(pages(page_size=1 << 20, num_pages=1, max_pages_per_seq=1 << 11))
+    big = ctypes.pointer(cache(rows=1 << 20))
+    for c in (None, big):
+        p = weights(f=fwd(**many), cache=c, pages=wide, weights_in=None, workspace_bytes=1 << 40)
+        assert rpb.relattn_key_weights(p) == UNSUPPORTED
+    # (these pass the check and stop at the next one)
+    assert rpb.relattn_key_weights(weights(f=fwd(**many), workspace=None)) == WORKSPACE
+    few = dict(many, max_seqlen_q=1, total_q=65)
+    assert rpb.relattn_key_weights(weights(f=fwd(**few), cache=big, pages=wide, weights_in=None, workspace=None)) == WORKSPACE
+
+
 def evict(**kw):
     d = dict(weights=A, cu_seqlens_k=2 * A, cu_seqlens_keep=3 * A, key_pos=None, batch=2, total_k=600, total_keep=100,
              max_seqlen_k=400, num_heads_kv=2, sink=4, recent=16, rows=600, rows_keep=100, pages=None, pages_keep=None,

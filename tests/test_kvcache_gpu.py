@@ -452,6 +452,31 @@ def test_key_weights_of_more_tiles_than_sms(kind, E, page, window):
     assert (host(out)[:, ~held] == 7).all()
 
 
+@pytest.mark.parametrize("page", [0, 1024])
+@pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
+def test_key_weights_under_a_bound_far_above_the_lengths(kind, page):
+    """max_seqlen_k is a bound only.  Paged, it makes 400 million units, nearly all
+    without a tile: passing over them takes seconds, and no wait gives up."""
+    c = U.Case((20, 17, 40, 33, 18, 64), (500, 700, 40, 90, 1025, 64), 8, 4, E=64, page=page)
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    keys = qc["k_values"] if kind == "nvfp4" else d["k"].double().numpy()
+    k = U.device_cache(qc, d) if kind == "nvfp4" else d["k"].cuda()
+    lse = np.full((c.Hq, sum(c.q_lens)), 6.0, np.float32)
+    kw = U.call_kw(c, d)
+    kw["max_seqlen_k"] = (1 << 31) - (1 << 16)
+    if page:
+        wide = torch.full((6, 1 << 21), -1, dtype=torch.int32, device="cuda")
+        wide[:, :d["table"].shape[1]] = d["table"].cuda()
+        kw["block_table"] = wide
+    out = torch.full((c.Hkv, d["rows"]), 7.0, device="cuda")
+    rpb.key_weights(d["q"].cuda(), k, d["r"].cuda(), d["P"].cuda(), torch.from_numpy(lse).cuda(), d["cu_q"].cuda(),
+                    d["cu_k"].cuda(), decay=0.0, out=out, **kw)
+    ok()
+    held = U.check_weights(c, d, keys, lse, None, 0.0, out)
+    assert (host(out)[:, ~held] == 7).all()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
 def test_rows_without_a_logsumexp_and_nan_keys(kind):
     """A row with lse = -inf gives nothing, and a NaN key spoils its own weight
