@@ -872,6 +872,7 @@ def _workspace(nbytes: int, workspace, device):
         workspace = torch.empty(words, dtype=torch.float32, device=device)
         return workspace, workspace.data_ptr(), 4 * words
     _need(workspace.device == device, "workspace is on another device")
+    _need(workspace.is_contiguous(), "workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

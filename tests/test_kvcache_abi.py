@@ -217,3 +217,13 @@ def test_python_checks_name_the_argument():
         rpb.store_nvfp4(k, k, cu, cu, tuple(c))
     with pytest.raises(ValueError, match="page_size"):
         rpb.store_nvfp4(k, k, cu, cu, c, block_table=torch.zeros(1, 2, dtype=torch.int32), page_size=48)
+
+
+def test_a_workspace_is_one_block_of_memory():
+    """A strided tensor's elements are not the bytes the library would write."""
+    cpu = torch.device("cpu")
+    for w in (torch.zeros(64, 4)[:, :2], torch.zeros(256)[::2], torch.zeros(1).expand(256)):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            rpb._workspace(512, w, cpu)
+    w = torch.zeros(256)[128:]
+    assert rpb._workspace(512, w, cpu) == (w, w.data_ptr(), 512)
