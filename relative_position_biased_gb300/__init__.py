@@ -684,6 +684,13 @@ class KvNvfp4(_KvTensors):
         self.c_pointer = ctypes.pointer(self.c_struct)
         return self
 
+    @classmethod
+    def _make(cls, tensors):                 # (_replace makes its result through it)
+        return cls(*tensors)
+
+    def __reduce__(self):                    # copies and pickles too
+        return type(self), tuple(self)
+
 
 def empty_nvfp4(rows: int, num_heads_kv: int, device, k_global=None, v_global=None) -> KvNvfp4:
     """A cache of ``rows`` rows, zeroed (every value reads 0 until it is stored)."""

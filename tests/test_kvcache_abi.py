@@ -1,6 +1,8 @@
 """Refusals of the compressed-cache entry points (no GPU needed: every one is
 decided on the host before a device is touched)."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -227,3 +229,20 @@ def test_a_workspace_is_one_block_of_memory():
             rpb._workspace(512, w, cpu)
     w = torch.zeros(256)[128:]
     assert rpb._workspace(512, w, cpu) == (w, w.data_ptr(), 512)
+
+
+def test_caches_made_from_a_cache_are_checked_too():
+    c = rpb.empty_nvfp4(64, 2, "cpu")
+    g = torch.ones(2)
+    other = rpb.empty_nvfp4(64, 2, "cpu")
+    d = c._replace(k=other.k, k_global=g)
+    assert isinstance(d, rpb.KvNvfp4) and (d.rows, d.num_heads_kv, d.device) == (64, 2, c.device)
+    assert (d.c_struct.k, d.c_struct.k_global, d.c_struct.v) == (other.k.data_ptr(), g.data_ptr(), c.v.data_ptr())
+    with pytest.raises(ValueError, match="cache.v must have shape"):
+        c._replace(v=c.v[:32])
+    with pytest.raises(ValueError, match="cache.k_global must be torch.float32"):
+        c._replace(k_global=g.double())
+    assert rpb.KvNvfp4._make(tuple(c)).c_struct.k == c.k.data_ptr()
+    assert copy.copy(c).c_struct.k == c.k.data_ptr()
+    for e in (copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
+        assert e.c_struct.k == e.k.data_ptr() != c.k.data_ptr() and e.rows == 64
