@@ -666,23 +666,28 @@ class _KvTensors(NamedTuple):
 class KvNvfp4(_KvTensors):
     """A 4-bit (NVFP4) K / V cache: code bytes k / v uint8 [rows, Hkv, 64], E4M3
     scale bytes k_scale / v_scale uint8 [rows, Hkv, 8], and optional fp32 [Hkv]
-    factors (None: 1).  The tensors are checked here, once."""
+    factors (None: 1).  The tensors are checked here, and again by a call that
+    finds one of them at another address (``t.data = ...``, ``t.set_(...)``)."""
 
     def __new__(cls, k, v, k_scale, v_scale, k_global=None, v_global=None):
+        self = super().__new__(cls, k, v, k_scale, v_scale, k_global, v_global)
+        self.c_struct = RelattnKvNvfp4()
+        self.c_pointer = ctypes.pointer(self.c_struct)
+        self._bind()
+        return self
+
+    def _bind(self) -> None:
         import torch
-        dev = k.device
+        k, dev = self.k, self.k.device
         _need(k.dim() == 3, "cache.k must have three dimensions")
         rows, H = (int(x) for x in k.shape[:2])
-        ptr = {}
-        for n, t, w in (("k", k, 64), ("v", v, 64), ("k_scale", k_scale, 8), ("v_scale", v_scale, 8)):
-            ptr[n] = _tensor(t, f"cache.{n}", torch.uint8, (rows, H, w), dev)
-        for n, t in (("k_global", k_global), ("v_global", v_global)):
-            ptr[n] = None if t is None else _tensor(t, f"cache.{n}", torch.float32, (H,), dev)
-        self = super().__new__(cls, k, v, k_scale, v_scale, k_global, v_global)
+        ptr = [_tensor(t, f"cache.{n}", torch.uint8, (rows, H, w), dev)
+               for n, t, w in zip(self._fields, self, (64, 64, 8, 8))]
+        ptr += [None if t is None else _tensor(t, f"cache.{n}", torch.float32, (H,), dev)
+                for n, t in zip(self._fields[4:], self[4:])]
         self.rows, self.num_heads_kv, self.device = rows, H, dev
-        self.c_struct = RelattnKvNvfp4(rows=rows, **ptr)
-        self.c_pointer = ctypes.pointer(self.c_struct)
-        return self
+        self.c_struct.__init__(*ptr, rows)
+        self.data_ptrs, self.addresses = [t.data_ptr for t in self if t is not None], [x for x in ptr if x is not None]
 
     @classmethod
     def _make(cls, tensors):                 # (_replace makes its result through it)
@@ -746,6 +751,8 @@ def _lengths(cu_q, cu_k, name_q: str, name_k: str, device):
 def _cache(cache: KvNvfp4, device) -> None:
     if not isinstance(cache, KvNvfp4):
         raise ValueError("cache must be a KvNvfp4")
+    if [f() for f in cache.data_ptrs] != cache.addresses:
+        cache._bind()
     if cache.device != device:
         raise ValueError(f"the cache is on {cache.device}, not {device}")
 

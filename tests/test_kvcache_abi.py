@@ -246,3 +246,20 @@ def test_caches_made_from_a_cache_are_checked_too():
     assert copy.copy(c).c_struct.k == c.k.data_ptr()
     for e in (copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
         assert e.c_struct.k == e.k.data_ptr() != c.k.data_ptr() and e.rows == 64
+
+
+def test_a_cache_follows_its_tensors_to_other_memory():
+    """Memory that a tensor has left is never passed to the library."""
+    g = torch.ones(2)
+    c = rpb.empty_nvfp4(64, 2, "cpu", k_global=g)
+    other = rpb.empty_nvfp4(64, 2, "cpu")
+    c.k.data = other.k
+    c.v_scale.set_(other.v_scale)
+    g.data = torch.full((2,), 2.0)
+    rpb._cache(c, c.device)
+    s = c.c_struct
+    assert (s.k, s.v, s.k_scale, s.v_scale, s.k_global, s.v_global, s.rows) == (
+        other.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(), other.v_scale.data_ptr(), g.data_ptr(), None, 64)
+    c.v.data = torch.zeros(32, 2, 64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="cache.v must have shape"):
+        rpb._cache(c, c.device)

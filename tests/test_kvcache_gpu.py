@@ -72,6 +72,22 @@ def test_store_writes_the_chunk_rows_and_no_others(q_lens, k_lens, Hkv, page, fa
         assert (np.abs(host(got.double()) - ref) <= np.abs(ref) * (2.0 ** -8 * (1 + 2.0 ** -20) + 2.0 ** -24)).all()
 
 
+def test_calls_follow_a_cache_to_other_memory():
+    x = U.bf16(np.ones((40, 1, 128))).cuda()
+    cu = W.cu_seqlens([40]).cuda()
+    cache = rpb.empty_nvfp4(40, 1, "cuda")
+    left = [cache.k.view(cache.k.shape), cache.k_scale.view(cache.k_scale.shape)]      # (kept alive)
+    rpb.store_nvfp4(x, x, cu, cu, cache)
+    cache.k.data = torch.zeros_like(cache.k)
+    cache.k_scale.set_(torch.zeros_like(cache.k_scale))
+    rpb.store_nvfp4(2 * x, 2 * x, cu, cu, cache)
+    ok()
+    assert torch.equal(cache.k, left[0]) and not torch.equal(cache.k_scale, left[1]) and (cache.k_scale != 0).all()
+    k, v = rpb.load_nvfp4(cache, cu, cu, total_q=40)
+    ok()
+    assert torch.equal(k, v) and (k > 1.5).all()
+
+
 def _store_one(x, factor=None):
     n = x.shape[0]
     cu = W.cu_seqlens([n]).cuda()
