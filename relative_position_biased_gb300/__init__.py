@@ -856,6 +856,8 @@ def load_nvfp4(cache: KvNvfp4, cu_seqlens_q, cu_seqlens_k, *, total_q: int, bloc
     """The last cu_seqlens_q rows of every sequence as bf16 (k, v) [total_q, Hkv,
     128] (pass cu_seqlens_k twice for all of them)."""
     import torch
+    if not isinstance(cache, KvNvfp4):
+        raise ValueError("cache must be a KvNvfp4")
     st = _stream_here(cache.device, stream)
     if st is None:
         with _switched(cache.device, stream):

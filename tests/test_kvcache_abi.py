@@ -263,3 +263,16 @@ def test_a_cache_follows_its_tensors_to_other_memory():
     c.v.data = torch.zeros(32, 2, 64, dtype=torch.uint8)
     with pytest.raises(ValueError, match="cache.v must have shape"):
         rpb._cache(c, c.device)
+
+
+def test_every_call_names_a_wrong_cache():
+    c = rpb.empty_nvfp4(64, 2, "cpu")
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    k = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    for wrong in (tuple(c), None, c.k):
+        with pytest.raises(ValueError, match="cache must be a KvNvfp4"):
+            rpb.load_nvfp4(wrong, cu, cu, total_q=4)
+        with pytest.raises(ValueError, match="cache must be a KvNvfp4"):
+            rpb.store_nvfp4(k, k, cu, cu, wrong)
+    with pytest.raises(ValueError, match="CUDA"):
+        rpb.load_nvfp4(c, cu, cu, total_q=4)
