@@ -995,13 +995,15 @@ _NO_PLANES = RelattnPlane * MAX_PLANES
 def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seqlen_k: int, recent: int, sink: int = 0,
           total_keep: int, total_k: Optional[int] = None, key_pos=None, block_table=None, page_size: int = 0,
           block_table_keep=None, page_size_keep: int = 0, key_pos_out=None, weights_out=None, workspace=None,
-          stream: Optional[int] = None):
+          rows_keep: Optional[int] = None, stream: Optional[int] = None):
     """Keeps, per sequence and kv head, the newest ``recent`` keys, the first
     ``sink`` and the heaviest of the rest (``weights`` fp32 [Hkv, rows]) -- in
     all cu_seqlens_keep[b+1] - cu_seqlens_keep[b] of sequence b -- and copies
     their rows of every plane [rows, Hkv, ...] into ``dst_planes``, in order of
     index.  Returns (key_pos [Hkv, rows_keep] int32, weights [Hkv, rows_keep])
-    of the new cache."""
+    of the new cache.  ``rows_keep``, the rows of the new cache, is that of
+    ``dst_planes``; without planes it may be given (a paged destination needs
+    it) and is else ``total_keep``."""
     import torch
     dev = weights.device
     st = _stream_here(dev, stream)
@@ -1011,13 +1013,17 @@ def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seq
                          recent=recent, sink=sink, total_keep=total_keep, total_k=total_k, key_pos=key_pos,
                          block_table=block_table, page_size=page_size, block_table_keep=block_table_keep,
                          page_size_keep=page_size_keep, key_pos_out=key_pos_out, weights_out=weights_out,
-                         workspace=workspace)
+                         workspace=workspace, rows_keep=rows_keep)
     n = len(planes)
     if not n == len(dst_planes) <= MAX_PLANES:
         raise ValueError(f"as many dst_planes as planes, at most {MAX_PLANES}")
     H, rows = _shape(weights, "weights", 2)
     batch, ck, ckeep = _lengths(cu_seqlens_k, cu_seqlens_keep, "cu_seqlens_k", "cu_seqlens_keep", dev)
-    rows_keep = dst_planes[0].shape[0] if n else int(total_keep)
+    if n:
+        _need(rows_keep is None or rows_keep == dst_planes[0].shape[0], "rows_keep is not that of dst_planes")
+        rows_keep = dst_planes[0].shape[0]
+    else:
+        rows_keep = int(total_keep if rows_keep is None else rows_keep)
     wp = _tensor(weights, "weights", torch.float32, (H, rows), dev)
     table = _NO_PLANES()
     for i in range(n):

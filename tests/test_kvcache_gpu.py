@@ -650,6 +650,33 @@ def test_evict_of_equal_weights_keeps_the_first():
     assert torch.equal(pos[0].cpu(), torch.arange(777, dtype=torch.int32))
 
 
+def test_evict_without_planes_into_pages():
+    """Positions and weights alone, at the rows of a paged cache: rows_keep says how
+    many it has."""
+    lens, keep, Hkv = (300, 170), (40, 33), 2
+    rows_to, table, where = U.rows_of(keep, 32, 4)
+    w = torch.rand(Hkv, sum(lens), device="cuda")
+    args = (w, W.cu_seqlens(lens).cuda(), W.cu_seqlens(keep).cuda())
+    kw = dict(max_seqlen_k=300, recent=8, sink=2, total_keep=sum(keep), block_table_keep=table.cuda(), page_size_keep=32)
+    pos, wk = rpb.evict([], [], *args, rows_keep=rows_to, **kw)
+    ok()
+    assert pos.shape == wk.shape == (Hkv, rows_to)
+    used = np.zeros(rows_to, bool)
+    for b in range(2):
+        used[where[b]] = True
+        for h in range(Hkv):
+            v = host(w)[h, sum(lens[:b]):sum(lens[:b]) + lens[b]]
+            idx = C.kept_keys(v, keep[b], 8, 2)
+            np.testing.assert_array_equal(host(pos)[h, where[b]], idx)
+            np.testing.assert_array_equal(host(wk)[h, where[b]], v[idx])
+    assert (host(pos)[:, ~used] == -1).all() and (host(wk)[:, ~used] == 0).all()
+    with pytest.raises(ValueError, match="rows must be a multiple of page_size"):
+        rpb.evict([], [], *args, **kw)
+    p = torch.zeros(sum(lens), Hkv, 4, device="cuda")
+    with pytest.raises(ValueError, match="rows_keep"):
+        rpb.evict([p], [p.new_zeros(rows_to, Hkv, 4)], *args, rows_keep=rows_to - 32, **kw)
+
+
 @pytest.mark.parametrize("given", [(True, True), (True, False), (False, True)])
 def test_evict_keeps_what_given_outputs_hold_elsewhere(given):
     w = torch.rand(2, 300, device="cuda")
