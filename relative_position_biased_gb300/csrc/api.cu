@@ -440,7 +440,8 @@ relattn_status validate_evict(const relattn_evict_params *p, EvictArgs *a) {
       p->sink < 0 || p->recent < 0 || p->num_planes < 0 || p->num_planes > RELATTN_MAX_PLANES ||
       p->total_keep > p->total_k)
     return RELATTN_ERR_INVALID_ARG;
-  if ((long)p->batch * p->num_heads_kv > 0x0fffffffL || p->max_seqlen_k > kMaxKeys) return RELATTN_ERR_UNSUPPORTED;
+  // (a grid holds 16 CTAs of each sequence and kv head)
+  if ((long)p->batch * p->num_heads_kv > 0x07ffffffL || p->max_seqlen_k > kMaxKeys) return RELATTN_ERR_UNSUPPORTED;
   *a = EvictArgs{};
   relattn_status st = cache_pages(p->pages, p->rows, p->max_seqlen_k, &a->src);
   if (st == RELATTN_OK) st = cache_pages(p->pages_keep, p->rows_keep, 0, &a->dst);

@@ -509,8 +509,7 @@ cudaError_t launch_evict(const EvictArgs &args, cudaStream_t stream) {
   // while 16K keys are enough, else of 1024
   int cs = 1;
   while (cs < kMaxCluster && a.max_k > cs * 16384) cs *= 2;
-  const long units = (long)a.batch * a.Hkv;
-  if (units * cs > 0x7fffffffL) return cudaErrorInvalidValue;
+  const long units = (long)a.batch * a.Hkv;   // (the host keeps units x kMaxCluster below 2^31)
   const long chunk = ((a.max_k + cs - 1) / cs + 31) & ~31L;
   cudaError_t e;
   if (a.wide) {

@@ -158,6 +158,12 @@ def test_evict_refuses(kw, want):
     assert rpb.relattn_evict(evict(**kw)) == want
 
 
+def test_evict_refuses_more_units_than_a_grid_holds():
+    """16 CTAs each of 2^27 (sequence, kv head) pairs: before anything is launched."""
+    for batch, want in ((1 << 26, UNSUPPORTED), ((1 << 26) - 1, WORKSPACE)):
+        assert rpb.relattn_evict(evict(batch=batch, max_seqlen_k=400, clear_out=1, workspace=None)) == want
+
+
 def test_empty_calls_are_accepted():
     assert rpb.relattn_decode_nvfp4(fwd(batch=0, total_q=0), cache()) == 0
     assert rpb.relattn_store_nvfp4(rows(batch=0)) == 0
