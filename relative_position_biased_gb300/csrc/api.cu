@@ -872,7 +872,8 @@ relattn_status relattn_key_weights(const relattn_key_weights_params *p, void *st
 }
 
 relattn_status relattn_evict_workspace_size(const relattn_evict_params *p, size_t *bytes) {
-  if (!p || !bytes || p->total_keep < 0 || p->num_heads_kv <= 0) return RELATTN_ERR_INVALID_ARG;
+  if (!p || !bytes || p->batch < 0 || p->total_keep < 0 || p->max_seqlen_k < 0 || p->num_heads_kv <= 0)
+    return RELATTN_ERR_INVALID_ARG;
   *bytes = evict_bytes(*p);
   return RELATTN_OK;
 }

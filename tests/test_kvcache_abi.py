@@ -164,6 +164,12 @@ def test_evict_refuses_more_units_than_a_grid_holds():
         assert rpb.relattn_evict(evict(batch=batch, max_seqlen_k=400, clear_out=1, workspace=None)) == want
 
 
+def test_evict_workspace_size_refuses_negative_sizes():
+    for kw in (dict(batch=-1), dict(max_seqlen_k=-1), dict(total_keep=-1), dict(num_heads_kv=0)):
+        assert rpb.relattn_evict_workspace_size(evict(**kw))[0] == INVALID
+    assert rpb.relattn_evict_workspace_size(evict(batch=-1, max_seqlen_k=40000))[0] == INVALID
+
+
 def test_empty_calls_are_accepted():
     assert rpb.relattn_decode_nvfp4(fwd(batch=0, total_q=0), cache()) == 0
     assert rpb.relattn_store_nvfp4(rows(batch=0)) == 0
