@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(ET, 1024 / ET) relattn_evict_select_kernel(con
 // the fastest block index: the heads of a row share lines.
 struct MoveArgs {
   const int32_t *src_row, *dst_row, *cu_keep;
-  int batch, total_keep, Hkv, planes;
+  int batch, total_keep, Hkv;
   long src_rows, dst_rows;
   const uint8_t *from[kMaxPlanes];
   uint8_t *to[kMaxPlanes];
@@ -533,7 +533,6 @@ cudaError_t launch_evict(const EvictArgs &args, cudaStream_t stream) {
   m.batch = a.batch;
   m.total_keep = a.total_keep;
   m.Hkv = a.Hkv;
-  m.planes = a.planes;
   m.src_rows = a.src.rows;
   m.dst_rows = a.dst.rows;
   long grid = 0;
