@@ -74,9 +74,16 @@ __device__ __forceinline__ int last_not_above(const int *v, int n, int x) {
   return lo;
 }
 
+// Sums of tile counts stop at kTooMany: cu_seqlens in order hold fewer than 2^31
+// keys, 2^27 weighted tiles.  Lengths that each pass the checks may be more
+// together (entries out of order, pages listed twice), and an int would overflow.
+constexpr int kTooMany = 1 << 30;
+__device__ __forceinline__ int add_tiles(int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)kTooMany); }
+
 // Running (weighted) tile counts of the sequences into prefix[0 .. batch] (batch <=
 // kWalkBatch), by a CTA of THREADS; returns the total.  Inconsistent sequences
-// hold no tile and are recorded once.
+// hold no tile and are recorded once; with too many tiles there is nothing to do,
+// which is recorded too.
 template <int THREADS>
 __device__ __forceinline__ int tile_prefix(const WalkArgs &p, int *prefix, int *wsum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -99,19 +106,23 @@ __device__ __forceinline__ int tile_prefix(const WalkArgs &p, int *prefix, int *
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+      if (lane >= o) inc = add_tiles(inc, y);
     }
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    int before = base, all = 0;
+    int before = base, all = base;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) before += wsum[w];
-      all += wsum[w];
+      if (w < warp) before = add_tiles(before, wsum[w]);
+      all = add_tiles(all, wsum[w]);
     }
     if (b < p.a.batch) prefix[b] = before + inc - n;
-    base += all;
+    base = all;
     __syncthreads();
+  }
+  if (base == kTooMany) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(p.a.err, kDevErrSeqlens);
+    base = 0;
   }
   if (tid == 0) prefix[p.a.batch] = base;
   __syncthreads();

@@ -567,6 +567,26 @@ def test_a_key_of_logit_minus_infinity_has_no_weight(Hq):
     assert host(w)[0, 40] == 0 and np.isfinite(host(w)).all() and (np.delete(host(w)[0], 40) > 0).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
+def test_key_weights_of_lengths_that_cannot_be_side_by_side(kind):
+    """cu_seqlens_k out of order: every second sequence passes the checks by itself,
+    together they have more keys than 32 bits count.  Nothing is done."""
+    batch, page = 300, 1 << 20
+    cu_k = torch.tensor([0, (1 << 31) - (1 << 16)] * (batch // 2) + [0], dtype=torch.int32, device="cuda")
+    table = torch.full((batch, 1 << 11), -1, dtype=torch.int32, device="cuda")
+    q = torch.ones(batch, 8, 128, dtype=torch.bfloat16, device="cuda")
+    k = torch.ones(page, 1, 128, dtype=torch.bfloat16, device="cuda")
+    if kind == "nvfp4":
+        k = rpb.empty_nvfp4(page, 1, "cuda")
+    out = torch.full((1, page), 7.0, device="cuda")
+    rpb.key_weights(q, k, None, None, torch.zeros(8, batch, device="cuda"),
+                    torch.arange(batch + 1, dtype=torch.int32, device="cuda"), cu_k, max_seqlen_q=1,
+                    max_seqlen_k=(1 << 31) - (1 << 16), alpha=0.1, out=out, total_k=page, block_table=table, page_size=page)
+    torch.cuda.synchronize()
+    assert rpb.relattn_get_device_error() == 6
+    assert (out == 7).all()
+
+
 # ------------------------------------------------------------------ eviction
 
 def _planes(rows, Hkv, kinds, seed=0):
