@@ -300,7 +300,9 @@ typedef struct relattn_positions {
  * take one of their own).  num_splits: 0 chooses,
  * n > 0 allows at most n partials per row.  Rows of no sequence keep their out
  * and lse.  The workspace size depends on params and on whether positions are
- * given.
+ * given; a bound max_seqlen_k far above the lengths makes it larger.  batch x
+ * num_heads_kv x (row blocks of 16 or 128) x max_seqlen_k above about 2^38 is
+ * RELATTN_ERR_UNSUPPORTED.
  */
 relattn_status relattn_decode_nvfp4(const relattn_params *params, const relattn_kv_nvfp4 *cache,
                                     const relattn_positions *positions, const relattn_paged_kv *pages,

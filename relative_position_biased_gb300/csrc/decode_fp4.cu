@@ -661,8 +661,9 @@ bool two_columns(const KernelArgs &a) { return a.max_q * a.group > 8; }
 
 // Slots, workspace and the least tiles a CTA takes.  A unit holds at most U
 // tiles and meets at most ceil(U / C) + 1 ranges of C tiles, so C >= U /
-// (slots - 1) keeps its pieces within the slots.  False when the sizes do not
-// fit the kernel's index types.
+// (slots - 1) keeps its pieces within the slots.  A unit meets no more ranges than
+// there are CTAs, so as many slots as CTAs do for any C: max_k may be a bound far
+// above the lengths.  False when the sizes do not fit the kernel's index types.
 bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want_splits, Fp4DecodePlan *plan) {
   const int rows = a.max_q * a.group;
   plan->tc = rows > kTcMinRows && !positions;
@@ -687,9 +688,10 @@ bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want
   long C = std::max<long>((total + grid - 1) / grid, kMinTiles);
   long splits = want_splits > 0 ? want_splits : U <= std::max(C, kWhole) ? 1 : (U + C - 1) / C + 1;
   if (a.batch > kWalkBatch) splits = 1;
-  if (splits > 1) splits = std::min<long>(splits, U + 1);
+  if (splits > 1) splits = std::min(std::min<long>(splits, U + 1), grid);
   plan->splits = (int)splits;
-  plan->c_min = splits > 1 ? (int)std::max<long>((U + splits - 2) / (splits - 1), want_splits > 0 ? 1 : kMinTiles) : 0;
+  const long least = want_splits > 0 ? 1 : kMinTiles;
+  plan->c_min = splits == 1 ? 0 : splits == grid ? (int)least : (int)std::max<long>((U + splits - 2) / (splits - 1), least);
   const size_t rows_all = (size_t)a.total_q * a.Hq;
   size_t end = 0;
   plan->lse_offset = 0;
@@ -699,7 +701,7 @@ bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want
   }
   plan->rel_offset = (end + 255) / 256 * 256;
   plan->ws_bytes = a.E > 0 ? plan->rel_offset + rows_all * a.E * sizeof(float) : end;
-  return splits <= 65535 && rows_all <= 0x7fffffffUL && (long)a.batch * heads <= 0x7fffffffL &&
+  return rows_all <= 0x7fffffffUL && (long)a.batch * heads <= 0x7fffffffL &&
          ((long)a.batch * U + grid) * heads <= 0x7fffffffL;
 }
 

@@ -216,6 +216,32 @@ def test_decode(i, splits):
     U.check_decode(c, d, qc["k_values"], qc["v_values"], out, lse)
 
 
+@pytest.mark.parametrize("splits", [0, 1, 5, 100000])
+@pytest.mark.parametrize("c", [
+    U.Case((1, 1), (700, 2050), 16, 2, base=64.0),                             # 8 rows
+    U.Case((3, 1), (2900, 40), 12, 2, E=100, window=300),                      # 18
+    U.Case((9, 2), (700, 4100), 8, 1, E=256, r_dim=64),                        # 72
+    U.Case((1, 2), (600, 2065), 8, 2, positions=True),
+], ids=["8", "18", "72", "positions"])
+def test_decode_under_a_bound_far_above_the_lengths(c, splits):
+    """max_seqlen_k is a bound only: the workspace stays that of as many partials as
+    the GPU runs CTAs, at most 4 an SM."""
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    bound = (1 << 31) - (1 << 16)
+    out, lse = run_decode(c, d, qc, num_splits=splits, max_seqlen_k=bound)
+    U.check_decode(c, d, qc["k_values"], qc["v_values"], out, lse)
+    prm = rpb.RelattnParams(q=1 << 20, k=None, v=None, r=1 << 20, P=1 << 20, cu_seqlens_q=1 << 20, cu_seqlens_k=1 << 20,
+                            batch=2, total_q=sum(c.q_lens), total_k=sum(c.k_lens), max_seqlen_q=max(c.q_lens),
+                            max_seqlen_k=bound, num_heads_q=c.Hq, num_heads_kv=c.Hkv, head_dim=128, r_dim=c.r_dim,
+                            rel_extent=c.E, window=c.window, alpha=0.1, log_scale_base=c.base, out=1 << 20, lse=1 << 20,
+                            workspace=None, workspace_bytes=0, num_splits=splits)
+    st, n = rpb.relattn_decode_nvfp4_workspace_size(prm, rpb.RelattnPositions(1 << 20, 1 << 20) if c.positions else None)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    row = sum(c.q_lens) * c.Hq
+    assert st == 0 and n <= row * (4 * sms * (128 + 1) * 4 + c.E * 4) + 512
+
+
 @pytest.mark.parametrize("batch", [65, 513])
 def test_decode_of_many_sequences(batch):
     """Past 384 sequences every unit has a CTA of its own."""
