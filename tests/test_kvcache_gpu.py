@@ -471,6 +471,47 @@ def test_key_weights(i, kind, decay):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("kw", [dict(q=1), dict(q=1, positions=True), dict(q=1, window=20, page=32), dict(q=5, page=64),
+                                dict(q=5, positions=True, E=9), dict(q=18), dict(q=18, window=40)],
+                         ids=["1", "1-pos", "1-win", "5", "5-pos", "18", "18-win"])
+def test_key_weights_of_many_sequences(kind, kw):
+    """Past 384 sequences few rows leave the walk too; some sequences have no row,
+    some no key."""
+    rng = np.random.default_rng(kw["q"])
+    k_lens = rng.integers(0, 90, 400)
+    q_lens = np.minimum(rng.integers(0, kw["q"] + 1, 400), k_lens)
+    q_lens[0] = kw["q"]
+    k_lens[0] = 300
+    c = U.Case(tuple(map(int, q_lens)), tuple(map(int, k_lens)), 8, 2, **{"E": 64, **{n: v for n, v in kw.items() if n != "q"}})
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    keys = qc["k_values"] if kind == "nvfp4" else d["k"].double().numpy()
+    k = U.device_cache(qc, d) if kind == "nvfp4" else d["k"].cuda()
+    lse = np.full((c.Hq, sum(c.q_lens)), 5.0, np.float32)
+    w_in = np.random.default_rng(6).uniform(0, 9, (c.Hkv, d["rows"])).astype(np.float32)
+    out = torch.full((c.Hkv, d["rows"]), 7.0, device="cuda")
+    rpb.key_weights(d["q"].cuda(), k, d["r"].cuda(), d["P"].cuda(), torch.from_numpy(lse).cuda(), d["cu_q"].cuda(),
+                    d["cu_k"].cuda(), weights_in=torch.from_numpy(w_in).cuda(), decay=0.5, out=out, **U.call_kw(c, d))
+    ok()
+    held = U.check_weights(c, d, keys, lse, w_in, 0.5, out)
+    assert (host(out)[:, ~held] == 7).all()
+
+
+@pytest.mark.parametrize("kw", [dict(q=1, positions=True), dict(q=3, page=32, window=30), dict(q=9), dict(q=9, positions=True)],
+                         ids=["1-pos", "3-win", "9", "9-pos"])
+def test_decode_of_many_sequences_of_every_kind(kw):
+    rng = np.random.default_rng(kw["q"] + 1)
+    k_lens = rng.integers(0, 90, 390)
+    q_lens = np.minimum(rng.integers(0, kw["q"] + 1, 390), k_lens)
+    q_lens[0], k_lens[0] = kw["q"], 300
+    c = U.Case(tuple(map(int, q_lens)), tuple(map(int, k_lens)), 8, 2, **{"E": 64, **{n: v for n, v in kw.items() if n != "q"}})
+    d = U.make(c)
+    qc = U.quantized(c, d)
+    out, lse = run_decode(c, d, qc)
+    U.check_decode(c, d, qc["k_values"], qc["v_values"], out, lse)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
 @pytest.mark.parametrize("E,page,window", [(64, 0, 0), (0, 32, 0), (200, 96, 3000)])
 def test_key_weights_of_more_tiles_than_sms(kind, E, page, window):
     """Every SM takes several tiles of 128 keys, of sequences of all lengths, some
