@@ -151,8 +151,9 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
 }
 
 // Power of two that brings a magnitude to 2^14 .. 2^15 (from its fp32 bits),
-// and its inverse: f16 then holds a bf16 row exactly down to 2^-38 of its
-// largest element.
+// and its inverse: f16, whose last place is 2^-24, then holds a bf16 row (8 bits)
+// exactly down to 2^-31 of its largest element, and smaller elements to within
+// 2^-39 of it.
 __device__ __forceinline__ float f16_row_scale(uint32_t top, float *back) {
   const int e = min(max((int)(top >> 23) - 127, -100), 127);
   *back = __uint_as_float((uint32_t)(e - 14 + 127) << 23);

@@ -18,7 +18,10 @@
 // tcgen05 path's way through shared memory, 2 bytes a value, costs more than the
 // products (decode_fp4_tc.cu takes it for many).
 // Measured: 64 sequences of 1 to 32 thousand keys, group 8, two kv heads: 97 us
-// (3.2 TB/s of the cache), issue slots 58 % busy.
+// (3.2 TB/s of the cache).  No pipe is full there: issue slots are 58 % busy, DRAM
+// 45 %, and without any conversion the call still took 80 us.  The rest is CTAs of
+// equal ranges that do not end together (62 to 82 us within one SM), R before
+// and the merge after them (7 and 10 us each by themselves).
 //   - Keys go along the matrix instruction's 16 rows, query rows along its 8
 //     columns: S^T = K q^T, O^T += V^T P^T.  One token of a GQA-8 group fills
 //     it; with 16 rows a unit takes two columns sets.
@@ -29,11 +32,12 @@
 //     words are interleaved before the conversion (four logical operations
 //     for 16 values), and a lane's 16 dims are one scale block.
 //   - A product code * scale has 6 bits and is exact in f16; the factor of the
-//     head is folded into the logit scale and the output.  q is bf16 and at
-//     most 2^38 below its row's maximum exact in f16 after a power-of-two
-//     scaling per row.  P is rounded to f16 (11 bits, half a step 2^-12 of
-//     the value), scaled by 2^7 so that what is lost below f16's range is
-//     2^-31 of the largest; everything else is fp32.
+//     head is folded into the logit scale and the output.  q is bf16 and exact in
+//     f16, after a power-of-two scaling per row, down to 2^-31 of its row's
+//     maximum; below that it is rounded by at most 2^-39 of the maximum.  P is
+//     rounded to f16 (11 bits, half a step 2^-12 of the value), scaled by 2^7 so
+//     that what is lost below f16's range is 2^-31 of the largest; everything
+//     else is fp32.
 //
 // A warp streams 32 keys at a time through its own ring of asynchronous
 // copies: no barrier among warps until the end of a piece.  The running
@@ -646,10 +650,13 @@ cudaError_t launch_main(const Fp4DecodeArgs &p, cudaStream_t stream) {
 // for 1 and 128 rows; here every 16 rows convert the cache again.  Measured (us,
 // this / that; 2 kv heads, E = 1024), 32, 40 and 128 rows: one sequence of 16384
 // keys 27 / 27, 28 / 27, 40 / 31; of 131072 64 / 43, 71 / 43, 111 / 48; 64
-// of 8192 137 / 155, 177 / 158, 478 / 195.
+// of 8192 137 / 155, 177 / 158, 478 / 195.  From 40 rows on that one is the
+// better throughout.  At 32 it depends on the keys of a CTA, which this rule does
+// not look at: it keeps the batch at 137 and leaves one long sequence at 64.
 constexpr int kTcMinRows = 32;
 // Its tiles that meet the bias band take some seven times as long as the others:
 // 175 us for 72 rows of a million keys and E = 1024, 208 with a weight of four.
+// (This weight and the next were measured at E = 1024 only.)
 constexpr int kTcBandExtra = 6;
 // And of this kernel about twice as long (64 sequences of 1 to 32 thousand keys:
 // 97 us, 104 without weights, 100 with three times).

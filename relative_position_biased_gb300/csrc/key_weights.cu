@@ -13,9 +13,10 @@
 // products) or 4-bit (codes times scales, exact in f16, as in decode_fp4.cu).
 //
 //   few rows (at most 16 per kv head, a decode step): the walk of the decode,
-//     a warp streams 32 keys at a time through its own ring; bound by the issue
-//     slots of the conversions with 4-bit keys (64 sequences of 1 to 32 thousand
-//     keys, group 8: 69 us, 2.5 TB/s of what must be read and written).
+//     a warp streams 32 keys at a time through its own ring.  64 sequences of 1 to 32
+//     thousand keys, group 8: 4-bit keys 70 us, 2.5 TB/s of what must be read and
+//     written, with no pipe full (issue slots 63 % busy, mostly conversions; DRAM
+//     37 %); bf16 keys 122 us, 4.7 TB/s.
 //   many rows: a CTA holds 128 keys as operands in registers and takes the
 //     rows that see them 32 at a time through shared memory; bound by the
 //     matrix instruction and the exponentials.  The bias is a product too:

@@ -659,8 +659,13 @@ cudaError_t launch_nb(const KeyWeightArgs &p, cudaStream_t stream, const CUtenso
 }  // namespace
 
 // 0: the shape is not for this kernel; 2: it takes every row; 1: it takes the
-// rows past the band (r's rows are not 16-byte multiples, or P's are not
-// aligned), the tiles kernel the others.
+// rows past the band (r's rows are not 16-byte multiples, or r is not aligned),
+// the tiles kernel the others.  Few tokens leave most of a step's 128 rows empty.
+// Measured (us, tiles kernel / this; group 8, two kv heads, E = 1024, 4-bit keys,
+// then bf16), 3, 5, 9 and 15 tokens: 64 sequences of 1 to 32 thousand keys 292 / 483,
+// 390 / 458, 493 / 461, 600 / 461; 302 / 411, 398 / 400, 499 / 407, 605 / 404; 4 of
+// 16 to 64 thousand 57 / 57, 75 / 82, 95 / 82, 113 / 81; 62 / 62, 78 / 72, 97 / 72,
+// 117 / 72.  (So this one would be the better from some 8 tokens on.)
 int key_weights_tc_kind(const KeyWeightArgs &p) {
   const KernelArgs &a = p.a;
   if (a.group > 128 || a.max_q < 16 || a.total_q < step_tokens(a.group) || !encoder()) return 0;
