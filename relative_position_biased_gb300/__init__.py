@@ -710,6 +710,12 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+def _fit(*sizes) -> None:
+    """(ctypes would cut a larger number to its low 32 bits)"""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes and counts must fit 32 bits: one of {sizes} does not")
+
+
 def _tensor(t, name: str, dtype, shape, device) -> int:
     """Address of a contiguous tensor of this type and shape on `device`."""
     if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
@@ -926,8 +932,10 @@ def decode_nvfp4(q, cache: KvNvfp4, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seq
         lp = lse.data_ptr()
     else:
         lp = _tensor(lse, "lse", torch.float32, (Hq, Tq), dev)
+    total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
+    _fit(total_k, max_seqlen_q, max_seqlen_k, window, num_splits)
     prm = RelattnParams(
-        qp, None, None, rp, Pp, cq, ck, batch, Tq, _total_k(total_k, block_table, cu_seqlens_k, rows),
+        qp, None, None, rp, Pp, cq, ck, batch, Tq, total_k,
         max_seqlen_q, max_seqlen_k, Hq, H, HEAD_DIM, rd, E, window, alpha, log_scale_base, op, lp, None, 0, num_splits)
     lib, need = _lib or load_library(), ctypes.c_size_t()
     ref, pos = ctypes.byref(prm), _ref(pos)
@@ -973,6 +981,7 @@ def key_weights(q, k, r, P, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: in
         out = torch.zeros(H, rows, dtype=torch.float32, device=dev)
     w_out = w_in if out is weights_in else _tensor(out, "out", torch.float32, (H, rows), dev)
     total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
+    _fit(total_k, max_seqlen_q, max_seqlen_k, window)
     if not fp4 and block_table is None:
         _need(total_k == rows, "a contiguous k has total_k rows")
     fwd = RelattnParams(
@@ -1044,9 +1053,12 @@ def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seq
                        else torch.full((H, rows_keep), -1, dtype=torch.int32, device=dev))
     if new_w:
         weights_out = (torch.empty if new_pos else torch.zeros)(H, rows_keep, dtype=torch.float32, device=dev)
+    total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
+    recent, sink = min(recent, 0x7fffffff), min(sink, 0x7fffffff)      # (no sequence has more keys)
+    _fit(total_k, total_keep, max_seqlen_k, recent, sink)
     prm = RelattnEvictParams(
         wp, ck, ckeep, None if key_pos is None else _tensor(key_pos, "key_pos", torch.int32, (H, rows), dev), batch,
-        _total_k(total_k, block_table, cu_seqlens_k, rows), total_keep, max_seqlen_k, H, sink, recent, rows, rows_keep,
+        total_k, total_keep, max_seqlen_k, H, sink, recent, rows, rows_keep,
         None if pages is None else ctypes.pointer(pages), None if pages_keep is None else ctypes.pointer(pages_keep),
         n, table, weights_out.data_ptr() if new_w else _tensor(weights_out, "weights_out", torch.float32, (H, rows_keep), dev),
         key_pos_out.data_ptr() if new_pos else _tensor(key_pos_out, "key_pos_out", torch.int32, (H, rows_keep), dev),

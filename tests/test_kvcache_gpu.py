@@ -728,6 +728,32 @@ def test_evict(k_lens, keep, recent, sink, kinds, page, page_to, ties):
             assert (q.cpu().float()[torch.from_numpy(~used)] == 3).all()
 
 
+def test_sizes_past_32_bits_are_refused_or_mean_all():
+    n, big = 300, 1 << 32
+    w = torch.rand(1, n, device="cuda")
+    cu, cu_keep = W.cu_seqlens([n]).cuda(), W.cu_seqlens([40]).cuda()
+    for recent, sink, want in ((big, 0, np.arange(260, 300)), (0, big, np.arange(40)), (big, big, np.arange(260, 300))):
+        pos, _ = rpb.evict([], [], w, cu, cu_keep, max_seqlen_k=n, recent=recent, sink=sink, total_keep=40)
+        ok()
+        np.testing.assert_array_equal(host(pos)[0], want)
+    q = torch.zeros(1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    cache, lse, cu1 = rpb.empty_nvfp4(n, 1, "cuda"), torch.zeros(1, 1, device="cuda"), W.cu_seqlens([1]).cuda()
+    good = dict(max_seqlen_q=1, max_seqlen_k=n, window=0, total_k=n)
+    for name, value in (("max_seqlen_q", big + 1), ("max_seqlen_k", big + n), ("window", big + 4), ("window", -big + 4),
+                        ("total_k", big + n)):
+        kw = {**good, name: value}
+        with pytest.raises(ValueError, match="32 bits"):
+            rpb.decode_nvfp4(q, cache, None, None, cu1, cu, alpha=0.1, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            rpb.key_weights(q, cache, None, None, lse, cu1, cu, alpha=0.1, **kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        rpb.decode_nvfp4(q, cache, None, None, cu1, cu, alpha=0.1, num_splits=big + 1, **good)
+    for kw in (dict(max_seqlen_k=big + n), dict(total_keep=big + 40), dict(total_k=big + n), dict(recent=-big + 4)):
+        with pytest.raises(ValueError, match="32 bits"):
+            rpb.evict([torch.zeros(n, 1, 4, device="cuda")], [torch.zeros(40, 1, 4, device="cuda")], w, cu, cu_keep,
+                      **{**dict(max_seqlen_k=n, recent=0, total_keep=40), **kw})
+
+
 def test_evict_of_equal_weights_keeps_the_first():
     n = 20000
     w = torch.zeros(1, n, device="cuda")
