@@ -855,7 +855,7 @@ relattn_status relattn_key_weights(const relattn_key_weights_params *p, void *st
     return RELATTN_ERR_INVALID_ARG;
   // no sequence is longer than the cache (checked on the device): a bound far above
   // the lengths would only make units of work without a key
-  const long max_k = p->pages ? f.max_seqlen_k : std::min<int64_t>(f.max_seqlen_k, rows);
+  const long max_k = p->pages ? f.max_seqlen_k : std::max<int64_t>(std::min<int64_t>(f.max_seqlen_k, rows), 1);
   if (!key_weights_walked(key_weight_sizes(f)) &&
       (max_k + kWalkTile - 1) / kWalkTile * f.batch * f.num_heads_kv > 0x7fffffffL)
     return RELATTN_ERR_UNSUPPORTED;

@@ -535,6 +535,27 @@ def test_key_weights_of_more_tiles_than_sms(kind, E, page, window):
     assert (host(out)[:, ~held] == 7).all()
 
 
+@pytest.mark.parametrize("q_len,bias", [(1, False), (5, True), (20, True)])
+def test_key_weights_of_a_cache_without_rows(q_len, bias):
+    """Query rows of no sequence and no key at all: nothing to do, no error."""
+    q = torch.ones(q_len, 8, 128, dtype=torch.bfloat16, device="cuda")
+    r = torch.ones(q_len, 8, 8, dtype=torch.bfloat16, device="cuda") if bias else None
+    P = torch.ones(8, 16, dtype=torch.bfloat16, device="cuda") if bias else None
+    lse, zero = torch.zeros(8, q_len, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    some = torch.full((64, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    w = torch.full((2, 64), 7.0, device="cuda")
+    work = torch.zeros(1 << 20, device="cuda")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    fwd = rpb.RelattnParams(q=ptr(q), k=ptr(some), v=None, r=ptr(r), P=ptr(P), cu_seqlens_q=ptr(zero), cu_seqlens_k=ptr(zero),
+                            batch=1, total_q=q_len, total_k=0, max_seqlen_q=q_len, max_seqlen_k=4096, num_heads_q=8,
+                            num_heads_kv=2, head_dim=128, r_dim=8 if bias else 0, rel_extent=16 if bias else 0, window=50,
+                            alpha=0.1, log_scale_base=0.0, out=None, lse=ptr(lse))
+    prm = rpb.RelattnKeyWeightsParams(fwd=fwd, weights_out=ptr(w), decay=1.0, workspace=ptr(work), workspace_bytes=4 << 20)
+    assert rpb.relattn_key_weights(prm, torch.cuda.current_stream().cuda_stream) == rpb.RELATTN_OK
+    ok()
+    assert (w == 7).all()
+
+
 @pytest.mark.parametrize("page", [0, 1024])
 @pytest.mark.parametrize("kind", ["bf16", "nvfp4"])
 def test_key_weights_under_a_bound_far_above_the_lengths(kind, page):
