@@ -17,7 +17,7 @@ and checked for
   have landed; a NaN list overwritten before it is read.
 
 Waits can be dropped or taken as an earlier form of the kernel had them: those
-protocols must fail, which pins the checker itself.
+protocols must fail, which pins the model itself.
 """
 import random
 
