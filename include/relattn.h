@@ -298,7 +298,9 @@ typedef struct relattn_positions {
  * best with at most 8 rows per kv head (max_seqlen_q x group); 16 rows share
  * one pass over the keys, and past 32 rows 128 do (with positions every 16
  * take one of their own).  num_splits: 0 chooses,
- * n > 0 allows at most n partials per row.  Rows of no sequence keep their out
+ * n > 0 allows at most n partials per row, or as many as keep the keys of one
+ * partial at 65536 (past 32 rows) or 131072: longer fp32 sums on the tensor cores
+ * lose more than 2^-11 of the result.  Rows of no sequence keep their out
  * and lse.  The workspace size depends on params and on whether positions are
  * given; a bound max_seqlen_k far above the lengths makes it larger.  batch x
  * num_heads_kv x (row blocks of 16 or 128) x max_seqlen_k above about 2^38 is

@@ -808,6 +808,8 @@ relattn_status relattn_decode_nvfp4(const relattn_params *p, const relattn_kv_nv
   x.hp = plan.hp;
   x.row_blocks = plan.row_blocks;
   x.splits = plan.splits;
+  x.whole = plan.whole;
+  x.waves = plan.waves;
   x.c_min = plan.c_min;
   x.tc = plan.tc;
   x.band_extra = plan.band_extra;

@@ -129,6 +129,59 @@ __device__ __forceinline__ int tile_prefix(const WalkArgs &p, int *prefix, int *
   return base;
 }
 
+// A CTA's way through the tiles of a decode, piece by piece.  The units' tiles
+// are laid end to end and cut into ranges of C; CTA c takes ranges [c k, (c + 1) k),
+// of at most `most` tiles each where the plan's k allows.  Or (p.whole) the CTA
+// has one unit, whose `total` tiles are cut in the same way.
+struct Ranges {
+  unsigned x, end, C;                        // the next tile, the one past the last, tiles of a range
+  __device__ __forceinline__ Ranges(const Fp4DecodeArgs &p, unsigned total, unsigned most) {
+    if (p.whole) {
+      x = 0, end = total;
+      C = max(most, total / (unsigned)p.splits + 1);
+      return;
+    }
+    const unsigned share = max((total + gridDim.x - 1) / gridDim.x, 1u);
+    const unsigned k = min((share + most - 1) / most, (unsigned)p.waves);
+    C = max((share + k - 1) / k, (unsigned)p.c_min);
+    x = (unsigned)min((unsigned long long)blockIdx.x * k * C, (unsigned long long)total);
+    end = x + (unsigned)min((unsigned long long)k * C, (unsigned long long)(total - x));
+  }
+};
+
+// One piece: tiles [t0, t0 + tiles) of its unit (none where a range ends within a
+// weighted tile), the slot it fills, and the slots that the unit's pieces use.
+struct Piece {
+  int t0, tiles, slot, used;
+};
+
+// The piece at at.x, which moves on past it.  `place` fills in the unit's head,
+// rows and positions from the unit group's number; per: tiles of a unit group.
+template <typename F>
+__device__ __forceinline__ Piece next_piece(const Fp4DecodeArgs &p, Ranges &at, Unit &u, const int *prefix, unsigned per, F place) {
+  Piece c;
+  const unsigned left = min(at.end - at.x, at.C - at.x % at.C);      // to the end of the range
+  if (p.whole) {
+    c = {(int)at.x, (int)left, (int)(at.x / at.C), (int)((at.end - 1) / at.C + 1)};
+    at.x += left;
+    return c;
+  }
+  const unsigned hr = at.x / per;
+  const int xb = (int)(at.x - hr * per);
+  u.b = last_not_above(prefix, p.a.batch, xb);       // it holds tile xb
+  const int real = unit_tiles(p, u.b, &u.s, &u.lo), v0 = xb - prefix[u.b];
+  const Weighted w = weighted_tiles(p, u.s, u.lo, real);
+  const int n = (int)min((unsigned)(w.total - v0), left);
+  place((int)hr);
+  const unsigned ustart = hr * per + prefix[u.b], first = ustart / at.C;
+  c.t0 = w.tile(v0);
+  c.tiles = w.tile(v0 + n) - c.t0;
+  c.slot = (int)(at.x / at.C - first);
+  c.used = (int)((ustart + w.total - 1) / at.C - first) + 1;
+  at.x += n;
+  return c;
+}
+
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));

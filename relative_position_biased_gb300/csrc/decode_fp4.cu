@@ -44,12 +44,13 @@
 // maximum is raised only when a logit passes it by more than 8 (base 2).
 //
 // Work split: the units (sequence, kv heads of a CTA, 16-row block) hold
-// ceil(keys / tile) tiles each; they are laid end to end, and CTA c takes
-// tiles [c C, (c+1) C).  A piece of a unit writes its partial to slot c -
-// (first CTA of the unit); the unit's first piece marks the slots no piece
-// fills.  With an even number of kv heads a CTA takes two of them, two warps
-// each, over the same 64 keys: their rows share 128-byte lines, and lines
-// fetched for one head only were read twice (538 MB for 311 MB of cache).
+// ceil(keys / tile) tiles each; they are laid end to end in ranges of C tiles, one
+// a CTA, or several where one would sum over too many keys.  A piece of a unit
+// writes its partial to slot (its range) - (first range of the unit); the unit's
+// first piece marks the slots no piece fills.  With an even number of kv heads a
+// CTA takes two of them, two warps each, over the same 64 keys: their rows share
+// 128-byte lines, and lines fetched for one head only were read twice (538 MB for
+// 311 MB of cache).
 #include <algorithm>
 
 #include "cache_walk.cuh"
@@ -509,47 +510,31 @@ __global__ void __launch_bounds__(FT, ctas_per_sm(NT)) relattn_decode_fp4_kernel
     u.nrows = min(kFp4Rows, u.s.lq * p.a.group - u.rb * kFp4Rows);
     u.qbase = first_query_pos(u.s, p.q_pos, u.b);
   };
-  if (p.splits == 1) {                       // one CTA per unit
+  unsigned per = 0, total = 0;               // tiles of a unit group, and of all (the plan keeps them below 2^31)
+  if (p.whole) {                             // one CTA per unit
     const int hr = blockIdx.x / p.a.batch;
     u.b = blockIdx.x - hr * p.a.batch;
     const int n = unit_tiles(p, u.b, &u.s, &u.lo);
     if (n < 0 && tid == 0) atomicOr(p.a.err, kDevErrSeqlens);
-    if (n > 0) {
-      place(hr);
-      if (u.nrows > 0) run_piece<NT, POS>(p, u, 0, n, 0, smem);
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
+    total = max(n, 0);
+    place(hr);
+  } else {
+    per = tile_prefix<FT>(p, prefix, wsum);
+    total = per * (unsigned)(p.a.Hkv / p.hp * p.row_blocks);
   }
-  const int base = tile_prefix<FT>(p, prefix, wsum);
-  // (the plan keeps the number of tiles below 2^31)
-  const unsigned per = base, total = per * (unsigned)(p.a.Hkv / p.hp * p.row_blocks);
-  const unsigned C = max((total + gridDim.x - 1) / gridDim.x, (unsigned)p.c_min);
-  unsigned x = (unsigned)min((unsigned long long)blockIdx.x * C, (unsigned long long)total);
-  const unsigned end = x + min(total - x, C);
-  while (x < end) {
-    const unsigned hr = x / per;
-    const int xb = (int)(x - hr * per);
-    u.b = last_not_above(prefix, p.a.batch, xb);   // it holds tile xb
-    const int real = unit_tiles(p, u.b, &u.s, &u.lo), v0 = xb - prefix[u.b];
-    const Weighted w = weighted_tiles(p, u.s, u.lo, real);
-    const int n = (int)min((unsigned)(w.total - v0), end - x);
-    place((int)hr);
-    if (u.nrows > 0) {
-      const unsigned ustart = hr * per + prefix[u.b], first = ustart / C;
-      const int t0 = w.tile(v0), tiles = w.tile(v0 + n) - t0, slot = (int)(blockIdx.x - first);
-      if (tiles > 0) run_piece<NT, POS>(p, u, t0, tiles, slot, smem);
-      // mark slots without a piece: the first piece those past the last, a range within a tile its own
-      const int from = tiles > 0 ? (int)((ustart + w.total - 1) / C - first) + 1 : slot, to = tiles > 0 ? p.splits : slot + 1;
-      if (t0 == 0 || tiles == 0) {
-        for (int i = tid; i < u.nrows * p.hp; i += FT) {
-          const int hs = i / u.nrows, rr = u.rb * kFp4Rows + i % u.nrows;
-          const long grow = (long)(u.s.q0 + rr / p.a.group) * p.a.Hq + (u.h - hsub + hs) * p.a.group + rr % p.a.group;
-          for (int k = from; k < to; ++k) p.a.lse_part[(long)k * p.a.total_q * p.a.Hq + grow] = -INFINITY;
-        }
+  Ranges at(p, total, kFp4MostTiles);
+  while (at.x < at.end) {
+    const Piece c = next_piece(p, at, u, prefix, per, place);
+    if (u.nrows <= 0) continue;
+    // mark slots without a piece: the first piece those past the last, a range within a tile its own
+    const int from = c.tiles > 0 ? c.used : c.slot, to = c.tiles > 0 ? p.splits : c.slot + 1;
+    if (c.t0 == 0 || c.tiles == 0)
+      for (int i = tid; i < u.nrows * p.hp; i += FT) {
+        const int hs = i / u.nrows, rr = u.rb * kFp4Rows + i % u.nrows;
+        const long grow = (long)(u.s.q0 + rr / p.a.group) * p.a.Hq + (u.h - hsub + hs) * p.a.group + rr % p.a.group;
+        for (int k = from; k < to; ++k) p.a.lse_part[(long)k * p.a.total_q * p.a.Hq + grow] = -INFINITY;
       }
-    }
-    x += n;
+    if (c.tiles > 0) run_piece<NT, POS>(p, u, c.t0, c.tiles, c.slot, smem);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -631,7 +616,7 @@ cudaError_t launch_main(const Fp4DecodeArgs &p, cudaStream_t stream) {
   auto *kernel = relattn_decode_fp4_kernel<NT, POS>;
   const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(kernel), F_RING, done);
   if (e != cudaSuccess) return e;
-  const long grid = p.splits == 1 ? (long)p.a.batch * (p.a.Hkv / p.hp) * p.row_blocks : (long)p.a.sms * ctas_per_sm(NT);
+  const long grid = p.whole ? (long)p.a.batch * (p.a.Hkv / p.hp) * p.row_blocks : (long)p.a.sms * ctas_per_sm(NT);
   if (grid > 0x7fffffffL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -666,11 +651,13 @@ bool two_columns(const KernelArgs &a) { return a.max_q * a.group > 8; }
 
 }  // namespace
 
-// Slots, workspace and the least tiles a CTA takes.  A unit holds at most U
+// Slots, workspace and the least tiles of a range.  A unit holds at most U
 // tiles and meets at most ceil(U / C) + 1 ranges of C tiles, so C >= U /
 // (slots - 1) keeps its pieces within the slots.  A unit meets no more ranges than
-// there are CTAs, so as many slots as CTAs do for any C: max_k may be a bound far
-// above the lengths.  False when the sizes do not fit the kernel's index types.
+// there are (CTAs x waves), so as many slots do for any C: max_k may be a bound far
+// above the lengths.  A unit that has a CTA of its own is cut into pieces only
+// where it is too long for one, by its own length and the slots.  False when the
+// sizes do not fit the kernel's index types.
 bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want_splits, Fp4DecodePlan *plan) {
   const int rows = a.max_q * a.group;
   plan->tc = rows > kTcMinRows && !positions;
@@ -692,13 +679,22 @@ bool plan_decode_fp4(const KernelArgs &a, long total_k, bool positions, int want
   // kernel: up to 8 tiles stay whole (one sequence of 8 tiles, caches cold: 18.6 us
   // whole, 22.7 in pieces of two; 12 tiles 25.7 and 24.7).
   const long kMinTiles = plan->tc ? 4 : 2, kWhole = plan->tc ? 0 : 8;
-  long C = std::max<long>((total + grid - 1) / grid, kMinTiles);
-  long splits = want_splits > 0 ? want_splits : U <= std::max(C, kWhole) ? 1 : (U + C - 1) / C + 1;
-  if (a.batch > kWalkBatch) splits = 1;
-  if (splits > 1) splits = std::min(std::min<long>(splits, U + 1), grid);
-  plan->splits = (int)splits;
+  const long most = plan->tc ? kFp4TcMostTiles : kFp4MostTiles;
+  const long share = std::max<long>((total + grid - 1) / grid, kMinTiles), waves = (share + most - 1) / most;
+  const long C = (share + waves - 1) / waves, ranges = grid * waves;
+  // pieces that the longest sequence needs, which total_k bounds as well
+  const long pieces = (std::min<long>(U, total_k / tile + 1 + plan->band_extra * band) + most - 1) / most;
   const long least = want_splits > 0 ? 1 : kMinTiles;
-  plan->c_min = splits == 1 ? 0 : splits == grid ? (int)least : (int)std::max<long>((U + splits - 2) / (splits - 1), least);
+  long splits = std::max<long>(pieces, 1);
+  plan->whole = a.batch > kWalkBatch || want_splits == 1 || (want_splits <= 0 && U <= std::max(C, kWhole));
+  if (!plan->whole) {
+    splits = want_splits > 0 ? std::max<long>(want_splits, pieces > 1 ? pieces + 1 : 2) : (U + C - 1) / C + 1;
+    splits = std::min(std::min<long>(splits, U + 1), ranges);
+    plan->whole = splits == 1;
+  }
+  plan->splits = (int)splits;
+  plan->waves = (int)waves;
+  plan->c_min = plan->whole ? 0 : splits == ranges ? (int)least : (int)std::max<long>((U + splits - 2) / (splits - 1), least);
   const size_t rows_all = (size_t)a.total_q * a.Hq;
   size_t end = 0;
   plan->lse_offset = 0;

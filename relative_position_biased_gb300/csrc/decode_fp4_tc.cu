@@ -100,36 +100,19 @@ __device__ __forceinline__ void for_pieces(const Fp4DecodeArgs &p, const int *pr
     u.nrows = min(kFp4TcRows, u.s.lq * p.a.group - u.rb * kFp4TcRows);
     u.qbase = u.s.lk - u.s.lq;
   };
-  if (p.splits == 1) {                       // one CTA per unit
+  unsigned total = (unsigned)base * (unsigned)(p.a.Hkv * p.row_blocks);      // (the plan keeps it below 2^31)
+  if (p.whole) {                             // one CTA per unit
     const int hr = blockIdx.x / p.a.batch;
     u.b = blockIdx.x - hr * p.a.batch;
     const int n = unit_tiles(p, u.b, &u.s, &u.lo);
     if (n < 0 && threadIdx.x == 0) atomicOr(p.a.err, kDevErrSeqlens);
-    if (n > 0) {
-      place(hr);
-      if (u.nrows > 0) body(u, 0, n, 0, 1);
-    }
-    return;
+    total = max(n, 0);
+    place(hr);
   }
-  // (the plan keeps the number of tiles below 2^31)
-  const unsigned per = base, total = per * (unsigned)(p.a.Hkv * p.row_blocks);
-  const unsigned C = max((total + gridDim.x - 1) / gridDim.x, (unsigned)p.c_min);
-  unsigned x = (unsigned)min((unsigned long long)blockIdx.x * C, (unsigned long long)total);
-  const unsigned end = x + min(total - x, C);
-  while (x < end) {
-    const unsigned hr = x / per;
-    const int xb = (int)(x - hr * per);
-    u.b = last_not_above(prefix, p.a.batch, xb);   // it holds tile xb
-    const int real = unit_tiles(p, u.b, &u.s, &u.lo), v0 = xb - prefix[u.b];
-    const Weighted w = weighted_tiles(p, u.s, u.lo, real);
-    const int n = (int)min((unsigned)(w.total - v0), end - x);
-    place((int)hr);
-    if (u.nrows > 0) {
-      const unsigned ustart = hr * per + prefix[u.b], first = ustart / C;
-      const int t0 = w.tile(v0);
-      if (!body(u, t0, w.tile(v0 + n) - t0, (int)(blockIdx.x - first), (int)((ustart + w.total - 1) / C - first) + 1)) return;
-    }
-    x += n;
+  Ranges at(p, total, kFp4TcMostTiles);
+  while (at.x < at.end) {
+    const Piece c = next_piece(p, at, u, prefix, (unsigned)base, place);
+    if (u.nrows > 0 && !body(u, c.t0, c.tiles, c.slot, c.used)) return;
   }
 }
 
@@ -205,7 +188,7 @@ __global__ void __launch_bounds__(TDT, 1) relattn_decode_fp4_tc_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + TD_SLOT);
   int base = 0;
-  if (p.splits > 1) base = tile_prefix<TDT>(p, prefix, wsum);
+  if (!p.whole) base = tile_prefix<TDT>(p, prefix, wsum);
 
   if (warp < SMW) {
     regs_inc<192>();
@@ -590,7 +573,7 @@ cudaError_t launch_decode_fp4_tc(const Fp4DecodeArgs &p, cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevicesAttr];
   const cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_decode_fp4_tc_kernel), (int)TD_SMEM, done);
   if (e != cudaSuccess) return e;
-  const long grid = p.splits == 1 ? (long)p.a.batch * p.a.Hkv * p.row_blocks : p.a.sms;
+  const long grid = p.whole ? (long)p.a.batch * p.a.Hkv * p.row_blocks : p.a.sms;
   if (grid > 0x7fffffffL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);

@@ -211,12 +211,20 @@ constexpr int kWalkTile = 128;        // keys a CTA takes at a time, over its kv
 struct Fp4DecodeArgs : WalkArgs {
   Fp4Cache kv;
   int row_blocks;      // row blocks per (sequence, kv head)
-  int splits;          // partial slots of a row; 1 = one CTA per unit, no partials
-  int c_min;           // least tiles a CTA takes (keeps a unit within its slots)
+  int splits;          // partial slots of a row; 1 = no partials
+  int whole;           // 1: one CTA per unit
+  int waves;           // else: most ranges a CTA takes
+  int c_min;           // and least tiles of a range (keeps a unit within its slots)
   int tc;              // 1: the tcgen05 kernel (decode_fp4_tc.cu)
 };
+// Most tiles summed in one piece.  The matrix instructions add to an fp32
+// accumulator by truncation: each takes about 1e-7 off it (measured, values of one
+// sign: 72 rows of 2^27 keys, 880 thousand in a piece, lost 0.5 % of the result,
+// 4 million in one piece 2.5 %).  4096 additions, 8 a tile on tcgen05 and 2 a tile in
+// a warp of the other kernel, keep that below 2^-11.
+constexpr int kFp4MostTiles = 2048, kFp4TcMostTiles = 512;
 struct Fp4DecodePlan {
-  int hp, row_blocks, splits, c_min, tc, band_extra;
+  int hp, row_blocks, splits, whole, waves, c_min, tc, band_extra;
   size_t lse_offset, rel_offset, ws_bytes;
 };
 constexpr int kFp4Rows = 16;          // query rows of a work unit

@@ -242,6 +242,50 @@ def test_decode_under_a_bound_far_above_the_lengths(c, splits):
     assert st == 0 and n <= row * (4 * sms * (128 + 1) * 4 + c.E * 4) + 512
 
 
+@pytest.mark.parametrize("nq,length,splits,batch", [
+    (9, 1 << 27, 0, 1), (9, 1 << 22, 1, 1), (9, 1 << 22, 3, 1), (9, 1 << 21, 0, 390),
+    (1, (1 << 31) - (1 << 16), 0, 1), (1, 1 << 24, 1, 1), (1, 1 << 23, 0, 390), (4, 1 << 24, 2, 1)])
+def test_long_sums_keep_their_magnitude(nq, length, splits, batch):
+    """The first sequence has one page of 65536 keys again and again, with values
+    whose mean is 1.  The matrix instructions add to fp32 by truncation; a piece
+    takes at most 4096 such additions, each short of less than a step (2^-23) of
+    what has been summed, so outputs are short of at most 4096 * 2^-23 of their
+    size.  The roundings of bf16 and of the f16 weights average out over the rows
+    and dims (2^-12 is left for them); a weight's sum of 2^15 fp32 additions is
+    off by half a step (2^-24) each at most."""
+    page, Hq = 1 << 16, 8
+    c = U.Case((nq,), (page,), Hq, 1, E=0, r_dim=0, factors=False, page=page)
+    d = U.make(c)
+    d["v"] = (d["v"].float() + 1.0).to(torch.bfloat16)
+    qc = U.quantized(c, d)
+    n = length // page
+    table = torch.full((batch, n), int(d["table"][0, 0]), dtype=torch.int32, device="cuda")
+    q = torch.cat([d["q"], d["q"][:1].expand(batch - 1, -1, -1)]).cuda().contiguous()
+    cu_q = W.cu_seqlens([nq] + [1] * (batch - 1)).cuda()
+    cu_k = W.cu_seqlens([length] + [70] * (batch - 1)).cuda()
+    out, lse = rpb.decode_nvfp4(q, U.device_cache(qc, d), None, None, cu_q, cu_k, max_seqlen_q=nq, max_seqlen_k=length,
+                                alpha=c.alpha, total_k=length + 70 * (batch - 1), block_table=table, page_size=page,
+                                num_splits=splits)
+    ok()
+    K, V = qc["k_values"][d["where"][0], 0], qc["v_values"][d["where"][0], 0]
+    short = []
+    for hq in range(Hq):
+        f = d["q"][:, hq].double().numpy()
+        x0, _ = C.logits(f, K, None, None, np.full(nq, page), np.arange(page), alpha=c.alpha)
+        x1, _ = C.logits(f, K, None, None, np.arange(page - nq, page), np.arange(page), alpha=c.alpha)      # the last copy
+        m = x0.max(1)[:, None]
+        s = (n - 1) * np.exp(x0 - m) + np.exp(x1 - m)
+        ref = s @ V / s.sum(1)[:, None]
+        short.append((host(out[:nq, hq].double()) - ref) / ref)
+        z = np.log(s.sum(1)) + m[:, 0]
+        assert np.abs(host(lse[hq, :nq].double()) - z).max() <= 2.0 ** 15 * 2.0 ** -24 + 2.0 ** -22 * np.abs(z).max()
+        if batch > 1:                                    # and a short one beside it
+            p, z = C.softmax(C.logits(f[:1], K[:70], None, None, [69], np.arange(70), alpha=c.alpha)[0])
+            assert np.abs(host(out[-1, hq].double()) - (p @ V[:70])[0]).max() <= 2.0 ** -7 * np.abs(V).max()
+            assert abs(float(lse[hq, -1]) - z[0]) <= 1e-5
+    assert abs(np.mean(short)) <= 4096 * 2.0 ** -23 + 2.0 ** -12, np.mean(short)
+
+
 @pytest.mark.parametrize("batch", [65, 513])
 def test_decode_of_many_sequences(batch):
     """Past 384 sequences every unit has a CTA of its own."""
