@@ -961,6 +961,72 @@ def test_captured_calls_replay_and_streams_do_not_share():
     ok()
 
 
+@pytest.mark.parametrize("nq,Hq,positions", [(1, 8, False), (2, 8, True), (9, 8, False), (9, 8, True)])
+def test_captured_calls_follow_new_lengths(nq, Hq, positions):
+    """A graph captured under bounds, for a batch with room to spare, replayed with
+    other lengths, pages and positions: decode, key weights and eviction."""
+    batch, Hkv, page, top, E = 5, 2, 32, 4000, 64
+    slots = -(-top // page)
+    rows = batch * slots // 2 * page
+    cap = dict(cu_q=torch.zeros(batch + 1, dtype=torch.int32, device="cuda"), cu_k=torch.zeros(batch + 1, dtype=torch.int32, device="cuda"),
+               cu_keep=torch.zeros(batch + 1, dtype=torch.int32, device="cuda"),
+               table=torch.full((batch, slots), -1, dtype=torch.int32, device="cuda"),
+               q=torch.zeros(batch * nq, Hq, 128, dtype=torch.bfloat16, device="cuda"),
+               r=torch.zeros(batch * nq, Hq, 16, dtype=torch.bfloat16, device="cuda"),
+               P=torch.zeros(16, E, dtype=torch.bfloat16, device="cuda"),
+               key_pos=torch.zeros(Hkv, rows, dtype=torch.int32, device="cuda"), q_pos=torch.zeros(batch, dtype=torch.int32, device="cuda"))
+    cache = rpb.empty_nvfp4(rows, Hkv, "cuda", torch.ones(Hkv, device="cuda"), torch.ones(Hkv, device="cuda"))
+    to = torch.zeros(500, Hkv, 8, dtype=torch.uint8, device="cuda")
+    pos = dict(key_pos=cap["key_pos"], q_pos=cap["q_pos"]) if positions else {}
+    kw = dict(max_seqlen_q=nq, max_seqlen_k=top, alpha=1 / np.sqrt(128), total_k=600, block_table=cap["table"], page_size=page, **pos)
+
+    def step():
+        out, lse = rpb.decode_nvfp4(cap["q"], cache, cap["r"], cap["P"], cap["cu_q"], cap["cu_k"], **kw)
+        w = rpb.key_weights(cap["q"], cache, cap["r"], cap["P"], lse, cap["cu_q"], cap["cu_k"], decay=0.0, **kw)
+        kept, wk = rpb.evict([cache.k_scale], [to], w, cap["cu_k"], cap["cu_keep"], max_seqlen_k=top, recent=4, sink=1, total_k=600,
+                             total_keep=500, block_table=cap["table"], page_size=page)
+        return out, lse, w, kept
+
+    step()                                               # warm up (on no sequence)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for q_lens, k_lens in (((1, nq, 0, 1, nq), (7, 500, 33, 1, 40)), ((nq,) * 5, (nq, 3500, 90, 64, 700)),
+                           ((1, 0, 0, 0, 0), (2000, 0, 0, 0, 0)), ((nq, 1), (3000, 4000))):
+        q_lens, k_lens = q_lens + (0,) * (5 - len(q_lens)), k_lens + (0,) * (5 - len(k_lens))
+        c = U.Case(q_lens, k_lens, Hq, Hkv, E=E, page=page, positions=positions, seed=sum(k_lens))
+        d = U.make(c)
+        qc = U.quantized(c, d)
+        n = d["rows"]
+        assert n <= rows
+        for t, x in zip(cache, U.device_cache(qc, d)):
+            t[:len(x)].copy_(x)
+        for name in ("q", "r"):
+            cap[name][:len(d[name])].copy_(d[name])
+        cap["P"].copy_(d["P"])
+        cap["cu_q"].copy_(d["cu_q"])
+        cap["cu_k"].copy_(d["cu_k"])
+        keep = [k // 20 for k in k_lens]
+        cap["cu_keep"].copy_(W.cu_seqlens(keep))
+        cap["table"][:, :d["table"].shape[1]].copy_(d["table"])
+        if positions:
+            cap["key_pos"][:, :n].copy_(d["key_pos"])
+            cap["q_pos"].copy_(d["q_pos"])
+        graph.replay()
+        ok()
+        out, lse, w, kept = got
+        Tq = sum(q_lens)
+        U.check_decode(c, d, qc["k_values"], qc["v_values"], out[:Tq], lse[:, :Tq])
+        U.check_weights(c, d, qc["k_values"], host(lse[:, :Tq]), None, 0.0, w[:, :n])
+        o = 0
+        for b, k in enumerate(keep):
+            for h in range(Hkv):
+                idx = C.kept_keys(host(w)[h, d["where"][b]], k, 4, 1)
+                np.testing.assert_array_equal(host(kept)[h, o:o + k], idx)
+                assert torch.equal(to[o:o + k, h], cache.k_scale[torch.from_numpy(d["where"][b][idx]).cuda(), h])
+            o += k
+
+
 def test_calls_of_many_rows_and_long_sequences_replay_side_by_side():
     """Decodes of 40 rows, key weights of 160 rows and selections by all SMs, in
     two graphs that replay on two streams at once."""
