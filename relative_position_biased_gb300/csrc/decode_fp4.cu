@@ -18,8 +18,8 @@
 // tcgen05 path's way through shared memory, 2 bytes a value, costs more than the
 // products (decode_fp4_tc.cu takes it for many).
 // Measured: 64 sequences of 1 to 32 thousand keys, group 8, two kv heads: 97 us
-// (3.2 TB/s of the cache).  No pipe is full there: issue slots are 58 % busy, DRAM
-// 45 %, and without any conversion the call still took 80 us.  The rest is CTAs of
+// (3.2 TB/s of the cache).  No pipe is full there: issue slots are 62 % busy, DRAM
+// 47 %, and without any conversion the call still took 80 us.  The rest is CTAs of
 // equal ranges that do not end together (62 to 82 us within one SM), R before
 // and the merge after them (7 and 10 us each by themselves).
 //   - Keys go along the matrix instruction's 16 rows, query rows along its 8
