@@ -7,7 +7,7 @@
 // make f16 tiles of 128 keys in shared memory (a product code * scale has 6
 // bits and is exact), one thread a row takes the softmax, and the products S =
 // Q K^T, O += P V read Q and P from tensor memory.  72 rows of a million keys
-// and two heads took five passes of the other kernel, 439 us; here 169 (1.8 TB/s).
+// and two heads took five passes of the other kernel, 439 us; here 170 (1.8 TB/s).
 //
 // What bounds it: no pipe (tensor a quarter, issue two fifths busy) but the way
 // of a tile through its steps, 1.3 us: conversion, product, a softmax warp of

@@ -17,8 +17,8 @@ constexpr int kFp4Blocks = kHeadDim / 16;     // scale bytes of a (row, head)
 // Sequences up to this many are laid end to end by the walking kernels (their
 // table leaves room for four decode CTAs per SM).  Past it a decode takes a CTA
 // per unit, and key weights of few rows the tiles kernel.  Measured (384 / 512
-// sequences of 512 to 4096 4-bit keys, one row, group 8, two kv heads): decode 127 /
-// 165 us, the same rate; key weights 81 / 347, three times as long per key.
+// sequences of 512 to 4096 4-bit keys, one row, group 8, two kv heads): decode 123 /
+// 168 us, the same rate; key weights 81 / 347, three times as long per key.
 constexpr int kWalkBatch = 384;
 
 // Four code bytes (one word, lowest byte first) as four f16 pairs, the low
