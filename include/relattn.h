@@ -176,6 +176,38 @@ relattn_status relattn_decode_paged(const relattn_params *params, const relattn_
                                    void *stream);
 
 /*
+ * Attention of new tokens over the cache that holds them, from one token to a
+ * whole prompt: relattn_prefill's arguments and results (any Lq_b <= Lk_b, the
+ * new tokens are the sequence's last rows) with two things that calls of their
+ * own do not have:
+ *   pages  K / V in pages as in relattn_decode_paged, of any page_size that is
+ *          a multiple of 16; NULL: contiguous rows.  A page that no row sees
+ *          (behind the window, or past the last key) is not looked at: its
+ *          table entry may be anything, and rows past a sequence's last key
+ *          may hold anything.  An entry outside [0, num_pages) of a page that
+ *          is needed makes its keys read as zero and records
+ *          RELATTN_ERR_DEVICE_ARGS.
+ *   sink   a sliding window keeps the first `sink` keys: key j is seen from
+ *          position i when 0 <= i - j and (i - j < window or j < sink).  The
+ *          relative bias applies to them as to any key.  0 for none; without
+ *          a window it changes nothing.
+ * (The pages name neither chunks over pages nor sinks; both are this library's
+ * own addition in their manner.)
+ * out and lse of a row are those of relattn_prefill for the same keys to
+ * rounding, and feed relattn_backward_sinks.  Rows of no sequence keep their
+ * out and lse; keys past max_seqlen_k or rows outside the arrays skip the
+ * sequence and record RELATTN_ERR_DEVICE_ARGS.  max_seqlen_k up to 2^31 - 2^16;
+ * batch and num_heads_q up to 65535.
+ * Workspace: relattn_extend_workspace_size() bytes of the same params, pages
+ * and sink, 16-byte aligned; its contents are scratch, so calls that may run at
+ * the same time need one each.
+ */
+relattn_status relattn_extend(const relattn_params *params, const relattn_paged_kv *pages, int32_t sink,
+                              void *stream);
+relattn_status relattn_extend_workspace_size(const relattn_params *params, const relattn_paged_kv *pages,
+                                             int32_t sink, size_t *bytes);
+
+/*
  * MXFP8 K / V cache (page "SGLang and Miles Add Day-0 Support for Inkling",
  * section "Relative Logits Optimization", paragraph "MXFP8 Support": K and V
  * stored in MXFP8, Q K^T as an MXFP8 product, P V in bf16 with V dequantised
@@ -506,6 +538,19 @@ relattn_status relattn_backward_workspace_size(const relattn_bwd_params *params,
 relattn_status relattn_backward(const relattn_bwd_params *params, void *stream);
 
 /*
+ * Gradients of a window that keeps the first `sink` keys (relattn_extend over
+ * contiguous rows): relattn_backward's arguments, formulas and errors, the sums
+ * over the keys 0 <= i - j < window or j < sink.  sink <= 1024 (larger:
+ * RELATTN_ERR_UNSUPPORTED); 0, or no window: relattn_backward's results.  The
+ * workspace (relattn_backward_sinks_workspace_size) holds relattn_backward's
+ * and the sinks' parts in fp32: 4 * total_q * Hq * 128 bytes of dq, as many
+ * with r_dim in place of 128 where rel_extent > window, and those of dk and dv.
+ */
+#define RELATTN_MAX_BACKWARD_SINK 1024
+relattn_status relattn_backward_sinks_workspace_size(const relattn_bwd_params *params, int32_t sink, size_t *bytes);
+relattn_status relattn_backward_sinks(const relattn_bwd_params *params, int32_t sink, void *stream);
+
+/*
  * Attention prologue: the step right before the attention forward (page
  * "SGLang and Miles Add Day-0 Support for Inkling", section "ShortConv
  * Optimization", paragraph "KV ShortConv + QK-norm + KV store"), for one
@@ -590,6 +635,20 @@ typedef struct relattn_kv_mxfp8_out {
 
 relattn_status relattn_prologue_mxfp8(const relattn_prologue_params *params,
                                       const relattn_kv_mxfp8_out *cache, void *stream);
+
+/*
+ * The prologue with a paged bf16 cache: k_cache / v_cache are pools of
+ * num_pages * page_size rows, and the chunk's row t of sequence b goes to the
+ * row of key (Lk_b - Lq_b) + t as relattn_decode_paged and relattn_extend
+ * address it.  page_size a multiple of 16 (else RELATTN_ERR_UNSUPPORTED);
+ * total_k is not read.  Arithmetic, conv states and checks are
+ * relattn_prologue's: the rows it writes are bit for bit the same.  A key past
+ * the table or a page outside the pool skips its row and records
+ * RELATTN_ERR_DEVICE_ARGS.  Two sequences may share pages that hold no row of
+ * their chunks.
+ */
+relattn_status relattn_prologue_paged(const relattn_prologue_params *params, const relattn_paged_kv *pages,
+                                      void *stream);
 
 /* ------------------------------------------------------------------ test hooks
  *

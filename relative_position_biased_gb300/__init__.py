@@ -43,6 +43,8 @@ EXPORTED = (
     "relattn_store_nvfp4", "relattn_load_nvfp4", "relattn_decode_nvfp4",
     "relattn_decode_nvfp4_workspace_size", "relattn_key_weights",
     "relattn_key_weights_workspace_size", "relattn_evict", "relattn_evict_workspace_size",
+    "relattn_extend", "relattn_extend_workspace_size", "relattn_prologue_paged",
+    "relattn_backward_sinks", "relattn_backward_sinks_workspace_size",
 )
 # exported by the test build only
 TEST_HOOKS = (
@@ -275,6 +277,11 @@ def _configure(path: str):
                 ("relattn_decode_nvfp4_workspace_size", [P, POS, SZ]),
                 ("relattn_key_weights", [ctypes.POINTER(RelattnKeyWeightsParams), vp]),
                 ("relattn_key_weights_workspace_size", [ctypes.POINTER(RelattnKeyWeightsParams), SZ]),
+                ("relattn_extend", [P, PG, ctypes.c_int32, vp]),
+                ("relattn_extend_workspace_size", [P, PG, ctypes.c_int32, SZ]),
+                ("relattn_prologue_paged", [ctypes.POINTER(RelattnPrologueParams), PG, vp]),
+                ("relattn_backward_sinks", [BP, ctypes.c_int32, vp]),
+                ("relattn_backward_sinks_workspace_size", [BP, ctypes.c_int32, SZ]),
                 ("relattn_evict", [ctypes.POINTER(RelattnEvictParams), vp]),
                 ("relattn_evict_workspace_size", [ctypes.POINTER(RelattnEvictParams), SZ])):
             f = getattr(lib, name)
@@ -459,8 +466,8 @@ def decode(q, k, v, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int, max_
 
 def prologue(q, k, v, conv_k, conv_v, norm_q, norm_k, cu_seqlens_q, cu_seqlens_k, k_cache,
              v_cache, *, eps: float = 1e-6, q_out=None, conv_state_in=None,
-             conv_state_out=None, total_k: Optional[int] = None, mxfp8=None,
-             stream: Optional[int] = None):
+             conv_state_out=None, total_k: Optional[int] = None, mxfp8=None, block_table=None,
+             page_size: int = 0, stream: Optional[int] = None):
     """ShortConv + Q/K RMSNorm + KV-cache write for one chunk, on device tensors.
 
     ``conv_state_in`` / ``conv_state_out`` are ``(k_state, v_state)`` pairs of
@@ -469,9 +476,14 @@ def prologue(q, k, v, conv_k, conv_v, norm_q, norm_k, cu_seqlens_q, cu_seqlens_k
     ``q_out=q`` to normalise in place).  With ``mxfp8=(k8, v8, k_scale,
     v_scale)`` (uint8 [total_k, Hkv, 128] codes and [total_k, Hkv, 4] scales)
     the cache rows are also written as MXFP8 (relattn_prologue_mxfp8); the bf16
-    caches may then be None.
+    caches may then be None.  With ``block_table`` int32 [batch,
+    max_pages_per_seq] the caches are pools of pages of ``page_size`` keys
+    (relattn_prologue_paged; bf16 only).
     """
     import torch
+    if block_table is not None:
+        return _prologue_paged(q, k, v, conv_k, conv_v, norm_q, norm_k, cu_seqlens_q, cu_seqlens_k, k_cache, v_cache,
+                               eps, q_out, conv_state_in, conv_state_out, mxfp8, block_table, page_size, stream)
     if q_out is None:
         q_out = torch.empty_like(q)
 
@@ -577,11 +589,13 @@ def decode_paged(q, k_pool, v_pool, r, P, cu_seqlens_q, cu_seqlens_k, block_tabl
 
 def backward(q, k, v, r, P, out, lse, dout, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int,
              max_seqlen_k: int, alpha: float, window: int = 0, log_scale_base: float = 0.0,
-             dq=None, dk=None, dv=None, dr=None, workspace=None, stream: Optional[int] = None):
+             dq=None, dk=None, dv=None, dr=None, workspace=None, stream: Optional[int] = None, sink: int = 0):
     """Gradients of sum(dout * out) w.r.t. q, k, v and r (P frozen), from the
     forward's inputs and its saved out / lse.  Returns (dq, dk, dv, dr); dr is
-    None when r has no channels."""
+    None when r has no channels.  ``sink``: the window keeps the first keys, as
+    in ``extend``, which gave out and lse (relattn_backward_sinks)."""
     import torch
+    _fit(sink)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -595,14 +609,27 @@ def backward(q, k, v, r, P, out, lse, dout, cu_seqlens_q, cu_seqlens_k, *, max_s
         dout=dout.data_ptr(), dq=dq.data_ptr(), dk=dk.data_ptr(), dv=dv.data_ptr(),
         dr=None if dr is None else dr.data_ptr())
     if workspace is None:
-        st, nbytes = relattn_backward_workspace_size(prm)
+        st, nbytes = relattn_backward_sinks_workspace_size(prm, sink) if sink else relattn_backward_workspace_size(prm)
         _check(st, "relattn_backward_workspace_size")
         workspace = torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=q.device)
     prm.workspace = workspace.data_ptr()
     prm.workspace_bytes = workspace.numel() * workspace.element_size()
-    _check(relattn_backward(prm, _current_stream() if stream is None else stream),
-           "relattn_backward")
+    st = _current_stream() if stream is None else stream
+    if sink:
+        _check(relattn_backward_sinks(prm, sink, st), "relattn_backward_sinks")
+    else:
+        _check(relattn_backward(prm, st), "relattn_backward")
     return dq, dk, dv, dr
+
+
+def relattn_backward_sinks(params: RelattnBwdParams, sink: int, stream: int = 0) -> int:
+    return load_library().relattn_backward_sinks(ctypes.byref(params), sink, ctypes.c_void_p(stream))
+
+
+def relattn_backward_sinks_workspace_size(params: RelattnBwdParams, sink: int) -> Tuple[int, int]:
+    n = ctypes.c_size_t(0)
+    st = load_library().relattn_backward_sinks_workspace_size(ctypes.byref(params), sink, ctypes.byref(n))
+    return st, int(n.value)
 
 
 # ------------------------------------------------------------------ 4-bit cache, key weights, eviction
@@ -1068,3 +1095,104 @@ def evict(planes, dst_planes, weights, cu_seqlens_k, cu_seqlens_keep, *, max_seq
     keep, prm.workspace, prm.workspace_bytes = _workspace(need.value, workspace, dev)
     _check(lib.relattn_evict(ref, st), "relattn_evict")
     return key_pos_out, weights_out
+
+
+# ------------------------------------------------------------------ new tokens over a cache, windows with sinks
+
+def relattn_extend(params: RelattnParams, pages: Optional[RelattnPagedKV] = None, sink: int = 0, stream: int = 0) -> int:
+    return load_library().relattn_extend(ctypes.byref(params), _ref(pages), sink, ctypes.c_void_p(stream))
+
+
+def relattn_extend_workspace_size(params: RelattnParams, pages: Optional[RelattnPagedKV] = None,
+                                  sink: int = 0) -> Tuple[int, int]:
+    n = ctypes.c_size_t(0)
+    st = load_library().relattn_extend_workspace_size(ctypes.byref(params), _ref(pages), sink, ctypes.byref(n))
+    return st, int(n.value)
+
+
+def relattn_prologue_paged(params: RelattnPrologueParams, pages: RelattnPagedKV, stream: int = 0) -> int:
+    return load_library().relattn_prologue_paged(ctypes.byref(params), ctypes.byref(pages), ctypes.c_void_p(stream))
+
+
+def extend(q, k, v, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int, max_seqlen_k: int, alpha: float,
+           window: int = 0, sink: int = 0, log_scale_base: float = 0.0, block_table=None, page_size: int = 0,
+           total_k: Optional[int] = None, num_splits: int = 0, out=None, lse=None, workspace=None,
+           stream: Optional[int] = None):
+    """Attention of new tokens -- one, a chunk, a whole prompt -- over the cache
+    that holds them: k / v bf16 [rows, Hkv, 128], contiguous, or with
+    ``block_table`` int32 [batch, max_pages_per_seq] a pool of pages of
+    ``page_size`` keys (a multiple of 16).  A ``window`` keeps the first
+    ``sink`` keys.  ``total_k`` (the sum of the key counts) sizes the work
+    split; without it a paged call reads it back from cu_seqlens_k, which waits
+    for the stream.  ``num_splits``: 0 chooses; n > 0 cuts a row's keys into at
+    most n partials.  Returns (out, lse)."""
+    import torch
+    dev = q.device
+    st = _stream_here(dev, stream)
+    if st is None:
+        with _switched(dev, stream):
+            return extend(q, k, v, r, P, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
+                          max_seqlen_k=max_seqlen_k, alpha=alpha, window=window, sink=sink, log_scale_base=log_scale_base,
+                          block_table=block_table, page_size=page_size, total_k=total_k, num_splits=num_splits, out=out,
+                          lse=lse, workspace=workspace)
+    rows, H, _ = _shape(k, "k", 3, HEAD_DIM)
+    kp, vp = _address(k, "k", torch.bfloat16, dev), _tensor(v, "v", torch.bfloat16, k.shape, dev)
+    Tq, Hq, rd, E, qp, rp, Pp = _queries(q, r, P, H, dev)
+    batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
+    pages = _pages(block_table, page_size, rows, dev, batch)
+    if out is None:
+        out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _tensor(out, "out", torch.bfloat16, (Tq, Hq, HEAD_DIM), dev)
+    if lse is None:
+        lse = torch.empty(Hq, Tq, dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    else:
+        lp = _tensor(lse, "lse", torch.float32, (Hq, Tq), dev)
+    if block_table is None:
+        _need(total_k is None or total_k == rows, "a contiguous k has total_k rows")
+    total_k = _total_k(total_k, block_table, cu_seqlens_k, rows)
+    _fit(total_k, max_seqlen_q, max_seqlen_k, window, sink, num_splits)
+    prm = RelattnParams(
+        qp, kp, vp, rp, Pp, cq, ck, batch, Tq, total_k, max_seqlen_q, max_seqlen_k, Hq, H, HEAD_DIM, rd, E, window,
+        alpha, log_scale_base, op, lp, None, 0, num_splits)
+    lib, need = _lib or load_library(), ctypes.c_size_t()
+    ref, pages = ctypes.byref(prm), _ref(pages)
+    _check(lib.relattn_extend_workspace_size(ref, pages, sink, ctypes.byref(need)), "relattn_extend_workspace_size")
+    keep, prm.workspace, prm.workspace_bytes = _workspace(need.value, workspace, dev)
+    _check(lib.relattn_extend(ref, pages, sink, st), "relattn_extend")
+    return out, lse
+
+
+def _prologue_paged(q, k, v, conv_k, conv_v, norm_q, norm_k, cu_seqlens_q, cu_seqlens_k, k_pool, v_pool, eps, q_out,
+                    conv_state_in, conv_state_out, mxfp8, block_table, page_size, stream):
+    import torch
+    _need(mxfp8 is None, "a paged cache is bf16 only")
+    dev, bf16, f32 = q.device, torch.bfloat16, torch.float32
+    st = _stream_here(dev, stream)
+    if st is None:
+        with _switched(dev, stream):
+            return _prologue_paged(q, k, v, conv_k, conv_v, norm_q, norm_k, cu_seqlens_q, cu_seqlens_k, k_pool, v_pool, eps,
+                                   q_out, conv_state_in, conv_state_out, mxfp8, block_table, page_size, None)
+    Tq, Hq, _ = _shape(q, "q", 3, HEAD_DIM)
+    H = int(_shape(k, "k", 3, HEAD_DIM)[1])
+    rows = int(_shape(k_pool, "k_cache", 3, H, HEAD_DIM)[0])
+    batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
+    pages = _pages(block_table, page_size, rows, dev, batch)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    states = [None] * 4
+    for i, (pair, name) in enumerate(((conv_state_in, "conv_state_in"), (conv_state_out, "conv_state_out"))):
+        if pair is not None:
+            states[2 * i:2 * i + 2] = [None if t is None else _tensor(t, name, bf16, (batch, 3, H * HEAD_DIM), dev)
+                                       for t in pair]
+    prm = RelattnPrologueParams(
+        _address(q, "q", bf16, dev), _tensor(k, "k", bf16, (Tq, H, HEAD_DIM), dev), _tensor(v, "v", bf16, (Tq, H, HEAD_DIM), dev),
+        _tensor(conv_k, "conv_k", f32, (H * HEAD_DIM, 4), dev), _tensor(conv_v, "conv_v", f32, (H * HEAD_DIM, 4), dev),
+        _tensor(norm_q, "norm_q", f32, (HEAD_DIM,), dev), _tensor(norm_k, "norm_k", f32, (HEAD_DIM,), dev), eps,
+        cq, ck, batch, Tq, 0, Hq, H, HEAD_DIM, _tensor(q_out, "q_out", bf16, (Tq, Hq, HEAD_DIM), dev),
+        _address(k_pool, "k_cache", bf16, dev), _tensor(v_pool, "v_cache", bf16, (rows, H, HEAD_DIM), dev), *states)
+    _check((_lib or load_library()).relattn_prologue_paged(ctypes.byref(prm), ctypes.byref(pages), st),
+           "relattn_prologue_paged")
+    return q_out

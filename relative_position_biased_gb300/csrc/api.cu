@@ -65,6 +65,7 @@ relattn_status device_state(int *dev_out, int **err_out, int *sms_out) {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr int kMaxRDim = 64;
+constexpr long kMaxKeys = 0x7fff0000L;      // of a sequence: the walks step past its end by less than the rest
 constexpr int kMaxDecodeRows = 16;
 
 relattn_status validate(const relattn_params *p, bool decode) {
@@ -255,7 +256,32 @@ size_t backward_workspace_bytes(const relattn_params &f) {
   return backward_d_bytes(f) + backward_rall_bytes(f) + backward_dq_part_bytes(f) + backward_dkv_part_bytes(f);
 }
 
-relattn_status validate_backward(const relattn_bwd_params *p) {
+// The workspace of a window with sinks goes on with (fp32) their part of dq
+// [Tq, Hq, 128], of dr [Tq, Hq, r_dim] where E reaches past the window, of dk
+// and dv [batch, Hkv, sink, 2, 128], and the partials of the last.
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+struct SinkBytes {
+  size_t dq, dr, dkv, part;
+};
+SinkBytes backward_sink_bytes(const relattn_params &f, int32_t sink) {
+  const size_t rows = (size_t)f.total_q * f.num_heads_q;
+  const bool far = f.r_dim > 0 && f.rel_extent > f.window;
+  return {rows * kHeadDim * sizeof(float), far ? align256(rows * f.r_dim * sizeof(float)) : 0,
+          align256((size_t)f.batch * f.num_heads_kv * sink * 2 * kHeadDim * sizeof(float)),
+          bwd_sink_part_bytes(f.batch, f.total_q, f.num_heads_kv, f.num_heads_q / f.num_heads_kv, sink)};
+}
+size_t backward_sinks_total(const relattn_params &f, int32_t sink) {
+  const size_t base = backward_workspace_bytes(f);
+  if (sink <= 0 || f.total_q == 0) return base;
+  const SinkBytes n = backward_sink_bytes(f, sink);
+  return align256(base) + n.dq + n.dr + n.dkv + n.part;
+}
+relattn_status check_backward_sink(const relattn_params &f, int32_t sink) {
+  if (sink < 0) return RELATTN_ERR_INVALID_ARG;
+  return sink > RELATTN_MAX_BACKWARD_SINK ? RELATTN_ERR_UNSUPPORTED : RELATTN_OK;
+}
+
+relattn_status validate_backward(const relattn_bwd_params *p, int32_t sink) {
   if (!p) return RELATTN_ERR_INVALID_ARG;
   const relattn_params &f = p->fwd;
   relattn_status st = validate(&f, false);
@@ -270,12 +296,14 @@ relattn_status validate_backward(const relattn_bwd_params *p) {
   if (f.r_dim > 0 && (!p->dr || !aligned16(p->dr))) return RELATTN_ERR_INVALID_ARG;
   if (f.r_dim > 0 && f.rel_extent > 0 && (!aligned16(f.r) || !aligned16(f.P)))
     return RELATTN_ERR_INVALID_ARG;
-  if (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < backward_workspace_bytes(f))
+  if (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < backward_sinks_total(f, sink))
     return RELATTN_ERR_WORKSPACE;
   return RELATTN_OK;
 }
 
-relattn_status validate_prologue(const relattn_prologue_params *p, const relattn_kv_mxfp8_out *mx = nullptr) {
+// kv: the bf16 cache is paged (its arrays then hold the pool's rows)
+relattn_status validate_prologue(const relattn_prologue_params *p, const relattn_kv_mxfp8_out *mx = nullptr,
+                                 const relattn_paged_kv *kv = nullptr) {
   if (!p) return RELATTN_ERR_INVALID_ARG;
   if (p->head_dim != kHeadDim) return RELATTN_ERR_UNSUPPORTED;
   if (p->batch < 0 || p->total_q < 0 || p->total_k < 0 || p->num_heads_q <= 0 ||
@@ -309,7 +337,8 @@ relattn_status validate_prologue(const relattn_prologue_params *p, const relattn
   const size_t row = (size_t)kHeadDim * 2;
   const size_t q_bytes = (size_t)p->total_q * p->num_heads_q * row;
   const size_t kv_bytes = (size_t)p->total_q * p->num_heads_kv * row;
-  const size_t cache_bytes = (size_t)p->total_k * p->num_heads_kv * row;
+  const size_t cache_rows = kv ? (size_t)kv->num_pages * kv->page_size : (size_t)p->total_k;
+  const size_t cache_bytes = cache_rows * p->num_heads_kv * row;
   const size_t state_bytes = (size_t)p->batch * 3 * p->num_heads_kv * row;
   if (p->q_out != p->q && overlaps(p->q_out, q_bytes, p->q, q_bytes)) return RELATTN_ERR_INVALID_ARG;
   const void *kv_in[] = {p->k, p->v};
@@ -324,10 +353,46 @@ relattn_status validate_prologue(const relattn_prologue_params *p, const relattn
   return RELATTN_OK;
 }
 
+// ---- new tokens over a cache, windows with sinks
+
+constexpr int kExtendPageUnit = 16;         // page sizes of the bf16 cache are multiples of it
+
+// Checks a bf16 page table; max_k: the longest sequence it has to hold (0: checked on the device).
+relattn_status check_pages(const relattn_paged_kv *kv, long max_k) {
+  if (kv->page_size <= 0 || kv->num_pages <= 0 || kv->max_pages_per_seq <= 0) return RELATTN_ERR_INVALID_ARG;
+  if (kv->page_size % kExtendPageUnit != 0) return RELATTN_ERR_UNSUPPORTED;
+  if ((long)kv->num_pages * kv->page_size > 0x7fffffffL) return RELATTN_ERR_UNSUPPORTED;
+  if ((long)kv->max_pages_per_seq * kv->page_size < max_k) return RELATTN_ERR_INVALID_ARG;
+  if (!kv->block_table || !aligned(kv->block_table, 4)) return RELATTN_ERR_INVALID_ARG;
+  return RELATTN_OK;
+}
+
+relattn_status validate_extend(const relattn_params *p, const relattn_paged_kv *kv, int32_t sink) {
+  relattn_status st = validate(p, false);
+  if (st != RELATTN_OK) return st;
+  if (sink < 0) return RELATTN_ERR_INVALID_ARG;
+  if (kv && (st = check_pages(kv, p->max_seqlen_k)) != RELATTN_OK) return st;
+  if (p->max_seqlen_k > kMaxKeys) return RELATTN_ERR_UNSUPPORTED;
+  return p->batch > 65535 || p->num_heads_q > 65535 ? RELATTN_ERR_UNSUPPORTED : RELATTN_OK;
+}
+
+relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, int32_t sink, KernelArgs *a) {
+  const relattn_status st = make_args(p, a);
+  if (st != RELATTN_OK) return st;
+  a->sink = a->window > 0 ? sink : 0;
+  a->kv_rows = kv ? kv->num_pages * kv->page_size : p->total_k;
+  if (kv) {
+    a->block_table = kv->block_table;
+    a->page_size = kv->page_size;
+    a->max_pages = kv->max_pages_per_seq;
+    a->num_pages = kv->num_pages;
+  }
+  return RELATTN_OK;
+}
+
 // ---- the 4-bit cache, key weights and eviction
 
 constexpr long kMaxRows = 0x7fffffffL;
-constexpr long kMaxKeys = 0x7fff0000L;      // of a sequence: the walks step past its end by less than the rest
 
 // Checks a page table and fills the row addressing; max_k: the longest
 // sequence it has to hold (0: checked on the device).
@@ -673,8 +738,9 @@ relattn_status relattn_backward_workspace_size(const relattn_bwd_params *p, size
   return RELATTN_OK;
 }
 
-relattn_status relattn_backward(const relattn_bwd_params *p, void *stream) {
-  relattn_status st = validate_backward(p);
+// sink: the keys that a window keeps (0 without a window)
+static relattn_status run_backward(const relattn_bwd_params *p, int32_t sink, void *stream) {
+  relattn_status st = validate_backward(p, sink);
   if (st != RELATTN_OK) return st;
   const relattn_params &f = p->fwd;
   if (f.batch == 0) return RELATTN_OK;
@@ -735,7 +801,32 @@ relattn_status relattn_backward(const relattn_bwd_params *p, void *stream) {
   a.p_vec_ok = bias && f.rel_extent % 8 == 0;
   a.q_tiles = (f.max_seqlen_q + 63) / 64;
   a.k_tiles = (f.max_seqlen_k + 63) / 64;
+  if ((a.sink = sink) > 0) {
+    const SinkBytes n = backward_sink_bytes(f, sink);
+    char *ws = static_cast<char *>(p->workspace) + align256(backward_workspace_bytes(f));
+    a.sink_dq = reinterpret_cast<float *>(ws);
+    a.sink_dr = n.dr > 0 ? reinterpret_cast<float *>(ws + n.dq) : nullptr;
+    a.sink_dkv = reinterpret_cast<float *>(ws + n.dq + n.dr);
+    a.sink_part = reinterpret_cast<float *>(ws + n.dq + n.dr + n.dkv);
+  }
   return cuda_status(launch_backward(a, sms, s));
+}
+
+relattn_status relattn_backward(const relattn_bwd_params *p, void *stream) { return run_backward(p, 0, stream); }
+
+relattn_status relattn_backward_sinks_workspace_size(const relattn_bwd_params *p, int32_t sink, size_t *bytes) {
+  relattn_status st = relattn_backward_workspace_size(p, bytes);
+  if (st != RELATTN_OK) return st;
+  if ((st = check_backward_sink(p->fwd, sink)) != RELATTN_OK) return st;
+  *bytes = backward_sinks_total(p->fwd, p->fwd.window > 0 ? sink : 0);
+  return RELATTN_OK;
+}
+
+relattn_status relattn_backward_sinks(const relattn_bwd_params *p, int32_t sink, void *stream) {
+  if (!p) return RELATTN_ERR_INVALID_ARG;
+  const relattn_status st = check_backward_sink(p->fwd, sink);
+  if (st != RELATTN_OK) return st;
+  return run_backward(p, p->fwd.window > 0 ? sink : 0, stream);
 }
 
 relattn_status relattn_prologue(const relattn_prologue_params *p, void *stream) {
@@ -760,6 +851,35 @@ relattn_status relattn_prologue_mxfp8(const relattn_prologue_params *p, const re
   if ((st = device_state(nullptr, &err, &sms)) != RELATTN_OK) return st;
   return cuda_status(launch_prologue(p, err, sms, g_test_prologue_skip,
                                      static_cast<cudaStream_t>(stream), cache));
+}
+
+relattn_status relattn_prologue_paged(const relattn_prologue_params *p, const relattn_paged_kv *pages, void *stream) {
+  if (!p || !pages) return RELATTN_ERR_INVALID_ARG;
+  relattn_status st = check_pages(pages, 0);
+  if (st == RELATTN_OK) st = validate_prologue(p, nullptr, pages);
+  if (st != RELATTN_OK) return st;
+  if (p->batch == 0) return RELATTN_OK;
+  int *err = nullptr, sms = 0;
+  if ((st = device_state(nullptr, &err, &sms)) != RELATTN_OK) return st;
+  return cuda_status(launch_prologue(p, err, sms, g_test_prologue_skip, static_cast<cudaStream_t>(stream), nullptr, pages));
+}
+
+relattn_status relattn_extend_workspace_size(const relattn_params *p, const relattn_paged_kv *pages, int32_t sink,
+                                             size_t *bytes) {
+  if (!p || !bytes) return RELATTN_ERR_INVALID_ARG;
+  const relattn_status st = validate_extend(p, pages, sink);
+  if (st != RELATTN_OK) return st;
+  *bytes = 0;
+  return RELATTN_OK;
+}
+
+relattn_status relattn_extend(const relattn_params *p, const relattn_paged_kv *pages, int32_t sink, void *stream) {
+  relattn_status st = validate_extend(p, pages, sink);
+  if (st != RELATTN_OK) return st;
+  if (p->batch == 0 || p->total_q == 0) return RELATTN_OK;
+  KernelArgs a;
+  if ((st = extend_args(p, pages, sink, &a)) != RELATTN_OK) return st;
+  return cuda_status(launch_extend_mma(a, static_cast<cudaStream_t>(stream)));
 }
 
 relattn_status relattn_store_nvfp4(const relattn_cache_rows_params *p, void *stream) {

@@ -566,11 +566,19 @@ __global__ void __launch_bounds__(NTB, 1) relattn_bwd_dq_kernel(const __grid_con
     const float fq = srow[r] * a.alpha;
     __nv_bfloat16 *dst = a.dq + row * kHeadDim + 2 * qq;
     const float *part = a.dq_split ? a.dq_part + row * kHeadDim + 2 * qq : nullptr;
+    // rows past the window: what the sinks add
+    const bool far = a.sink > 0 && pos[r] >= a.window;
+    const float *spart = far ? a.sink_dq + row * kHeadDim + 2 * qq : nullptr;
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
       float x0 = dq[n][2 * r] * fq, x1 = dq[n][2 * r + 1] * fq;
       if (part) {
         const float2 pp = *reinterpret_cast<const float2 *>(part + n * 8);
+        x0 += pp.x;
+        x1 += pp.y;
+      }
+      if (spart) {
+        const float2 pp = *reinterpret_cast<const float2 *>(spart + n * 8);
         x0 += pp.x;
         x1 += pp.y;
       }
@@ -583,7 +591,8 @@ __global__ void __launch_bounds__(NTB, 1) relattn_bwd_dq_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = n * 8 + 2 * qq + e;
-          if (c < a.rd) drd[c] = __float2bfloat16_rn(dr[n][2 * r + e] * srow[r]);
+          if (c < a.rd)
+            drd[c] = __float2bfloat16_rn(dr[n][2 * r + e] * srow[r] + (far && a.sink_dr ? a.sink_dr[row * a.rd + c] : 0.f));
         }
     }
   }
@@ -870,6 +879,16 @@ __global__ void __launch_bounds__(NTB, 1) relattn_bwd_dkdv_kernel(const __grid_c
     const size_t row = (size_t)(ck + j0 + kl) * a.Hkv + g;
     __nv_bfloat16 *dkd = a.dk + row * kHeadDim + 2 * qq;
     __nv_bfloat16 *dvd = a.dv + row * kHeadDim + 2 * qq;
+    if (j0 + kl < a.sink) {                // what rows past the window add
+      const float *sd = a.sink_dkv + (((size_t)b * a.Hkv + g) * a.sink + j0 + kl) * 2 * kHeadDim + 2 * qq;
+#pragma unroll
+      for (int n = 0; n < 16; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          dk[n][2 * rr + e] += sd[n * 8 + e];
+          dv[n][2 * rr + e] += sd[kHeadDim + n * 8 + e];
+        }
+    }
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
       *reinterpret_cast<uint32_t *>(dkd + n * 8) = pack_bf16x2(dk[n][2 * rr], dk[n][2 * rr + 1]);
@@ -909,6 +928,10 @@ cudaError_t launch_backward(const BwdArgs &a, int sms, cudaStream_t stream) {
   BwdArgs aq = a;
   aq.dq_split = tcq && bias ? 1 : 0;
   aq.rall_ok = tc && bias ? 1 : 0;       // the pre-pass above ran
+  if (a.sink > 0) {                      // the sinks' parts, which the kernels below add
+    cudaError_t e = launch_bwd_sink(aq, stream);
+    if (e != cudaSuccess) return e;
+  }
   if (tcq) {
     cudaError_t e = launch_bwd_dq_tc(aq, stream);
     if (e != cudaSuccess) return e;

@@ -396,6 +396,16 @@ relattn_bwd_dkdv_tc_kernel(const __grid_constant__ BwdArgs a,
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
+          if (jl < nkeys && j < a.sink && half == 0) {   // what rows past the window add
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4) {
+              const float4 x = sink_dkv4(a, b, g, j, which, 8 * c + q4);
+              v[4 * q4] = __float_as_uint(__uint_as_float(v[4 * q4]) + x.x);
+              v[4 * q4 + 1] = __float_as_uint(__uint_as_float(v[4 * q4 + 1]) + x.y);
+              v[4 * q4 + 2] = __float_as_uint(__uint_as_float(v[4 * q4 + 2]) + x.z);
+              v[4 * q4 + 3] = __float_as_uint(__uint_as_float(v[4 * q4 + 3]) + x.w);
+            }
+          }
           if (jl < nkeys && pdst) {
             float4 *d4 = reinterpret_cast<float4 *>(pdst + 32 * c);
 #pragma unroll
@@ -751,13 +761,27 @@ relattn_bwd_dq_tc_kernel(const __grid_constant__ BwdArgs a,
                                   __uint_as_float(v[4 * q4 + 2]) * a.alpha, __uint_as_float(v[4 * q4 + 3]) * a.alpha);
         } else {
           __nv_bfloat16 *dst = a.dq + row * kHeadDim + col;
+          if (a.sink > 0 && pos >= a.window) {   // rows past the window: what the sinks add
+            const float4 *sp = reinterpret_cast<const float4 *>(a.sink_dq + row * kHeadDim + col);
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4) {
+              const float4 x = sp[q4];
+              v[4 * q4] = __float_as_uint(fmaf(__uint_as_float(v[4 * q4]), a.alpha, x.x));
+              v[4 * q4 + 1] = __float_as_uint(fmaf(__uint_as_float(v[4 * q4 + 1]), a.alpha, x.y));
+              v[4 * q4 + 2] = __float_as_uint(fmaf(__uint_as_float(v[4 * q4 + 2]), a.alpha, x.z));
+              v[4 * q4 + 3] = __float_as_uint(fmaf(__uint_as_float(v[4 * q4 + 3]), a.alpha, x.w));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a.alpha);
+          }
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
             uint4 o;
-            o.x = pack_bf16x2(__uint_as_float(v[8 * q4 + 0]) * a.alpha, __uint_as_float(v[8 * q4 + 1]) * a.alpha);
-            o.y = pack_bf16x2(__uint_as_float(v[8 * q4 + 2]) * a.alpha, __uint_as_float(v[8 * q4 + 3]) * a.alpha);
-            o.z = pack_bf16x2(__uint_as_float(v[8 * q4 + 4]) * a.alpha, __uint_as_float(v[8 * q4 + 5]) * a.alpha);
-            o.w = pack_bf16x2(__uint_as_float(v[8 * q4 + 6]) * a.alpha, __uint_as_float(v[8 * q4 + 7]) * a.alpha);
+            o.x = pack_bf16x2(__uint_as_float(v[8 * q4 + 0]), __uint_as_float(v[8 * q4 + 1]));
+            o.y = pack_bf16x2(__uint_as_float(v[8 * q4 + 2]), __uint_as_float(v[8 * q4 + 3]));
+            o.z = pack_bf16x2(__uint_as_float(v[8 * q4 + 4]), __uint_as_float(v[8 * q4 + 5]));
+            o.w = pack_bf16x2(__uint_as_float(v[8 * q4 + 6]), __uint_as_float(v[8 * q4 + 7]));
             *reinterpret_cast<uint4 *>(dst + 8 * q4) = o;
           }
         }

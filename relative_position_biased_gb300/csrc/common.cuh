@@ -64,7 +64,25 @@ struct KernelArgs {
   // few-row decode (decode_tc.cu): R = r . P of every decode row and
   // distance < E, fp32 [total_q * Hq][E] in the workspace (null without a bias)
   const float *rdec;
+  // new tokens over a cache (relattn_extend): a window keeps the keys below
+  // sink as well; kv_rows = rows of the k / v arrays (the page pool, or total_k)
+  int sink;
+  int kv_rows;
 };
+
+// The sequence's query rows and (contiguous) key rows lie in their arrays.
+__device__ __forceinline__ bool extend_rows_ok(const KernelArgs &a, int cq, int Lq, int ck, int Lk) {
+  if (cq < 0 || (long)cq + Lq > a.total_q) return false;
+  if (a.block_table) return (long)a.max_pages * a.page_size >= Lk;
+  return ck >= 0 && (long)ck + Lk <= a.kv_rows;
+}
+// Row of key j of sequence b, -1 where its page lies outside the pool.
+__device__ __forceinline__ long extend_key_row(const KernelArgs &a, int b, int ck, int j) {
+  if (!a.block_table) return (long)ck + j;
+  const int slot = j / a.page_size;
+  const int pg = __ldg(a.block_table + (size_t)b * a.max_pages + slot);
+  return (unsigned)pg < (unsigned)a.num_pages ? (long)pg * a.page_size + (j - slot * a.page_size) : -1;
+}
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

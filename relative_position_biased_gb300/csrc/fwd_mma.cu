@@ -47,7 +47,9 @@ struct Layout {
 
 __device__ __forceinline__ int floor8(int x) { return x & ~7; }
 
-template <bool DECODE, int NW, int STAGES, int PW>
+// EXT: the new tokens' attention of relattn_extend -- prefill rows over keys
+// that may lie in pages, with a window that may keep the first a.sink keys.
+template <bool DECODE, bool EXT, int NW, int STAGES, int PW>
 __global__ void __launch_bounds__(NW * 32, 1) relattn_fwd_mma_kernel(const __grid_constant__ KernelArgs a) {
   using L = Layout<NW, STAGES, PW>;
   constexpr int M = L::M;
@@ -75,6 +77,10 @@ __global__ void __launch_bounds__(NW * 32, 1) relattn_fwd_mma_kernel(const __gri
     if (tid == 0) atomicOr(a.err, kDevErrSeqlens);
     return;
   }
+  if (EXT && !extend_rows_ok(a, cq, Lq, ck, Lk)) {
+    if (tid == 0) atomicOr(a.err, kDevErrSeqlens);
+    return;
+  }
   const int off = Lk - Lq;  // bottom-right alignment
   const int row0 = DECODE ? row_block * M : q_tile * M;
   const int nrows = min(M, (DECODE ? Lq * a.group : Lq) - row0);
@@ -98,8 +104,14 @@ __global__ void __launch_bounds__(NW * 32, 1) relattn_fwd_mma_kernel(const __gri
     kbeg += split * a.split_chunk;
     kend = min(kend, kbeg + a.split_chunk);
   }
-  const int ntiles = kend > kbeg ? (kend - kbeg + BN - 1) / BN : 0;
-  auto tile_j0 = [&](int it) { return kbeg + (ntiles - 1 - it) * BN; };  // diagonal first
+  const int nwin = kend > kbeg ? (kend - kbeg + BN - 1) / BN : 0;
+  // then the tiles of the first a.sink keys that the window has left behind
+  const int nsink = EXT && a.window > 0 ? min((a.sink + BN - 1) / BN, kbeg / BN) : 0;
+  const int ntiles = nwin + nsink;
+  auto tile_j0 = [&](int it) {
+    if (EXT && it >= nwin) return (ntiles - 1 - it) * BN;
+    return kbeg + (nwin - 1 - it) * BN;                                  // diagonal first
+  };
 
   const bool has_bias = a.rd > 0 && a.E > 0;
   auto is_band = [&](int j0) { return has_bias && (p_min - (j0 + BN - 1) < a.E); };
@@ -108,8 +120,17 @@ __global__ void __launch_bounds__(NW * 32, 1) relattn_fwd_mma_kernel(const __gri
   auto load_kv = [&](int j0, int stage) {
     for (int idx = tid; idx < BN * 16; idx += NT) {
       const int row = idx >> 4, c = idx & 15, j = j0 + row;
-      const bool ok = j < Lk;
-      const size_t g = ((size_t)(ck + (ok ? j : 0)) * a.Hkv + kv_head) * kHeadDim + c * 8;
+      bool ok = j < Lk;
+      size_t at = (size_t)ck + (ok ? j : 0);
+      if (EXT) {
+        // keys that no row of the tile sees read as zero, whatever the table says of them
+        ok = ok && j <= p_max && (j >= j_lo || j < a.sink);
+        const long r = ok ? extend_key_row(a, b, ck, j) : 0;
+        if (r < 0 && c == 0) atomicOr(a.err, kDevErrSeqlens);
+        ok = ok && r >= 0;
+        at = ok ? (size_t)r : 0;
+      }
+      const size_t g = (at * a.Hkv + kv_head) * kHeadDim + c * 8;
       const uint32_t sw = row * 256 + ((c ^ (row & 7)) << 4);
       cp_async16(sbase + L::off_k + stage * L::kv_stage + sw, a.k + g, ok);
       cp_async16(sbase + L::off_v + stage * L::kv_stage + sw, a.v + g, ok);
@@ -325,7 +346,7 @@ __global__ void __launch_bounds__(NW * 32, 1) relattn_fwd_mma_kernel(const __gri
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int j = j0 + n * 8 + 2 * qq + e;
-            const bool vis = j <= pos[r] && (a.window <= 0 || pos[r] - j < a.window);
+            const bool vis = j <= pos[r] && (a.window <= 0 || pos[r] - j < a.window || (EXT && j < a.sink));
             if (!vis) s[n][2 * r + e] = -INFINITY;
           }
         }
@@ -413,11 +434,11 @@ __global__ void __launch_bounds__(NW * 32, 1) relattn_fwd_mma_kernel(const __gri
 constexpr int kPrefillWarps = 8, kPrefillStages = 2, kPrefillPW = 208;
 constexpr int kDecodeStages = 3, kDecodePW = 112;
 
-template <bool DECODE, int NW, int STAGES, int PW>
+template <bool DECODE, bool EXT, int NW, int STAGES, int PW>
 cudaError_t launch_impl(const KernelArgs &a, dim3 grid, cudaStream_t stream) {
   using L = Layout<NW, STAGES, PW>;
   const int smem = L::total(a.rd_pad);
-  auto kern = relattn_fwd_mma_kernel<DECODE, NW, STAGES, PW>;
+  auto kern = relattn_fwd_mma_kernel<DECODE, EXT, NW, STAGES, PW>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<grid, NW * 32, smem, stream>>>(a);
@@ -451,17 +472,22 @@ size_t decode_mma_smem_bytes(int warps, int rd_pad) {
 
 cudaError_t launch_prefill_mma(const KernelArgs &a, cudaStream_t stream) {
   dim3 grid(a.q_tiles, a.Hq, a.batch);
-  return launch_impl<false, kPrefillWarps, kPrefillStages, kPrefillPW>(a, grid, stream);
+  return launch_impl<false, false, kPrefillWarps, kPrefillStages, kPrefillPW>(a, grid, stream);
+}
+
+cudaError_t launch_extend_mma(const KernelArgs &a, cudaStream_t stream) {
+  dim3 grid(a.q_tiles, a.Hq, a.batch);
+  return launch_impl<false, true, kPrefillWarps, kPrefillStages, kPrefillPW>(a, grid, stream);
 }
 
 cudaError_t launch_decode_mma(const KernelArgs &a, int warps, cudaStream_t stream) {
   dim3 grid(a.num_splits, a.Hkv * a.row_blocks, a.batch);
   switch (warps) {
-    case 1: return launch_impl<true, 1, kDecodeStages, kDecodePW>(a, grid, stream);
-    case 2: return launch_impl<true, 2, kDecodeStages, kDecodePW>(a, grid, stream);
-    case 4: return launch_impl<true, 4, kDecodeStages, kDecodePW>(a, grid, stream);
-    case 5: return launch_impl<true, 5, kDecodeStages, kDecodePW>(a, grid, stream);
-    case 8: return launch_impl<true, 8, kDecodeStages, kDecodePW>(a, grid, stream);
+    case 1: return launch_impl<true, false, 1, kDecodeStages, kDecodePW>(a, grid, stream);
+    case 2: return launch_impl<true, false, 2, kDecodeStages, kDecodePW>(a, grid, stream);
+    case 4: return launch_impl<true, false, 4, kDecodeStages, kDecodePW>(a, grid, stream);
+    case 5: return launch_impl<true, false, 5, kDecodeStages, kDecodePW>(a, grid, stream);
+    case 8: return launch_impl<true, false, 8, kDecodeStages, kDecodePW>(a, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -59,6 +59,8 @@ size_t prefill_mma_smem_bytes(int rd_pad);
 size_t decode_mma_smem_bytes(int warps, int rd_pad);
 
 cudaError_t launch_prefill_mma(const KernelArgs &a, cudaStream_t stream);
+// new tokens over a contiguous or paged cache, a window with sinks: any shape
+cudaError_t launch_extend_mma(const KernelArgs &a, cudaStream_t stream);
 
 // tcgen05 / TMA kernels: need 16-byte aligned q/k/v/out (and r/P), r_dim % 8 == 0,
 // rel_extent % 8 == 0, r_dim <= 64 and at least one 128-key tile of K/V.
@@ -129,7 +131,21 @@ struct BwdArgs {
   float alpha, alpha_log2e, inv_ln_base;
   int p_vec_ok;                // 16-byte vector loads of P allowed (E % 8 == 0)
   int q_tiles, k_tiles;        // 64-row / 64-key tiles per sequence (max)
+  // A window with sinks (bwd_sink.cu), else sink = 0 and null: what the keys
+  // below `sink` outside the windows add, fp32, computed before the kernels
+  // that add it.  Only rows at positions >= window have sink_dq / sink_dr.
+  int sink;
+  float *sink_dq;              // workspace [Tq, Hq, 128]
+  float *sink_dr;              // workspace [Tq, Hq, r_dim], where E reaches past the window; else null
+  float *sink_dkv;             // workspace [batch, Hkv, sink, 2 (dk, dv), 128]
+  float *sink_part;            // workspace: partials of sink_dkv
 };
+// float4 group `lane` of key j's (dk, dv)[which] sink sum
+__device__ __forceinline__ float4 sink_dkv4(const BwdArgs &a, int b, int g, int j, int which, int lane) {
+  return reinterpret_cast<const float4 *>(a.sink_dkv)[((((size_t)b * a.Hkv + g) * a.sink + j) * 2 + which) * (kHeadDim / 4) + lane];
+}
+size_t bwd_sink_part_bytes(int batch, int total_q, int Hkv, int group, int sink);
+cudaError_t launch_bwd_sink(const BwdArgs &a, cudaStream_t stream);
 size_t bwd_dq_smem_bytes(int rd_pad);
 size_t bwd_dkdv_smem_bytes(int rd_pad);
 cudaError_t launch_backward(const BwdArgs &a, int sms, cudaStream_t stream);
@@ -147,7 +163,8 @@ cudaError_t launch_bwd_dq_tc(const BwdArgs &a, cudaStream_t stream);
 // skip_tile = test hook (a token tile whose copies are never issued; -1 = off).
 // mx: an MXFP8 cache to write as well (or instead, with null bf16 caches).
 cudaError_t launch_prologue(const relattn_prologue_params *p, int *err, int sms, int skip_tile,
-                            cudaStream_t stream, const relattn_kv_mxfp8_out *mx = nullptr);
+                            cudaStream_t stream, const relattn_kv_mxfp8_out *mx = nullptr,
+                            const relattn_paged_kv *pages = nullptr);
 
 // The 4-bit (NVFP4) K / V cache (nvfp4.cuh): codes [rows, Hkv, 64] (16-byte
 // aligned), scales [rows, Hkv, 8] (8-byte aligned), factors [Hkv] or null (1).

@@ -48,7 +48,21 @@ struct PrologueArgs {
   uint8_t *k8, *v8, *ks8, *vs8;
   int *err;
   int skip_tile;   // test hook: a token tile whose copies are never issued (-1: none)
+  // paged cache (null: contiguous rows): key p of sequence b in pool row
+  // block_table[b * max_pages + p / page_size] * page_size + p % page_size
+  const int32_t *block_table;
+  int page_size, max_pages, num_pages;
 };
+
+// Cache row of key p of sequence b (ck = cu_k[b], ck1 = cu_k[b + 1]); -1 where
+// it lies outside the cache.
+__device__ __forceinline__ long cache_row_of(const PrologueArgs &a, int b, int ck, int ck1, int p) {
+  if (a.block_table == nullptr) return ck >= 0 && ck1 <= a.total_k ? (long)ck + p : -1;
+  const int slot = p / a.page_size;
+  if (slot >= a.max_pages) return -1;
+  const int pg = __ldg(a.block_table + (size_t)b * a.max_pages + slot);
+  return (unsigned)pg < (unsigned)a.num_pages ? (long)pg * a.page_size + (p - slot * a.page_size) : -1;
+}
 
 // MXFP8 of a cache row's 32-dim block spread over 32 / N lanes (N values
 // each, consecutive lanes holding consecutive dims; `mask` covers them):
@@ -136,7 +150,8 @@ relattn_prologue_kernel(const PrologueArgs a) {
       const int Lq = a.cu_q[b + 1] - cq, Lk = a.cu_k[b + 1] - ck;
       const int tc = t - cq;                                // row within the chunk
       // the row must lie in its sequence and the sequence's cache rows in the cache
-      if (tc < 0 || tc >= Lq || Lk < Lq || ck < 0 || a.cu_k[b + 1] > a.total_k) {
+      const long crow = tc >= 0 && tc < Lq && Lk >= Lq ? cache_row_of(a, b, ck, a.cu_k[b + 1], Lk - Lq + tc) : -1;
+      if (crow < 0) {
         if (lane == 0) atomicOr(a.err, kDevErrSeqlens);
         continue;
       }
@@ -154,7 +169,7 @@ relattn_prologue_kernel(const PrologueArgs a) {
           x[j][d][0] = x[j][d][1] = x[j][d][2] = x[j][d][3] = 0.f;
         }
       }
-      out_row[j] = (long)ck + (Lk - Lq) + tc;
+      out_row[j] = crow;
     }
     // ---- arithmetic and stores
 #pragma unroll
@@ -362,7 +377,7 @@ struct KvRow {
 // warp waits for the stage, does its share of the rows and releases it.  No
 // block-wide barrier inside the loop.  Stage layout: q [T][Hq][128], then k
 // and v [T + 3][Hkv][128] each (row j of k / v is token t0 - 3 + j).  Token
-// info: {row in the sequence's chunk, cache row - token, ok, sequence}.
+// info: {row in the sequence's chunk, cache row, ok, sequence}.
 __global__ void __launch_bounds__(kStagedThreads, 2)
 relattn_prologue_staged_kernel(const PrologueArgs a, int T) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -421,9 +436,9 @@ relattn_prologue_staged_kernel(const PrologueArgs a, int T) {
         const int cq = a.cu_q[b], ck = a.cu_k[b];
         const int Lq = a.cu_q[b + 1] - cq, Lk = a.cu_k[b + 1] - ck;
         const int pos = t - cq;
-        const bool ok = pos >= 0 && pos < Lq && Lk >= Lq && ck >= 0 && a.cu_k[b + 1] <= a.total_k;
-        if (!ok) atomicOr(a.err, kDevErrSeqlens);
-        info_all[st * kMaxTileTokens + lane] = make_int4(pos, ck + (Lk - Lq) - cq, ok ? 1 : 0, b);
+        const long crow = pos >= 0 && pos < Lq && Lk >= Lq ? cache_row_of(a, b, ck, a.cu_k[b + 1], Lk - Lq + pos) : -1;
+        if (crow < 0) atomicOr(a.err, kDevErrSeqlens);
+        info_all[st * kMaxTileTokens + lane] = make_int4(pos, (int)crow, crow >= 0 ? 1 : 0, b);
       }
       __syncwarp();
       if (lane == 0 && tile != a.skip_tile) {
@@ -515,7 +530,7 @@ relattn_prologue_staged_kernel(const PrologueArgs a, int T) {
           }
         }
         R.w = wsm + (R.is_k ? 0 : kTaps * C) + h * kHeadDim + dim;
-        R.crow = (size_t)(t0 + tt + in.y) * Hkv + h;
+        R.crow = (size_t)in.y * Hkv + h;      // (used where the row is live)
       };
       auto conv = [&](const KvRow &R, float (&y)[8]) {
 #pragma unroll
@@ -570,8 +585,12 @@ relattn_prologue_staged_kernel(const PrologueArgs a, int T) {
 }  // namespace
 
 cudaError_t launch_prologue(const relattn_prologue_params *p, int *err, int sms, int skip_tile,
-                            cudaStream_t stream, const relattn_kv_mxfp8_out *mx) {
+                            cudaStream_t stream, const relattn_kv_mxfp8_out *mx, const relattn_paged_kv *pages) {
   PrologueArgs a;
+  a.block_table = pages ? pages->block_table : nullptr;
+  a.page_size = pages ? pages->page_size : 0;
+  a.max_pages = pages ? pages->max_pages_per_seq : 0;
+  a.num_pages = pages ? pages->num_pages : 0;
   a.skip_tile = skip_tile;
   a.k8 = mx ? static_cast<uint8_t *>(mx->k) : nullptr;
   a.v8 = mx ? static_cast<uint8_t *>(mx->v) : nullptr;
