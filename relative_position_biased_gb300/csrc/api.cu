@@ -151,7 +151,8 @@ struct DecodePlan {
 
 // kv_rows: rows of the K / V tensors the kernels address (total_k, or the
 // page pool's rows for paged K / V)
-relattn_status plan_decode(const relattn_params *p, DecodePlan *plan, long kv_rows = -1) {
+// sink: keys that a window keeps besides its own
+relattn_status plan_decode(const relattn_params *p, DecodePlan *plan, long kv_rows = -1, long sink = 0) {
   int sms = 0;
   relattn_status st = device_state(nullptr, nullptr, &sms);
   if (st != RELATTN_OK) return st;
@@ -172,7 +173,7 @@ relattn_status plan_decode(const relattn_params *p, DecodePlan *plan, long kv_ro
   // keys any CTA of one (sequence, kv head) may visit, from an aligned start
   long max_vis = p->max_seqlen_k;
   if (p->window > 0) {
-    const long w = (long)p->window + p->max_seqlen_q - 1 + (tile - 1);
+    const long w = (long)p->window + p->max_seqlen_q - 1 + (tile - 1) + (sink + tile - 1) / tile * tile;
     if (w < max_vis) max_vis = w;
   }
   if (max_vis < 1) max_vis = 1;
@@ -376,6 +377,15 @@ relattn_status validate_extend(const relattn_params *p, const relattn_paged_kv *
   return p->batch > 65535 || p->num_heads_q > 65535 ? RELATTN_ERR_UNSUPPORTED : RELATTN_OK;
 }
 
+// How relattn_extend runs: at most 16 rows per kv head on the few-row decode
+// kernel, else (any shape) on the warp-MMA kernel.
+enum class ExtendKind { kMma, kFew };
+struct ExtendPlan {
+  ExtendKind kind;
+  DecodePlan few;
+  size_t ws_bytes;
+};
+
 relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, int32_t sink, KernelArgs *a) {
   const relattn_status st = make_args(p, a);
   if (st != RELATTN_OK) return st;
@@ -387,6 +397,18 @@ relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, 
     a->max_pages = kv->max_pages_per_seq;
     a->num_pages = kv->num_pages;
   }
+  return RELATTN_OK;
+}
+
+relattn_status plan_extend(const relattn_params *p, const KernelArgs &a, ExtendPlan *plan) {
+  *plan = ExtendPlan{};
+  if (decode_few_rows_supported(a, a.kv_rows)) {
+    plan->kind = ExtendKind::kFew;
+    const relattn_status st = plan_decode(p, &plan->few, a.kv_rows, a.sink);
+    plan->ws_bytes = plan->few.ws_bytes;
+    return st;
+  }
+  plan->kind = ExtendKind::kMma;
   return RELATTN_OK;
 }
 
@@ -867,9 +889,15 @@ relattn_status relattn_prologue_paged(const relattn_prologue_params *p, const re
 relattn_status relattn_extend_workspace_size(const relattn_params *p, const relattn_paged_kv *pages, int32_t sink,
                                              size_t *bytes) {
   if (!p || !bytes) return RELATTN_ERR_INVALID_ARG;
-  const relattn_status st = validate_extend(p, pages, sink);
+  relattn_status st = validate_extend(p, pages, sink);
   if (st != RELATTN_OK) return st;
   *bytes = 0;
+  if (p->batch == 0 || p->total_q == 0) return RELATTN_OK;
+  KernelArgs a;
+  ExtendPlan plan;
+  if ((st = extend_args(p, pages, sink, &a)) != RELATTN_OK) return st;
+  if ((st = plan_extend(p, a, &plan)) != RELATTN_OK) return st;
+  *bytes = plan.ws_bytes;
   return RELATTN_OK;
 }
 
@@ -877,9 +905,27 @@ relattn_status relattn_extend(const relattn_params *p, const relattn_paged_kv *p
   relattn_status st = validate_extend(p, pages, sink);
   if (st != RELATTN_OK) return st;
   if (p->batch == 0 || p->total_q == 0) return RELATTN_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   KernelArgs a;
+  ExtendPlan plan;
   if ((st = extend_args(p, pages, sink, &a)) != RELATTN_OK) return st;
-  return cuda_status(launch_extend_mma(a, static_cast<cudaStream_t>(stream)));
+  if ((st = plan_extend(p, a, &plan)) != RELATTN_OK) return st;
+  if (plan.ws_bytes > 0 && (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < plan.ws_bytes))
+    return RELATTN_ERR_WORKSPACE;
+  char *ws = static_cast<char *>(p->workspace);
+  if (plan.kind == ExtendKind::kFew) {
+    a.num_splits = plan.few.splits;
+    a.split_chunk = plan.few.chunk;
+    if (plan.few.splits > 1) {
+      a.o_part = reinterpret_cast<float *>(ws);
+      a.lse_part = reinterpret_cast<float *>(ws + plan.few.lse_offset);
+    }
+    if (decode_rel_bytes(a) > 0) a.rdec = reinterpret_cast<const float *>(ws + plan.few.rel_offset);
+    const cudaError_t e = launch_extend_few_rows(a, s);
+    if (e != cudaSuccess || plan.few.splits == 1) return cuda_status(e);
+    return cuda_status(launch_extend_combine(a, plan.few.splits, true, s));
+  }
+  return cuda_status(launch_extend_mma(a, s));
 }
 
 relattn_status relattn_store_nvfp4(const relattn_cache_rows_params *p, void *stream) {

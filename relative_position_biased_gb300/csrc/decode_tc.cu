@@ -99,6 +99,10 @@ static_assert(NR == 16, "one 16-column chunk of S^T");
 constexpr int MAXST = 4;                   // K or V ring stages at most (the layouts pick their own)
 constexpr int NTHR = 352;                  // 11 warps (roles below)
 constexpr int PV_WARP = 10;
+// EXT: a warp of its own for the V copies (a small page's copy takes the issuing
+// warp about 50 cycles: 64 sequences of 1 to 32 thousand keys in 16-key pages
+// 219 us with it, 297 without)
+constexpr int V_WARP = 11;
 constexpr float kRescale = 8.f;            // log2 units
 
 constexpr uint32_t BOX = 16384;            // 128 rows of 128 bytes (64 bf16 dims or 128 fp8 dims), 128B swizzle
@@ -194,6 +198,7 @@ struct DecArgs {
   float *rslot;      // per (CTA, softmax warpgroup): R^T [nt_e * 128][rs] fp32
   int q_bytes;       // bytes of the item's q box pair
   int n_items;
+  int box;           // relattn_extend: rows of a K / V copy (a page's share of a tile)
 };
 
 // Reduction over the warp's 32 lanes of each of the 16 per-lane values, left
@@ -224,10 +229,16 @@ __device__ __forceinline__ float transpose_reduce(const float (&v)[NR], int lane
 struct Item {
   int b, g, sp, cq, ck, nrows, p0, p_last, kbeg, ntiles;
   int np;   // stream-K: the pieces of the item's (sequence, kv head) unit
+  // EXT: kbeg counts from the sequence's first tile of the walk: `sunk` keys of
+  // whole tiles from key 0 (a window's sinks), then the keys from kbase on
+  int sunk, kbase;
 };
 
-template <bool F8>
-__global__ void __launch_bounds__(NTHR, 1)
+// EXT: the keys of relattn_extend -- pages smaller than a tile (a copy per page,
+// issued by a lane each), pages that no row needs never looked up, rows past
+// the last key cleared, windows that keep their sinks.
+template <bool F8, bool EXT>
+__global__ void __launch_bounds__(EXT ? NTHR + 32 : NTHR, 1)
 relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
                          const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k,
@@ -257,6 +268,13 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
   int *ord = reinterpret_cast<int *>(smem + L::SM_ORD);
   const bool sorted = a.batch <= kOrd;
   const bool sk = da.streamk != 0 && sorted;
+  // EXT: keys of the tiles that hold sinks before the window's first tile
+  auto sink_keys = [&](int kbase) -> int { return a.window > 0 ? min((a.sink + KT - 1) / KT * KT, kbase) : 0; };
+  // first key of tile t of an item
+  auto key0 = [&](const Item &it, int t) -> int {
+    const int v = it.kbeg + KT * t;
+    return !EXT || v < it.sunk ? v : v - it.sunk + it.kbase;
+  };
   auto load_item_into = [&](int idx, Item &it) -> int {   // 1 work, 0 nothing, -1 inconsistent lengths
     int q, u;
     int t_lo = 0, t_hi = 0;
@@ -311,13 +329,19 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
     it.p_last = it.p0 + Lq - 1;
     const int j_lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
     const int kbase = j_lo & ~(KT - 1);
+    if constexpr (EXT) {
+      if (!extend_rows_ok(a, it.cq, Lq, it.ck, Lk)) return -1;
+      it.kbase = kbase;
+      it.sunk = sink_keys(kbase);
+    }
+    const int k0 = EXT ? 0 : kbase, k_end = EXT ? it.sunk + it.p_last + 1 - kbase : it.p_last + 1;
     if (sk) {
-      it.kbeg = kbase + KT * t_lo;
+      it.kbeg = k0 + KT * t_lo;
       it.ntiles = max(0, t_hi - t_lo);
       return 1;
     }
-    it.kbeg = kbase + it.sp * a.split_chunk;
-    const int kend = min(it.p_last + 1, it.kbeg + a.split_chunk);
+    it.kbeg = k0 + it.sp * a.split_chunk;
+    const int kend = min(k_end, it.kbeg + a.split_chunk);
     it.ntiles = kend > it.kbeg ? (kend - it.kbeg + KT - 1) / KT : 0;
     it.np = a.num_splits;
     return 1;
@@ -329,21 +353,28 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
   // iff it has a band tile
   const bool rel_tc = !F8 && da.rel_mode == 2;
   auto first_band = [&](const Item &it) -> int {
+    if constexpr (EXT) {
+      const int x = it.p0 - (KT - 1) - a.E;      // a band tile's first key is above it
+      if (x < 0) return 0;
+      int v = x / KT * KT + KT;                  // (tiles start at multiples of KT)
+      if (v >= it.sunk) v = it.sunk + max(0, v - it.kbase);
+      return max(0, v - it.kbeg) / KT;
+    }
     const int x = it.p0 - it.kbeg - (KT - 1) - a.E;
     return x < 0 ? 0 : x / KT + 1;
   };
   auto band_item = [&](const Item &it) -> bool { return rel_tc && first_band(it) < it.ntiles; };
   // the 128-distance blocks an item's band tiles read: its distances run
   // from p0 - (last key of its tiles) to p_last - (first key), clipped to E
-  auto r_lo = [&](const Item &it) -> int { return max(0, it.p0 - (it.kbeg + KT * it.ntiles - 1)) / KT; };
-  auto r_hi = [&](const Item &it) -> int { return min(da.nt_e - 1, (it.p_last - it.kbeg) / KT); };
+  auto r_lo = [&](const Item &it) -> int { return max(0, it.p0 - (key0(it, it.ntiles - 1) + KT - 1)) / KT; };
+  auto r_hi = [&](const Item &it) -> int { return min(da.nt_e - 1, (it.p_last - key0(it, 0)) / KT); };
   const uint32_t tmem_cols = rel_tc ? (uint32_t)kRelTmemCols : L::TMEM_COLS;
   const uint32_t TM_RS = TM_PT + 32u * (uint32_t)da.nt_e;   // R of the current item
 
   // ------------------------------------------------------------ set-up
   // q and the P buffers start as zeros: rows past an item's real ones then
   // score 0 instead of whatever the memory held
-  for (int i = tid; i < (int)(L::SM_K - L::SM_P) / 16; i += NTHR)
+  for (int i = tid; i < (int)(L::SM_K - L::SM_P) / 16; i += EXT ? NTHR + 32 : NTHR)
     *reinterpret_cast<uint4 *>(smem + L::SM_P + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   if (tid == 0) {
@@ -410,6 +441,7 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
         const int p0 = Lk - Lq, p_last = p0 + Lq - 1;
         const int j_lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
         vis = (long)p_last + 1 - (j_lo & ~(KT - 1));
+        if (EXT) vis += sink_keys(j_lo & ~(KT - 1));
       }
       const long nf = min((long)a.num_splits, vis / a.split_chunk);
       // (stream-K: the unit's tiles instead)
@@ -475,6 +507,37 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
   int issued_q = 0, issued_k = 0, issued_v = 0;
   bool issued_pt = false;
 
+  // EXT: the copies of tile t, one a lane (lane = part of the tile), where some
+  // row needs the part.  Its page is looked up as soon as the tile is known
+  // and first used when the tile's stage is free: nothing waits for the load.
+  auto part_needed = [&](const Item &it, int p) -> bool {
+    return lane * da.box < KT && p <= it.p_last &&
+           (a.window <= 0 || p + da.box > it.p0 - a.window + 1 || p < a.sink);
+  };
+  auto part_page = [&](const Item &it, int t) -> int {
+    const int p = key0(it, t) + lane * da.box;
+    if (a.block_table == nullptr || !part_needed(it, p)) return 0;
+    return __ldg(a.block_table + (size_t)it.b * a.max_pages + p / a.page_size);
+  };
+  // the part's first row; before the arrays (the copy reads zeros) where it is
+  // not needed or its page lies outside the pool
+  auto part_row = [&](const Item &it, int t, int pg) -> int {
+    const int p = key0(it, t) + lane * da.box;
+    if (!part_needed(it, p)) return -KT;
+    if (a.block_table == nullptr) return it.ck + p;
+    if ((unsigned)pg < (unsigned)a.num_pages) return pg * a.page_size + p % a.page_size;
+    atomicOr(a.err, kDevErrSeqlens);
+    return -KT;
+  };
+  auto copy_parts = [&](uint32_t dst, const CUtensorMap *map, int g, int row, uint32_t br) {
+    if (lane == 0) mbar_arrive_expect_tx(br, L::KTILE);
+    __syncwarp();
+    if (lane * da.box < KT) {
+      tma_load_3d(dst + lane * da.box * 128, map, 0, g, row, br);
+      tma_load_3d(dst + BOX + lane * da.box * 128, map, 64, g, row, br);
+    }
+  };
+
   if (warp == 0) {
     // ====================================================== TMA producer
     // Two cursors over the CTA's tiles: the K copies run ahead as soon as a K
@@ -510,12 +573,14 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
       }
       return pg * a.page_size + p % a.page_size;
     };
-    bool k_live = next_item(kidx, ik), v_live = next_item(vidx, iv), q_due = k_live;
+    bool k_live = next_item(kidx, ik), v_live = !EXT && next_item(vidx, iv), q_due = k_live;
+    // (the next tile's rows are looked up as soon as it is known)
+    int kpage = EXT && k_live ? part_page(ik, 0) : 0;
     long long idle_since = -1;
     // in-kernel R: P [r_dim][E] into the (still empty) V ring, 128 distances
     // x r_dim channels per box; the V copies start once the softmax warps
     // have moved it into tensor memory
-    bool pt_free = !rel_tc;
+    bool pt_free = EXT || !rel_tc;
     if (rel_tc) {
       if (lane == 0) {
         const uint32_t box = 256u * (uint32_t)a.rd;
@@ -578,7 +643,10 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
       } else if (k_live) {
         const int st = GK % L::KST;
         if (GK < L::KST || ready(bar(B_K_EMPTY + st), ((GK / L::KST) - 1) & 1)) {
-          if (lane == 0 && GK != a.test_skip_k_tile) {   // (test hook: a skipped tile is never loaded)
+          if constexpr (EXT) {
+            if (GK != a.test_skip_k_tile)
+              copy_parts(sb + L::SM_K + st * L::KTILE, &map_k, ik.g, part_row(ik, kt, kpage), bar(B_K_FULL + st));
+          } else if (lane == 0 && GK != a.test_skip_k_tile) {   // (test hook: a skipped tile is never loaded)
             const int row = tile_row(ik, kt);
             mbar_arrive_expect_tx(bar(B_K_FULL + st), L::KTILE);
             tma_load_3d(sb + L::SM_K + st * L::KTILE, &map_k, 0, ik.g, row, bar(B_K_FULL + st));
@@ -591,6 +659,7 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
             k_live = next_item(kidx, ik);
             q_due = k_live;
           }
+          if (EXT && k_live) kpage = part_page(ik, kt);
           moved = true;
         }
       }
@@ -714,6 +783,25 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
       mma_commit_e(bar(B_DRAIN));
       volatile int keep_waiting = 0;
       mbar_wait(bar(B_DRAIN), 0, &keep_waiting, 9, 400000000ll);
+    }
+    __syncwarp();
+  } else if (EXT && warp == V_WARP) {
+    // ====================================================== V copies
+    Item it{};
+    bool run = !rel_tc || mbar_wait_warp(bar(B_PT_SMEM_FREE), 0, abort_flag, 26);
+    for (int idx = w0; idx < wN && run; idx += wS) {
+      if (load_item_into(idx, it) <= 0) continue;
+      int page = it.ntiles > 0 ? part_page(it, 0) : 0;
+      for (int t = 0; t < it.ntiles && run; ++t) {
+        const int st = issued_v % L::VST;
+        if (issued_v >= L::VST &&
+            !(run = __all_sync(0xffffffffu, mbar_wait_suspend(bar(B_V_EMPTY + st), ((issued_v / L::VST) - 1) & 1,
+                                                              abort_flag, 27))))
+          break;
+        copy_parts(sb + L::SM_V + st * L::KTILE, &map_v, it.g, part_row(it, t, page), bar(B_V_FULL + st));
+        ++issued_v;
+        if (t + 1 < it.ntiles) page = part_page(it, t + 1);
+      }
     }
     __syncwarp();
   } else if (warp == PV_WARP) {
@@ -888,7 +976,7 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
       }
       for (int t = (wg - T) & 1; t < I.ntiles && ok; t += 2, ++tl) {
         const int G = T + t;
-        const int j0 = I.kbeg + KT * t, j = j0 + key;
+        const int j0 = key0(I, t), j = j0 + key;
         const bool band = has_bias && (I.p_last - j0 >= 0) && (I.p0 - (j0 + KT - 1) < a.E);
         const bool edge = (j0 + KT - 1 > I.p0) || (a.window > 0 && j0 < I.p_last - a.window + 1);
         if (t == copy_at) {
@@ -1000,7 +1088,7 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
             const int pos = __float_as_int(rowc[i].z);
-            if (!(j <= pos && (a.window <= 0 || j > pos - a.window))) y[i] = -INFINITY;
+            if (!(j <= pos && (a.window <= 0 || j > pos - a.window || (EXT && j < a.sink)))) y[i] = -INFINITY;
           }
         }
         // the tile's per-row maximum over this warp's keys (lane l: row l % 16),
@@ -1089,6 +1177,17 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
           for (int i = 0; i < NR; ++i)
             *reinterpret_cast<__nv_bfloat16 *>(smem + kb + (uint32_t)i * 128u +
                                                ((kc ^ ((uint32_t)i & 7u)) << 4)) = __float2bfloat16_rn(y[i]);
+        }
+        if (EXT && j0 + KT > I.p_last + 1) {
+          // values past the last key (rows of no key, of another sequence): zero,
+          // so that a NaN there does not meet a weight of zero in the product
+          const int st = G % L::VST;
+          if (!(ok = warp_wait(bar(B_V_FULL + st), (G / L::VST) & 1, 25))) break;
+          if (j > I.p_last) {
+            uint4 *v = reinterpret_cast<uint4 *>(smem + L::SM_V + st * L::KTILE + key * 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[BOX / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -1216,6 +1315,12 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
     for (int G = max(0, issued_k - L::KST); G < issued_k; ++G)
       if (G != a.test_skip_k_tile)
         mbar_wait(bar(B_K_FULL + G % L::KST), (G / L::KST) & 1, &keep_waiting, 15, 400000000ll);
+    if (!EXT)
+      for (int G = max(0, issued_v - L::VST); G < issued_v; ++G)
+        mbar_wait(bar(B_V_FULL + G % L::VST), (G / L::VST) & 1, &keep_waiting, 15, 400000000ll);
+  }
+  if (EXT && warp == V_WARP && lane == 0 && *abort_flag) {
+    volatile int keep_waiting = 0;
     for (int G = max(0, issued_v - L::VST); G < issued_v; ++G)
       mbar_wait(bar(B_V_FULL + G % L::VST), (G / L::VST) & 1, &keep_waiting, 15, 400000000ll);
   }
@@ -1291,10 +1396,11 @@ __global__ void __launch_bounds__(RD) relattn_decode_rel_kernel(const KernelArgs
 template <typename K>
 cudaError_t launch_decode_kernel(K kernel, int grid, uint32_t smem, cudaStream_t stream, const DecArgs &da,
                                  const CUtensorMap &m0, const CUtensorMap &m1, const CUtensorMap &m2,
-                                 const CUtensorMap &m3, const CUtensorMap &m4, bool pdl) {
+                                 const CUtensorMap &m3, const CUtensorMap &m4, bool pdl,
+                                 int threads = NTHR) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(NTHR);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -1410,7 +1516,10 @@ size_t decode_rel_bytes(const KernelArgs &a) {
   return b;
 }
 
-cudaError_t launch_decode_few_rows(const KernelArgs &a, int kv_rows, cudaStream_t stream) {
+namespace {
+
+template <bool EXT>
+cudaError_t launch_few_rows(const KernelArgs &a, int kv_rows, cudaStream_t stream) {
   DecArgs da;
   da.a = a;
   da.kscale = da.vscale = nullptr;
@@ -1422,9 +1531,10 @@ cudaError_t launch_decode_few_rows(const KernelArgs &a, int kv_rows, cudaStream_
   if (items > 0x7fffffffL) return cudaErrorInvalidValue;
   da.n_items = (int)items;
   set_walk(a, da);
+  da.box = EXT ? extend_box(a) : KT;
   CUtensorMap mq, mk, mv, mr;
   if (!encode_heads(&mq, a.q, a.Hq, a.total_q, a.group, a.max_q) ||
-      !encode_heads(&mk, a.k, a.Hkv, kv_rows, 1, KT) || !encode_heads(&mv, a.v, a.Hkv, kv_rows, 1, KT))
+      !encode_heads(&mk, a.k, a.Hkv, kv_rows, 1, da.box) || !encode_heads(&mv, a.v, a.Hkv, kv_rows, 1, da.box))
     return cudaErrorInvalidValue;
   CUtensorMap mp = mq;
   mr = mq;   // (unused unless R is computed in the kernel)
@@ -1461,11 +1571,21 @@ cudaError_t launch_decode_few_rows(const KernelArgs &a, int kv_rows, cudaStream_
   }
   static std::atomic<bool> attr_set[kMaxDevicesAttr];
   constexpr uint32_t smem = Lay<false>::SMEM_BYTES;
-  cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_decode_tc_kernel<false>),
+  cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_decode_tc_kernel<false, EXT>),
                                     (int)smem, attr_set);
   if (e != cudaSuccess) return e;
-  return launch_decode_kernel(relattn_decode_tc_kernel<false>, walk_grid(a, da, items), smem, stream, da, mq,
-                              mk, mv, mr, mp, da.rel_mode == 1);
+  return launch_decode_kernel(relattn_decode_tc_kernel<false, EXT>, walk_grid(a, da, items), smem, stream, da, mq,
+                              mk, mv, mr, mp, da.rel_mode == 1, EXT ? NTHR + 32 : NTHR);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_few_rows(const KernelArgs &a, int kv_rows, cudaStream_t stream) {
+  return launch_few_rows<false>(a, kv_rows, stream);
+}
+
+cudaError_t launch_extend_few_rows(const KernelArgs &a, cudaStream_t stream) {
+  return launch_few_rows<true>(a, a.kv_rows, stream);
 }
 
 cudaError_t launch_decode_mxfp8(const KernelArgs &a, const void *k8, const void *v8, const void *ks,
@@ -1484,6 +1604,7 @@ cudaError_t launch_decode_mxfp8(const KernelArgs &a, const void *k8, const void 
   set_walk(a, da);
   da.rel_mode = da.has_bias ? 1 : 0;
   da.nt_e = da.rs = da.r_bytes = 0;
+  da.box = KT;
   da.rslot = nullptr;
   if (da.has_bias) {
     cudaError_t e = launch_decode_rel(a, stream);
@@ -1506,12 +1627,12 @@ cudaError_t launch_decode_mxfp8(const KernelArgs &a, const void *k8, const void 
     return cudaErrorInvalidValue;
   static std::atomic<bool> attr_set[kMaxDevicesAttr];
   constexpr uint32_t smem = Lay<true>::SMEM_BYTES;
-  cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_decode_tc_kernel<true>),
+  cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_decode_tc_kernel<true, false>),
                                     (int)smem, attr_set);
   if (e != cudaSuccess) return e;
   // (the q and r maps are not read: the producer quantises q rows itself,
   // and R comes from the R kernel)
-  return launch_decode_kernel(relattn_decode_tc_kernel<true>, walk_grid(a, da, items), smem, stream, da, mk,
+  return launch_decode_kernel(relattn_decode_tc_kernel<true, false>, walk_grid(a, da, items), smem, stream, da, mk,
                               mk, mv, mk, mk, da.rel_mode == 1);
 }
 

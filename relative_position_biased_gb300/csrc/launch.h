@@ -59,8 +59,23 @@ size_t prefill_mma_smem_bytes(int rd_pad);
 size_t decode_mma_smem_bytes(int warps, int rd_pad);
 
 cudaError_t launch_prefill_mma(const KernelArgs &a, cudaStream_t stream);
-// new tokens over a contiguous or paged cache, a window with sinks: any shape
+// New tokens over a contiguous or paged cache, a window with sinks
+// (relattn_extend): on warp-level MMAs, any shape (fwd_mma.cu); at most 16 rows
+// per kv head (decode_tc.cu, where decode_few_rows_supported; partials when
+// num_splits > 1).
 cudaError_t launch_extend_mma(const KernelArgs &a, cudaStream_t stream);
+cudaError_t launch_extend_few_rows(const KernelArgs &a, cudaStream_t stream);
+// rows of one K / V copy: a tile of 128 keys, or the largest part of it that
+// pages (multiples of 16 keys) always hold whole
+inline int extend_box(const KernelArgs &a) {
+  if (!a.block_table) return 128;
+  int box = 16;
+  while (box < 128 && a.page_size % (2 * box) == 0) box *= 2;
+  return box;
+}
+// out / lse from `slots` partials of every row of a sequence (extend_tc.cu);
+// other rows keep theirs
+cudaError_t launch_extend_combine(const KernelArgs &a, int slots, bool pdl, cudaStream_t stream);
 
 // tcgen05 / TMA kernels: need 16-byte aligned q/k/v/out (and r/P), r_dim % 8 == 0,
 // rel_extent % 8 == 0, r_dim <= 64 and at least one 128-key tile of K/V.
