@@ -378,12 +378,14 @@ relattn_status validate_extend(const relattn_params *p, const relattn_paged_kv *
 }
 
 // How relattn_extend runs: at most 16 rows per kv head on the few-row decode
-// kernel, else (any shape) on the warp-MMA kernel.
-enum class ExtendKind { kMma, kFew };
+// kernel, more on the tcgen05 kernels of many rows (where shapes and alignment
+// allow), any shape on the warp-MMA kernel.
+enum class ExtendKind { kMma, kFew, kTc };
 struct ExtendPlan {
   ExtendKind kind;
   DecodePlan few;
-  size_t ws_bytes;
+  ExtendTcArgs tc;
+  size_t ws_bytes, lse_offset;
 };
 
 relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, int32_t sink, KernelArgs *a) {
@@ -400,6 +402,56 @@ relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, 
   return RELATTN_OK;
 }
 
+// The tcgen05 kernels of many rows: ranges of the keys, pieces of the band and
+// the partials they need.
+void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *plan) {
+  constexpr long kTile = kTcKeyTile, kMinChunk = 8, kMaxRanges = 64;
+  ExtendTcArgs &x = plan->tc;
+  x.a = a;
+  const bool bias = a.rd > 0 && a.E > 0;
+  x.tokens = 128 / a.group;
+  x.row_tiles = (a.max_q + 2 * x.tokens - 1) / (2 * x.tokens);
+  // row tiles in pairs, the key tiles of one at most and on the average
+  const long pairs = std::min<long>((long)a.batch * x.row_tiles, a.total_q / (2 * x.tokens) + a.batch) * a.Hkv;
+  long most = (a.max_k + kTile - 1) / kTile;
+  if (a.window > 0)
+    most = std::min<long>(most, ((long)a.window + 2 * x.tokens + 2 * kTile) / kTile + (std::min(a.sink, a.max_k) + kTile - 1) / kTile);
+  most = std::max<long>(most, 1);
+  const long mean = std::max<long>(std::min<long>(most, p->total_k / a.batch / kTile), 1);
+  long chunk = most;
+  if (p->num_splits > 0) {
+    chunk = (most + p->num_splits - 1) / p->num_splits;
+  } else if (pairs < 3L * a.sms) {
+    chunk = std::max<long>(kMinChunk, (pairs * mean + 4L * a.sms - 1) / (4L * a.sms));
+  }
+  chunk = std::max<long>(std::min(chunk, most), (most + kMaxRanges - 1) / kMaxRanges);
+  x.splits = (int)((most + chunk - 1) / chunk);
+  x.chunk = (int)chunk;
+  // the band: relattn_prefill's on contiguous rows in one piece (its rows are
+  // positions of one head: half the work of a packed row's shift); sinks outside
+  // the window must have no bias there
+  x.band = !bias ? kBandNone : kBandPacked;
+  x.band_pieces = 1;
+  x.band_tiles = 0;
+  if (bias) {
+    const int rows = extend_band_rows(a);
+    const long tiles = ((long)a.E + rows / a.group + 126) / kTile + 2;
+    const long items = std::min<long>((long)a.batch * (((long)a.max_q * a.group + rows - 1) / rows),
+                                      (long)a.total_q * a.group / rows + a.batch) * a.Hkv;
+    if (p->num_splits <= 0 && items < a.sms) x.band_pieces = (int)std::max<long>(1, std::min<long>(a.sms / items, tiles / 2));
+    if (x.splits == 1 && x.band_pieces == 1 && !a.block_table && a.total_q >= 128 && a.max_q >= 128 &&
+        (a.sink == 0 || a.E <= a.window))
+      x.band = kBandPrefill;
+    x.band_tiles = (int)((tiles + x.band_pieces - 1) / x.band_pieces);
+  }
+  x.slots = x.splits > 1 || x.band_pieces > 1 ? x.splits + (bias ? x.band_pieces : 0) : 1;
+  if (x.slots > 1) {
+    const size_t rows = (size_t)a.total_q * a.Hq;
+    plan->lse_offset = (size_t)x.slots * rows * kHeadDim * sizeof(float);
+    plan->ws_bytes = plan->lse_offset + (size_t)x.slots * rows * sizeof(float);
+  }
+}
+
 relattn_status plan_extend(const relattn_params *p, const KernelArgs &a, ExtendPlan *plan) {
   *plan = ExtendPlan{};
   if (decode_few_rows_supported(a, a.kv_rows)) {
@@ -409,7 +461,30 @@ relattn_status plan_extend(const relattn_params *p, const KernelArgs &a, ExtendP
     return st;
   }
   plan->kind = ExtendKind::kMma;
+  if (tc_supported(a, a.kv_rows) && a.alpha_log2e > 0.f && a.group <= 128) {
+    plan->kind = ExtendKind::kTc;
+    plan_extend_tc(p, a, plan);
+  }
   return RELATTN_OK;
+}
+
+relattn_status run_extend_tc(const relattn_params *p, ExtendPlan &plan, cudaStream_t s) {
+  ExtendTcArgs &x = plan.tc;
+  if (x.slots > 1) {
+    x.a.o_part = static_cast<float *>(p->workspace);
+    x.a.lse_part = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + plan.lse_offset);
+  }
+  cudaError_t e = cudaSuccess;
+  if (x.band == kBandPacked) {
+    e = launch_extend_band(x, s);
+  } else if (x.band == kBandPrefill) {
+    KernelArgs a = x.a;
+    a.band_only = 1;
+    e = launch_prefill_tc(a, p->total_k, s);
+  }
+  if (e == cudaSuccess) e = launch_extend_main(x, s);
+  if (e == cudaSuccess && x.slots > 1) e = launch_extend_combine(x.a, x.slots, false, s);
+  return e == cudaSuccess ? RELATTN_OK : RELATTN_ERR_CUDA;
 }
 
 // ---- the 4-bit cache, key weights and eviction
@@ -925,6 +1000,7 @@ relattn_status relattn_extend(const relattn_params *p, const relattn_paged_kv *p
     if (e != cudaSuccess || plan.few.splits == 1) return cuda_status(e);
     return cuda_status(launch_extend_combine(a, plan.few.splits, true, s));
   }
+  if (plan.kind == ExtendKind::kTc) return run_extend_tc(p, plan, s);
   return cuda_status(launch_extend_mma(a, s));
 }
 

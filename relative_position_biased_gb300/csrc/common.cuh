@@ -76,6 +76,9 @@ __device__ __forceinline__ bool extend_rows_ok(const KernelArgs &a, int cq, int 
   if (a.block_table) return (long)a.max_pages * a.page_size >= Lk;
   return ck >= 0 && (long)ck + Lk <= a.kv_rows;
 }
+// First key that the packed band kernel takes for the row at position pos: those
+// within E, from the start of their 128-key tile on.
+__device__ __forceinline__ int extend_band_first(const KernelArgs &a, int pos) { return max(0, pos - a.E + 1) & ~127; }
 // Row of key j of sequence b, -1 where its page lies outside the pool.
 __device__ __forceinline__ long extend_key_row(const KernelArgs &a, int b, int ck, int j) {
   if (!a.block_table) return (long)ck + j;
