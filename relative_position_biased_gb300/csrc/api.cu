@@ -405,7 +405,7 @@ relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, 
 // The tcgen05 kernels of many rows: ranges of the keys, pieces of the band and
 // the partials they need.
 void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *plan) {
-  constexpr long kTile = kTcKeyTile, kMinChunk = 8, kMaxRanges = 64;
+  constexpr long kTile = kTcKeyTile, kMaxRanges = 64;
   ExtendTcArgs &x = plan->tc;
   x.a = a;
   const bool bias = a.rd > 0 && a.E > 0;
@@ -421,28 +421,33 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
   long chunk = most;
   if (p->num_splits > 0) {
     chunk = (most + p->num_splits - 1) / p->num_splits;
-  } else if (pairs < 3L * a.sms) {
-    chunk = std::max<long>(kMinChunk, (pairs * mean + 4L * a.sms - 1) / (4L * a.sms));
+  } else {
+    // the cut with the shortest time, in steps of a key tile (1.8 us): waves of
+    // CTAs, each with a start of some four steps; partials cost a launch and their
+    // traffic
+    const double rows_us = (double)a.total_q * a.Hq * kHeadDim * 8 / 6.5e6;    // of a partial, out and in
+    double best = 1e30;
+    for (long k = 1; k <= std::min(kMaxRanges, most); ++k) {
+      const long c = (most + k - 1) / k, per = (mean + c - 1) / c, ctas = pairs * per;
+      double t = (double)((ctas + a.sms - 1) / a.sms) * (std::min(c, mean) + 4);
+      if (ctas <= a.sms) t = c + 4;
+      if (k > 1) t += 4 + per * rows_us / 1.8;
+      if (t < best) best = t, chunk = c;
+    }
   }
   chunk = std::max<long>(std::min(chunk, most), (most + kMaxRanges - 1) / kMaxRanges);
   x.splits = (int)((most + chunk - 1) / chunk);
   x.chunk = (int)chunk;
-  // the band: relattn_prefill's on contiguous rows in one piece (its rows are
-  // positions of one head: half the work of a packed row's shift); sinks outside
-  // the window must have no bias there
-  x.band = !bias ? kBandNone : kBandPacked;
+  // the band, in pieces where its items leave SMs idle
+  x.band = bias ? 1 : 0;
   x.band_pieces = 1;
-  x.band_tiles = 0;
+  x.band_steps = 0;
   if (bias) {
-    const int rows = extend_band_rows(a);
-    const long tiles = ((long)a.E + rows / a.group + 126) / kTile + 2;
-    const long items = std::min<long>((long)a.batch * (((long)a.max_q * a.group + rows - 1) / rows),
-                                      (long)a.total_q * a.group / rows + a.batch) * a.Hkv;
-    if (p->num_splits <= 0 && items < a.sms) x.band_pieces = (int)std::max<long>(1, std::min<long>(a.sms / items, tiles / 2));
-    if (x.splits == 1 && x.band_pieces == 1 && !a.block_table && a.total_q >= 128 && a.max_q >= 128 &&
-        (a.sink == 0 || a.E <= a.window))
-      x.band = kBandPrefill;
-    x.band_tiles = (int)((tiles + x.band_pieces - 1) / x.band_pieces);
+    const int tokens = extend_band_tokens(a);
+    const long steps = ((long)a.E + tokens + 126) / 64 + 3;        // at most, of a row block
+    const long items = std::min<long>((long)a.batch * ((a.max_q + tokens - 1) / tokens), a.total_q / tokens + a.batch) * a.Hkv;
+    if (p->num_splits <= 0 && items < a.sms) x.band_pieces = (int)std::max<long>(1, std::min<long>(a.sms / items, steps / 4));
+    x.band_steps = (int)((steps + x.band_pieces - 1) / x.band_pieces);
   }
   x.slots = x.splits > 1 || x.band_pieces > 1 ? x.splits + (bias ? x.band_pieces : 0) : 1;
   if (x.slots > 1) {
@@ -474,16 +479,9 @@ relattn_status run_extend_tc(const relattn_params *p, ExtendPlan &plan, cudaStre
     x.a.o_part = static_cast<float *>(p->workspace);
     x.a.lse_part = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + plan.lse_offset);
   }
-  cudaError_t e = cudaSuccess;
-  if (x.band == kBandPacked) {
-    e = launch_extend_band(x, s);
-  } else if (x.band == kBandPrefill) {
-    KernelArgs a = x.a;
-    a.band_only = 1;
-    e = launch_prefill_tc(a, p->total_k, s);
-  }
+  cudaError_t e = x.band == 0 ? cudaSuccess : launch_extend_band(x, s);
   if (e == cudaSuccess) e = launch_extend_main(x, s);
-  if (e == cudaSuccess && x.slots > 1) e = launch_extend_combine(x.a, x.slots, false, s);
+  if (e == cudaSuccess && x.slots > 1) e = launch_extend_combine(x.a, x.slots, true, s);
   return e == cudaSuccess ? RELATTN_OK : RELATTN_ERR_CUDA;
 }
 

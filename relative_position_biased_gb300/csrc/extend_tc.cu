@@ -82,19 +82,10 @@ __device__ __forceinline__ float row_max(const float (&x)[N]) {
   }
 }
 
-// First key that the band kernel has for the row at position pos of a sequence
-// whose query rows start at position off; keys at and after it are not this kernel's.
-__device__ __forceinline__ int band_first(const ExtendTcArgs &x, int pos, int off) {
-  const KernelArgs &a = x.a;
-  if (x.band == kBandNone) return 0x7fffffff;
-  if (x.band == kBandPacked) return extend_band_first(a, pos);
-  // relattn_prefill's: 128-key tiles from the first position of the row's tile
-  // of 128 backwards, those with some distance below E
-  const int p0 = off + ((pos - off) & ~(BM - 1));
-  const int j_lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  const int tiles = (p0 - j_lo + BN - 1) / BN + 1, lim = a.E + BN - 1;
-  const int nb = BN * (tiles - 1) < lim ? tiles : min(tiles, (lim + BN - 1) / BN);
-  return max(0, p0 - BN * (nb - 1));
+// First key that the band kernel has for the row at position pos; keys at and
+// after it are not this kernel's.
+__device__ __forceinline__ int band_first(const ExtendTcArgs &x, int pos) {
+  return x.band == 0 ? 0x7fffffff : extend_band_first(x.a, pos);
 }
 
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -108,6 +99,16 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
   auto bar = [&](int i) { return sb + SM_BAR + 8u * i; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM_ABORT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // With partials this kernel runs beside the band's, as its programmatic
+  // dependent, and the merge may be launched behind it.  Its first CTA ends after
+  // the band's grid, so that whoever waits for this grid has waited for both.
+  asm volatile("griddepcontrol.launch_dependents;");
+  struct EndAfterBand {
+    __device__ ~EndAfterBand() {
+      if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+  } end_after_band;
 
   // ------------------------------------------------------------ work item
   const int kv_head = blockIdx.y, b = blockIdx.z;
@@ -126,17 +127,16 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
   // keys: [w_lo, w_hi) tiles of the window, and before them the tiles of the sinks
   // that the last row's window has left behind
   const int j_lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  const int b_first = band_first(x, p0, off), b_last = band_first(x, p_last, off);
-  int far = a.window > 0 ? min(a.sink, max(0, p_last - a.window + 1)) : 0;
-  if (x.band == kBandPacked) far = min(far, b_last);
+  const int b_first = band_first(x, p0), b_last = band_first(x, p_last);
+  const int far = a.window > 0 ? min(min(a.sink, max(0, p_last - a.window + 1)), b_last) : 0;
   const int w_lo = j_lo / BN;
-  const int w_hi = (max(min(p_last + 1, b_last), far) + BN - 1) / BN;
+  const int w_hi = (min(p_last + 1, b_last) + BN - 1) / BN;
   const int n_sink = min((far + BN - 1) / BN, w_lo), n_all = n_sink + max(0, w_hi - w_lo);
   auto key0 = [&](int v) { return BN * (v < n_sink ? v : w_lo + v - n_sink); };
   const int v_end = min(n_all, (split + 1) * x.chunk), n_main = max(0, v_end - split * x.chunk);
   auto tile_key = [&](int i) { return key0(v_end - 1 - i); };      // nearest first
   const bool partial = x.slots > 1;
-  const bool init = x.band != kBandNone && !partial;                // go on from the band's out / lse
+  const bool init = x.band != 0 && !partial;                // go on from the band's out / lse
   const size_t rows_all = (size_t)a.total_q * a.Hq;
   if (n_main <= 0) {
     if (partial)                                                    // a range without keys
@@ -321,23 +321,16 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
     const int wq = warp & 3;                     // lane quarter (TMEM lanes 32 wq ..)
     const int a_row = 32 * wq + lane;            // row == TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-    // token and head of the row; rows past the tile's tokens repeat others
-    const int tt = a_row / a.group;
-    const bool valid = tt < TT && w * TT + tt < ntok;
-    const int tok = tok0 + min(w * TT + min(tt, TT - 1), ntok - 1);
-    const int h = kv_head * a.group + a_row % a.group;
-    const int pos = off + tok;
+    // the row: a token and a head (rows past the tile's tokens repeat others).
+    // Only its position stays in a register through the tiles.
+    auto row_token = [&]() { return tok0 + min(w * TT + min(a_row / a.group, TT - 1), ntok - 1); };
+    auto row_head = [&]() { return kv_head * a.group + a_row % a.group; };
+    const int pos = off + row_token();
     const float sc = log_scale(pos, a.inv_ln_base);
     const float cqk = a.alpha_log2e * sc;        // > 0 (checked on the host)
     const bool releaser = (w == nw - 1) && (wq == 0) && (lane == 0);   // frees K / V stages
     const uint32_t obuf = tmem + lane_base + TM_O + 128u * (uint32_t)w;
     const uint32_t sbuf = tmem + lane_base + TM_S + 128u * (uint32_t)w;
-    const size_t qrow = (size_t)(cq + tok) * a.Hq + h;
-    // the row's keys: its window below the band's first, and the sinks its window
-    // has left behind
-    const int row_first = band_first(x, pos, off);
-    const int k_hi = min(pos, row_first - 1), k_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    const int k_far = a.window <= 0 ? 0 : min(min(a.sink, k_lo), x.band == kBandPacked ? row_first : 0x7fffffff);
     auto warp_wait = [&](uint32_t br, uint32_t parity, int site) -> bool {
       const bool r = mbar_wait(br, parity, abort_flag, site);
       return __all_sync(0xffffffffu, r);
@@ -346,12 +339,13 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
     float m_ref = -INFINITY, l = 0.f;
     if (init) {
       // the band's state: m = lse log2(e), l = 1, O = out (normalised)
+      const int tok = row_token(), h = row_head();
       const float lse0 = a.lse[(size_t)h * a.total_q + cq + tok];
       if (lse0 != -INFINITY) {
         m_ref = lse0 * kLog2e;
         l = 1.f;
       }
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.out + qrow * kHeadDim);
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.out + ((size_t)(cq + tok) * a.Hq + h) * kHeadDim);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t r[32];
@@ -381,6 +375,18 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
         if (i > 0) mbar_arrive(bar(B_V_EMPTY + (i - 1) % V_STAGES));
       }
       tc_fence_after();
+      if (w == 0 && tile_key(i) + BN > Lk) {
+        // values past the last key (rows of no key, of another sequence): zero, so
+        // that a NaN there does not meet a weight of zero.  Tile 0's product is
+        // issued first, so this half of its P guards tile 1's as well.
+        if (!(ok = warp_wait(bar(B_V_FULL + i % V_STAGES), (i / V_STAGES) & 1, 51))) break;
+        if (tile_key(i) + a_row >= Lk) {
+          uint4 *v = reinterpret_cast<uint4 *>(smem + SM_V + (i % V_STAGES) * TILE_BYTES + a_row * 128);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = v[BOX_BYTES / 16 + k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
       float x_[128];   // raw scores; the scale is applied inside the exponent
       __syncwarp();
       tmem_ld32f<0>(sbuf + 0u, x_);
@@ -396,9 +402,20 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
       // key or starts before the last row's window)
       const bool need_mask = j0 + BN - 1 > min(p0, b_first - 1) || (a.window > 0 && j0 < p_last - a.window + 1);
       if (need_mask) {
-        const int kmin = k_lo - j0, kmax = k_hi - j0, kfar = k_far - j0;
+        // the row's keys: its window below the band's first, and the sinks that its
+        // window has left behind, as a bit a key
+        int pp = pos;
+        asm volatile("" : "+r"(pp));             // (worked out here: kept, they would spill)
+        const int first = band_first(x, pp), lo = a.window > 0 ? max(0, pp - a.window + 1) : 0;
+        const int kmin = lo - j0, kend = min(pp + 1, first) - j0;
+        const int kfar = j0 < far ? min(min(a.sink, lo), first) - j0 : 0;
+        auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-        for (int k = 0; k < 128; ++k) x_[k] = ((k >= kmin && k <= kmax) || k < kfar) ? x_[k] : -INFINITY;
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t seen = (below(kend - 32 * c) & ~below(kmin - 32 * c)) | below(kfar - 32 * c);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x_[32 * c + k] = (seen >> k) & 1u ? x_[32 * c + k] : -INFINITY;
+        }
       }
       // P (bf16 pairs) of keys 32c .. 32c + 31 over S_w columns [16c, 16c + 16)
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -461,18 +478,6 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
           tmem_st32(obuf + 32u * c, r);
         }
       }
-      if (w == 0 && j0 + BN > Lk) {
-        // values past the last key (rows of no key, of another sequence): zero, so
-        // that a NaN there does not meet a weight of zero.  Tile 0's product is
-        // issued first, so this half of its P guards tile 1's as well.
-        if (!(ok = warp_wait(bar(B_V_FULL + i % V_STAGES), (i / V_STAGES) & 1, 51))) break;
-        if (j0 + a_row >= Lk) {
-          uint4 *v = reinterpret_cast<uint4 *>(smem + SM_V + (i % V_STAGES) * TILE_BYTES + a_row * 128);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = v[BOX_BYTES / 16 + k] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar(B_P_HALF + w));
@@ -488,6 +493,9 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
       if (ok) ok = warp_wait(bar(B_PV_TAIL + w), 0, 49);
       if (ok) {
         tc_fence_after();
+        const int tok = row_token(), h = row_head(), tt = a_row / a.group;
+        const bool valid = tt < TT && w * TT + tt < ntok;
+        const size_t qrow = (size_t)(cq + tok) * a.Hq + h;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float row_lse = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
 #pragma unroll
@@ -576,17 +584,30 @@ __global__ void __launch_bounds__(256) relattn_extend_combine_kernel(const __gri
     for (int s = lane; s < slots; s += 32) m = fmaxf(m, a.lse_part[(long)s * rows + row]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll 4
-    for (int s = wi; s < slots; s += RW) {
-      const float ls = a.lse_part[(long)s * rows + row];
-      if (ls == -INFINITY) continue;
-      const float4 v = *reinterpret_cast<const float4 *>(a.o_part + ((long)s * rows + row) * kHeadDim + lane * 4);
+    // 32 slots at a time, those of them that hold something: four loads in flight
+    for (int s0 = 32 * wi; s0 < slots; s0 += 32 * RW) {
+      const float ls = s0 + lane < slots ? a.lse_part[(long)(s0 + lane) * rows + row] : -INFINITY;
       const float w = exp2f((ls - m) * kLog2e);
-      z += w;
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+      for (unsigned full = __ballot_sync(0xffffffffu, ls != -INFINITY); full;) {
+        float4 v[4];
+        float f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = full ? __ffs(full) - 1 : 0;
+          f[k] = full ? __shfl_sync(0xffffffffu, w, i) : 0.f;
+          v[k] = full ? *reinterpret_cast<const float4 *>(a.o_part + ((long)(s0 + i) * rows + row) * kHeadDim + lane * 4)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+          full &= full - 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          z += f[k];
+          acc.x = fmaf(f[k], v[k].x, acc.x);
+          acc.y = fmaf(f[k], v[k].y, acc.y);
+          acc.z = fmaf(f[k], v[k].z, acc.z);
+          acc.w = fmaf(f[k], v[k].w, acc.w);
+        }
+      }
     }
   }
   if (RW > 1) {
@@ -650,14 +671,22 @@ cudaError_t launch_extend_main(const ExtendTcArgs &args, cudaStream_t stream) {
   static std::atomic<bool> attr_set[kMaxDevicesAttr];
   cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_extend_main_kernel), (int)SMEM_BYTES, attr_set);
   if (e != cudaSuccess) return e;
-  relattn_extend_main_kernel<<<dim3((unsigned)(x.row_tiles * x.splits), a.Hkv, a.batch), NTHREADS, SMEM_BYTES, stream>>>(
-      x, mq, mk, mv);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(x.row_tiles * x.splits), a.Hkv, a.batch);
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = x.slots > 1 && x.band != 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, relattn_extend_main_kernel, x, mq, mk, mv);
 }
 
 cudaError_t launch_extend_combine(const KernelArgs &a, int slots, bool pdl, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  const bool wide = slots >= 16;                 // (few rows then: more loads of one in flight)
+  const bool wide = slots > 32;                  // (more loads of a row in flight: 8 warps a row, 32 slots each)
   cfg.gridDim = dim3((unsigned)(wide ? (long)a.total_q * a.Hq : ((long)a.total_q * a.Hq + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;

@@ -133,9 +133,6 @@ struct TcArgs {
   // into a K-ring slot, copied to TMEM by the MMA issuer; r straight into
   // the r tile), so a CTA's next item starts without the softmax warps
   int stage_tma;
-  // EXT (launch_extend_band): query rows of an item, items, K / V copies of this
-  // many rows, pieces of a row's band and the tiles of one, the first one's slot
-  int block_rows, n_items, box, pieces, piece_tiles, slot0;
 };
 
 __device__ __forceinline__ int floor_div64(int x) { return x >= 0 ? x >> 6 : -((63 - x) >> 6); }
@@ -185,16 +182,9 @@ struct Item {
   int cq, ck, off, p0, p_last;
   int ntiles, Dt0, span, nb_tiles, s2, nsteps;
   int c_start, c_first, c_last;   // r.P chunks of the band (s2 > 0)
-  int lk;                         // EXT: keys of the sequence
 };
 
-// EXT (with DECODE and WALK): the bias band of relattn_extend -- decode's packed
-// rows for any number of tokens, over the keys from extend_band_first of a row
-// to its own.  Tiles start at multiples of 128 keys (whole pages, or parts of
-// them: a copy per part); K and V copies come from a warp each.  With a window
-// that keeps sinks inside the bias the tiles run on to them: what lies between
-// is masked.
-template <bool DECODE, bool WALK, bool EXT>
+template <bool DECODE, bool WALK>
 __global__ void __launch_bounds__(NTHREADS, 1)
 relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
                       const __grid_constant__ CUtensorMap map_k,
@@ -224,11 +214,11 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
   // like the prefill's, in longest-first order (see load_item)
   // (WALK = false: decode with one item per CTA, the item from blockIdx)
   const int dec_units = DECODE ? a.Hkv * a.row_blocks : 1;
-  const int n_items = EXT ? ta.n_items : DECODE ? (WALK ? a.num_splits * dec_units * a.batch : 1) : a.q_tiles * a.Hq * a.batch;
+  const int n_items = DECODE ? (WALK ? a.num_splits * dec_units * a.batch : 1) : a.q_tiles * a.Hq * a.batch;
   const int item0 = (DECODE && !WALK) ? 0 : (int)blockIdx.x;
   const int item_step = (DECODE && !WALK) ? 1 : (int)gridDim.x;
   int *ord = reinterpret_cast<int *>(smem + SM_ORD);
-  const bool dec_sorted = DECODE && WALK && !EXT && a.batch <= kCuCache;
+  const bool dec_sorted = DECODE && WALK && a.batch <= kCuCache;
   // work of the items before the current one, for barrier phases / stages
   int hb = 0, fb = 0, tb = 0, ob = 0;     // half steps, full steps, key tiles, r.P chunks
   // V-ring slots: the item's q rows take one ahead of its value tiles (TMA
@@ -265,15 +255,7 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
   // 1 = work to do, 0 = nothing (row tile past the sequence, empty split),
   // -1 = inconsistent sequence lengths (reported by the caller, item skipped)
   auto load_item = [&](int idx) -> int {
-    if constexpr (EXT) {
-      // (row block from the last backwards, sequence, kv head, piece)
-      const int per = a.batch * a.Hkv * ta.pieces, xi = idx / per, rem = idx - xi * per;
-      I.split = rem % ta.pieces;
-      I.kv_head = rem / ta.pieces % a.Hkv;
-      I.b = rem / (ta.pieces * a.Hkv);
-      I.row0 = (a.row_blocks - 1 - xi) * ta.block_rows;
-      I.h_fixed = 0;
-    } else if constexpr (DECODE) {
+    if constexpr (DECODE) {
       // slot idx -> position: rounds of gridDim.x slots, every other full round
       // reversed (a snake), over pairs (sequence, split) ordered full chunks
       // first, then partial chunks by size, then the rest; each pair is
@@ -326,9 +308,7 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
     I.ck = cuk[I.b];
     const int Lq = cuq[I.b + 1] - I.cq, Lk = cuk[I.b + 1] - I.ck;
     if (Lq < 0 || Lk < Lq || Lq > a.max_q || Lk > a.max_k) return -1;
-    // (kv_rows: a call of relattn_extend)
-    if ((EXT || a.kv_rows > 0) && !extend_rows_ok(a, I.cq, Lq, I.ck, Lk)) return -1;
-    I.nrows = min(EXT ? ta.block_rows : BM, (DECODE ? Lq * a.group : Lq) - I.row0);
+    I.nrows = min(BM, (DECODE ? Lq * a.group : Lq) - I.row0);
     if (I.nrows <= 0) return 0;
     I.off = Lk - Lq;
     I.p0 = I.off + row_t(0);
@@ -336,16 +316,7 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
     const int j_lo = a.window > 0 ? max(0, I.p0 - a.window + 1) : 0;
     // 128-key tiles from the diagonal backwards: tile t starts at key
     // p0 - D(t); the rows sit at positions p0 + delta, 0 <= delta <= span
-    if constexpr (EXT) {
-      const int b0 = extend_band_first(a, I.p0);
-      const int low = (min(a.sink, j_lo) > b0 ? b0 : max(b0, j_lo)) / BN;   // first and
-      const int high = I.p_last / BN - I.split * ta.piece_tiles;            // last tile
-      I.ntiles = min(ta.piece_tiles, max(0, high - low + 1));
-      I.Dt0 = I.p0 - BN * high;
-      I.span = I.p_last - I.p0;
-      I.split += ta.slot0;
-      I.lk = Lk;
-    } else if constexpr (DECODE) {
+    if constexpr (DECODE) {
       const int kbase = j_lo & ~(BN - 1);
       const int kbeg = kbase + I.split * a.split_chunk;
       const int kend = min(I.p_last + 1, kbeg + a.split_chunk);
@@ -359,9 +330,7 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
     }
     // band tiles (some distance < E) form a prefix of the tile order
     I.nb_tiles = 0;
-    if (EXT) {
-      I.nb_tiles = I.ntiles;
-    } else if (ta.has_bias && I.ntiles > 0) {
+    if (ta.has_bias && I.ntiles > 0) {
       const int lim = a.E + BN - 1;              // band iff D - 127 < E
       I.nb_tiles = tile_D(I.ntiles - 1) < lim ? I.ntiles : max(0, (lim - I.Dt0 + BN - 1) / BN);
       if (I.nb_tiles > I.ntiles) I.nb_tiles = I.ntiles;
@@ -498,86 +467,9 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + SM_TMEM_SLOT);
   // TMA copies issued by the producer thread (to drain them if the CTA gives up)
   int issued_k = 0, issued_v = 0, issued_p = 0, issued_rt = 0;
-  // EXT: the copies of the current item's tile t, one a lane (lane = part of the
-  // tile); a part that no row needs, or whose page lies outside the pool, reads zeros
-  auto part_key = [&](int t) { return I.p0 - tile_D(t) + lane * ta.box; };
-  auto part_needed = [&](int t) -> bool {
-    const int p = part_key(t);
-    return lane * ta.box < BN && p <= I.p_last && (a.window <= 0 || p + ta.box > I.p0 - a.window + 1 || p < a.sink);
-  };
-  auto part_page = [&](int t) -> int {
-    if (a.block_table == nullptr || t >= I.ntiles || !part_needed(t)) return 0;
-    return __ldg(a.block_table + (size_t)I.b * a.max_pages + part_key(t) / a.page_size);
-  };
-  auto copy_parts = [&](uint32_t dst, const CUtensorMap *map, int t, int pg, uint32_t br) {
-    const int p = part_key(t);
-    int row = -BN;
-    if (part_needed(t)) {
-      if (a.block_table == nullptr) row = I.ck + p;
-      else if ((unsigned)pg < (unsigned)a.num_pages) row = pg * a.page_size + p % a.page_size;
-      else atomicOr(a.err, kDevErrSeqlens);
-    }
-    if (lane == 0) mbar_arrive_expect_tx(br, KV_STAGE_BYTES);
-    __syncwarp();
-    if (lane * ta.box < BN) {
-      tma_load_3d(dst + lane * ta.box * 128, map, 0, I.kv_head, row, br);
-      tma_load_3d(dst + KV_BOX_BYTES + lane * ta.box * 128, map, 64, I.kv_head, row, br);
-    }
-    __syncwarp();
-  };
   if (warp < 4) {
   if constexpr (!DECODE || WALK) regs_dec<kRegsSupport>();
-  if (EXT && warp == 0) {
-    // ======================================================== P slices and K tiles
-    const uint32_t p_bytes = 128u * (uint32_t)a.rd;
-    bool run = true;
-    for (int idx = item0; idx < n_items && run; idx += item_step) {
-      const int li = load_item(idx);
-      if (li < 0 && lane == 0) atomicOr(a.err, kDevErrSeqlens);
-      if (li <= 0) continue;
-      int c_next = I.c_start, page = part_page(0);
-      for (int t = 0; t < I.ntiles && run; ++t) {
-        const int c_need = c_new(2 * t + 1);   // newest chunk of the tile's second half step
-        for (; c_next <= c_need && run; ++c_next) {
-          const int o = chunk_idx(c_next), st = o % P_STAGES;
-          if (o >= P_STAGES) run = mbar_wait_warp(bar(B_PS_EMPTY + st), ((o / P_STAGES) - 1) & 1, abort_flag, 3);
-          if (!run) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(B_PS_FULL + st), p_bytes);
-            tma_load_2d(sb + SM_PS + st * 8192, &map_p, HN * c_next, 0, bar(B_PS_FULL + st));
-          }
-          __syncwarp();
-          issued_p = o + 1;
-        }
-        const int kg = tb + t, st = kg % K_STAGES;
-        if (run && kg >= K_STAGES) run = mbar_wait_warp(bar(B_K_EMPTY + st), ((kg / K_STAGES) - 1) & 1, abort_flag, 1);
-        if (!run) break;
-        // (test hook: a skipped tile is never loaded)
-        if (kg != a.test_skip_k_tile) copy_parts(sb + SM_K + st * KV_STAGE_BYTES, &map_k, t, page, bar(B_K_FULL + st));
-        issued_k = kg + 1;
-        page = part_page(t + 1);
-      }
-      finish_item();
-    }
-    __syncwarp();
-  } else if (EXT && warp == 2) {
-    // ======================================================== V tiles
-    bool run = true;
-    for (int idx = item0; idx < n_items && run; idx += item_step) {
-      if (load_item(idx) <= 0) continue;
-      int page = part_page(0);
-      for (int t = 0; t < I.ntiles; ++t) {
-        const int vg = vslot(t), st = vg % V_STAGES;
-        if (vg >= V_STAGES) run = mbar_wait_warp(bar(B_V_EMPTY + st), ((vg / V_STAGES) - 1) & 1, abort_flag, 4);
-        if (!run) break;
-        copy_parts(sb + SM_V + st * KV_STAGE_BYTES, &map_v, t, page, bar(B_V_FULL + st));
-        issued_v = vg + 1;
-        page = part_page(t + 1);
-      }
-      finish_item();
-    }
-    __syncwarp();
-  } else if (warp == 0) {
+  if (warp == 0) {
     // ======================================================== TMA producer
     // Per tile t: the P slices its half steps need (band tiles), then K(t),
     // then V(t) -- the order the MMA issuer consumes them, so a wait here only
@@ -1114,13 +1006,11 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
           tc_fence_before();
           mbar_arrive(bar(B_R_FREE));
           // y[u] = window[i0 - u] = z[95 - i0 + u] with 95 - i0 in [18, 64]
-          // (EXT: rows of a warp span up to 32 positions, [2, 64])
-          constexpr int ZB = EXT ? 2 : 18;
           const int i0 = D + delta - 32 * wg - bal;
-          const int sh = 95 - i0 - ZB;
-          float *zz = z + ZB;   // 96 - ZB entries
+          const int sh = 95 - i0 - 18;
+          float *zz = z + 18;   // 78 entries
 #pragma unroll
-          for (int i = 0; i < 64 - ZB; ++i) zz[i] = (sh & 32) ? zz[i + 32] : zz[i];
+          for (int i = 0; i < 46; ++i) zz[i] = (sh & 32) ? zz[i + 32] : zz[i];
 #pragma unroll
           for (int i = 0; i < 47; ++i) zz[i] = (sh & 16) ? zz[i + 16] : zz[i];
 #pragma unroll
@@ -1137,16 +1027,8 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
                   qk_over_bias, zz[u], zz[u + 1]);
         }
         const bool need_mask =
-            (j0 + HN - 1 > I.p0) || (a.window > 0 && j0 < I.p_last - a.window + 1) || (j0 < 0) ||
-            (EXT && j0 < extend_band_first(a, I.p_last));
-        if (EXT && need_mask) {
-          // from the row's first band key to its own, in its window or a sink
-          const int jb = j0 + 32 * wg;
-          const int kmax = pos - jb, kband = extend_band_first(a, pos) - jb;
-          const int kmin = a.window > 0 ? pos - a.window + 1 - jb : -jb, kfar = a.sink - jb;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (i <= kmax && i >= kband && (i >= kmin || i < kfar)) ? x[i] : -INFINITY;
-        } else if (need_mask) {
+            (j0 + HN - 1 > I.p0) || (a.window > 0 && j0 < I.p_last - a.window + 1) || (j0 < 0);
+        if (need_mask) {
           // visible keys of this row: one range [kmin, kmax] of this thread's keys
           const int jb = j0 + 32 * wg;
           const int kmax = pos - jb;
@@ -1286,18 +1168,6 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
           tmem_st32(oaddr, r);
         }
       }
-      if (EXT && s == 0 && I.p0 - tile_D(0) + BN > I.lk) {
-        // values past the sequence's last key (rows of no key, of another
-        // sequence): zero, so that a NaN there does not meet a weight of zero
-        const int vg = vslot(0);
-        if (!(ok = warp_wait(bar(B_V_FULL + vg % V_STAGES), (vg / V_STAGES) & 1, 21))) break;
-        if (wg == 0 && I.p0 - tile_D(0) + a_row >= I.lk) {
-          uint4 *v = reinterpret_cast<uint4 *>(smem + SM_V + (vg % V_STAGES) * KV_STAGE_BYTES + a_row * 128);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = v[KV_BOX_BYTES / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
       tmem_wait_st();
       tc_fence_before();
       if (s < I.s2) mbar_arrive(bar(B_P_FULL + step_kind(s)));
@@ -1387,18 +1257,12 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
     for (int t = max(0, issued_k - K_STAGES); t < issued_k; ++t)
       if (t != a.test_skip_k_tile)
         mbar_wait(bar(B_K_FULL + t % K_STAGES), (t / K_STAGES) & 1, &keep_waiting, 2, 400000000ll);
-    if (!EXT)
-      for (int t = max(0, issued_v - V_STAGES); t < issued_v; ++t)
-        mbar_wait(bar(B_V_FULL + t % V_STAGES), (t / V_STAGES) & 1, &keep_waiting, 2, 400000000ll);
+    for (int t = max(0, issued_v - V_STAGES); t < issued_v; ++t)
+      mbar_wait(bar(B_V_FULL + t % V_STAGES), (t / V_STAGES) & 1, &keep_waiting, 2, 400000000ll);
     for (int o = max(0, issued_p - P_STAGES); o < issued_p; ++o)
       mbar_wait(bar(B_PS_FULL + o % P_STAGES), (o / P_STAGES) & 1, &keep_waiting, 2, 400000000ll);
     if (issued_rt > 0)
       mbar_wait(bar(B_RT_FULL), (issued_rt - 1) & 1, &keep_waiting, 2, 400000000ll);
-  }
-  if (EXT && warp == 2 && lane == 0 && *abort_flag) {
-    volatile int keep_waiting = 0;
-    for (int t = max(0, issued_v - V_STAGES); t < issued_v; ++t)
-      mbar_wait(bar(B_V_FULL + t % V_STAGES), (t / V_STAGES) & 1, &keep_waiting, 2, 400000000ll);
   }
   if (warp == 1) {
     tc_fence_after();
@@ -1449,15 +1313,16 @@ bool tc_supported(const KernelArgs &a, int total_k) {
 
 namespace {
 
-template <bool DECODE, bool WALK, bool EXT = false>
-cudaError_t launch_tc(const KernelArgs &a, int total_k, dim3 grid, cudaStream_t stream, TcArgs ta = {}) {
+template <bool DECODE, bool WALK>
+cudaError_t launch_tc(const KernelArgs &a, int total_k, dim3 grid, cudaStream_t stream) {
+  TcArgs ta;
   ta.a = a;
   ta.has_bias = a.rd > 0 && a.E > 0;
   CUtensorMap mk, mv, mp;
   {
     cuuint64_t dims[3] = {128, (cuuint64_t)a.Hkv, (cuuint64_t)total_k};
     cuuint64_t strides[2] = {256, (cuuint64_t)a.Hkv * 256};
-    cuuint32_t box[3] = {64, 1, (cuuint32_t)(EXT ? ta.box : BN)};
+    cuuint32_t box[3] = {64, 1, BN};
     if (!encode(&mk, a.k, 3, dims, strides, box)) return cudaErrorInvalidValue;
     if (!encode(&mv, a.v, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
@@ -1488,10 +1353,10 @@ cudaError_t launch_tc(const KernelArgs &a, int total_k, dim3 grid, cudaStream_t 
     if (!encode(&mq, a.q, 3, dq, sq, bq) || !encode(&mr, a.r, 3, dr, sr, br)) ta.stage_tma = 0;
   }
   static std::atomic<bool> attr_set[kMaxDevicesAttr];
-  cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_fwd_tc_kernel<DECODE, WALK, EXT>),
+  cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_fwd_tc_kernel<DECODE, WALK>),
                                     (int)SMEM_BYTES, attr_set);
   if (e != cudaSuccess) return e;
-  relattn_fwd_tc_kernel<DECODE, WALK, EXT><<<grid, NTHREADS, SMEM_BYTES, stream>>>(ta, mk, mv, mp, mq, mr);
+  relattn_fwd_tc_kernel<DECODE, WALK><<<grid, NTHREADS, SMEM_BYTES, stream>>>(ta, mk, mv, mp, mq, mr);
   return cudaGetLastError();
 }
 
@@ -1520,27 +1385,6 @@ cudaError_t launch_decode_tc(const KernelArgs &a, int total_k, cudaStream_t stre
   if (a.sms <= 0 || items <= a.sms)
     return launch_tc<true, false>(a, total_k, dim3(a.num_splits, a.Hkv * a.row_blocks, a.batch), stream);
   return launch_tc<true, true>(a, total_k, dim3((unsigned)a.sms, 1, 1), stream);
-}
-
-// Rows of a band item: 128, or where a row is a token of its own, as many as keep
-// the span of positions within three 64-distance chunks of r.P.
-int extend_band_rows(const KernelArgs &a) { return a.group == 1 ? 64 : BM; }
-
-cudaError_t launch_extend_band(const ExtendTcArgs &x, cudaStream_t stream) {
-  KernelArgs a = x.a;
-  TcArgs ta = {};
-  ta.block_rows = extend_band_rows(a);
-  ta.box = extend_box(a);
-  ta.pieces = x.band_pieces;
-  ta.piece_tiles = x.band_tiles;
-  ta.slot0 = x.splits;
-  a.num_splits = x.slots;                      // (more than one: partials)
-  a.row_blocks = (int)(((long)a.max_q * a.group + ta.block_rows - 1) / ta.block_rows);
-  const long items = (long)a.row_blocks * a.batch * a.Hkv * ta.pieces;
-  if (items > 0x7fffffffL) return cudaErrorInvalidValue;
-  ta.n_items = (int)items;
-  const long ctas = a.sms > 0 && items > a.sms ? (long)a.sms : items;
-  return launch_tc<true, true, true>(a, a.kv_rows, dim3((unsigned)ctas, 1, 1), stream, ta);
 }
 
 }  // namespace relattn

@@ -73,23 +73,21 @@ inline int extend_box(const KernelArgs &a) {
   while (box < 128 && a.page_size % (2 * box) == 0) box *= 2;
   return box;
 }
-// More rows, on tcgen05 (extend_tc.cu): the keys outside the bias band, those of
-// which a row's band kernel has none: all without a bias; with one, what the
-// packed band kernel (fwd_tc.cu) or relattn_prefill's leaves.
-enum ExtendBand { kBandNone, kBandPacked, kBandPrefill };
+// More rows, on tcgen05: the bias band (extend_band.cu) and the keys before it
+// (all of them without a bias; extend_tc.cu).
 struct ExtendTcArgs {
   KernelArgs a;
-  int band;            // ExtendBand
+  int band;            // 1: a bias, whose band has a kernel of its own
   int tokens;          // of a row tile: 128 / group
   int row_tiles;       // pairs of row tiles per (sequence, kv head), of max_q tokens
   int splits, chunk;   // ranges of `chunk` key tiles
   int slots;           // partials of a row: the ranges', then the band pieces'; 1: none
-  int band_pieces, band_tiles;   // packed band: pieces of a row's keys, tiles of one
+  int band_pieces, band_steps;   // pieces of a row's band, steps of 64 keys of one
   int box, q_bytes;    // (set by the launcher)
 };
 cudaError_t launch_extend_main(const ExtendTcArgs &x, cudaStream_t stream);
 cudaError_t launch_extend_band(const ExtendTcArgs &x, cudaStream_t stream);
-int extend_band_rows(const KernelArgs &a);
+int extend_band_tokens(const KernelArgs &a);   // of a work item
 // out / lse from `slots` partials of every row of a sequence (extend_tc.cu);
 // other rows keep theirs
 cudaError_t launch_extend_combine(const KernelArgs &a, int slots, bool pdl, cudaStream_t stream);
