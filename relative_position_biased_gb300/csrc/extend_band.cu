@@ -68,8 +68,8 @@ struct Lay {
 };
 constexpr int B_K_FULL = 0, B_K_EMPTY = B_K_FULL + K_STAGES, B_V_FULL = B_K_EMPTY + K_STAGES, B_V_EMPTY = B_V_FULL + 3,
               B_PS_FULL = B_V_EMPTY + 3, B_PS_EMPTY = B_PS_FULL + P_STAGES, B_RT_FULL = B_PS_EMPTY + P_STAGES,
-              B_RT_EMPTY = B_RT_FULL + 1, B_S_FULL = B_RT_EMPTY + 1, B_P_FULL = B_S_FULL + 2, B_PV = B_P_FULL + 2,
-              B_R_FULL = B_PV + 2, B_R_FREE = B_R_FULL + 2, B_XCH = B_R_FREE + 2, B_RW = B_XCH + 4, B_DRAIN = B_RW + 4,
+              B_RT_EMPTY = B_RT_FULL + 1, B_S_FULL = B_RT_EMPTY + 1, B_P_FULL = B_S_FULL + 2, B_R_FULL = B_P_FULL + 2,
+              B_R_FREE = B_R_FULL + 2, B_XCH = B_R_FREE + 2, B_RW = B_XCH + 4, B_TAIL = B_RW + 4, B_DRAIN = B_TAIL + 1,
               B_COUNT = B_DRAIN + 1;
 template <bool WIDE>
 constexpr uint32_t smem_bytes() { return Lay<WIDE>::SM_BAR + B_COUNT * 8 + 16 + 1024; }
@@ -182,7 +182,6 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       mbar_init(bar(B_PS_EMPTY + i), 1);
       mbar_init(bar(B_S_FULL + i), 1);
       mbar_init(bar(B_P_FULL + i), 256);
-      mbar_init(bar(B_PV + i), 1);
       mbar_init(bar(B_R_FULL + i), 1);
       mbar_init(bar(B_R_FREE + i), 256);
     }
@@ -192,6 +191,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       mbar_init(bar(B_XCH + i), 64);
       mbar_init(bar(B_RW + i), 64);
     }
+    mbar_init(bar(B_TAIL), 1);
     mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -278,7 +278,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
           if (k != a.test_skip_k_tile) copy_parts(sb + L::SM_K + st * STAGE, &map_k, I.first - s, page, bar(B_K_FULL + st));
           issued_k = k + 1;
           page = part_page(s + 1 < I.steps ? I.first - s - 1 : -1);
-          for (; c <= I.c_first + s; ++c) {         // the chunks up to the newest that step s needs
+          for (; c <= min(I.c_first + s + 1, I.c_first + I.steps - 1); ++c) {   // (a step ahead, as R)
             const int o = ob + c - I.c_start, st = o % P_STAGES;
             if (o >= P_STAGES && !(run = wait_parked(bar(B_PS_EMPTY + st), ((o / P_STAGES) - 1) & 1, 62))) break;
             if (lane == 0) {
@@ -348,7 +348,6 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
         if (r_ksteps > 2) mma_ss_e<1>(d, rd0 + 4, pd + 256, id_r);
         if (r_ksteps > 3) mma_ss_e<1>(d, rd0 + 6, pd + 384, id_r);
         mma_commit_e(bar(B_R_FULL + (o & 1)));
-        mma_commit_e(bar(B_PS_EMPTY + st));
         if (c == I.c_first + I.steps - 1) mma_commit_e(bar(B_RT_EMPTY));   // the item's last chunk
         return true;
       };
@@ -367,7 +366,6 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
         mma_ts_e<1>(d, q + 48, kd + 516, id_s);
         mma_ts_e<1>(d, q + 56, kd + 518, id_s);
         mma_commit_e(bar(B_S_FULL + (k & 1)));
-        mma_commit_e(bar(B_K_EMPTY + st));
         return true;
       };
       auto issue_pv = [&](int s) -> bool {
@@ -382,8 +380,8 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
         mma_ts_e<1>(o, p + 8, vd + 128, id_o);
         mma_ts_e<1>(o, p + 16, vd + 256, id_o);
         mma_ts_e<1>(o, p + 24, vd + 384, id_o);
-        mma_commit_e(bar(B_PV + (k & 1)));
         mma_commit_e(bar(B_V_EMPTY + st));
+        if (s == I.steps - 1) mma_commit_e(bar(B_TAIL));   // (that slot may take the next q rows before it is looked at)
         return true;
       };
       for (int idx = idx0; idx < n_items && ok; idx += idx_step) {
@@ -398,14 +396,14 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
           for (int k = 0; k < 4; ++k) tmem_cp_128x256b_e(tmem + TM_Q + 32u * h + 8u * k, qd + 2 * k);
           mma_commit_e(bar(B_V_EMPTY + st));
         }
-        // S(0) first: it needs no r, and R's third chunk waits for the softmax
+        // S(0) first: it needs no r, and R's third chunk waits for the softmax.  R runs
+        // a step ahead of S: behind it, the softmax waited half of a step for it.
+        const int c_last = I.c_first + I.steps - 1;
         if (ok) ok = issue_s(0);
-        for (int c = I.c_start; c <= I.c_first && ok; ++c) ok = issue_r(c);
+        for (int c = I.c_start; c <= min(I.c_first + 1, c_last) && ok; ++c) ok = issue_r(c);
         for (int s = 0; s < I.steps && ok; ++s) {
-          if (s + 1 < I.steps) {
-            if (!(ok = issue_s(s + 1))) break;
-            if (!(ok = issue_r(I.c_first + s + 1))) break;
-          }
+          if (s + 1 < I.steps && !(ok = issue_s(s + 1))) break;
+          if (I.c_first + s + 2 <= c_last && !(ok = issue_r(I.c_first + s + 2))) break;
           ok = issue_pv(s);
         }
         finish_item();
@@ -422,6 +420,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     const int wg = (warp - 4) >> 2;
     const int wq = warp & 3;                     // lane quarter (TMEM lanes 32 wq ..)
     const int a_row = 32 * wq + lane;            // row == TMEM lane
+    const bool leader = warp == 4 && lane == 0;  // (an arrival costs the issuer less than a commit)
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
     const int row_tok = a_row / a.group;         // (rows past the item's tokens repeat its last one)
     float *ring = reinterpret_cast<float *>(smem + L::SM_R) + a_row;
@@ -429,6 +428,11 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     auto warp_wait = [&](uint32_t br, uint32_t parity, int site) -> bool {
       const bool r = mbar_wait(br, parity, abort_flag, site);
       return __all_sync(0xffffffffu, r);
+    };
+    // the product of the item's step s is done: its V slot is free
+    auto pv_wait = [&](int s, int site) -> bool {
+      const int v = vb + 2 + s;
+      return warp_wait(bar(B_V_EMPTY + v % V_STAGES), (v / V_STAGES) & 1, site);
     };
     int n_xch = 0, n_rw = 0;
     // this thread's value with the other warpgroup's for the same row
@@ -444,6 +448,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     auto copy_chunk = [&](int c) -> bool {
       const int o = ob + c - I.c_start;
       if (!warp_wait(bar(B_R_FULL + (o & 1)), (o >> 1) & 1, 75)) return false;
+      if (leader) mbar_arrive(bar(B_PS_EMPTY + o % P_STAGES));     // its P slice is read
       tc_fence_after();
       uint32_t w[32];
       __syncwarp();
@@ -483,6 +488,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
         const int k = gs + s, j0 = HN * (I.first - s);
         const uint32_t sbuf = tmem + lane_base + TM_S + 64u * (uint32_t)(k & 1);
         if (!(ok = warp_wait(bar(B_S_FULL + (k & 1)), (k >> 1) & 1, 76))) break;
+        if (leader) mbar_arrive(bar(B_K_EMPTY + k % K_STAGES));      // its keys are read
         tc_fence_after();
         // the row's R at distances d - u of the thread's keys j0 + 32 wg + u
         float x[32];
@@ -551,7 +557,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
         // O moves to a new maximum only when a row of the warp needs it (the whole
         // warp then, its half of the columns), once the last step's product is done
         if (__any_sync(0xffffffffu, rescale_o)) {
-          if (!(ok = warp_wait(bar(B_PV + ((k - 1) & 1)), ((k - 1) >> 1) & 1, 78))) break;
+          if (!(ok = pv_wait(s - 1, 78))) break;
           tc_fence_after();
           const float cf = rescale_o ? corr : 1.f;
 #pragma unroll
@@ -585,8 +591,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       }
       if (!ok) break;
       // ---- epilogue (the issuer is on the next item already)
-      const int k_last = gs + I.steps - 1;
-      if (!(ok = warp_wait(bar(B_PV + (k_last & 1)), (k_last >> 1) & 1, 80))) break;
+      if (!(ok = warp_wait(bar(B_TAIL), n_it & 1, 80))) break;
       const float lt = l + exchange(l, ok);
       if (!ok) break;
       tc_fence_after();
