@@ -586,13 +586,14 @@ __global__ void __launch_bounds__(NTB, 1) relattn_bwd_dq_kernel(const __grid_con
     }
     if (a.dr != nullptr) {
       __nv_bfloat16 *drd = a.dr + row * a.rd;
+      const float *sdr = far && a.sink_dr && sink_in_bias(a, pos[r]) ? a.sink_dr + row * a.rd : nullptr;
 #pragma unroll
       for (int n = 0; n < 8; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = n * 8 + 2 * qq + e;
           if (c < a.rd)
-            drd[c] = __float2bfloat16_rn(dr[n][2 * r + e] * srow[r] + (far && a.sink_dr ? a.sink_dr[row * a.rd + c] : 0.f));
+            drd[c] = __float2bfloat16_rn(dr[n][2 * r + e] * srow[r] + (sdr ? sdr[c] : 0.f));
         }
     }
   }

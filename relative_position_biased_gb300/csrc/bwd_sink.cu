@@ -126,6 +126,27 @@ __global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_co
         mma_bf16_16816(dp[0], da[0], da[1], da[2], da[3], vf[0], vf[1]);
         mma_bf16_16816(dp[1], da[0], da[1], da[2], da[3], vf[2], vf[3]);
       }
+      // ---- the bias of the pairs within E (a sink outside the window lies there only
+      // where E reaches past it), all loads in flight together
+      float rb[2][4] = {};
+      if (bias) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int xr = x + gq + 8 * r, t = token(xr);
+          const size_t row = (size_t)(s.cq + t) * a.Hq + head(xr);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int d = off + t - (j0 + (i >> 1) * 8 + 2 * qq + (i & 1));
+            const bool in = d >= a.window && d < a.E;
+            if (a.rall_ok) {
+              rb[r][i] = in ? __ldg(a.Rall + row * a.e_pad + d) : 0.f;
+            } else if (in) {
+              for (int c = 0; c < a.rd; ++c)
+                rb[r][i] = fmaf(__bfloat162float(a.r[row * a.rd + c]), __bfloat162float(a.P[(size_t)c * a.E + d]), rb[r][i]);
+            }
+          }
+        }
+      }
       // ---- p and s alpha dl; a row's keys outside its window, of the sinks
       uint32_t pw[2][2], dw[2][2];         // [row half][key half], bf16 pairs of keys
       float rest[2][4];                    // s dl (for dr)
@@ -134,7 +155,7 @@ __global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_co
         const int xr = x + gq + 8 * r, t = token(xr), h = head(xr), pos = off + t;
         const bool live = xr < x1;
         const float srow = log_scale(pos, a.inv_ln_base);
-        const size_t li = (size_t)h * a.total_q + s.cq + t, row = (size_t)(s.cq + t) * a.Hq + h;
+        const size_t li = (size_t)h * a.total_q + s.cq + t;
         const float lse2 = a.lse[li] * kLog2e, Di = a.Dsum[li];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -143,17 +164,7 @@ __global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_co
           for (int e = 0; e < 2; ++e) {
             const int j = j0 + n * 8 + 2 * qq + e, d = pos - j;
             const bool vis = live && j < a.sink && d >= a.window;
-            float z = sc[n][2 * r + e] * a.alpha;
-            if (bias && vis && d < a.E) {
-              if (a.rall_ok) {
-                z += a.Rall[row * a.e_pad + d];
-              } else {
-                float dot = 0.f;
-                for (int c = 0; c < a.rd; ++c)
-                  dot = fmaf(__bfloat162float(a.r[row * a.rd + c]), __bfloat162float(a.P[(size_t)c * a.E + d]), dot);
-                z += dot;
-              }
-            }
+            const float z = fmaf(sc[n][2 * r + e], a.alpha, rb[r][2 * n + e]);
             const float p = vis ? fast_exp2(fmaf(z, srow * kLog2e, -lse2)) : 0.f;
             pv[e] = p;
             const float w = vis ? p * (dp[n][2 * r + e] - Di) * srow : 0.f;
@@ -207,36 +218,26 @@ __global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_co
       // per channel, s dl from the lane that holds it
       if (bias) {
 #pragma unroll 1
-        for (int r = 0; r < 2; ++r)
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            const int xr = x + i + 8 * r;
-            const int t = token(xr), pos = off + t;
-            const bool any = xr < x1 && pos - min(j0 + SK - 1, a.sink - 1) < a.E;   // (warp-uniform)
-            float acc[2] = {0.f, 0.f};
-            if (any)
+        for (int i = 0; i < 16; ++i) {
+          const int xr = x + i, t = token(xr), pos = off + t;
+          if (xr >= x1 || !sink_in_bias(a, pos)) continue;      // (warp-uniform)
+          const int c0 = min(lane, a.rd - 1), c1 = min(lane + 32, a.rd - 1);
+          float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float v = __shfl_sync(0xffffffffu, r ? rest[n][2 + (k & 1)] : rest[n][k & 1], 4 * i + (k >> 1));
-                  const int d = pos - (j0 + n * 8 + k);
-                  if (v != 0.f && d >= 0 && d < a.E)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                      const int c = lane + 32 * u;
-                      if (c < a.rd) acc[u] = fmaf(v, __bfloat162float(a.P[(size_t)c * a.E + d]), acc[u]);
-                    }
-                }
-            if (xr < x1) {
-              float *dst = a.sink_dr + ((size_t)(s.cq + t) * a.Hq + head(xr)) * a.rd;
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int c = lane + 32 * u;
-                if (c < a.rd) dst[c] = kb > 0 ? dst[c] + acc[u] : acc[u];
-              }
-            }
+          for (int k = 0; k < 16; ++k) {
+            const float v0 = __shfl_sync(0xffffffffu, rest[k >> 3][k & 1], 4 * (i & 7) + ((k & 7) >> 1));
+            const float v1 = __shfl_sync(0xffffffffu, rest[k >> 3][2 + (k & 1)], 4 * (i & 7) + ((k & 7) >> 1));
+            const int d = pos - (j0 + k);
+            const bool in = d >= a.window && d < a.E;
+            const float v = in ? (i < 8 ? v0 : v1) : 0.f;
+            const __nv_bfloat16 *p = a.P + (in ? d : 0);
+            acc0 = fmaf(v, __bfloat162float(p[(size_t)c0 * a.E]), acc0);
+            acc1 = fmaf(v, __bfloat162float(p[(size_t)c1 * a.E]), acc1);
           }
+          float *dst = a.sink_dr + ((size_t)(s.cq + t) * a.Hq + head(xr)) * a.rd;
+          if (lane < a.rd) dst[lane] = kb > 0 ? dst[lane] + acc0 : acc0;
+          if (lane + 32 < a.rd) dst[lane + 32] = kb > 0 ? dst[lane + 32] + acc1 : acc1;
+        }
       }
       __syncwarp();                        // the stage is read
     }

@@ -166,10 +166,15 @@ struct BwdArgs {
   // that add it.  Only rows at positions >= window have sink_dq / sink_dr.
   int sink;
   float *sink_dq;              // workspace [Tq, Hq, 128]
-  float *sink_dr;              // workspace [Tq, Hq, r_dim], where E reaches past the window; else null
+  float *sink_dr;              // workspace [Tq, Hq, r_dim], where E reaches past the window (sink_in_bias); else null
   float *sink_dkv;             // workspace [batch, Hkv, sink, 2 (dk, dv), 128]
   float *sink_part;            // workspace: partials of sink_dkv
 };
+// The bias of the row at position pos (at least the window) reaches a sink that
+// the window has left behind: the row has a sink_dr.
+__device__ __forceinline__ bool sink_in_bias(const BwdArgs &a, int pos) {
+  return pos - min(a.sink - 1, pos - a.window) < a.E;
+}
 // float4 group `lane` of key j's (dk, dv)[which] sink sum
 __device__ __forceinline__ float4 sink_dkv4(const BwdArgs &a, int b, int g, int j, int which, int lane) {
   return reinterpret_cast<const float4 *>(a.sink_dkv)[((((size_t)b * a.Hkv + g) * a.sink + j) * 2 + which) * (kHeadDim / 4) + lane];
