@@ -423,14 +423,14 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
     chunk = (most + p->num_splits - 1) / p->num_splits;
   } else {
     // the cut with the shortest time, in steps of a key tile (1.8 us): waves of
-    // CTAs, each with a start of some four steps; partials cost a launch and their
+    // CTAs, each with a start of some six steps; partials cost a launch and their
     // traffic
     const double rows_us = (double)a.total_q * a.Hq * kHeadDim * 8 / 6.5e6;    // of a partial, out and in
     double best = 1e30;
     for (long k = 1; k <= std::min(kMaxRanges, most); ++k) {
       const long c = (most + k - 1) / k, per = (mean + c - 1) / c, ctas = pairs * per;
-      double t = (double)((ctas + a.sms - 1) / a.sms) * (std::min(c, mean) + 4);
-      if (ctas <= a.sms) t = c + 4;
+      double t = (double)((ctas + a.sms - 1) / a.sms) * (std::min(c, mean) + 6);
+      if (ctas <= a.sms) t = c + 6;
       if (k > 1) t += 4 + per * rows_us / 1.8;
       if (t < best) best = t, chunk = c;
     }

@@ -100,9 +100,11 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM_ABORT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // With partials this kernel runs beside the band's, as its programmatic
-  // dependent, and the merge may be launched behind it.  Its first CTA ends after
-  // the band's grid, so that whoever waits for this grid has waited for both.
+  // This kernel is launched as the band's programmatic dependent: its CTAs take SMs
+  // as the band's leave them.  With partials they need nothing of the band (else
+  // the softmax warps wait for it before they read its results), and the merge
+  // may be launched behind them.  The first CTA ends after the band's grid, so
+  // that whoever waits for this grid has waited for both.
   asm volatile("griddepcontrol.launch_dependents;");
   struct EndAfterBand {
     __device__ ~EndAfterBand() {
@@ -339,6 +341,7 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
     float m_ref = -INFINITY, l = 0.f;
     if (init) {
       // the band's state: m = lse log2(e), l = 1, O = out (normalised)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       const int tok = row_token(), h = row_head();
       const float lse0 = a.lse[(size_t)h * a.total_q + cq + tok];
       if (lse0 != -INFINITY) {
@@ -680,7 +683,7 @@ cudaError_t launch_extend_main(const ExtendTcArgs &args, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = x.slots > 1 && x.band != 0 ? 1 : 0;
+  cfg.numAttrs = x.band != 0 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, relattn_extend_main_kernel, x, mq, mk, mv);
 }
 
