@@ -81,7 +81,8 @@ def check(c, sink=0, **kw):
 
 # ------------------------------------------------------------------ lengths, layouts, masks
 
-LAYOUTS = [(16, 2, 64, 1024), (4, 1, 32, 64), (12, 4, 16, 200), (4, 4, 16, 64), (8, 1, 0, 0), (6, 2, 24, 77), (5, 1, 7, 33)]
+LAYOUTS = [(16, 2, 64, 1024), (4, 1, 32, 64), (12, 4, 16, 200), (4, 4, 16, 64), (8, 1, 0, 0), (6, 2, 24, 77), (5, 1, 7, 33),
+           (8, 2, 8, 128)]
 
 
 @pytest.mark.parametrize("Hq,Hkv,rd,E", LAYOUTS)
@@ -125,6 +126,78 @@ def test_many_sequences():
     check(U.Case((1,) * 150, k_lens, 8, 2, r_dim=16, E=64, page=16, seed=3))
     q_lens = tuple(min(n, int(x)) for n, x in zip(k_lens, rng.integers(0, 40, 150)))
     check(U.Case(q_lens, k_lens, 8, 2, r_dim=16, E=64, window=50, page=16, seed=3), 3)
+
+
+@pytest.mark.parametrize("Hq,Hkv,rd,E", [(20, 1, 16, 64), (32, 1, 64, 128), (128, 1, 8, 64), (130, 1, 8, 64), (24, 8, 8, 136),
+                                         (3, 1, 64, 64), (2, 1, 40, 600), (6, 6, 16, 2048)])
+@pytest.mark.parametrize("q_lens,k_lens,window,sink", [((33, 1), (200, 150), 0, 0), ((5, 140), (700, 300), 90, 6)])
+def test_groups_and_extents(Hq, Hkv, rd, E, q_lens, k_lens, window, sink):
+    check(U.Case(q_lens, k_lens, Hq, Hkv, r_dim=rd, E=E, window=window, page=16, seed=Hq), sink)
+
+
+def test_sequences_without_tokens_or_keys():
+    for q_lens, k_lens in (((0, 1, 0), (0, 70, 300)), ((0, 40, 0, 20), (0, 70, 300, 20)), ((0,), (0,))):
+        if sum(q_lens):
+            check(U.Case(q_lens, k_lens, 8, 2, r_dim=16, E=64, page=32))
+    # no rows at all: nothing is launched
+    c = U.Case((0,), (60,), 8, 2, r_dim=16, E=64)
+    out, lse = call(c, U.make(c), 0, max_seqlen_q=1)
+    ok()
+    assert out.shape == (0, 8, 128) and lse.shape == (8, 0)
+
+
+@pytest.mark.parametrize("q_len", [1, 30])
+def test_a_pool_of_more_than_32_bits_of_elements(q_len):
+    """The pages used lie past 2^31 elements (and 2^32 bytes) of the pool."""
+    page, pages = 64, 140000
+    c = U.Case((q_len,), (500,), 8, 2, r_dim=16, E=64, window=200, page=page, seed=3)
+    d = U.make(c)
+    k, v = (torch.empty(pages * page, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.numel() > 1 << 31
+    n = d["table"].shape[1]
+    far = torch.arange(pages - n, pages, dtype=torch.int32).flip(0)
+    for i in range(n):
+        src, dst = int(d["table"][0, i]) * page, int(far[i]) * page
+        k[dst:dst + page] = d["k"][src:src + page].cuda()
+        v[dst:dst + page] = d["v"][src:src + page].cuda()
+    kw = dict(U.call_kw(c, d), sink=4, block_table=far.view(1, -1).cuda())
+    out, lse = rpb.extend(d["q"].cuda(), k, v, d["r"].cuda(), d["P"].cuda(), d["cu_q"].cuda(), d["cu_k"].cuda(), **kw)
+    ok()
+    ref, z, e_out, e_lse = bounds(c, d, 4)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= e_out).all()
+    assert (np.abs(lse.double().cpu().numpy() - z) <= e_lse).all()
+    # and the prologue writes there
+    x, _ = prologue_inputs(c)
+    cu = [U.W.cu_seqlens(m).cuda() for m in (c.q_lens, c.k_lens)]
+    flat = [torch.zeros(500, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    rpb.prologue(*x.values(), *cu, *flat)
+    rpb.prologue(*x.values(), *cu, k, v, block_table=far.view(1, -1).cuda(), page_size=page)
+    ok()
+    p = torch.arange(500 - q_len, 500)
+    at = (far.long()[p // page] * page + p % page).cuda()
+    assert torch.equal(flat[0][500 - q_len:], k[at]) and torch.equal(flat[1][500 - q_len:], v[at])
+
+
+def test_python_refuses_other_layouts():
+    c = U.Case((3,), (200,), 8, 2, r_dim=16, E=64, page=32)
+    d = U.make(c)
+    t = {n: U.cuda(d[n]) for n in ("q", "k", "v", "r", "P", "cu_q", "cu_k")}
+    kw = dict(U.call_kw(c, d))
+    run = lambda **over: rpb.extend(*dict(t, **over).values(), **kw)  # noqa: E731
+    wide = torch.zeros(d["rows"], 2, 256, dtype=torch.bfloat16, device="cuda")
+    for over in (dict(k=wide[..., :128]), dict(v=t["v"][:-32]), dict(q=t["q"].float()), dict(cu_k=t["cu_k"].long()),
+                 dict(P=t["P"][:8]), dict(v=t["v"].cpu()), dict(k=wide[..., :128], v=wide[..., 128:])):
+        with pytest.raises(ValueError):
+            run(**over)
+    with pytest.raises(ValueError, match="multiple of page_size"):
+        rpb.extend(*t.values(), **dict(kw, page_size=80))
+    with pytest.raises(ValueError, match="total_k rows"):
+        rpb.extend(*t.values(), **dict(kw, block_table=None, total_k=100))
+    with pytest.raises(rpb.RelattnError):                        # a workspace too small for the call
+        rpb.extend(t["q"].repeat(20, 1, 1), t["k"], t["v"], t["r"].repeat(20, 1, 1), t["P"],
+                   torch.tensor([0, 60], dtype=torch.int32, device="cuda"), t["cu_k"],
+                   **dict(kw, max_seqlen_q=60, num_splits=2, workspace=torch.empty(16, device="cuda")))
+    ok()
 
 
 # ------------------------------------------------------------------ pages and rows that must not matter
@@ -272,6 +345,38 @@ GRAD_LAYOUTS = [(16, 2, 64, 1024), (4, 1, 32, 64), (12, 4, 16, 200), (4, 4, 16, 
 @pytest.mark.parametrize("q_lens,k_lens", [((1,), (1,)), ((40, 21), (40, 21)), ((300, 1, 150), (300, 90, 200)), ((130,), (430,))])
 def test_gradients(Hq, Hkv, rd, E, window, sink, q_lens, k_lens):
     check_grads(U.Case(q_lens, k_lens, Hq, Hkv, r_dim=rd, E=E, window=window, seed=sink), sink)
+
+
+def test_gradients_of_inconsistent_lengths_leave_the_sequence_out():
+    c = U.Case((60, 90, 50), (60, 90, 50), 8, 2, r_dim=16, E=64, window=20)
+    d, out, lse, dout, args, kw = grads(c, 3)
+    good = rpb.backward(*args, sink=3, **kw)
+    ok()
+    got = [torch.full_like(t, 7.0) for t in good]
+    rpb.backward(*args, sink=3, **dict(kw, max_seqlen_q=60, max_seqlen_k=60), **dict(zip(("dq", "dk", "dv", "dr"), got)))
+    torch.cuda.synchronize()
+    assert rpb.relattn_get_device_error() == 6
+    for a, b in zip(good, got):
+        assert torch.equal(a[:60], b[:60]) and torch.equal(a[150:], b[150:]) and (b[60:150] == 7).all()
+
+
+def test_gradients_captured_and_replayed():
+    c = U.Case((200, 120), (200, 120), 8, 2, r_dim=16, E=64, window=40)
+    d, out, lse, dout, args, kw = grads(c, 3)
+    want = rpb.backward(*args, sink=3, **kw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        rpb.backward(*args, sink=3, **kw)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = rpb.backward(*args, sink=3, **kw)
+    for t in got:
+        t.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
 def test_gradients_log_scale_and_longer():
