@@ -454,6 +454,8 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
     const size_t rows = (size_t)a.total_q * a.Hq;
     plan->lse_offset = (size_t)x.slots * rows * kHeadDim * sizeof(float);
     plan->ws_bytes = plan->lse_offset + (size_t)x.slots * rows * sizeof(float);
+  } else if (bias) {
+    plan->ws_bytes = (size_t)a.total_q * a.Hq * 2 * sizeof(float);     // (the carry)
   }
 }
 
@@ -478,6 +480,8 @@ relattn_status run_extend_tc(const relattn_params *p, ExtendPlan &plan, cudaStre
   if (x.slots > 1) {
     x.a.o_part = static_cast<float *>(p->workspace);
     x.a.lse_part = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + plan.lse_offset);
+  } else {
+    x.carry = static_cast<float *>(p->workspace);
   }
   cudaError_t e = x.band == 0 ? cudaSuccess : launch_extend_band(x, s);
   if (e == cudaSuccess) e = launch_extend_main(x, s);

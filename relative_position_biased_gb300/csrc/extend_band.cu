@@ -31,6 +31,7 @@
 // Every wait is bounded; a timeout sets the device error word, the CTA drains
 // its own copies / MMAs with bounded waits, frees tensor memory and exits.
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -435,14 +436,14 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       return warp_wait(bar(B_V_EMPTY + v % V_STAGES), (v / V_STAGES) & 1, site);
     };
     int n_xch = 0, n_rw = 0;
-    // this thread's value with the other warpgroup's for the same row
-    auto exchange = [&](float v, bool &okx) -> float {
-      float *xb = xbuf + (n_xch & 1) * 256;
-      xb[wg * 128 + a_row] = v;
+    // this thread's value to the other warpgroup's thread of the same row, and its
+    auto hand_over = [&](float v) {
+      xbuf[(n_xch & 1) * 256 + wg * 128 + a_row] = v;
       mbar_arrive(bar(B_XCH + wq));
+    };
+    auto take_over = [&](bool &okx) -> float {
       okx = warp_wait(bar(B_XCH + wq), n_xch & 1, 74);
-      ++n_xch;
-      return xb[(1 - wg) * 128 + a_row];
+      return xbuf[(n_xch++ & 1) * 256 + (1 - wg) * 128 + a_row];
     };
     // this warpgroup's 32 distances of chunk c into the ring
     auto copy_chunk = [&](int c) -> bool {
@@ -523,7 +524,8 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
         }
         // x holds alpha S + bias; the logit in log2 units is x * cbias
         const float mloc = row_max(x) * cbias;
-        const float mo = exchange(mloc, ok);
+        hand_over(mloc);
+        const float mo = take_over(ok);
         if (!ok) break;
         const float mx = fmaxf(mloc, mo);
         float corr = 1.f;
@@ -592,34 +594,55 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       if (!ok) break;
       // ---- epilogue (the issuer is on the next item already)
       if (!(ok = warp_wait(bar(B_TAIL), n_it & 1, 80))) break;
-      const float lt = l + exchange(l, ok);
+      hand_over(l);
+      const float lt = l + take_over(ok);
       if (!ok) break;
       tc_fence_after();
       const float inv = lt > 0.f ? 1.f / lt : 0.f;
       const float row_lse = lt > 0.f ? (m_ref + __log2f(lt)) * kLn2 : -INFINITY;
+      float o[64];
+      __syncwarp();
+      tmem_ld32f<0>(tmem + lane_base + TM_O + 64u * wg, o);
+      tmem_ld32f<32>(tmem + lane_base + TM_O + 64u * wg + 32u, o);
+      tmem_wait_ld_f<0>(o);
+      reg_dep_f<32>(o);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t r[32];
-        __syncwarp();
-        tmem_ld32(tmem + lane_base + TM_O + 64u * wg + 32u * c, r);
-        tmem_wait_ld(r);
-        if (valid && partial) {
-          float4 *dst = reinterpret_cast<float4 *>(a.o_part + part_row * kHeadDim + 64 * wg + 32 * c);
+      for (int i = 0; i < 64; ++i) o[i] *= inv;
+      if (partial) {
+        if (valid) {
+          float4 *dst = reinterpret_cast<float4 *>(a.o_part + part_row * kHeadDim + 64 * wg);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      } else {
+        // the row is done, or goes on over the keys before the band: then as f16,
+        // each half of it scaled by the power of two that brings its largest element
+        // to 2^14 .. 2^15
+        const int Lq = I.lk - (I.p0 - I.tok0), pair = 2 * ba.x.tokens;
+        const bool more = extend_tiles(ba.x, tok / pair * pair, Lq, I.lk).n_all > 0;
+        uint4 *dst = reinterpret_cast<uint4 *>(a.out + qrow * kHeadDim + 64 * wg);
+        if (more) {
+          float top[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top[i] = fmaxf(fabsf(o[i]), fabsf(o[32 + i]));
+          const int e = min(max((int)(__float_as_uint(row_max(top)) >> 23) - 127, -100), 127);
+          const float down = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __half2 hv = __floats2half2_rn(o[8 * i + 2 * k] * down, o[8 * i + 2 * k + 1] * down);
+              w[k] = *reinterpret_cast<const uint32_t *>(&hv);
+            }
+            if (valid) dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (valid) ba.x.carry[2 * qrow + wg] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+        } else if (valid) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
-                                 __uint_as_float(r[4 * i + 2]) * inv, __uint_as_float(r[4 * i + 3]) * inv);
-        } else if (valid) {
-          __nv_bfloat16 *dst = a.out + qrow * kHeadDim + 64 * wg + 32 * c;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(r[8 * i + 0]) * inv, __uint_as_float(r[8 * i + 1]) * inv);
-            v.y = pack_bf16x2(__uint_as_float(r[8 * i + 2]) * inv, __uint_as_float(r[8 * i + 3]) * inv);
-            v.z = pack_bf16x2(__uint_as_float(r[8 * i + 4]) * inv, __uint_as_float(r[8 * i + 5]) * inv);
-            v.w = pack_bf16x2(__uint_as_float(r[8 * i + 6]) * inv, __uint_as_float(r[8 * i + 7]) * inv);
-            *reinterpret_cast<uint4 *>(dst + 8 * i) = v;
-          }
+            dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
         }
       }
       tc_fence_before();                         // (before the next item's first P is handed over)

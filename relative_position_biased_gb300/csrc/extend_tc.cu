@@ -31,6 +31,7 @@
 // Every wait is bounded; a timeout sets the device error word, the CTA drains
 // its own copies / MMAs with bounded waits, frees tensor memory and exits.
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -82,12 +83,6 @@ __device__ __forceinline__ float row_max(const float (&x)[N]) {
   }
 }
 
-// First key that the band kernel has for the row at position pos; keys at and
-// after it are not this kernel's.
-__device__ __forceinline__ int band_first(const ExtendTcArgs &x, int pos) {
-  return x.band == 0 ? 0x7fffffff : extend_band_first(x.a, pos);
-}
-
 __global__ void __launch_bounds__(NTHREADS, 1)
 relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
@@ -124,16 +119,9 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
   const int TT = x.tokens;                            // tokens of a row tile
   const int tok0 = 2 * TT * tile;
   if (tok0 >= Lq) return;
-  const int ntok = min(2 * TT, Lq - tok0), nw = ntok > TT ? 2 : 1;
-  const int off = Lk - Lq, p0 = off + tok0, p_last = p0 + ntok - 1;
-  // keys: [w_lo, w_hi) tiles of the window, and before them the tiles of the sinks
-  // that the last row's window has left behind
-  const int j_lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  const int b_first = band_first(x, p0), b_last = band_first(x, p_last);
-  const int far = a.window > 0 ? min(min(a.sink, max(0, p_last - a.window + 1)), b_last) : 0;
-  const int w_lo = j_lo / BN;
-  const int w_hi = (min(p_last + 1, b_last) + BN - 1) / BN;
-  const int n_sink = min((far + BN - 1) / BN, w_lo), n_all = n_sink + max(0, w_hi - w_lo);
+  const ExtendTiles T = extend_tiles(x, tok0, Lq, Lk);
+  const int ntok = T.ntok, nw = ntok > TT ? 2 : 1, off = Lk - Lq, p0 = T.p0, p_last = T.p_last;
+  const int b_first = T.b_first, far = T.far, w_lo = T.w_lo, n_sink = T.n_sink, n_all = T.n_all;
   auto key0 = [&](int v) { return BN * (v < n_sink ? v : w_lo + v - n_sink); };
   const int v_end = min(n_all, (split + 1) * x.chunk), n_main = max(0, v_end - split * x.chunk);
   auto tile_key = [&](int i) { return key0(v_end - 1 - i); };      // nearest first
@@ -340,10 +328,11 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
 
     float m_ref = -INFINITY, l = 0.f;
     if (init) {
-      // the band's state: m = lse log2(e), l = 1, O = out (normalised)
+      // the band's state: m = lse log2(e), l = 1, O = what it left in out
       asm volatile("griddepcontrol.wait;" ::: "memory");
       const int tok = row_token(), h = row_head();
       const float lse0 = a.lse[(size_t)h * a.total_q + cq + tok];
+      const float2 ups = reinterpret_cast<const float2 *>(x.carry)[(size_t)(cq + tok) * a.Hq + h];
       if (lse0 != -INFINITY) {
         m_ref = lse0 * kLog2e;
         l = 1.f;
@@ -351,6 +340,7 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
       const uint4 *src = reinterpret_cast<const uint4 *>(a.out + ((size_t)(cq + tok) * a.Hq + h) * kHeadDim);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
+        const float up = c < 2 ? ups.x : ups.y;
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -358,8 +348,9 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
           const uint32_t pr[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            r[8 * i + 2 * k] = __float_as_uint(__uint_as_float(pr[k] << 16));
-            r[8 * i + 2 * k + 1] = __float_as_uint(__uint_as_float(pr[k] & 0xffff0000u));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pr[k]));
+            r[8 * i + 2 * k] = __float_as_uint(f.x * up);
+            r[8 * i + 2 * k + 1] = __float_as_uint(f.y * up);
           }
         }
         __syncwarp();
@@ -409,7 +400,7 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
         // window has left behind, as a bit a key
         int pp = pos;
         asm volatile("" : "+r"(pp));             // (worked out here: kept, they would spill)
-        const int first = band_first(x, pp), lo = a.window > 0 ? max(0, pp - a.window + 1) : 0;
+        const int first = extend_row_first(x, pp), lo = a.window > 0 ? max(0, pp - a.window + 1) : 0;
         const int kmin = lo - j0, kend = min(pp + 1, first) - j0;
         const int kfar = j0 < far ? min(min(a.sink, lo), first) - j0 : 0;
         auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
