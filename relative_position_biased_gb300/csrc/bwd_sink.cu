@@ -18,6 +18,8 @@
 // the 16 keys stay in its registers over all its rows.  P and dS are turned for
 // dk and dv in registers (movmatrix).  The sums of the CTAs go to slots that a
 // second kernel adds in order: no atomics, the same result every time.
+#include <algorithm>
+
 #include "launch.h"
 #include "nvfp4.cuh"
 
@@ -26,11 +28,16 @@ namespace {
 
 constexpr int SW = 8, ST = SW * 32;        // warps, threads
 constexpr int SK = 16;                     // keys of a block
-constexpr int SROWS = 1024;                // (token, head) rows of a CTA
+// (token, head) rows of a CTA: 1024 where that leaves two waves of CTAs and more
+// (a partial costs 16 KB), else fewer, down to one pass of the warps
+constexpr int kRowsMax = 1024, kRowsMin = 16 * SW;
 constexpr int kSinkRing = 2;
 constexpr int STAGE = 2 * 16 * 256;        // a warp's 16 rows of q and dout
 constexpr int OFF_K = 0, OFF_V = SK * 256, OFF_RING = 2 * SK * 256;
-constexpr int SMEM = OFF_RING + SW * kSinkRing * STAGE;
+constexpr int PS_ROW = 66;                 // bf16 of a distance of a warp's P slice (33 words: no bank conflicts)
+constexpr int PS_BYTES = 32 * PS_ROW * 2;
+constexpr int OFF_PS = OFF_RING + SW * kSinkRing * STAGE;
+constexpr int SMEM = OFF_PS + SW * PS_BYTES;
 constexpr int PART = 2 * SK * kHeadDim;    // floats of a slot
 static_assert(SW * 64 * 32 * 4 <= SW * kSinkRing * STAGE, "the merge reuses the ring");
 
@@ -51,19 +58,19 @@ __device__ __forceinline__ SinkRows sink_rows(const BwdArgs &a, int b) {
   return s;
 }
 // first slot of a sequence: floor(x) + 1 >= ceil(x) leaves every sequence enough
-__device__ __forceinline__ long first_slot(const BwdArgs &a, int b, int cq) { return (long)cq * a.group / SROWS + b; }
+__device__ __forceinline__ long first_slot(const BwdArgs &a, int rows, int b, int cq) { return (long)cq * a.group / rows + b; }
 __device__ __forceinline__ long slot_at(const BwdArgs &a, long slots, int g, int kb, long slot) {
   return (((long)g * ((a.sink + SK - 1) / SK) + kb) * slots + slot) * PART;
 }
 
-__global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_constant__ BwdArgs a, long slots) {
+__global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_constant__ BwdArgs a, int rows, long slots) {
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = smem_addr(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, qq = lane & 3;
   const int g = blockIdx.y, b = blockIdx.z;
   const SinkRows s = sink_rows(a, b);
   if (!s.ok && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrSeqlens);
-  const int x0 = (int)min((long)blockIdx.x * SROWS, (long)s.n), x1 = min(x0 + SROWS, s.n);
+  const int x0 = (int)min((long)blockIdx.x * rows, (long)s.n), x1 = min(x0 + rows, s.n);
   if (x0 >= x1) return;
   const int off = s.Lk - s.Lq, nkb = (a.sink + SK - 1) / SK;
   const uint32_t ring = sbase + OFF_RING + warp * kSinkRing * STAGE;
@@ -214,29 +221,36 @@ __global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_co
         mma_bf16_16816(dk[2 * dpi], d0, d1, d2, d3, b0, b1);
         mma_bf16_16816(dk[2 * dpi + 1], d0, d1, d2, d3, b2, b3);
       }
-      // ---- dr of the rows whose bias reaches a sink outside the window: a lane
-      // per channel, s dl from the lane that holds it
-      if (bias) {
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i) {
-          const int xr = x + i, t = token(xr), pos = off + t;
-          if (xr >= x1 || !sink_in_bias(a, pos)) continue;      // (warp-uniform)
-          const int c0 = min(lane, a.rd - 1), c1 = min(lane + 32, a.rd - 1);
-          float acc0 = 0.f, acc1 = 0.f;
+      // ---- dr of the rows whose bias reaches a sink outside the window: the columns
+      // of P that the 16 rows meet turned into shared memory [distance][channel],
+      // then two channels a lane (r_dim <= 64), s dl from the lane that holds it
+      if (bias && sink_in_bias(a, off + token(x))) {              // (the first row's distances are the least)
+        const int dmin = off + token(x) - (j0 + SK - 1);          // 31 distances at most
+        __nv_bfloat16 *ps = reinterpret_cast<__nv_bfloat16 *>(smem + OFF_PS + warp * PS_BYTES);
+        const bool col = dmin + lane >= a.window && dmin + lane < a.E;
+#pragma unroll 8
+        for (int c = 0; c < a.rd; ++c) ps[lane * PS_ROW + c] = col ? a.P[(size_t)c * a.E + dmin + lane] : __float2bfloat16(0.f);
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float v0 = __shfl_sync(0xffffffffu, rest[k >> 3][k & 1], 4 * (i & 7) + ((k & 7) >> 1));
-            const float v1 = __shfl_sync(0xffffffffu, rest[k >> 3][2 + (k & 1)], 4 * (i & 7) + ((k & 7) >> 1));
-            const int d = pos - (j0 + k);
-            const bool in = d >= a.window && d < a.E;
-            const float v = in ? (i < 8 ? v0 : v1) : 0.f;
-            const __nv_bfloat16 *p = a.P + (in ? d : 0);
-            acc0 = fmaf(v, __bfloat162float(p[(size_t)c0 * a.E]), acc0);
-            acc1 = fmaf(v, __bfloat162float(p[(size_t)c1 * a.E]), acc1);
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int xr = x + 8 * r + i, t = token(xr), pos = off + t;
+            if (xr >= x1 || !sink_in_bias(a, pos)) continue;      // (warp-uniform)
+            float acc0 = 0.f, acc1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < SK; ++k) {
+              const float v = __shfl_sync(0xffffffffu, rest[k >> 3][2 * r + (k & 1)], 4 * i + ((k & 7) >> 1));
+              const int d = pos - (j0 + k);
+              if (d < a.window || d >= a.E) continue;             // (no term, whatever s dl is)
+              const float2 p = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162 *>(ps + (d - dmin) * PS_ROW)[lane]);
+              acc0 = fmaf(v, p.x, acc0);
+              acc1 = fmaf(v, p.y, acc1);
+            }
+            float *dst = a.sink_dr + ((size_t)(s.cq + t) * a.Hq + head(xr)) * a.rd + 2 * lane;
+            if (2 * lane < a.rd) dst[0] = kb > 0 ? dst[0] + acc0 : acc0;
+            if (2 * lane + 1 < a.rd) dst[1] = kb > 0 ? dst[1] + acc1 : acc1;
           }
-          float *dst = a.sink_dr + ((size_t)(s.cq + t) * a.Hq + head(xr)) * a.rd;
-          if (lane < a.rd) dst[lane] = kb > 0 ? dst[lane] + acc0 : acc0;
-          if (lane + 32 < a.rd) dst[lane + 32] = kb > 0 ? dst[lane + 32] + acc1 : acc1;
         }
       }
       __syncwarp();                        // the stage is read
@@ -244,7 +258,7 @@ __global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_co
     cp_async_wait<0>();
 
     // ---- the warps' dk, then dv, through the ring into the CTA's slot
-    float *part = a.sink_part + slot_at(a, slots, g, kb, first_slot(a, b, s.cq) + blockIdx.x);
+    float *part = a.sink_part + slot_at(a, slots, g, kb, first_slot(a, rows, b, s.cq) + blockIdx.x);
     float *red = reinterpret_cast<float *>(smem + OFF_RING);      // [warp][64][32 lanes]
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
@@ -267,34 +281,40 @@ __global__ void __launch_bounds__(ST, 1) relattn_bwd_sink_kernel(const __grid_co
 }
 
 // sink_dkv[b][g][j] = the slots' sums in order (zero where no row has the sink)
-__global__ void __launch_bounds__(2 * kHeadDim) relattn_bwd_sink_sum_kernel(const __grid_constant__ BwdArgs a, long slots) {
+__global__ void __launch_bounds__(2 * kHeadDim) relattn_bwd_sink_sum_kernel(const __grid_constant__ BwdArgs a, int rows, long slots) {
   const int j = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int which = threadIdx.x / kHeadDim, dim = threadIdx.x % kHeadDim;
   const SinkRows s = sink_rows(a, b);
-  const int n = (s.n + SROWS - 1) / SROWS;
+  const int n = (s.n + rows - 1) / rows;
   const float *src = a.sink_part + (which * SK + j % SK) * kHeadDim + dim;
   float v = 0.f;
-  for (int i = 0; i < n; ++i) v += src[slot_at(a, slots, g, j / SK, first_slot(a, b, s.cq) + i)];
+  for (int i = 0; i < n; ++i) v += src[slot_at(a, slots, g, j / SK, first_slot(a, rows, b, s.cq) + i)];
   a.sink_dkv[((((size_t)b * a.Hkv + g) * a.sink + j) * 2 + which) * kHeadDim + dim] = v;
 }
 
-long sink_slots(int batch, int total_q, int group) { return (long)total_q * group / SROWS + batch; }
+int sink_rows_of_cta(int total_q, int Hq) {
+  const long want = (long)total_q * Hq / (2 * 152) / kRowsMin * kRowsMin;
+  return (int)std::min<long>(std::max<long>(want, kRowsMin), kRowsMax);
+}
+long sink_slots(int batch, int total_q, int group, int rows) { return (long)total_q * group / rows + batch; }
 
 }  // namespace
 
 size_t bwd_sink_part_bytes(int batch, int total_q, int Hkv, int group, int sink) {
-  return (size_t)Hkv * ((sink + SK - 1) / SK) * sink_slots(batch, total_q, group) * PART * sizeof(float);
+  const int rows = sink_rows_of_cta(total_q, Hkv * group);
+  return (size_t)Hkv * ((sink + SK - 1) / SK) * sink_slots(batch, total_q, group, rows) * PART * sizeof(float);
 }
 
 cudaError_t launch_bwd_sink(const BwdArgs &a, cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevicesAttr];
   cudaError_t e = set_max_smem_once(reinterpret_cast<const void *>(relattn_bwd_sink_kernel), SMEM, done);
   if (e != cudaSuccess) return e;
-  const long slots = sink_slots(a.batch, a.total_q, a.group);
-  const unsigned chunks = (unsigned)(((long)a.max_q * a.group + SROWS - 1) / SROWS);
-  relattn_bwd_sink_kernel<<<dim3(chunks, a.Hkv, a.batch), ST, SMEM, stream>>>(a, slots);
+  const int rows = sink_rows_of_cta(a.total_q, a.Hq);
+  const long slots = sink_slots(a.batch, a.total_q, a.group, rows);
+  const unsigned chunks = (unsigned)(((long)std::min(a.max_q, a.total_q) * a.group + rows - 1) / rows);
+  relattn_bwd_sink_kernel<<<dim3(chunks, a.Hkv, a.batch), ST, SMEM, stream>>>(a, rows, slots);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  relattn_bwd_sink_sum_kernel<<<dim3(a.sink, a.Hkv, a.batch), 2 * kHeadDim, 0, stream>>>(a, slots);
+  relattn_bwd_sink_sum_kernel<<<dim3(a.sink, a.Hkv, a.batch), 2 * kHeadDim, 0, stream>>>(a, rows, slots);
   return cudaGetLastError();
 }
 
