@@ -379,7 +379,7 @@ relattn_status validate_extend(const relattn_params *p, const relattn_paged_kv *
 
 // How relattn_extend runs: at most 16 rows per kv head on the few-row decode
 // kernel, more on the tcgen05 kernels of many rows (where shapes and alignment
-// allow), any shape on the warp-MMA kernel.
+// allow), any other shape and short calls (extend_short) on the warp-MMA kernel.
 enum class ExtendKind { kMma, kFew, kTc };
 struct ExtendPlan {
   ExtendKind kind;
@@ -459,15 +459,28 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
   }
 }
 
+// Few rows of few keys: one launch of the warp-MMA kernel, a CTA per 128 rows of a
+// head that walks the keys in order, against the cost of cutting and merging them.
+// 1 token, 4 heads (one kv head): 13 us against 27-31 at 64 keys, 25 against 35 at
+// 300, 31 against 35-37 at 400; 40 tokens, 16 heads: 25 against 23 at 200 keys and
+// 29 against 25 at 300, with 8 us less of the host's time.  With more CTAs than SMs
+// it loses at once (64 tokens of 16 heads, 200 keys: 144 against 31).
+bool extend_short(const relattn_params *p, const KernelArgs &a) {
+  constexpr long kKeys = 320;
+  const long seen = a.window > 0 ? (long)a.window + std::min(a.max_q, 128) + a.sink : a.max_k;
+  return p->num_splits <= 0 && std::min<long>(seen, a.max_k) <= kKeys && (long)a.q_tiles * a.Hq * a.batch <= a.sms;
+}
+
 relattn_status plan_extend(const relattn_params *p, const KernelArgs &a, ExtendPlan *plan) {
   *plan = ExtendPlan{};
+  plan->kind = ExtendKind::kMma;
+  if (extend_short(p, a)) return RELATTN_OK;
   if (decode_few_rows_supported(a, a.kv_rows)) {
     plan->kind = ExtendKind::kFew;
     const relattn_status st = plan_decode(p, &plan->few, a.kv_rows, a.sink);
     plan->ws_bytes = plan->few.ws_bytes;
     return st;
   }
-  plan->kind = ExtendKind::kMma;
   if (tc_supported(a, a.kv_rows) && a.alpha_log2e > 0.f && a.group <= 128) {
     plan->kind = ExtendKind::kTc;
     plan_extend_tc(p, a, plan);

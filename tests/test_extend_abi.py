@@ -84,9 +84,9 @@ def test_backward_workspace():
     plain = rpb.relattn_backward_workspace_size(bwd())[1]
     assert rpb.relattn_backward_sinks_workspace_size(bwd(), 0) == (0, plain)
     assert rpb.relattn_backward_sinks_workspace_size(bwd(fwd(window=0)), 4)[1] == rpb.relattn_backward_workspace_size(bwd(fwd(window=0)))[1]
-    # dq 40 x 8 x 128 fp32; dk, dv 2 x 2 x 4 x 2 x 128; partials: 2 heads x (40 x 4 / 1024 + 2) slots of 2 x 16 x 128
+    # dq 40 x 8 x 128 fp32; dk, dv 2 x 2 x 4 x 2 x 128; partials: 2 heads x (40 x 4 / 128 + 2) slots (128 rows each) of 2 x 16 x 128
     plain = (plain + 255) // 256 * 256
-    want = plain + 40 * 8 * 512 + 2 * 2 * 4 * 1024 + 2 * 2 * 2 * 16 * 512
+    want = plain + 40 * 8 * 512 + 2 * 2 * 4 * 1024 + 2 * 3 * 2 * 16 * 512
     assert rpb.relattn_backward_sinks_workspace_size(bwd(), 4) == (0, want)
     # the bias reaches past the window: dr 40 x 8 x 16 fp32 as well
     assert rpb.relattn_backward_sinks_workspace_size(bwd(fwd(window=63)), 4) == (0, want + 40 * 8 * 64)

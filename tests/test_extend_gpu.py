@@ -103,6 +103,24 @@ def test_windows_with_sinks(Hq, Hkv, rd, E, window, sink, page, q_lens, k_lens):
     check(U.Case(q_lens, k_lens, Hq, Hkv, r_dim=rd, E=E, window=window, page=page, seed=window + sink), sink)
 
 
+@pytest.mark.parametrize("num_splits", [1, 2])       # (0 takes the warp-MMA kernel for most of these)
+@pytest.mark.parametrize("Hq,Hkv,rd,E", LAYOUTS)
+@pytest.mark.parametrize("page,q_lens,k_lens,window,sink", [
+    (0, (1,), (1,), 0, 0), (16, (1, 1), (17, 300), 0, 0), (16, (2, 0, 9), (64, 16, 129), 40, 3), (32, (33, 7), (33, 250), 0, 0),
+    (0, (129, 1), (300, 256), 60, 2), (64, (40, 1), (41, 1), 9, 1),
+])
+def test_short_sequences_on_the_kernels_of_long_ones(Hq, Hkv, rd, E, page, q_lens, k_lens, window, sink, num_splits):
+    check(U.Case(q_lens, k_lens, Hq, Hkv, r_dim=rd, E=E, window=window, page=page, seed=len(q_lens) + page), sink,
+          num_splits=num_splits)
+
+
+@pytest.mark.parametrize("k_len", [310, 320, 321, 330])
+@pytest.mark.parametrize("q_len,window,sink", [(1, 0, 0), (1, 300, 19), (1, 300, 20), (20, 0, 0), (20, 290, 10), (20, 290, 11)])
+def test_lengths_about_where_the_kernels_change(q_len, window, sink, k_len):
+    check(U.Case((q_len,), (k_len,), 4, 1, r_dim=32, E=64, window=window, page=16, seed=k_len), sink)
+    check(U.Case((q_len,), (k_len + 3000,), 4, 1, r_dim=32, E=64, window=window, page=16, seed=k_len), sink)
+
+
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("base", [0.0, 16.0])
 @pytest.mark.parametrize("q_lens,k_lens", [((1, 1), (90, 300)), ((40, 300), (90, 300))])
