@@ -385,7 +385,8 @@ struct ExtendPlan {
   ExtendKind kind;
   DecodePlan few;
   ExtendTcArgs tc;
-  size_t ws_bytes, lse_offset;
+  size_t ws_bytes, lse_offset, piece_offset, cut_offset;
+  int partials;                // of a row, about
 };
 
 relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, int32_t sink, KernelArgs *a) {
@@ -402,42 +403,25 @@ relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, 
   return RELATTN_OK;
 }
 
-// The tcgen05 kernels of many rows: ranges of the keys, pieces of the band and
-// the partials they need.
+// The tcgen05 kernels of many rows: CTAs that share the keys before the band,
+// pieces of the band, and the partials that both leave.
 void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *plan) {
-  constexpr long kTile = kTcKeyTile, kMaxRanges = 64;
+  constexpr long kTile = kTcKeyTile, kMinShare = 72;      // units: 6 a step of a pair of row tiles, 21 a piece (extend_tc.cu)
   ExtendTcArgs &x = plan->tc;
   x.a = a;
   const bool bias = a.rd > 0 && a.E > 0;
   x.tokens = 128 / a.group;
-  x.row_tiles = (a.max_q + 2 * x.tokens - 1) / (2 * x.tokens);
-  // row tiles in pairs, the key tiles of one at most and on the average
-  const long pairs = std::min<long>((long)a.batch * x.row_tiles, a.total_q / (2 * x.tokens) + a.batch) * a.Hkv;
+  // pairs of row tiles and the units of one, at most
+  const long pairs = std::min<long>((long)a.batch * (((long)a.max_q + 2 * x.tokens - 1) / (2 * x.tokens)),
+                                    a.total_q / (2 * x.tokens) + a.batch) * a.Hkv;
   long most = (a.max_k + kTile - 1) / kTile;
   if (a.window > 0)
     most = std::min<long>(most, ((long)a.window + 2 * x.tokens + 2 * kTile) / kTile + (std::min(a.sink, a.max_k) + kTile - 1) / kTile);
-  most = std::max<long>(most, 1);
-  const long mean = std::max<long>(std::min<long>(most, p->total_k / a.batch / kTile), 1);
-  long chunk = most;
-  if (p->num_splits > 0) {
-    chunk = (most + p->num_splits - 1) / p->num_splits;
-  } else {
-    // the cut with the shortest time, in steps of a key tile (1.8 us): waves of
-    // CTAs, each with a start of some six steps; partials cost a launch and their
-    // traffic
-    const double rows_us = (double)a.total_q * a.Hq * kHeadDim * 8 / 6.5e6;    // of a partial, out and in
-    double best = 1e30;
-    for (long k = 1; k <= std::min(kMaxRanges, most); ++k) {
-      const long c = (most + k - 1) / k, per = (mean + c - 1) / c, ctas = pairs * per;
-      double t = (double)((ctas + a.sms - 1) / a.sms) * (std::min(c, mean) + 6);
-      if (ctas <= a.sms) t = c + 6;
-      if (k > 1) t += 4 + per * rows_us / 1.8;
-      if (t < best) best = t, chunk = c;
-    }
-  }
-  chunk = std::max<long>(std::min(chunk, most), (most + kMaxRanges - 1) / kMaxRanges);
-  x.splits = (int)((most + chunk - 1) / chunk);
-  x.chunk = (int)chunk;
+  const long units = 6 * std::max<long>(most, 1) + 21;
+  // (shares of units / (n - 1) meet at most n - 1 ends of them in a row tile)
+  x.min_share = std::max<long>(kMinShare, p->num_splits > 1 ? (units + p->num_splits - 2) / (p->num_splits - 1) : 0);
+  x.ctas = (int)std::min<long>(a.sms, std::max<long>((pairs * units + x.min_share - 1) / x.min_share, 1));
+  x.piece_tokens = std::min(2 * x.tokens, a.max_q);
   // the band, in pieces where its items leave SMs idle
   x.band = bias ? 1 : 0;
   x.band_pieces = 1;
@@ -445,17 +429,22 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
   if (bias) {
     const int tokens = extend_band_tokens(a);
     const long steps = ((long)a.E + tokens + 126) / 64 + 3;        // at most, of a row block
-    const long items = std::min<long>((long)a.batch * ((a.max_q + tokens - 1) / tokens), a.total_q / tokens + a.batch) * a.Hkv;
+    const long items = std::min<long>((long)a.batch * (((long)a.max_q + tokens - 1) / tokens), a.total_q / tokens + a.batch) * a.Hkv;
     if (p->num_splits <= 0 && items < a.sms) x.band_pieces = (int)std::max<long>(1, std::min<long>(a.sms / items, steps / 4));
     x.band_steps = (int)((steps + x.band_pieces - 1) / x.band_pieces);
   }
-  x.slots = x.splits > 1 || x.band_pieces > 1 ? x.splits + (bias ? x.band_pieces : 0) : 1;
-  if (x.slots > 1) {
-    const size_t rows = (size_t)a.total_q * a.Hq;
-    plan->lse_offset = (size_t)x.slots * rows * kHeadDim * sizeof(float);
-    plan->ws_bytes = plan->lse_offset + (size_t)x.slots * rows * sizeof(float);
-  } else if (bias) {
-    plan->ws_bytes = (size_t)a.total_q * a.Hq * 2 * sizeof(float);     // (the carry)
+  x.slots = x.band_pieces > 1 ? x.band_pieces + 1 : 1;
+  // workspace: partials by row (or the carry), the CTAs' pieces, their cuts
+  const size_t rows = (size_t)a.total_q * a.Hq, piece_rows = 2 * (size_t)x.ctas * x.piece_tokens * a.group;
+  const auto up16 = [](size_t n) { return (n + 15) / 16 * 16; };
+  plan->lse_offset = x.slots > 1 ? x.slots * rows * kHeadDim * sizeof(float) : 0;
+  plan->piece_offset = up16(x.slots > 1 ? plan->lse_offset + x.slots * rows * sizeof(float) : bias ? rows * 2 * sizeof(float) : 0);
+  plan->ws_bytes = plan->piece_offset;
+  plan->partials = x.slots;
+  if (p->num_splits != 1 && (x.ctas > 1 || x.slots > 1)) {
+    plan->cut_offset = up16(plan->piece_offset + piece_rows * (kHeadDim + 1) * sizeof(float));
+    plan->ws_bytes = plan->cut_offset + x.ctas * sizeof(int4);
+    plan->partials += (int)(x.ctas / std::max<long>(pairs, 1)) + 1;
   }
 }
 
@@ -490,15 +479,21 @@ relattn_status plan_extend(const relattn_params *p, const KernelArgs &a, ExtendP
 
 relattn_status run_extend_tc(const relattn_params *p, ExtendPlan &plan, cudaStream_t s) {
   ExtendTcArgs &x = plan.tc;
+  char *ws = static_cast<char *>(p->workspace);
   if (x.slots > 1) {
-    x.a.o_part = static_cast<float *>(p->workspace);
-    x.a.lse_part = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + plan.lse_offset);
+    x.a.o_part = reinterpret_cast<float *>(ws);
+    x.a.lse_part = reinterpret_cast<float *>(ws + plan.lse_offset);
   } else {
-    x.carry = static_cast<float *>(p->workspace);
+    x.carry = reinterpret_cast<float *>(ws);
+  }
+  if (plan.cut_offset > 0) {
+    x.piece = reinterpret_cast<float *>(ws + plan.piece_offset);
+    x.piece_lse = x.piece + 2 * (size_t)x.ctas * x.piece_tokens * x.a.group * kHeadDim;
+    x.cut = reinterpret_cast<int4 *>(ws + plan.cut_offset);
   }
   cudaError_t e = x.band == 0 ? cudaSuccess : launch_extend_band(x, s);
   if (e == cudaSuccess) e = launch_extend_main(x, s);
-  if (e == cudaSuccess && x.slots > 1) e = launch_extend_combine(x.a, x.slots, true, s);
+  if (e == cudaSuccess && x.cut != nullptr) e = launch_extend_combine(x, plan.partials, s);
   return e == cudaSuccess ? RELATTN_OK : RELATTN_ERR_CUDA;
 }
 
@@ -1013,7 +1008,10 @@ relattn_status relattn_extend(const relattn_params *p, const relattn_paged_kv *p
     if (decode_rel_bytes(a) > 0) a.rdec = reinterpret_cast<const float *>(ws + plan.few.rel_offset);
     const cudaError_t e = launch_extend_few_rows(a, s);
     if (e != cudaSuccess || plan.few.splits == 1) return cuda_status(e);
-    return cuda_status(launch_extend_combine(a, plan.few.splits, true, s));
+    ExtendTcArgs x{};
+    x.a = a;
+    x.slots = plan.few.splits;
+    return cuda_status(launch_extend_combine(x, x.slots, s));
   }
   if (plan.kind == ExtendKind::kTc) return run_extend_tc(p, plan, s);
   return cuda_status(launch_extend_mma(a, s));

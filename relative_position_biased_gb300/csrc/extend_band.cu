@@ -153,7 +153,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     const int low = (min(a.sink, j_lo) > b0 ? b0 : max(b0, j_lo)) / HN;
     I.first = I.p_last / HN - piece * ba.x.band_steps;
     I.steps = min(ba.x.band_steps, max(0, I.first - low + 1));
-    I.slot = ba.x.splits + piece;
+    I.slot = piece;
     const int D0 = I.p0 - HN * I.first;
     I.c_first = floor_div64(D0 + I.ntok - 1);
     I.c_start = max(0, floor_div64(D0 - (HN - 1)));

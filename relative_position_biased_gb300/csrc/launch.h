@@ -79,11 +79,18 @@ struct ExtendTcArgs {
   KernelArgs a;
   int band;            // 1: a bias, whose band has a kernel of its own
   int tokens;          // of a row tile: 128 / group
-  int row_tiles;       // pairs of row tiles per (sequence, kv head), of max_q tokens
-  int splits, chunk;   // ranges of `chunk` key tiles
-  int slots;           // partials of a row: the ranges', then the band pieces'; 1: none
+  int ctas;            // of extend_tc.cu, each a share of the key tiles
+  long min_share;      // units that a share holds at least
+  int slots;           // partials by row: the band pieces', then the rest's first piece; 1: none
   int band_pieces, band_steps;   // pieces of a row's band, steps of 64 keys of one
   int box, q_bytes;    // (set by the launcher)
+  // Two pieces a CTA (fp32 rows of piece_tokens tokens x a group, and their lse): the
+  // one that its share starts with, behind a cut, and the one that it ends with,
+  // before a cut; cut[i] = (sequence, pair of row tiles, kv head, steps before it) of
+  // share i's start, no cut if that is 0.  Null: row tiles are not cut.
+  int piece_tokens;
+  float *piece, *piece_lse;
+  int4 *cut;
   // In one piece the band hands its rows on in `out`: f16 with a power of two for
   // each half of a row in `carry` (workspace, fp32 [total_q][Hq][2]), 3 bits more
   // than bf16 in the same bytes.  (In bf16 the rows of 4 chunks of 2048 under a window of 4096
@@ -118,9 +125,10 @@ __device__ __forceinline__ ExtendTiles extend_tiles(const ExtendTcArgs &x, int t
 cudaError_t launch_extend_main(const ExtendTcArgs &x, cudaStream_t stream);
 cudaError_t launch_extend_band(const ExtendTcArgs &x, cudaStream_t stream);
 int extend_band_tokens(const KernelArgs &a);   // of a work item
-// out / lse from `slots` partials of every row of a sequence (extend_tc.cu);
-// other rows keep theirs
-cudaError_t launch_extend_combine(const KernelArgs &a, int slots, bool pdl, cudaStream_t stream);
+// out / lse from their partials (extend_tc.cu), about `partials` a row: of every
+// row of a sequence with x.slots > 1 (other rows keep theirs), else of the row tiles
+// that were cut.  A programmatic dependent of the kernel before it on the stream.
+cudaError_t launch_extend_combine(const ExtendTcArgs &x, int partials, cudaStream_t stream);
 
 // tcgen05 / TMA kernels: need 16-byte aligned q/k/v/out (and r/P), r_dim % 8 == 0,
 // rel_extent % 8 == 0, r_dim <= 64 and at least one 128-key tile of K/V.
