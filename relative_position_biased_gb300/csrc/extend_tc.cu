@@ -5,7 +5,7 @@
 // Per row, x(i,j) = s(i) alpha q_i . k_j over the keys that the band kernel leaves
 // (page "SGLang and Miles Add Day-0 Support for Inkling", section "Attention
 // with Relative Positional Embedding"), softmax, P V.  The band kernel has, per
-// row, the keys from a first one on (band_first below).
+// row, the keys from a first one on (extend_band_first).
 //
 // An item is up to 256 rows of one kv head, (token, head of the group) pairs in two
 // tiles of 128 that share every K / V tile, against key tiles of 128 from the nearest

@@ -121,6 +121,37 @@ def test_lengths_about_where_the_kernels_change(q_len, window, sink, k_len):
     check(U.Case((q_len,), (k_len + 3000,), 4, 1, r_dim=32, E=64, window=window, page=16, seed=k_len), sink)
 
 
+@pytest.fixture
+def few_ctas():
+    """(the test build runs the kernels that share their work on a few CTAs)"""
+    with rpb.test_library():
+        yield lambda n: rpb.relattn_test_band_ctas(n) == 0 or pytest.fail("no hook")
+        rpb.relattn_test_band_ctas(0)
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 3, 7, 40])
+@pytest.mark.parametrize("E,window,sink,num_splits", [(64, 0, 0, 0), (64, 700, 5, 0), (0, 0, 0, 0), (0, 300, 200, 3), (520, 0, 0, 2)])
+@pytest.mark.parametrize("Hq,Hkv,page,q_lens,k_lens", [
+    (8, 1, 16, (300, 5, 0, 70, 1), (1500, 2900, 40, 600, 333)),        # row tiles of one and of two, some cut
+    (6, 2, 0, (90, 0, 0, 33), (2000, 0, 70, 2500)),                    # group 3: tiles that its heads do not fill
+    (16, 2, 128, (17,), (6000,)),                                      # a tile in many shares
+])
+def test_shares_of_any_number_of_ctas(few_ctas, ctas, E, window, sink, num_splits, Hq, Hkv, page, q_lens, k_lens):
+    few_ctas(ctas)
+    check(U.Case(q_lens, k_lens, Hq, Hkv, r_dim=16 if E else 0, E=E, window=window, page=page, seed=ctas), sink,
+          num_splits=num_splits)
+
+
+def test_shares_of_many_sequences(few_ctas):
+    """More sequences than a warp's 32 lanes and than the 12 warps that count their work, many of them empty or short."""
+    rng = np.random.default_rng(8)
+    q_lens = tuple(int(x) for x in rng.integers(0, 60, 90) * (rng.random(90) < 0.6))
+    k_lens = tuple(n + int(x) for n, x in zip(q_lens, rng.integers(0, 600, 90) * (rng.random(90) < 0.5)))
+    for ctas in (0, 5, 31):
+        few_ctas(ctas)
+        check(U.Case(q_lens, k_lens, 8, 1, r_dim=16, E=64, page=16, seed=2))
+
+
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("base", [0.0, 16.0])
 @pytest.mark.parametrize("q_lens,k_lens", [((1, 1), (90, 300)), ((40, 300), (90, 300))])
