@@ -12,7 +12,9 @@
 // is added before the results' one rounding to bf16.
 //
 // What bounds it: every row past the window is read (q, dout: 512 bytes) and its
-// dq part written (512 bytes), for 16 keys' five products: HBM.  A warp takes 16
+// dq part written (512 bytes), for 16 keys' five products: HBM.  4 x 8192 tokens of
+// 16 heads, window 4096: 67 us for 268 MB, 4.0 TB/s (the sums 5 us); few rows are a
+// chain of loads instead: 5 sequences of 90 to 1500 tokens of 8 heads take 20.  A warp takes 16
 // rows (token, head of the group) at a time against 16 keys, in m16n8k16
 // instructions; its rows come through a two-stage ring of its own; dk and dv of
 // the 16 keys stay in its registers over all its rows.  P and dS are turned for
@@ -28,8 +30,9 @@ namespace {
 
 constexpr int SW = 8, ST = SW * 32;        // warps, threads
 constexpr int SK = 16;                     // keys of a block
-// (token, head) rows of a CTA: 1024 where that leaves two waves of CTAs and more
-// (a partial costs 16 KB), else fewer, down to one pass of the warps
+// (token, head) rows of a CTA: 1024 where that leaves two CTAs an SM and more, else
+// fewer, down to one pass of the warps.  Each CTA's partial costs 16 KB: 4 x 8192
+// tokens 67 us with 1024 rows, 112 with 128; 5 sequences of 90 - 1500 67 and 20.
 constexpr int kRowsMax = 1024, kRowsMin = 16 * SW;
 constexpr int kSinkRing = 2;
 constexpr int STAGE = 2 * 16 * 256;        // a warp's 16 rows of q and dout

@@ -28,6 +28,13 @@
 // step, warps 8-11 keys 32-63.
 // Tensor memory: Q [0,64), O [64,192), S 2 x 64 [192,320) (P in bf16 over it),
 // R 2 x 64 [320,448).
+// What bounds it: a step's chain -- S and R out of tensor memory, R's way through
+// shared memory, the exchange of the maximum between a row's two threads, the
+// exponentials, P -- takes 2,000 cycles; issue slots 41 %, tensor pipe 25 % (4 x 8192
+// tokens, Hq 16 / Hkv 2, r_dim 64, E 1024, window 4096: 568 us; R issued with its own
+// step instead of one ahead 710, four softmax warpgroups or P before the step's
+// maximum no faster).
+//
 // Every wait is bounded; a timeout sets the device error word, the CTA drains
 // its own copies / MMAs with bounded waits, frees tensor memory and exits.
 #include <cudaTypedefs.h>
