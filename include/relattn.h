@@ -194,7 +194,8 @@ relattn_status relattn_decode_paged(const relattn_params *params, const relattn_
  * (The pages name neither chunks over pages nor sinks; both are this library's
  * own addition in their manner.)
  * out and lse of a row are those of relattn_prefill for the same keys to
- * rounding, and feed relattn_backward_sinks.  Rows of no sequence keep their
+ * rounding, and feed relattn_backward_sinks.  out must not overlap q, k, v
+ * or r (RELATTN_ERR_INVALID_ARG).  Rows of no sequence keep their
  * out and lse; keys past max_seqlen_k or rows outside the arrays skip the
  * sequence and record RELATTN_ERR_DEVICE_ARGS.  max_seqlen_k up to 2^31 - 2^16;
  * batch and num_heads_q up to 65535.

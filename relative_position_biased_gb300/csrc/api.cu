@@ -373,8 +373,15 @@ relattn_status validate_extend(const relattn_params *p, const relattn_paged_kv *
   if (st != RELATTN_OK) return st;
   if (sink < 0) return RELATTN_ERR_INVALID_ARG;
   if (kv && (st = check_pages(kv, p->max_seqlen_k)) != RELATTN_OK) return st;
-  if (p->max_seqlen_k > kMaxKeys) return RELATTN_ERR_UNSUPPORTED;
-  return p->batch > 65535 || p->num_heads_q > 65535 ? RELATTN_ERR_UNSUPPORTED : RELATTN_OK;
+  if (p->max_seqlen_k > kMaxKeys || p->batch > 65535 || p->num_heads_q > 65535) return RELATTN_ERR_UNSUPPORTED;
+  // (out holds the band's rows while the rest of the call still reads q)
+  const size_t q_bytes = (size_t)p->total_q * p->num_heads_q * kHeadDim * 2;
+  const size_t rows = kv ? (size_t)kv->num_pages * kv->page_size : (size_t)p->total_k;
+  const size_t kv_bytes = rows * p->num_heads_kv * kHeadDim * 2, r_bytes = p->r ? (size_t)p->total_q * p->num_heads_q * p->r_dim * 2 : 0;
+  if (overlaps(p->out, q_bytes, p->q, q_bytes) || overlaps(p->out, q_bytes, p->k, kv_bytes) ||
+      overlaps(p->out, q_bytes, p->v, kv_bytes) || overlaps(p->out, q_bytes, p->r, r_bytes))
+    return RELATTN_ERR_INVALID_ARG;
+  return RELATTN_OK;
 }
 
 // How relattn_extend runs: at most 16 rows per kv head on the few-row decode
@@ -434,6 +441,10 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
     const long items = std::min<long>((long)a.batch * (((long)a.max_q + tokens - 1) / tokens), a.total_q / tokens + a.batch) * a.Hkv;
     if (p->num_splits <= 0 && 2 * items < a.sms) x.band_pieces = (int)std::max<long>(1, std::min<long>(a.sms / items, steps / 4));
     x.band_steps = (int)((steps + x.band_pieces - 1) / x.band_pieces);
+    x.band_tokens = tokens;
+    // (24 us for the 17 steps of a bias of 1024, 6 of them its start and end)
+    const long met = std::min<long>(x.band_steps, (std::min(a.E, a.window > 0 ? a.window : a.E) + tokens) / 64 + 1);
+    if (p->num_splits <= 0) x.band_units = (int)(4 * met + 24);
   }
   x.slots = x.band_pieces > 1 ? x.band_pieces + 1 : 1;
   // workspace: partials by row (or the carry), the CTAs' pieces, their cuts

@@ -23,6 +23,11 @@
 // A step adds 64 distances and needs those of 64 keys and the block's tokens: 160
 // hold up to 32 tokens (groups of 4 and more: 128 rows), 192 up to 64.
 //
+// The list of items is counted from the lengths on the device, so that a batch whose
+// sequences are far shorter than the longest has no empty ones (4096 tokens of one
+// sequence and one of 63 others: the band 428 us with a place in the list for every
+// block that a sequence might have, 117 so).
+//
 // Warps: 0: r rows, P slices and K tiles; 1: tensor memory, issues the products;
 // 2: q rows and V tiles; 4-11: softmax, thread = row, warps 4-7 keys 0-31 of a
 // step, warps 8-11 keys 32-63.
@@ -86,7 +91,7 @@ static_assert(smem_bytes<false>() <= 227 * 1024 && smem_bytes<true>() <= 227 * 1
 struct BandArgs {
   ExtendTcArgs x;
   int tokens;             // of an item
-  int blocks, n_items;
+  int n_items;            // at most (sequences that do not overlap)
   int box, row_bytes;     // rows of a K / V copy; bytes of 64 dims (or channels) of an item's q (or r) rows
 };
 
@@ -136,23 +141,50 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // ------------------------------------------------------------ work items
-  // (token block from the last backwards, sequence, kv head, piece); every role
-  // walks the same list and its counters run on
+  // (sequence, token block from the last backwards, kv head, piece), the list without
+  // gaps, every grid-th one from the CTA's number on.  Every role walks the same list
+  // and its counters run on.  32 sequences at a time lie in the lanes of a warp.
   Item I{};
   int gs = 0, vb = 0, ob = 0, n_it = 0;   // steps, V slots, chunks and items (with steps) so far
-  auto load_item = [&](int idx) -> int {  // 1 rows to do (steps may be 0), 0 none, -1 inconsistent lengths
-    const int per = a.batch * a.Hkv * ba.x.band_pieces, xi = idx / per, rem = idx - xi * per;
-    const int piece = rem % ba.x.band_pieces;
-    I.g = rem / ba.x.band_pieces % a.Hkv;
-    I.b = rem / (ba.x.band_pieces * a.Hkv);
-    I.tok0 = (ba.blocks - 1 - xi) * ba.tokens;
-    I.cq = __ldg(a.cu_q + I.b);
-    I.ck = __ldg(a.cu_k + I.b);
-    const int Lq = __ldg(a.cu_q + I.b + 1) - I.cq;
-    I.lk = __ldg(a.cu_k + I.b + 1) - I.ck;
-    if (Lq < 0 || I.lk < Lq || Lq > a.max_q || I.lk > a.max_k || !extend_rows_ok(a, I.cq, Lq, I.ck, I.lk)) return -1;
+  int c0 = -32, c_run = 0, c_all = 0;     // first of the sequences, items before them, theirs
+  int s_cq = 0, s_ck = 0, s_Lq = 0, s_Lk = 0, s_upto = 0;      // lane's sequence, items up to its end
+  const int per_block = a.Hkv * ba.x.band_pieces;
+  auto next_item = [&](int n) -> bool {   // the list's n-th (n grows); its steps may be 0
+    if (n >= ba.n_items) return false;
+    while (n >= c_run + c_all) {
+      c_run += c_all;
+      c0 += 32;
+      if (c0 >= a.batch) return false;
+      s_Lq = 0;
+      if (c0 + lane < a.batch) {
+        s_cq = __ldg(a.cu_q + c0 + lane);
+        s_ck = __ldg(a.cu_k + c0 + lane);
+        s_Lq = __ldg(a.cu_q + c0 + lane + 1) - s_cq;
+        s_Lk = __ldg(a.cu_k + c0 + lane + 1) - s_ck;
+        if (s_Lq < 0 || s_Lk < s_Lq || s_Lq > a.max_q || s_Lk > a.max_k || !extend_rows_ok(a, s_cq, s_Lq, s_ck, s_Lk)) {
+          atomicOr(a.err, kDevErrSeqlens);
+          s_Lq = 0;
+        }
+      }
+      s_upto = (s_Lq + ba.tokens - 1) / ba.tokens * per_block;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s_upto, o);
+        if (lane >= o) s_upto += u;
+      }
+      c_all = __shfl_sync(0xffffffffu, s_upto, 31);
+    }
+    const int i = __ffs(__ballot_sync(0xffffffffu, c_run + s_upto > n)) - 1;
+    I.b = c0 + i;
+    I.cq = __shfl_sync(0xffffffffu, s_cq, i);
+    I.ck = __shfl_sync(0xffffffffu, s_ck, i);
+    I.lk = __shfl_sync(0xffffffffu, s_Lk, i);
+    const int Lq = __shfl_sync(0xffffffffu, s_Lq, i);
+    const int left = c_run + __shfl_sync(0xffffffffu, s_upto, i) - 1 - n;      // items of the sequence behind it
+    const int piece = ba.x.band_pieces - 1 - left % ba.x.band_pieces;
+    I.g = a.Hkv - 1 - left / ba.x.band_pieces % a.Hkv;
+    I.tok0 = left / per_block * ba.tokens;      // (last block first)
     I.ntok = min(ba.tokens, Lq - I.tok0);
-    if (I.ntok <= 0) return 0;
     I.p0 = I.lk - Lq + I.tok0;
     I.p_last = I.p0 + I.ntok - 1;
     // keys from the first row's band (or window, unless sinks lie in the band before it) on
@@ -164,7 +196,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     const int D0 = I.p0 - HN * I.first;
     I.c_first = floor_div64(D0 + I.ntok - 1);
     I.c_start = max(0, floor_div64(D0 - (HN - 1)));
-    return 1;
+    return true;
   };
   auto finish_item = [&]() {
     if (I.steps == 0) return;
@@ -173,7 +205,6 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     ob += I.c_first + I.steps - I.c_start;          // (a chunk a step)
     ++n_it;
   };
-  const int idx0 = blockIdx.x, idx_step = gridDim.x, n_items = ba.n_items;
 
   // ------------------------------------------------------------ setup
   if (tid == 0) {
@@ -264,10 +295,8 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     if (warp == 0) {
       // ====================================================== r rows, P slices, K tiles
       bool run = true;
-      for (int idx = idx0; idx < n_items && run; idx += idx_step) {
-        const int li = load_item(idx);
-        if (li < 0 && lane == 0) atomicOr(a.err, kDevErrSeqlens);
-        if (li <= 0 || I.steps == 0) continue;
+      for (int n = blockIdx.x; run && next_item(n); n += gridDim.x) {
+        if (I.steps == 0) continue;
         if (n_it > 0 && !(run = wait_parked(bar(B_RT_EMPTY), (n_it - 1) & 1, 61))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(B_RT_FULL), (uint32_t)ba.row_bytes);
@@ -302,8 +331,8 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     } else if (warp == 2) {
       // ====================================================== q rows, V tiles
       bool run = true;
-      for (int idx = idx0; idx < n_items && run; idx += idx_step) {
-        if (load_item(idx) <= 0 || I.steps == 0) continue;
+      for (int n = blockIdx.x; run && next_item(n); n += gridDim.x) {
+        if (I.steps == 0) continue;
         int page = part_page(I.first);
         for (int h = 0; h < 2 && run; ++h) {        // 64 dims of the item's q rows a slot
           const int v = vb + h, st = v % V_STAGES;
@@ -392,8 +421,8 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
         if (s == I.steps - 1) mma_commit_e(bar(B_TAIL));   // (that slot may take the next q rows before it is looked at)
         return true;
       };
-      for (int idx = idx0; idx < n_items && ok; idx += idx_step) {
-        if (load_item(idx) <= 0 || I.steps == 0) continue;
+      for (int n = blockIdx.x; ok && next_item(n); n += gridDim.x) {
+        if (I.steps == 0) continue;
         r_in = false;
         // q rows: two V slots -> TMEM (in order behind the products that read the last ones)
         for (int h = 0; h < 2 && ok; ++h) {
@@ -475,8 +504,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       return true;
     };
     bool ok = true;
-    for (int idx = idx0; idx < n_items && ok; idx += idx_step) {
-      if (load_item(idx) <= 0) continue;
+    for (int n = blockIdx.x; ok && next_item(n); n += gridDim.x) {
       const int tok = I.tok0 + min(row_tok, I.ntok - 1), h = I.g * a.group + a_row % a.group;
       const bool valid = row_tok < I.ntok;
       const int pos = I.p0 + (tok - I.tok0);
@@ -734,9 +762,9 @@ cudaError_t launch_extend_band(const ExtendTcArgs &x, cudaStream_t stream) {
   BandArgs ba = {};
   ba.x = x;
   ba.tokens = extend_band_tokens(a);
-  ba.blocks = (a.max_q + ba.tokens - 1) / ba.tokens;
-  const long items = (long)ba.blocks * a.batch * a.Hkv * x.band_pieces;
-  if (items > 0x7fffffffL) return cudaErrorInvalidValue;
+  const long blocks = std::min<long>((long)a.batch * (((long)a.max_q + ba.tokens - 1) / ba.tokens), a.total_q / ba.tokens + a.batch);
+  const long items = blocks * a.Hkv * x.band_pieces;
+  if (items > 1L << 25) return cudaErrorInvalidValue;        // (q of more than memory holds; 32 sequences' sum fits an int)
   ba.n_items = (int)items;
   ba.box = std::min(extend_box(a), HN);
   const int q_tokens = std::min(ba.tokens, a.total_q);        // a box stays inside the tensor

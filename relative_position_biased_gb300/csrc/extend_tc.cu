@@ -20,8 +20,8 @@
 // and counts of tiles that are no multiple of the SMs leave none idle.  A tile within
 // one share is final; of a cut one each piece leaves a normalised fp32 partial, two a
 // CTA at most, and relattn_extend_join_kernel adds them.  (12 chunks of 4-88 tokens on
-// 6.6k-50k keys: 166 us with ranges of equal length for every tile, 148 so; 4 chunks
-// of 2048 under a window of 4096, 3.4 tiles an SM: 375 and 369.)  The band's row joins
+// 6.6k-50k keys: 166 us with ranges of equal length for every tile, 138 so; 4 chunks
+// of 2048 under a window of 4096, 3.4 tiles an SM: 375 and 364.)  The band's row joins
 // the piece with the nearest keys in its epilogue; where the band comes in pieces
 // itself, all partials are kept by row and relattn_extend_combine_kernel adds them.
 //
@@ -73,8 +73,8 @@ constexpr int B_Q_FULL = 0, B_K_FULL = 1, B_K_EMPTY = B_K_FULL + K_STAGES, B_V_F
 constexpr uint32_t SM_TMEM_SLOT = SM_BAR + B_COUNT * 8;
 constexpr uint32_t SM_ABORT = SM_TMEM_SLOT + 8;
 constexpr uint32_t SM_ITEM = (SM_ABORT + 8 + 15) & ~15u;
-constexpr uint32_t SM_PLAN = SM_ITEM + ITEMS * 80;   // units of every warp's sequences, begin and end of the share
-constexpr uint32_t SM_TOTAL = SM_PLAN + 12 * 8 + 2 * 16;
+constexpr uint32_t SM_PLAN = SM_ITEM + ITEMS * 80;   // units and band items of every warp's sequences, begin and end of the share
+constexpr uint32_t SM_TOTAL = SM_PLAN + 2 * 12 * 8 + 2 * 16;
 constexpr uint32_t SMEM_BYTES = SM_TOTAL + 1024;   // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
@@ -139,8 +139,9 @@ __device__ __forceinline__ long warp_scan(long v) {       // inclusive
 }
 // A warp's walk over the sequences [b0, b1): their units, or with a target (below
 // the units, >= 0) its place as (sequence, pair of row tiles, kv head, steps before
-// it): 0 steps or -1 for all of them, the tile is not cut there.
-__device__ __forceinline__ long walk_units(const ExtendTcArgs &x, int b0, int b1, long target, int4 *at) {
+// it): 0 steps or -1 for all of them, the tile is not cut there.  blocks: token
+// blocks of the band's items.
+__device__ __forceinline__ long walk_units(const ExtendTcArgs &x, int b0, int b1, long target, int4 *at, long &blocks) {
   const int lane = threadIdx.x & 31;
   const long heads = x.a.Hkv;
   long run = 0;
@@ -148,6 +149,7 @@ __device__ __forceinline__ long walk_units(const ExtendTcArgs &x, int b0, int b1
   for (int c0 = b0; c0 < b1; c0 += 32) {
     Seq s{};
     if (c0 + lane < b1) s = load_seq(x, c0 + lane);
+    if (x.band != 0 && s.tiles > 0) blocks += (s.Lq + x.band_tokens - 1) / x.band_tokens;
     long mine = 0;
     if (__reduce_max_sync(0xffffffffu, s.tiles) <= 4) {
 #pragma unroll 1
@@ -232,27 +234,42 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
 
   // ------------------------------------------------------------ the CTA's share
   long *sum = reinterpret_cast<long *>(smem + SM_PLAN);
-  int4 *edge = reinterpret_cast<int4 *>(smem + SM_PLAN + 12 * 8);
+  int4 *edge = reinterpret_cast<int4 *>(smem + SM_PLAN + 2 * 12 * 8);
   const int seq0 = (int)((long)a.batch * warp / 12), seq1 = (int)((long)a.batch * (warp + 1) / 12);
   const long me = blockIdx.x;
-  long mine = 0, before = 0, total = 0, shares = 0;
+  long mine = 0, before = 0, total = 0, shares = 0, early = 0, lead = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {       // the units; the share's first, its end
-    const long target = pass == 0 ? -1 : total * (me + pass - 1) / shares;
+    // the first unit of share c: CTAs from `early` on start `lead` units later
+    const long c = me + pass - 1, late = max(shares - early, 0l);
+    const long target = pass == 0 ? -1 : (total + late * lead) * c / shares - max(c - early, 0l) * lead;
     if (pass == 0 || (target >= before && target < before + mine)) {
-      const long n = walk_units(x, seq0, seq1, pass == 0 ? -1 : target - before, edge + pass - 1);
-      if (pass == 0) mine = n;
+      long blocks = 0;
+      const long n = walk_units(x, seq0, seq1, pass == 0 ? -1 : target - before, edge + pass - 1, blocks);
+      if (pass == 0) {
+        mine = n;
+        early = __reduce_add_sync(0xffffffffu, (int)blocks);
+      }
     } else if (target == total && tid == 0) {
       edge[pass - 1] = make_int4(a.batch, 0, 0, 0);
     }
     if (pass > 0) continue;
-    if (lane == 0) sum[warp] = mine;
+    if (lane == 0) sum[warp] = mine, sum[12 + warp] = early;
     __syncthreads();
+    long items = 0;
     for (int w = 0; w < 12; ++w) {
       if (w < warp) before += sum[w];
       total += sum[w];
+      items += sum[12 + w];
     }
     shares = min((long)gridDim.x, max(total / x.min_share, 1l));
+    // The band's items over its CTAs: this kernel's first CTAs get the SMs that have
+    // one less, the others theirs up to an item later (0, 2/5, 1 of an item's time: 12
+    // chunks of 4-88 tokens, one item an SM at most, 145, 141, 138 us; 4 chunks of 2048
+    // with 6 or 7 366, 362, 372; 3 chunks 297, 289, 291).
+    items *= a.Hkv * x.band_pieces;
+    early = a.sms - items % a.sms;
+    lead = min(items < a.sms ? (long)x.band_units : (long)x.band_units * 2 / 5, total / (2 * shares));
     if (total == 0 || me >= shares) {
       if (tid == 0 && x.cut) x.cut[me] = make_int4(0, 0, 0, 0);
       return;
@@ -404,13 +421,41 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
         if (end) break;
         past = false;
         it.s0 = 0;
-        if (++it.head == a.Hkv) {
-          it.head = 0;
-          for (++tile; tile >= q.tiles;) {
-            tile = 0;
-            if (++it.b >= a.batch) break;
-            q = load_seq(x, it.b);
+        if (++it.head < a.Hkv) continue;
+        // the next tile with steps, 32 tiles or sequences at a time
+        it.head = 0;
+        ++tile;
+        unsigned left = 0;                                 // sequences of the 32 from c0 on that may have one
+        Seq mine = q;
+        int c0 = it.b + 1 - 32;
+        for (;;) {
+          unsigned hit = 0;
+#pragma unroll 1
+          for (; tile < q.tiles && !hit; tile += 32)
+            hit = __ballot_sync(0xffffffffu, tile + lane < q.tiles && tile_units(x, tile + lane, q.Lq, q.Lk) > 0);
+          if (hit) {
+            tile += __ffs(hit) - 1 - 32;
+            break;
           }
+          while (!left && c0 + 32 < a.batch) {
+            c0 += 32;
+            mine = Seq{};
+            if (c0 + lane < a.batch) mine = load_seq(x, c0 + lane);
+            left = __ballot_sync(0xffffffffu, mine.tiles > 1 || (mine.tiles == 1 && tile_units(x, 0, mine.Lq, mine.Lk) > 0));
+          }
+          if (!left) {
+            it.b = a.batch;
+            break;
+          }
+          const int i = __ffs(left) - 1;
+          left &= left - 1;
+          it.b = c0 + i;
+          tile = 0;
+          q.cq = __shfl_sync(0xffffffffu, mine.cq, i);
+          q.ck = __shfl_sync(0xffffffffu, mine.ck, i);
+          q.Lq = __shfl_sync(0xffffffffu, mine.Lq, i);
+          q.Lk = __shfl_sync(0xffffffffu, mine.Lk, i);
+          q.tiles = __shfl_sync(0xffffffffu, mine.tiles, i);
         }
       }
       if (run) {

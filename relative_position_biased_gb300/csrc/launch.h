@@ -83,6 +83,7 @@ struct ExtendTcArgs {
   long min_share;      // units that a share holds at least
   int slots;           // partials by row: the band pieces', then the rest's first piece; 1: none
   int band_pieces, band_steps;   // pieces of a row's band, steps of 64 keys of one
+  int band_tokens, band_units;   // tokens of an item of the band; its time in extend_tc.cu's units (0: not looked at)
   int box, q_bytes;    // (set by the launcher)
   // Two pieces a CTA (fp32 rows of piece_tokens tokens x a group, and their lse): the
   // one that its share starts with, behind a cut, and the one that it ends with,

@@ -36,6 +36,9 @@ def pages(**kw):
     (dict(batch=-1), INVALID), (dict(batch=65536), UNSUPPORTED), (dict(max_seqlen_k=29), INVALID),
     (dict(num_heads_q=65536, num_heads_kv=65536), UNSUPPORTED),
     (dict(max_seqlen_k=(1 << 31) - (1 << 16) + 1), UNSUPPORTED),
+    # out over q (the call reads it on), or over a part of k, v or r
+    (dict(out=A), INVALID), (dict(out=A + 40 * 8 * 256 - 16), INVALID), (dict(k=8 * A - 600 * 2 * 256 + 256), INVALID),
+    (dict(v=8 * A + 512), INVALID), (dict(r=8 * A - 16), INVALID),
 ])
 def test_extend_refuses_parameters(kw, want):
     assert rpb.relattn_extend(fwd(**kw)) == want
