@@ -399,7 +399,7 @@ struct ExtendPlan {
 relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, int32_t sink, KernelArgs *a) {
   const relattn_status st = make_args(p, a);
   if (st != RELATTN_OK) return st;
-  a->sink = a->window > 0 ? sink : 0;
+  a->sink = a->window > 0 ? std::min(sink, p->max_seqlen_k) : 0;      // (rounded up to tiles below)
   a->kv_rows = kv ? kv->num_pages * kv->page_size : p->total_k;
   if (kv) {
     a->block_table = kv->block_table;

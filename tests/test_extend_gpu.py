@@ -152,6 +152,20 @@ def test_shares_of_many_sequences(few_ctas):
         check(U.Case(q_lens, k_lens, 8, 1, r_dim=16, E=64, page=16, seed=2))
 
 
+@pytest.mark.parametrize("q_len,num_splits", [(1, 0), (1, 1), (1, 3), (40, 0), (40, 1), (300, 0)])
+@pytest.mark.parametrize("rd", [16, 7])                     # (7: the kernel of any shape)
+def test_the_largest_window_and_number_of_sinks(q_len, num_splits, rd):
+    top = 2 ** 31 - 1
+    c = U.Case((q_len, 1), (900, 50), 8, 2, r_dim=rd, E=64, window=100, page=16, seed=1)
+    d = U.make(c)
+    a = call(c, d, top, num_splits=num_splits)
+    b = call(c, d, 900, num_splits=num_splits)
+    ok()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check(c, 900, num_splits=num_splits)
+    check(U.Case((q_len, 1), (900, 50), 8, 2, r_dim=rd, E=64, window=top, page=16, seed=1), top, num_splits=num_splits)
+
+
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("base", [0.0, 16.0])
 @pytest.mark.parametrize("q_lens,k_lens", [((1, 1), (90, 300)), ((40, 300), (90, 300))])
