@@ -369,6 +369,51 @@ def test_calls_repeat_bit_for_bit_on_any_stream(q_lens):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_random_batches_are_prefills():
+    """Contiguous and paged, mixed lengths and kernels: relattn_prefill's out and
+    lse.  Each is within 2^-8 (2 sum p |v| + |out|) <= 2^-8 3 max |v| of the exact
+    out (P and out in bf16), and lse within 256 2^-24 of a logit's products."""
+    rng = np.random.default_rng(12)
+    for n in range(28):
+        Hq, Hkv = [(16, 2), (8, 1), (4, 4), (12, 4), (20, 1), (6, 6)][n % 6]
+        kind, E = n % 4, int(rng.choice([0, 64, 520, 1024]))
+        b = (3, 200, 20, 1)[kind]
+        q_lens = rng.integers(0, (900, 4, 2, 200)[kind], b) + (kind == 3)
+        if kind == 2:
+            q_lens[rng.integers(b)] = rng.integers(1, 1500)
+        k_lens = q_lens + rng.integers(0, (3000, 300, 5000, 20000)[kind], b)
+        if q_lens.sum() == 0:
+            continue
+        c = U.Case(tuple(q_lens.tolist()), tuple(k_lens.tolist()), Hq, Hkv, r_dim=16 if E else 0, E=E, page=int(rng.choice([16, 48, 128])),
+                   window=int(rng.choice([0, 0, 90, 2000])), base=float(rng.choice([0, 16])), seed=n)
+        d = U.make(c)
+        at = torch.from_numpy(np.concatenate(d["where"]).astype(np.int64))
+        t = {m: U.cuda(d[m]) for m in ("q", "r", "P", "cu_q", "cu_k")}
+        k, v = d["k"][at].cuda(), d["v"][at].cuda()
+        kw = dict(max_seqlen_q=int(q_lens.max()), max_seqlen_k=int(k_lens.max()), alpha=c.alpha, window=c.window, log_scale_base=c.base)
+        want = rpb.prefill(t["q"], k, v, t["r"], t["P"], t["cu_q"], t["cu_k"], **kw)
+        num_splits = int(rng.choice([0, 0, 1, 3]))
+        for got in (rpb.extend(t["q"], k, v, t["r"], t["P"], t["cu_q"], t["cu_k"], num_splits=num_splits, **kw),
+                    call(c, d, 0, num_splits=num_splits)):
+            ok()
+            assert (got[0].float() - want[0].float()).abs().max() <= 2 * 2.0 ** -8 * 3 * v.abs().max().float(), n
+            assert (got[1] - want[1]).abs().max() <= 2 * 256 * 2.0 ** -24 * 200, n      # (products of a logit: below 200 here)
+
+
+@pytest.mark.parametrize("q_lens,k_lens,window,num_splits", [
+    ((1, 1), (5000, 40), 0, 0), ((300, 5, 70), (3000, 2900, 600), 0, 0), ((1300, 40), (4000, 40), 0, 0), ((1300, 40), (4000, 40), 500, 3),
+    ((200, 100), (200, 100), 0, 1),
+])
+def test_a_workspace_may_hold_anything(q_lens, k_lens, window, num_splits):
+    c = U.Case(q_lens, k_lens, 16, 2, r_dim=16, E=128, window=window, page=16, seed=4)
+    d = U.make(c)
+    a = call(c, d, 4, num_splits=num_splits)
+    for fill in (0, 255, 1):
+        b = call(c, d, 4, num_splits=num_splits, workspace=torch.full((1 << 27,), fill, dtype=torch.uint8, device="cuda"))
+        ok()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 # ------------------------------------------------------------------ gradients
 
 def grads(c, sink):
@@ -410,6 +455,21 @@ def test_gradients(Hq, Hkv, rd, E, window, sink, q_lens, k_lens):
     check_grads(U.Case(q_lens, k_lens, Hq, Hkv, r_dim=rd, E=E, window=window, seed=sink), sink)
 
 
+@pytest.mark.parametrize("Hq,Hkv,rd,E", [(16, 2, 64, 1024), (4, 4, 0, 0), (20, 1, 16, 128)])
+@pytest.mark.parametrize("window", [1, 70, 600])
+@pytest.mark.parametrize("q_lens,k_lens", [((1000, 3, 0, 250), (1000, 900, 20, 251)), ((7,) * 150, (7, 30, 300) * 50)])
+def test_gradients_of_sinks_that_are_all_keys_need_no_window(Hq, Hkv, rd, E, window, q_lens, k_lens):
+    """Both sums are over the same pairs, in another order; each gradient is within
+    2^-7 of the exact one's norm (the library's bound for relattn_backward)."""
+    d, out, lse, dout, args, kw = grads(U.Case(q_lens, k_lens, Hq, Hkv, r_dim=rd, E=E, seed=window), 0)
+    a = rpb.backward(*args, **kw)
+    b = rpb.backward(*args, **dict(kw, window=window), sink=1024)
+    ok()
+    for x, y in zip(a, b):
+        if x is not None:
+            assert (x.float() - y.float()).norm() <= 2 * 2.0 ** -7 * x.float().norm()
+
+
 def test_gradients_of_inconsistent_lengths_leave_the_sequence_out():
     c = U.Case((60, 90, 50), (60, 90, 50), 8, 2, r_dim=16, E=64, window=20)
     d, out, lse, dout, args, kw = grads(c, 3)
@@ -440,6 +500,15 @@ def test_gradients_captured_and_replayed():
     g.replay()
     ok()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_a_workspace_of_gradients_may_hold_anything():
+    d, out, lse, dout, args, kw = grads(U.Case((300, 120), (300, 200), 8, 2, r_dim=16, E=128, window=40), 30)
+    a = rpb.backward(*args, sink=30, **kw)
+    for fill in (0, 255):
+        b = rpb.backward(*args, sink=30, workspace=torch.full((1 << 26,), fill, dtype=torch.uint8, device="cuda"), **kw)
+        ok()
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_gradients_log_scale_and_longer():
