@@ -429,6 +429,7 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
   x.min_share = std::max<long>(kMinShare, p->num_splits > 1 ? (units + p->num_splits - 2) / (p->num_splits - 1) : 0);
   x.ctas = (int)std::min<long>(a.sms, std::max<long>((pairs * units + x.min_share - 1) / x.min_share, 1));
   x.piece_tokens = std::min(2 * x.tokens, a.max_q);
+  x.out32 = aligned(a.out, 32) ? 1 : 0;
   // the band, in pieces where its items leave more than half of the SMs idle (a bias of
   // 1024: 200 tokens on 32768 keys 84 us, 101 in one piece; on 2000 keys 52 and 60; 600
   // tokens on 8192 keys, whose items take every second SM, 89 in two and 84 in one)

@@ -663,21 +663,24 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
           const int e = min(max((int)(__float_as_uint(row_max(top)) >> 23) - 127, -100), 127);
           const float down = __uint_as_float((uint32_t)(14 - e + 127) << 23);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __half2 hv = __floats2half2_rn(o[8 * i + 2 * k] * down, o[8 * i + 2 * k + 1] * down);
+            for (int k = 0; k < 8; ++k) {
+              const __half2 hv = __floats2half2_rn(o[16 * i + 2 * k] * down, o[16 * i + 2 * k + 1] * down);
               w[k] = *reinterpret_cast<const uint32_t *>(&hv);
             }
-            if (valid) dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (valid) store32(dst + 2 * i, w, ba.x.out32);
           }
           if (valid) ba.x.carry[2 * qrow + wg] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
         } else if (valid) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
+            store32(dst + 2 * i, w, ba.x.out32);
+          }
         }
       }
       tc_fence_before();                         // (before the next item's first P is handed over)

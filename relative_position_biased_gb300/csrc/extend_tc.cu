@@ -805,9 +805,12 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
         } else if (valid) {
           uint4 *dst = reinterpret_cast<uint4 *>(a.out + qrow * kHeadDim + 32 * c);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
+            store32(dst + 2 * i, w, x.out32);
+          }
         }
       }
       tc_fence_before();                         // (before the next item's first P is handed over)

@@ -85,6 +85,7 @@ struct ExtendTcArgs {
   int band_pieces, band_steps;   // pieces of a row's band, steps of 64 keys of one
   int band_tokens, band_units;   // tokens of an item of the band; its time in extend_tc.cu's units (0: not looked at)
   int box, q_bytes;    // (set by the launcher)
+  int out32;           // out is aligned to 32 bytes
   // Two pieces a CTA (fp32 rows of piece_tokens tokens x a group, and their lse): the
   // one that its share starts with, behind a cut, and the one that it ends with,
   // before a cut; cut[i] = (sequence, pair of row tiles, kv head, steps before it) of
@@ -122,6 +123,18 @@ __device__ __forceinline__ ExtendTiles extend_tiles(const ExtendTcArgs &x, int t
   t.n_sink = min((t.far + 127) / 128, t.w_lo);
   t.n_all = t.n_sink + max(0, w_hi - t.w_lo);
   return t;
+}
+// 32 bytes a thread in one access where the address allows it (a row of a thread's
+// own: half as many passes over the lines as with 16)
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8], bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 cudaError_t launch_extend_main(const ExtendTcArgs &x, cudaStream_t stream);
 cudaError_t launch_extend_band(const ExtendTcArgs &x, cudaStream_t stream);
