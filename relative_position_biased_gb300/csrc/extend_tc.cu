@@ -21,7 +21,7 @@
 // one share is final; of a cut one each piece leaves a normalised fp32 partial, two a
 // CTA at most, and relattn_extend_join_kernel adds them.  (12 chunks of 4-88 tokens on
 // 6.6k-50k keys: 166 us with ranges of equal length for every tile, 138 so; 4 chunks
-// of 2048 under a window of 4096, 3.4 tiles an SM: 375 and 364.)  The band's row joins
+// of 2048 under a window of 4096, 3.4 tiles an SM: 375 and 362.)  The band's row joins
 // the piece with the nearest keys in its epilogue; where the band comes in pieces
 // itself, all partials are kept by row and relattn_extend_combine_kernel adds them.
 //
