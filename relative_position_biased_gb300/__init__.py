@@ -1176,23 +1176,30 @@ def _prologue_paged(q, k, v, conv_k, conv_v, norm_q, norm_k, cu_seqlens_q, cu_se
             return _prologue_paged(q, k, v, conv_k, conv_v, norm_q, norm_k, cu_seqlens_q, cu_seqlens_k, k_pool, v_pool, eps,
                                    q_out, conv_state_in, conv_state_out, mxfp8, block_table, page_size, None)
     Tq, Hq, _ = _shape(q, "q", 3, HEAD_DIM)
-    H = int(_shape(k, "k", 3, HEAD_DIM)[1])
-    rows = int(_shape(k_pool, "k_cache", 3, H, HEAD_DIM)[0])
+    rows, H, _ = pool = _shape(k_pool, "k_cache", 3, HEAD_DIM)
+    C = H * HEAD_DIM
+    new, taps, gain = (Tq, H, HEAD_DIM), (C, 4), (HEAD_DIM,)
     batch, cq, ck = _lengths(cu_seqlens_q, cu_seqlens_k, "cu_seqlens_q", "cu_seqlens_k", dev)
     pages = _pages(block_table, page_size, rows, dev, batch)
+    qp = _address(q, "q", bf16, dev)
     if q_out is None:
         q_out = torch.empty_like(q)
-    states = [None] * 4
-    for i, (pair, name) in enumerate(((conv_state_in, "conv_state_in"), (conv_state_out, "conv_state_out"))):
-        if pair is not None:
-            states[2 * i:2 * i + 2] = [None if t is None else _tensor(t, name, bf16, (batch, 3, H * HEAD_DIM), dev)
-                                       for t in pair]
+        op = q_out.data_ptr()
+    else:
+        op = _tensor(q_out, "q_out", bf16, (Tq, Hq, HEAD_DIM), dev)
+
+    def state(pair, name):
+        if pair is None:
+            return None, None
+        a, b = pair
+        s = (batch, 3, C)
+        return None if a is None else _tensor(a, name, bf16, s, dev), None if b is None else _tensor(b, name, bf16, s, dev)
     prm = RelattnPrologueParams(
-        _address(q, "q", bf16, dev), _tensor(k, "k", bf16, (Tq, H, HEAD_DIM), dev), _tensor(v, "v", bf16, (Tq, H, HEAD_DIM), dev),
-        _tensor(conv_k, "conv_k", f32, (H * HEAD_DIM, 4), dev), _tensor(conv_v, "conv_v", f32, (H * HEAD_DIM, 4), dev),
-        _tensor(norm_q, "norm_q", f32, (HEAD_DIM,), dev), _tensor(norm_k, "norm_k", f32, (HEAD_DIM,), dev), eps,
-        cq, ck, batch, Tq, 0, Hq, H, HEAD_DIM, _tensor(q_out, "q_out", bf16, (Tq, Hq, HEAD_DIM), dev),
-        _address(k_pool, "k_cache", bf16, dev), _tensor(v_pool, "v_cache", bf16, (rows, H, HEAD_DIM), dev), *states)
+        qp, _tensor(k, "k", bf16, new, dev), _tensor(v, "v", bf16, new, dev), _tensor(conv_k, "conv_k", f32, taps, dev),
+        _tensor(conv_v, "conv_v", f32, taps, dev), _tensor(norm_q, "norm_q", f32, gain, dev),
+        _tensor(norm_k, "norm_k", f32, gain, dev), eps, cq, ck, batch, Tq, 0, Hq, H, HEAD_DIM, op,
+        _address(k_pool, "k_cache", bf16, dev), _tensor(v_pool, "v_cache", bf16, pool, dev),
+        *state(conv_state_in, "conv_state_in"), *state(conv_state_out, "conv_state_out"))
     _check((_lib or load_library()).relattn_prologue_paged(ctypes.byref(prm), ctypes.byref(pages), st),
            "relattn_prologue_paged")
     return q_out

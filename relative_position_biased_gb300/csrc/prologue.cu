@@ -624,6 +624,10 @@ cudaError_t launch_prologue(const relattn_prologue_params *p, int *err, int sms,
   const uint32_t tok_bytes = (uint32_t)(a.Hq + 2 * a.Hkv) * kHeadDim * 2;
   int T = (int)(kTargetStageBytes / tok_bytes);
   T = T < 1 ? 1 : (T > kMaxTileTokens ? kMaxTileTokens : T);
+  // few tokens: tiles for all SMs (64 single tokens of Hq 16 / Hkv 2 in tiles of 8 took
+  // 15.6 us, one a tile 8.1; 256 of them 17.9 and 10.4)
+  const int share = (a.total_q + (sms > 0 ? sms : 1) - 1) / (sms > 0 ? sms : 1);
+  if (T > share && share > 0) T = share;
   const size_t stage_bytes = (size_t)T * a.Hq * kHeadDim * 2 + 2 * (size_t)(T + kHalo) * a.Hkv * kHeadDim * 2;
   const size_t smem = kWeightOffset + 2 * kTaps * (size_t)a.Hkv * kHeadDim * 4 + kStages * stage_bytes;
   if (rows > 0 && smem <= kPrologueMaxSmem) {
