@@ -199,6 +199,9 @@ relattn_status relattn_decode_paged(const relattn_params *params, const relattn_
  * out and lse; keys past max_seqlen_k or rows outside the arrays skip the
  * sequence and record RELATTN_ERR_DEVICE_ARGS.  max_seqlen_k up to 2^31 - 2^16;
  * batch and num_heads_q up to 65535.
+ * num_splits: 0 lets the library cut a row's keys as it sees fit; n > 0 allows at
+ * most n partials of a row (1: none).  total_k (with pages the sum of the key
+ * counts) is used for planning only.
  * Workspace: relattn_extend_workspace_size() bytes of the same params, pages
  * and sink, 16-byte aligned; its contents are scratch, so calls that may run at
  * the same time need one each.

@@ -413,7 +413,9 @@ relattn_status extend_args(const relattn_params *p, const relattn_paged_kv *kv, 
 // The tcgen05 kernels of many rows: CTAs that share the keys before the band,
 // pieces of the band, and the partials that both leave.
 void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *plan) {
-  constexpr long kTile = kTcKeyTile, kMinShare = 72;      // units: 6 a step of a pair of row tiles, 21 a piece (extend_tc.cu)
+  // A share has at least 5 steps of a pair of row tiles (6 units each, extend_tc.cu):
+  // 40 tokens on 8192 keys 39 us, with 12 steps 50; 200 on 2000 keys 42 and 54
+  constexpr long kTile = kTcKeyTile, kMinShare = 30;
   ExtendTcArgs &x = plan->tc;
   x.a = a;
   const bool bias = a.rd > 0 && a.E > 0;
@@ -430,9 +432,11 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
   x.ctas = (int)std::min<long>(a.sms, std::max<long>((pairs * units + x.min_share - 1) / x.min_share, 1));
   x.piece_tokens = std::min(2 * x.tokens, a.max_q);
   x.out32 = aligned(a.out, 32) ? 1 : 0;
-  // the band, in pieces where its items leave more than half of the SMs idle (a bias of
-  // 1024: 200 tokens on 32768 keys 84 us, 101 in one piece; on 2000 keys 52 and 60; 600
-  // tokens on 8192 keys, whose items take every second SM, 89 in two and 84 in one)
+  // the band, in pieces of 6 steps and more where its items leave more than half of the
+  // SMs idle (a bias of 1024: 200 tokens on 32768 keys 84 us, 101 in one piece; on 2000
+  // keys 52 and 60; 600 tokens on 8192 keys, whose items take every second SM, 89 in two
+  // and 84 in one; pieces of 4 steps: 200 tokens on 2000 keys 48 for 42, 8 x 20 on 2500
+  // keys 50 for 37)
   x.band = bias ? 1 : 0;
   x.band_pieces = 1;
   x.band_steps = 0;
@@ -440,7 +444,7 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
     const int tokens = extend_band_tokens(a);
     const long steps = ((long)a.E + tokens + 126) / 64 + 3;        // at most, of a row block
     const long items = std::min<long>((long)a.batch * (((long)a.max_q + tokens - 1) / tokens), a.total_q / tokens + a.batch) * a.Hkv;
-    if (p->num_splits <= 0 && 2 * items < a.sms) x.band_pieces = (int)std::max<long>(1, std::min<long>(a.sms / items, steps / 4));
+    if (p->num_splits <= 0 && 2 * items < a.sms) x.band_pieces = (int)std::max<long>(1, std::min<long>(a.sms / items, steps / 6));
     x.band_steps = (int)((steps + x.band_pieces - 1) / x.band_pieces);
     x.band_tokens = tokens;
     // (24 us for the 17 steps of a bias of 1024, 6 of them its start and end)
