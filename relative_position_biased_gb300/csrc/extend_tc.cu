@@ -744,15 +744,15 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
     const size_t qrow = (size_t)(it->cq + tok) * a.Hq + h, lrow = (size_t)h * a.total_q + it->cq + tok;
     const bool by_row = x.slots > 1 && s0 == 0, own = !by_row && !(x.slots <= 1 && it->whole);
     const bool join = x.band != 0 && x.slots <= 1 && s0 == 0;
-    uint4 band[4] = {};                          // the next 32 dims of it
-    const uint4 *src = reinterpret_cast<const uint4 *>(a.out + qrow * kHeadDim);
+    uint32_t band[2][8] = {};                    // the next 32 dims of it
+    const __nv_bfloat16 *src = a.out + qrow * kHeadDim;
     float band_lse = -INFINITY;
     float2 ups = make_float2(0.f, 0.f);
     if (join) {
       if (!band_done) asm volatile("griddepcontrol.wait;" ::: "memory");
       band_done = true;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) band[i] = src[i];
+      for (int i = 0; i < 2; ++i) load32(src + 16 * i, band[i], x.out32);
       band_lse = a.lse[lrow];
       ups = reinterpret_cast<const float2 *>(x.carry)[qrow];
     }
@@ -787,15 +787,14 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
         if (join) {
           const float up = c < 2 ? ups.x : ups.y;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t pr[4] = {band[i].x, band[i].y, band[i].z, band[i].w};
-            if (c < 3) band[i] = src[4 * (c + 1) + i];
+          for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pr[k]));
-              o[8 * i + 2 * k] = fmaf(f.x, up, o[8 * i + 2 * k]);
-              o[8 * i + 2 * k + 1] = fmaf(f.y, up, o[8 * i + 2 * k + 1]);
+            for (int k = 0; k < 8; ++k) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&band[i][k]));
+              o[16 * i + 2 * k] = fmaf(f.x, up, o[16 * i + 2 * k]);
+              o[16 * i + 2 * k + 1] = fmaf(f.y, up, o[16 * i + 2 * k + 1]);
             }
+            if (c < 3) load32(src + 32 * (c + 1) + 16 * i, band[i], x.out32);
           }
         }
         if (valid && (by_row || own)) {

@@ -136,6 +136,17 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8], bool wh
     reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
 }
+__device__ __forceinline__ void load32(const void *p, uint32_t (&v)[8], bool whole) {
+  if (whole) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
 cudaError_t launch_extend_main(const ExtendTcArgs &x, cudaStream_t stream);
 cudaError_t launch_extend_band(const ExtendTcArgs &x, cudaStream_t stream);
 int extend_band_tokens(const KernelArgs &a);   // of a work item
