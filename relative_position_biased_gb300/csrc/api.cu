@@ -454,13 +454,13 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
   x.slots = x.band_pieces > 1 ? x.band_pieces + 1 : 1;
   // workspace: partials by row (or the carry), the CTAs' pieces, their cuts
   const size_t rows = (size_t)a.total_q * a.Hq, piece_rows = 2 * (size_t)x.ctas * x.piece_tokens * a.group;
-  const auto up16 = [](size_t n) { return (n + 15) / 16 * 16; };
+  const auto up32 = [](size_t n) { return (n + 31) / 32 * 32; };
   plan->lse_offset = x.slots > 1 ? x.slots * rows * kHeadDim * sizeof(float) : 0;
-  plan->piece_offset = up16(x.slots > 1 ? plan->lse_offset + x.slots * rows * sizeof(float) : bias ? rows * 2 * sizeof(float) : 0);
+  plan->piece_offset = up32(x.slots > 1 ? plan->lse_offset + x.slots * rows * sizeof(float) : bias ? rows * 2 * sizeof(float) : 0);
   plan->ws_bytes = plan->piece_offset;
   plan->partials = x.slots;
   if (p->num_splits != 1 && (x.ctas > 1 || x.slots > 1)) {
-    plan->cut_offset = up16(plan->piece_offset + piece_rows * (kHeadDim + 1) * sizeof(float));
+    plan->cut_offset = up32(plan->piece_offset + piece_rows * (kHeadDim + 1) * sizeof(float));
     plan->ws_bytes = plan->cut_offset + x.ctas * sizeof(int4);
     plan->partials += (int)(x.ctas / std::max<long>(pairs, 1)) + 1;
   }
@@ -500,6 +500,7 @@ relattn_status plan_extend(const relattn_params *p, const KernelArgs &a, ExtendP
 relattn_status run_extend_tc(const relattn_params *p, ExtendPlan &plan, cudaStream_t s) {
   ExtendTcArgs &x = plan.tc;
   char *ws = static_cast<char *>(p->workspace);
+  x.part32 = aligned(ws, 32) ? 1 : 0;
   if (x.slots > 1) {
     x.a.o_part = reinterpret_cast<float *>(ws);
     x.a.lse_part = reinterpret_cast<float *>(ws + plan.lse_offset);

@@ -645,9 +645,14 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       for (int i = 0; i < 64; ++i) o[i] *= inv;
       if (partial) {
         if (valid) {
-          float4 *dst = reinterpret_cast<float4 *>(a.o_part + part_row * kHeadDim + 64 * wg);
+          float *dst = a.o_part + part_row * kHeadDim + 64 * wg;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) {
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * i + k]);
+            store32(dst + 8 * i, v, ba.x.part32);
+          }
         }
       } else {
         // the row is done, or goes on over the keys before the band: then as f16,

@@ -21,7 +21,7 @@
 // one share is final; of a cut one each piece leaves a normalised fp32 partial, two a
 // CTA at most, and relattn_extend_join_kernel adds them.  (12 chunks of 4-88 tokens on
 // 6.6k-50k keys: 166 us with ranges of equal length for every tile, 138 so; 4 chunks
-// of 2048 under a window of 4096, 3.4 tiles an SM: 375 and 362.)  The band's row joins
+// of 2048 under a window of 4096, 3.4 tiles an SM: 375 and 357.)  The band's row joins
 // the piece with the nearest keys in its epilogue; where the band comes in pieces
 // itself, all partials are kept by row and relattn_extend_combine_kernel adds them.
 //
@@ -798,9 +798,14 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
           }
         }
         if (valid && (by_row || own)) {
-          float4 *dst = reinterpret_cast<float4 *>(part + at * kHeadDim + 32 * c);
+          float *dst = part + at * kHeadDim + 32 * c;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * i + k]);
+            store32(dst + 8 * i, v, x.part32);
+          }
         } else if (valid) {
           uint4 *dst = reinterpret_cast<uint4 *>(a.out + qrow * kHeadDim + 32 * c);
 #pragma unroll

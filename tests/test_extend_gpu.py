@@ -414,6 +414,22 @@ def test_a_workspace_may_hold_anything(q_lens, k_lens, window, num_splits):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("q_lens,k_lens,num_splits", [((1, 1), (5000, 40), 0), ((300, 5, 70), (3000, 2900, 600), 0),
+                                                      ((1300, 40), (4000, 40), 0), ((300, 40), (4000, 600), 1), ((5,), (60,), 0)])
+def test_out_and_workspace_of_sixteen_byte_alignment(q_lens, k_lens, num_splits):
+    c = U.Case(q_lens, k_lens, 16, 2, r_dim=16, E=128, page=16, seed=4)
+    d = U.make(c)
+    a = call(c, d, 0, num_splits=num_splits)
+    n = sum(q_lens) * 16 * 128
+    out = torch.full((n + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty((1 << 27) + 16, dtype=torch.uint8, device="cuda")[16:]
+    mine = out[8:8 + n].view(sum(q_lens), 16, 128)
+    assert mine.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+    b = call(c, d, 0, num_splits=num_splits, out=mine, workspace=ws)
+    ok()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and (out[:8] == 7).all() and (out[8 + n:] == 7).all()
+
+
 # ------------------------------------------------------------------ gradients
 
 def grads(c, sink):
