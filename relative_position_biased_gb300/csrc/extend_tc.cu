@@ -20,7 +20,7 @@
 // and counts of tiles that are no multiple of the SMs leave none idle.  A tile within
 // one share is final; of a cut one each piece leaves a normalised fp32 partial, two a
 // CTA at most, and relattn_extend_join_kernel adds them.  (12 chunks of 4-88 tokens on
-// 6.6k-50k keys: 166 us with ranges of equal length for every tile, 138 so; 4 chunks
+// 6.6k-50k keys: 166 us with ranges of equal length for every tile, 131 so; 4 chunks
 // of 2048 under a window of 4096, 3.4 tiles an SM: 375 and 357.)  The band's row joins
 // the piece with the nearest keys in its epilogue; where the band comes in pieces
 // itself, all partials are kept by row and relattn_extend_combine_kernel adds them.
@@ -957,14 +957,14 @@ __global__ void __launch_bounds__(256) relattn_extend_combine_kernel(const __gri
 
 // The same for the rows of the tiles that shares cut, whose partials are the pieces
 // before the first cut and behind each: a row of blocks for every share's start,
-// which ends at once unless that is a tile's first cut.  A warp takes JROWS rows, so
-// that their loads are in flight together (two pieces a row as a rule).
-constexpr int JROWS = 4;
+// which ends at once unless that is a tile's first cut.  A warp a row: a chain of
+// loads (two pieces a row as a rule), which many short warps hide best until their
+// instructions fill the issue slots (78 %): 12 chunks of 4-88 tokens on 6.6k-50k keys
+// take 131 us, with two rows a warp 133, four 137, eight 153.
 __global__ void __launch_bounds__(256) relattn_extend_join_kernel(const __grid_constant__ ExtendTcArgs x) {
   const KernelArgs &a = x.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = blockIdx.x + 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (a tile has at most 32 cuts a round of the loop below)
   const int4 c = x.cut[share], next = x.cut[min(share + lane, x.ctas - 1)];
   if (c.w <= 0 || same_tile(c, x.cut[share - 1])) return;
   int n = 1;                                     // partials: the piece before the cut, those behind
@@ -974,47 +974,33 @@ __global__ void __launch_bounds__(256) relattn_extend_join_kernel(const __grid_c
     n += k;
     if (k < 32) break;
   }
-  const int cq = a.cu_q[c.x], Lq = a.cu_q[c.x + 1] - cq, tok0 = 2 * x.tokens * c.y;
-  const int rows = min(x.piece_tokens, Lq - tok0) * a.group, r0 = (blockIdx.y * 8 + warp) * JROWS;
-  if (r0 >= rows) return;
+  const int cq = a.cu_q[c.x], tok0 = 2 * x.tokens * c.y, r = blockIdx.y * 8 + warp;
+  if (r >= min(x.piece_tokens, a.cu_q[c.x + 1] - cq - tok0) * a.group) return;
   const long stride = (long)x.piece_tokens * a.group;
-  const long first = (long)(2 * (share - 1) + 1) * stride, behind = (long)(2 * share) * stride;
-  float m[JROWS], z[JROWS];
-  float4 acc[JROWS];
-#pragma unroll
-  for (int k = 0; k < JROWS; ++k) {
-    m[k] = -INFINITY, z[k] = 0.f;
-    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  const long first = (long)(2 * (share - 1) + 1) * stride + r, behind = (long)(2 * share) * stride + r;
+  float m = -INFINITY, z = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
   for (int s = 0; s < n; ++s) {
     const long at = s == 0 ? first : behind + 2 * stride * (s - 1);
-#pragma unroll
-    for (int k = 0; k < JROWS; ++k) {
-      const long r = at + min(r0 + k, rows - 1);
-      const float ls = x.piece_lse[r];
-      const float4 v = *reinterpret_cast<const float4 *>(x.piece + r * kHeadDim + lane * 4);
-      const float top = fmaxf(m[k], ls), old = m[k] == -INFINITY ? 0.f : exp2f((m[k] - top) * kLog2e);
-      const float w = ls == -INFINITY ? 0.f : exp2f((ls - top) * kLog2e);
-      m[k] = top;
-      z[k] = fmaf(z[k], old, w);
-      acc[k].x = fmaf(acc[k].x, old, w * v.x);
-      acc[k].y = fmaf(acc[k].y, old, w * v.y);
-      acc[k].z = fmaf(acc[k].z, old, w * v.z);
-      acc[k].w = fmaf(acc[k].w, old, w * v.w);
-    }
+    const float ls = x.piece_lse[at];
+    const float4 v = *reinterpret_cast<const float4 *>(x.piece + at * kHeadDim + lane * 4);
+    const float top = fmaxf(m, ls), old = m == -INFINITY ? 0.f : exp2f((m - top) * kLog2e);
+    const float w = ls == -INFINITY ? 0.f : exp2f((ls - top) * kLog2e);
+    m = top;
+    z = fmaf(z, old, w);
+    acc.x = fmaf(acc.x, old, w * v.x);
+    acc.y = fmaf(acc.y, old, w * v.y);
+    acc.z = fmaf(acc.z, old, w * v.z);
+    acc.w = fmaf(acc.w, old, w * v.w);
   }
-#pragma unroll
-  for (int k = 0; k < JROWS; ++k) {
-    const int r = r0 + k, t = cq + tok0 + r / a.group, h = c.z * a.group + r % a.group;
-    if (r >= rows) break;
-    const float inv = z[k] == 0.f ? 0.f : 1.f / z[k];
-    uint2 packed;
-    packed.x = pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
-    packed.y = pack_bf16x2(acc[k].z * inv, acc[k].w * inv);
-    *reinterpret_cast<uint2 *>(a.out + ((long)t * a.Hq + h) * kHeadDim + lane * 4) = packed;
-    if (lane == 0) a.lse[(long)h * a.total_q + t] = z[k] == 0.f ? -INFINITY : m[k] + logf(z[k]);
-  }
+  const int t = cq + tok0 + r / a.group, h = c.z * a.group + r % a.group;
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  uint2 packed;
+  packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2 *>(a.out + ((long)t * a.Hq + h) * kHeadDim + lane * 4) = packed;
+  if (lane == 0) a.lse[(long)h * a.total_q + t] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -1085,7 +1071,7 @@ cudaError_t launch_extend_combine(const ExtendTcArgs &x, int partials, cudaStrea
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (x.slots <= 1) {
-    cfg.gridDim = dim3((unsigned)x.ctas - 1, (unsigned)((x.piece_tokens * a.group + 8 * JROWS - 1) / (8 * JROWS)));
+    cfg.gridDim = dim3((unsigned)x.ctas - 1, (unsigned)((x.piece_tokens * a.group + 7) / 8));
     return cudaLaunchKernelEx(&cfg, relattn_extend_join_kernel, x);
   }
   cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
