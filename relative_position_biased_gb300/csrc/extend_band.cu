@@ -21,7 +21,9 @@
 // then 32 loads at constant offsets from one address.  A row is read and written
 // by the two threads that share it, so their two warps meet, not the CTA.
 // A step adds 64 distances and needs those of 64 keys and the block's tokens: 160
-// hold up to 32 tokens (groups of 4 and more: 128 rows), 192 up to 64.
+// hold up to 32 tokens (groups of 4 and more: 128 rows), 192 up to 64.  From step to
+// step a row's two threads have met before either writes again; at an item's start they
+// have not, and what both would write to the same place is written once (extend_ring.h).
 //
 // The list of items is counted from the lengths on the device, so that a batch whose
 // sequences are far shorter than the longest has no empty ones (4096 tokens of one
@@ -47,6 +49,7 @@
 
 #include <algorithm>
 
+#include "extend_ring.h"
 #include "launch.h"
 #include "tc_common.cuh"
 
@@ -101,8 +104,6 @@ struct Item {
   int slot;
   int c_start, c_first;   // r.P chunks: the oldest that step 0 reads, the newest
 };
-
-__device__ __forceinline__ int floor_div64(int x) { return x >> 6; }
 
 template <int N>
 __device__ __forceinline__ float row_max(const float (&x)[N]) {
@@ -194,8 +195,9 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     I.steps = min(ba.x.band_steps, max(0, I.first - low + 1));
     I.slot = piece;
     const int D0 = I.p0 - HN * I.first;
-    I.c_first = floor_div64(D0 + I.ntok - 1);
-    I.c_start = max(0, floor_div64(D0 - (HN - 1)));
+    const BandChunks chunks = band_chunks(D0, I.ntok);
+    I.c_first = chunks.first;
+    I.c_start = chunks.start;
     return true;
   };
   auto finish_item = [&]() {
@@ -493,7 +495,8 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       tmem_wait_ld(w);
       tc_fence_before();
       mbar_arrive(bar(B_R_FREE + (o & 1)));
-      const int slot = (2 * o + wg) % L::SLOTS;
+      if (!band_stored(c, wg, I.c_first, L::SLOTS)) return true;
+      const int slot = band_slot(o, wg, L::SLOTS);
       float *dst = ring + slot * 32 * BM;
 #pragma unroll
       for (int i = 0; i < 32; ++i) dst[i * BM] = __uint_as_float(w[i]);
