@@ -76,8 +76,11 @@ __device__ __forceinline__ bool extend_rows_ok(const KernelArgs &a, int cq, int 
   if (a.block_table) return (long)a.max_pages * a.page_size >= Lk;
   return ck >= 0 && (long)ck + Lk <= a.kv_rows;
 }
-// First key that the packed band kernel takes for the row at position pos: those
-// within E, from the start of their 128-key tile on.
+// First key that the packed band kernel takes for a pair of row tiles whose first row
+// is at position pos: the keys within E of any of its rows, from the start of their
+// 128-key tile on.  It is the same for all rows of the pair, so that no row's weight of
+// zero meets a key that another row of its tile sees (where that key's value is
+// infinite the product would be NaN).
 __device__ __forceinline__ int extend_band_first(const KernelArgs &a, int pos) { return max(0, pos - a.E + 1) & ~127; }
 // Row of key j of sequence b, -1 where its page lies outside the pool.
 __device__ __forceinline__ long extend_key_row(const KernelArgs &a, int b, int ck, int j) {

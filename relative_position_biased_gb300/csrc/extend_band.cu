@@ -1,8 +1,9 @@
 // extend_band.cu -- the relative-bias band of relattn_extend on 5th-generation
-// tensor cores: for the row at position i the keys from extend_band_first(i) to
-// i, x(i,j) = s(i) (alpha q_i.k_j + [0 <= i-j < E] r_i . P[:, i-j]) (page "SGLang
-// and Miles Add Day-0 Support for Inkling", section "Attention with Relative
-// Positional Embedding"), softmax, P V.  The keys before are extend_tc.cu's.
+// tensor cores: for the row at position i the keys from extend_band_first (of its
+// pair of row tiles in extend_tc.cu) to i, x(i,j) = s(i) (alpha q_i.k_j + [0 <= i-j
+// < E] r_i . P[:, i-j]) (page "SGLang and Miles Add Day-0 Support for Inkling",
+// section "Attention with Relative Positional Embedding"), softmax, P V.  The keys
+// before are extend_tc.cu's.
 //
 // An item is up to 128 rows of one kv head, (token, head of the group) pairs of
 // consecutive tokens, against 64-key steps from the diagonal backwards (or a
@@ -188,8 +189,10 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
     I.ntok = min(ba.tokens, Lq - I.tok0);
     I.p0 = I.lk - Lq + I.tok0;
     I.p_last = I.p0 + I.ntok - 1;
-    // keys from the first row's band (or window, unless sinks lie in the band before it) on
-    const int j_lo = a.window > 0 ? max(0, I.p0 - a.window + 1) : 0, b0 = extend_band_first(a, I.p0);
+    // keys from the band's first (or the window's, unless sinks lie in the band before it)
+    // on; an item lies within a pair of row tiles, whose tokens are a multiple of its own
+    const int j_lo = a.window > 0 ? max(0, I.p0 - a.window + 1) : 0;
+    const int b0 = extend_band_first(a, I.p0 - I.tok0 % (2 * ba.x.tokens));
     const int low = (min(a.sink, j_lo) > b0 ? b0 : max(b0, j_lo)) / HN;
     I.first = I.p_last / HN - piece * ba.x.band_steps;
     I.steps = min(ba.x.band_steps, max(0, I.first - low + 1));
@@ -548,14 +551,14 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
         for (int u = 0; u < 32; u += 2)
           ffma2(x[u], x[u + 1], __uint_as_float(sr[u]), __uint_as_float(sr[u + 1]), qk_over_bias, qk_over_bias,
                 x[u], x[u + 1]);
-        if (j0 + HN - 1 > I.p0 || j0 < extend_band_first(a, I.p_last) || (a.window > 0 && j0 < I.p_last - a.window + 1)) {
-          // from the row's first band key to its own, in its window or a sink: a bit a key
+        if (j0 + HN - 1 > I.p0 || (a.window > 0 && j0 < I.p_last - a.window + 1)) {
+          // up to the row's own key, in its window or a sink: a bit a key
           const int jb = j0 + 32 * wg;
           auto below = [&](int key) -> uint32_t {   // the thread's keys below `key`
             const int n = key - jb;
             return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
           };
-          uint32_t seen = below(pos + 1) & ~below(extend_band_first(a, pos));
+          uint32_t seen = below(pos + 1);
           if (a.window > 0) seen &= ~below(pos - a.window + 1) | below(a.sink);
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = (seen >> i) & 1u ? x[i] : -INFINITY;

@@ -5,7 +5,7 @@
 // Per row, x(i,j) = s(i) alpha q_i . k_j over the keys that the band kernel leaves
 // (page "SGLang and Miles Add Day-0 Support for Inkling", section "Attention
 // with Relative Positional Embedding"), softmax, P V.  The band kernel has, per
-// row, the keys from a first one on (extend_band_first).
+// item, the keys from a first one on (extend_band_first).
 //
 // An item is up to 256 rows of one kv head, (token, head of the group) pairs in two
 // tiles of 128 that share every K / V tile, against key tiles of 128 from the nearest
@@ -202,9 +202,9 @@ __device__ __forceinline__ long walk_units(const ExtendTcArgs &x, int b0, int b1
 // A piece of work: steps [s0, s0 + steps) of a pair of row tiles, nearest keys first
 struct Item {
   int b, head, cq, ck, Lk, off, tok0, ntok;       // off: position of token 0
-  int s0, steps, n_all, n_sink, w_lo, p0, p_last, b_first, far;
+  int s0, steps, n_all, n_sink, w_lo, p0, p_last, far;
   int whole;                                      // 1: its steps are all of the tile's; 0: steps = 0 ends the list
-  int pad[2];
+  int pad[3];
 };
 static_assert(sizeof(Item) == 80, "ring of items");
 
@@ -399,7 +399,7 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
           it.cq = q.cq, it.ck = q.ck, it.Lk = q.Lk, it.off = q.Lk - q.Lq;
           it.tok0 = 2 * x.tokens * tile, it.ntok = T.ntok;
           it.steps = s1 - it.s0, it.n_all = T.n_all, it.n_sink = T.n_sink, it.w_lo = T.w_lo;
-          it.p0 = T.p0, it.p_last = T.p_last, it.b_first = T.b_first, it.far = T.far;
+          it.p0 = T.p0, it.p_last = T.p_last, it.far = T.far;
           it.whole = it.steps == T.n_all;
           if (!(run = put())) break;
           // a box: the tokens of a row tile x the group's heads x 64 dims (rows past the
@@ -611,7 +611,7 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
     // (the item's rows see all of a key tile unless it passes the first row's last
     // key or starts before the last row's window)
     const int n_sink = it->n_sink, w_lo = it->w_lo, v0 = it->n_all - 1 - it->s0, Lk = it->Lk;
-    const int all_to = min(it->p0, it->b_first - 1) + 1 - BN, all_from = a.window > 0 ? it->p_last - a.window + 1 : 0;
+    const int all_to = it->p0 + 1 - BN, all_from = a.window > 0 ? it->p_last - a.window + 1 : 0;
 #pragma unroll 1
     for (int v = v0; v > v0 - steps; --v) {
       if (!(ok = warp_wait(bar(B_S_FULL + w), s_parity, 48))) break;
@@ -649,13 +649,13 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
       reg_dep_f<96>(x_);
       const bool need_mask = j0 > all_to || j0 < all_from;
       if (need_mask) {
-        // the row's keys: its window below the band's first, and the sinks that its
-        // window has left behind, as a bit a key
+        // the row's keys: its window, and the sinks that its window has left behind, as
+        // a bit a key
         int pp = pos;
         asm volatile("" : "+r"(pp));             // (worked out here: kept, they would spill)
-        const int first = extend_row_first(x, pp), lo = a.window > 0 ? max(0, pp - a.window + 1) : 0;
-        const int kmin = lo - j0, kend = min(pp + 1, first) - j0;
-        const int kfar = j0 < it->far ? min(min(a.sink, lo), first) - j0 : 0;
+        const int lo = a.window > 0 ? max(0, pp - a.window + 1) : 0;
+        const int kmin = lo - j0, kend = pp + 1 - j0;
+        const int kfar = j0 < it->far ? min(a.sink, lo) - j0 : 0;
         auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

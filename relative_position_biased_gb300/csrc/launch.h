@@ -104,22 +104,18 @@ struct ExtendTcArgs {
 // the tiles of the first `far` keys, the sinks that the last row's window has left
 // behind.
 struct ExtendTiles {
-  int p0, p_last, ntok, j_lo, b_first, far, w_lo, n_sink, n_all;
+  int p0, p_last, ntok, far, w_lo, n_sink, n_all;
 };
-__device__ __forceinline__ int extend_row_first(const ExtendTcArgs &x, int pos) {   // the band's first key of a row
-  return x.band == 0 ? 0x7fffffff : extend_band_first(x.a, pos);
-}
 __device__ __forceinline__ ExtendTiles extend_tiles(const ExtendTcArgs &x, int tok0, int Lq, int Lk) {
   ExtendTiles t;
   t.ntok = min(2 * x.tokens, Lq - tok0);
   t.p0 = Lk - Lq + tok0;
   t.p_last = t.p0 + t.ntok - 1;
-  t.j_lo = x.a.window > 0 ? max(0, t.p0 - x.a.window + 1) : 0;
-  t.b_first = extend_row_first(x, t.p0);
-  const int b_last = extend_row_first(x, t.p_last);
-  t.far = x.a.window > 0 ? min(min(x.a.sink, max(0, t.p_last - x.a.window + 1)), b_last) : 0;
-  t.w_lo = t.j_lo / 128;
-  const int w_hi = (min(t.p_last + 1, b_last) + 127) / 128;
+  const int j_lo = x.a.window > 0 ? max(0, t.p0 - x.a.window + 1) : 0;
+  const int first = x.band == 0 ? 0x7fffffff : extend_band_first(x.a, t.p0);   // the band's (a tile's start)
+  t.far = x.a.window > 0 ? min(min(x.a.sink, max(0, t.p_last - x.a.window + 1)), first) : 0;
+  t.w_lo = j_lo / 128;
+  const int w_hi = (min(t.p_last + 1, first) + 127) / 128;
   t.n_sink = min((t.far + 127) / 128, t.w_lo);
   t.n_all = t.n_sink + max(0, w_hi - t.w_lo);
   return t;

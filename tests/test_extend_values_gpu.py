@@ -1,6 +1,8 @@
 """relattn_extend on what the tests of its lengths and layouts leave out: blocks of
 the band that straddle 64 keys, unusual values.  Tolerances as in test_extend_gpu.py."""
+import numpy as np
 import pytest
+import torch
 
 from tests import kvcache_util as U
 from tests import test_extend_gpu as X
@@ -16,3 +18,47 @@ def test_pieces_of_the_band_whose_blocks_straddle_64_keys(Hq, Hkv, more):
     """The band in pieces: the first step of all but the nearest reads three chunks of
     distances where a block's rows straddle a multiple of 64."""
     X.check(U.Case((40,), (3000 + more,), Hq, Hkv, r_dim=16, E=1024, page=16, seed=more))
+
+
+# Shapes that take every kernel: (Hq, Hkv, r_dim, E, page, tokens, keys, window, sink, num_splits)
+PATHS = [
+    (4, 1, 32, 64, 16, (1, 3), (200, 310), 0, 0, 0),             # short: one launch of the warp-MMA kernel
+    (6, 2, 7, 33, 48, (40,), (500,), 90, 5, 0),                  # a shape that TMA does not describe
+    (16, 2, 64, 256, 16, (1, 1), (5000, 900), 0, 0, 0),          # few rows, in splits
+    (8, 2, 16, 64, 0, (2, 1), (900, 700), 0, 0, 1),              # in one
+    (16, 2, 16, 128, 16, (40,), (2000,), 0, 0, 1),               # many rows, nothing cut: the band hands its rows on
+    (4, 4, 16, 64, 0, (300, 70), (900, 600), 0, 0, 1),
+    (16, 2, 64, 128, 64, (300, 70), (3000, 2600), 1000, 70, 1),
+    (8, 1, 16, 128, 128, (600, 5, 200), (5000, 2000, 3500), 0, 0, 0),    # row tiles cut
+    (16, 2, 16, 1024, 16, (40,), (6000,), 0, 0, 0),              # the band cut
+    (16, 2, 0, 0, 16, (40,), (6000,), 0, 0, 0),                  # no band
+    (16, 2, 16, 1024, 0, (300,), (300,), 0, 0, 1),               # nothing but the band
+]
+
+
+def place(p):
+    Hq, Hkv, rd, E, page, q_lens, k_lens, window, sink, splits = p
+    c = U.Case(q_lens, k_lens, Hq, Hkv, r_dim=rd, E=E, window=window, page=page, seed=Hq + len(q_lens))
+    return c, U.make(c), sink, splits
+
+
+def rows_of(c, b):
+    first = sum(c.q_lens[:b])
+    return slice(first, first + c.q_lens[b])
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_an_infinite_value_of_v_gives_infinities(path, value):
+    """A key that every row of its sequence sees holds an infinity in one channel:
+    every row's weight of it is above zero, so that channel is that infinity."""
+    c, d, sink, splits = place(path)
+    at = []
+    for b, (nq, nk) in enumerate(zip(c.q_lens, c.k_lens)):
+        g, ch = b % c.Hkv, 7 + 64 * (b % 2)
+        d["v"][d["where"][b][max(nk - nq - 5, 0)], g, ch] = value
+        at.append((rows_of(c, b), slice(g * (c.Hq // c.Hkv), (g + 1) * (c.Hq // c.Hkv)), ch))
+    out, _ = X.call(c, d, sink, num_splits=splits)
+    X.ok()
+    for rows, heads, ch in at:
+        assert (out[rows, heads, ch] == value).all()
