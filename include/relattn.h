@@ -194,7 +194,11 @@ relattn_status relattn_decode_paged(const relattn_params *params, const relattn_
  * (The pages name neither chunks over pages nor sinks; both are this library's
  * own addition in their manner.)
  * out and lse of a row are those of relattn_prefill for the same keys to
- * rounding, and feed relattn_backward_sinks.  out must not overlap q, k, v
+ * rounding, and feed relattn_backward_sinks.  An infinity or a NaN in v shows
+ * in its channel of the rows that see it and in no other channel; other rows of
+ * its sequence may get a NaN in that channel (a weight of zero times it).  Sums
+ * are fp32, of weights up to 2^8, and divided at the end: |v| above 2^120 may
+ * overflow on the way.  out must not overlap q, k, v
  * or r (RELATTN_ERR_INVALID_ARG).  Rows of no sequence keep their
  * out and lse; keys past max_seqlen_k or rows outside the arrays skip the
  * sequence and record RELATTN_ERR_DEVICE_ARGS.  max_seqlen_k up to 2^31 - 2^16;

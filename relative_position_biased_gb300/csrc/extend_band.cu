@@ -663,15 +663,22 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       } else {
         // the row is done, or goes on over the keys before the band: then as f16,
         // each half of it scaled by the power of two that brings its largest element
-        // to 2^14 .. 2^15
+        // to 2^14 .. 2^15.  f16 then has 8 bits and more of elements from 2^-17 on (its
+        // unit below 2^-14 is 2^-24); a half with smaller ones, an infinity or a NaN
+        // goes in bf16.
         const int Lq = I.lk - (I.p0 - I.tok0), pair = 2 * ba.x.tokens;
         const bool more = extend_tiles(ba.x, tok / pair * pair, Lq, I.lk).n_all > 0;
         uint4 *dst = reinterpret_cast<uint4 *>(a.out + qrow * kHeadDim + 64 * wg);
         if (more) {
-          float top[32];
+          uint32_t top = 0u, least = ~0u;        // of the magnitudes' bits, zeros aside (less one: still a bound)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) top[i] = fmaxf(fabsf(o[i]), fabsf(o[32 + i]));
-          const int e = min(max((int)(__float_as_uint(row_max(top)) >> 23) - 127, -100), 127);
+          for (int i = 0; i < 64; ++i) {
+            const uint32_t m = __float_as_uint(o[i]) & 0x7fffffffu;
+            top = max(top, m);
+            least = min(least, m - 1u);
+          }
+          const int e = min(max((int)(top >> 23) - 127, -100), 127);
+          const bool wide = top >= 0x7f800000u || (int)(least >> 23) - 127 < e - 31;
           const float down = __uint_as_float((uint32_t)(14 - e + 127) << 23);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -679,11 +686,11 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const __half2 hv = __floats2half2_rn(o[16 * i + 2 * k] * down, o[16 * i + 2 * k + 1] * down);
-              w[k] = *reinterpret_cast<const uint32_t *>(&hv);
+              w[k] = wide ? pack_bf16x2(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]) : *reinterpret_cast<const uint32_t *>(&hv);
             }
             if (valid) store32(dst + 2 * i, w, ba.x.out32);
           }
-          if (valid) ba.x.carry[2 * qrow + wg] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+          if (valid) ba.x.carry[2 * qrow + wg] = wide ? -1.f : __uint_as_float((uint32_t)(e - 14 + 127) << 23);
         } else if (valid) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

@@ -763,6 +763,8 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
       if (releaser) mbar_arrive(bar(B_V_EMPTY + (kt - 1) % V_STAGES));
       float inv = l > 0.f ? 1.f / l : 0.f;
       float row_lse = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+      const bool wide0 = ups.x < 0.f, wide1 = ups.y < 0.f;       // (that half of the band's row is bf16)
+      ups = make_float2(fabsf(ups.x), fabsf(ups.y));
       if (join && band_lse != -INFINITY) {
         const float top = fmaxf(row_lse, band_lse), wm = __expf(row_lse - top), wb = __expf(band_lse - top);
         inv *= wm / (wm + wb);
@@ -786,11 +788,13 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
         for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(r[k]) * inv;
         if (join) {
           const float up = c < 2 ? ups.x : ups.y;
+          const bool wide = c < 2 ? wide0 : wide1;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&band[i][k]));
+              float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&band[i][k]));
+              if (wide) f = make_float2(__uint_as_float(band[i][k] << 16), __uint_as_float(band[i][k] & 0xffff0000u));
               o[16 * i + 2 * k] = fmaf(f.x, up, o[16 * i + 2 * k]);
               o[16 * i + 2 * k + 1] = fmaf(f.y, up, o[16 * i + 2 * k + 1]);
             }

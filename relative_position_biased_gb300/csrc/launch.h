@@ -96,7 +96,9 @@ struct ExtendTcArgs {
   // In one piece the band hands its rows on in `out`: f16 with a power of two for
   // each half of a row in `carry` (workspace, fp32 [total_q][Hq][2]), 3 bits more
   // than bf16 in the same bytes.  (In bf16 the rows of 4 chunks of 2048 under a window of 4096
-  // were 0.0026 off the 64-bit values on the whole, 0.0024 so.)
+  // were 0.0026 off the 64-bit values on the whole, 0.0024 so.)  A half whose elements
+  // f16 would not hold to bf16's 8 bits -- they are more than 2^31 apart, or one is
+  // infinite or NaN -- goes in bf16, and its place in `carry` is -1.
   float *carry;
 };
 // The key tiles of 128 that are not the band's, of the row tiles from token tok0

@@ -62,3 +62,45 @@ def test_an_infinite_value_of_v_gives_infinities(path, value):
     X.ok()
     for rows, heads, ch in at:
         assert (out[rows, heads, ch] == value).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan"), 1e30, -3e38])
+def test_one_large_value_of_v_stays_in_its_channel(path, value):
+    """A key that every row of its sequence sees holds an infinity, a NaN or a value
+    far above the others in one channel: that channel follows, the others do not change."""
+    c, d, sink, splits = place(path)
+    at = []
+    for b, (nq, nk) in enumerate(zip(c.q_lens, c.k_lens)):
+        g, ch = b % c.Hkv, 7 + 64 * (b % 2)
+        d["v"][d["where"][b][max(nk - nq - 5, 0)], g, ch] = value
+        at.append((rows_of(c, b), slice(g * (c.Hq // c.Hkv), (g + 1) * (c.Hq // c.Hkv)), ch))
+    out, lse = X.call(c, d, sink, num_splits=splits)
+    X.ok()
+    got, got_z = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    finite = dict(d, v=torch.where(d["v"].isfinite(), d["v"], torch.zeros_like(d["v"])))
+    ref, z, e_out, e_lse = X.bounds(c, finite, sink)
+    # the sums of a row are fp32 and divided at the end; their weights are up to 2^8, so
+    # a value of more than 2^120 (3e38 is 2^128) may pass the largest fp32 on the way
+    if not abs(value) < 2.0 ** 120:
+        for rows, heads, ch in at:
+            hit = got[rows, heads, ch]
+            right = np.isnan(hit) if np.isnan(value) else hit == np.sign(value) * np.inf
+            if np.isfinite(value):
+                right |= np.abs(hit - ref[rows, heads, ch]) <= e_out[rows, heads, ch]
+            assert right.all(), hit
+            got[rows, heads, ch] = ref[rows, heads, ch] = 0
+    assert (np.abs(got - ref) <= e_out).all(), np.abs(got - ref).max()
+    assert (np.abs(got_z - z) <= e_lse).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_channels_of_any_size(path):
+    """Channels of v from 2^-60 to 2^60 of the others: each is right to its own size."""
+    c, d, sink, splits = place(path)
+    scale = torch.exp2(torch.arange(128.0) * 37 % 121 - 60)
+    d["v"] = (d["v"].float() * scale).bfloat16()
+    out, lse = X.call(c, d, sink, num_splits=splits)
+    X.ok()
+    ref, z, e_out, e_lse = X.bounds(c, d, sink)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= e_out).all()
