@@ -196,7 +196,8 @@ relattn_status relattn_decode_paged(const relattn_params *params, const relattn_
  * out and lse of a row are those of relattn_prefill for the same keys to
  * rounding, and feed relattn_backward_sinks.  An infinity or a NaN in v shows
  * in its channel of the rows that see it and in no other channel; other rows of
- * its sequence may get a NaN in that channel (a weight of zero times it).  Sums
+ * its sequence may get a NaN in that channel (a weight of zero times it).  A
+ * NaN logit makes its row of out and its lse NaN, however the keys are cut.  Sums
  * are fp32, of weights up to 2^8, and divided at the end: |v| above 2^120 may
  * overflow on the way.  out must not overlap q, k, v
  * or r (RELATTN_ERR_INVALID_ARG).  Rows of no sequence keep their

@@ -152,6 +152,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 // Length-dependent log-scale s(i) = max(1, ln(i+1)/ln(base)) (1 when off).
+// What a row's sum of weights l divides by, and its logsumexp (m: the logits' maximum
+// in log2 units): 0 and -inf for a row without keys.  The sum of a row that saw a NaN
+// logit is NaN, and so are both, for the merge of partial results to keep it.
+__device__ __forceinline__ float row_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float row_logsumexp(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
+
 __device__ __forceinline__ float log_scale(int pos, float inv_ln_base) {
   if (inv_ln_base <= 0.f) return 1.f;
   return fmaxf(1.f, logf(static_cast<float>(pos + 1)) * inv_ln_base);

@@ -1246,7 +1246,7 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
           const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - m);
           const float f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - m);
           const float l = l0 * f0 + l1 * f1;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = row_inverse(l);
           const float o1 = mbuf[i * 128 + key];
           o[i] = ((f0 > 0.f ? o[i] * f0 : 0.f) + (f1 > 0.f ? o1 * f1 : 0.f)) * inv;
           if (lane == i) {
@@ -1265,7 +1265,7 @@ relattn_decode_tc_kernel(const __grid_constant__ DecArgs da,
             a.out[qrow * kHeadDim + key] = __float2bfloat16_rn(o[i]);
         }
         if (row_owner && lane < nrows) {
-          const float row_lse = (lrow > 0.f && mrow != -INFINITY) ? (mrow + __log2f(lrow)) * kLn2 : -INFINITY;
+          const float row_lse = row_logsumexp(mrow, lrow);
           const size_t qrow = (size_t)__float_as_int(rowc[lane].w);
           if (partial) {
             // (stream-K: the unit's first piece marks the split slots no piece

@@ -639,8 +639,7 @@ relattn_extend_band_kernel(const __grid_constant__ BandArgs ba, const __grid_con
       const float lt = l + take_over(ok);
       if (!ok) break;
       tc_fence_after();
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
-      const float row_lse = lt > 0.f ? (m_ref + __log2f(lt)) * kLn2 : -INFINITY;
+      const float inv = row_inverse(lt), row_lse = row_logsumexp(m_ref, lt);
       float o[64];
       __syncwarp();
       tmem_ld32f<0>(tmem + lane_base + TM_O + 64u * wg, o);

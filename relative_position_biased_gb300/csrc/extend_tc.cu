@@ -761,8 +761,7 @@ relattn_extend_main_kernel(const __grid_constant__ ExtendTcArgs x, const __grid_
     if (ok) {
       tc_fence_after();
       if (releaser) mbar_arrive(bar(B_V_EMPTY + (kt - 1) % V_STAGES));
-      float inv = l > 0.f ? 1.f / l : 0.f;
-      float row_lse = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+      float inv = row_inverse(l), row_lse = row_logsumexp(m_ref, l);
       const bool wide0 = ups.x < 0.f, wide1 = ups.y < 0.f;       // (that half of the band's row is bf16)
       ups = make_float2(fabsf(ups.x), fabsf(ups.y));
       if (join && band_lse != -INFINITY) {

@@ -412,8 +412,7 @@ __global__ void __launch_bounds__(NW * 32, 1) relattn_fwd_mma_kernel(const __gri
     if (rl >= nrows) continue;
     const int t = row_t(rl), h = row_h(rl);
     const size_t row = (size_t)(cq + t) * a.Hq + h;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const float lse = l > 0.f ? (m_r[r] + __log2f(l)) * kLn2 : -INFINITY;
+    const float inv = row_inverse(l), lse = row_logsumexp(m_r[r], l);
     if (final_out) {
       __nv_bfloat16 *dst = a.out + row * kHeadDim + 2 * qq;
 #pragma unroll

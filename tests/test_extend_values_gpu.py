@@ -104,3 +104,24 @@ def test_channels_of_any_size(path):
     X.ok()
     ref, z, e_out, e_lse = X.bounds(c, d, sink)
     assert (np.abs(out.double().cpu().numpy() - ref) <= e_out).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("back", [0, 7, 150, 260, 800])
+def test_a_nan_key_reaches_the_rows_that_see_it_whatever_is_cut(path, back):
+    """out and lse of the rows that see a key of NaN are NaN; other rows are as without it."""
+    c, d, sink, splits = place(path)
+    want, z, e_out, e_lse = X.bounds(c, d, sink)
+    hit = np.zeros((sum(c.q_lens), c.Hq), bool)
+    for b, (nq, nk) in enumerate(zip(c.q_lens, c.k_lens)):
+        j, g = max(nk - 1 - back, 0), b % c.Hkv
+        d["k"][d["where"][b][j], g] = float("nan")
+        pos = nk - nq + np.arange(nq)
+        sees = (pos >= j) & ((c.window <= 0) | (pos - j < c.window) | (j < sink))
+        hit[rows_of(c, b), g * (c.Hq // c.Hkv):(g + 1) * (c.Hq // c.Hkv)] |= sees[:, None]
+    out, lse = X.call(c, d, sink, num_splits=splits)
+    X.ok()
+    got, got_z = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isnan(got[hit]).all() and np.isnan(got_z[hit.T]).all()
+    assert (np.abs(got - want)[~hit] <= e_out[~hit]).all()
+    assert (np.abs(got_z - z)[~hit.T] <= e_lse[~hit.T]).all()
