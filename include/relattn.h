@@ -23,7 +23,8 @@
  * h / (num_heads_q / num_heads_kv).
  *
  * Outputs: out = softmax-weighted sum of v (bf16) and the per-row natural-log
- * logsumexp of the logits (fp32).
+ * logsumexp of the logits (fp32). A row that sees a NaN logit is NaN in
+ * both, however its keys are split.
  *
  * Positions are bottom-right aligned: query row t of sequence b sits at
  * position (Lk_b - Lq_b) + t, where Lq_b / Lk_b come from cu_seqlens_q / _k.

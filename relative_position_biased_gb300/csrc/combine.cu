@@ -48,12 +48,13 @@ relattn_combine_kernel(const float *__restrict__ o_part, const float *__restrict
 
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float z = 0.f;
-  if (active && m != -INFINITY) {
+  if (active) {
 #pragma unroll 4
     for (int s = wi; s < num_splits; s += RW) {
       const float ls = lse_part[(long)s * rows + row];
       float4 v = *reinterpret_cast<const float4 *>(o_part + ((long)s * rows + row) * kHeadDim + lane * 4);
-      // an empty split (lse = -inf) contributes nothing, whatever its o_s holds
+      // an empty split (lse = -inf) contributes nothing, whatever its o_s holds; a NaN
+      // (of a NaN logit) stays in z
       const bool empty = ls == -INFINITY;
       const float w = empty ? 0.f : exp2f((ls - m) * kLog2e);
       if (empty) v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -80,14 +81,14 @@ relattn_combine_kernel(const float *__restrict__ o_part, const float *__restrict
     }
   }
   if (!active) return;
-  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const float inv = row_inverse(z);
   uint2 packed;
   packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2 *>(out + row * kHeadDim + lane * 4) = packed;
   if (lane == 0) {
     const long t = row / num_heads, h = row - t * num_heads;
-    lse[h * total_q + t] = z > 0.f ? m + logf(z) : -INFINITY;
+    lse[h * total_q + t] = z == 0.f ? -INFINITY : m + logf(z);
   }
 }
 

@@ -1204,8 +1204,7 @@ relattn_fwd_tc_kernel(const __grid_constant__ TcArgs ta,
     if (ok) {
       const float lt = l + l_other;
       tc_fence_after();
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
-      const float row_lse = lt > 0.f ? (m_ref + __log2f(lt)) * kLn2 : -INFINITY;
+      const float inv = row_inverse(lt), row_lse = row_logsumexp(m_ref, lt);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t r[32];

@@ -409,8 +409,7 @@ relattn_fwd_tc_main_kernel(const __grid_constant__ KernelArgs a,
     if (ok) {
       tc_fence_after();
       const bool valid = a_row < nrows;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float row_lse = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+      const float inv = row_inverse(l), row_lse = row_logsumexp(m_ref, l);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t r[32];
