@@ -443,7 +443,7 @@ void plan_extend_tc(const relattn_params *p, const KernelArgs &a, ExtendPlan *pl
   if (bias) {
     const int tokens = extend_band_tokens(a);
     const long steps = ((long)a.E + 2 * x.tokens + 126) / 64 + 3;  // at most, of a row block
-    const long items = std::min<long>((long)a.batch * (((long)a.max_q + tokens - 1) / tokens), a.total_q / tokens + a.batch) * a.Hkv;
+    const long items = extend_band_items(a);
     if (p->num_splits <= 0 && 2 * items < a.sms) x.band_pieces = (int)std::max<long>(1, std::min<long>(a.sms / items, steps / 6));
     x.band_steps = (int)((steps + x.band_pieces - 1) / x.band_pieces);
     x.band_tokens = tokens;

@@ -782,10 +782,7 @@ cudaError_t launch_extend_band(const ExtendTcArgs &x, cudaStream_t stream) {
   BandArgs ba = {};
   ba.x = x;
   ba.tokens = extend_band_tokens(a);
-  const long blocks = std::min<long>((long)a.batch * (((long)a.max_q + ba.tokens - 1) / ba.tokens), a.total_q / ba.tokens + a.batch);
-  const long items = blocks * a.Hkv * x.band_pieces;
-  if (items > 1L << 25) return cudaErrorInvalidValue;        // (q of more than memory holds; 32 sequences' sum fits an int)
-  ba.n_items = (int)items;
+  ba.n_items = (int)(extend_band_items(a) * x.band_pieces);   // (pieces only where items are fewer than SMs)
   ba.box = std::min(extend_box(a), HN);
   const int q_tokens = std::min(ba.tokens, a.total_q);        // a box stays inside the tensor
   ba.row_bytes = 128 * a.group * q_tokens;

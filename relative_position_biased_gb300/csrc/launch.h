@@ -3,6 +3,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -149,6 +150,16 @@ __device__ __forceinline__ void load32(const void *p, uint32_t (&v)[8], bool who
 cudaError_t launch_extend_main(const ExtendTcArgs &x, cudaStream_t stream);
 cudaError_t launch_extend_band(const ExtendTcArgs &x, cudaStream_t stream);
 int extend_band_tokens(const KernelArgs &a);   // of a work item
+// Work items of the band in one piece, at most (every token block has a token, and a
+// sequence one block that is not full).  Below 2^31 for any q that memory holds, as an
+// item has a row of q, 256 bytes, of its own; and a full block has 64 and more, so that
+// 32 sequences' items are below 2^31 even where wrong lengths let them overlap.
+inline long extend_band_items(const KernelArgs &a) {
+  const int tokens = extend_band_tokens(a);
+  const long blocks = std::min<long>((long)a.batch * (((long)a.max_q + tokens - 1) / tokens),
+                                     std::min<long>(a.total_q / tokens + (long)a.batch, a.total_q));
+  return std::min<long>(blocks * a.Hkv, 0x7fff0000L);
+}
 // out / lse from their partials (extend_tc.cu), about `partials` a row: of every
 // row of a sequence with x.slots > 1 (other rows keep theirs), else of the row tiles
 // that were cut.  A programmatic dependent of the kernel before it on the stream.

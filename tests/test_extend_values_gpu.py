@@ -125,3 +125,18 @@ def test_a_nan_key_reaches_the_rows_that_see_it_whatever_is_cut(path, back):
     assert np.isnan(got[hit]).all() and np.isnan(got_z[hit.T]).all()
     assert (np.abs(got - want)[~hit] <= e_out[~hit]).all()
     assert (np.abs(got_z - z)[~hit.T] <= e_lse[~hit.T]).all()
+
+
+def test_a_batch_of_many_empty_sequences_and_heads():
+    """Sequences times heads above 2^25, with 17 tokens in all: the call runs, and asks for the workspace that it takes."""
+    batch, H, q_len, k_len = 65535, 520, 17, 400
+    c = U.Case((q_len,), (k_len,), H, H, r_dim=16, E=64, seed=4)
+    d = U.make(c)
+    for n, m in (("cu_q", q_len), ("cu_k", k_len)):
+        d[n] = torch.zeros(batch + 1, dtype=torch.int32)
+        d[n][40000:] = m
+    out, lse = X.call(c, d, 0)
+    X.ok()
+    ref, z, e_out, e_lse = X.bounds(c, d, 0)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= e_out).all()
+    assert (np.abs(lse.double().cpu().numpy() - z) <= e_lse).all()
