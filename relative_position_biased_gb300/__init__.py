@@ -596,6 +596,12 @@ def backward(q, k, v, r, P, out, lse, dout, cu_seqlens_q, cu_seqlens_k, *, max_s
     in ``extend``, which gave out and lse (relattn_backward_sinks)."""
     import torch
     _fit(sink)
+    here = _stream_here(q.device, stream)
+    if here is None:
+        with _switched(q.device, stream):
+            return backward(q, k, v, r, P, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
+                            max_seqlen_k=max_seqlen_k, alpha=alpha, window=window, log_scale_base=log_scale_base, dq=dq,
+                            dk=dk, dv=dv, dr=dr, workspace=workspace, sink=sink)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -614,11 +620,10 @@ def backward(q, k, v, r, P, out, lse, dout, cu_seqlens_q, cu_seqlens_k, *, max_s
         workspace = torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=q.device)
     prm.workspace = workspace.data_ptr()
     prm.workspace_bytes = workspace.numel() * workspace.element_size()
-    st = _current_stream() if stream is None else stream
     if sink:
-        _check(relattn_backward_sinks(prm, sink, st), "relattn_backward_sinks")
+        _check(relattn_backward_sinks(prm, sink, here), "relattn_backward_sinks")
     else:
-        _check(relattn_backward(prm, st), "relattn_backward")
+        _check(relattn_backward(prm, here), "relattn_backward")
     return dq, dk, dv, dr
 
 
