@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional, Tuple
@@ -388,6 +389,22 @@ def relattn_version() -> str:
 
 # ------------------------------------------------------------------ torch conveniences
 
+def _placed(call):
+    """Runs a call with its first tensor's device current and, where a stream is
+    given, that stream too: what it allocates (a workspace that it gives back on
+    return among it) then belongs to the stream that it launches on."""
+    name = call.__code__.co_varnames[0]
+
+    @functools.wraps(call)
+    def placed(*args, stream: Optional[int] = None, **kw):
+        device = (args[0] if args else kw[name]).device
+        if _stream_here(device, stream) is not None:
+            return call(*args, **kw)
+        with _switched(device, stream):
+            return call(*args, **kw)
+    return placed
+
+
 def make_params(q, k, v, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int,
                 max_seqlen_k: int, alpha: float, window: int = 0, log_scale_base: float = 0.0,
                 out=None, lse=None, workspace=None, num_splits: int = 0,
@@ -426,6 +443,7 @@ def _outputs(q, out, lse):
     return out, lse
 
 
+@_placed
 def prefill(q, k, v, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int, max_seqlen_k: int,
             alpha: float, window: int = 0, log_scale_base: float = 0.0, out=None, lse=None,
             stream: Optional[int] = None):
@@ -447,6 +465,7 @@ def decode_workspace(params: RelattnParams, device):
     return torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device)
 
 
+@_placed
 def decode(q, k, v, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int, max_seqlen_k: int,
            alpha: float, window: int = 0, log_scale_base: float = 0.0, num_splits: int = 0,
            out=None, lse=None, workspace=None, stream: Optional[int] = None):
@@ -464,6 +483,7 @@ def decode(q, k, v, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int, max_
     return out, lse
 
 
+@_placed
 def prologue(q, k, v, conv_k, conv_v, norm_q, norm_k, cu_seqlens_q, cu_seqlens_k, k_cache,
              v_cache, *, eps: float = 1e-6, q_out=None, conv_state_in=None,
              conv_state_out=None, total_k: Optional[int] = None, mxfp8=None, block_table=None,
@@ -519,6 +539,7 @@ def relattn_quantize_mxfp8(x: int, n_blocks: int, codes: int, scales: int, strea
     return load_library().relattn_quantize_mxfp8(x, n_blocks, codes, scales, stream)
 
 
+@_placed
 def quantize_mxfp8(x, stream: Optional[int] = None):
     """MXFP8 of a contiguous bf16 CUDA tensor whose last dimension is a multiple
     of 32: (codes uint8 with x's shape, scales uint8 with the last dimension
@@ -534,6 +555,7 @@ def quantize_mxfp8(x, stream: Optional[int] = None):
     return codes, scales
 
 
+@_placed
 def decode_mxfp8(q, k8, v8, k_scale, v_scale, r, P, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q: int,
                  max_seqlen_k: int, alpha: float, window: int = 0, log_scale_base: float = 0.0,
                  num_splits: int = 0, out=None, lse=None, workspace=None, stream: Optional[int] = None):
@@ -557,6 +579,7 @@ def decode_mxfp8(q, k8, v8, k_scale, v_scale, r, P, cu_seqlens_q, cu_seqlens_k, 
     return out, lse
 
 
+@_placed
 def decode_paged(q, k_pool, v_pool, r, P, cu_seqlens_q, cu_seqlens_k, block_table, *,
                  page_size: int, max_seqlen_q: int, max_seqlen_k: int, alpha: float,
                  window: int = 0, log_scale_base: float = 0.0, num_splits: int = 0,
