@@ -554,7 +554,9 @@ relattn_status relattn_backward(const relattn_bwd_params *params, void *stream);
  * RELATTN_ERR_UNSUPPORTED); 0, or no window: relattn_backward's results.  The
  * workspace (relattn_backward_sinks_workspace_size) holds relattn_backward's
  * and the sinks' parts in fp32: 4 * total_q * Hq * 128 bytes of dq, as many
- * with r_dim in place of 128 where rel_extent > window, and those of dk and dv.
+ * with r_dim in place of 128 where rel_extent > window, those of dk and dv, and
+ * partial sums of these: up to 16 KB for each kv head, 16 sinks and 128 to 1024 of
+ * its rows (32768 tokens of 16 heads on 2: 9 MB for 16 sinks, 0.5 GB for 1024).
  */
 #define RELATTN_MAX_BACKWARD_SINK 1024
 relattn_status relattn_backward_sinks_workspace_size(const relattn_bwd_params *params, int32_t sink, size_t *bytes);

@@ -12,7 +12,8 @@
 // is added before the results' one rounding to bf16.
 //
 // What bounds it: every row past the window is read (q, dout: 512 bytes) and its
-// dq part written (512 bytes), for 16 keys' five products: HBM.  4 x 8192 tokens of
+// dq part written (512 bytes), for 16 keys' five products: HBM (once for every 16
+// sinks: beyond them dq and dr are read and added to as well).  4 x 8192 tokens of
 // 16 heads, window 4096: 67 us for 268 MB, 4.0 TB/s (the sums 5 us); few rows are a
 // chain of loads instead: 5 sequences of 90 to 1500 tokens of 8 heads take 20.  A warp takes 16
 // rows (token, head of the group) at a time against 16 keys, in m16n8k16
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(2 * kHeadDim) relattn_bwd_sink_sum_kernel(cons
   a.sink_dkv[((((size_t)b * a.Hkv + g) * a.sink + j) * 2 + which) * kHeadDim + dim] = v;
 }
 
+// (152 SMs: the workspace's size follows from it and is given without a device)
 int sink_rows_of_cta(int total_q, int Hq) {
   const long want = (long)total_q * Hq / (2 * 152) / kRowsMin * kRowsMin;
   return (int)std::min<long>(std::max<long>(want, kRowsMin), kRowsMax);

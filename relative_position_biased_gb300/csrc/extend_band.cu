@@ -39,7 +39,7 @@
 // What bounds it: a step's chain -- S and R out of tensor memory, R's way through
 // shared memory, the exchange of the maximum between a row's two threads, the
 // exponentials, P -- takes 2,000 cycles; issue slots 41 %, tensor pipe 25 % (4 x 8192
-// tokens, Hq 16 / Hkv 2, r_dim 64, E 1024, window 4096: 549 us; R issued with its own
+// tokens, Hq 16 / Hkv 2, r_dim 64, E 1024, window 4096: 553 us; R issued with its own
 // step instead of one ahead 710, four softmax warpgroups or P before the step's
 // maximum no faster).
 //

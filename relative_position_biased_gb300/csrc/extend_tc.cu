@@ -20,7 +20,7 @@
 // and counts of tiles that are no multiple of the SMs leave none idle.  A tile within
 // one share is final; of a cut one each piece leaves a normalised fp32 partial, two a
 // CTA at most, and relattn_extend_join_kernel adds them.  (12 chunks of 4-88 tokens on
-// 6.6k-50k keys: 166 us with ranges of equal length for every tile, 131 so; 4 chunks
+// 6.6k-50k keys: 166 us with ranges of equal length for every tile, 132 so; 4 chunks
 // of 2048 under a window of 4096, 3.4 tiles an SM: 375 and 357.)  The band's row joins
 // the piece with the nearest keys in its epilogue; where the band comes in pieces
 // itself, all partials are kept by row and relattn_extend_combine_kernel adds them.
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(256) relattn_extend_combine_kernel(const __gri
 // which ends at once unless that is a tile's first cut.  A warp a row: a chain of
 // loads (two pieces a row as a rule), which many short warps hide best until their
 // instructions fill the issue slots (78 %): 12 chunks of 4-88 tokens on 6.6k-50k keys
-// take 131 us, with two rows a warp 133, four 137, eight 153.
+// take 132 us, on the same GPU with two rows a warp 133, four 137, eight 153.
 __global__ void __launch_bounds__(256) relattn_extend_join_kernel(const __grid_constant__ ExtendTcArgs x) {
   const KernelArgs &a = x.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = blockIdx.x + 1;
