@@ -85,3 +85,33 @@ def test_combine(nan, empty):
     # weights, products and sums in fp32 (2^-16 of |o| < 6 at most), one rounding of out
     assert (out.double() - ref)[~bad].abs().max() <= 2.0 ** -8 * ref[~bad].abs().max() + 6 * 2.0 ** -16
     assert (lse.T.double() - torch.logsumexp(z.double(), 0))[~bad].abs().max() <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("num_splits", [0, 1, 3])
+@pytest.mark.parametrize("q_lens", [(1, 2), (9, 3)])
+@pytest.mark.parametrize("which", ["decode", "decode_mxfp8", "decode_nvfp4", "extend"])
+def test_a_nan_in_q_is_its_rows_alone(which, q_lens, num_splits):
+    if which == "decode_mxfp8" and q_lens[0] > 2:
+        pytest.skip("16 rows per kv head at most")
+    c = U.Case(q_lens, (5000, 900), 16, 2, r_dim=64, E=128)
+    d = U.make(c)
+    kw = dict(max_seqlen_q=max(q_lens), max_seqlen_k=5000, alpha=c.alpha, num_splits=num_splits)
+    t = {n: U.cuda(d[n]) for n in ("q", "k", "v", "r", "P", "cu_q", "cu_k")}
+    rest = (t["r"], t["P"], t["cu_q"], t["cu_k"])
+    if which == "decode_mxfp8":
+        (k8, ks), (v8, vs) = rpb.quantize_mxfp8(t["k"]), rpb.quantize_mxfp8(t["v"])
+        run = lambda q: rpb.decode_mxfp8(q, k8, v8, ks, vs, *rest, **kw)  # noqa: E731
+    elif which == "decode_nvfp4":
+        cache = U.device_cache(U.quantized(c, d), d)
+        run = lambda q: rpb.decode_nvfp4(q, cache, *rest, **kw)[:2]  # noqa: E731
+    else:
+        run = lambda q: getattr(rpb, which)(q, t["k"], t["v"], *rest, **kw)  # noqa: E731
+    want = run(t["q"])
+    q = t["q"].clone()
+    q[0, 3, 100], q[-1, 9, 0] = float("nan"), float("nan")
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    hit[0, 3] = hit[-1, 9] = True
+    out, lse = run(q)
+    X.ok()
+    assert out[hit].isnan().all() and lse.T[hit].isnan().all()
+    assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse.T[~hit], want[1].T[~hit])
